@@ -351,6 +351,105 @@ size_t gmm_kde_workspace_bytes(const gmm_data* queries, int64_t M);
 gmm_status gmm_kde_score(const gmm_data* queries, const float* ref, int64_t M, int64_t ld_ref, double bandwidth,
                          float* logdens, void* ws, size_t ws_bytes, void* stream);
 
+/* A linear head over V classes: logit v of a row x is w_v . x + bias_v, with
+ * class v, feature d at w[v * ld_w + d] (elements of `dtype`), ld_w >= D.  The
+ * posterior of a mixture with one shared spherical variance is such a head:
+ * w_k = mu_k / sigma^2, bias_k = log pi_k - |mu_k|^2 / (2 sigma^2). */
+typedef struct {
+  const void* w;
+  int32_t dtype;     /* gmm_dtype, the rows'                                   */
+  int64_t V, ld_w;
+  const float* bias; /* (V) float32, nullable                                  */
+} gmm_head;
+
+/* Softmax cross entropy of rows under a linear head -- the discriminative
+ * counterpart of the mixture's log-likelihood, by the same fused log-sum-exp
+ * (Flash-GMM Section 3: no N x V matrix in device memory).  With
+ * l_iv = w_v . x_i + bias_v, for each row i of each problem:
+ *   lse  (B,N) float32 = log sum_v exp(l_iv)
+ *   loss (B,N) float32 = lse_i - l_{i, labels_i}
+ * labels (B,N) int32: a negative label leaves the row out (loss 0; its lse is
+ * still formed); a label >= V gives loss NaN.  Rows and head are float32, bf16
+ * or half, of one type, at any stride and alignment of their elements
+ * (operands off 16 bytes are copied piecewise); logits are exact products
+ * summed in float32.  Scores of one row to 64 rows take a path that reads the
+ * head once.  Window: D <= 65536, V < 2^31, B*N < 2^31.  A row whose logits
+ * are all -inf has lse -inf and loss NaN.  N = 0 launches nothing.
+ * Workspace: gmm_softmax_xent_workspace_bytes (bounded: rows are taken in
+ * chunks).  Deterministic. */
+size_t gmm_softmax_xent_workspace_bytes(const gmm_data* rows, const gmm_head* head);
+gmm_status gmm_softmax_xent(const gmm_data* rows, const gmm_head* head, const int32_t* labels, float* loss, float* lse,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients, with lse as gmm_softmax_xent wrote it for these operands and
+ * gloss (B,N) float32 the loss's gradient per row (NULL: 1 for every row).
+ * With G_iv = gloss_i (exp(l_iv - lse_i) - [v == labels_i]), 0 for rows whose
+ * label is negative (whatever their values, NaN included):
+ *   dx (B,N,D) = sum_v G_iv w_v;  dw (V,D) = sum_i G_iv x_i;  dbias (V) = sum_i G_iv
+ * dx and dw in the rows' type, contiguous, dbias float32; each nullable, one
+ * given.  accumulate != 0 adds to what they hold.  A label >= V makes the
+ * gradients that its row reaches NaN.  G is formed in pieces of at most 2^27
+ * elements in the workspace and rounded once to the rows' type for the two
+ * products (float32 accumulation; half rows scaled by a power of two first).
+ * The gradients may not overlap each other or the inputs.  Workspace:
+ * gmm_softmax_xent_grad_workspace_bytes, want = 1 (dx) + 2 (dw) + 4 (dbias).
+ * Deterministic. */
+size_t gmm_softmax_xent_grad_workspace_bytes(const gmm_data* rows, const gmm_head* head, int32_t want);
+gmm_status gmm_softmax_xent_grad(const gmm_data* rows, const gmm_head* head, const int32_t* labels, const float* lse,
+                                 const float* gloss, void* dx, void* dw, float* dbias, int32_t accumulate, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* Rows rebuilt from codes: for problem b and row i
+ *   out[b][i] = scale sum_j weights[b][i][j] table[b][idx[b][i][j]]
+ * over the row's entries as gmm_ivf_lists reads them (its leading values in
+ * [0, K); the first value outside ends the row; a row with none gives zeros),
+ * so that a top-m assignment (idx, resp), k-means labels (m = 1, no weights)
+ * or token ids rebuild their rows.
+ *   table   (B,K,D) rows as gmm_data describes them, with N = K
+ *   idx     (B,N,m) int32; weights (B,N,m) float32, nullable (1)
+ *   out     (B,N,D) in the table's type, contiguous; summed in float32
+ * Any stride and alignment of the elements.  D <= 65536, B*N*m < 2^31,
+ * B*K < 2^31.  N = 0 launches nothing.  No workspace. */
+gmm_status gmm_codebook_lookup(const gmm_data* table, int64_t N, int32_t m, const int32_t* idx, const float* weights,
+                               float scale, void* out, void* stream);
+
+/* Its gradients, dout (B,N,D) rows being the gradient of out:
+ *   dtable[b][k]      = scale sum over the entries with idx[b][i][j] = k of
+ *                       weights[b][i][j] dout[b][i]      (B,K,D), dout's type
+ *   dweights[b][i][j] = scale dout[b][i] . table[b][idx[b][i][j]]  (B,N,m)
+ *                       float32, 0 where the row has ended
+ * each nullable, one given; table only for dweights, of dout's type.  The
+ * entries are summed in float32 in the order of a stable sort by code, so the
+ * result does not depend on the run (no atomics on sums).  Codes without
+ * entries get zeros; accumulate != 0 adds to dtable instead (dweights is
+ * always written).  The gradients may not overlap each other or the inputs.
+ * Workspace: gmm_codebook_lookup_grad_workspace_bytes. */
+size_t gmm_codebook_lookup_grad_workspace_bytes(const gmm_data* dout, int64_t K, int32_t m);
+gmm_status gmm_codebook_lookup_grad(const gmm_data* dout, int64_t K, int32_t m, const int32_t* idx, const float* weights,
+                                    float scale, const gmm_data* table, void* dtable, float* dweights, int32_t accumulate,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/* A contiguous tensor of n elements, read from src and written to dst (dst ==
+ * src: in place). */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t dtype; /* gmm_dtype */
+} gmm_tensor;
+
+/* The 2-norm over every element of `count` gradients, and the gradients scaled
+ * so that it is at most max_norm (>= 0; infinity: the norm and a copy):
+ *   norm = sqrt(sum g^2);  dst = min(1, max_norm / (norm + 1e-6)) src
+ * norm float32 device, nullable.  Squares and sums are float64.  An infinite
+ * norm scales by 0 (infinite elements become NaN), a NaN norm makes every
+ * element NaN.  `grads` is host memory, read during the call.  No dst may
+ * overlap another tensor, nor its own src in part.  Workspace:
+ * gmm_clip_grad_norm_workspace_bytes.  Deterministic. */
+size_t gmm_clip_grad_norm_workspace_bytes(int32_t count);
+gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max_norm, float* norm, void* ws,
+                              size_t ws_bytes, void* stream);
+
 /* Host-side summary of a comp_status array that the caller copied to host
  * memory (count int32 values, as written by gmm_mstep / gmm_fit_step /
  * gmm_topk_fit_step): GMM_ERR_NOT_PD if any component carries flag 2 (its

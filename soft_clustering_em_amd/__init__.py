@@ -18,6 +18,14 @@ torch stream; every step of the computation runs in the HIP kernels.
   gmm_kmeans_step(X, centroids, labels=None, counts=None, inertia=None, ws=None)
   gmm_fisher_vector(X, w, mu, var, power=True, l2=True, fv=None, ws=None)
   gmm_topk_fit_step(X, w, mu, cv, cov, topk, reg_covar=1e-6, mean_loglik=None, comp_status=None, ws=None)
+  gmm_kde_score(Y, ref, bandwidth, out=None, ws=None)
+  gmm_softmax_xent(X, W, labels, bias=None, loss=None, lse=None, ws=None)             -> (loss, lse)
+  gmm_softmax_xent_grad(X, W, labels, lse, gloss=None, bias=None, dX=None, dW=None, dbias=None,
+                        accumulate=False, ws=None)                                    -> (dX, dW, dbias)
+  gmm_codebook_lookup(table, idx, weights=None, scale=1.0, out=None)                  -> rows
+  gmm_codebook_lookup_grad(dout, idx, K, table=None, weights=None, scale=1.0, dtable=None, dweights=None,
+                           accumulate=False, ws=None)                                 -> (dtable, dweights)
+  gmm_clip_grad_norm(grads, max_norm, out=None, norm=None, ws=None)                   -> norm
   gmm_check_components(comp_status)          -> (status, first index or -1); synchronises
 
 The estimator calls (score_samples, predict, score, aic, bic, fit with
@@ -31,13 +39,14 @@ from __future__ import annotations
 import ctypes
 
 from . import _abi
-from ._abi import (COV_CODES, GmmError, GmmData, GmmOptions, GmmParams, GmmStats, OP_ESTEP, OP_FIT,
-                   OP_TOPM)
+from ._abi import (COV_CODES, GmmError, GmmData, GmmHead, GmmOptions, GmmParams, GmmStats, GmmTensor, OP_ESTEP,
+                   OP_FIT, OP_TOPM)
 
 __all__ = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step",
            "gmm_predict_proba_topm", "gmm_ivf_workspace_bytes", "gmm_ivf_lists", "gmm_kmeans_workspace_bytes",
            "gmm_kmeans_step", "gmm_fisher_vector_workspace_bytes", "gmm_fisher_vector",
-           "gmm_topk_fit_workspace_bytes", "gmm_topk_fit_step", "new_stats", "GmmError",
+           "gmm_topk_fit_workspace_bytes", "gmm_topk_fit_step", "gmm_softmax_xent", "gmm_softmax_xent_grad",
+           "gmm_codebook_lookup", "gmm_codebook_lookup_grad", "gmm_clip_grad_norm", "new_stats", "GmmError",
            "cov_shape"]
 
 
@@ -358,6 +367,257 @@ def gmm_topk_fit_step(X, w, mu, cv, cov, topk, reg_covar=1e-6, mean_loglik=None,
     _abi.check(_abi.lib().gmm_topk_fit_step(ctypes.byref(d), ctypes.byref(p), int(topk), ctypes.byref(o),
                                             _ptr(mean_loglik), _ptr(comp_status), _ptr(ws), ws.numel(),
                                             _stream(stream)))
+
+
+class _on:
+    """The device of a call's tensors as the current one, and the stream that
+    the call runs on as the current stream (the caller's own, or the device's
+    current one), so that a workspace allocated inside belongs to it."""
+
+    __slots__ = ("guards", "stream")
+
+    def __init__(self, stream, *tensors):
+        torch = _torch()
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and (t.device != dev or not t.is_cuda):
+                raise ValueError(f"every tensor must be on one GPU (got {t.device} and {dev})")
+        # a guard costs microseconds: none where the call changes nothing
+        self.guards = [torch.cuda.device(dev)] if torch.cuda.current_device() != dev.index else []
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+            for t in tensors:  # memory freed by its owner while this stream still reads it
+                if t is not None:
+                    t.record_stream(stream)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+
+    def __enter__(self):
+        for c in self.guards:
+            c.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.guards):
+            c.__exit__(*exc)
+
+
+def _expect(name, t, dtype, shape):
+    """t as the library takes it: a contiguous tensor of one type and shape."""
+    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"(got {t.dtype}, {tuple(t.shape)})")
+
+
+def _rows(name, t):
+    """The gmm_data of rows at any strides that keep D contiguous and rows apart."""
+    torch = _torch()
+    if t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be (N, D) or (B, N, D)")
+    D = int(t.shape[-1])
+    if D < 1 or (t.dim() == 3 and t.shape[0] < 1):
+        raise ValueError(f"{name} needs B >= 1 and D >= 1")
+    if D > 1 and t.numel() > 0 and t.stride(-1) != 1:
+        raise ValueError(f"{name} needs unit stride along D")
+    # strides along an axis of one element mean nothing
+    N = int(t.shape[-2])
+    ld = int(t.stride(-2)) if N > 1 else D
+    if t.dim() == 2:
+        return GmmData(ctypes.c_void_p(t.data_ptr()), _dtype_code(t), 1, N, D, max(ld, D) if N <= 1 else ld, N * ld)
+    B = int(t.shape[0])
+    sb = int(t.stride(0)) if B > 1 else N * ld
+    return GmmData(ctypes.c_void_p(t.data_ptr()), _dtype_code(t), B, N, D, ld, max(sb, N * ld) if N == 0 else sb)
+
+
+def _head(X, W, bias):
+    torch = _torch()
+    h = _rows("W", W)
+    if W.dim() != 2 or W.shape[1] != X.shape[-1] or W.dtype != X.dtype:
+        raise ValueError("W must be (V, D) of the rows' D and type")
+    if bias is not None:
+        _expect("bias", bias, torch.float32, (W.shape[0],))
+    return GmmHead(h.x, h.dtype, h.N, h.ld_x, _ptr(bias))
+
+
+def gmm_softmax_xent(X, W, labels, bias=None, loss=None, lse=None, ws=None, stream=None):
+    """Softmax cross entropy of the rows X ((N, D) or (B, N, D) float32,
+    bfloat16 or float16) under the linear head W (V, D) of their type, with
+    labels (X's leading shape, int32; negative: the row is left out).
+    Returns (loss, lse), float32 of X's leading shape; lse is what
+    gmm_softmax_xent_grad takes."""
+    torch = _torch()
+    d, h = _rows("X", X), _head(X, W, bias)
+    lead = X.shape[:-1]
+    _expect("labels", labels, torch.int32, lead)
+    with _on(stream, X, W, labels, bias, loss, lse, ws) as s:
+        loss = torch.empty(lead, dtype=torch.float32, device=X.device) if loss is None else loss
+        lse = torch.empty(lead, dtype=torch.float32, device=X.device) if lse is None else lse
+        _expect("loss", loss, torch.float32, lead)
+        _expect("lse", lse, torch.float32, lead)
+        if ws is None:
+            n = int(_abi.lib().gmm_softmax_xent_workspace_bytes(ctypes.byref(d), ctypes.byref(h)))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=X.device)
+        _abi.check(_abi.lib().gmm_softmax_xent(ctypes.byref(d), ctypes.byref(h), _ptr(labels), _ptr(loss), _ptr(lse),
+                                               _ptr(ws), ws.numel() * ws.element_size(), s))
+    return loss, lse
+
+
+def _wanted(given, like, shape, dtype):
+    """A gradient's buffer: the caller's, none (False), or a new one (None)."""
+    torch = _torch()
+    if given is False:
+        return None
+    return torch.empty(shape, dtype=dtype, device=like.device) if given is None else given
+
+
+def gmm_softmax_xent_grad(X, W, labels, lse, gloss=None, bias=None, dX=None, dW=None, dbias=None, accumulate=False,
+                          ws=None, stream=None):
+    """Gradients of sum_i gloss_i loss_i (gloss: float32 of X's leading shape,
+    None: ones) with the lse of gmm_softmax_xent: (dX, dW, dbias), dX (X's
+    shape) and dW (V, D) in the rows' type, dbias (V,) float32 (None without a
+    bias).  Buffers not given are allocated; False leaves one out.
+    accumulate=True adds to the buffers, all of which are then given."""
+    torch = _torch()
+    d, h = _rows("X", X), _head(X, W, bias)
+    lead = X.shape[:-1]
+    _expect("labels", labels, torch.int32, lead)
+    _expect("lse", lse, torch.float32, lead)
+    if gloss is not None:
+        _expect("gloss", gloss, torch.float32, lead)
+    if bias is None and dbias is None:
+        dbias = False
+    if accumulate and any(t is None for t in (dX, dW, dbias)):
+        raise ValueError("accumulate=True adds to given buffers (False leaves a gradient out)")
+    given = [t for t in (dX, dW, dbias) if t is not None and t is not False]
+    with _on(stream, X, W, labels, lse, gloss, bias, ws, *given) as s:
+        dX, dW = _wanted(dX, X, X.shape, X.dtype), _wanted(dW, W, W.shape, W.dtype)
+        dbias = _wanted(dbias, W, (W.shape[0],), torch.float32)
+        for name, t, like in (("dX", dX, X), ("dW", dW, W)):
+            if t is not None:
+                _expect(name, t, like.dtype, like.shape)
+        if dbias is not None:
+            _expect("dbias", dbias, torch.float32, (W.shape[0],))
+        if ws is None:
+            want = (dX is not None) + 2 * (dW is not None) + 4 * (dbias is not None)
+            n = int(_abi.lib().gmm_softmax_xent_grad_workspace_bytes(ctypes.byref(d), ctypes.byref(h), want))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=X.device)
+        _abi.check(_abi.lib().gmm_softmax_xent_grad(ctypes.byref(d), ctypes.byref(h), _ptr(labels), _ptr(lse),
+                                                    _ptr(gloss), _ptr(dX), _ptr(dW), _ptr(dbias),
+                                                    int(bool(accumulate)), _ptr(ws), ws.numel() * ws.element_size(),
+                                                    s))
+    return dX, dW, dbias
+
+
+def _code_shape(rows_dim, idx, weights):
+    """(B, N, m) of codes of rows with rows_dim axes: (N,) or (N, m), with a
+    leading B where the rows have one; m = 1 codes may leave their axis out."""
+    torch = _torch()
+    if idx.dtype != torch.int32 or not idx.is_contiguous():
+        raise ValueError("idx must be a contiguous int32 tensor")
+    if idx.dim() not in (rows_dim - 1, rows_dim):
+        raise ValueError(f"idx must have {rows_dim - 1} or {rows_dim} axes beside rows of {rows_dim}")
+    if weights is not None:
+        _expect("weights", weights, torch.float32, idx.shape)
+    lead = idx.shape if idx.dim() == rows_dim - 1 else idx.shape[:-1]
+    m = 1 if idx.dim() == rows_dim - 1 else int(idx.shape[-1])
+    return (int(lead[0]) if rows_dim == 3 else 1), int(lead[-1]), m, tuple(lead)
+
+
+def gmm_codebook_lookup(table, idx, weights=None, scale=1.0, out=None, stream=None):
+    """Rows rebuilt from codes: out_i = scale * sum_j weights_ij table[idx_ij]
+    over a row's leading codes in [0, K).  table (K, D) or (B, K, D) float32,
+    bfloat16 or float16; idx (N,), (N, m) (a leading B beside a table with
+    one) int32; weights of idx's shape, float32 (None: 1).  Returns
+    idx's leading shape + (D,), in the table's type."""
+    torch = _torch()
+    d = _rows("table", table)
+    B, N, m, lead = _code_shape(table.dim(), idx, weights)
+    if B != d.B:
+        raise ValueError("idx and table differ in B")
+    shape = lead + (int(d.D),)
+    with _on(stream, table, idx, weights, out) as s:
+        out = torch.empty(shape, dtype=table.dtype, device=table.device) if out is None else out
+        _expect("out", out, table.dtype, shape)
+        _abi.check(_abi.lib().gmm_codebook_lookup(ctypes.byref(d), N, m, _ptr(idx), _ptr(weights), float(scale),
+                                                  _ptr(out), s))
+    return out
+
+
+def gmm_codebook_lookup_grad(dout, idx, K, table=None, weights=None, scale=1.0, dtable=None, dweights=None,
+                             accumulate=False, ws=None, stream=None):
+    """Gradients of gmm_codebook_lookup for the rows' gradient dout ((N, D) or
+    (B, N, D)): (dtable, dweights), dtable (K, D) or (B, K, D) in dout's type,
+    dweights of idx's shape, float32 (None without weights or a table).
+    Buffers not given are allocated; False leaves one out.  accumulate=True
+    adds to the given dtable."""
+    torch = _torch()
+    d = _rows("dout", dout)
+    B, N, m, lead = _code_shape(dout.dim(), idx, weights)
+    if (B, N) != (d.B, d.N):
+        raise ValueError("idx and dout differ in their rows")
+    t = None
+    if table is not None:
+        if table.dtype != dout.dtype or table.dim() != dout.dim() or table.shape[-1] != dout.shape[-1] \
+                or table.shape[-2] != K or (dout.dim() == 3 and table.shape[0] != dout.shape[0]):
+            raise ValueError("table must be (K, D) or (B, K, D) of dout's type, B and D")
+        t = _rows("table", table)
+    if dweights is None and (table is None or weights is None):
+        dweights = False
+    if dweights is not False and table is None:
+        raise ValueError("dweights needs the table")
+    if accumulate and dtable is None:
+        raise ValueError("accumulate=True adds to a given dtable")
+    K = int(K)
+    shape = (K, int(d.D)) if dout.dim() == 2 else (B, K, int(d.D))
+    given = [x for x in (dtable, dweights) if x is not None and x is not False]
+    with _on(stream, dout, idx, table, weights, ws, *given) as s:
+        dtable = _wanted(dtable, dout, shape, dout.dtype)
+        dweights = _wanted(dweights, dout, idx.shape, torch.float32)
+        if dtable is not None:
+            _expect("dtable", dtable, dout.dtype, shape)
+        if dweights is not None:
+            _expect("dweights", dweights, torch.float32, idx.shape)
+        if ws is None:
+            n = 0
+            if dtable is not None:
+                n = int(_abi.lib().gmm_codebook_lookup_grad_workspace_bytes(ctypes.byref(d), K, m))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dout.device)
+        _abi.check(_abi.lib().gmm_codebook_lookup_grad(
+            ctypes.byref(d), K, m, _ptr(idx), _ptr(weights), float(scale),
+            ctypes.byref(t) if t is not None else None, _ptr(dtable), _ptr(dweights), int(bool(accumulate)), _ptr(ws),
+            ws.numel() * ws.element_size(), s))
+    return dtable, dweights
+
+
+def gmm_clip_grad_norm(grads, max_norm, out=None, norm=None, ws=None, stream=None):
+    """The 2-norm over all the gradients (a list of contiguous float32,
+    bfloat16 or float16 tensors), which are scaled by min(1, max_norm /
+    (norm + 1e-6)) in place, or into the tensors of out (same shapes and
+    types).  Returns the norm before the scaling, (1,) float32."""
+    torch = _torch()
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("need one gradient or more")
+    if len(outs) != len(grads):
+        raise ValueError("out must hold one tensor per gradient")
+    desc = (GmmTensor * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if g.dtype not in (torch.float32, torch.bfloat16, torch.float16) or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be a contiguous float32, bfloat16 or float16 tensor")
+        if o is not g:
+            _expect(f"out[{i}]", o, g.dtype, g.shape)
+        desc[i] = GmmTensor(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
+    with _on(stream, *grads, *outs, norm, ws) as s:
+        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device) if norm is None else norm
+        _expect("norm", norm, torch.float32, (1,))
+        if ws is None:
+            n = int(_abi.lib().gmm_clip_grad_norm_workspace_bytes(len(grads)))
+            ws = torch.empty(n, dtype=torch.uint8, device=grads[0].device)
+        _abi.check(_abi.lib().gmm_clip_grad_norm(desc, len(grads), float(max_norm), _ptr(norm), _ptr(ws),
+                                                 ws.numel() * ws.element_size(), s))
+    return norm
 
 
 def gmm_check_components(comp_status):

@@ -24,6 +24,9 @@ EXPORTED = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step
             "gmm_predict_proba_topm", "gmm_ivf_workspace_bytes", "gmm_ivf_lists", "gmm_kmeans_workspace_bytes",
             "gmm_kmeans_step", "gmm_fisher_vector_workspace_bytes", "gmm_fisher_vector",
             "gmm_topk_fit_workspace_bytes", "gmm_topk_fit_step", "gmm_kde_workspace_bytes", "gmm_kde_score",
+            "gmm_softmax_xent_workspace_bytes", "gmm_softmax_xent", "gmm_softmax_xent_grad_workspace_bytes",
+            "gmm_softmax_xent_grad", "gmm_codebook_lookup", "gmm_codebook_lookup_grad_workspace_bytes",
+            "gmm_codebook_lookup_grad", "gmm_clip_grad_norm_workspace_bytes", "gmm_clip_grad_norm",
             "gmm_check_components", "gmm_status_str",
             "gmm_last_error", "gmm_version"]
 
@@ -47,6 +50,16 @@ class GmmStats(ctypes.Structure):
 class GmmOptions(ctypes.Structure):
     _fields_ = [("reg_covar", ctypes.c_double), ("flags", ctypes.c_uint32),
                 ("event_begin", ctypes.c_void_p), ("event_end", ctypes.c_void_p)]
+
+
+class GmmHead(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("V", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("bias", ctypes.c_void_p)]
+
+
+class GmmTensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 class GmmError(RuntimeError):
@@ -109,6 +122,24 @@ def lib() -> ctypes.CDLL:
         L.gmm_topk_fit_workspace_bytes.restype = ctypes.c_size_t
         L.gmm_topk_fit_step.argtypes = [ctypes.POINTER(GmmData), ctypes.POINTER(GmmParams), ctypes.c_int32,
                                         ctypes.POINTER(GmmOptions), P, P, P, ctypes.c_size_t, P]
+        D, H = ctypes.POINTER(GmmData), ctypes.POINTER(GmmHead)
+        L.gmm_softmax_xent_workspace_bytes.argtypes = [D, H]
+        L.gmm_softmax_xent.argtypes = [D, H, P, P, P, P, ctypes.c_size_t, P]
+        L.gmm_softmax_xent_grad_workspace_bytes.argtypes = [D, H, ctypes.c_int32]
+        L.gmm_softmax_xent_grad.argtypes = [D, H, P, P, P, P, P, P, ctypes.c_int32, P, ctypes.c_size_t, P]
+        L.gmm_codebook_lookup.argtypes = [D, ctypes.c_int64, ctypes.c_int32, P, P, ctypes.c_float, P, P]
+        L.gmm_codebook_lookup_grad_workspace_bytes.argtypes = [D, ctypes.c_int64, ctypes.c_int32]
+        L.gmm_codebook_lookup_grad.argtypes = [D, ctypes.c_int64, ctypes.c_int32, P, P, ctypes.c_float, D, P, P,
+                                               ctypes.c_int32, P, ctypes.c_size_t, P]
+        L.gmm_clip_grad_norm_workspace_bytes.argtypes = [ctypes.c_int32]
+        L.gmm_clip_grad_norm.argtypes = [ctypes.POINTER(GmmTensor), ctypes.c_int32, ctypes.c_double, P, P,
+                                         ctypes.c_size_t, P]
+        for f in (L.gmm_softmax_xent_workspace_bytes, L.gmm_softmax_xent_grad_workspace_bytes,
+                  L.gmm_codebook_lookup_grad_workspace_bytes, L.gmm_clip_grad_norm_workspace_bytes):
+            f.restype = ctypes.c_size_t
+        for f in (L.gmm_softmax_xent, L.gmm_softmax_xent_grad, L.gmm_codebook_lookup, L.gmm_codebook_lookup_grad,
+                  L.gmm_clip_grad_norm):
+            f.restype = ctypes.c_int
         for f in (L.gmm_estep_stats, L.gmm_mstep, L.gmm_fit_step, L.gmm_fit, L.gmm_fit_step_noalloc, L.gmm_fit_step_streamed,
                   L.gmm_predict_proba_topm,
                   L.gmm_ivf_lists,

@@ -13,6 +13,7 @@
 #include <cmath>
 #include <mutex>
 #include <string>
+#include <vector>
 
 namespace gmm {
 
@@ -1307,6 +1308,290 @@ gmm_status gmm_kde_score(const gmm_data* queries, const float* ref, int64_t M, i
   a.out = logdens;
   e = launch_kde(a, L.DP, s);
   if (e != hipSuccess) return hip_fail(e, "kernel density launch");
+  return GMM_OK;
+}
+
+// ---- softmax cross entropy under a linear head
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char *p = (const char*)a, *q = (const char*)b;
+  return p && q && na > 0 && nb > 0 && p < q + nb && q < p + na;
+}
+
+// bytes from the first to the last element of a strided operand
+static int64_t data_span(const gmm_data* d, int64_t es) {
+  if (d->N == 0) return 0;
+  return ((d->B > 1 ? (d->B - 1) * d->stride_b : 0) + (d->N - 1) * d->ld_x + d->D) * es;
+}
+
+static gmm_status xent_args(const gmm_data* d, const gmm_head* h, XentArgs* a) {
+  gmm_status st = check_data(d);
+  if (st != GMM_OK) return st;
+  if (!h) return fail(GMM_ERR_INVALID_ARG, "head descriptor is NULL");
+  if (h->V < 1) return fail(GMM_ERR_INVALID_ARG, "V must be >= 1 (got %lld)", (long long)h->V);
+  if (!h->w) return fail(GMM_ERR_INVALID_ARG, "head w is NULL");
+  if (h->ld_w < d->D) return fail(GMM_ERR_INVALID_ARG, "ld_w (%lld) < D (%lld)", (long long)h->ld_w, (long long)d->D);
+  if (h->dtype != d->dtype)
+    return fail(h->dtype >= GMM_DT_F32 && h->dtype <= GMM_DT_F16 ? GMM_ERR_UNSUPPORTED : GMM_ERR_INVALID_ARG,
+                "the head's dtype (%d) must be the rows' (%d)", h->dtype, d->dtype);
+  if (d->D > 65536) return fail(GMM_ERR_UNSUPPORTED, "D (%lld) > 65536", (long long)d->D);
+  if (h->V >= ((int64_t)1 << 31)) return fail(GMM_ERR_UNSUPPORTED, "V must stay below 2^31");
+  if (d->N > 0 && d->B > (((int64_t)1 << 31) - 1) / d->N) return fail(GMM_ERR_UNSUPPORTED, "B*N must stay below 2^31");
+  a->x = d->x;
+  a->w = h->w;
+  a->bias = h->bias;
+  a->labels = nullptr;
+  a->dtype = d->dtype;
+  a->es = d->dtype == GMM_DT_F32 ? 4 : 2;
+  a->B = d->B;
+  a->N = d->N;
+  a->D = d->D;
+  a->V = h->V;
+  a->ld = d->ld_x;
+  a->stride_b = d->B > 1 ? d->stride_b : 0;
+  a->ld_w = h->ld_w;
+  if ((uintptr_t)a->x % a->es || (uintptr_t)a->w % a->es)
+    return fail(GMM_ERR_INVALID_ARG, "rows and head must be aligned to their elements");
+  return GMM_OK;
+}
+
+static gmm_status check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || ((uintptr_t)ws) % kAlign != 0) return fail(GMM_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (have < need) return fail(GMM_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", have, need);
+  return GMM_OK;
+}
+
+size_t gmm_softmax_xent_workspace_bytes(const gmm_data* rows, const gmm_head* head) {
+  XentArgs a;
+  if (xent_args(rows, head, &a) != GMM_OK) return 0;
+  return std::max(kAlign, xent_plan(a, false, false, false, false).bytes);
+}
+
+gmm_status gmm_softmax_xent(const gmm_data* rows, const gmm_head* head, const int32_t* labels, float* loss, float* lse,
+                            void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  XentArgs a;
+  gmm_status st = xent_args(rows, head, &a);
+  if (st != GMM_OK) return st;
+  const int64_t R = a.B * a.N;
+  if (R > 0 && (!labels || !loss || !lse)) return fail(GMM_ERR_INVALID_ARG, "labels, loss and lse must be non-NULL");
+  if (overlap(loss, 4 * R, lse, 4 * R)) return fail(GMM_ERR_INVALID_ARG, "loss and lse overlap");
+  const XentPlan p = xent_plan(a, false, false, false, false);
+  if ((st = check_ws(ws, ws_bytes, std::max(kAlign, p.bytes))) != GMM_OK) return st;
+  if (R == 0) return GMM_OK;
+  a.labels = labels;
+  const hipError_t e = launch_xent(a, p, loss, lse, static_cast<char*>(ws), (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "softmax cross entropy launch");
+  return GMM_OK;
+}
+
+size_t gmm_softmax_xent_grad_workspace_bytes(const gmm_data* rows, const gmm_head* head, int32_t want) {
+  XentArgs a;
+  if (xent_args(rows, head, &a) != GMM_OK) return 0;
+  return std::max(kAlign, xent_plan(a, true, want & 1, want & 2, want & 4).bytes);
+}
+
+gmm_status gmm_softmax_xent_grad(const gmm_data* rows, const gmm_head* head, const int32_t* labels, const float* lse,
+                                 const float* gloss, void* dx, void* dw, float* dbias, int32_t accumulate, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  g_err.clear();
+  XentArgs a;
+  gmm_status st = xent_args(rows, head, &a);
+  if (st != GMM_OK) return st;
+  const int64_t R = a.B * a.N;
+  if (R > 0 && (!labels || !lse)) return fail(GMM_ERR_INVALID_ARG, "labels and lse must be non-NULL");
+  if (!dx && !dw && !dbias) return fail(GMM_ERR_INVALID_ARG, "one of dx, dw and dbias must be non-NULL");
+  const int64_t nx = R * a.D * a.es, nw = a.V * a.D * a.es, nb = a.V * 4;
+  const int64_t sx = data_span(rows, a.es), sw = ((a.V - 1) * a.ld_w + a.D) * a.es;
+  const struct {
+    const void* p;
+    int64_t n;
+  } out[3] = {{dx, nx}, {dw, nw}, {dbias, nb}}, in[6] = {{a.x, sx},       {a.w, sw},    {a.bias, nb},
+                                                         {labels, 4 * R}, {lse, 4 * R}, {gloss, 4 * R}};
+  for (int i = 0; i < 3; ++i) {
+    if ((uintptr_t)out[i].p % (i < 2 ? a.es : 4)) return fail(GMM_ERR_INVALID_ARG, "a gradient is misaligned");
+    for (int j = 0; j < 6; ++j)
+      if (overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+        return fail(GMM_ERR_INVALID_ARG, "a gradient overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(GMM_ERR_INVALID_ARG, "two gradients overlap");
+  }
+  const XentPlan p = xent_plan(a, true, dx, dw, dbias);
+  if ((st = check_ws(ws, ws_bytes, std::max(kAlign, p.bytes))) != GMM_OK) return st;
+  if (R == 0) {  // sums over no rows
+    hipError_t e = hipSuccess;
+    if (!accumulate && dw) e = launch_zero(dw, nw, (hipStream_t)stream);
+    if (!accumulate && dbias && e == hipSuccess) e = launch_zero(dbias, nb, (hipStream_t)stream);
+    return e == hipSuccess ? GMM_OK : hip_fail(e, "gradient zero launch");
+  }
+  a.labels = labels;
+  const hipError_t e =
+      launch_xent_grad(a, p, lse, gloss, dx, dw, dbias, accumulate != 0, static_cast<char*>(ws), (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "softmax cross entropy gradient launch");
+  return GMM_OK;
+}
+
+// ---- codebook lookup
+static gmm_status lookup_check(int64_t B, int64_t N, int32_t m, int64_t K, int64_t D) {
+  if (m < 1) return fail(GMM_ERR_INVALID_ARG, "m must be >= 1 (got %d)", m);
+  if (K < 1) return fail(GMM_ERR_INVALID_ARG, "K must be >= 1 (got %lld)", (long long)K);
+  if (N < 0) return fail(GMM_ERR_INVALID_ARG, "N must be >= 0");
+  const int64_t lim = ((int64_t)1 << 31) - 1;
+  if (N > 0 && (B > lim / N || B * N > lim / m)) return fail(GMM_ERR_UNSUPPORTED, "B*N*m must stay below 2^31");
+  if (K > lim / B) return fail(GMM_ERR_UNSUPPORTED, "B*K must stay below 2^31");
+  if (D > 65536) return fail(GMM_ERR_UNSUPPORTED, "D (%lld) > 65536", (long long)D);
+  return GMM_OK;
+}
+
+gmm_status gmm_codebook_lookup(const gmm_data* table, int64_t N, int32_t m, const int32_t* idx, const float* weights,
+                               float scale, void* out, void* stream) {
+  g_err.clear();
+  gmm_status st = check_data(table);
+  if (st != GMM_OK) return st;
+  st = lookup_check(table->B, N, m, table->N, table->D);
+  if (st != GMM_OK) return st;
+  const int64_t R = table->B * N, es = table->dtype == GMM_DT_F32 ? 4 : 2;
+  if (R > 0 && (!idx || !out)) return fail(GMM_ERR_INVALID_ARG, "idx and out must be non-NULL");
+  if ((uintptr_t)table->x % es || (uintptr_t)out % es)
+    return fail(GMM_ERR_INVALID_ARG, "table and out must be aligned to their elements");
+  if (overlap(out, R * table->D * es, table->x, data_span(table, es)) || overlap(out, R * table->D * es, idx, 4 * R * m) ||
+      overlap(out, R * table->D * es, weights, 4 * R * m))
+    return fail(GMM_ERR_INVALID_ARG, "out overlaps an input");
+  if (R == 0) return GMM_OK;
+  LookupArgs a{};
+  a.table = table->x;
+  a.ld = table->ld_x;
+  a.stride_b = table->B > 1 ? table->stride_b : 0;
+  a.idx = idx;
+  a.weights = weights;
+  a.scale = scale;
+  a.dtype = table->dtype;
+  a.m = m;
+  a.B = table->B;
+  a.N = N;
+  a.K = table->N;
+  a.D = table->D;
+  a.out = out;
+  const hipError_t e = launch_lookup(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "codebook lookup launch");
+  return GMM_OK;
+}
+
+size_t gmm_codebook_lookup_grad_workspace_bytes(const gmm_data* dout, int64_t K, int32_t m) {
+  if (check_data(dout) != GMM_OK || lookup_check(dout->B, dout->N, m, K, dout->D) != GMM_OK) return 0;
+  return std::max(kAlign, lookup_plan(dout->B, dout->N, m, K, dout->D, true).bytes);
+}
+
+gmm_status gmm_codebook_lookup_grad(const gmm_data* dout, int64_t K, int32_t m, const int32_t* idx, const float* weights,
+                                    float scale, const gmm_data* table, void* dtable, float* dweights, int32_t accumulate,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  gmm_status st = check_data(dout);
+  if (st != GMM_OK) return st;
+  st = lookup_check(dout->B, dout->N, m, K, dout->D);
+  if (st != GMM_OK) return st;
+  const int64_t R = dout->B * dout->N, es = dout->dtype == GMM_DT_F32 ? 4 : 2;
+  if (!dtable && !dweights) return fail(GMM_ERR_INVALID_ARG, "one of dtable and dweights must be non-NULL");
+  if (R > 0 && !idx) return fail(GMM_ERR_INVALID_ARG, "idx must be non-NULL");
+  if ((uintptr_t)dout->x % es || (uintptr_t)dtable % es)
+    return fail(GMM_ERR_INVALID_ARG, "dout and dtable must be aligned to their elements");
+  if (dweights) {
+    st = check_data(table);
+    if (st != GMM_OK) return st;
+    if (table->B != dout->B || table->N != K || table->D != dout->D)
+      return fail(GMM_ERR_INVALID_ARG, "the table must be (B, K, D) of dout's B and D");
+    if (table->dtype != dout->dtype) return fail(GMM_ERR_UNSUPPORTED, "the table's dtype must be dout's");
+    if ((uintptr_t)table->x % es) return fail(GMM_ERR_INVALID_ARG, "the table must be aligned to its elements");
+  }
+  const int64_t nt = dout->B * K * dout->D * es, nw = 4 * R * m;
+  const void* in[4] = {dout->x, idx, weights, dweights ? table->x : nullptr};
+  const int64_t nin[4] = {data_span(dout, es), nw, nw, dweights ? data_span(table, es) : 0};
+  for (int i = 0; i < 4; ++i)
+    if (overlap(dtable, nt, in[i], nin[i]) || overlap(dweights, nw, in[i], nin[i]))
+      return fail(GMM_ERR_INVALID_ARG, "a gradient overlaps an input");
+  if (overlap(dtable, nt, dweights, nw)) return fail(GMM_ERR_INVALID_ARG, "two gradients overlap");
+  const LookupPlan p = lookup_plan(dout->B, dout->N, m, K, dout->D, dtable != nullptr);
+  if ((st = check_ws(ws, ws_bytes, std::max(kAlign, p.bytes))) != GMM_OK) return st;
+  LookupArgs a{};
+  if (dweights) {
+    a.table = table->x;
+    a.ld = table->ld_x;
+    a.stride_b = table->B > 1 ? table->stride_b : 0;
+  }
+  a.dout = dout->x;
+  a.ld_g = dout->ld_x;
+  a.stride_g = dout->B > 1 ? dout->stride_b : 0;
+  a.idx = idx;
+  a.weights = weights;
+  a.scale = scale;
+  a.dtype = dout->dtype;
+  a.m = m;
+  a.accumulate = accumulate != 0;
+  a.B = dout->B;
+  a.N = dout->N;
+  a.K = K;
+  a.D = dout->D;
+  a.dtable = dtable;
+  a.dweights = dweights;
+  const hipError_t e = launch_lookup_grad(a, p, static_cast<char*>(ws), (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "codebook gradient launch");
+  return GMM_OK;
+}
+
+// ---- gradient norm and clipping
+size_t gmm_clip_grad_norm_workspace_bytes(int32_t count) {
+  if (count < 1) return 0;
+  const size_t launches = ((size_t)count + kClipTensors - 1) / kClipTensors;
+  return align_up(sizeof(double) * kClipParts * launches) + kAlign;
+}
+
+gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max_norm, float* norm, void* ws,
+                              size_t ws_bytes, void* stream) {
+  g_err.clear();
+  if (!grads || count < 1) return fail(GMM_ERR_INVALID_ARG, "need one gradient or more");
+  if (!(max_norm >= 0.0)) return fail(GMM_ERR_INVALID_ARG, "max_norm must be >= 0");
+  std::vector<ClipTensor> t;
+  struct Span {
+    const char *p, *q;
+    int tensor;
+    bool out;
+  };
+  std::vector<Span> spans;
+  try {
+    t.resize(count);
+    spans.reserve(2 * (size_t)count);
+  } catch (...) {
+    return fail(GMM_ERR_INVALID_ARG, "no host memory for %d gradients", count);
+  }
+  for (int i = 0; i < count; ++i) {
+    const gmm_tensor& g = grads[i];
+    if (g.dtype != GMM_DT_F32 && g.dtype != GMM_DT_BF16 && g.dtype != GMM_DT_F16)
+      return fail(GMM_ERR_INVALID_ARG, "gradient %d: unknown dtype %d", i, g.dtype);
+    if (g.n < 0) return fail(GMM_ERR_INVALID_ARG, "gradient %d: n must be >= 0", i);
+    if (g.n >= ((int64_t)1 << 40)) return fail(GMM_ERR_UNSUPPORTED, "gradient %d: too large", i);
+    const int64_t es = g.dtype == GMM_DT_F32 ? 4 : 2;
+    if (g.n > 0 && (!g.src || !g.dst)) return fail(GMM_ERR_INVALID_ARG, "gradient %d: src and dst must be non-NULL", i);
+    if (((uintptr_t)g.src | (uintptr_t)g.dst) % es) return fail(GMM_ERR_INVALID_ARG, "gradient %d is misaligned", i);
+    t[i] = ClipTensor{g.src, g.dst, g.n, 0, g.dtype};
+    if (g.n == 0) continue;
+    const char *src = (const char*)g.src, *dst = (const char*)g.dst;
+    spans.push_back({dst, dst + g.n * es, i, true});
+    if (src != dst) spans.push_back({src, src + g.n * es, i, false});
+  }
+  // no output may overlap another tensor's input or output, nor its own input in part
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.p < b.p; });
+  const char *end_any = nullptr, *end_out = nullptr;
+  for (const Span& s : spans) {
+    if (s.out ? s.p < end_any : s.p < end_out) return fail(GMM_ERR_INVALID_ARG, "gradient %d overlaps another tensor", s.tensor);
+    end_any = std::max(end_any, s.q);
+    if (s.out) end_out = std::max(end_out, s.q);
+  }
+  const size_t need = gmm_clip_grad_norm_workspace_bytes(count);
+  gmm_status st = check_ws(ws, ws_bytes, need);
+  if (st != GMM_OK) return st;
+  double* part = static_cast<double*>(ws);
+  float* coef = reinterpret_cast<float*>(static_cast<char*>(ws) + need - kAlign);
+  const hipError_t e = launch_clip(t.data(), count, max_norm, norm, part, coef, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "gradient clipping launch");
   return GMM_OK;
 }
 

@@ -281,6 +281,88 @@ hipError_t launch_kmeans_update(const void* x, int xtype, int64_t B, int64_t N, 
                                 int D, const int64_t* offsets, const int32_t* rows, float* C, int64_t* counts,
                                 double* ip, double* inertia, hipStream_t s);
 
+// softmax cross entropy under a linear head (gmm_xent.hip)
+struct XentArgs {
+  const void* x;                 // rows: problem b, row i, feature d at x[b stride_b + i ld + d]
+  const void* w;                 // head: class v, feature d at w[v ld_w + d]
+  const float* bias;             // (V) or null
+  const int32_t* labels;         // (B, N)
+  int dtype, es;                 // gmm_dtype of rows and head, its bytes
+  int64_t B, N, D, V, ld, stride_b, ld_w;
+};
+struct XentPlan {
+  bool skinny, pack_x, pack_w;   // few rows; rows / head copied to aligned rows first
+  bool slab_x, slab_w;           // products summed in float32 slabs
+  int kbytes, split_x, split_w;
+  int64_t Dp, nc, vc;            // padded D of the copies; rows of a chunk, classes of a piece
+  int64_t np_r, np_v, ldg, ldgt, lds;
+  size_t off_part, off_lab, off_coef, off_bmax, off_scal, off_G, off_GT, off_XT, off_WT, off_dbp, off_sx, off_sw, off_px,
+      off_pw, bytes;
+};
+XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db);
+hipError_t launch_xent(const XentArgs& a, const XentPlan& p, float* loss, float* lse, char* ws, hipStream_t s);
+hipError_t launch_xent_grad(const XentArgs& a, const XentPlan& p, const float* lse, const float* gloss, void* dx, void* dw,
+                            float* db, int accumulate, char* ws, hipStream_t s);
+
+// codebook lookup and its gradients (gmm_lookup.hip)
+struct LookupArgs {
+  const void* table;       // problem b, code k, feature d at table[b stride_b + k ld + d]
+  int64_t ld, stride_b;
+  const void* dout;        // problem b, row i, feature d at dout[b stride_g + i ld_g + d]
+  int64_t ld_g, stride_g;
+  const int32_t* idx;      // (B, N, m)
+  const float* weights;    // (B, N, m) or null
+  float scale;
+  int dtype, m, accumulate;
+  int64_t B, N, K, D;
+  void* out;               // (B, N, D)
+  void* dtable;            // (B, K, D) or null
+  float* dweights;         // (B, N, m) or null
+};
+constexpr int kSortBlock = 4096;  // entries per workgroup of the sort
+struct SortPass {
+  int64_t S, nblk;
+  uint32_t none;           // key of the entries that take no part: past every code
+  int shift, bits, bins;
+  const uint32_t *kin, *sin;  // keys and entries; null: the first pass reads the codes
+  uint32_t *kout, *sout, *hist, *base;
+};
+struct SumArgs {
+  int64_t S, C, chunks, Dp;
+  uint32_t none;
+  const uint32_t *key, *src;
+  float* part;             // (chunks, 2, Dp): partial sums of the run at a chunk's start / end
+};
+struct LookupPlan {
+  int64_t S, nblk, C, chunks, Dp;
+  uint32_t none;
+  int passes, bits;
+  size_t off_key[2], off_src[2], off_hist, off_base, off_part, bytes;
+};
+LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, bool want_table);
+hipError_t launch_lookup(const LookupArgs& a, hipStream_t s);
+hipError_t launch_lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipStream_t s);
+hipError_t launch_zero(void* p, int64_t bytes, hipStream_t s);
+
+// gradient norm and clipping (gmm_clip.hip)
+constexpr int kClipTensors = 64;     // tensors per launch (their descriptions are kernel arguments)
+constexpr int64_t kClipPiece = 8192; // elements per piece
+constexpr int kClipParts = 2048;     // workgroups (partial sums) per launch at most
+struct ClipTensor {
+  const void* src;
+  void* dst;
+  int64_t n, piece0;
+  int32_t dtype;
+};
+struct ClipArgs {
+  ClipTensor t[kClipTensors];
+  int count;
+  int64_t pieces;
+  double* part;
+};
+hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, float* coef,
+                       hipStream_t s);
+
 // fused E-step + statistics (gmm_estep.hip)
 hipError_t launch_estep(const Plan& p, const EStepArgs& a, hipStream_t s);
 // blocked components: mode 1 the per-(row, block) (max, sum) pass, 2 the

@@ -1,0 +1,533 @@
+// gmm_lookup.hip -- rows rebuilt from codes (a codebook or embedding lookup
+// with weights and a scale), and the gradients of that lookup.
+//
+// What it computes.  Row i of a problem has up to m codes idx_i0 .. idx_i,m-1
+// (its leading values in [0, K); the first value outside ends the row) with
+// weights w_ij (1 where none are given), as the multi-assignment writes them:
+//   out_i = s sum_j w_ij T[idx_ij]
+//   dT_k  = s sum over the entries (i, j) with idx_ij = k of w_ij dout_i
+//   dw_ij = s <dout_i, T[idx_ij]>
+// Sums are float32, rounded once to the rows' type.
+//
+// How.
+//   lookup   a thread per 16 bytes of a row; the row's codes are read by every
+//            thread of the row (one address, the L1 serves it).
+//   dw       a group of up to 64 lanes per row, the dot products over it.
+//   dT       deterministic, no atomics: the entries are sorted by code (a
+//            stable radix sort of at most 10 bits a pass: block histograms,
+//            their prefixes, ranks by ballot), then summed in that order in
+//            chunks of entries.  A run of one code inside a chunk is written
+//            at once; a run that crosses a chunk's ends leaves partial sums,
+//            which a last kernel joins, so that a code with most of the
+//            entries is summed by as many workgroups as many codes are.
+// Bound by memory: every dout row is read once per entry, every dT row
+// written once.
+#include "gmm_internal.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace gmm {
+
+namespace {
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes at any alignment of their element
+template <typename T>
+struct Vec {
+  static constexpr int E = 16 / (int)sizeof(T);
+  float v[E];
+  __device__ void load(const T* p, int n) {  // n: elements that exist (E or more: all)
+    if (n >= E) {
+      T t[E];
+      __builtin_memcpy(t, p, 16);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = (float)t[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = e < n ? (float)p[e] : 0.f;
+    }
+  }
+  __device__ void store(T* p, int n) const {
+    if (n >= E) {
+      T t[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) t[e] = (T)v[e];
+      __builtin_memcpy(p, t, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < n) p[e] = (T)v[e];
+    }
+  }
+};
+
+// lanes per row: a power of two, 2^lg
+struct RowSplit {
+  int lg, slabs;
+};
+
+template <typename T>
+__device__ inline void lookup_row(const LookupArgs& A, int64_t row, int64_t d, int n) {
+  constexpr int E = Vec<T>::E;
+  const int64_t b = A.B == 1 ? 0 : row / A.N;
+  const T* t = reinterpret_cast<const T*>(A.table) + b * A.stride_b + d;
+  const int32_t* ix = A.idx + row * A.m;
+  const float* w = A.weights ? A.weights + row * A.m : nullptr;
+  Vec<T> acc;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc.v[e] = 0.f;
+  constexpr int U = 4;  // rows of the table in flight
+  for (int j0 = 0; j0 < A.m; j0 += U) {
+    int k[U];
+    float wj[U];
+    bool live = true;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u] = j0 + u < A.m ? ix[j0 + u] : -1;
+      live = live && k[u] >= 0 && k[u] < A.K;
+      if (!live) k[u] = -1;
+      wj[u] = w && j0 + u < A.m ? w[j0 + u] : 1.f;
+    }
+    Vec<T> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k[u] >= 0) r[u].load(t + k[u] * A.ld, n);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k[u] >= 0)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc.v[e] = fmaf(wj[u], r[u].v[e], acc.v[e]);
+    if (!live) break;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc.v[e] *= A.scale;
+  acc.store(reinterpret_cast<T*>(A.out) + row * A.D + d, n);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) lookup_kernel(LookupArgs A, RowSplit S) {
+  constexpr int E = Vec<T>::E;
+  const int64_t d = ((int64_t)blockIdx.y << S.lg | (threadIdx.x & ((1 << S.lg) - 1))) * E;
+  if (d >= A.D) return;
+  const int n = (int)min((int64_t)E, A.D - d);
+  for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> S.lg; row < A.B * A.N;  // over all problems
+       row += (int64_t)gridDim.x * 256 >> S.lg)
+    lookup_row<T>(A, row, d, n);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) dweights_kernel(LookupArgs A, int lg) {
+  constexpr int E = Vec<T>::E;
+  const int lane = threadIdx.x & ((1 << lg) - 1);
+  for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg; row < A.B * A.N;  // whole groups of lanes
+       row += (int64_t)gridDim.x * 256 >> lg) {
+    const int64_t b = A.B == 1 ? 0 : row / A.N, i = row - b * A.N;
+    const T* t = reinterpret_cast<const T*>(A.table) + b * A.stride_b;
+    const T* g = reinterpret_cast<const T*>(A.dout) + b * A.stride_g + i * A.ld_g;
+    const int32_t* ix = A.idx + row * A.m;
+    float* out = A.dweights + row * A.m;
+    bool live = true;
+    for (int j = 0; j < A.m; ++j) {
+      const int k = ix[j];
+      live = live && k >= 0 && k < A.K;
+      float s = 0.f;
+      if (live)
+        for (int64_t d = (int64_t)lane * E; d < A.D; d += (int64_t)E << lg) {
+          const int n = (int)min((int64_t)E, A.D - d);
+          Vec<T> a, r;
+          a.load(g + d, n);
+          r.load(t + k * A.ld + d, n);
+  #pragma unroll
+          for (int e = 0; e < E; ++e) s = fmaf(a.v[e], r.v[e], s);
+        }
+      for (int o = 1; o < 1 << lg; o <<= 1) s += __shfl_xor(s, o);
+      if (lane == 0) out[j] = live ? A.scale * s : 0.f;
+    }
+  }
+}
+
+// ---- entries sorted by code.  An entry is e = row * m + slot over all
+// problems, its key b * K + code; entries that take no part get key B K.
+__device__ inline uint32_t key_of(const LookupArgs& A, int64_t e, uint32_t none) {
+  const int64_t row = e / A.m;
+  const int j = (int)(e - row * A.m);
+  const int32_t* ix = A.idx + row * A.m;
+  int k = 0;
+  for (int q = 0; q <= j; ++q) {
+    k = ix[q];
+    if (k < 0 || k >= A.K) return none;
+  }
+  return (uint32_t)((A.B == 1 ? 0 : row / A.N) * A.K + k);
+}
+
+// digit counts of a block of kSortBlock entries
+__global__ void __launch_bounds__(256) sort_count_kernel(LookupArgs A, SortPass P) {
+  extern __shared__ uint32_t cnt[];
+  for (int d = threadIdx.x; d < P.bins; d += 256) cnt[d] = 0;
+  __syncthreads();
+  const int64_t e0 = (int64_t)blockIdx.x * kSortBlock;
+  for (int u = 0; u < kSortBlock / 256; ++u) {
+    const int64_t e = e0 + u * 256 + threadIdx.x;
+    if (e >= P.S) break;
+    const uint32_t key = P.kin ? P.kin[e] : key_of(A, e, P.none);
+    atomicAdd(&cnt[(key >> P.shift) & (P.bins - 1)], 1u);  // in LDS; a count has no order
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < P.bins; d += 256) P.hist[(int64_t)blockIdx.x * P.bins + d] = cnt[d];
+}
+
+// counts [block][digit] -> first position of the digit's entries of the block
+__global__ void __launch_bounds__(1024) sort_scan_kernel(SortPass P) {
+  __shared__ uint32_t tot[1024];
+  const int d = threadIdx.x;
+  uint32_t s = 0;
+  if (d < P.bins) {
+    constexpr int U = 8;
+    int64_t b = 0;
+    for (; b + U <= P.nblk; b += U) {
+      uint32_t v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = P.hist[(b + u) * P.bins + d];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        P.hist[(b + u) * P.bins + d] = s;
+        s += v[u];
+      }
+    }
+    for (; b < P.nblk; ++b) {
+      const uint32_t v = P.hist[b * P.bins + d];
+      P.hist[b * P.bins + d] = s;
+      s += v;
+    }
+  }
+  tot[d] = s;
+  __syncthreads();
+  for (int o = 1; o < 1024; o <<= 1) {  // inclusive scan over the digits
+    const uint32_t v = d >= o ? tot[d - o] : 0;
+    __syncthreads();
+    tot[d] += v;
+    __syncthreads();
+  }
+  if (d < P.bins) P.base[d] = tot[d] - s;
+}
+
+// places a block's entries; equal digits keep their order
+__global__ void __launch_bounds__(256) sort_scatter_kernel(LookupArgs A, SortPass P) {
+  extern __shared__ uint32_t next[];  // [4 waves][bins]: the wave's next position of a digit
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  constexpr int PER = kSortBlock / 4;  // consecutive entries of a wave
+  const int64_t e0 = (int64_t)blockIdx.x * kSortBlock + wv * PER;
+  for (int d = threadIdx.x; d < 4 * P.bins; d += 256) next[d] = 0;
+  __syncthreads();
+  uint32_t key[PER / 64], src[PER / 64];
+#pragma unroll
+  for (int u = 0; u < PER / 64; ++u) {
+    const int64_t e = e0 + u * 64 + lane;
+    key[u] = src[u] = 0;
+    if (e < P.S) {
+      key[u] = P.kin ? P.kin[e] : key_of(A, e, P.none);
+      src[u] = P.sin ? P.sin[e] : (uint32_t)e;
+      atomicAdd(&next[wv * P.bins + ((key[u] >> P.shift) & (P.bins - 1))], 1u);
+    }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < P.bins; d += 256) {
+    uint32_t at = P.base[d] + P.hist[(int64_t)blockIdx.x * P.bins + d];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t c = next[w * P.bins + d];
+      next[w * P.bins + d] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  volatile uint32_t* mine = next + wv * P.bins;
+  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
+#pragma unroll
+  for (int u = 0; u < PER / 64; ++u) {
+    const bool in = e0 + u * 64 + lane < P.S;
+    const uint32_t d = (key[u] >> P.shift) & (P.bins - 1);
+    uint64_t same = __builtin_amdgcn_ballot_w64(in);
+    for (int bit = 0; bit < P.bits; ++bit) {
+      const uint64_t set = __builtin_amdgcn_ballot_w64((d >> bit) & 1);
+      same &= (d >> bit) & 1 ? set : ~set;
+    }
+    if (in) {
+      const uint32_t at = mine[d] + __builtin_popcountll(same & below);
+      P.kout[at] = key[u];
+      P.sout[at] = src[u];
+    }
+    __builtin_amdgcn_wave_barrier();  // every lane has read its digit's position
+    if (in && (same >> lane) == 1ull) mine[d] += __builtin_popcountll(same);  // the digit's last lane
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// any bytes <- 0 (a kernel: memory operations in a captured graph are avoided)
+__global__ void __launch_bounds__(256) zero_kernel(char* p, int64_t bytes) {
+  const int64_t n = bytes / 16;
+  const u32x4 z = {0u, 0u, 0u, 0u};
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256)
+    __builtin_memcpy(p + t * 16, &z, 16);
+  if (blockIdx.x == 0 && threadIdx.x < bytes % 16) p[n * 16 + threadIdx.x] = 0;
+}
+
+template <typename T>
+__device__ inline void put(const LookupArgs& A, uint32_t key, int64_t d, int n, Vec<T>& acc) {
+  T* p = reinterpret_cast<T*>(A.dtable) + (int64_t)key * A.D + d;
+#pragma unroll
+  for (int e = 0; e < Vec<T>::E; ++e) acc.v[e] *= A.scale;
+  if (A.accumulate) {
+    Vec<T> old;
+    old.load(p, n);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::E; ++e) acc.v[e] += old.v[e];
+  }
+  acc.store(p, n);
+}
+
+// Sums the entries of a chunk, in sorted order; a group of 2^lg lanes holds
+// 16 bytes of columns a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_kernel(LookupArgs A, SumArgs P, RowSplit S) {
+  constexpr int E = Vec<T>::E, U = 8;
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> S.lg;
+  const int64_t d = ((int64_t)blockIdx.y << S.lg | (threadIdx.x & ((1 << S.lg) - 1))) * E;
+  if (c >= P.chunks || d >= A.D) return;
+  const int n = (int)min((int64_t)E, A.D - d);
+  const int64_t s0 = c * P.C, s1 = min(P.S, s0 + P.C);
+  const uint32_t before = s0 > 0 ? P.key[s0 - 1] : 0xffffffffu, after = s1 < P.S ? P.key[s1] : 0xffffffffu;
+  Vec<T> acc;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc.v[e] = 0.f;
+  uint32_t cur = P.key[s0];
+  bool first = true;  // the run reaches the chunk's start
+  auto partial = [&](int slot) {
+    float* p = P.part + ((c * 2 + slot) * P.Dp + d);
+#pragma unroll
+    for (int e = 0; e < E; ++e) p[e] = acc.v[e];  // Dp: D rounded up to whole chunks
+  };
+  for (int64_t s = s0; s < s1; s += U) {
+    uint32_t k[U];
+    Vec<T> r[U];
+    float w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) k[u] = s + u < s1 ? P.key[s + u] : P.none;
+    if (k[0] >= P.none) break;  // the entries behind the last code
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k[u] < P.none) {
+        const uint32_t e = P.src[s + u];
+        const int64_t row = A.m == 1 ? e : e / (uint32_t)A.m;
+        const int64_t b = A.B == 1 ? 0 : row / A.N;
+        w[u] = A.weights ? A.weights[e] : 1.f;
+        r[u].load(reinterpret_cast<const T*>(A.dout) + b * A.stride_g + (row - b * A.N) * A.ld_g + d, n);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k[u] >= P.none) continue;
+      if (k[u] != cur) {
+        if (first && before == cur) partial(0);
+        else put<T>(A, cur, d, n, acc);
+        first = false;
+        cur = k[u];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc.v[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc.v[e] = fmaf(w[u], r[u].v[e], acc.v[e]);
+    }
+  }
+  if (cur >= P.none) return;
+  if (first && before == cur) partial(0);
+  else if (after == cur) partial(1);
+  else put<T>(A, cur, d, n, acc);
+}
+
+// Joins the runs that cross chunks: the workgroup of the chunk where such a
+// run starts adds its tail and the heads of the chunks that it goes on into,
+// 8 groups of 32 lanes over the chunks, 16 bytes of float32 columns a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) join_runs_kernel(LookupArgs A, SumArgs P) {
+  __shared__ float4 red[8][32];
+  const int64_t c = blockIdx.x;
+  const int64_t s1 = (c + 1) * P.C;
+  if (s1 >= P.S) return;
+  const uint32_t key = P.key[s1 - 1];
+  if (key >= P.none || P.key[s1] != key) return;                                 // no run crosses this end
+  if (c > 0 && P.key[c * P.C] == key && P.key[c * P.C - 1] == key) return;       // it started earlier
+  // the last chunk whose first entry has the key
+  int64_t lo = c + 1, hi = P.chunks - 1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) / 2;
+    if (P.key[mid * P.C] == key) lo = mid;
+    else hi = mid - 1;
+  }
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t d = ((int64_t)blockIdx.y * 32 + lane) * 4;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (d < A.D) {
+    if (g == 0) a = *reinterpret_cast<const float4*>(P.part + (c * 2 + 1) * P.Dp + d);
+    for (int64_t q = c + 1 + g; q <= lo; q += 8) {
+      const float4 v = *reinterpret_cast<const float4*>(P.part + q * 2 * P.Dp + d);
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+  }
+  red[g][lane] = a;
+  __syncthreads();
+  if (g != 0 || d >= A.D) return;
+  for (int q = 1; q < 8; ++q) {
+    const float4 v = red[q][lane];
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  const float v[4] = {a.x, a.y, a.z, a.w};
+  T* p = reinterpret_cast<T*>(A.dtable) + (int64_t)key * A.D + d;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (d + e < A.D) p[e] = (T)(A.scale * v[e] + (A.accumulate ? (float)p[e] : 0.f));
+}
+
+constexpr int64_t kMaxGrid = 1 << 22;  // workgroups along x: a launch has fewer than 2^32 threads an axis
+
+RowSplit row_split(int64_t D, int E) {
+  const int64_t ch = (D + E - 1) / E;
+  RowSplit s{0, 1};
+  while (s.lg < 8 && (1 << s.lg) < ch) ++s.lg;
+  s.slabs = (int)((ch + (1 << s.lg) - 1) >> s.lg);
+  return s;
+}
+
+#define GMM_TRY(call)             \
+  do {                            \
+    const hipError_t e_ = (call); \
+    if (e_ != hipSuccess) return e_; \
+  } while (0)
+
+template <typename T>
+hipError_t lookup(const LookupArgs& a, hipStream_t s) {
+  const RowSplit sp = row_split(a.D, Vec<T>::E);
+  const int64_t rows = a.B * a.N, per = 256 >> sp.lg;
+  const dim3 grid((unsigned)std::min<int64_t>((rows + per - 1) / per, kMaxGrid), (unsigned)sp.slabs);
+  hipLaunchKernelGGL((lookup_kernel<T>), grid, dim3(256), 0, s, a, sp);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipStream_t s) {
+  const int64_t rows = a.B * a.N;
+  if (a.dweights && rows > 0) {
+    int lg = row_split(a.D, Vec<T>::E).lg;
+    lg = std::min(lg, 6);
+    const int64_t per = 256 >> lg;
+    hipLaunchKernelGGL((dweights_kernel<T>), dim3((unsigned)std::min<int64_t>((rows + per - 1) / per, kMaxGrid)), dim3(256), 0, s, a,
+                       lg);
+    GMM_TRY(hipGetLastError());
+  }
+  if (!a.dtable) return hipSuccess;
+  if (!a.accumulate) GMM_TRY(launch_zero(a.dtable, a.B * a.K * a.D * (int64_t)sizeof(T), s));
+  if (rows == 0) return hipSuccess;
+  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + p.off_key[0]), reinterpret_cast<uint32_t*>(ws + p.off_key[1])};
+  uint32_t* srcs[2] = {reinterpret_cast<uint32_t*>(ws + p.off_src[0]), reinterpret_cast<uint32_t*>(ws + p.off_src[1])};
+  SortPass P{};
+  P.S = p.S;
+  P.nblk = p.nblk;
+  P.none = p.none;
+  P.hist = reinterpret_cast<uint32_t*>(ws + p.off_hist);
+  P.base = reinterpret_cast<uint32_t*>(ws + p.off_base);
+  P.bits = p.bits;
+  P.bins = 1 << p.bits;
+  for (int q = 0; q < p.passes; ++q) {
+    P.shift = q * p.bits;
+    P.kin = q ? keys[(q + 1) & 1] : nullptr;
+    P.sin = q ? srcs[(q + 1) & 1] : nullptr;
+    P.kout = keys[q & 1];
+    P.sout = srcs[q & 1];
+    hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)p.nblk), dim3(256), P.bins * 4, s, a, P);
+    GMM_TRY(hipGetLastError());
+    hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(1024), 0, s, P);
+    GMM_TRY(hipGetLastError());
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3((unsigned)p.nblk), dim3(256), P.bins * 16, s, a, P);
+    GMM_TRY(hipGetLastError());
+  }
+  SumArgs Q{};
+  Q.S = p.S;
+  Q.C = p.C;
+  Q.chunks = p.chunks;
+  Q.Dp = p.Dp;
+  Q.none = p.none;
+  Q.key = keys[(p.passes - 1) & 1];
+  Q.src = srcs[(p.passes - 1) & 1];
+  Q.part = reinterpret_cast<float*>(ws + p.off_part);
+  const RowSplit sp = row_split(a.D, Vec<T>::E);
+  const int64_t per = 256 >> sp.lg;
+  hipLaunchKernelGGL((sum_kernel<T>), dim3((unsigned)((p.chunks + per - 1) / per), (unsigned)sp.slabs), dim3(256), 0, s, a, Q,
+                     sp);
+  GMM_TRY(hipGetLastError());
+  if (p.chunks > 1) {
+    hipLaunchKernelGGL((join_runs_kernel<T>), dim3((unsigned)(p.chunks - 1), (unsigned)((a.D + 127) / 128)), dim3(256), 0, s,
+                       a, Q);
+    GMM_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+}  // namespace
+
+hipError_t launch_zero(void* p, int64_t bytes, hipStream_t s) {
+  if (bytes <= 0) return hipSuccess;
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(8192, (bytes / 16 + 255) / 256));
+  hipLaunchKernelGGL(zero_kernel, dim3(grid), dim3(256), 0, s, (char*)p, bytes);
+  return hipGetLastError();
+}
+
+LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, bool want_table) {
+  LookupPlan p{};
+  if (!want_table || B * N == 0) return p;
+  p.S = B * N * m;
+  p.none = (uint32_t)(B * K);
+  int total = 0;
+  while (((int64_t)1 << total) <= B * K) ++total;  // bits of the key B K
+  p.passes = (total + 9) / 10;
+  p.bits = (total + p.passes - 1) / p.passes;
+  p.nblk = (p.S + kSortBlock - 1) / kSortBlock;
+  // entries of a chunk: 32, more where that makes over 2^13 chunks
+  p.C = 32;
+  while (p.C < 1024 && p.S / p.C > 1 << 13) p.C *= 2;
+  p.chunks = (p.S + p.C - 1) / p.C;
+  p.Dp = (D + 7) / 8 * 8;
+  size_t o = 0;
+  for (int i = 0; i < 2; ++i) {
+    p.off_key[i] = o; o = upz(o + sizeof(uint32_t) * (size_t)p.S);
+    p.off_src[i] = o; o = upz(o + sizeof(uint32_t) * (size_t)p.S);
+  }
+  p.off_hist = o; o = upz(o + sizeof(uint32_t) * ((size_t)p.nblk << p.bits));
+  p.off_base = o; o = upz(o + sizeof(uint32_t) * ((size_t)1 << p.bits));
+  p.off_part = o; o = upz(o + sizeof(float) * (size_t)(2 * p.chunks * p.Dp));
+  p.bytes = o;
+  return p;
+}
+
+hipError_t launch_lookup(const LookupArgs& a, hipStream_t s) {
+  if (a.dtype == 1) return lookup<__bf16>(a, s);
+  if (a.dtype == 2) return lookup<_Float16>(a, s);
+  return lookup<float>(a, s);
+}
+
+hipError_t launch_lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipStream_t s) {
+  if (a.dtype == 1) return lookup_grad<__bf16>(a, p, ws, s);
+  if (a.dtype == 2) return lookup_grad<_Float16>(a, p, ws, s);
+  return lookup_grad<float>(a, p, ws, s);
+}
+
+}  // namespace gmm

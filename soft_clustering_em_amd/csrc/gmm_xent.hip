@@ -1,0 +1,983 @@
+// gmm_xent.hip -- softmax cross entropy of rows under a linear head of V
+// classes, and its gradient, without the N x V logits ever being kept.
+//
+// What it computes.  For row x_i with label y_i, head rows W_v and bias b_v:
+//   l_iv   = W_v . x_i + b_v
+//   lse_i  = log sum_v exp(l_iv)
+//   loss_i = lse_i - l_{i, y_i}
+//   G_iv   = g_i (exp(l_iv - lse_i) - [v = y_i])       (g_i: the loss's gradient)
+//   dX = G W,   dW = G^T X,   db = sum_i G_i
+// (the log-sum-exp and the responsibility-weighted sums of the mixture's
+// E-step, with a head's weights in the place of means and variances).
+//
+// How.  Everything is one matrix-core kernel, C[m][n] = sum_k A[m][k] B[n][k]
+// with both operands contiguous along k, under three epilogues:
+//   LSE   rows x classes: each tile leaves one (max, sum of exponentials) per
+//         row, and the label's logit; a small kernel joins the tiles;
+//   GRAD  rows x classes of one piece: the logits again, turned into G in the
+//         accumulators; G and its transpose are written in the rows' type;
+//   OUT   the products G W and G^T X over such a piece.
+// A piece is at most 2^27 (float32: 2^26) elements of G, whatever N and V.
+// Recomputing the logits costs a third more arithmetic than keeping them and
+// takes their N V floats out of memory.  W and X enter the OUT products
+// transposed (a piece of W, the rows of a chunk: copies of a few percent of
+// the product's traffic), so that one main loop serves all three.
+//
+// The tile's operands go from global memory straight into LDS with 16-byte
+// buffer loads, two buffers, one barrier per k-tile of 128 bytes.  The loads
+// carry their own bounds: a row or k-chunk outside the operand has an offset
+// past the resource's end and arrives as zeros.  A row's 16-byte chunk c sits
+// in slot c ^ f(row) of its LDS row, so the fragment reads of 16 rows touch
+// all 64 banks.
+//
+// Rounding.  Accumulators, maxima, sums, G and the bias gradient are float32;
+// G is rounded once to the rows' type to enter the matrix cores (2^-9 of each
+// element for bf16, the size of the rounding of the outputs themselves), after
+// it was divided by max |g_i| (scal_kernel says why).
+#include "gmm_internal.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace gmm {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr unsigned kOutside = 0x80000000u;  // an offset past every resource's end
+
+constexpr int kVm0 = 0x0f70;  // s_waitcnt vmcnt(0): the loads into LDS too
+
+enum Mode { LSE = 0, GRAD = 1, OUT = 2 };
+
+template <typename T>
+__device__ inline float to_f32(T v) {
+  return (float)v;
+}
+
+// one 16-byte chunk per lane of both operands: acc[n][m] += B[n][:] A[m][:]
+template <typename T>
+__device__ inline f32x4 mma(u32x4 b, u32x4 a, f32x4 c);
+template <>
+__device__ inline f32x4 mma<__bf16>(u32x4 b, u32x4 a, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0,
+                                                 0);
+}
+template <>
+__device__ inline f32x4 mma<_Float16>(u32x4 b, u32x4 a, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
+}
+template <>
+__device__ inline f32x4 mma<float>(u32x4 b, u32x4 a, f32x4 c) {
+  // element j of every lane's chunk: k = 4 (lane / 16) + j, the same order in both operands
+  const f32x4 bf = __builtin_bit_cast(f32x4, b), af = __builtin_bit_cast(f32x4, a);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[j], af[j], c, 0, 0, 0);
+  return c;
+}
+
+struct GemmArgs {
+  const char* A;       // [M][K], row stride lda bytes
+  const char* B;       // [N][K], row stride ldb bytes
+  int64_t lda, ldb;
+  int64_t M, N;
+  int kbytes;          // valid bytes of a row (a multiple of 16)
+  int ktiles, splits;  // 128-byte k-tiles, shared among splits
+  int tm, tn;          // tiles
+  // LSE and GRAD: classes v0 .. v0 + N of the head
+  const float* bias;   // (V) or null
+  const int32_t* labels;
+  int64_t v0;
+  float2* part;        // LSE: [tile n][M]
+  float* lab;          // LSE: the label's logit
+  const float* lse;    // GRAD
+  const float* coef;   // GRAD: g_i (0: the row takes no part)
+  const float* scal;   // {multiplier of G, its inverse}; null: 1
+  char* G;             // GRAD: [M][ldg] rows' type
+  char* GT;            // GRAD: [N][ldgt], null: not wanted
+  int64_t ldg, ldgt;   // elements, whole k-tiles
+  float* dbp;          // GRAD: [tile m][N] column sums, null: not wanted
+  // OUT
+  float* slab;         // [splits][M][lds] float32, null: straight to out
+  int64_t lds, slab_stride;
+  int add;             // slabs: add to what is there
+  char* out;           // [M][N] rows' type
+  int accumulate;      // out: add to what is there
+  const float* rowlive;  // rows with 0 here get zeros (null: none)
+};
+
+// tile of the workgroup: consecutive tiles of a group of 8 tile rows on one
+// XCD (workgroups go round the 8 XCDs), so that an XCD's L2 holds what they share
+__device__ inline void tile_of(const GemmArgs& P, int& tm, int& tn, int& z) {
+  const unsigned total = gridDim.x, id = blockIdx.x;
+  const unsigned q = total / 8, r = total % 8, x = id % 8, i = id / 8;
+  const unsigned pid = x * q + (x < r ? x : r) + i;
+  const unsigned per = (unsigned)P.tm * P.tn;
+  z = pid / per;
+  const unsigned t = pid % per, width = 8u * P.tn, first = t / width * 8;
+  const unsigned rows = min((unsigned)P.tm - first, 8u);
+  tm = first + (t % width) % rows;
+  tn = (t % width) / rows;
+}
+
+// row m's label, counted from class n of the piece (-1: not among the next 2^20)
+__device__ inline int label_at(const GemmArgs& P, int64_t m, int64_t n) {
+  if (m >= P.M) return -1;
+  const int64_t y = (int64_t)P.labels[m] - P.v0 - n;
+  return y < 0 || y >= (1 << 20) ? -1 : (int)y;
+}
+
+template <typename T>
+__device__ inline void store4(T* p, f32x4 v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<f32x4*>(p) = v;
+  } else {
+    T t[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+    *reinterpret_cast<u32x2*>(p) = __builtin_bit_cast(u32x2, t);
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int MODE>
+__global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
+  constexpr int NT = WM * WN * 64;          // threads
+  constexpr int MT = BM / WM / 16, NN = BN / WN / 16;  // 16 x 16 tiles of a wave
+  constexpr int JA = BM * 8 / NT, JB = BN * 8 / NT;    // 16-byte loads of a thread per k-tile
+  constexpr int kStage = (BM + BN) * 128;
+  // two objects, so that the reads of one do not wait for the loads into the other
+  __shared__ __attribute__((aligned(1024))) char st0[kStage];
+  __shared__ __attribute__((aligned(1024))) char st1[kStage];
+
+  int tm, tn, z;
+  tile_of(P, tm, tn, z);
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wv / WN, wn = wv % WN;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int mrows = (int)min((int64_t)BM, P.M - m0), nrows = (int)min((int64_t)BN, P.N - n0);
+
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(P.A) + m0 * P.lda, 0, (unsigned)((mrows - 1) * P.lda + P.kbytes), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(P.B) + n0 * P.ldb, 0, (unsigned)((nrows - 1) * P.ldb + P.kbytes), 0x00020000);
+  // lane l of load j: LDS row 8 (j * waves + wave) + l / 8, slot l % 8
+  unsigned oa[JA], ob[JB];
+  int ca[JA], cb[JB];
+#pragma unroll
+  for (int j = 0; j < JA; ++j) {
+    const int row = 8 * (j * (NT / 64) + wv) + (lane >> 3);
+    ca[j] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    oa[j] = row < mrows ? (unsigned)(row * P.lda) + ca[j] : kOutside;
+  }
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int row = 8 * (j * (NT / 64) + wv) + (lane >> 3);
+    cb[j] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    ob[j] = row < nrows ? (unsigned)(row * P.ldb) + cb[j] : kOutside;
+  }
+  auto issue = [&](char* st, int kt) {
+    const int kb = kt * 128;
+#pragma unroll
+    for (int j = 0; j < JA; ++j) {
+      const unsigned o = (kb + ca[j] < P.kbytes && oa[j] != kOutside) ? oa[j] + kb : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ra, (__attribute__((address_space(3))) void*)(st + (j * (NT / 64) + wv) * 1024), 16, o, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      const unsigned o = (kb + cb[j] < P.kbytes && ob[j] != kOutside) ? ob[j] + kb : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rb, (__attribute__((address_space(3))) void*)(st + BM * 128 + (j * (NT / 64) + wv) * 1024), 16, o, 0, 0, 0);
+    }
+  };
+
+  f32x4 acc[MT][NN];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int lr = lane & 15, lq = lane >> 4;
+  const int fsw = (lr >> 1) & 7;
+  auto compute = [&](const char* st) {
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      const int slot = ((step * 4 + lq) ^ fsw) * 16;
+      u32x4 b[NN];
+#pragma unroll
+      for (int j = 0; j < NN; ++j)
+        b[j] = *reinterpret_cast<const u32x4*>(st + BM * 128 + ((wn * NN + j) * 16 + lr) * 128 + slot);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const u32x4 a = *reinterpret_cast<const u32x4*>(st + ((wm * MT + i) * 16 + lr) * 128 + slot);
+#pragma unroll
+        for (int j = 0; j < NN; ++j) acc[i][j] = mma<T>(b[j], a, acc[i][j]);
+      }
+    }
+  };
+
+  const int kt0 = (int)((int64_t)P.ktiles * z / P.splits), kt1 = (int)((int64_t)P.ktiles * (z + 1) / P.splits);
+  // Loads of a tile run while the tile before it is computed; a wait and a
+  // barrier between tiles: every wave's loads have landed and the buffer that
+  // is loaded next is read out.
+  auto landed = [] {
+    __builtin_amdgcn_s_waitcnt(kVm0);
+    __syncthreads();
+  };
+  int kt = kt0;
+  if (kt < kt1) issue(st0, kt);
+  for (; kt + 2 < kt1; kt += 2) {
+    landed();
+    issue(st1, kt + 1);
+    compute(st0);
+    landed();
+    issue(st0, kt + 2);
+    compute(st1);
+  }
+  if (kt < kt1) {  // one or two are left
+    landed();
+    if (kt + 1 < kt1) issue(st1, kt + 1);
+    compute(st0);
+    if (kt + 1 < kt1) {
+      landed();
+      compute(st1);
+    }
+  }
+
+  // accumulator element e of acc[i][j]: row m = 16 (wm MT + i) + lr of the
+  // tile, column n = 16 (wn NN + j) + 4 lq + e
+  const int mw = wm * MT * 16 + lr, nw = wn * NN * 16 + 4 * lq;
+
+  if constexpr (MODE == OUT) {
+    const bool vec = (P.N % 4) == 0;  // rows of out start 4 elements apart
+    const float sc = P.scal ? P.scal[1] : 1.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int64_t m = m0 + mw + 16 * i;
+      if (m >= P.M) continue;
+      const bool dead = P.rowlive && P.rowlive[m] == 0.f;
+#pragma unroll
+      for (int j = 0; j < NN; ++j) {
+        const int64_t n = n0 + nw + 16 * j;
+        if (n >= P.N) continue;
+        f32x4 v = acc[i][j];
+        if (P.slab) {
+          float* p = P.slab + z * P.slab_stride + m * P.lds + n;  // lds: N rounded up to 4
+          if (P.add) v += *reinterpret_cast<const f32x4*>(p);
+          *reinterpret_cast<f32x4*>(p) = v;
+          continue;
+        }
+        v = dead ? f32x4{0.f, 0.f, 0.f, 0.f} : v * sc;
+        T* p = reinterpret_cast<T*>(P.out) + m * P.N + n;
+        if (vec && !P.accumulate) {
+          store4<T>(p, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < P.N) p[e] = (T)(v[e] + (P.accumulate ? to_f32(p[e]) : 0.f));
+        }
+      }
+    }
+    return;
+  } else {
+    // logits: the bias, and -inf past the last class
+    f32x4 bv[NN];
+#pragma unroll
+    for (int j = 0; j < NN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t n = n0 + nw + 16 * j + e;
+        bv[j][e] = n < P.N ? (P.bias ? P.bias[P.v0 + n] : 0.f) : -INFINITY;
+      }
+    __syncthreads();  // the last k-tile is read out: LDS is free
+
+    if constexpr (MODE == LSE) {
+      float2* red = reinterpret_cast<float2*>(st0);  // [WN][BM]
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + mw + 16 * i;
+        const int y = label_at(P, m, n0 + nw);
+        float mx = -INFINITY, lab = 0.f;
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[i][j][e] += bv[j][e];
+            mx = fmaxf(mx, acc[i][j][e]);
+            lab = y == 16 * j + e ? acc[i][j][e] : lab;
+          }
+        if (y >= 0 && y < 16 * NN && (y & 15) < 4) P.lab[m] = lab;  // this lane holds the label's column
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float base = mx == -INFINITY ? 0.f : mx;  // nothing but -inf: a sum of 0
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - base) * kLog2e);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lq == 0) red[wn * BM + mw + 16 * i] = make_float2(mx, s);
+        __builtin_amdgcn_sched_barrier(0);  // one row block's temporaries at a time
+      }
+      __syncthreads();
+      for (int r = tid; r < mrows; r += NT) {
+        float mx = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) mx = fmaxf(mx, red[w * BM + r].x);
+        const float base = mx == -INFINITY ? 0.f : mx;  // a wave of -inf alone has sum 0
+#pragma unroll
+        for (int w = 0; w < WN; ++w) {
+          const float2 t = red[w * BM + r];
+          s += t.y * __builtin_amdgcn_exp2f((t.x - base) * kLog2e);
+        }
+        P.part[(int64_t)tn * P.M + m0 + r] = make_float2(mx, s);
+      }
+    } else {
+      constexpr int kRegion = 16384;                       // bytes of LDS per wave
+      constexpr int SUB = kRegion / (NN * 16 * 16 * (int)sizeof(T)) < MT ? kRegion / (NN * 16 * 16 * (int)sizeof(T)) : MT;
+      constexpr int EPC = 16 / (int)sizeof(T);             // elements of a 16-byte chunk
+      constexpr int CR = SUB * 16 / EPC, CL = 16 / EPC;    // chunks of a transposed row; of 16 elements
+      static_assert(MT % SUB == 0 && 4 * CL <= CR, "transposing in whole sub-tiles");
+      static_assert(WM * WN * kRegion <= 2 * kStage, "the waves' regions fill the two stages");
+      T* reg = reinterpret_cast<T*>((wv < WM * WN / 2 ? st0 : st1) + (wv % (WM * WN / 2)) * kRegion);
+      const float mult = P.scal ? P.scal[0] : 1.f;
+      float cs[NN][4];
+#pragma unroll
+      for (int j = 0; j < NN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[j][e] = 0.f;
+#pragma unroll
+      for (int i0 = 0; i0 < MT; i0 += SUB) {
+#pragma unroll
+        for (int ii = 0; ii < SUB; ++ii) {
+          const int i = i0 + ii;
+          const int64_t m = m0 + mw + 16 * i;
+          const float c = m < P.M ? P.coef[m] : 0.f;
+          const float ls = m < P.M ? P.lse[m] : 0.f;
+          const int y = label_at(P, m, n0 + nw);
+          const float cm = c * mult;
+#pragma unroll
+          for (int j = 0; j < NN; ++j) {
+            f32x4 g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = __builtin_amdgcn_exp2f((acc[i][j][e] + bv[j][e] - ls) * kLog2e);
+              const bool live = c != 0.f && n0 + nw + 16 * j + e < P.N;  // NaN is live
+              g[e] = live ? cm * (p - (y == 16 * j + e ? 1.f : 0.f)) : 0.f;
+              cs[j][e] += g[e];
+            }
+            const int64_t n = n0 + nw + 16 * j;
+            if (m < P.M && n < P.ldg) store4<T>(reinterpret_cast<T*>(P.G) + m * P.ldg + n, g);
+            if (P.GT) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int ml = 16 * ii + lr;
+                const int ch = (ml / EPC) ^ (CL * lq);  // rows 4 apart would share banks
+                reg[(16 * j + 4 * lq + e) * (SUB * 16) + ch * EPC + ml % EPC] = (T)g[e];
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one 16 x 16 tile's temporaries at a time
+          }
+        }
+        if (P.GT) {
+          __syncthreads();
+#pragma unroll
+          for (int t = 0; t < NN * 16 * CR / 64; ++t) {
+            const int idx = t * 64 + lane, nl = idx / CR, ch = idx % CR;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(reg + nl * (SUB * 16) + (ch ^ (CL * ((nl >> 2) & 3))) * EPC);
+            const int64_t n = n0 + wn * NN * 16 + nl, m = m0 + wm * MT * 16 + i0 * 16 + ch * EPC;
+            if (n < P.N && m < P.ldgt) *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + n * P.ldgt + m) = v;
+          }
+          __syncthreads();
+        }
+      }
+      if (P.dbp) {
+        float* red = reinterpret_cast<float*>(st0);  // [WM][BN]
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = cs[j][e];
+            v += __shfl_xor(v, 1);
+            v += __shfl_xor(v, 2);
+            v += __shfl_xor(v, 4);
+            v += __shfl_xor(v, 8);
+            if (lr == 0) red[wm * BN + nw + 16 * j + e] = v;
+          }
+        __syncthreads();
+        for (int c = tid; c < nrows; c += NT) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < WM; ++w) v += red[w * BN + c];
+          P.dbp[(int64_t)tm * P.N + n0 + c] = v;
+        }
+      }
+    }
+  }
+}
+
+struct RowsArgs {
+  const char* x;            // element (b, i, d) at x + es (b stride_b + i ld + d)
+  int64_t N, ld, stride_b;  // rows per problem
+  int64_t r0, nr;           // rows of this chunk, over all problems
+  int D;
+};
+__device__ inline int64_t row_offset(const RowsArgs& R, int64_t r) {
+  return (r / R.N) * R.stride_b + (r % R.N) * R.ld;
+}
+
+// Scoring of a few rows (serving): at most 16 MT rows against the whole head,
+// bound by reading W once.  A wave owns 16 classes and walks their rows of W
+// from global memory into MFMA fragments (no LDS: nothing is shared); the
+// rows' fragments come from the L1.  One (max, sum) per row and 64 classes.
+template <typename T>
+__device__ inline u32x4 chunk_at(const char* row, int k, int bytes) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (k + 16 <= bytes) {
+    __builtin_memcpy(&v, row + k, 16);  // any alignment of the elements
+  } else if (k < bytes) {
+    T t[16 / sizeof(T)];
+#pragma unroll
+    for (int e = 0; e < 16 / (int)sizeof(T); ++e)
+      t[e] = k + e * (int)sizeof(T) < bytes ? reinterpret_cast<const T*>(row + k)[e] : T(0);
+    v = __builtin_bit_cast(u32x4, t);
+  }
+  return v;
+}
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(256) skinny_kernel(GemmArgs P, RowsArgs R) {
+  constexpr int U = 8;  // k-steps of 64 bytes in flight
+  __shared__ float2 red[4][16 * MT];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lr = lane & 15, lq = lane >> 4;
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wv) * 16;
+  const int64_t nr = min(n0 + lr, P.N - 1);  // classes past the last read its row and are masked
+  const char* w = P.B + nr * P.ldb;
+  const char* x[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    x[i] = R.x + row_offset(R, min((int64_t)(16 * i + lr), P.M - 1)) * (int64_t)sizeof(T);
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = lq * 16; k0 < P.kbytes + lq * 16; k0 += 64 * U) {
+    u32x4 b[U], a[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 64 * u;
+      b[u] = chunk_at<T>(w, k, P.kbytes);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) a[u][i] = chunk_at<T>(x[i], k, P.kbytes);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i] = mma<T>(b[u], a[u][i], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = 16 * i + lr;
+    const int64_t y = m < P.M ? (int64_t)P.labels[m] - n0 - 4 * lq : -1;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t n = n0 + 4 * lq + e;
+      acc[i][e] = n < P.N ? acc[i][e] + (P.bias ? P.bias[n] : 0.f) : -INFINITY;
+      mx = fmaxf(mx, acc[i][e]);
+      if (y == e && n < P.N) P.lab[m] = acc[i][e];
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f((acc[i][e] - base) * kLog2e);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lq == 0) red[wv][16 * i + lr] = make_float2(mx, s);
+  }
+  __syncthreads();
+  const int r = threadIdx.x;
+  if (r < 16 * MT && r < P.M) {
+    float mx = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w2 = 0; w2 < 4; ++w2) mx = fmaxf(mx, red[w2][r].x);
+    const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int w2 = 0; w2 < 4; ++w2) s += red[w2][r].y * __builtin_amdgcn_exp2f((red[w2][r].x - base) * kLog2e);
+    P.part[(int64_t)blockIdx.x * P.M + r] = make_float2(mx, s);
+  }
+}
+
+// Joins the tiles' (max, sum): RB rows per workgroup, 256 / RB threads a row.
+template <int RB>
+__global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t ntiles, int64_t M, const int32_t* labels,
+                                                   int64_t V, const float* lab, float* loss, float* lse) {
+  constexpr int SL = 256 / RB;
+  __shared__ float2 red[SL][RB];
+  const int r = threadIdx.x % RB, sl = threadIdx.x / RB;
+  const int64_t m = (int64_t)blockIdx.x * RB + r;
+  float mx = -INFINITY, s = 0.f;
+  if (m < M) {
+    constexpr int U = 8;  // loads in flight
+    for (int64_t t0 = sl; t0 < ntiles; t0 += SL * U) {
+      float2 v[U];
+      float nm = mx;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + (int64_t)u * SL;
+        v[u] = t < ntiles ? part[t * M + m] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) nm = fmaxf(nm, v[u].x);
+      const float base = nm == -INFINITY ? 0.f : nm;
+      s *= __builtin_amdgcn_exp2f((mx - base) * kLog2e);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += v[u].y * __builtin_amdgcn_exp2f((v[u].x - base) * kLog2e);
+      mx = nm;
+    }
+  }
+  red[sl][r] = make_float2(mx, s);
+  __syncthreads();
+  if (sl != 0 || m >= M) return;
+  float top = -INFINITY, tot = 0.f;
+  for (int k = 0; k < SL; ++k) top = fmaxf(top, red[k][r].x);
+  const float base = top == -INFINITY ? 0.f : top;
+  for (int k = 0; k < SL; ++k) tot += red[k][r].y * __builtin_amdgcn_exp2f((red[k][r].x - base) * kLog2e);
+  const float z = top + logf(tot);
+  const int32_t y = labels[m];
+  lse[m] = z;
+  loss[m] = y < 0 ? 0.f : y >= V ? NAN : z - lab[m];
+}
+
+// coef_i: the loss's gradient of a labelled row, 0 where the label is
+// negative, NaN past the last class; block maxima of |coef|.
+__global__ void __launch_bounds__(256) coef_kernel(const int32_t* labels, const float* gloss, int64_t M, int64_t V,
+                                                   float* coef, float* bmax) {
+  __shared__ float red[4];
+  float mx = 0.f;
+  for (int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x; m < M; m += (int64_t)gridDim.x * 256) {
+    const int32_t y = labels[m];
+    const float c = y < 0 ? 0.f : y >= V ? NAN : (gloss ? gloss[m] : 1.f);
+    coef[m] = c;
+    mx = fmaxf(mx, fabsf(c));
+  }
+  for (int o = 32; o; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
+  __syncthreads();
+  if (threadIdx.x == 0) bmax[blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+// scal: what G is multiplied by before it is rounded, and the inverse that its
+// products are multiplied by.  1 / max |coef|: the rows of a mean loss then have
+// label entries p - 1 next to -1, which round to nearly nothing off, where
+// coef (p - 1) would round every row's the same way; `top` further on for half
+// rows, so that small probabilities stay in range.
+__global__ void __launch_bounds__(64) scal_kernel(const float* bmax, int n, float top, float* scal) {
+  float mx = 0.f;
+  for (int i = threadIdx.x; i < n; i += 64) mx = fmaxf(mx, bmax[i]);
+  for (int o = 32; o; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  if (threadIdx.x == 0) {
+    if (!(mx > 0.f)) mx = 1.f;  // no row takes part
+    mx = fminf(fmaxf(mx, 0x1p-100f), 0x1p100f);
+    scal[0] = top / mx;
+    scal[1] = mx / top;
+  }
+}
+
+// rows of any layout -> [nr][Dp], zeros past D
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(RowsArgs R, T* dst, int Dp) {
+  const int64_t n = R.nr * Dp;
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
+    const int64_t r = t / Dp;
+    const int d = (int)(t % Dp);
+    dst[t] = d < R.D ? reinterpret_cast<const T*>(R.x)[row_offset(R, R.r0 + r) + d] : T(0);
+  }
+}
+
+// rows of any layout -> [D][ldo], zeros past nr; rows with live = 0 become zeros
+template <typename T>
+__global__ void __launch_bounds__(256) transpose_kernel(RowsArgs R, const float* live, T* dst, int64_t ldo) {
+  __shared__ T tile[64][64 + 4 / sizeof(T)];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int d0 = blockIdx.y * 64, c = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int64_t r = r0 + w + 4 * u;
+    T v = T(0);
+    if (r < R.nr && d0 + c < R.D && !(live && live[r] == 0.f))
+      v = reinterpret_cast<const T*>(R.x)[row_offset(R, R.r0 + r) + d0 + c];
+    tile[w + 4 * u][c] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int d = w + 4 * u;
+    if (d0 + d < R.D && r0 + c < ldo) dst[(int64_t)(d0 + d) * ldo + r0 + c] = tile[c][d];
+  }
+}
+
+// out[r][c] = scale sum_z slab[z][r][c]  (+ out)
+template <typename T>
+__global__ void __launch_bounds__(256) finish_kernel(const float* slab, int splits, int64_t stride, int64_t lds, int64_t M,
+                                                     int64_t N, const float* scal, const float* live, T* out,
+                                                     int accumulate) {
+  const int64_t q = lds / 4, n = M * q;
+  const float sc = scal ? scal[1] : 1.f;
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
+    const int64_t r = t / q, c = t % q * 4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(slab + z * stride + r * lds + c);
+    v = live && live[r] == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * sc;
+    T* p = out + r * N + c;
+    if (N % 4 == 0 && !accumulate) {
+      store4<T>(p, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < N) p[e] = (T)(v[e] + (accumulate ? to_f32(p[e]) : 0.f));
+    }
+  }
+}
+
+// db[n] = scale sum over tile rows of the column sums (+ db)
+__global__ void __launch_bounds__(256) dbias_kernel(const float* dbp, int tm, int64_t N, const float* scal, float* db,
+                                                    int add) {
+  __shared__ float red[4][64];
+  const int c = threadIdx.x & 63, sl = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + c;
+  float v = 0.f;
+  if (n < N)
+    for (int t = sl; t < tm; t += 4) v += dbp[(int64_t)t * N + n];
+  red[sl][c] = v;
+  __syncthreads();
+  if (sl == 0 && n < N) {
+    v = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+    v *= scal ? scal[1] : 1.f;
+    db[n] = add ? db[n] + v : v;
+  }
+}
+
+template <typename T, int MODE>
+hipError_t launch_gemm(GemmArgs& P, bool big, hipStream_t s) {
+  const int bt = big ? 256 : 128;
+  P.tm = (int)((P.M + bt - 1) / bt);
+  P.tn = (int)((P.N + bt - 1) / bt);
+  const dim3 grid((unsigned)((int64_t)P.tm * P.tn * P.splits));
+  if (big) hipLaunchKernelGGL((gemm_kernel<T, 256, 256, 2, 4, MODE>), grid, dim3(512), 0, s, P);
+  else hipLaunchKernelGGL((gemm_kernel<T, 128, 128, 2, 2, MODE>), grid, dim3(256), 0, s, P);
+  return hipGetLastError();
+}
+
+int64_t tiles(int64_t M, int64_t N, int bt) { return ((M + bt - 1) / bt) * ((N + bt - 1) / bt); }
+// 256 x 256 tiles where they fill the card's compute units at least once
+bool big_tiles(int64_t M, int64_t N) { return tiles(M, N, 256) >= kNumCU; }
+// parts of the k axis that bring a product of few tiles to two workgroups per
+// compute unit, each part 8 k-tiles or longer
+int split_k(int64_t M, int64_t N, int64_t ktiles) {
+  const int64_t t = tiles(M, N, big_tiles(M, N) ? 256 : 128);
+  int64_t sp = t >= kNumCU ? 1 : (2 * kNumCU) / t;
+  sp = std::min<int64_t>(sp, ktiles / 8);
+  return (int)std::max<int64_t>(sp, 1);
+}
+unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64_t>(1, std::min((n + 255) / 256, cap)); }
+
+}  // namespace
+
+static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db) {
+  XentPlan p{};
+  const int64_t es = a.es, kt = 128 / es;
+  p.kbytes = (int)(up(a.D * es, 16));
+  const bool aligned_x = ((uintptr_t)a.x | (uintptr_t)(a.ld * es)) % 16 == 0 && (a.D * es) % 16 == 0 &&
+                         a.ld * es * 256 < ((int64_t)1 << 31) && (a.B == 1 || a.stride_b == a.N * a.ld);
+  const bool aligned_w = ((uintptr_t)a.w | (uintptr_t)(a.ld_w * es)) % 16 == 0 && (a.D * es) % 16 == 0 &&
+                         a.ld_w * es * 256 < ((int64_t)1 << 31);
+  p.pack_x = !aligned_x;
+  p.pack_w = !aligned_w;
+  p.Dp = up(a.D, 16 / es);
+  const int64_t R = std::max<int64_t>(a.B * a.N, 1), V = a.V;
+  size_t o = 0;
+  if (!grad) {
+    p.skinny = R <= 64;
+    if (p.skinny) p.pack_x = p.pack_w = false;  // it takes any alignment
+    // rows of a chunk: at most 2^24 (max, sum) pairs; classes of a piece: all,
+    // or 2^15 where they are copied to aligned rows first
+    const int64_t per = p.skinny ? 64 : 128;
+    p.vc = p.pack_w ? std::min<int64_t>(V, 1 << 15) : V;
+    const int64_t nt = (V + per - 1) / per + V / p.vc + 1;
+    p.nc = std::min<int64_t>(R, std::max<int64_t>(256, ((int64_t)1 << 24) / nt / 256 * 256));
+    p.off_part = o; o = upz(o + sizeof(float2) * (size_t)(nt * p.nc));
+    p.off_lab = o;  o = upz(o + sizeof(float) * (size_t)p.nc);
+  } else {
+    const int64_t cap = (int64_t)1 << (es == 2 ? 27 : 26);
+    const int64_t side = 1 << 15;
+    const int64_t Rp = up(R, kt), Vp = up(V, kt);
+    if (R <= V) {
+      p.nc = std::min(Rp, side);
+      p.vc = std::min(Vp, std::max<int64_t>(256, cap / p.nc / 256 * 256));
+    } else {
+      p.vc = std::min(Vp, side);
+      p.nc = std::min(Rp, std::max<int64_t>(256, cap / p.vc / 256 * 256));
+    }
+    p.ldg = up(std::min(p.vc, Vp), kt);
+    p.ldgt = up(std::min(p.nc, Rp), kt);
+    const int64_t mc = std::min(p.nc, R), vcc = std::min(p.vc, V);
+    p.np_v = (V + p.vc - 1) / p.vc;
+    p.np_r = (R + p.nc - 1) / p.nc;
+    p.lds = up(a.D, 4);
+    p.off_coef = o; o = upz(o + sizeof(float) * (size_t)R);
+    p.off_bmax = o; o = upz(o + sizeof(float) * 1024);
+    p.off_scal = o; o = upz(o + sizeof(float) * 2);
+    p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * es));
+    if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
+    if (want_dx) {
+      p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * es));
+      p.split_x = split_k(mc, a.D, p.ldg / kt);
+      p.slab_x = p.split_x > 1 || p.np_v > 1;
+      if (p.slab_x) { p.off_sx = o; o = upz(o + sizeof(float) * (size_t)(p.split_x * R * p.lds)); }
+    }
+    if (want_dw) {
+      p.off_GT = o; o = upz(o + (size_t)(vcc * p.ldgt * es));
+      p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * es));
+      p.split_w = split_k(vcc, a.D, p.ldgt / kt);
+      p.slab_w = p.split_w > 1 || p.np_r > 1;
+      if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
+    }
+  }
+  if (p.pack_x) { p.off_px = o; o = upz(o + (size_t)(std::min(p.nc, R) * p.Dp * es)); }
+  if (p.pack_w) { p.off_pw = o; o = upz(o + (size_t)(std::min(p.vc, V) * p.Dp * es)); }
+  p.bytes = o;
+  return p;
+}
+
+namespace {
+
+#define GMM_TRY(call)                                  \
+  do {                                                 \
+    const hipError_t e_ = (call);                      \
+    if (e_ != hipSuccess) return e_;                   \
+  } while (0)
+
+template <typename T>
+hipError_t pack(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s) {
+  hipLaunchKernelGGL((pack_kernel<T>), dim3(blocks(r.nr * Dp)), dim3(256), 0, s, r, reinterpret_cast<T*>(dst), (int)Dp);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t transpose(const RowsArgs& r, const float* live, char* dst, int64_t ldo, hipStream_t s) {
+  const dim3 grid((unsigned)((ldo + 63) / 64), (unsigned)((r.D + 63) / 64));
+  hipLaunchKernelGGL((transpose_kernel<T>), grid, dim3(256), 0, s, r, live, reinterpret_cast<T*>(dst), ldo);
+  return hipGetLastError();
+}
+
+// the operands of a chunk of rows against a piece of the head
+template <typename T>
+hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int64_t nr, int64_t v0, int64_t nv,
+                          char* ws, bool new_rows, bool new_classes, GemmArgs& P, hipStream_t s) {
+  const int64_t es = sizeof(T);
+  if (p.pack_x) {
+    if (new_rows) {
+      RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
+      GMM_TRY(pack<T>(r, ws + p.off_px, p.Dp, s));
+    }
+    P.A = ws + p.off_px;
+    P.lda = p.Dp * es;
+  } else {
+    P.A = (const char*)a.x + r0 * a.ld * es;
+    P.lda = a.ld * es;
+  }
+  if (p.pack_w) {
+    if (new_classes) {
+      RowsArgs r{(const char*)a.w, a.V, a.ld_w, 0, v0, nv, (int)a.D};
+      GMM_TRY(pack<T>(r, ws + p.off_pw, p.Dp, s));
+    }
+    P.B = ws + p.off_pw;
+    P.ldb = p.Dp * es;
+  } else {
+    P.B = (const char*)a.w + v0 * a.ld_w * es;
+    P.ldb = a.ld_w * es;
+  }
+  P.M = nr;
+  P.N = nv;
+  P.kbytes = p.kbytes;
+  P.ktiles = (p.kbytes + 127) / 128;
+  P.splits = 1;
+  P.bias = a.bias;
+  P.labels = a.labels + r0;
+  P.v0 = v0;
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse, char* ws, hipStream_t s) {
+  const int64_t R = a.B * a.N;
+  float2* part = reinterpret_cast<float2*>(ws + p.off_part);
+  float* lab = reinterpret_cast<float*>(ws + p.off_lab);
+  for (int64_t r0 = 0; r0 < R; r0 += p.nc) {
+    const int64_t nr = std::min(p.nc, R - r0);
+    int64_t nt = 0;
+    for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) {
+      const int64_t nv = std::min(p.vc, a.V - v0);
+      GemmArgs P{};
+      GMM_TRY(logit_operands<T>(a, p, r0, nr, v0, nv, ws, v0 == 0, p.vc < a.V || r0 == 0, P, s));
+      P.part = part + nt * nr;
+      P.lab = lab;
+      if (p.skinny) {
+        P.kbytes = (int)(a.D * (int64_t)sizeof(T));
+        P.B = (const char*)a.w;
+        P.ldb = a.ld_w * (int64_t)sizeof(T);
+        const RowsArgs x{(const char*)a.x, a.N, a.ld, a.stride_b, 0, nr, (int)a.D};
+        const dim3 grid((unsigned)((nv + 63) / 64));
+        if (nr <= 16) hipLaunchKernelGGL((skinny_kernel<T, 1>), grid, dim3(256), 0, s, P, x);
+        else if (nr <= 32) hipLaunchKernelGGL((skinny_kernel<T, 2>), grid, dim3(256), 0, s, P, x);
+        else hipLaunchKernelGGL((skinny_kernel<T, 4>), grid, dim3(256), 0, s, P, x);
+        GMM_TRY(hipGetLastError());
+        nt += grid.x;
+      } else {
+        GMM_TRY((launch_gemm<T, LSE>(P, big_tiles(nr, nv), s)));
+        nt += P.tn;
+      }
+    }
+    float *lo = loss + r0, *ls = lse + r0;
+    const int32_t* y = a.labels + r0;
+    if (nr == 1)
+      hipLaunchKernelGGL(join_kernel<1>, dim3(1), dim3(256), 0, s, part, nt, nr, y, a.V, lab, lo, ls);
+    else if (nr <= 4096)
+      hipLaunchKernelGGL(join_kernel<16>, dim3((unsigned)((nr + 15) / 16)), dim3(256), 0, s, part, nt, nr, y, a.V, lab, lo, ls);
+    else
+      hipLaunchKernelGGL(join_kernel<64>, dim3((unsigned)((nr + 63) / 64)), dim3(256), 0, s, part, nt, nr, y, a.V, lab, lo, ls);
+    GMM_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, const float* gloss, char* dx, char* dw,
+                    float* db, int accumulate, char* ws, hipStream_t s) {
+  const int64_t R = a.B * a.N, es = sizeof(T), kt = 128 / es;
+  float* coef = reinterpret_cast<float*>(ws + p.off_coef);
+  float* bmax = reinterpret_cast<float*>(ws + p.off_bmax);
+  float* scal = nullptr;
+  const unsigned cb = blocks(R, 1024);
+  hipLaunchKernelGGL(coef_kernel, dim3(cb), dim3(256), 0, s, a.labels, gloss, R, a.V, coef, bmax);
+  GMM_TRY(hipGetLastError());
+  if (es == 2) {
+    scal = reinterpret_cast<float*>(ws + p.off_scal);
+    hipLaunchKernelGGL(scal_kernel, dim3(1), dim3(64), 0, s, bmax, (int)cb, a.dtype == 2 ? 32768.f : 1.f, scal);
+    GMM_TRY(hipGetLastError());
+  }
+  for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) {
+    const int64_t nv = std::min(p.vc, a.V - v0);
+    if (dx) {
+      RowsArgs r{(const char*)a.w, a.V, a.ld_w, 0, v0, nv, (int)a.D};
+      GMM_TRY(transpose<T>(r, nullptr, ws + p.off_WT, up(nv, kt), s));
+    }
+    for (int64_t r0 = 0; r0 < R; r0 += p.nc) {
+      const int64_t nr = std::min(p.nc, R - r0);
+      GemmArgs P{};
+      GMM_TRY(logit_operands<T>(a, p, r0, nr, v0, nv, ws, p.np_r > 1 || v0 == 0, r0 == 0, P, s));
+      P.lse = lse + r0;
+      P.coef = coef + r0;
+      P.scal = scal;
+      P.G = ws + p.off_G;
+      P.ldg = up(nv, kt);
+      P.GT = dw ? ws + p.off_GT : nullptr;
+      P.ldgt = up(nr, kt);
+      P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
+      GMM_TRY((launch_gemm<T, GRAD>(P, big_tiles(nr, nv), s)));
+      if (db) {
+        hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((nv + 63) / 64)), dim3(256), 0, s, P.dbp, P.tm, nv, scal, db + v0,
+                           accumulate || r0 > 0);
+        GMM_TRY(hipGetLastError());
+      }
+      if (dx) {  // dX of the chunk += G W of the piece
+        GemmArgs Q{};
+        Q.A = P.G;
+        Q.lda = P.ldg * es;
+        Q.B = ws + p.off_WT;
+        Q.ldb = P.ldg * es;
+        Q.M = nr;
+        Q.N = a.D;
+        Q.kbytes = (int)(P.ldg * es);
+        Q.ktiles = (int)(P.ldg / kt);
+        Q.splits = std::min<int>(p.split_x, Q.ktiles);
+        Q.scal = scal;
+        Q.rowlive = coef + r0;
+        Q.out = dx + r0 * a.D * es;
+        Q.accumulate = accumulate;
+        if (p.slab_x) {
+          Q.splits = p.split_x;  // every slab is written by the first piece; empty k ranges add zeros
+          Q.slab = reinterpret_cast<float*>(ws + p.off_sx) + r0 * p.lds;
+          Q.lds = p.lds;
+          Q.slab_stride = R * p.lds;
+          Q.add = v0 > 0;
+        }
+        GMM_TRY((launch_gemm<T, OUT>(Q, big_tiles(nr, a.D), s)));
+        if (p.slab_x && v0 + nv >= a.V) {
+          hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(nr * p.lds / 4)), dim3(256), 0, s, Q.slab, Q.splits,
+                             Q.slab_stride, p.lds, nr, a.D, scal, coef + r0, reinterpret_cast<T*>(Q.out), accumulate);
+          GMM_TRY(hipGetLastError());
+        }
+      }
+      if (dw) {  // dW of the piece += G^T X of the chunk
+        RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
+        if (p.np_r > 1 || v0 == 0) GMM_TRY(transpose<T>(r, coef + r0, ws + p.off_XT, P.ldgt, s));
+        GemmArgs Q{};
+        Q.A = P.GT;
+        Q.lda = P.ldgt * es;
+        Q.B = ws + p.off_XT;
+        Q.ldb = P.ldgt * es;
+        Q.M = nv;
+        Q.N = a.D;
+        Q.kbytes = (int)(P.ldgt * es);
+        Q.ktiles = (int)(P.ldgt / kt);
+        Q.splits = p.split_w;
+        Q.scal = scal;
+        Q.out = dw + v0 * a.D * es;
+        Q.accumulate = accumulate;
+        if (p.slab_w) {
+          Q.slab = reinterpret_cast<float*>(ws + p.off_sw);
+          Q.lds = p.lds;
+          Q.slab_stride = std::min(p.vc, a.V) * p.lds;
+          Q.add = r0 > 0;
+        }
+        GMM_TRY((launch_gemm<T, OUT>(Q, big_tiles(nv, a.D), s)));
+        if (p.slab_w && r0 + nr >= R) {
+          hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(nv * p.lds / 4)), dim3(256), 0, s, Q.slab, Q.splits,
+                             Q.slab_stride, p.lds, nv, a.D, scal, (const float*)nullptr, reinterpret_cast<T*>(Q.out),
+                             accumulate);
+          GMM_TRY(hipGetLastError());
+        }
+      }
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_xent(const XentArgs& a, const XentPlan& p, float* loss, float* lse, char* ws, hipStream_t s) {
+  if (a.dtype == 1) return forward<__bf16>(a, p, loss, lse, ws, s);
+  if (a.dtype == 2) return forward<_Float16>(a, p, loss, lse, ws, s);
+  return forward<float>(a, p, loss, lse, ws, s);
+}
+
+hipError_t launch_xent_grad(const XentArgs& a, const XentPlan& p, const float* lse, const float* gloss, void* dx, void* dw,
+                            float* db, int accumulate, char* ws, hipStream_t s) {
+  char *x = (char*)dx, *w = (char*)dw;
+  if (a.dtype == 1) return backward<__bf16>(a, p, lse, gloss, x, w, db, accumulate, ws, s);
+  if (a.dtype == 2) return backward<_Float16>(a, p, lse, gloss, x, w, db, accumulate, ws, s);
+  return backward<float>(a, p, lse, gloss, x, w, db, accumulate, ws, s);
+}
+
+}  // namespace gmm

@@ -1,0 +1,251 @@
+"""gmm_softmax_xent and gmm_softmax_xent_grad against the plain 64-bit form, on
+the GPU: every element of every output inside the bound that its arithmetic
+gives (tests/head_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import head_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def g():
+    assert torch.cuda.is_available(), "GPU tests need a visible GPU"
+    import soft_clustering_em_amd as g
+    return g
+
+
+def make(N, D, V, dtype, bias=True, ignored=0.1, pad=0, offset=0, seed=0, B=None, spread=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed + 7919 * N + 31 * D + V)
+    lead = (N,) if B is None else (B, N)
+    X = torch.randn(*lead, D + pad + offset, generator=gen, device="cuda").to(TYPES[dtype])[..., offset:offset + D]
+    W = (torch.randn(V, D + offset, generator=gen, device="cuda") * (spread / D ** 0.5)).to(TYPES[dtype])[:, offset:]
+    b = torch.randn(V, generator=gen, device="cuda") if bias else None
+    y = torch.randint(0, V, lead, generator=gen, device="cuda", dtype=torch.int32)
+    y = y.masked_fill(torch.rand(lead, generator=gen, device="cuda") < ignored, -1)
+    gl = torch.rand(lead, generator=gen, device="cuda") / N
+    return X, W, b, y, gl
+
+
+def check(g, X, W, b, y, gl, grads=("dX", "dW", "db")):
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    want, tol = ref.xent(X, W, y, b, gl)
+    ref.within("lse", lse, want["lse"], tol["lse"])
+    ref.within("loss", loss, want["loss"], tol["loss"])
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    assert (db is None) == (b is None)
+    for name, got in (("dX", dX), ("dW", dW), ("db", db)):
+        if got is not None and name in grads:
+            ref.within(name, got, want[name], tol[name])
+    return loss, lse, dX, dW, db
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("N,D,V", [(1, 64, 100), (1, 1, 1), (1, 7, 2), (5, 8, 63), (16, 128, 64), (17, 65, 65), (33, 40, 300),
+                                   (64, 256, 1000), (65, 64, 129), (130, 33, 257), (128, 128, 128), (300, 515, 1003),
+                                   (777, 130, 501), (1000, 96, 2), (257, 1000, 4100)])
+def test_sizes(g, dtype, N, D, V):
+    check(g, *make(N, D, V, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [3, 200])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (13, 0), (0, 1), (5, 3), (0, 8)])
+def test_strides_and_alignment(g, dtype, N, pad, offset):
+    check(g, *make(N, 72, 130, dtype, pad=pad, offset=offset))
+    check(g, *make(N, 71, 130, dtype, pad=pad, offset=offset, bias=False))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_batched_rows(g, dtype):
+    for N, pad in ((40, 0), (40, 8), (9, 3)):
+        X, W, b, y, gl = make(N, 64, 90, dtype, B=5, pad=pad)
+        whole = check(g, X, W, b, y, gl)
+        half_of = X[:, : N // 2]  # problems apart
+        part = check(g, half_of, W, b, y[:, : N // 2].contiguous(), gl[:, : N // 2].contiguous())
+        assert torch.equal(part[0], whole[0][:, : N // 2]) or N // 2 * 5 <= 64 < N * 5
+
+
+@pytest.mark.parametrize("dtype,N,D,V", [("bf16", 40000, 8, 5000), ("bf16", 5000, 8, 40000), ("f32", 20000, 16, 5000),
+                                         ("f16", 33000, 8, 33000), ("bf16", 4100, 72, 4500), ("f32", 4100, 40, 4500),
+                                         ("bf16", 100000, 130, 40)])
+def test_chunks_of_rows_and_pieces_of_the_head(g, dtype, N, D, V):
+    check(g, *make(N, D, V, dtype, ignored=0.02))
+
+
+@pytest.mark.parametrize("N", [7, 200])
+def test_rows_left_out_take_no_part(g, N):
+    X, W, b, y, gl = make(N, 64, 300, "bf16", ignored=0.5)
+    y[0], y[1] = -1, 5
+    loss, lse, dX, dW, db = check(g, X, W, b, y, gl)
+    X2 = X.clone()
+    X2[y < 0] = float("nan")
+    gl2 = gl.masked_fill(y < 0, float("inf"))
+    loss2, lse2 = g.gmm_softmax_xent(X2, W, y, bias=b)
+    dX2, dW2, db2 = g.gmm_softmax_xent_grad(X2, W, y, lse2, gloss=gl2, bias=b)
+    assert torch.equal(loss, loss2) and torch.equal(dX, dX2) and torch.equal(dW, dW2) and torch.equal(db, db2)
+    assert (loss[y < 0] == 0).all() and (dX[y < 0] == 0).all() and torch.isnan(lse2[y < 0]).all()
+    y[:] = -100
+    loss, lse = g.gmm_softmax_xent(X2, W, y, bias=b)
+    dX, dW, db = g.gmm_softmax_xent_grad(X2, W, y, lse, bias=b)
+    assert not loss.any() and not dX.any() and not dW.any() and not db.any()
+
+
+@pytest.mark.parametrize("N", [4, 150])
+def test_label_past_the_head_is_nan(g, N):
+    X, W, b, y, gl = make(N, 32, 70, "f32", ignored=0.0)
+    y[2] = 70
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    assert torch.isnan(loss[2]) and torch.isnan(loss).sum() == 1 and not torch.isnan(lse).any()
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    assert torch.isnan(dX[2]).all() and torch.isnan(dX).any(dim=1).sum() == 1
+    assert torch.isnan(dW).all() and torch.isnan(db).all()
+
+
+@pytest.mark.parametrize("N", [6, 140])
+def test_classes_masked_by_the_bias(g, N):
+    X, W, b, y, gl = make(N, 64, 400, "bf16", ignored=0.0)
+    b[3:390] = -float("inf")  # whole tiles without a class
+    y.copy_(torch.arange(N, device="cuda", dtype=torch.int32) % 3)
+    loss, lse, dX, dW, db = check(g, X, W, b, y, gl)
+    assert not dW[3:390].any() and not db[3:390].any()
+    b[:] = -float("inf")
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    assert (lse == -float("inf")).all() and torch.isnan(loss).all()
+
+
+@pytest.mark.parametrize("N", [6, 140])
+def test_infinite_and_nan_logits(g, N):
+    X, W, b, y, gl = make(N, 16, 200, "f32", ignored=0.0)
+    X[1, 3] = float("nan")
+    X[2, 0] = float("inf")
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[1] = rest[2] = False
+    assert torch.isnan(lse[1]) and torch.isnan(lse[2])
+    assert torch.isfinite(lse[rest]).all() and torch.isfinite(loss[rest]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_confident_rows_and_large_logits(g, dtype):
+    X, W, b, y, gl = make(200, 64, 300, dtype, spread=60.0)
+    check(g, X, W, b, y, gl)
+    top = (X.float() @ W.float().t() + b).argmax(1).int()
+    check(g, X, W, b, top, gl)
+
+
+def test_row_gradients_of_mixed_size_in_half(g):
+    X, W, b, y, gl = make(300, 64, 500, "f16", ignored=0.0)
+    gl = torch.exp(torch.linspace(-20, 6, 300, device="cuda"))
+    check(g, X, W, b, y, gl)
+    check(g, X, W, b, y, torch.zeros_like(gl))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_accumulate_and_parts(g, dtype):
+    X, W, b, y, gl = make(150, 72, 333, dtype)
+    _, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    for keep in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1)):
+        got = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, **{k: None if on else False for k, on in zip(("dX", "dW", "dbias"), keep)})
+        for a, whole, on in zip(got, (dX, dW, db), keep):
+            assert (a is None) if not on else torch.equal(a, whole)
+    # added once, to what is there: one rounding of the exact sum
+    old = [torch.randn_like(t) for t in (dX, dW, db)]
+    acc = [t.clone() for t in old]
+    g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, dX=acc[0], dW=acc[1], dbias=acc[2], accumulate=True)
+    want, tol = ref.xent(X, W, y, b, gl)
+    for name, o, a in zip(("dX", "dW", "db"), old, acc):
+        s = want[name] + o.double()
+        ref.within(name, a, s, tol[name] + (ref.half(a.dtype) + 2 * ref.U) * (s.abs() + o.double().abs() + tol[name]))
+
+
+def test_no_rows(g):
+    X = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    W = torch.randn(100, 64, device="cuda").bfloat16()
+    y = torch.empty(0, device="cuda", dtype=torch.int32)
+    b = torch.zeros(100, device="cuda")
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    assert loss.shape == (0,) and lse.shape == (0,)
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, bias=b)
+    assert dX.shape == (0, 64) and not dW.any() and not db.any()
+    acc = torch.ones_like(dW)
+    g.gmm_softmax_xent_grad(X, W, y, lse, dX=False, dW=acc, accumulate=True, dbias=False)
+    assert (acc == 1).all()
+
+
+def test_gradient_against_differences(g):
+    """Central differences of the 64-bit loss: their own error is h^2 / 6 times
+    the third derivative, at most 6 sum_i |g_i| (max |w_v| or |x_i|)^3."""
+    X, W, b, y, gl = make(4, 5, 7, "f32", ignored=0.0)
+    _, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    _, tol = ref.xent(X, W, y, b, gl)
+    x, w, bb, yy, gg = (t.cpu().double().numpy() for t in (X, W, b, y, gl))
+    yy = yy.astype(int)
+
+    def f(x, w, bb):
+        L = x @ w.T + bb
+        m = L.max(1, keepdims=True)
+        return float((gg * (m[:, 0] + np.log(np.exp(L - m).sum(1)) - L[np.arange(4), yy])).sum())
+
+    h = 1e-4
+    M = max(np.abs(x).max(), np.abs(w).max(), 1.0)
+    slack = h * h * np.abs(gg).sum() * (5 * M) ** 3 + 1e-15 / h * 100
+    for name, arr, got in (("x", x, dX), ("w", w, dW), ("b", bb, db)):
+        diff = np.zeros_like(arr)
+        for i in np.ndindex(arr.shape):
+            up, dn = arr.copy(), arr.copy()
+            up[i] += h
+            dn[i] -= h
+            args = {"x": x, "w": w, "bb": bb}
+            key = "bb" if name == "b" else name
+            diff[i] = (f(**{**args, key: up}) - f(**{**args, key: dn})) / (2 * h)
+        bound = tol[{"x": "dX", "w": "dW", "b": "db"}[name]] + slack
+        ref.within("d" + name, got, torch.from_numpy(diff).cuda(), bound)
+
+
+@pytest.mark.parametrize("N", [10, 500])
+def test_same_inputs_same_bits_also_captured_and_on_another_stream(g, N):
+    X, W, b, y, gl = make(N, 128, 700, "bf16")
+
+    def step():
+        loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+        return (loss, lse) + g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+
+    first = [t.clone() for t in step()]
+    for a, c in zip(first, step()):
+        assert torch.equal(a, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for k in range(4):
+        X.normal_()
+        X.mul_(k + 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, c in zip(outs, step()):
+            assert torch.equal(a, c), k
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b, stream=side)
+    side.synchronize()
+    assert torch.equal(loss, outs[0])
+
+
+def test_rows_far_apart(g):
+    """Row offsets past 2^31 bytes: rows of a wide array."""
+    ld = (1 << 22) + 8
+    big = torch.empty(520, ld, device="cuda", dtype=torch.bfloat16)
+    X = big[:, :40]
+    X.copy_(torch.randn(520, 40, device="cuda"))
+    _, W, b, y, gl = make(520, 40, 120, "bf16")
+    check(g, X, W, b, y, gl)
+    check(g, X[::40], W, b, y[::40].contiguous(), gl[::40].contiguous())
