@@ -291,7 +291,8 @@ struct XentArgs {
   int64_t B, N, D, V, ld, stride_b, ld_w;
 };
 struct XentPlan {
-  bool skinny, pack_x, pack_w;   // few rows; rows / head copied to aligned rows first
+  bool small, skinny;            // at most 128 features (gmm_xent_small.hip); few rows
+  bool pack_x, pack_w;           // rows / head copied to aligned rows first
   bool slab_x, slab_w;           // products summed in float32 slabs
   int kbytes, split_x, split_w;
   int64_t Dp, nc, vc;            // padded D of the copies; rows of a chunk, classes of a piece

@@ -35,6 +35,7 @@
 // element for bf16, the size of the rounding of the outputs themselves), after
 // it was divided by max |g_i| (scal_kernel says why).
 #include "gmm_internal.h"
+#include "gmm_xent.h"
 
 #include <hip/hip_runtime.h>
 
@@ -44,44 +45,7 @@ namespace gmm {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr unsigned kOutside = 0x80000000u;  // an offset past every resource's end
-
-constexpr int kVm0 = 0x0f70;  // s_waitcnt vmcnt(0): the loads into LDS too
-
 enum Mode { LSE = 0, GRAD = 1, OUT = 2 };
-
-template <typename T>
-__device__ inline float to_f32(T v) {
-  return (float)v;
-}
-
-// one 16-byte chunk per lane of both operands: acc[n][m] += B[n][:] A[m][:]
-template <typename T>
-__device__ inline f32x4 mma(u32x4 b, u32x4 a, f32x4 c);
-template <>
-__device__ inline f32x4 mma<__bf16>(u32x4 b, u32x4 a, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0,
-                                                 0);
-}
-template <>
-__device__ inline f32x4 mma<_Float16>(u32x4 b, u32x4 a, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
-}
-template <>
-__device__ inline f32x4 mma<float>(u32x4 b, u32x4 a, f32x4 c) {
-  // element j of every lane's chunk: k = 4 (lane / 16) + j, the same order in both operands
-  const f32x4 bf = __builtin_bit_cast(f32x4, b), af = __builtin_bit_cast(f32x4, a);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(bf[j], af[j], c, 0, 0, 0);
-  return c;
-}
 
 struct GemmArgs {
   const char* A;       // [M][K], row stride lda bytes
@@ -132,16 +96,6 @@ __device__ inline int label_at(const GemmArgs& P, int64_t m, int64_t n) {
   if (m >= P.M) return -1;
   const int64_t y = (int64_t)P.labels[m] - P.v0 - n;
   return y < 0 || y >= (1 << 20) ? -1 : (int)y;
-}
-
-template <typename T>
-__device__ inline void store4(T* p, f32x4 v) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<f32x4*>(p) = v;
-  } else {
-    T t[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-    *reinterpret_cast<u32x2*>(p) = __builtin_bit_cast(u32x2, t);
-  }
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int MODE>
@@ -422,35 +376,6 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
   }
 }
 
-struct RowsArgs {
-  const char* x;            // element (b, i, d) at x + es (b stride_b + i ld + d)
-  int64_t N, ld, stride_b;  // rows per problem
-  int64_t r0, nr;           // rows of this chunk, over all problems
-  int D;
-};
-__device__ inline int64_t row_offset(const RowsArgs& R, int64_t r) {
-  return (r / R.N) * R.stride_b + (r % R.N) * R.ld;
-}
-
-// Scoring of a few rows (serving): at most 16 MT rows against the whole head,
-// bound by reading W once.  A wave owns 16 classes and walks their rows of W
-// from global memory into MFMA fragments (no LDS: nothing is shared); the
-// rows' fragments come from the L1.  One (max, sum) per row and 64 classes.
-template <typename T>
-__device__ inline u32x4 chunk_at(const char* row, int k, int bytes) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (k + 16 <= bytes) {
-    __builtin_memcpy(&v, row + k, 16);  // any alignment of the elements
-  } else if (k < bytes) {
-    T t[16 / sizeof(T)];
-#pragma unroll
-    for (int e = 0; e < 16 / (int)sizeof(T); ++e)
-      t[e] = k + e * (int)sizeof(T) < bytes ? reinterpret_cast<const T*>(row + k)[e] : T(0);
-    v = __builtin_bit_cast(u32x4, t);
-  }
-  return v;
-}
-
 template <typename T, int MT>
 __global__ void __launch_bounds__(256) skinny_kernel(GemmArgs P, RowsArgs R) {
   constexpr int U = 8;  // k-steps of 64 bytes in flight
@@ -694,6 +619,7 @@ unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
+// what a call does and where its parts of the workspace lie
 XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db) {
   XentPlan p{};
   const int64_t es = a.es, kt = 128 / es;
@@ -707,7 +633,40 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
   p.Dp = up(a.D, 16 / es);
   const int64_t R = std::max<int64_t>(a.B * a.N, 1), V = a.V;
   size_t o = 0;
-  if (!grad) {
+  p.small = a.D <= 128 && R > 64;
+  if (p.small) {
+    // rows stream past in chunks only where they are copied to aligned rows
+    // first, classes likewise (a chunk's and a piece's copies stay under 2^27 bytes)
+    p.nc = p.pack_x && want_dw ? std::min<int64_t>(R, 1 << 18) : R;
+    p.vc = p.pack_w && (!grad || want_dx) ? std::min<int64_t>(V, 1 << 18) : V;
+    p.np_r = (R + p.nc - 1) / p.nc;
+    p.np_v = (V + p.vc - 1) / p.vc;
+    p.lds = up(a.D, 4);
+    p.pack_x = p.pack_x && grad && want_dw;
+    p.pack_w = p.pack_w && (!grad || want_dx);
+    if (!grad) {
+      p.split_x = xent_small_splits(R, p.vc, a.dtype, a.D, 0);
+      if (p.split_x * p.np_v > 1) {
+        p.off_part = o; o = upz(o + sizeof(float2) * (size_t)(p.split_x * p.np_v * R));
+        p.off_lab = o;  o = upz(o + sizeof(float) * (size_t)R);
+      }
+    } else {
+      p.off_coef = o; o = upz(o + sizeof(float) * (size_t)R);
+      p.off_bmax = o; o = upz(o + sizeof(float) * 1024);
+      p.off_scal = o; o = upz(o + sizeof(float) * 2);
+      if (want_dx) {
+        p.split_x = xent_small_splits(R, p.vc, a.dtype, a.D, 1);
+        p.slab_x = p.split_x > 1 || p.np_v > 1;
+        if (p.slab_x) { p.off_sx = o; o = upz(o + sizeof(float) * (size_t)(p.split_x * R * p.lds)); }
+      }
+      if (want_dw || want_db) {
+        p.split_w = xent_small_splits(V, p.nc, a.dtype, a.D, 2);
+        p.slab_w = p.split_w > 1 || p.np_r > 1 || !want_dw;
+        if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * V * p.lds)); }
+        if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * V)); }
+      }
+    }
+  } else if (!grad) {
     p.skinny = R <= 64;
     if (p.skinny) p.pack_x = p.pack_w = false;  // it takes any alignment
     // rows of a chunk: at most 2^24 (max, sum) pairs; classes of a piece: all,
@@ -818,8 +777,136 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
   return hipSuccess;
 }
 
+// ---- rows of at most 128 features (gmm_xent_small.hip)
+template <typename T>
+hipError_t stream_classes(const XentArgs& a, const XentPlan& p, int64_t v0, int64_t nv, char* ws, SmallArgs& P,
+                          hipStream_t s) {
+  const int64_t es = sizeof(T);
+  P.own = RowsArgs{(const char*)a.x, a.N, a.ld, a.stride_b, 0, a.B * a.N, (int)a.D};
+  P.stream = (const char*)a.w + v0 * a.ld_w * es;
+  P.ld_stream = a.ld_w * es;
+  if (p.pack_w) {
+    const RowsArgs r{(const char*)a.w, a.V, a.ld_w, 0, v0, nv, (int)a.D};
+    GMM_TRY(pack<T>(r, ws + p.off_pw, p.Dp, s));
+    P.stream = ws + p.off_pw;
+    P.ld_stream = p.Dp * es;
+  }
+  P.count = nv;
+  P.v0 = v0;
+  P.V = a.V;
+  P.splits = p.split_x;
+  P.bias = a.bias;
+  P.labels = a.labels;
+  P.w = (const char*)a.w;
+  P.ld_w = a.ld_w;
+  return hipSuccess;
+}
+
+hipError_t join(const float2* part, int64_t nt, int64_t nr, const int32_t* labels, int64_t V, const float* lab,
+                float* loss, float* lse, hipStream_t s) {
+  if (nr == 1)
+    hipLaunchKernelGGL(join_kernel<1>, dim3(1), dim3(256), 0, s, part, nt, nr, labels, V, lab, loss, lse);
+  else if (nr <= 4096)
+    hipLaunchKernelGGL(join_kernel<16>, dim3((unsigned)((nr + 15) / 16)), dim3(256), 0, s, part, nt, nr, labels, V, lab,
+                       loss, lse);
+  else
+    hipLaunchKernelGGL(join_kernel<64>, dim3((unsigned)((nr + 63) / 64)), dim3(256), 0, s, part, nt, nr, labels, V, lab,
+                       loss, lse);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t small_forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse, char* ws, hipStream_t s) {
+  const int64_t R = a.B * a.N;
+  const bool joined = p.split_x * p.np_v > 1;
+  float2* part = reinterpret_cast<float2*>(ws + p.off_part);
+  float* lab = reinterpret_cast<float*>(ws + p.off_lab);
+  int64_t nt = 0;
+  for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) {
+    SmallArgs P{};
+    GMM_TRY(stream_classes<T>(a, p, v0, std::min(p.vc, a.V - v0), ws, P, s));
+    P.part = joined ? part + nt * R : nullptr;
+    P.lab = lab;
+    P.loss = loss;
+    P.lse_out = lse;
+    GMM_TRY(launch_xent_small(P, a.dtype, 0, s));
+    nt += p.split_x;
+  }
+  return joined ? join(part, nt, R, a.labels, a.V, lab, loss, lse, s) : hipSuccess;
+}
+
+template <typename T>
+hipError_t small_backward(const XentArgs& a, const XentPlan& p, const float* lse, const float* coef, const float* scal,
+                          char* dx, char* dw, float* db, int accumulate, char* ws, hipStream_t s) {
+  const int64_t R = a.B * a.N, es = sizeof(T);
+  if (dx) {
+    float* slab = p.slab_x ? reinterpret_cast<float*>(ws + p.off_sx) : nullptr;
+    for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) {
+      SmallArgs P{};
+      GMM_TRY(stream_classes<T>(a, p, v0, std::min(p.vc, a.V - v0), ws, P, s));
+      P.lse = lse;
+      P.coef = coef;
+      P.slab = slab;
+      P.lds = p.lds;
+      P.slab_stride = R * p.lds;
+      P.add = v0 > 0;
+      P.out = dx;
+      P.accumulate = accumulate;
+      GMM_TRY(launch_xent_small(P, a.dtype, 1, s));
+    }
+    if (slab) {
+      hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(R * p.lds / 4)), dim3(256), 0, s, slab, p.split_x, R * p.lds, p.lds,
+                         R, a.D, (const float*)nullptr, coef, reinterpret_cast<T*>(dx), accumulate);
+      GMM_TRY(hipGetLastError());
+    }
+  }
+  if (!dw && !db) return hipSuccess;
+  float* slab = p.slab_w ? reinterpret_cast<float*>(ws + p.off_sw) : nullptr;
+  for (int64_t r0 = 0; r0 < R; r0 += p.nc) {
+    const int64_t nr = std::min(p.nc, R - r0);
+    SmallArgs P{};
+    P.own = RowsArgs{(const char*)a.w, a.V, a.ld_w, 0, 0, a.V, (int)a.D};
+    P.stream = (const char*)a.x;
+    P.ld_stream = a.ld * es;
+    if (p.pack_x) {
+      const RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
+      GMM_TRY(pack<T>(r, ws + p.off_px, p.Dp, s));
+      P.stream = ws + p.off_px;
+      P.ld_stream = p.Dp * es;
+    }
+    P.count = nr;
+    P.V = a.V;
+    P.splits = p.split_w;
+    P.bias = a.bias;
+    P.labels = a.labels + r0;
+    P.lse = lse + r0;
+    P.coef = coef + r0;
+    P.scal = scal;
+    P.slab = slab;
+    P.lds = p.lds;
+    P.slab_stride = a.V * p.lds;
+    P.add = r0 > 0;
+    P.out = dw;
+    P.accumulate = accumulate;
+    P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
+    GMM_TRY(launch_xent_small(P, a.dtype, 2, s));
+    if (db) {  // the column sums were multiplied back already
+      hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((a.V + 63) / 64)), dim3(256), 0, s, P.dbp, p.split_w, a.V,
+                         (const float*)nullptr, db, accumulate || r0 > 0);
+      GMM_TRY(hipGetLastError());
+    }
+  }
+  if (slab && dw) {
+    hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(a.V * p.lds / 4)), dim3(256), 0, s, slab, p.split_w, a.V * p.lds,
+                       p.lds, a.V, a.D, (const float*)nullptr, (const float*)nullptr, reinterpret_cast<T*>(dw), accumulate);
+    GMM_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
 template <typename T>
 hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse, char* ws, hipStream_t s) {
+  if (p.small) return small_forward<T>(a, p, loss, lse, ws, s);
   const int64_t R = a.B * a.N;
   float2* part = reinterpret_cast<float2*>(ws + p.off_part);
   float* lab = reinterpret_cast<float*>(ws + p.off_lab);
@@ -848,15 +935,7 @@ hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse
         nt += P.tn;
       }
     }
-    float *lo = loss + r0, *ls = lse + r0;
-    const int32_t* y = a.labels + r0;
-    if (nr == 1)
-      hipLaunchKernelGGL(join_kernel<1>, dim3(1), dim3(256), 0, s, part, nt, nr, y, a.V, lab, lo, ls);
-    else if (nr <= 4096)
-      hipLaunchKernelGGL(join_kernel<16>, dim3((unsigned)((nr + 15) / 16)), dim3(256), 0, s, part, nt, nr, y, a.V, lab, lo, ls);
-    else
-      hipLaunchKernelGGL(join_kernel<64>, dim3((unsigned)((nr + 63) / 64)), dim3(256), 0, s, part, nt, nr, y, a.V, lab, lo, ls);
-    GMM_TRY(hipGetLastError());
+    GMM_TRY(join(part, nt, nr, a.labels + r0, a.V, lab, loss + r0, lse + r0, s));
   }
   return hipSuccess;
 }
@@ -876,6 +955,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
     hipLaunchKernelGGL(scal_kernel, dim3(1), dim3(64), 0, s, bmax, (int)cb, a.dtype == 2 ? 32768.f : 1.f, scal);
     GMM_TRY(hipGetLastError());
   }
+  if (p.small) return small_backward<T>(a, p, lse, coef, scal, dx, dw, db, accumulate, ws, s);
   for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) {
     const int64_t nv = std::min(p.vc, a.V - v0);
     if (dx) {

@@ -1,0 +1,446 @@
+// gmm_xent_small.hip -- softmax cross entropy and its gradients for rows of at
+// most 128 features (the width of the mixtures' rows), without G in memory.
+//
+// With few features the products are cheap and what costs is everything per
+// element of the N x V matrix: its exponential and, were G written, its bytes.
+// So nothing of it leaves the registers.  A wave keeps the rows of one side
+// (the owner: 16 RB rows, features as matrix-core fragments), the other side
+// streams through LDS in tiles of 64 rows, and each 16 x 16 block of logits
+// becomes in turn
+//   LSE  owner rows, streamed classes: a running maximum and sum per lane
+//   DX   owner rows, streamed classes: p - [v = y], rounded to the rows' type,
+//        the second operand of dX^T += W^T G^T right from the registers
+//   DW   owner classes, streamed rows: the same with c (p - [v = y]) and X
+// The logits are formed as stream x owner^T, so that a lane holds 4 consecutive
+// streamed rows of one owner row: the k order that the second product's
+// fragment wants (two blocks for the 32 of a 16-bit instruction), and its other
+// operand, the streamed tile with its rows along k, comes out of LDS through
+// the transposing read (float32: element reads).  The bias enters as the
+// accumulator's start.  Three exponentials an element (LSE, DX, DW) and 10 N V D
+// flops take the place of G's traffic, 8 bytes an element.
+//
+// LDS: a tile's rows are RBytes = D_padded * size apart, a row's 16-byte chunk c
+// in slot c ^ f(row); f makes the reads of 16 rows touch all 64 banks.
+//
+// Rounding: as in gmm_xent.hip.  DX rounds p - [v = y] itself and multiplies
+// by the row's coefficient in float32 at the end; half: p is scaled by 2^15
+// (in the exponent).
+#include "gmm_internal.h"
+#include "gmm_xent.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace gmm {
+
+namespace {
+
+enum Pass { LSE = 0, DX = 1, DW = 2 };
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr int kTile = 64;  // streamed rows per tile
+
+template <typename T>
+__device__ inline float dot16(u32x4 a, u32x4 b) {
+  T x[16 / sizeof(T)], y[16 / sizeof(T)];
+  __builtin_memcpy(x, &a, 16);
+  __builtin_memcpy(y, &b, 16);
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16 / (int)sizeof(T); ++e) s = fmaf((float)x[e], (float)y[e], s);
+  return s;
+}
+
+template <typename T, int DP, int RB, int PASS>
+__global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
+  constexpr int ES = sizeof(T), RBytes = DP * ES, KC = RBytes / 16, KS = KC / 4;
+  constexpr int kBytes = kTile * RBytes, JS = kBytes / 4096;  // 16-byte loads of a thread per tile
+  constexpr int RPB = RBytes >= 256 ? 1 : 256 / RBytes, FM = (KC < 16 ? KC : 16) - 1;
+  constexpr int NB = kTile / 16, ND = DP / 16;
+  constexpr float kTop = ES == 2 && !__is_same(T, __bf16) ? 32768.f : 1.f;  // DX: scale of p
+  __shared__ __attribute__((aligned(1024))) char st0[kBytes];
+  __shared__ __attribute__((aligned(1024))) char st1[kBytes];
+  __shared__ __attribute__((aligned(16))) float sp0[PASS == DW ? 3 * kTile : kTile];
+  __shared__ __attribute__((aligned(16))) float sp1[PASS == DW ? 3 * kTile : kTile];
+
+  // workgroups of one split of the stream on one XCD (they go round the 8)
+  const unsigned total = gridDim.x, id = blockIdx.x, q8 = total / 8, r8 = total % 8, xc = id % 8;
+  const unsigned pid = xc * q8 + (xc < r8 ? xc : r8) + id / 8;
+  const int split = pid / P.tiles_own, tile_own = pid % P.tiles_own;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int64_t o0 = ((int64_t)tile_own * 4 + wv) * (16 * RB);  // the wave's first owner row
+  const int kbytes = P.own.D * ES;
+
+  const int ntiles = (int)((P.count + kTile - 1) / kTile);
+  const int t0 = (int)((int64_t)ntiles * split / P.splits), t1 = (int)((int64_t)ntiles * (split + 1) / P.splits);
+  // rows of a tile; those of tiles from t1 on belong to others or to nobody and
+  // load as zeros that weigh nothing, so that a part may run one tile past its end
+  auto rows_of = [&](int t) { return t < t1 ? (int)min((int64_t)kTile, P.count - (int64_t)t * kTile) : 0; };
+
+  // ---- the owner's rows and what goes with each
+  u32x4 own[RB][KS];
+  float oa[RB];  // LSE, DX: -lse log2(e) (+ log2 kTop);  DW: the class's bias
+  float oc[RB];  // DX: the row's coefficient
+  int oy[RB];    // LSE: label;  DX: label within the piece;  DW: the class
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int64_t o = o0 + 16 * i + lr;
+    bool live = o < P.own.nr;
+    oa[i] = oc[i] = 0.f;
+    oy[i] = -1;
+    if (PASS == LSE && live) oy[i] = P.labels[o];
+    if (PASS == DX && live) {
+      oc[i] = P.coef[o];
+      live = oc[i] != 0.f;  // a row that takes no part is read as zeros
+    }
+    if (PASS == DX) {
+      oa[i] = live ? fmaf(-P.lse[o], kLog2e, __builtin_log2f(kTop)) : -INFINITY;
+      if (live) oy[i] = P.labels[o] - (int)P.v0;  // a class of this piece, or none
+    }
+    if (PASS == DW) {
+      oy[i] = (int)o;
+      oa[i] = live ? (P.bias ? P.bias[o] : 0.f) : -INFINITY;
+    }
+    const char* row = P.own.x + (live ? row_offset(P.own, o) : 0) * (int64_t)ES;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      own[i][k] = live ? chunk_at<T>(row, (k * 4 + lq) * 16, kbytes) : u32x4{0u, 0u, 0u, 0u};
+  }
+
+  // ---- streamed tiles.  Load j of a thread: row row0 + j RPJ of the tile, one
+  // 16-byte chunk, the same of every row but for f's bit 3 where rows are 512 bytes
+  constexpr int RPJ = 4096 / RBytes;
+  const int kpad = (kbytes + 15) & ~15;  // the stream's rows hold zeros from D to whole chunks
+  const int row0 = (wv * 1024 + lane * 16) / RBytes;
+  const int ch0 = ((wv * 1024 + lane * 16) % RBytes / 16) ^ ((row0 / RPB) & FM);
+  const unsigned last = (unsigned)P.count - 1;
+  float flag[JS];  // DW: the coefficients of the rows that are issued next
+  auto flags = [&](int t) {
+    if constexpr (PASS == DW) {  // rows past the last read the last one's; issue() leaves them out
+#pragma unroll
+      for (int j = 0; j < JS; ++j) flag[j] = P.coef[min((unsigned)(t * kTile + row0 + j * RPJ), last)];
+    }
+  };
+  auto issue = [&](char* st, int t) {
+    const int n = rows_of(t);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(P.stream) + (n > 0 ? (int64_t)t * kTile * P.ld_stream : 0), 0,
+        n > 0 ? (unsigned)((n - 1) * P.ld_stream + kpad) : 0u, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < JS; ++j) {
+      const int ch = RBytes == 512 ? ch0 ^ (8 * (j & 1)) : ch0;
+      bool in = row0 + j * RPJ < n && ch * 16 < kpad;
+      if (PASS == DW) in = in && flag[j] != 0.f;  // rows that take no part arrive as zeros
+      const unsigned o = in ? (unsigned)((row0 + j * RPJ) * (int)P.ld_stream + ch * 16) : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(st + (j * 4 + wv) * 1024), 16, o, 0, 0, 0);
+    }
+  };
+  // what goes with each streamed row: LSE, DX: bias;  DW: -lse log2(e), c, label
+  float pa = 0.f, pb = 0.f;
+  int py = -1;
+  const float mult = PASS == DW && P.scal ? P.scal[0] : 1.f;
+  const unsigned prow = lane;  // every wave fetches the 64 rows, the first puts them
+  auto fetch = [&](int t) {
+    const unsigned r = min((unsigned)(t * kTile) + prow, last);
+    if constexpr (PASS == DW) {
+      pa = P.lse[r];
+      pb = P.coef[r];
+      py = P.labels[r];
+    } else {
+      pa = P.bias ? P.bias[P.v0 + r] : 0.f;
+    }
+  };
+  auto put = [&](float* sp, int t) {
+    if (wv != 0) return;
+    const bool in = lane < rows_of(t);
+    if constexpr (PASS == DW) {
+      const bool live = in && pb != 0.f;
+      sp[lane] = live ? pa * -kLog2e : -INFINITY;
+      sp[kTile + lane] = live ? pb * mult : 0.f;
+      sp[2 * kTile + lane] = __builtin_bit_cast(float, live ? py : -1);
+    } else {
+      sp[lane] = in ? pa : -INFINITY;
+    }
+  };
+
+  constexpr int NA = PASS == LSE ? 1 : RB;
+  f32x4 acc[NA][ND];  // DX, DW: element e of acc[i][d]: feature 16 d + 4 lq + e of owner row 16 i + lr
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[i][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float mx[RB], sm[RB];  // LSE: maximum and sum;  DW: mx is the bias gradient
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    mx[i] = PASS == LSE ? -1e38f : 0.f;  // finite: -inf logits stay below it
+    sm[i] = 0.f;
+  }
+
+  // logits of streamed block jb (16 rows) against owner block i
+  const int fr = (lr / RPB) & FM;
+  auto logits = [&](const char* st, const float* sp, int jb, f32x4* s) {
+    if constexpr (PASS == DW) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) s[i] = f32x4{oa[i], oa[i], oa[i], oa[i]};
+    } else {
+      const f32x4 b = *reinterpret_cast<const f32x4*>(sp + 16 * jb + 4 * lq);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) s[i] = b;
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(st + (16 * jb + lr) * RBytes + (((k * 4 + lq) ^ fr) * 16));
+#pragma unroll
+      for (int i = 0; i < RB; ++i) s[i] = mma<T>(a, own[i][k], s[i]);
+    }
+  };
+  // G of a block, in place
+  auto gradient = [&](const float* sp, int jb, int t, f32x4* s) {
+    if constexpr (PASS == DX) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const int y = oy[i] - t * kTile - 4 * lq - 16 * jb;  // never equal where there is no label
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, oa[i]));
+          s[i][e] = p - (y == e ? kTop : 0.f);
+        }
+      }
+    } else {
+      const f32x4 nl = *reinterpret_cast<const f32x4*>(sp + 16 * jb + 4 * lq);
+      const f32x4 c = *reinterpret_cast<const f32x4*>(sp + kTile + 16 * jb + 4 * lq);
+      const i32x4 y = *reinterpret_cast<const i32x4*>(sp + 2 * kTile + 16 * jb + 4 * lq);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, nl[e]));
+          s[i][e] = c[e] * (p - (y[e] == oy[i] ? 1.f : 0.f));
+        }
+        mx[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+        asm volatile("" : "+v"(mx[i]));  // summed here: left alone, every G would stay in a register until the loop's end
+      }
+    }
+  };
+
+  auto compute = [&](const char* st, const float* sp, int t) {
+    if constexpr (PASS == LSE) {
+      f32x4 s[NB][RB];
+#pragma unroll
+      for (int jb = 0; jb < NB; ++jb) logits(st, sp, jb, s[jb]);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        float m = mx[i];
+#pragma unroll
+        for (int jb = 0; jb < NB; ++jb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = fmaxf(m, s[jb][i][e]);
+        const float nm = -m * kLog2e;
+        float a = sm[i] * __builtin_amdgcn_exp2f((mx[i] - m) * kLog2e);  // exactly 1 where nothing changed
+#pragma unroll
+        for (int jb = 0; jb < NB; ++jb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a += __builtin_amdgcn_exp2f(fmaf(s[jb][i][e], kLog2e, nm));
+        sm[i] = a;
+        mx[i] = m;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < NB / 2; ++h) {
+        f32x4 s[2][RB];
+        u32x2 g[RB][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          logits(st, sp, 2 * h + u, s[u]);
+          gradient(sp, 2 * h + u, t, s[u]);
+          if constexpr (ES == 2)
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+              const T v[4] = {(T)s[u][i][0], (T)s[u][i][1], (T)s[u][i][2], (T)s[u][i][3]};
+              g[i][u] = __builtin_bit_cast(u32x2, v);
+            }
+          __builtin_amdgcn_sched_barrier(0);  // one block's temporaries at a time
+        }
+        if constexpr (ES == 2) {
+          // lane 16 a + b reads feature 16 d + b of streamed rows 4 a .. 4 a + 3 of either block
+          const int rr = lane >> 2, fx = (rr / RPB) & FM;
+          const char* src = st + (32 * h + rr) * RBytes + 8 * (lane & 1);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const int slot = ((2 * d + ((lane & 3) >> 1)) ^ fx) * 16;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(src + slot));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(src + 16 * RBytes + slot));
+            const u32x4 a = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+              acc[i][d] = mma<T>(a, u32x4{g[i][0][0], g[i][0][1], g[i][1][0], g[i][1][1]}, acc[i][d]);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = 4 * lq + e, fx = (row / RPB) & FM;
+              const char* src = st + (32 * h + 16 * u + row) * RBytes + 4 * (lr & 3);
+#pragma unroll
+              for (int d = 0; d < ND; ++d) {
+                const float a = *reinterpret_cast<const float*>(src + ((4 * d + (lr >> 2)) ^ fx) * 16);
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                  acc[i][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, s[u][i][e], acc[i][d], 0, 0, 0);
+              }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+
+  // loads of a tile run while the tile before it is computed
+  auto step = [&](char* cur, float* pcur, char* nxt, float* pnxt, int t) {
+    __builtin_amdgcn_s_waitcnt(kVm0);
+    __syncthreads();
+    issue(nxt, t + 1);
+    fetch(t + 1);
+    flags(t + 2);
+    compute(cur, pcur, t);
+    put(pnxt, t + 1);
+  };
+  flags(t0);
+  issue(st0, t0);
+  fetch(t0);
+  put(sp0, t0);
+  flags(t0 + 1);
+  for (int t = t0; t < t1; t += 2) {
+    step(st0, sp0, st1, sp1, t);
+    step(st1, sp1, st0, sp0, t + 1);
+  }
+  __builtin_amdgcn_s_waitcnt(kVm0);  // nothing of the last loads is in flight at the end
+
+  // ---- results
+  if constexpr (PASS == LSE) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int64_t o = o0 + 16 * i + lr;
+      const bool in = o < P.own.nr;
+      // the label's logit: the owner's fragments against the label's row of the head
+      const bool lab = oy[i] >= 0 && oy[i] < P.V;
+      float l = 0.f;
+      const char* wr = P.w + (lab ? oy[i] * P.ld_w * ES : 0);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        if (lab) l += dot16<T>(own[i][k], chunk_at<T>(wr, (k * 4 + lq) * 16, kbytes));
+      float m = mx[i], s = sm[i];
+#pragma unroll
+      for (int off = 16; off < 64; off <<= 1) {
+        l += __shfl_xor(l, off);
+        const float m2 = __shfl_xor(m, off), s2 = __shfl_xor(s, off), top = fmaxf(m, m2);
+        s = s * __builtin_amdgcn_exp2f((m - top) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - top) * kLog2e);
+        m = top;
+      }
+      if (lab && P.bias) l += P.bias[oy[i]];
+      if (!in || lq != 0) continue;
+      if (P.part) {
+        P.part[split * P.own.nr + o] = make_float2(m, s);
+        if (split == 0) P.lab[o] = l;
+      } else {
+        const float z = m + logf(s);
+        P.lse_out[o] = z;
+        P.loss[o] = oy[i] < 0 ? 0.f : lab ? z - l : NAN;
+      }
+    }
+  } else {
+    const float back = PASS == DW && P.scal ? P.scal[1] : 1.f;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int64_t o = o0 + 16 * i + lr;
+      const bool in = o < P.own.nr;
+      if (PASS == DW && P.dbp) {
+        float v = mx[i] * back;
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if (in && lq == 0) P.dbp[split * P.own.nr + o] = v;
+      }
+      if (!in) continue;
+      const float c = PASS == DX ? oc[i] / kTop : back;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const int64_t f = 16 * d + 4 * lq;
+        if (f >= P.own.D) continue;
+        f32x4 v = acc[i][d] * c;
+        if (PASS == DX && oc[i] == 0.f) v = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (P.slab) {
+          float* p = P.slab + split * P.slab_stride + o * P.lds + f;
+          if (P.add) v += *reinterpret_cast<const f32x4*>(p);
+          *reinterpret_cast<f32x4*>(p) = v;
+          continue;
+        }
+        T* p = reinterpret_cast<T*>(P.out) + o * P.own.D + f;
+        if (f + 4 <= P.own.D && !P.accumulate) {
+          store4<T>(p, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (f + e < P.own.D) p[e] = (T)(v[e] + (P.accumulate ? to_f32(p[e]) : 0.f));
+        }
+      }
+    }
+  }
+}
+
+// 16-row blocks of a wave: as many as the registers hold
+constexpr int owner_blocks(int es, int dp, int pass) {
+  const int bytes = es * dp;
+  if (pass == LSE) return es == 4 && bytes > 128 ? 2 : 4;
+  return bytes > 256 ? 1 : bytes > 128 ? 2 : 4;
+}
+
+template <typename T, int DP, int PASS>
+hipError_t launch_p(const SmallArgs& P, hipStream_t s) {
+  constexpr int RB = owner_blocks(sizeof(T), DP, PASS);
+  const dim3 grid((unsigned)((int64_t)P.tiles_own * P.splits));
+  hipLaunchKernelGGL((small_kernel<T, DP, RB, PASS>), grid, dim3(256), 0, s, P);
+  return hipGetLastError();
+}
+template <typename T, int DP>
+hipError_t launch(const SmallArgs& P, int pass, hipStream_t s) {
+  if (pass == LSE) return launch_p<T, DP, LSE>(P, s);
+  if (pass == DX) return launch_p<T, DP, DX>(P, s);
+  return launch_p<T, DP, DW>(P, s);
+}
+
+template <typename T>
+hipError_t launch_t(const SmallArgs& P, int pass, hipStream_t s) {
+  if (P.own.D <= 32) return launch<T, 32>(P, pass, s);
+  if (P.own.D <= 64) return launch<T, 64>(P, pass, s);
+  return launch<T, 128>(P, pass, s);
+}
+
+}  // namespace
+
+int xent_small_rows(int dtype, int64_t D, int pass) {
+  return 64 * owner_blocks(dtype == 0 ? 4 : 2, D <= 32 ? 32 : D <= 64 ? 64 : 128, pass);
+}
+
+int xent_small_splits(int64_t owners, int64_t streamed, int dtype, int64_t D, int pass) {
+  const int rows = xent_small_rows(dtype, D, pass);
+  const int64_t t = (owners + rows - 1) / rows, tiles = (streamed + kTile - 1) / kTile;
+  const int64_t want = t >= 2 * kNumCU ? 1 : (2 * kNumCU) / t;
+  return (int)std::max<int64_t>(1, std::min(want, tiles / 4));
+}
+
+hipError_t launch_xent_small(SmallArgs P, int dtype, int pass, hipStream_t s) {
+  const int rows = xent_small_rows(dtype, P.own.D, pass);
+  P.tiles_own = (int)((P.own.nr + rows - 1) / rows);
+  if (dtype == 1) return launch_t<__bf16>(P, pass, s);
+  if (dtype == 2) return launch_t<_Float16>(P, pass, s);
+  return launch_t<float>(P, pass, s);
+}
+
+}  // namespace gmm
