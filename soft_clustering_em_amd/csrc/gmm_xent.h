@@ -18,6 +18,13 @@ constexpr unsigned kOutside = 0x80000000u;  // an offset past every resource's e
 
 constexpr int kVm0 = 0x0f70;  // s_waitcnt vmcnt(0): the loads into LDS too
 
+typedef __attribute__((address_space(3))) char lds_char;
+// 16 bytes per lane from a buffer straight to LDS: lane l to at + 16 l; an
+// offset past the resource's end brings zeros
+__device__ inline void load_lds16(__amdgpu_buffer_rsrc_t r, lds_char* at, unsigned offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)at, 16, offset, 0, 0, 0);
+}
+
 template <typename T>
 __device__ inline float to_f32(T v) {
   return (float)v;

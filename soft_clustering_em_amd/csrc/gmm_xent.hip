@@ -98,6 +98,10 @@ __device__ inline int label_at(const GemmArgs& P, int64_t m, int64_t n) {
   return y < 0 || y >= (1 << 20) ? -1 : (int)y;
 }
 
+// this wave's loads into LDS have landed and its LDS reads are done; then the
+// other waves' too
+__device__ inline void next_tile() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 template <typename T, int BM, int BN, int WM, int WN, int MODE>
 __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
   constexpr int NT = WM * WN * 64;          // threads
@@ -119,35 +123,27 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
       const_cast<char*>(P.A) + m0 * P.lda, 0, (unsigned)((mrows - 1) * P.lda + P.kbytes), 0x00020000);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<char*>(P.B) + n0 * P.ldb, 0, (unsigned)((nrows - 1) * P.ldb + P.kbytes), 0x00020000);
-  // lane l of load j: LDS row 8 (j * waves + wave) + l / 8, slot l % 8
-  unsigned oa[JA], ob[JB];
-  int ca[JA], cb[JB];
+  const int kt0 = (int)((int64_t)P.ktiles * z / P.splits), kt1 = (int)((int64_t)P.ktiles * (z + 1) / P.splits);
+  // load j of lane l: LDS row 8 (j * waves + wave) + l / 8, slot l % 8, which
+  // holds the same chunk c for every j.  Rows past the operand's last have
+  // offsets past the resource's end by themselves.
+  static_assert((NT / 64) % 2 == 0, "rows of a thread's loads are a multiple of 16 apart");
+  const int row0 = 8 * wv + (lane >> 3), c16 = ((lane & 7) ^ ((row0 >> 1) & 7)) * 16;
+  const unsigned oa = (unsigned)(row0 * P.lda) + c16, ob = (unsigned)(row0 * P.ldb) + c16;
+  const unsigned sa = (unsigned)(8 * (NT / 64) * P.lda), sb = (unsigned)(8 * (NT / 64) * P.ldb);
+  const int kend = min(P.kbytes, kt1 * 128);  // bytes of a row that this split reads end here
+  auto issue = [&](lds_char* st, int kt) {
+    const unsigned kb = kt * 128;
+    // past the last k the offset's top bit is set (added, not selected: a
+    // select becomes branches around the loads)
+    const unsigned out = (int)kb + c16 < kend ? 0u : kOutside;
+    const unsigned xa = oa + out, xb = ob + out;
 #pragma unroll
-  for (int j = 0; j < JA; ++j) {
-    const int row = 8 * (j * (NT / 64) + wv) + (lane >> 3);
-    ca[j] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-    oa[j] = row < mrows ? (unsigned)(row * P.lda) + ca[j] : kOutside;
-  }
+    for (int j = 0; j < JA; ++j)
+      load_lds16(ra, st + (j * (NT / 64) + wv) * 1024, xa + (kb + j * sa));
 #pragma unroll
-  for (int j = 0; j < JB; ++j) {
-    const int row = 8 * (j * (NT / 64) + wv) + (lane >> 3);
-    cb[j] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-    ob[j] = row < nrows ? (unsigned)(row * P.ldb) + cb[j] : kOutside;
-  }
-  auto issue = [&](char* st, int kt) {
-    const int kb = kt * 128;
-#pragma unroll
-    for (int j = 0; j < JA; ++j) {
-      const unsigned o = (kb + ca[j] < P.kbytes && oa[j] != kOutside) ? oa[j] + kb : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ra, (__attribute__((address_space(3))) void*)(st + (j * (NT / 64) + wv) * 1024), 16, o, 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      const unsigned o = (kb + cb[j] < P.kbytes && ob[j] != kOutside) ? ob[j] + kb : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (__attribute__((address_space(3))) void*)(st + BM * 128 + (j * (NT / 64) + wv) * 1024), 16, o, 0, 0, 0);
-    }
+    for (int j = 0; j < JB; ++j)
+      load_lds16(rb, st + BM * 128 + (j * (NT / 64) + wv) * 1024, xb + (kb + j * sb));
   };
 
   f32x4 acc[MT][NN];
@@ -157,51 +153,59 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
     for (int j = 0; j < NN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int lr = lane & 15, lq = lane >> 4;
-  const int fsw = (lr >> 1) & 7;
-  auto compute = [&](const char* st) {
+  constexpr int MH = MT / 2;
+  auto read_a = [&](const char* st, int half, int g, u32x4* f) {
+    const int slot = ((half * 4 + lq) ^ ((lr >> 1) & 7)) * 16;
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      const int slot = ((step * 4 + lq) ^ fsw) * 16;
-      u32x4 b[NN];
+    for (int i = 0; i < MH; ++i)
+      f[i] = *reinterpret_cast<const u32x4*>(st + ((wm * MT + g * MH + i) * 16 + lr) * 128 + slot);
+  };
+  auto read_b = [&](const char* st, int half, u32x4* f) {
+    const int slot = ((half * 4 + lq) ^ ((lr >> 1) & 7)) * 16;
 #pragma unroll
-      for (int j = 0; j < NN; ++j)
-        b[j] = *reinterpret_cast<const u32x4*>(st + BM * 128 + ((wn * NN + j) * 16 + lr) * 128 + slot);
+    for (int j = 0; j < NN; ++j)
+      f[j] = *reinterpret_cast<const u32x4*>(st + BM * 128 + ((wn * NN + j) * 16 + lr) * 128 + slot);
+  };
+  auto multiply = [&](const u32x4* fb, const u32x4* fa, int g) {
+    __builtin_amdgcn_sched_barrier(0);  // the reads and loads before it first: they have the longest way
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const u32x4 a = *reinterpret_cast<const u32x4*>(st + ((wm * MT + i) * 16 + lr) * 128 + slot);
+    for (int i = 0; i < MH; ++i)
 #pragma unroll
-        for (int j = 0; j < NN; ++j) acc[i][j] = mma<T>(b[j], a, acc[i][j]);
-      }
-    }
+      for (int j = 0; j < NN; ++j) acc[g * MH + i][j] = mma<T>(fb[j], fa[i], acc[g * MH + i][j]);
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  const int kt0 = (int)((int64_t)P.ktiles * z / P.splits), kt1 = (int)((int64_t)P.ktiles * (z + 1) / P.splits);
-  // Loads of a tile run while the tile before it is computed; a wait and a
-  // barrier between tiles: every wave's loads have landed and the buffer that
-  // is loaded next is read out.
-  auto landed = [] {
-    __builtin_amdgcn_s_waitcnt(kVm0);
-    __syncthreads();
+  // A k-tile is multiplied in four steps (two halves of k, two of the wave's
+  // rows), each from registers that the step before it read from LDS, so that
+  // no product waits for LDS.  A tile's buffer is free once the last step's
+  // operands are in registers: the tile after next starts into it there, and
+  // has until the same point of the next tile to land.
+  u32x4 b0[NN], b1[NN], a0[MH], a1[MH];
+  auto tile = [&](char* cur, const char* nxt, int k) {
+    read_a(cur, 0, 1, a1);
+    multiply(b0, a0, 0);
+    read_b(cur, 1, b1);
+    read_a(cur, 1, 0, a0);
+    multiply(b0, a1, 1);
+    read_a(cur, 1, 1, a1);
+    multiply(b1, a0, 0);
+    next_tile();  // tile k + 1 has landed, tile k is read out
+    issue((lds_char*)cur, k + 2);
+    read_b(nxt, 0, b0);
+    read_a(nxt, 0, 0, a0);
+    multiply(b1, a1, 1);
   };
+  issue((lds_char*)st0, kt0);
+  next_tile();
+  issue((lds_char*)st1, kt0 + 1);
+  read_b(st0, 0, b0);
+  read_a(st0, 0, 0, a0);
   int kt = kt0;
-  if (kt < kt1) issue(st0, kt);
-  for (; kt + 2 < kt1; kt += 2) {
-    landed();
-    issue(st1, kt + 1);
-    compute(st0);
-    landed();
-    issue(st0, kt + 2);
-    compute(st1);
+  for (; kt + 2 <= kt1; kt += 2) {
+    tile(st0, st1, kt);
+    tile(st1, st0, kt + 1);
   }
-  if (kt < kt1) {  // one or two are left
-    landed();
-    if (kt + 1 < kt1) issue(st1, kt + 1);
-    compute(st0);
-    if (kt + 1 < kt1) {
-      landed();
-      compute(st1);
-    }
-  }
+  if (kt < kt1) tile(st0, st1, kt);
 
   // accumulator element e of acc[i][j]: row m = 16 (wm MT + i) + lr of the
   // tile, column n = 16 (wn NN + j) + 4 lq + e
@@ -248,7 +252,8 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
         const int64_t n = n0 + nw + 16 * j + e;
         bv[j][e] = n < P.N ? (P.bias ? P.bias[P.v0 + n] : 0.f) : -INFINITY;
       }
-    __syncthreads();  // the last k-tile is read out: LDS is free
+    __builtin_amdgcn_s_waitcnt(kVm0);
+    __syncthreads();  // no load is on its way, the last k-tile is read out: LDS is free
 
     if constexpr (MODE == LSE) {
       float2* red = reinterpret_cast<float2*>(st0);  // [WN][BM]
