@@ -67,10 +67,7 @@ __device__ inline int64_t row_offset(const RowsArgs& R, int64_t r) {
   return (r / R.N) * R.stride_b + (r % R.N) * R.ld;
 }
 
-// Scoring of a few rows (serving): at most 16 MT rows against the whole head,
-// bound by reading W once.  A wave owns 16 classes and walks their rows of W
-// from global memory into MFMA fragments (no LDS: nothing is shared); the
-// rows' fragments come from the L1.  One (max, sum) per row and 64 classes.
+// chunk k / 16 of a row of `bytes` bytes, zeros past them; any alignment of the elements
 template <typename T>
 __device__ inline u32x4 chunk_at(const char* row, int k, int bytes) {
   u32x4 v = {0u, 0u, 0u, 0u};

@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
       static_assert(WM * WN * kRegion <= 2 * kStage, "the waves' regions fill the two stages");
       T* reg = reinterpret_cast<T*>((wv < WM * WN / 2 ? st0 : st1) + (wv % (WM * WN / 2)) * kRegion);
       const float mult = P.scal ? P.scal[0] : 1.f;
+      const unsigned pick = lane & 1 ? 0x03020706u : 0x05040100u;  // this lane's column of a pair
       float cs[NN][4];
 #pragma unroll
       for (int j = 0; j < NN; ++j)
@@ -332,13 +333,28 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
               cs[j][e] += g[e];
             }
             const int64_t n = n0 + nw + 16 * j;
-            if (m < P.M && n < P.ldg) store4<T>(reinterpret_cast<T*>(P.G) + m * P.ldg + n, g);
-            if (P.GT) {
+            const int ml = 16 * ii + lr, nl = 16 * j + 4 * lq;
+            if constexpr (sizeof(T) == 2) {
+              const T t[4] = {(T)g[0], (T)g[1], (T)g[2], (T)g[3]};
+              const u32x2 w = __builtin_bit_cast(u32x2, t);
+              if (m < P.M && n < P.ldg) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + m * P.ldg + n) = w;
+              if (P.GT) {
+                // a dword holds two columns of one row; neighbouring rows' lanes
+                // trade, so that each writes two rows of one column
+                const int mp = ml & ~1, ch = (mp / EPC) ^ (CL * lq);  // rows 4 apart would share banks
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int ml = 16 * ii + lr;
-                const int ch = (ml / EPC) ^ (CL * lq);  // rows 4 apart would share banks
-                reg[(16 * j + 4 * lq + e) * (SUB * 16) + ch * EPC + ml % EPC] = (T)g[e];
+                for (int u = 0; u < 2; ++u) {
+                  const unsigned o = __builtin_amdgcn_mov_dpp(w[u], 0xB1, 0xF, 0xF, true);  // quad_perm 1 0 3 2
+                  const unsigned v = __builtin_amdgcn_perm(o, w[u], pick);
+                  *reinterpret_cast<unsigned*>(reg + (nl + 2 * u + (lane & 1)) * (SUB * 16) + ch * EPC + mp % EPC) = v;
+                }
+              }
+            } else {
+              if (m < P.M && n < P.ldg) store4<T>(reinterpret_cast<T*>(P.G) + m * P.ldg + n, g);
+              if (P.GT) {
+                const int ch = (ml / EPC) ^ (CL * lq);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) reg[(nl + e) * (SUB * 16) + ch * EPC + ml % EPC] = (T)g[e];
               }
             }
             __builtin_amdgcn_sched_barrier(0);  // one 16 x 16 tile's temporaries at a time
@@ -381,6 +397,10 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
   }
 }
 
+// Scoring of a few rows (serving): at most 16 MT rows against the whole head,
+// bound by reading W once.  A wave owns 16 classes and walks their rows of W
+// from global memory into MFMA fragments (no LDS: nothing is shared); the
+// rows' fragments come from the L1.  One (max, sum) per row and 64 classes.
 template <typename T, int MT>
 __global__ void __launch_bounds__(256) skinny_kernel(GemmArgs P, RowsArgs R) {
   constexpr int U = 8;  // k-steps of 64 bytes in flight
