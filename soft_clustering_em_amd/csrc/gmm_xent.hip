@@ -552,39 +552,62 @@ __global__ void __launch_bounds__(256) pack_kernel(RowsArgs R, T* dst, int Dp) {
   }
 }
 
-// rows of any layout -> [D][ldo], zeros past nr; rows with live = 0 become zeros
+// rows of any layout -> [D][ldo], zeros past nr; rows with live = 0 become
+// zeros.  64 x 64 tiles, 16 bytes a thread in and out.
 template <typename T>
 __global__ void __launch_bounds__(256) transpose_kernel(RowsArgs R, const float* live, T* dst, int64_t ldo) {
-  __shared__ T tile[64][64 + 4 / sizeof(T)];
+  constexpr int E = 16 / (int)sizeof(T), CR = 64 / E;  // elements of a chunk, chunks of a tile row
+  __shared__ __attribute__((aligned(16))) T tile[64][64 + E];
   const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int d0 = blockIdx.y * 64, c = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int d0 = blockIdx.y * 64;
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const int64_t r = r0 + w + 4 * u;
-    T v = T(0);
-    if (r < R.nr && d0 + c < R.D && !(live && live[r] == 0.f))
-      v = reinterpret_cast<const T*>(R.x)[row_offset(R, R.r0 + r) + d0 + c];
-    tile[w + 4 * u][c] = v;
+  for (int u = 0; u < 64 * CR / 256; ++u) {
+    const int i = threadIdx.x + 256 * u, rr = i / CR, c = i % CR;
+    const int64_t r = r0 + rr;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (r < R.nr && !(live && live[r] == 0.f))
+      v = chunk_at<T>(R.x + row_offset(R, R.r0 + r) * (int64_t)sizeof(T), (d0 + c * E) * (int)sizeof(T),
+                      R.D * (int)sizeof(T));
+    *reinterpret_cast<u32x4*>(&tile[rr][c * E]) = v;
   }
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const int d = w + 4 * u;
-    if (d0 + d < R.D && r0 + c < ldo) dst[(int64_t)(d0 + d) * ldo + r0 + c] = tile[c][d];
+  for (int u = 0; u < 64 * CR / 256; ++u) {
+    const int i = threadIdx.x + 256 * u, d = i / CR, c = i % CR;
+    T v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = tile[c * E + e][d];
+    if (d0 + d < R.D && r0 + c * E < ldo)  // ldo: whole k-tiles
+      __builtin_memcpy(dst + (int64_t)(d0 + d) * ldo + r0 + c * E, v, 16);
   }
 }
 
-// out[r][c] = scale sum_z slab[z][r][c]  (+ out)
-template <typename T>
+// out[r][c] = scale sum_z slab[z][r][c]  (+ out); SL threads share a sum over z
+template <typename T, int SL>
 __global__ void __launch_bounds__(256) finish_kernel(const float* slab, int splits, int64_t stride, int64_t lds, int64_t M,
                                                      int64_t N, const float* scal, const float* live, T* out,
                                                      int accumulate) {
+  constexpr int W = 256 / SL;
+  __shared__ f32x4 red[SL == 1 ? 1 : 256];
   const int64_t q = lds / 4, n = M * q;
   const float sc = scal ? scal[1] : 1.f;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
-    const int64_t r = t / q, c = t % q * 4;
+  const int sl = threadIdx.x / W;
+  for (int64_t t0 = (int64_t)blockIdx.x * W; t0 < n; t0 += (int64_t)gridDim.x * W) {
+    const int64_t t = t0 + threadIdx.x % W;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(slab + z * stride + r * lds + c);
+    if (t < n)  // lds / 4 groups a row: element 4 t of the slab
+#pragma unroll 8
+      for (int z = sl; z < splits; z += SL) v += *reinterpret_cast<const f32x4*>(slab + z * stride + 4 * t);
+    if constexpr (SL > 1) {
+      __syncthreads();
+      red[threadIdx.x] = v;
+      __syncthreads();
+      if (sl == 0)
+#pragma unroll
+        for (int k = 1; k < SL; ++k) v += red[k * W + threadIdx.x];
+    }
+    if (sl != 0 || t >= n) continue;
+    const int64_t r = t / q, c = t % q * 4;
     v = live && live[r] == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * sc;
     T* p = out + r * N + c;
     if (N % 4 == 0 && !accumulate) {
@@ -597,19 +620,21 @@ __global__ void __launch_bounds__(256) finish_kernel(const float* slab, int spli
   }
 }
 
-// db[n] = scale sum over tile rows of the column sums (+ db)
+// db[n] = scale sum over tile rows of the column sums (+ db); 16 threads a sum
 __global__ void __launch_bounds__(256) dbias_kernel(const float* dbp, int tm, int64_t N, const float* scal, float* db,
                                                     int add) {
-  __shared__ float red[4][64];
-  const int c = threadIdx.x & 63, sl = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + c;
+  __shared__ float red[16][16];
+  const int c = threadIdx.x & 15, sl = threadIdx.x >> 4;
+  const int64_t n = (int64_t)blockIdx.x * 16 + c;
   float v = 0.f;
   if (n < N)
-    for (int t = sl; t < tm; t += 4) v += dbp[(int64_t)t * N + n];
+#pragma unroll 8
+    for (int t = sl; t < tm; t += 16) v += dbp[(int64_t)t * N + n];
   red[sl][c] = v;
   __syncthreads();
   if (sl == 0 && n < N) {
-    v = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+#pragma unroll
+    for (int k = 1; k < 16; ++k) v += red[k][c];
     v *= scal ? scal[1] : 1.f;
     db[n] = add ? db[n] + v : v;
   }
@@ -753,6 +778,19 @@ namespace {
   } while (0)
 
 template <typename T>
+hipError_t finish(const float* slab, int splits, int64_t stride, int64_t lds, int64_t M, int64_t N, const float* scal,
+                  const float* live, char* out, int accumulate, hipStream_t s) {
+  const int64_t n = M * lds / 4;
+  // 16 threads a sum where one would walk 16 slabs or more
+  if (splits >= 16)
+    hipLaunchKernelGGL((finish_kernel<T, 16>), dim3(blocks(n * 16)), dim3(256), 0, s, slab, splits, stride, lds, M, N, scal,
+                       live, reinterpret_cast<T*>(out), accumulate);
+  else
+    hipLaunchKernelGGL((finish_kernel<T, 1>), dim3(blocks(n)), dim3(256), 0, s, slab, splits, stride, lds, M, N, scal, live,
+                       reinterpret_cast<T*>(out), accumulate);
+  return hipGetLastError();
+}
+template <typename T>
 hipError_t pack(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s) {
   hipLaunchKernelGGL((pack_kernel<T>), dim3(blocks(r.nr * Dp)), dim3(256), 0, s, r, reinterpret_cast<T*>(dst), (int)Dp);
   return hipGetLastError();
@@ -880,9 +918,7 @@ hipError_t small_backward(const XentArgs& a, const XentPlan& p, const float* lse
       GMM_TRY(launch_xent_small(P, a.dtype, 1, s));
     }
     if (slab) {
-      hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(R * p.lds / 4)), dim3(256), 0, s, slab, p.split_x, R * p.lds, p.lds,
-                         R, a.D, (const float*)nullptr, coef, reinterpret_cast<T*>(dx), accumulate);
-      GMM_TRY(hipGetLastError());
+      GMM_TRY(finish<T>(slab, p.split_x, R * p.lds, p.lds, R, a.D, nullptr, coef, dx, accumulate, s));
     }
   }
   if (!dw && !db) return hipSuccess;
@@ -916,15 +952,13 @@ hipError_t small_backward(const XentArgs& a, const XentPlan& p, const float* lse
     P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
     GMM_TRY(launch_xent_small(P, a.dtype, 2, s));
     if (db) {  // the column sums were multiplied back already
-      hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((a.V + 63) / 64)), dim3(256), 0, s, P.dbp, p.split_w, a.V,
+      hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((a.V + 15) / 16)), dim3(256), 0, s, P.dbp, p.split_w, a.V,
                          (const float*)nullptr, db, accumulate || r0 > 0);
       GMM_TRY(hipGetLastError());
     }
   }
   if (slab && dw) {
-    hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(a.V * p.lds / 4)), dim3(256), 0, s, slab, p.split_w, a.V * p.lds,
-                       p.lds, a.V, a.D, (const float*)nullptr, (const float*)nullptr, reinterpret_cast<T*>(dw), accumulate);
-    GMM_TRY(hipGetLastError());
+    GMM_TRY(finish<T>(slab, p.split_w, a.V * p.lds, p.lds, a.V, a.D, nullptr, nullptr, dw, accumulate, s));
   }
   return hipSuccess;
 }
@@ -1001,7 +1035,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
       GMM_TRY((launch_gemm<T, GRAD>(P, big_tiles(nr, nv), s)));
       if (db) {
-        hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((nv + 63) / 64)), dim3(256), 0, s, P.dbp, P.tm, nv, scal, db + v0,
+        hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((nv + 15) / 16)), dim3(256), 0, s, P.dbp, P.tm, nv, scal, db + v0,
                            accumulate || r0 > 0);
         GMM_TRY(hipGetLastError());
       }
@@ -1029,9 +1063,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
         }
         GMM_TRY((launch_gemm<T, OUT>(Q, big_tiles(nr, a.D), s)));
         if (p.slab_x && v0 + nv >= a.V) {
-          hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(nr * p.lds / 4)), dim3(256), 0, s, Q.slab, Q.splits,
-                             Q.slab_stride, p.lds, nr, a.D, scal, coef + r0, reinterpret_cast<T*>(Q.out), accumulate);
-          GMM_TRY(hipGetLastError());
+          GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nr, a.D, scal, coef + r0, Q.out, accumulate, s));
         }
       }
       if (dw) {  // dW of the piece += G^T X of the chunk
@@ -1058,10 +1090,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
         }
         GMM_TRY((launch_gemm<T, OUT>(Q, big_tiles(nv, a.D), s)));
         if (p.slab_w && r0 + nr >= R) {
-          hipLaunchKernelGGL((finish_kernel<T>), dim3(blocks(nv * p.lds / 4)), dim3(256), 0, s, Q.slab, Q.splits,
-                             Q.slab_stride, p.lds, nv, a.D, scal, (const float*)nullptr, reinterpret_cast<T*>(Q.out),
-                             accumulate);
-          GMM_TRY(hipGetLastError());
+          GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nv, a.D, scal, nullptr, Q.out, accumulate, s));
         }
       }
     }
