@@ -37,10 +37,11 @@ covariance parameters are float32 and are updated in place by the M-step.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 from . import _abi
-from ._abi import (COV_CODES, GmmError, GmmData, GmmHead, GmmOptions, GmmParams, GmmStats, GmmTensor, OP_ESTEP,
-                   OP_FIT, OP_TOPM)
+from ._abi import (COV_CODES, GmmError, GmmData, GmmHead, GmmOptions, GmmParams, GmmStats, OP_ESTEP, OP_FIT,
+                   OP_TOPM)
 
 __all__ = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step",
            "gmm_predict_proba_topm", "gmm_ivf_workspace_bytes", "gmm_ivf_lists", "gmm_kmeans_workspace_bytes",
@@ -378,18 +379,18 @@ class _on:
 
     def __init__(self, stream, *tensors):
         torch = _torch()
-        dev = tensors[0].device
+        index = tensors[0].get_device()  # -1: not on a GPU
         for t in tensors:
-            if t is not None and (t.device != dev or not t.is_cuda):
-                raise ValueError(f"every tensor must be on one GPU (got {t.device} and {dev})")
+            if t is not None and (index < 0 or t.get_device() != index):
+                raise ValueError(f"every tensor must be on one GPU (got {t.device} and {tensors[0].device})")
         # a guard costs microseconds: none where the call changes nothing
-        self.guards = [torch.cuda.device(dev)] if torch.cuda.current_device() != dev.index else []
+        self.guards = [torch.cuda.device(index)] if torch.cuda.current_device() != index else []
         if stream is not None:
             self.guards.append(torch.cuda.stream(stream))
             for t in tensors:  # memory freed by its owner while this stream still reads it
                 if t is not None:
                     t.record_stream(stream)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(index)
 
     def __enter__(self):
         for c in self.guards:
@@ -602,20 +603,23 @@ def gmm_clip_grad_norm(grads, max_norm, out=None, norm=None, ws=None, stream=Non
         raise ValueError("need one gradient or more")
     if len(outs) != len(grads):
         raise ValueError("out must hold one tensor per gradient")
-    desc = (GmmTensor * len(grads))()
+    codes = {torch.float32: _abi.DT_F32, torch.bfloat16: _abi.DT_BF16, torch.float16: _abi.DT_F16}
+    desc = array("q")  # a gmm_tensor is four 8-byte words: src, dst, n, dtype
     for i, (g, o) in enumerate(zip(grads, outs)):
-        if g.dtype not in (torch.float32, torch.bfloat16, torch.float16) or not g.is_contiguous():
+        code = codes.get(g.dtype)
+        if code is None or not g.is_contiguous():
             raise ValueError(f"gradient {i} must be a contiguous float32, bfloat16 or float16 tensor")
         if o is not g:
-            _expect(f"out[{i}]", o, g.dtype, g.shape)
-        desc[i] = GmmTensor(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
-    with _on(stream, *grads, *outs, norm, ws) as s:
+            if o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
+                _expect(f"out[{i}]", o, g.dtype, g.shape)
+        desc.extend((g.data_ptr(), o.data_ptr(), g.numel(), code))
+    with _on(stream, *grads, *(() if outs is grads else outs), norm, ws) as s:
         norm = torch.empty(1, dtype=torch.float32, device=grads[0].device) if norm is None else norm
         _expect("norm", norm, torch.float32, (1,))
         if ws is None:
             n = int(_abi.lib().gmm_clip_grad_norm_workspace_bytes(len(grads)))
             ws = torch.empty(n, dtype=torch.uint8, device=grads[0].device)
-        _abi.check(_abi.lib().gmm_clip_grad_norm(desc, len(grads), float(max_norm), _ptr(norm), _ptr(ws),
+        _abi.check(_abi.lib().gmm_clip_grad_norm(desc.buffer_info()[0], len(grads), float(max_norm), _ptr(norm), _ptr(ws),
                                                  ws.numel() * ws.element_size(), s))
     return norm
 

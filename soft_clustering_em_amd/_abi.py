@@ -132,7 +132,7 @@ def lib() -> ctypes.CDLL:
         L.gmm_codebook_lookup_grad.argtypes = [D, ctypes.c_int64, ctypes.c_int32, P, P, ctypes.c_float, D, P, P,
                                                ctypes.c_int32, P, ctypes.c_size_t, P]
         L.gmm_clip_grad_norm_workspace_bytes.argtypes = [ctypes.c_int32]
-        L.gmm_clip_grad_norm.argtypes = [ctypes.POINTER(GmmTensor), ctypes.c_int32, ctypes.c_double, P, P,
+        L.gmm_clip_grad_norm.argtypes = [P, ctypes.c_int32, ctypes.c_double, P, P,
                                          ctypes.c_size_t, P]
         for f in (L.gmm_softmax_xent_workspace_bytes, L.gmm_softmax_xent_grad_workspace_bytes,
                   L.gmm_codebook_lookup_grad_workspace_bytes, L.gmm_clip_grad_norm_workspace_bytes):

@@ -317,16 +317,19 @@ struct LookupArgs {
   int dtype, m, accumulate;
   int64_t B, N, K, D;
   void* out;               // (B, N, D)
+  bool stream;             // out is aligned: its stores pass by the caches
   void* dtable;            // (B, K, D) or null
   float* dweights;         // (B, N, m) or null
 };
-constexpr int kSortBlock = 4096;  // entries per workgroup of the sort
+constexpr int kSortSmall = 4, kSortLarge = 32;  // entries per thread of the sort, 256 threads a workgroup
 struct SortPass {
   int64_t S, nblk;
   uint32_t none;           // key of the entries that take no part: past every code
   int shift, bits, bins;
   const uint32_t *kin, *sin;  // keys and entries; null: the first pass reads the codes
   uint32_t *kout, *sout, *hist, *base;
+  char* zero;              // share of dtable that is cleared beside this kernel
+  int64_t zbytes;
 };
 struct SumArgs {
   int64_t S, C, chunks, Dp;
@@ -337,7 +340,7 @@ struct SumArgs {
 struct LookupPlan {
   int64_t S, nblk, C, chunks, Dp;
   uint32_t none;
-  int passes, bits;
+  int passes, bits, per;   // entries per thread of the sort
   size_t off_key[2], off_src[2], off_hist, off_base, off_part, bytes;
 };
 LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, bool want_table);

@@ -50,12 +50,14 @@ struct Vec {
       for (int e = 0; e < E; ++e) v[e] = e < n ? (float)p[e] : 0.f;
     }
   }
-  __device__ void store(T* p, int n) const {
+  // rows that nobody reads back soon pass by the caches where they are aligned
+  __device__ void store(T* p, int n, bool stream = false) const {
     if (n >= E) {
       T t[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) t[e] = (T)v[e];
-      __builtin_memcpy(p, t, 16);
+      if (stream) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, t), reinterpret_cast<u32x4*>(p));
+      else __builtin_memcpy(p, t, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -104,7 +106,7 @@ __device__ inline void lookup_row(const LookupArgs& A, int64_t row, int64_t d, i
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) acc.v[e] *= A.scale;
-  acc.store(reinterpret_cast<T*>(A.out) + row * A.D + d, n);
+  acc.store(reinterpret_cast<T*>(A.out) + row * A.D + d, n, A.stream);
 }
 
 template <typename T>
@@ -130,21 +132,38 @@ __global__ void __launch_bounds__(256) dweights_kernel(LookupArgs A, int lg) {
     const int32_t* ix = A.idx + row * A.m;
     float* out = A.dweights + row * A.m;
     bool live = true;
-    for (int j = 0; j < A.m; ++j) {
-      const int k = ix[j];
-      live = live && k >= 0 && k < A.K;
-      float s = 0.f;
-      if (live)
-        for (int64_t d = (int64_t)lane * E; d < A.D; d += (int64_t)E << lg) {
-          const int n = (int)min((int64_t)E, A.D - d);
-          Vec<T> a, r;
-          a.load(g + d, n);
-          r.load(t + k * A.ld + d, n);
-  #pragma unroll
-          for (int e = 0; e < E; ++e) s = fmaf(a.v[e], r.v[e], s);
-        }
-      for (int o = 1; o < 1 << lg; o <<= 1) s += __shfl_xor(s, o);
-      if (lane == 0) out[j] = live ? A.scale * s : 0.f;
+    constexpr int U = 4;  // codes at a time: their loads and their sums overlap
+    for (int j0 = 0; j0 < A.m; j0 += U) {
+      int k[U];
+      float s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) k[u] = ix[min(j0 + u, A.m - 1)];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        live = live && j0 + u < A.m && k[u] >= 0 && k[u] < A.K;
+        k[u] = live ? k[u] : -1;
+        s[u] = 0.f;
+      }
+      for (int64_t d = (int64_t)lane * E; d < A.D; d += (int64_t)E << lg) {
+        const int n = (int)min((int64_t)E, A.D - d);
+        Vec<T> a, r[U];
+        a.load(g + d, n);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k[u] >= 0) r[u].load(t + k[u] * A.ld + d, n);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k[u] >= 0)
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[u] = fmaf(a.v[e], r[u].v[e], s[u]);
+      }
+      for (int o = 1; o < 1 << lg; o <<= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] += __shfl_xor(s[u], o);
+      if (lane == 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j0 + u < A.m) out[j0 + u] = k[u] >= 0 ? A.scale * s[u] : 0.f;
     }
   }
 }
@@ -163,79 +182,114 @@ __device__ inline uint32_t key_of(const LookupArgs& A, int64_t e, uint32_t none)
   return (uint32_t)((A.B == 1 ? 0 : row / A.N) * A.K + k);
 }
 
-// digit counts of a block of kSortBlock entries
+// any bytes <- 0 (a kernel: memory operations in a captured graph are avoided)
+__global__ void __launch_bounds__(256) zero_kernel(char* p, int64_t bytes) {
+  const int64_t n = bytes / 16;
+  const u32x4 z = {0u, 0u, 0u, 0u};
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256)
+    __builtin_memcpy(p + t * 16, &z, 16);
+  if (blockIdx.x == 0 && threadIdx.x < bytes % 16) p[n * 16 + threadIdx.x] = 0;
+}
+
+// The sort's kernels wait for latencies on a few workgroups; the workgroups
+// past theirs clear a share of dT meanwhile.
+__device__ inline bool cleared(const SortPass& P, unsigned own) {
+  if (blockIdx.x < own) return false;
+  const u32x4 z = {0u, 0u, 0u, 0u};
+  const int64_t n = P.zbytes / 16, step = (int64_t)(gridDim.x - own) * 256;
+  for (int64_t t = (int64_t)(blockIdx.x - own) * 256 + threadIdx.x; t < n; t += step) __builtin_memcpy(P.zero + t * 16, &z, 16);
+  return true;
+}
+
+// digit counts of a block of 256 PER entries
+template <int PER>
 __global__ void __launch_bounds__(256) sort_count_kernel(LookupArgs A, SortPass P) {
+  if (cleared(P, (unsigned)P.nblk)) return;
   extern __shared__ uint32_t cnt[];
+  const int64_t e0 = (int64_t)blockIdx.x * (256 * PER) + threadIdx.x;
+  uint32_t key[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int64_t e = e0 + u * 256;
+    key[u] = e < P.S ? (P.kin ? P.kin[e] : key_of(A, e, P.none)) : 0;
+  }
   for (int d = threadIdx.x; d < P.bins; d += 256) cnt[d] = 0;
   __syncthreads();
-  const int64_t e0 = (int64_t)blockIdx.x * kSortBlock;
-  for (int u = 0; u < kSortBlock / 256; ++u) {
-    const int64_t e = e0 + u * 256 + threadIdx.x;
-    if (e >= P.S) break;
-    const uint32_t key = P.kin ? P.kin[e] : key_of(A, e, P.none);
-    atomicAdd(&cnt[(key >> P.shift) & (P.bins - 1)], 1u);  // in LDS; a count has no order
-  }
+#pragma unroll
+  for (int u = 0; u < PER; ++u)
+    if (e0 + u * 256 < P.S) atomicAdd(&cnt[(key[u] >> P.shift) & (P.bins - 1)], 1u);  // in LDS; a count has no order
   __syncthreads();
   for (int d = threadIdx.x; d < P.bins; d += 256) P.hist[(int64_t)blockIdx.x * P.bins + d] = cnt[d];
 }
 
-// counts [block][digit] -> first position of the digit's entries of the block
-__global__ void __launch_bounds__(1024) sort_scan_kernel(SortPass P) {
-  __shared__ uint32_t tot[1024];
-  const int d = threadIdx.x;
+// counts [block][digit] -> the digit's entries in earlier blocks, and their
+// total; 16 digits a workgroup, 16 threads a digit
+__global__ void __launch_bounds__(256) sort_scan_kernel(SortPass P) {
+  if (cleared(P, (P.bins + 15) / 16)) return;
+  __shared__ uint32_t tot[16][16];
+  const int c = threadIdx.x & 15, sl = threadIdx.x >> 4, d = blockIdx.x * 16 + c;
+  const int64_t per = (P.nblk + 15) / 16, b0 = min(P.nblk, sl * per), b1 = min(P.nblk, b0 + per);
   uint32_t s = 0;
-  if (d < P.bins) {
-    constexpr int U = 8;
-    int64_t b = 0;
-    for (; b + U <= P.nblk; b += U) {
-      uint32_t v[U];
+  if (d < P.bins)
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; ++b) s += P.hist[b * P.bins + d];
+  tot[sl][c] = s;
+  __syncthreads();
+  s = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = P.hist[(b + u) * P.bins + d];
+  for (int k = 0; k < 16; ++k) s += k < sl ? tot[k][c] : 0;
+  if (d >= P.bins) return;
+  constexpr int U = 8;
+  for (int64_t b = b0; b < b1; b += U) {
+    uint32_t v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) v[u] = b + u < b1 ? P.hist[(b + u) * P.bins + d] : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u < b1) {
         P.hist[(b + u) * P.bins + d] = s;
         s += v[u];
       }
-    }
-    for (; b < P.nblk; ++b) {
-      const uint32_t v = P.hist[b * P.bins + d];
-      P.hist[b * P.bins + d] = s;
-      s += v;
-    }
   }
-  tot[d] = s;
-  __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {  // inclusive scan over the digits
-    const uint32_t v = d >= o ? tot[d - o] : 0;
-    __syncthreads();
-    tot[d] += v;
-    __syncthreads();
-  }
-  if (d < P.bins) P.base[d] = tot[d] - s;
+  if (sl == 15) P.base[d] = s;
 }
 
 // places a block's entries; equal digits keep their order
+template <int PER>
 __global__ void __launch_bounds__(256) sort_scatter_kernel(LookupArgs A, SortPass P) {
+  if (cleared(P, (unsigned)P.nblk)) return;
   extern __shared__ uint32_t next[];  // [4 waves][bins]: the wave's next position of a digit
+  __shared__ uint32_t part[256];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  constexpr int PER = kSortBlock / 4;  // consecutive entries of a wave
-  const int64_t e0 = (int64_t)blockIdx.x * kSortBlock + wv * PER;
+  const int64_t e0 = ((int64_t)blockIdx.x * 4 + wv) * (64 * PER);  // consecutive entries of a wave
+  uint32_t key[PER], src[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int64_t e = e0 + u * 64 + lane;
+    key[u] = e < P.S ? (P.kin ? P.kin[e] : key_of(A, e, P.none)) : 0;
+    src[u] = e < P.S ? (P.sin ? P.sin[e] : (uint32_t)e) : 0;
+  }
+  // the digits' totals -> where each digit's entries begin
+  uint32_t sum = 0;
+  const int dper = (P.bins + 255) / 256, d0 = threadIdx.x * dper;
+  for (int d = d0; d < min(P.bins, d0 + dper); ++d) sum += P.base[d];
+  part[threadIdx.x] = sum;
   for (int d = threadIdx.x; d < 4 * P.bins; d += 256) next[d] = 0;
   __syncthreads();
-  uint32_t key[PER / 64], src[PER / 64];
-#pragma unroll
-  for (int u = 0; u < PER / 64; ++u) {
-    const int64_t e = e0 + u * 64 + lane;
-    key[u] = src[u] = 0;
-    if (e < P.S) {
-      key[u] = P.kin ? P.kin[e] : key_of(A, e, P.none);
-      src[u] = P.sin ? P.sin[e] : (uint32_t)e;
-      atomicAdd(&next[wv * P.bins + ((key[u] >> P.shift) & (P.bins - 1))], 1u);
-    }
+  for (int o = 1; o < 256; o <<= 1) {
+    const uint32_t v = (int)threadIdx.x >= o ? part[threadIdx.x - o] : 0;
+    __syncthreads();
+    part[threadIdx.x] += v;
+    __syncthreads();
   }
+#pragma unroll
+  for (int u = 0; u < PER; ++u)
+    if (e0 + u * 64 + lane < P.S) atomicAdd(&next[wv * P.bins + ((key[u] >> P.shift) & (P.bins - 1))], 1u);
   __syncthreads();
-  for (int d = threadIdx.x; d < P.bins; d += 256) {
-    uint32_t at = P.base[d] + P.hist[(int64_t)blockIdx.x * P.bins + d];
+  uint32_t first = part[threadIdx.x] - sum;
+  for (int d = d0; d < min(P.bins, d0 + dper); ++d) {
+    uint32_t at = first + P.hist[(int64_t)blockIdx.x * P.bins + d];
+    first += P.base[d];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const uint32_t c = next[w * P.bins + d];
@@ -247,7 +301,7 @@ __global__ void __launch_bounds__(256) sort_scatter_kernel(LookupArgs A, SortPas
   volatile uint32_t* mine = next + wv * P.bins;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
 #pragma unroll
-  for (int u = 0; u < PER / 64; ++u) {
+  for (int u = 0; u < PER; ++u) {
     const bool in = e0 + u * 64 + lane < P.S;
     const uint32_t d = (key[u] >> P.shift) & (P.bins - 1);
     uint64_t same = __builtin_amdgcn_ballot_w64(in);
@@ -266,15 +320,6 @@ __global__ void __launch_bounds__(256) sort_scatter_kernel(LookupArgs A, SortPas
   }
 }
 
-// any bytes <- 0 (a kernel: memory operations in a captured graph are avoided)
-__global__ void __launch_bounds__(256) zero_kernel(char* p, int64_t bytes) {
-  const int64_t n = bytes / 16;
-  const u32x4 z = {0u, 0u, 0u, 0u};
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256)
-    __builtin_memcpy(p + t * 16, &z, 16);
-  if (blockIdx.x == 0 && threadIdx.x < bytes % 16) p[n * 16 + threadIdx.x] = 0;
-}
-
 template <typename T>
 __device__ inline void put(const LookupArgs& A, uint32_t key, int64_t d, int n, Vec<T>& acc) {
   T* p = reinterpret_cast<T*>(A.dtable) + (int64_t)key * A.D + d;
@@ -290,10 +335,11 @@ __device__ inline void put(const LookupArgs& A, uint32_t key, int64_t d, int n, 
 }
 
 // Sums the entries of a chunk, in sorted order; a group of 2^lg lanes holds
-// 16 bytes of columns a lane.
+// 16 bytes of columns a lane.  The rows of the next U entries are on their way
+// while the U before them are added.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_kernel(LookupArgs A, SumArgs P, RowSplit S) {
-  constexpr int E = Vec<T>::E, U = 8;
+  constexpr int E = Vec<T>::E, U = 4;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> S.lg;
   const int64_t d = ((int64_t)blockIdx.y << S.lg | (threadIdx.x & ((1 << S.lg) - 1))) * E;
   if (c >= P.chunks || d >= A.D) return;
@@ -304,44 +350,62 @@ __global__ void __launch_bounds__(256) sum_kernel(LookupArgs A, SumArgs P, RowSp
 #pragma unroll
   for (int e = 0; e < E; ++e) acc.v[e] = 0.f;
   uint32_t cur = P.key[s0];
+  if (cur >= P.none) return;  // entries behind the last code
   bool first = true;  // the run reaches the chunk's start
   auto partial = [&](int slot) {
     float* p = P.part + ((c * 2 + slot) * P.Dp + d);
 #pragma unroll
     for (int e = 0; e < E; ++e) p[e] = acc.v[e];  // Dp: D rounded up to whole chunks
   };
-  for (int64_t s = s0; s < s1; s += U) {
+  struct Batch {
     uint32_t k[U];
-    Vec<T> r[U];
     float w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = s + u < s1 ? P.key[s + u] : P.none;
-    if (k[0] >= P.none) break;  // the entries behind the last code
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k[u] < P.none) {
-        const uint32_t e = P.src[s + u];
-        const int64_t row = A.m == 1 ? e : e / (uint32_t)A.m;
-        const int64_t b = A.B == 1 ? 0 : row / A.N;
-        w[u] = A.weights ? A.weights[e] : 1.f;
-        r[u].load(reinterpret_cast<const T*>(A.dout) + b * A.stride_g + (row - b * A.N) * A.ld_g + d, n);
-      }
+    Vec<T> r[U];
+  };
+  const bool whole = n == E;
+  auto load = [&](int64_t s, Batch& t) {
+    uint32_t e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (k[u] >= P.none) continue;
-      if (k[u] != cur) {
+      const bool in = s + u < s1;
+      t.k[u] = in ? P.key[s + u] : P.none;
+      e[u] = in ? P.src[s + u] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t.k[u] >= P.none) e[u] = 0;  // entry 0 always exists
+      const int64_t row = A.m == 1 ? e[u] : e[u] / (uint32_t)A.m;
+      const int64_t b = A.B == 1 ? 0 : row / A.N;
+      t.w[u] = A.weights ? A.weights[e[u]] : 1.f;
+      const T* p = reinterpret_cast<const T*>(A.dout) + b * A.stride_g + (row - b * A.N) * A.ld_g + d;
+      if (whole) t.r[u].load(p, E);
+      else t.r[u].load(p, n);
+    }
+  };
+  auto add = [&](const Batch& t) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t.k[u] >= P.none) continue;
+      if (t.k[u] != cur) {
         if (first && before == cur) partial(0);
         else put<T>(A, cur, d, n, acc);
         first = false;
-        cur = k[u];
+        cur = t.k[u];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc.v[e] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc.v[e] = fmaf(w[u], r[u].v[e], acc.v[e]);
+      for (int e = 0; e < E; ++e) acc.v[e] = fmaf(t.w[u], t.r[u].v[e], acc.v[e]);
     }
+  };
+  Batch x, y;
+  load(s0, x);
+  for (int64_t s = s0; s < s1; s += 2 * U) {
+    load(s + U, y);
+    add(x);
+    load(s + 2 * U, x);
+    add(y);
   }
-  if (cur >= P.none) return;
   if (first && before == cur) partial(0);
   else if (after == cur) partial(1);
   else put<T>(A, cur, d, n, acc);
@@ -367,35 +431,40 @@ __global__ void __launch_bounds__(256) join_runs_kernel(LookupArgs A, SumArgs P)
     else hi = mid - 1;
   }
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int64_t d = ((int64_t)blockIdx.y * 32 + lane) * 4;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (d < A.D) {
-    if (g == 0) a = *reinterpret_cast<const float4*>(P.part + (c * 2 + 1) * P.Dp + d);
-    for (int64_t q = c + 1 + g; q <= lo; q += 8) {
-      const float4 v = *reinterpret_cast<const float4*>(P.part + q * 2 * P.Dp + d);
+  for (int64_t d0 = (int64_t)blockIdx.y * 128; d0 < A.D; d0 += (int64_t)gridDim.y * 128) {
+    const int64_t d = d0 + 4 * lane;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d < A.D) {
+      if (g == 0) a = *reinterpret_cast<const float4*>(P.part + (c * 2 + 1) * P.Dp + d);
+#pragma unroll 4
+      for (int64_t q = c + 1 + g; q <= lo; q += 8) {
+        const float4 v = *reinterpret_cast<const float4*>(P.part + q * 2 * P.Dp + d);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+    }
+    __syncthreads();
+    red[g][lane] = a;
+    __syncthreads();
+    if (g != 0 || d >= A.D) continue;
+    for (int q = 1; q < 8; ++q) {
+      const float4 v = red[q][lane];
       a.x += v.x;
       a.y += v.y;
       a.z += v.z;
       a.w += v.w;
     }
-  }
-  red[g][lane] = a;
-  __syncthreads();
-  if (g != 0 || d >= A.D) return;
-  for (int q = 1; q < 8; ++q) {
-    const float4 v = red[q][lane];
-    a.x += v.x;
-    a.y += v.y;
-    a.z += v.z;
-    a.w += v.w;
-  }
-  const float v[4] = {a.x, a.y, a.z, a.w};
-  T* p = reinterpret_cast<T*>(A.dtable) + (int64_t)key * A.D + d;
+    const float v[4] = {a.x, a.y, a.z, a.w};
+    T* p = reinterpret_cast<T*>(A.dtable) + (int64_t)key * A.D + d;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (d + e < A.D) p[e] = (T)(A.scale * v[e] + (A.accumulate ? (float)p[e] : 0.f));
+    for (int e = 0; e < 4; ++e)
+      if (d + e < A.D) p[e] = (T)(A.scale * v[e] + (A.accumulate ? (float)p[e] : 0.f));
+  }
 }
 
+constexpr int64_t kLookupGrid = 8192;
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups along x: a launch has fewer than 2^32 threads an axis
 
 RowSplit row_split(int64_t D, int E) {
@@ -413,10 +482,11 @@ RowSplit row_split(int64_t D, int E) {
   } while (0)
 
 template <typename T>
-hipError_t lookup(const LookupArgs& a, hipStream_t s) {
+hipError_t lookup(LookupArgs a, hipStream_t s) {
+  a.stream = ((uintptr_t)a.out | (uintptr_t)(a.D * (int64_t)sizeof(T))) % 16 == 0;
   const RowSplit sp = row_split(a.D, Vec<T>::E);
   const int64_t rows = a.B * a.N, per = 256 >> sp.lg;
-  const dim3 grid((unsigned)std::min<int64_t>((rows + per - 1) / per, kMaxGrid), (unsigned)sp.slabs);
+  const dim3 grid((unsigned)std::min<int64_t>((rows + per - 1) / per, kLookupGrid), (unsigned)sp.slabs);
   hipLaunchKernelGGL((lookup_kernel<T>), grid, dim3(256), 0, s, a, sp);
   return hipGetLastError();
 }
@@ -433,8 +503,8 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
     GMM_TRY(hipGetLastError());
   }
   if (!a.dtable) return hipSuccess;
-  if (!a.accumulate) GMM_TRY(launch_zero(a.dtable, a.B * a.K * a.D * (int64_t)sizeof(T), s));
-  if (rows == 0) return hipSuccess;
+  const int64_t bytes = a.accumulate ? 0 : a.B * a.K * a.D * (int64_t)sizeof(T);
+  if (rows == 0) return launch_zero(a.dtable, bytes, s);
   uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + p.off_key[0]), reinterpret_cast<uint32_t*>(ws + p.off_key[1])};
   uint32_t* srcs[2] = {reinterpret_cast<uint32_t*>(ws + p.off_src[0]), reinterpret_cast<uint32_t*>(ws + p.off_src[1])};
   SortPass P{};
@@ -445,19 +515,32 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
   P.base = reinterpret_cast<uint32_t*>(ws + p.off_base);
   P.bits = p.bits;
   P.bins = 1 << p.bits;
+  // dT is cleared in equal shares beside the sort's 3 kernels a pass, the last
+  // odd bytes on their own
+  const int64_t share = bytes / (3 * p.passes) / 16 * 16;
+  P.zbytes = share;
+  P.zero = static_cast<char*>(a.dtable);
+  const unsigned zgrid = (unsigned)std::min<int64_t>(2048, (share / 16 + 255) / 256);
   for (int q = 0; q < p.passes; ++q) {
     P.shift = q * p.bits;
     P.kin = q ? keys[(q + 1) & 1] : nullptr;
     P.sin = q ? srcs[(q + 1) & 1] : nullptr;
     P.kout = keys[q & 1];
     P.sout = srcs[q & 1];
-    hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)p.nblk), dim3(256), P.bins * 4, s, a, P);
+    const dim3 grid((unsigned)p.nblk + zgrid), scan((P.bins + 15) / 16 + zgrid);
+    if (p.per == kSortSmall) hipLaunchKernelGGL(sort_count_kernel<kSortSmall>, grid, dim3(256), P.bins * 4, s, a, P);
+    else hipLaunchKernelGGL(sort_count_kernel<kSortLarge>, grid, dim3(256), P.bins * 4, s, a, P);
     GMM_TRY(hipGetLastError());
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(1024), 0, s, P);
+    P.zero += share;
+    hipLaunchKernelGGL(sort_scan_kernel, scan, dim3(256), 0, s, P);
     GMM_TRY(hipGetLastError());
-    hipLaunchKernelGGL(sort_scatter_kernel, dim3((unsigned)p.nblk), dim3(256), P.bins * 16, s, a, P);
+    P.zero += share;
+    if (p.per == kSortSmall) hipLaunchKernelGGL(sort_scatter_kernel<kSortSmall>, grid, dim3(256), P.bins * 16, s, a, P);
+    else hipLaunchKernelGGL(sort_scatter_kernel<kSortLarge>, grid, dim3(256), P.bins * 16, s, a, P);
     GMM_TRY(hipGetLastError());
+    P.zero += share;
   }
+  GMM_TRY(launch_zero(P.zero, bytes - 3 * p.passes * share, s));
   SumArgs Q{};
   Q.S = p.S;
   Q.C = p.C;
@@ -473,8 +556,8 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
                      sp);
   GMM_TRY(hipGetLastError());
   if (p.chunks > 1) {
-    hipLaunchKernelGGL((join_runs_kernel<T>), dim3((unsigned)(p.chunks - 1), (unsigned)((a.D + 127) / 128)), dim3(256), 0, s,
-                       a, Q);
+    hipLaunchKernelGGL((join_runs_kernel<T>), dim3((unsigned)(p.chunks - 1), (unsigned)std::min<int64_t>(4, (a.D + 127) / 128)), dim3(256),
+                       0, s, a, Q);
     GMM_TRY(hipGetLastError());
   }
   return hipSuccess;
@@ -500,7 +583,8 @@ LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, bo
   while (((int64_t)1 << total) <= B * K) ++total;  // bits of the key B K
   p.passes = (total + 9) / 10;
   p.bits = (total + p.passes - 1) / p.passes;
-  p.nblk = (p.S + kSortBlock - 1) / kSortBlock;
+  p.per = p.S <= 1 << 20 ? kSortSmall : kSortLarge;
+  p.nblk = (p.S + 256 * p.per - 1) / (256 * p.per);
   // entries of a chunk: 32, more where that makes over 2^13 chunks
   p.C = 32;
   while (p.C < 1024 && p.S / p.C > 1 << 13) p.C *= 2;

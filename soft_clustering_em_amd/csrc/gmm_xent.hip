@@ -541,14 +541,17 @@ __global__ void __launch_bounds__(64) scal_kernel(const float* bmax, int n, floa
   }
 }
 
-// rows of any layout -> [nr][Dp], zeros past D
+// rows of any layout -> [nr][Dp], zeros past D; a thread per 16 bytes
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(RowsArgs R, T* dst, int Dp) {
-  const int64_t n = R.nr * Dp;
+  constexpr int E = 16 / (int)sizeof(T);
+  const int CR = Dp / E;  // Dp: whole chunks
+  const int64_t n = R.nr * CR;
   for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
-    const int64_t r = t / Dp;
-    const int d = (int)(t % Dp);
-    dst[t] = d < R.D ? reinterpret_cast<const T*>(R.x)[row_offset(R, R.r0 + r) + d] : T(0);
+    const int64_t r = t / CR;
+    const int c = (int)(t - r * CR) * 16;
+    const u32x4 v = chunk_at<T>(R.x + row_offset(R, R.r0 + r) * (int64_t)sizeof(T), c, R.D * (int)sizeof(T));
+    *reinterpret_cast<u32x4*>(reinterpret_cast<char*>(dst) + t * 16) = v;
   }
 }
 
@@ -792,7 +795,8 @@ hipError_t finish(const float* slab, int splits, int64_t stride, int64_t lds, in
 }
 template <typename T>
 hipError_t pack(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s) {
-  hipLaunchKernelGGL((pack_kernel<T>), dim3(blocks(r.nr * Dp)), dim3(256), 0, s, r, reinterpret_cast<T*>(dst), (int)Dp);
+  hipLaunchKernelGGL((pack_kernel<T>), dim3(blocks(r.nr * Dp * (int64_t)sizeof(T) / 16, 1 << 16)), dim3(256), 0, s, r,
+                     reinterpret_cast<T*>(dst), (int)Dp);
   return hipGetLastError();
 }
 template <typename T>
