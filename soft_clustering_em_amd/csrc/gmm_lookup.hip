@@ -198,6 +198,7 @@ __device__ inline bool cleared(const SortPass& P, unsigned own) {
   const u32x4 z = {0u, 0u, 0u, 0u};
   const int64_t n = P.zbytes / 16, step = (int64_t)(gridDim.x - own) * 256;
   for (int64_t t = (int64_t)(blockIdx.x - own) * 256 + threadIdx.x; t < n; t += step) __builtin_memcpy(P.zero + t * 16, &z, 16);
+  if (blockIdx.x == own && threadIdx.x < P.zbytes % 16) P.zero[n * 16 + threadIdx.x] = 0;
   return true;
 }
 
@@ -515,12 +516,11 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
   P.base = reinterpret_cast<uint32_t*>(ws + p.off_base);
   P.bits = p.bits;
   P.bins = 1 << p.bits;
-  // dT is cleared in equal shares beside the sort's 3 kernels a pass, the last
-  // odd bytes on their own
+  // dT is cleared in equal shares beside the sort's 3 kernels a pass
   const int64_t share = bytes / (3 * p.passes) / 16 * 16;
   P.zbytes = share;
   P.zero = static_cast<char*>(a.dtable);
-  const unsigned zgrid = (unsigned)std::min<int64_t>(2048, (share / 16 + 255) / 256);
+  const unsigned zgrid = bytes ? (unsigned)std::min<int64_t>(2048, share / 4096 + 1) : 0;
   for (int q = 0; q < p.passes; ++q) {
     P.shift = q * p.bits;
     P.kin = q ? keys[(q + 1) & 1] : nullptr;
@@ -535,12 +535,12 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
     hipLaunchKernelGGL(sort_scan_kernel, scan, dim3(256), 0, s, P);
     GMM_TRY(hipGetLastError());
     P.zero += share;
+    if (q == p.passes - 1) P.zbytes = bytes - (3 * p.passes - 1) * share;
     if (p.per == kSortSmall) hipLaunchKernelGGL(sort_scatter_kernel<kSortSmall>, grid, dim3(256), P.bins * 16, s, a, P);
     else hipLaunchKernelGGL(sort_scatter_kernel<kSortLarge>, grid, dim3(256), P.bins * 16, s, a, P);
     GMM_TRY(hipGetLastError());
     P.zero += share;
   }
-  GMM_TRY(launch_zero(P.zero, bytes - 3 * p.passes * share, s));
   SumArgs Q{};
   Q.S = p.S;
   Q.C = p.C;
