@@ -494,12 +494,20 @@ __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t n
     }
   }
   red[sl][r] = make_float2(mx, s);
-  __syncthreads();
+  // halves of the slices, one into the other
+#pragma unroll
+  for (int h = SL / 2; h > 0; h /= 2) {
+    __syncthreads();
+    if (sl < h) {
+      const float2 t = red[sl + h][r];
+      const float top = fmaxf(mx, t.x), base = top == -INFINITY ? 0.f : top;
+      s = s * __builtin_amdgcn_exp2f((mx - base) * kLog2e) + t.y * __builtin_amdgcn_exp2f((t.x - base) * kLog2e);
+      mx = top;
+      red[sl][r] = make_float2(mx, s);
+    }
+  }
   if (sl != 0 || m >= M) return;
-  float top = -INFINITY, tot = 0.f;
-  for (int k = 0; k < SL; ++k) top = fmaxf(top, red[k][r].x);
-  const float base = top == -INFINITY ? 0.f : top;
-  for (int k = 0; k < SL; ++k) tot += red[k][r].y * __builtin_amdgcn_exp2f((red[k][r].x - base) * kLog2e);
+  const float top = mx, tot = s;
   const float z = top + logf(tot);
   const int32_t y = labels[m];
   lse[m] = z;

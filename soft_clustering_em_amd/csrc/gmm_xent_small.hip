@@ -61,6 +61,16 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   constexpr int kBytes = kTile * RBytes, JS = kBytes / 4096;  // 16-byte loads of a thread per tile
   constexpr int RPB = RBytes >= 256 ? 1 : 256 / RBytes, FM = (KC < 16 ? KC : 16) - 1;
   constexpr int NB = kTile / 16, ND = DP / 16;
+  // f(row), on the rows that share 256 bytes as one (g): a fragment read's 16
+  // lanes at a time are rows 0-3 and 12-15 of one chunk and rows 4-11 of the
+  // next, so the first eight's places have to be whole pairs; a transposing
+  // read takes pairs of chunks of 8 rows, so those have to be of 8 pairs
+  // (16-bit rows; float32 rows are read by element instead)
+  auto swizzle = [](int row) {
+    const int g = (row / RPB) & FM, H = (FM + 1) / 2;
+    if (ES == 4) return g;
+    return g < H ? 2 * g : 2 * ((g - H) ^ (H / 2)) + 1;
+  };
   constexpr float kTop = ES == 2 && !__is_same(T, __bf16) ? 32768.f : 1.f;  // DX: scale of p
   __shared__ __attribute__((aligned(1024))) char st0[kBytes];
   __shared__ __attribute__((aligned(1024))) char st1[kBytes];
@@ -114,10 +124,11 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
 
   // ---- streamed tiles.  Load j of a thread: row row0 + j RPJ of the tile, one
   // 16-byte chunk, the same of every row but for f's bit 3 where rows are 512 bytes
+  // (rows a multiple of 16 apart have the same f)
   constexpr int RPJ = 4096 / RBytes;
   const int kpad = (kbytes + 15) & ~15;  // the stream's rows hold zeros from D to whole chunks
   const int row0 = (wv * 1024 + lane * 16) / RBytes;
-  const int ch0 = ((wv * 1024 + lane * 16) % RBytes / 16) ^ ((row0 / RPB) & FM);
+  const int ch0 = ((wv * 1024 + lane * 16) % RBytes / 16) ^ swizzle(row0);
   const unsigned last = (unsigned)P.count - 1;
   float flag[JS];  // DW: the coefficients of the rows that are issued next
   auto flags = [&](int t) {
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   }
 
   // logits of streamed block jb (16 rows) against owner block i
-  const int fr = (lr / RPB) & FM;
+  const int fr = swizzle(lr);
   auto logits = [&](const char* st, const float* sp, int jb, f32x4* s) {
     if constexpr (PASS == DW) {
 #pragma unroll
@@ -201,16 +212,17 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
     }
   };
   // G of a block, in place
+  // (a block holds few labels: the lanes vote before they look for theirs)
   auto gradient = [&](const float* sp, int jb, int t, f32x4* s) {
     if constexpr (PASS == DX) {
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        const int y = oy[i] - t * kTile - 4 * lq - 16 * jb;  // never equal where there is no label
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, oa[i]));
-          s[i][e] = p - (y == e ? kTop : 0.f);
-        }
+        for (int e = 0; e < 4; ++e) s[i][e] = __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, oa[i]));
+        const int y = oy[i] - t * kTile - 16 * jb;  // outside 0 .. 15 where the block has not got the label
+        if (__builtin_amdgcn_ballot_w64((unsigned)y < 16u))
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] -= y == 4 * lq + e ? kTop : 0.f;
       }
     } else {
       const f32x4 nl = *reinterpret_cast<const f32x4*>(sp + 16 * jb + 4 * lq);
@@ -219,10 +231,10 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, nl[e]));
-          s[i][e] = c[e] * (p - (y[e] == oy[i] ? 1.f : 0.f));
-        }
+        for (int e = 0; e < 4; ++e) s[i][e] = c[e] * __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, nl[e]));
+        if (__builtin_amdgcn_ballot_w64(y[0] == oy[i] || y[1] == oy[i] || y[2] == oy[i] || y[3] == oy[i]))
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] -= y[e] == oy[i] ? c[e] : 0.f;
         mx[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
         asm volatile("" : "+v"(mx[i]));  // summed here: left alone, every G would stay in a register until the loop's end
       }
@@ -256,8 +268,9 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
         f32x4 s[2][RB];
         u32x2 g[RB][2];
 #pragma unroll
+        for (int u = 0; u < 2; ++u) logits(st, sp, 2 * h + u, s[u]);
+#pragma unroll
         for (int u = 0; u < 2; ++u) {
-          logits(st, sp, 2 * h + u, s[u]);
           gradient(sp, 2 * h + u, t, s[u]);
           if constexpr (ES == 2)
 #pragma unroll
@@ -265,11 +278,10 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
               const T v[4] = {(T)s[u][i][0], (T)s[u][i][1], (T)s[u][i][2], (T)s[u][i][3]};
               g[i][u] = __builtin_bit_cast(u32x2, v);
             }
-          __builtin_amdgcn_sched_barrier(0);  // one block's temporaries at a time
         }
         if constexpr (ES == 2) {
           // lane 16 a + b reads feature 16 d + b of streamed rows 4 a .. 4 a + 3 of either block
-          const int rr = lane >> 2, fx = (rr / RPB) & FM;
+          const int rr = lane >> 2, fx = swizzle(rr);
           const char* src = st + (32 * h + rr) * RBytes + 8 * (lane & 1);
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int row = 4 * lq + e, fx = (row / RPB) & FM;
+              const int row = 4 * lq + e, fx = swizzle(row);
               const char* src = st + (32 * h + 16 * u + row) * RBytes + 4 * (lr & 3);
 #pragma unroll
               for (int d = 0; d < ND; ++d) {
