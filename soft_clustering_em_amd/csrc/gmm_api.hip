@@ -1478,7 +1478,7 @@ gmm_status gmm_codebook_lookup(const gmm_data* table, int64_t N, int32_t m, cons
 
 size_t gmm_codebook_lookup_grad_workspace_bytes(const gmm_data* dout, int64_t K, int32_t m) {
   if (check_data(dout) != GMM_OK || lookup_check(dout->B, dout->N, m, K, dout->D) != GMM_OK) return 0;
-  return std::max(kAlign, lookup_plan(dout->B, dout->N, m, K, dout->D, true).bytes);
+  return std::max(kAlign, lookup_plan(dout->B, dout->N, m, K, dout->D, dout->dtype, true).bytes);
 }
 
 gmm_status gmm_codebook_lookup_grad(const gmm_data* dout, int64_t K, int32_t m, const int32_t* idx, const float* weights,
@@ -1509,7 +1509,7 @@ gmm_status gmm_codebook_lookup_grad(const gmm_data* dout, int64_t K, int32_t m, 
     if (overlap(dtable, nt, in[i], nin[i]) || overlap(dweights, nw, in[i], nin[i]))
       return fail(GMM_ERR_INVALID_ARG, "a gradient overlaps an input");
   if (overlap(dtable, nt, dweights, nw)) return fail(GMM_ERR_INVALID_ARG, "two gradients overlap");
-  const LookupPlan p = lookup_plan(dout->B, dout->N, m, K, dout->D, dtable != nullptr);
+  const LookupPlan p = lookup_plan(dout->B, dout->N, m, K, dout->D, dout->dtype, dtable != nullptr);
   if ((st = check_ws(ws, ws_bytes, std::max(kAlign, p.bytes))) != GMM_OK) return st;
   LookupArgs a{};
   if (dweights) {

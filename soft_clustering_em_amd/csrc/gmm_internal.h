@@ -321,6 +321,7 @@ struct LookupArgs {
   void* dtable;            // (B, K, D) or null
   float* dweights;         // (B, N, m) or null
 };
+constexpr int kRankEntries = 8192;           // entries that one kernel sorts at most
 constexpr int kSortSmall = 4, kSortLarge = 32;  // entries per thread of the sort, 256 threads a workgroup
 struct SortPass {
   int64_t S, nblk;
@@ -343,7 +344,7 @@ struct LookupPlan {
   int passes, bits, per;   // entries per thread of the sort
   size_t off_key[2], off_src[2], off_hist, off_base, off_part, bytes;
 };
-LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, bool want_table);
+LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, int dtype, bool want_table);
 hipError_t launch_lookup(const LookupArgs& a, hipStream_t s);
 hipError_t launch_lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipStream_t s);
 hipError_t launch_zero(void* p, int64_t bytes, hipStream_t s);

@@ -202,6 +202,31 @@ __device__ inline bool cleared(const SortPass& P, unsigned own) {
   return true;
 }
 
+// The whole sort of up to kRankEntries entries in one kernel: an entry's place
+// is the number of smaller keys and of equal ones before it, counted by 8 lanes
+// over every key in LDS.
+__global__ void __launch_bounds__(256) sort_rank_kernel(LookupArgs A, SortPass P) {
+  if (cleared(P, (unsigned)P.nblk)) return;
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kRankEntries];
+  const int S = (int)P.S, S4 = (S + 3) / 4;
+  for (int e = threadIdx.x; e < 4 * S4; e += 256) keys[e] = e < S ? key_of(A, e, P.none) : 0xffffffffu;
+  __syncthreads();
+  const int e = blockIdx.x * 32 + (threadIdx.x >> 3), p = threadIdx.x & 7;
+  const uint32_t mine = keys[min(e, S - 1)];
+  uint32_t place = 0;
+  for (int c = p; c < S4; c += 8) {
+    const u32x4 k = *reinterpret_cast<const u32x4*>(keys + 4 * c);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) place += k[u] < mine + (4 * c + u < e ? 1u : 0u);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) place += __shfl_xor(place, o);
+  if (p == 0 && e < S) {
+    P.kout[place] = mine;
+    P.sout[place] = (uint32_t)e;
+  }
+}
+
 // digit counts of a block of 256 PER entries
 template <int PER>
 __global__ void __launch_bounds__(256) sort_count_kernel(LookupArgs A, SortPass P) {
@@ -517,10 +542,16 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
   P.bits = p.bits;
   P.bins = 1 << p.bits;
   // dT is cleared in equal shares beside the sort's 3 kernels a pass
-  const int64_t share = bytes / (3 * p.passes) / 16 * 16;
+  const int64_t share = p.passes ? bytes / (3 * p.passes) / 16 * 16 : bytes;
   P.zbytes = share;
   P.zero = static_cast<char*>(a.dtable);
   const unsigned zgrid = bytes ? (unsigned)std::min<int64_t>(2048, share / 4096 + 1) : 0;
+  if (p.passes == 0) {
+    P.kout = keys[0];
+    P.sout = srcs[0];
+    hipLaunchKernelGGL(sort_rank_kernel, dim3((unsigned)p.nblk + zgrid), dim3(256), 0, s, a, P);
+    GMM_TRY(hipGetLastError());
+  }
   for (int q = 0; q < p.passes; ++q) {
     P.shift = q * p.bits;
     P.kin = q ? keys[(q + 1) & 1] : nullptr;
@@ -547,8 +578,8 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
   Q.chunks = p.chunks;
   Q.Dp = p.Dp;
   Q.none = p.none;
-  Q.key = keys[(p.passes - 1) & 1];
-  Q.src = srcs[(p.passes - 1) & 1];
+  Q.key = keys[p.passes ? (p.passes - 1) & 1 : 0];
+  Q.src = srcs[p.passes ? (p.passes - 1) & 1 : 0];
   Q.part = reinterpret_cast<float*>(ws + p.off_part);
   const RowSplit sp = row_split(a.D, Vec<T>::E);
   const int64_t per = 256 >> sp.lg;
@@ -574,20 +605,27 @@ hipError_t launch_zero(void* p, int64_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
-LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, bool want_table) {
+LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, int dtype, bool want_table) {
   LookupPlan p{};
   if (!want_table || B * N == 0) return p;
   p.S = B * N * m;
   p.none = (uint32_t)(B * K);
-  int total = 0;
-  while (((int64_t)1 << total) <= B * K) ++total;  // bits of the key B K
-  p.passes = (total + 9) / 10;
-  p.bits = (total + p.passes - 1) / p.passes;
-  p.per = p.S <= 1 << 20 ? kSortSmall : kSortLarge;
-  p.nblk = (p.S + 256 * p.per - 1) / (256 * p.per);
-  // entries of a chunk: 32, more where that makes over 2^13 chunks
-  p.C = 32;
-  while (p.C < 1024 && p.S / p.C > 1 << 13) p.C *= 2;
+  if (p.S <= kRankEntries) {  // passes 0: one kernel ranks them
+    p.nblk = (p.S + 31) / 32;
+  } else {
+    int total = 0;
+    while (((int64_t)1 << total) <= B * K) ++total;  // bits of the key B K
+    p.passes = (total + 9) / 10;
+    p.bits = (total + p.passes - 1) / p.passes;
+    p.per = p.S <= 1 << 20 ? kSortSmall : kSortLarge;
+    p.nblk = (p.S + 256 * p.per - 1) / (256 * p.per);
+  }
+  // entries of a chunk: as few as fill the card with threads (a thread per 16
+  // bytes of a chunk), 8 at least, and at most 2^13 chunks up to 2^23 entries
+  const RowSplit sp = row_split(D, dtype == 0 ? 4 : 8);
+  const int64_t lanes = (int64_t)sp.slabs << sp.lg;
+  p.C = 8;
+  while (p.C < 1024 && (p.S / p.C * lanes > 1 << 18 || p.S / p.C > 1 << 13)) p.C *= 2;
   p.chunks = (p.S + p.C - 1) / p.C;
   p.Dp = (D + 7) / 8 * 8;
   size_t o = 0;

@@ -34,7 +34,7 @@ def make(N, m, D, K, dtype, weighted=True, seed=0, skew=False, offset=0, pad=0):
 
 SIZES = [(1, 1, 1, 1), (1, 1, 4096, 50), (1, 4, 128, 10), (3, 2, 7, 1), (100, 4, 128, 64), (257, 3, 65, 5), (1000, 1, 33, 2000),
          (4096, 4, 128, 300), (4097, 16, 20, 1000), (5000, 1, 520, 7), (9000, 5, 8, 1030), (70, 1, 8200, 40),
-         (30000, 2, 16, 120000)]
+         (30000, 2, 16, 120000), (8192, 1, 12, 700), (2731, 3, 40, 90), (8193, 1, 12, 700), (33, 1, 5, 2)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
