@@ -89,6 +89,7 @@ struct SmallArgs {
   RowsArgs own;            // LSE, DX: the rows; DW: the classes
   const char* stream;      // LSE, DX: classes v0 .. v0 + count of the head; DW: the chunk's rows
   int64_t ld_stream;       // bytes, a multiple of 16
+  int64_t plane;           // float32: bytes from one bf16 plane of the stream to the next
   int64_t count;           // streamed rows
   int64_t v0;              // first class of the piece
   int64_t V;
@@ -113,6 +114,8 @@ struct SmallArgs {
   float* dbp;              // DW: [split][owners] column sums of G, null: not wanted
 };
 
+// float32 rows -> three bf16 planes [3][nr][Dp]
+hipError_t launch_xent_split(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s);
 // passes of launch_xent_small: 0 LSE, 1 DX, 2 DW
 hipError_t launch_xent_small(SmallArgs P, int dtype, int pass, hipStream_t s);
 int xent_small_rows(int dtype, int64_t D, int pass);  // owner rows of a workgroup

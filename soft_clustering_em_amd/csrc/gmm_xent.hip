@@ -697,14 +697,16 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
   p.small = a.D <= 128 && R > 64;
   if (p.small) {
     // rows stream past in chunks only where they are copied to aligned rows
-    // first, classes likewise (a chunk's and a piece's copies stay under 2^27 bytes)
-    p.nc = p.pack_x && want_dw ? std::min<int64_t>(R, 1 << 18) : R;
-    p.vc = p.pack_w && (!grad || want_dx) ? std::min<int64_t>(V, 1 << 18) : V;
+    // first (float32: as planes), classes likewise
+    const bool split = es == 4;  // copied as bf16 planes
+    p.pack_x = (p.pack_x || split) && grad && (want_dw || want_db);
+    p.pack_w = (p.pack_w || split) && (!grad || want_dx);
+    p.nc = p.pack_x ? std::min<int64_t>(R, 1 << 20) : R;
+    p.vc = p.pack_w ? std::min<int64_t>(V, 1 << 18) : V;
+    p.Dp = up(a.D, 8);
     p.np_r = (R + p.nc - 1) / p.nc;
     p.np_v = (V + p.vc - 1) / p.vc;
     p.lds = up(a.D, 4);
-    p.pack_x = p.pack_x && grad && want_dw;
-    p.pack_w = p.pack_w && (!grad || want_dx);
     if (!grad) {
       p.split_x = xent_small_splits(R, p.vc, a.dtype, a.D, 0);
       if (p.split_x * p.np_v > 1) {
@@ -774,8 +776,9 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
       if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
     }
   }
-  if (p.pack_x) { p.off_px = o; o = upz(o + (size_t)(std::min(p.nc, R) * p.Dp * es)); }
-  if (p.pack_w) { p.off_pw = o; o = upz(o + (size_t)(std::min(p.vc, V) * p.Dp * es)); }
+  const int64_t pes = p.small ? (es == 4 ? 6 : 2) : es;  // bytes of a copied element
+  if (p.pack_x) { p.off_px = o; o = upz(o + (size_t)(std::min(p.nc, R) * p.Dp * pes)); }
+  if (p.pack_w) { p.off_pw = o; o = upz(o + (size_t)(std::min(p.vc, V) * p.Dp * pes)); }
   p.bytes = o;
   return p;
 }
@@ -854,6 +857,16 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
 
 // ---- rows of at most 128 features (gmm_xent_small.hip)
 template <typename T>
+hipError_t copy_stream(const RowsArgs& r, char* dst, int64_t Dp, SmallArgs& P, hipStream_t s) {
+  if constexpr (sizeof(T) == 4) GMM_TRY(launch_xent_split(r, dst, Dp, s));
+  else GMM_TRY(pack<T>(r, dst, Dp, s));
+  P.stream = dst;
+  P.ld_stream = Dp * 2;
+  P.plane = r.nr * Dp * 2;
+  return hipSuccess;
+}
+
+template <typename T>
 hipError_t stream_classes(const XentArgs& a, const XentPlan& p, int64_t v0, int64_t nv, char* ws, SmallArgs& P,
                           hipStream_t s) {
   const int64_t es = sizeof(T);
@@ -862,9 +875,7 @@ hipError_t stream_classes(const XentArgs& a, const XentPlan& p, int64_t v0, int6
   P.ld_stream = a.ld_w * es;
   if (p.pack_w) {
     const RowsArgs r{(const char*)a.w, a.V, a.ld_w, 0, v0, nv, (int)a.D};
-    GMM_TRY(pack<T>(r, ws + p.off_pw, p.Dp, s));
-    P.stream = ws + p.off_pw;
-    P.ld_stream = p.Dp * es;
+    GMM_TRY(copy_stream<T>(r, ws + p.off_pw, p.Dp, P, s));
   }
   P.count = nv;
   P.v0 = v0;
@@ -943,9 +954,7 @@ hipError_t small_backward(const XentArgs& a, const XentPlan& p, const float* lse
     P.ld_stream = a.ld * es;
     if (p.pack_x) {
       const RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
-      GMM_TRY(pack<T>(r, ws + p.off_px, p.Dp, s));
-      P.stream = ws + p.off_px;
-      P.ld_stream = p.Dp * es;
+      GMM_TRY(copy_stream<T>(r, ws + p.off_px, p.Dp, P, s));
     }
     P.count = nr;
     P.V = a.V;

@@ -13,14 +13,17 @@
 //   DW   owner classes, streamed rows: the same with c (p - [v = y]) and X
 // The logits are formed as stream x owner^T, so that a lane holds 4 consecutive
 // streamed rows of one owner row: the k order that the second product's
-// fragment wants (two blocks for the 32 of a 16-bit instruction), and its other
+// fragment wants (two blocks for the 32 of an instruction), and its other
 // operand, the streamed tile with its rows along k, comes out of LDS through
-// the transposing read (float32: element reads).  The bias enters as the
-// accumulator's start.  Three exponentials an element (LSE, DX, DW) and 10 N V D
+// the transposing read.  The bias enters as the accumulator's start.  Three exponentials an element (LSE, DX, DW) and 10 N V D
 // flops take the place of G's traffic, 8 bytes an element.
 //
 // LDS: a tile's rows are RBytes = D_padded * size apart, a row's 16-byte chunk c
 // in slot c ^ f(row); f makes the reads of 16 rows touch all 64 banks.
+//
+// float32 rows run on the bf16 matrix cores too, as three planes (kPairs): six
+// products at 16 times the rate of the float32 instruction, what they leave out
+// below 2^-23 of |x| |w|, the size of the roundings of the sum.
 //
 // Rounding: as in gmm_xent.hip.  DX rounds p - [v = y] itself and multiplies
 // by the row's coefficient in float32 at the end; half: p is scaled by 2^15
@@ -31,6 +34,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gmm {
 
@@ -42,7 +46,42 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
-constexpr int kTile = 64;  // streamed rows per tile
+// float32 rows enter the matrix cores as three bf16 planes, x = h + m + l, each
+// the rounding of what the ones before it leave; of the nine products of two
+// such sums the six down to 2^-16 of the largest are taken
+constexpr int kPairs[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
+constexpr int planes(int es) { return es == 4 ? 3 : 1; }
+// streamed rows per tile
+constexpr int tile_rows(int es, int dp) { return es == 4 && dp == 128 ? 32 : 64; }
+
+// 4 float32 -> 4 bf16 of each plane
+__device__ inline void split4(f32x4 v, u32x2* p) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const __bf16 t[4] = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    p[k] = __builtin_bit_cast(u32x2, t);
+    if (k < 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float r = v[e] - (float)t[e];
+        v[e] = __builtin_isfinite(v[e]) ? r : 0.f;  // an infinity or NaN stays in the first plane
+      }
+  }
+}
+
+// rows of any layout -> [3][nr][Dp] bf16 planes, zeros past D; a thread per 4 elements
+__global__ void __launch_bounds__(256) split_kernel(RowsArgs R, char* dst, int Dp) {
+  const int q = Dp / 4;
+  const int64_t n = R.nr * q, plane = R.nr * Dp * 2;
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
+    const int64_t r = t / q;
+    const int c = (int)(t - r * q) * 16;
+    u32x2 p[3];
+    split4(__builtin_bit_cast(f32x4, chunk_at<float>(R.x + row_offset(R, R.r0 + r) * 4, c, R.D * 4)), p);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x2*>(dst + k * plane + t * 8) = p[k];
+  }
+}
 
 template <typename T>
 __device__ inline float dot16(u32x4 a, u32x4 b) {
@@ -55,23 +94,24 @@ __device__ inline float dot16(u32x4 a, u32x4 b) {
   return s;
 }
 
-template <typename T, int DP, int RB, int PASS>
+// S: the rows' type; its matrix-core form is itself, or bf16 planes
+template <typename S, int DP, int RB, int PASS>
 __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
-  constexpr int ES = sizeof(T), RBytes = DP * ES, KC = RBytes / 16, KS = KC / 4;
-  constexpr int kBytes = kTile * RBytes, JS = kBytes / 4096;  // 16-byte loads of a thread per tile
+  using T = std::conditional_t<sizeof(S) == 4, __bf16, S>;
+  constexpr int PL = planes(sizeof(S)), NP = PL == 1 ? 1 : 6, kTile = tile_rows(sizeof(S), DP);
+  constexpr int RBytes = DP * 2, KC = RBytes / 16, KS = KC / 4;
+  constexpr int kPlane = kTile * RBytes, kBytes = PL * kPlane, JS = kPlane / 4096;  // 16-byte loads of a thread per plane
   constexpr int RPB = RBytes >= 256 ? 1 : 256 / RBytes, FM = (KC < 16 ? KC : 16) - 1;
   constexpr int NB = kTile / 16, ND = DP / 16;
   // f(row), on the rows that share 256 bytes as one (g): a fragment read's 16
   // lanes at a time are rows 0-3 and 12-15 of one chunk and rows 4-11 of the
   // next, so the first eight's places have to be whole pairs; a transposing
   // read takes pairs of chunks of 8 rows, so those have to be of 8 pairs
-  // (16-bit rows; float32 rows are read by element instead)
   auto swizzle = [](int row) {
     const int g = (row / RPB) & FM, H = (FM + 1) / 2;
-    if (ES == 4) return g;
     return g < H ? 2 * g : 2 * ((g - H) ^ (H / 2)) + 1;
   };
-  constexpr float kTop = ES == 2 && !__is_same(T, __bf16) ? 32768.f : 1.f;  // DX: scale of p
+  constexpr float kTop = __is_same(S, _Float16) ? 32768.f : 1.f;  // DX: scale of p
   __shared__ __attribute__((aligned(1024))) char st0[kBytes];
   __shared__ __attribute__((aligned(1024))) char st1[kBytes];
   __shared__ __attribute__((aligned(16))) float sp0[PASS == DW ? 3 * kTile : kTile];
@@ -84,7 +124,6 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t o0 = ((int64_t)tile_own * 4 + wv) * (16 * RB);  // the wave's first owner row
-  const int kbytes = P.own.D * ES;
 
   const int ntiles = (int)((P.count + kTile - 1) / kTile);
   const int t0 = (int)((int64_t)ntiles * split / P.splits), t1 = (int)((int64_t)ntiles * (split + 1) / P.splits);
@@ -93,7 +132,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   auto rows_of = [&](int t) { return t < t1 ? (int)min((int64_t)kTile, P.count - (int64_t)t * kTile) : 0; };
 
   // ---- the owner's rows and what goes with each
-  u32x4 own[RB][KS];
+  u32x4 own[RB][PL][KS];
   float oa[RB];  // LSE, DX: -lse log2(e) (+ log2 kTop);  DW: the class's bias
   float oc[RB];  // DX: the row's coefficient
   int oy[RB];    // LSE: label;  DX: label within the piece;  DW: the class
@@ -116,17 +155,27 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
       oy[i] = (int)o;
       oa[i] = live ? (P.bias ? P.bias[o] : 0.f) : -INFINITY;
     }
-    const char* row = P.own.x + (live ? row_offset(P.own, o) : 0) * (int64_t)ES;
+    const char* row = P.own.x + (live ? row_offset(P.own, o) : 0) * (int64_t)sizeof(S);
+    const int bytes = live ? P.own.D * (int)sizeof(S) : 0;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-      own[i][k] = live ? chunk_at<T>(row, (k * 4 + lq) * 16, kbytes) : u32x4{0u, 0u, 0u, 0u};
+    for (int k = 0; k < KS; ++k) {
+      if constexpr (PL == 1) {
+        own[i][0][k] = chunk_at<S>(row, (k * 4 + lq) * 16, bytes);
+      } else {
+        u32x2 p[2][3];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          split4(__builtin_bit_cast(f32x4, chunk_at<S>(row, (k * 4 + lq) * 32 + 16 * u, bytes)), p[u]);
+#pragma unroll
+        for (int l = 0; l < PL; ++l) own[i][l][k] = u32x4{p[0][l][0], p[0][l][1], p[1][l][0], p[1][l][1]};
+      }
+    }
   }
 
   // ---- streamed tiles.  Load j of a thread: row row0 + j RPJ of the tile, one
-  // 16-byte chunk, the same of every row but for f's bit 3 where rows are 512 bytes
-  // (rows a multiple of 16 apart have the same f)
+  // 16-byte chunk, the same of every row (rows a multiple of 16 apart have the same f)
   constexpr int RPJ = 4096 / RBytes;
-  const int kpad = (kbytes + 15) & ~15;  // the stream's rows hold zeros from D to whole chunks
+  const int kpad = (P.own.D * 2 + 15) & ~15;  // the stream's rows hold zeros from D to whole chunks
   const int row0 = (wv * 1024 + lane * 16) / RBytes;
   const int ch0 = ((wv * 1024 + lane * 16) % RBytes / 16) ^ swizzle(row0);
   const unsigned last = (unsigned)P.count - 1;
@@ -139,26 +188,27 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   };
   auto issue = [&](char* st, int t) {
     const int n = rows_of(t);
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(P.stream) + (n > 0 ? (int64_t)t * kTile * P.ld_stream : 0), 0,
-        n > 0 ? (unsigned)((n - 1) * P.ld_stream + kpad) : 0u, 0x00020000);
 #pragma unroll
-    for (int j = 0; j < JS; ++j) {
-      const int ch = RBytes == 512 ? ch0 ^ (8 * (j & 1)) : ch0;
-      bool in = row0 + j * RPJ < n && ch * 16 < kpad;
-      if (PASS == DW) in = in && flag[j] != 0.f;  // rows that take no part arrive as zeros
-      const unsigned o = in ? (unsigned)((row0 + j * RPJ) * (int)P.ld_stream + ch * 16) : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (__attribute__((address_space(3))) void*)(st + (j * 4 + wv) * 1024), 16, o, 0, 0, 0);
+    for (int l = 0; l < PL; ++l) {
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<char*>(P.stream) + l * P.plane + (n > 0 ? (int64_t)t * kTile * P.ld_stream : 0), 0,
+          n > 0 ? (unsigned)((n - 1) * P.ld_stream + kpad) : 0u, 0x00020000);
+#pragma unroll
+      for (int j = 0; j < JS; ++j) {
+        bool in = row0 + j * RPJ < n && ch0 * 16 < kpad;
+        if (PASS == DW) in = in && flag[j] != 0.f;  // rows that take no part arrive as zeros
+        const unsigned o = in ? (unsigned)((row0 + j * RPJ) * (int)P.ld_stream + ch0 * 16) : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (__attribute__((address_space(3))) void*)(st + l * kPlane + (j * 4 + wv) * 1024), 16, o, 0, 0, 0);
+      }
     }
   };
   // what goes with each streamed row: LSE, DX: bias;  DW: -lse log2(e), c, label
   float pa = 0.f, pb = 0.f;
   int py = -1;
   const float mult = PASS == DW && P.scal ? P.scal[0] : 1.f;
-  const unsigned prow = lane;  // every wave fetches the 64 rows, the first puts them
   auto fetch = [&](int t) {
-    const unsigned r = min((unsigned)(t * kTile) + prow, last);
+    const unsigned r = min((unsigned)(t * kTile) + lane, last);
     if constexpr (PASS == DW) {
       pa = P.lse[r];
       pb = P.coef[r];
@@ -168,7 +218,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
     }
   };
   auto put = [&](float* sp, int t) {
-    if (wv != 0) return;
+    if (wv != 0 || lane >= kTile) return;  // every wave fetches, the first puts
     const bool in = lane < rows_of(t);
     if constexpr (PASS == DW) {
       const bool live = in && pb != 0.f;
@@ -206,9 +256,14 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
     }
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(st + (16 * jb + lr) * RBytes + (((k * 4 + lq) ^ fr) * 16));
+      u32x4 a[PL];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) s[i] = mma<T>(a, own[i][k], s[i]);
+      for (int l = 0; l < PL; ++l)
+        a[l] = *reinterpret_cast<const u32x4*>(st + l * kPlane + (16 * jb + lr) * RBytes + (((k * 4 + lq) ^ fr) * 16));
+#pragma unroll
+      for (int p = NP - 1; p >= 0; --p)  // the small products first
+#pragma unroll
+        for (int i = 0; i < RB; ++i) s[i] = mma<T>(a[kPairs[p][0]], own[i][kPairs[p][1]][k], s[i]);
     }
   };
   // G of a block, in place
@@ -246,6 +301,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
       f32x4 s[NB][RB];
 #pragma unroll
       for (int jb = 0; jb < NB; ++jb) logits(st, sp, jb, s[jb]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
         float m = mx[i];
@@ -266,47 +322,41 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
 #pragma unroll
       for (int h = 0; h < NB / 2; ++h) {
         f32x4 s[2][RB];
-        u32x2 g[RB][2];
+        u32x2 g[RB][2][PL];
 #pragma unroll
         for (int u = 0; u < 2; ++u) logits(st, sp, 2 * h + u, s[u]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           gradient(sp, 2 * h + u, t, s[u]);
-          if constexpr (ES == 2)
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            if constexpr (PL == 1) {
+              const T v[4] = {(T)s[u][i][0], (T)s[u][i][1], (T)s[u][i][2], (T)s[u][i][3]};
+              g[i][u][0] = __builtin_bit_cast(u32x2, v);
+            } else {
+              split4(s[u][i], g[i][u]);
+            }
+          }
+        }
+        // lane 16 a + b reads feature 16 d + b of streamed rows 4 a .. 4 a + 3 of either block
+        const int rr = lane >> 2, fx = swizzle(rr);
+        const char* src = st + (32 * h + rr) * RBytes + 8 * (lane & 1);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const int slot = ((2 * d + ((lane & 3) >> 1)) ^ fx) * 16;
+          u32x4 a[PL];
+#pragma unroll
+          for (int l = 0; l < PL; ++l) {
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(src + l * kPlane + slot));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(src + l * kPlane + 16 * RBytes + slot));
+            a[l] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          }
+#pragma unroll
+          for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-              const T v[4] = {(T)s[u][i][0], (T)s[u][i][1], (T)s[u][i][2], (T)s[u][i][3]};
-              g[i][u] = __builtin_bit_cast(u32x2, v);
-            }
-        }
-        if constexpr (ES == 2) {
-          // lane 16 a + b reads feature 16 d + b of streamed rows 4 a .. 4 a + 3 of either block
-          const int rr = lane >> 2, fx = swizzle(rr);
-          const char* src = st + (32 * h + rr) * RBytes + 8 * (lane & 1);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const int slot = ((2 * d + ((lane & 3) >> 1)) ^ fx) * 16;
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(src + slot));
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(src + 16 * RBytes + slot));
-            const u32x4 a = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-              acc[i][d] = mma<T>(a, u32x4{g[i][0][0], g[i][0][1], g[i][1][0], g[i][1][1]}, acc[i][d]);
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int row = 4 * lq + e, fx = swizzle(row);
-              const char* src = st + (32 * h + 16 * u + row) * RBytes + 4 * (lr & 3);
-#pragma unroll
-              for (int d = 0; d < ND; ++d) {
-                const float a = *reinterpret_cast<const float*>(src + ((4 * d + (lr >> 2)) ^ fx) * 16);
-#pragma unroll
-                for (int i = 0; i < RB; ++i)
-                  acc[i][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, s[u][i][e], acc[i][d], 0, 0, 0);
-              }
+              const u32x2 *g0 = &g[i][0][kPairs[p][1]], *g1 = &g[i][1][kPairs[p][1]];
+              acc[i][d] = mma<T>(a[kPairs[p][0]], u32x4{(*g0)[0], (*g0)[1], (*g1)[0], (*g1)[1]}, acc[i][d]);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -341,13 +391,14 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
     for (int i = 0; i < RB; ++i) {
       const int64_t o = o0 + 16 * i + lr;
       const bool in = o < P.own.nr;
-      // the label's logit: the owner's fragments against the label's row of the head
+      // the label's logit: the row against the label's row of the head
       const bool lab = oy[i] >= 0 && oy[i] < P.V;
       float l = 0.f;
-      const char* wr = P.w + (lab ? oy[i] * P.ld_w * ES : 0);
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-        if (lab) l += dot16<T>(own[i][k], chunk_at<T>(wr, (k * 4 + lq) * 16, kbytes));
+      const int bytes = P.own.D * (int)sizeof(S);
+      const char* wr = P.w + (lab ? oy[i] * P.ld_w * (int64_t)sizeof(S) : 0);
+      const char* xr = P.own.x + (lab ? row_offset(P.own, o) : 0) * (int64_t)sizeof(S);
+      if (lab)
+        for (int c = lq * 16; c < bytes; c += 64) l += dot16<S>(chunk_at<S>(xr, c, bytes), chunk_at<S>(wr, c, bytes));
       float m = mx[i], s = sm[i];
 #pragma unroll
       for (int off = 16; off < 64; off <<= 1) {
@@ -393,13 +444,13 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
           *reinterpret_cast<f32x4*>(p) = v;
           continue;
         }
-        T* p = reinterpret_cast<T*>(P.out) + o * P.own.D + f;
+        S* p = reinterpret_cast<S*>(P.out) + o * P.own.D + f;
         if (f + 4 <= P.own.D && !P.accumulate) {
-          store4<T>(p, v);
+          store4<S>(p, v);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (f + e < P.own.D) p[e] = (T)(v[e] + (P.accumulate ? to_f32(p[e]) : 0.f));
+            if (f + e < P.own.D) p[e] = (S)(v[e] + (P.accumulate ? to_f32(p[e]) : 0.f));
         }
       }
     }
@@ -408,9 +459,9 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
 
 // 16-row blocks of a wave: as many as the registers hold
 constexpr int owner_blocks(int es, int dp, int pass) {
-  const int bytes = es * dp;
-  if (pass == LSE) return es == 4 && bytes > 128 ? 2 : 4;
-  return bytes > 256 ? 1 : bytes > 128 ? 2 : 4;
+  if (es == 2) return pass == LSE || dp <= 64 ? 4 : 2;
+  if (pass == LSE) return dp >= 64 ? 2 : 4;
+  return dp == 128 ? 1 : 2;
 }
 
 template <typename T, int DP, int PASS>
@@ -442,9 +493,16 @@ int xent_small_rows(int dtype, int64_t D, int pass) {
 
 int xent_small_splits(int64_t owners, int64_t streamed, int dtype, int64_t D, int pass) {
   const int rows = xent_small_rows(dtype, D, pass);
-  const int64_t t = (owners + rows - 1) / rows, tiles = (streamed + kTile - 1) / kTile;
+  const int64_t t = (owners + rows - 1) / rows, tiles = (streamed + 63) / 64;
   const int64_t want = t >= 2 * kNumCU ? 1 : (2 * kNumCU) / t;
   return (int)std::max<int64_t>(1, std::min(want, tiles / 4));
+}
+
+hipError_t launch_xent_split(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s) {
+  const int64_t n = r.nr * Dp / 4;
+  hipLaunchKernelGGL(split_kernel, dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 1 << 16))),
+                     dim3(256), 0, s, r, dst, (int)Dp);
+  return hipGetLastError();
 }
 
 hipError_t launch_xent_small(SmallArgs P, int dtype, int pass, hipStream_t s) {
