@@ -7,9 +7,11 @@ Every per-row and per-component number comes from the HIP library:
 score_samples and predict from gmm_predict_proba_topm (m = 1: the best
 component and log p(x_i)), score from gmm_estep_stats (sum_i log p(x_i)),
 fit from gmm_fit_step (or gmm_topk_fit_step, the approximate top-k mode of
-the GMMXX README), KernelDensity.score_samples from gmm_kde_score.  What runs
-here is argument handling, the stopping rule and the AIC/BIC arithmetic on B
-returned scalars.
+the GMMXX README), KernelDensity.score_samples from gmm_kde_score, the rows
+that reconstruct rebuilds from gmm_codebook_lookup, SoftmaxHead's losses and
+gradients from gmm_softmax_xent, gmm_softmax_xent_grad and gmm_clip_grad_norm.
+What runs here is argument handling, the stopping rule, the AIC/BIC arithmetic
+on B returned scalars and SoftmaxHead's parameter update.
 
   n_parameters(cov, K, D)                       -> int
   score_samples(X, w, mu, cv, cov)              -> (B, N) float32 log p(x_i)
@@ -21,6 +23,7 @@ returned scalars.
   GaussianMixture(n_components, covariance_type, ...)  the same calls as a scikit-learn style class
   KMeans(n_clusters, ...)                       Lloyd iterations over gmm_kmeans_step (the hard limit)
   KernelDensity(bandwidth)                      Gaussian kernel density estimate over gmm_kde_score
+  SoftmaxHead(n_classes, ...)                   linear softmax classifier (the discriminative posterior)
 """
 from __future__ import annotations
 
@@ -29,8 +32,9 @@ from dataclasses import dataclass
 
 import numpy as np
 
-from . import (gmm_estep_stats, gmm_fit, gmm_fit_step, gmm_kde_score, gmm_kmeans_step, gmm_predict_proba_topm,
-               gmm_topk_fit_step, gmm_topk_fit_workspace_bytes, new_stats)
+from . import (gmm_clip_grad_norm, gmm_codebook_lookup, gmm_estep_stats, gmm_fit, gmm_fit_step, gmm_kde_score,
+               gmm_kmeans_step, gmm_predict_proba_topm, gmm_softmax_xent, gmm_softmax_xent_grad, gmm_topk_fit_step,
+               gmm_topk_fit_workspace_bytes, new_stats)
 
 
 def _torch():
@@ -301,6 +305,14 @@ class GaussianMixture:
         gmm_predict_proba_topm(X, *self._theta(), m, threshold, idx, resp, count=count)
         return idx, resp, count
 
+    def reconstruct(self, X, m=4, threshold=0.1):
+        """The rows rebuilt from their soft multi-assignment: sum_j r_ij
+        mu_{idx_ij} over the components that predict_proba_topm keeps, (N, D)
+        float32 (with every component kept, the posterior mean of the row's
+        component mean)."""
+        idx, resp, _ = self.predict_proba_topm(X, m, threshold)
+        return gmm_codebook_lookup(self.means_, idx, weights=resp)
+
 
 class KMeans:
     """k-means by Lloyd iterations, each one gmm_kmeans_step (nearest
@@ -362,6 +374,13 @@ class KMeans:
     def fit_predict(self, X):
         return self.fit(X).labels_
 
+    def reconstruct(self, labels):
+        """The centres of labels ((N,) int32, as predict returns them), (N, D)
+        float32; a label outside [0, n_clusters) gives a row of zeros."""
+        if not hasattr(self, "cluster_centers_"):
+            raise RuntimeError("call fit first")
+        return gmm_codebook_lookup(self.cluster_centers_, labels)
+
 
 class KernelDensity:
     """Gaussian kernel density estimate in the scikit-learn style
@@ -390,3 +409,100 @@ class KernelDensity:
     def score(self, Y):
         return float(self.score_samples(Y).double().sum().item())
 
+
+class SoftmaxHead:
+    """A linear softmax classifier over n_classes, p(k | x) = softmax(W x + b)_k:
+    the posterior of a mixture with one shared spherical variance
+    (W_k = mu_k / s^2, b_k = log pi_k - |mu_k|^2 / (2 s^2)), trained on labels
+    instead of on the rows' density -- a router over the lists of a coarse
+    quantizer, for example, from the labels of KMeans or GaussianMixture.
+
+    fit(X, y) runs full-batch gradient descent with momentum on the mean
+    cross entropy of the labelled rows (y (N,) int32; a negative label leaves a
+    row out), each step one gmm_softmax_xent, one gmm_softmax_xent_grad and,
+    with max_grad_norm, one gmm_clip_grad_norm over both gradients, until the
+    loss changes by less than tol.  X is (N, D) float32, bfloat16 or float16 on
+    the GPU.  Fitted state: coef_ (K, D) and intercept_ (K,) float32, loss_ (the
+    mean loss entering the last step), loss_history_, grad_norm_ (the last
+    step's norm before clipping, None without it), n_iter_."""
+
+    def __init__(self, n_classes, learning_rate=1.0, momentum=0.9, max_iter=100, tol=1e-6, max_grad_norm=None):
+        if int(n_classes) < 1:
+            raise ValueError("n_classes must be >= 1")
+        if max_grad_norm is not None and not float(max_grad_norm) > 0.0:
+            raise ValueError("max_grad_norm must be > 0")
+        self.n_classes = int(n_classes)
+        self.learning_rate, self.momentum = float(learning_rate), float(momentum)
+        self.max_iter, self.tol = int(max_iter), float(tol)
+        self.max_grad_norm = None if max_grad_norm is None else float(max_grad_norm)
+
+    @classmethod
+    def from_mixture(cls, mixture, variance=None, **kwargs):
+        """The head that is the posterior of a fitted spherical GaussianMixture
+        with its variances replaced by one (None: their mean under the
+        weights)."""
+        if mixture.covariance_type != "spherical":
+            raise ValueError("the mixture must be spherical")
+        w, mu, cv, _ = mixture._theta()
+        head = cls(mixture.n_components, **kwargs)
+        s2 = (w * cv).sum() / w.sum() if variance is None else float(variance)
+        return head._set(mu / s2, w.log() - (mu * mu).sum(1) / (2 * s2))
+
+    def _set(self, coef, intercept):
+        self.coef_, self.intercept_ = coef.float().contiguous(), intercept.float().contiguous()
+        return self
+
+    def _check(self, X, y):
+        torch = _torch()
+        if X.dim() != 2:
+            raise ValueError("X is (N, D)")
+        if y.dtype != torch.int32 or y.shape != X.shape[:1]:
+            raise ValueError("y is (N,) int32")
+
+    def loss_and_gradients(self, X, y):
+        """(mean loss, its gradients for coef_ and intercept_): a 0-dimensional
+        and two float32 tensors on the GPU."""
+        torch = _torch()
+        self._check(X, y)
+        if not hasattr(self, "coef_"):
+            raise RuntimeError("call fit first")
+        y = y.contiguous()
+        W = self.coef_.to(X.dtype)
+        loss, lse = gmm_softmax_xent(X, W, y, bias=self.intercept_)
+        n = (y >= 0).sum().clamp_min(1).float()
+        gloss = (1.0 / n).expand(y.shape).contiguous()
+        _, dW, db = gmm_softmax_xent_grad(X, W, y, lse, gloss=gloss, bias=self.intercept_, dX=False)
+        return loss.sum() / n, dW.float(), db
+
+    def fit(self, X, y):
+        torch = _torch()
+        self._check(X, y)
+        if not hasattr(self, "coef_"):
+            self._set(torch.zeros(self.n_classes, X.shape[1], device=X.device),
+                      torch.zeros(self.n_classes, device=X.device))
+        step = [torch.zeros_like(self.coef_), torch.zeros_like(self.intercept_)]
+        self.loss_history_, self.grad_norm_ = [], None
+        for self.n_iter_ in range(1, self.max_iter + 1):
+            loss, *grads = self.loss_and_gradients(X, y)
+            if self.max_grad_norm is not None:
+                self.grad_norm_ = gmm_clip_grad_norm(grads, self.max_grad_norm)
+            for p, v, g in zip((self.coef_, self.intercept_), step, grads):
+                v.mul_(self.momentum).add_(g)
+                p.sub_(v, alpha=self.learning_rate)
+            self.loss_history_.append(float(loss))
+            if len(self.loss_history_) > 1 and abs(self.loss_history_[-2] - self.loss_history_[-1]) < self.tol:
+                break
+        self.loss_ = self.loss_history_[-1]
+        return self
+
+    def log_proba(self, X, y):
+        """log p(y_i | x_i) of every row (0 where the label is negative), (N,) float32."""
+        self._check(X, y)
+        if not hasattr(self, "coef_"):
+            raise RuntimeError("call fit first")
+        return -gmm_softmax_xent(X, self.coef_.to(X.dtype), y.contiguous(), bias=self.intercept_)[0]
+
+    def score(self, X, y):
+        """The mean log p(y_i | x_i) of the labelled rows, on the host."""
+        lp = self.log_proba(X, y)
+        return float(lp.double().sum() / (y >= 0).sum().clamp_min(1))
