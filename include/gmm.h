@@ -371,9 +371,10 @@ typedef struct {
  * labels (B,N) int32: a negative label leaves the row out (loss 0; its lse is
  * still formed); a label >= V gives loss NaN.  Rows and head are float32, bf16
  * or half, of one type, at any stride and alignment of their elements
- * (operands off 16 bytes are copied piecewise); logits are exact products
- * summed in float32.  Scores of one row to 64 rows take a path that reads the
- * head once.  Window: D <= 65536, V < 2^31, B*N < 2^31.  A row whose logits
+ * (operands off 16 bytes are copied piecewise); logits are summed in float32
+ * (float32 rows of D <= 128: products of three bf16 planes, right to 2^-23 of
+ * |x| |w|; a row with an infinity then has NaN results).  Scores of one row to 64 rows take a path that reads the
+ * head once.  Window: D <= 65536, V < 2^27, B*N < 2^28.  A row whose logits
  * are all -inf has lse -inf and loss NaN.  N = 0 launches nothing.
  * Workspace: gmm_softmax_xent_workspace_bytes (bounded: rows are taken in
  * chunks).  Deterministic. */

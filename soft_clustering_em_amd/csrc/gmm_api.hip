@@ -1334,8 +1334,9 @@ static gmm_status xent_args(const gmm_data* d, const gmm_head* h, XentArgs* a) {
     return fail(h->dtype >= GMM_DT_F32 && h->dtype <= GMM_DT_F16 ? GMM_ERR_UNSUPPORTED : GMM_ERR_INVALID_ARG,
                 "the head's dtype (%d) must be the rows' (%d)", h->dtype, d->dtype);
   if (d->D > 65536) return fail(GMM_ERR_UNSUPPORTED, "D (%lld) > 65536", (long long)d->D);
-  if (h->V >= ((int64_t)1 << 31)) return fail(GMM_ERR_UNSUPPORTED, "V must stay below 2^31");
-  if (d->N > 0 && d->B > (((int64_t)1 << 31) - 1) / d->N) return fail(GMM_ERR_UNSUPPORTED, "B*N must stay below 2^31");
+  // a launch has fewer than 2^32 threads an axis: 16 a class, 4 a row at most
+  if (h->V >= ((int64_t)1 << 27)) return fail(GMM_ERR_UNSUPPORTED, "V must stay below 2^27");
+  if (d->N > 0 && d->B > (((int64_t)1 << 28) - 1) / d->N) return fail(GMM_ERR_UNSUPPORTED, "B*N must stay below 2^28");
   a->x = d->x;
   a->w = h->w;
   a->bias = h->bias;
@@ -1375,6 +1376,11 @@ gmm_status gmm_softmax_xent(const gmm_data* rows, const gmm_head* head, const in
   const int64_t R = a.B * a.N;
   if (R > 0 && (!labels || !loss || !lse)) return fail(GMM_ERR_INVALID_ARG, "labels, loss and lse must be non-NULL");
   if (overlap(loss, 4 * R, lse, 4 * R)) return fail(GMM_ERR_INVALID_ARG, "loss and lse overlap");
+  const int64_t sw = ((a.V - 1) * a.ld_w + a.D) * a.es;
+  for (const void* o : {(const void*)loss, (const void*)lse})
+    if (overlap(o, 4 * R, a.x, data_span(rows, a.es)) || overlap(o, 4 * R, a.w, sw) || overlap(o, 4 * R, a.bias, 4 * a.V) ||
+        overlap(o, 4 * R, labels, 4 * R))
+      return fail(GMM_ERR_INVALID_ARG, "an output overlaps an input");
   const XentPlan p = xent_plan(a, false, false, false, false);
   if ((st = check_ws(ws, ws_bytes, std::max(kAlign, p.bytes))) != GMM_OK) return st;
   if (R == 0) return GMM_OK;

@@ -17,6 +17,8 @@ namespace gmm {
 
 namespace {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 template <typename T>
 __device__ inline double squares(const T* p, int64_t n) {
   constexpr int E = 16 / (int)sizeof(T);
@@ -42,12 +44,15 @@ template <typename T>
 __device__ inline void scaled(const T* p, T* q, int64_t n, float c) {
   constexpr int E = 16 / (int)sizeof(T);
   const int64_t nv = n / E;
+  const bool aligned = (uintptr_t)q % 16 == 0;  // stored past the caches: nobody reads it back soon
+#pragma unroll 4
   for (int64_t t = threadIdx.x; t < nv; t += 256) {
     T v[E];
     __builtin_memcpy(v, p + t * E, 16);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = (T)(c * (float)v[e]);
-    __builtin_memcpy(q + t * E, v, 16);
+    if (aligned) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(q + t * E));
+    else __builtin_memcpy(q + t * E, v, 16);
   }
   if ((int)threadIdx.x < n - nv * E) {
     const int64_t i = nv * E + threadIdx.x;
@@ -96,9 +101,10 @@ __global__ void __launch_bounds__(256) coefficient_kernel(const double* part, in
   *coef = c < 1.0 || c != c ? (float)c : 1.f;  // a NaN norm gives NaN gradients
 }
 
+// from the last piece to the first: the norm's pass left the last ones in the caches
 __global__ void __launch_bounds__(256) scale_kernel(ClipArgs A, const float* coef) {
   const float c = *coef;
-  for (int64_t p = blockIdx.x; p < A.pieces; p += gridDim.x) {
+  for (int64_t p = A.pieces - 1 - blockIdx.x; p >= 0; p -= gridDim.x) {
     const ClipTensor& t = A.t[tensor_of(A, p)];
     if (c == 1.f && t.src == t.dst) continue;
     const int64_t i0 = (p - t.piece0) * kClipPiece, n = min(kClipPiece, t.n - i0);

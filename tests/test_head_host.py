@@ -30,8 +30,8 @@ BAD_OPERANDS = [
     (dict(D=0, ld=0), {}, INV), (dict(N=-1), {}, INV), (dict(Bn=0), {}, INV), (dict(ld=63), {}, INV),
     (dict(Bn=2, sb=100), {}, INV), (dict(x=None), {}, INV), (dict(dtype=7), {}, INV),
     ({}, dict(V=0), INV), ({}, dict(w=None), INV), ({}, dict(ld=63), INV), ({}, dict(dtype=9), INV),
-    ({}, dict(dtype=_abi.DT_F32), UNS), (dict(D=65537), dict(D=65537), UNS), ({}, dict(V=1 << 31), UNS),
-    (dict(N=1 << 31), {}, UNS), (dict(N=1 << 20, Bn=1 << 12), {}, UNS), (dict(x=P((1 << 40) + 1)), {}, INV),
+    ({}, dict(dtype=_abi.DT_F32), UNS), (dict(D=65537), dict(D=65537), UNS), ({}, dict(V=1 << 27), UNS),
+    (dict(N=1 << 28), {}, UNS), (dict(N=1 << 18, Bn=1 << 12), {}, UNS), (dict(x=P((1 << 40) + 1)), {}, INV),
     ({}, dict(w=P((2 << 40) + 1)), INV),
 ]
 
@@ -56,6 +56,8 @@ def test_xent_refuses_bad_pointers_and_workspaces():
         a[miss] = None
         assert L.gmm_softmax_xent(d, h, *a, WS, BIG, None) == INV
     assert L.gmm_softmax_xent(d, h, C, E, P((4 << 40) + 8), WS, BIG, None) == INV  # lse inside loss
+    for on in (A, B, C):  # loss on the rows, the head, the labels
+        assert L.gmm_softmax_xent(d, h, C, on, F, WS, BIG, None) == INV and "overlaps" in last()
     n = L.gmm_softmax_xent_workspace_bytes(d, h)
     assert n > 0 and n % 256 == 0
     for ws, have in ((None, BIG), (P((1 << 50) + 16), BIG), (WS, n - 1)):
@@ -76,7 +78,9 @@ def test_xent_refuses_bad_pointers_and_workspaces():
 def test_xent_workspaces_are_bounded():
     L = _abi.lib()
     f = lambda N, V: L.gmm_softmax_xent_workspace_bytes(ctypes.byref(rows(N=N)), ctypes.byref(head(V=V)))  # noqa: E731
-    assert f(10 ** 9, 10 ** 5) < 1 << 28
+    assert 0 < f(10 ** 8, 10 ** 5) < 1 << 32
+    wide = L.gmm_softmax_xent_workspace_bytes(ctypes.byref(rows(N=10 ** 8, D=256)), ctypes.byref(head(V=10 ** 5, D=256)))
+    assert 0 < wide < 1 << 28
     assert f(1, 10 ** 6) < 1 << 20
     # G's pieces: far below N V elements
     g = L.gmm_softmax_xent_grad_workspace_bytes(ctypes.byref(rows(N=10 ** 6)), ctypes.byref(head(V=10 ** 6)), 7)
