@@ -51,6 +51,27 @@ __device__ inline f32x4 mma<float>(u32x4 b, u32x4 a, f32x4 c) {
   return c;
 }
 
+// float32 rows enter the matrix cores as three bf16 planes, x = h + m + l, each
+// the rounding of what the ones before it leave; of the nine products of two
+// such sums the six down to 2^-16 of the largest are taken
+constexpr int kPairs[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
+constexpr int planes(int es) { return es == 4 ? 3 : 1; }
+
+// 4 float32 -> 4 bf16 of each plane
+__device__ inline void split4(f32x4 v, u32x2* p) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const __bf16 t[4] = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    p[k] = __builtin_bit_cast(u32x2, t);
+    if (k < 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float r = v[e] - (float)t[e];
+        v[e] = __builtin_isfinite(v[e]) ? r : 0.f;  // an infinity or NaN stays in the first plane
+      }
+  }
+}
+
 template <typename T>
 __device__ inline void store4(T* p, f32x4 v) {
   T t[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};

@@ -40,6 +40,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gmm {
 
@@ -52,8 +53,9 @@ struct GemmArgs {
   const char* B;       // [N][K], row stride ldb bytes
   int64_t lda, ldb;
   int64_t M, N;
-  int kbytes;          // valid bytes of a row (a multiple of 16)
-  int ktiles, splits;  // 128-byte k-tiles, shared among splits
+  int64_t pa, pb;      // float32: bytes from one bf16 plane of an operand to the next
+  int kbytes;          // valid bytes of a row (of one plane), a multiple of 16
+  int ktiles, splits;  // 128-byte k-tiles (over all pairs of planes), shared among splits
   int tm, tn;          // tiles
   // LSE and GRAD: classes v0 .. v0 + N of the head
   const float* bias;   // (V) or null
@@ -64,8 +66,8 @@ struct GemmArgs {
   const float* lse;    // GRAD
   const float* coef;   // GRAD: g_i (0: the row takes no part)
   const float* scal;   // {multiplier of G, its inverse}; null: 1
-  char* G;             // GRAD: [M][ldg] rows' type
-  char* GT;            // GRAD: [N][ldgt], null: not wanted
+  char* G;             // GRAD: [M][ldg] 16-bit, [3] of them for float32
+  char* GT;            // GRAD: [N][ldgt] likewise, null: not wanted
   int64_t ldg, ldgt;   // elements, whole k-tiles
   float* dbp;          // GRAD: [tile m][N] column sums, null: not wanted
   // OUT
@@ -102,8 +104,11 @@ __device__ inline int label_at(const GemmArgs& P, int64_t m, int64_t n) {
 // other waves' too
 __device__ inline void next_tile() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <typename T, int BM, int BN, int WM, int WN, int MODE>
+// S: the rows' type; its matrix-core form is itself, or bf16 planes
+template <typename S, int BM, int BN, int WM, int WN, int MODE>
 __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
+  using T = std::conditional_t<sizeof(S) == 4, __bf16, S>;
+  constexpr int PL = planes(sizeof(S)), NP = PL == 1 ? 1 : 6;
   constexpr int NT = WM * WN * 64;          // threads
   constexpr int MT = BM / WM / 16, NN = BN / WN / 16;  // 16 x 16 tiles of a wave
   constexpr int JA = BM * 8 / NT, JB = BN * 8 / NT;    // 16-byte loads of a thread per k-tile
@@ -119,10 +124,6 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int mrows = (int)min((int64_t)BM, P.M - m0), nrows = (int)min((int64_t)BN, P.N - n0);
 
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<char*>(P.A) + m0 * P.lda, 0, (unsigned)((mrows - 1) * P.lda + P.kbytes), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<char*>(P.B) + n0 * P.ldb, 0, (unsigned)((nrows - 1) * P.ldb + P.kbytes), 0x00020000);
   const int kt0 = (int)((int64_t)P.ktiles * z / P.splits), kt1 = (int)((int64_t)P.ktiles * (z + 1) / P.splits);
   // load j of lane l: LDS row 8 (j * waves + wave) + l / 8, slot l % 8, which
   // holds the same chunk c for every j.  Rows past the operand's last have
@@ -131,12 +132,24 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
   const int row0 = 8 * wv + (lane >> 3), c16 = ((lane & 7) ^ ((row0 >> 1) & 7)) * 16;
   const unsigned oa = (unsigned)(row0 * P.lda) + c16, ob = (unsigned)(row0 * P.ldb) + c16;
   const unsigned sa = (unsigned)(8 * (NT / 64) * P.lda), sb = (unsigned)(8 * (NT / 64) * P.ldb);
-  const int kend = min(P.kbytes, kt1 * 128);  // bytes of a row that this split reads end here
+  // k-tiles are issued in order; the pairs of planes follow each other, the
+  // small products first
+  const int per = P.ktiles / NP;
+  int pair = NP - 1 - kt0 / per, kk = kt0 % per;
   auto issue = [&](lds_char* st, int kt) {
-    const unsigned kb = kt * 128;
+    const char *A = P.A + m0 * P.lda, *B = P.B + n0 * P.ldb;
+    if (PL > 1) {
+      A += kPairs[max(pair, 0)][0] * P.pa;
+      B += kPairs[max(pair, 0)][1] * P.pb;
+    }
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(A), 0, (unsigned)((mrows - 1) * P.lda + P.kbytes), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(B), 0, (unsigned)((nrows - 1) * P.ldb + P.kbytes), 0x00020000);
+    const unsigned kb = kk * 128;
     // past the last k the offset's top bit is set (added, not selected: a
     // select becomes branches around the loads)
-    const unsigned out = (int)kb + c16 < kend ? 0u : kOutside;
+    const unsigned out = kt < kt1 && (int)kb + c16 < P.kbytes ? 0u : kOutside;
     const unsigned xa = oa + out, xb = ob + out;
 #pragma unroll
     for (int j = 0; j < JA; ++j)
@@ -144,6 +157,10 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
 #pragma unroll
     for (int j = 0; j < JB; ++j)
       load_lds16(rb, st + BM * 128 + (j * (NT / 64) + wv) * 1024, xb + (kb + j * sb));
+    if (++kk == per) {
+      kk = 0;
+      --pair;
+    }
   };
 
   f32x4 acc[MT][NN];
@@ -231,13 +248,13 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
           continue;
         }
         v = dead ? f32x4{0.f, 0.f, 0.f, 0.f} : v * sc;
-        T* p = reinterpret_cast<T*>(P.out) + m * P.N + n;
+        S* p = reinterpret_cast<S*>(P.out) + m * P.N + n;
         if (vec && !P.accumulate) {
-          store4<T>(p, v);
+          store4<S>(p, v);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (n + e < P.N) p[e] = (T)(v[e] + (P.accumulate ? to_f32(p[e]) : 0.f));
+            if (n + e < P.N) p[e] = (S)(v[e] + (P.accumulate ? to_f32(p[e]) : 0.f));
         }
       }
     }
@@ -299,10 +316,13 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
       }
     } else {
       constexpr int kRegion = 16384;                       // bytes of LDS per wave
-      constexpr int SUB = kRegion / (NN * 16 * 16 * (int)sizeof(T)) < MT ? kRegion / (NN * 16 * 16 * (int)sizeof(T)) : MT;
-      constexpr int EPC = 16 / (int)sizeof(T);             // elements of a 16-byte chunk
+      constexpr int kSub = kRegion / (PL * NN * 16 * 16 * 2);
+      constexpr int SUB = kSub < MT ? kSub : MT;           // row blocks transposed at a time
+      constexpr int EPC = 8;                               // elements of a 16-byte chunk
       constexpr int CR = SUB * 16 / EPC, CL = 16 / EPC;    // chunks of a transposed row; of 16 elements
-      static_assert(MT % SUB == 0 && 4 * CL <= CR, "transposing in whole sub-tiles");
+      constexpr int kGPlane = NN * 16 * SUB * 16;          // elements of a plane in the region
+      static_assert(MT % SUB == 0, "transposing in whole sub-tiles");
+      const int64_t gp = P.M * P.ldg, tp = P.N * P.ldgt;   // elements of a plane of G and of its transpose
       static_assert(WM * WN * kRegion <= 2 * kStage, "the waves' regions fill the two stages");
       T* reg = reinterpret_cast<T*>((wv < WM * WN / 2 ? st0 : st1) + (wv % (WM * WN / 2)) * kRegion);
       const float mult = P.scal ? P.scal[0] : 1.f;
@@ -334,27 +354,27 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
             }
             const int64_t n = n0 + nw + 16 * j;
             const int ml = 16 * ii + lr, nl = 16 * j + 4 * lq;
-            if constexpr (sizeof(T) == 2) {
+            u32x2 w[3];
+            if constexpr (PL == 1) {
               const T t[4] = {(T)g[0], (T)g[1], (T)g[2], (T)g[3]};
-              const u32x2 w = __builtin_bit_cast(u32x2, t);
-              if (m < P.M && n < P.ldg) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + m * P.ldg + n) = w;
+              w[0] = __builtin_bit_cast(u32x2, t);
+            } else {
+              split4(g, w);
+            }
+#pragma unroll
+            for (int l = 0; l < PL; ++l) {
+              if (m < P.M && n < P.ldg) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + l * gp + m * P.ldg + n) = w[l];
               if (P.GT) {
                 // a dword holds two columns of one row; neighbouring rows' lanes
                 // trade, so that each writes two rows of one column
-                const int mp = ml & ~1, ch = (mp / EPC) ^ (CL * lq);  // rows 4 apart would share banks
+                const int mp = ml & ~1, ch = (mp / EPC) ^ ((CL * lq) & (CR - 1));  // rows 4 apart would share banks
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                  const unsigned o = __builtin_amdgcn_mov_dpp(w[u], 0xB1, 0xF, 0xF, true);  // quad_perm 1 0 3 2
-                  const unsigned v = __builtin_amdgcn_perm(o, w[u], pick);
-                  *reinterpret_cast<unsigned*>(reg + (nl + 2 * u + (lane & 1)) * (SUB * 16) + ch * EPC + mp % EPC) = v;
+                  const unsigned o = __builtin_amdgcn_mov_dpp(w[l][u], 0xB1, 0xF, 0xF, true);  // quad_perm 1 0 3 2
+                  const unsigned v = __builtin_amdgcn_perm(o, w[l][u], pick);
+                  *reinterpret_cast<unsigned*>(reg + l * kGPlane + (nl + 2 * u + (lane & 1)) * (SUB * 16) + ch * EPC +
+                                               mp % EPC) = v;
                 }
-              }
-            } else {
-              if (m < P.M && n < P.ldg) store4<T>(reinterpret_cast<T*>(P.G) + m * P.ldg + n, g);
-              if (P.GT) {
-                const int ch = (ml / EPC) ^ (CL * lq);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) reg[(nl + e) * (SUB * 16) + ch * EPC + ml % EPC] = (T)g[e];
               }
             }
             __builtin_amdgcn_sched_barrier(0);  // one 16 x 16 tile's temporaries at a time
@@ -363,12 +383,15 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
         if (P.GT) {
           __syncthreads();
 #pragma unroll
-          for (int t = 0; t < NN * 16 * CR / 64; ++t) {
-            const int idx = t * 64 + lane, nl = idx / CR, ch = idx % CR;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(reg + nl * (SUB * 16) + (ch ^ (CL * ((nl >> 2) & 3))) * EPC);
-            const int64_t n = n0 + wn * NN * 16 + nl, m = m0 + wm * MT * 16 + i0 * 16 + ch * EPC;
-            if (n < P.N && m < P.ldgt) *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + n * P.ldgt + m) = v;
-          }
+          for (int l = 0; l < PL; ++l)
+#pragma unroll
+            for (int t = 0; t < NN * 16 * CR / 64; ++t) {
+              const int idx = t * 64 + lane, nl = idx / CR, ch = idx % CR;
+              const u32x4 v = *reinterpret_cast<const u32x4*>(reg + l * kGPlane + nl * (SUB * 16) +
+                                                              (ch ^ ((CL * ((nl >> 2) & 3)) & (CR - 1))) * EPC);
+              const int64_t n = n0 + wn * NN * 16 + nl, m = m0 + wm * MT * 16 + i0 * 16 + ch * EPC;
+              if (n < P.N && m < P.ldgt) *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + l * tp + n * P.ldgt + m) = v;
+            }
           __syncthreads();
         }
       }
@@ -563,12 +586,12 @@ __global__ void __launch_bounds__(256) pack_kernel(RowsArgs R, T* dst, int Dp) {
   }
 }
 
-// rows of any layout -> [D][ldo], zeros past nr; rows with live = 0 become
-// zeros.  64 x 64 tiles, 16 bytes a thread in and out.
-template <typename T>
-__global__ void __launch_bounds__(256) transpose_kernel(RowsArgs R, const float* live, T* dst, int64_t ldo) {
-  constexpr int E = 16 / (int)sizeof(T), CR = 64 / E;  // elements of a chunk, chunks of a tile row
-  __shared__ __attribute__((aligned(16))) T tile[64][64 + E];
+// rows of any layout -> [D][ldo] 16-bit (float32: [3] planes of it), zeros past
+// nr; rows with live = 0 become zeros.  64 x 64 tiles, 16 bytes a thread in and out.
+template <typename S>
+__global__ void __launch_bounds__(256) transpose_kernel(RowsArgs R, const float* live, char* dst, int64_t ldo) {
+  constexpr int E = 16 / (int)sizeof(S), CR = 64 / E;  // elements of a chunk, chunks of a tile row
+  __shared__ __attribute__((aligned(16))) S tile[64][64 + E];
   const int64_t r0 = (int64_t)blockIdx.x * 64;
   const int d0 = blockIdx.y * 64;
 #pragma unroll
@@ -577,19 +600,31 @@ __global__ void __launch_bounds__(256) transpose_kernel(RowsArgs R, const float*
     const int64_t r = r0 + rr;
     u32x4 v = {0u, 0u, 0u, 0u};
     if (r < R.nr && !(live && live[r] == 0.f))
-      v = chunk_at<T>(R.x + row_offset(R, R.r0 + r) * (int64_t)sizeof(T), (d0 + c * E) * (int)sizeof(T),
-                      R.D * (int)sizeof(T));
+      v = chunk_at<S>(R.x + row_offset(R, R.r0 + r) * (int64_t)sizeof(S), (d0 + c * E) * (int)sizeof(S),
+                      R.D * (int)sizeof(S));
     *reinterpret_cast<u32x4*>(&tile[rr][c * E]) = v;
   }
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < 64 * CR / 256; ++u) {
-    const int i = threadIdx.x + 256 * u, d = i / CR, c = i % CR;
-    T v[E];
+  for (int u = 0; u < 2; ++u) {
+    const int i = threadIdx.x + 256 * u, d = i / 8, c = i % 8;
+    if (d0 + d >= R.D || r0 + c * 8 >= ldo) continue;  // ldo: whole k-tiles
+    char* p = dst + ((int64_t)(d0 + d) * ldo + r0 + c * 8) * 2;
+    if constexpr (sizeof(S) == 2) {
+      S v[8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = tile[c * E + e][d];
-    if (d0 + d < R.D && r0 + c * E < ldo)  // ldo: whole k-tiles
-      __builtin_memcpy(dst + (int64_t)(d0 + d) * ldo + r0 + c * E, v, 16);
+      for (int e = 0; e < 8; ++e) v[e] = tile[c * 8 + e][d];
+      __builtin_memcpy(p, v, 16);
+    } else {
+      u32x2 w[2][3];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        split4(f32x4{tile[c * 8 + 4 * h][d], tile[c * 8 + 4 * h + 1][d], tile[c * 8 + 4 * h + 2][d], tile[c * 8 + 4 * h + 3][d]},
+               w[h]);
+#pragma unroll
+      for (int l = 0; l < 3; ++l)
+        *reinterpret_cast<u32x4*>(p + l * R.D * ldo * 2) = u32x4{w[0][l][0], w[0][l][1], w[1][l][0], w[1][l][1]};
+    }
   }
 }
 
@@ -683,27 +718,26 @@ static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 // what a call does and where its parts of the workspace lie
 XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db) {
   XentPlan p{};
-  const int64_t es = a.es, kt = 128 / es;
-  p.kbytes = (int)(up(a.D * es, 16));
+  const int64_t es = a.es, kt = 64;
+  const int64_t pl = es == 4 ? 3 : 1;  // 16-bit planes of an element
+  p.kbytes = (int)up(a.D * 2, 16);
   const bool aligned_x = ((uintptr_t)a.x | (uintptr_t)(a.ld * es)) % 16 == 0 && (a.D * es) % 16 == 0 &&
                          a.ld * es * 256 < ((int64_t)1 << 31) && (a.B == 1 || a.stride_b == a.N * a.ld);
   const bool aligned_w = ((uintptr_t)a.w | (uintptr_t)(a.ld_w * es)) % 16 == 0 && (a.D * es) % 16 == 0 &&
                          a.ld_w * es * 256 < ((int64_t)1 << 31);
-  p.pack_x = !aligned_x;
-  p.pack_w = !aligned_w;
-  p.Dp = up(a.D, 16 / es);
+  p.pack_x = !aligned_x || es == 4;
+  p.pack_w = !aligned_w || es == 4;
+  p.Dp = up(a.D, 8);
   const int64_t R = std::max<int64_t>(a.B * a.N, 1), V = a.V;
   size_t o = 0;
   p.small = a.D <= 128 && R > 64;
   if (p.small) {
     // rows stream past in chunks only where they are copied to aligned rows
     // first (float32: as planes), classes likewise
-    const bool split = es == 4;  // copied as bf16 planes
-    p.pack_x = (p.pack_x || split) && grad && (want_dw || want_db);
-    p.pack_w = (p.pack_w || split) && (!grad || want_dx);
+    p.pack_x = p.pack_x && grad && (want_dw || want_db);
+    p.pack_w = p.pack_w && (!grad || want_dx);
     p.nc = p.pack_x ? std::min<int64_t>(R, 1 << 20) : R;
     p.vc = p.pack_w ? std::min<int64_t>(V, 1 << 18) : V;
-    p.Dp = up(a.D, 8);
     p.np_r = (R + p.nc - 1) / p.nc;
     p.np_v = (V + p.vc - 1) / p.vc;
     p.lds = up(a.D, 4);
@@ -760,25 +794,24 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     p.off_coef = o; o = upz(o + sizeof(float) * (size_t)R);
     p.off_bmax = o; o = upz(o + sizeof(float) * 1024);
     p.off_scal = o; o = upz(o + sizeof(float) * 2);
-    p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * es));
+    p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * 2 * pl));
     if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
     if (want_dx) {
-      p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * es));
-      p.split_x = split_k(mc, a.D, p.ldg / kt);
+      p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * 2 * pl));
+      p.split_x = split_k(mc, a.D, p.ldg / kt * (pl == 1 ? 1 : 6));
       p.slab_x = p.split_x > 1 || p.np_v > 1;
       if (p.slab_x) { p.off_sx = o; o = upz(o + sizeof(float) * (size_t)(p.split_x * R * p.lds)); }
     }
     if (want_dw) {
-      p.off_GT = o; o = upz(o + (size_t)(vcc * p.ldgt * es));
-      p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * es));
-      p.split_w = split_k(vcc, a.D, p.ldgt / kt);
+      p.off_GT = o; o = upz(o + (size_t)(vcc * p.ldgt * 2 * pl));
+      p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * 2 * pl));
+      p.split_w = split_k(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6));
       p.slab_w = p.split_w > 1 || p.np_r > 1;
       if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
     }
   }
-  const int64_t pes = p.small ? (es == 4 ? 6 : 2) : es;  // bytes of a copied element
-  if (p.pack_x) { p.off_px = o; o = upz(o + (size_t)(std::min(p.nc, R) * p.Dp * pes)); }
-  if (p.pack_w) { p.off_pw = o; o = upz(o + (size_t)(std::min(p.vc, V) * p.Dp * pes)); }
+  if (p.pack_x) { p.off_px = o; o = upz(o + (size_t)(std::min(p.nc, R) * p.Dp * 2 * pl)); }
+  if (p.pack_w) { p.off_pw = o; o = upz(o + (size_t)(std::min(p.vc, V) * p.Dp * 2 * pl)); }
   p.bytes = o;
   return p;
 }
@@ -804,8 +837,10 @@ hipError_t finish(const float* slab, int splits, int64_t stride, int64_t lds, in
                        reinterpret_cast<T*>(out), accumulate);
   return hipGetLastError();
 }
+// rows copied to aligned ones of Dp 16-bit elements (float32: as planes)
 template <typename T>
 hipError_t pack(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s) {
+  if constexpr (sizeof(T) == 4) return launch_xent_split(r, dst, Dp, s);
   hipLaunchKernelGGL((pack_kernel<T>), dim3(blocks(r.nr * Dp * (int64_t)sizeof(T) / 16, 1 << 16)), dim3(256), 0, s, r,
                      reinterpret_cast<T*>(dst), (int)Dp);
   return hipGetLastError();
@@ -813,7 +848,7 @@ hipError_t pack(const RowsArgs& r, char* dst, int64_t Dp, hipStream_t s) {
 template <typename T>
 hipError_t transpose(const RowsArgs& r, const float* live, char* dst, int64_t ldo, hipStream_t s) {
   const dim3 grid((unsigned)((ldo + 63) / 64), (unsigned)((r.D + 63) / 64));
-  hipLaunchKernelGGL((transpose_kernel<T>), grid, dim3(256), 0, s, r, live, reinterpret_cast<T*>(dst), ldo);
+  hipLaunchKernelGGL((transpose_kernel<T>), grid, dim3(256), 0, s, r, live, dst, ldo);
   return hipGetLastError();
 }
 
@@ -828,7 +863,8 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
       GMM_TRY(pack<T>(r, ws + p.off_px, p.Dp, s));
     }
     P.A = ws + p.off_px;
-    P.lda = p.Dp * es;
+    P.lda = p.Dp * 2;
+    P.pa = nr * p.Dp * 2;
   } else {
     P.A = (const char*)a.x + r0 * a.ld * es;
     P.lda = a.ld * es;
@@ -839,7 +875,8 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
       GMM_TRY(pack<T>(r, ws + p.off_pw, p.Dp, s));
     }
     P.B = ws + p.off_pw;
-    P.ldb = p.Dp * es;
+    P.ldb = p.Dp * 2;
+    P.pb = nv * p.Dp * 2;
   } else {
     P.B = (const char*)a.w + v0 * a.ld_w * es;
     P.ldb = a.ld_w * es;
@@ -847,7 +884,7 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
   P.M = nr;
   P.N = nv;
   P.kbytes = p.kbytes;
-  P.ktiles = (p.kbytes + 127) / 128;
+  P.ktiles = (p.kbytes + 127) / 128 * (sizeof(T) == 4 ? 6 : 1);
   P.splits = 1;
   P.bias = a.bias;
   P.labels = a.labels + r0;
@@ -858,8 +895,7 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
 // ---- rows of at most 128 features (gmm_xent_small.hip)
 template <typename T>
 hipError_t copy_stream(const RowsArgs& r, char* dst, int64_t Dp, SmallArgs& P, hipStream_t s) {
-  if constexpr (sizeof(T) == 4) GMM_TRY(launch_xent_split(r, dst, Dp, s));
-  else GMM_TRY(pack<T>(r, dst, Dp, s));
+  GMM_TRY(pack<T>(r, dst, Dp, s));
   P.stream = dst;
   P.ld_stream = Dp * 2;
   P.plane = r.nr * Dp * 2;
@@ -1023,7 +1059,8 @@ hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse
 template <typename T>
 hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, const float* gloss, char* dx, char* dw,
                     float* db, int accumulate, char* ws, hipStream_t s) {
-  const int64_t R = a.B * a.N, es = sizeof(T), kt = 128 / es;
+  const int64_t R = a.B * a.N, es = sizeof(T), kt = 64;
+  const int pairs = es == 4 ? 6 : 1;
   float* coef = reinterpret_cast<float*>(ws + p.off_coef);
   float* bmax = reinterpret_cast<float*>(ws + p.off_bmax);
   float* scal = nullptr;
@@ -1063,13 +1100,15 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       if (dx) {  // dX of the chunk += G W of the piece
         GemmArgs Q{};
         Q.A = P.G;
-        Q.lda = P.ldg * es;
+        Q.lda = P.ldg * 2;
+        Q.pa = nr * P.ldg * 2;
         Q.B = ws + p.off_WT;
-        Q.ldb = P.ldg * es;
+        Q.ldb = P.ldg * 2;
+        Q.pb = a.D * P.ldg * 2;
         Q.M = nr;
         Q.N = a.D;
-        Q.kbytes = (int)(P.ldg * es);
-        Q.ktiles = (int)(P.ldg / kt);
+        Q.kbytes = (int)(P.ldg * 2);
+        Q.ktiles = (int)(P.ldg / kt) * pairs;
         Q.splits = std::min<int>(p.split_x, Q.ktiles);
         Q.scal = scal;
         Q.rowlive = coef + r0;
@@ -1092,13 +1131,15 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
         if (p.np_r > 1 || v0 == 0) GMM_TRY(transpose<T>(r, coef + r0, ws + p.off_XT, P.ldgt, s));
         GemmArgs Q{};
         Q.A = P.GT;
-        Q.lda = P.ldgt * es;
+        Q.lda = P.ldgt * 2;
+        Q.pa = nv * P.ldgt * 2;
         Q.B = ws + p.off_XT;
-        Q.ldb = P.ldgt * es;
+        Q.ldb = P.ldgt * 2;
+        Q.pb = a.D * P.ldgt * 2;
         Q.M = nv;
         Q.N = a.D;
-        Q.kbytes = (int)(P.ldgt * es);
-        Q.ktiles = (int)(P.ldgt / kt);
+        Q.kbytes = (int)(P.ldgt * 2);
+        Q.ktiles = (int)(P.ldgt / kt) * pairs;
         Q.splits = p.split_w;
         Q.scal = scal;
         Q.out = dw + v0 * a.D * es;

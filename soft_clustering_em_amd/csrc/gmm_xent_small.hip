@@ -46,28 +46,8 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
-// float32 rows enter the matrix cores as three bf16 planes, x = h + m + l, each
-// the rounding of what the ones before it leave; of the nine products of two
-// such sums the six down to 2^-16 of the largest are taken
-constexpr int kPairs[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
-constexpr int planes(int es) { return es == 4 ? 3 : 1; }
 // streamed rows per tile
 constexpr int tile_rows(int es, int dp) { return es == 4 && dp == 128 ? 32 : 64; }
-
-// 4 float32 -> 4 bf16 of each plane
-__device__ inline void split4(f32x4 v, u32x2* p) {
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const __bf16 t[4] = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-    p[k] = __builtin_bit_cast(u32x2, t);
-    if (k < 2)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float r = v[e] - (float)t[e];
-        v[e] = __builtin_isfinite(v[e]) ? r : 0.f;  // an infinity or NaN stays in the first plane
-      }
-  }
-}
 
 // rows of any layout -> [3][nr][Dp] bf16 planes, zeros past D; a thread per 4 elements
 __global__ void __launch_bounds__(256) split_kernel(RowsArgs R, char* dst, int Dp) {
