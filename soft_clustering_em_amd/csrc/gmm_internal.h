@@ -294,6 +294,7 @@ struct XentPlan {
   bool small, skinny;            // at most 128 features (gmm_xent_small.hip); few rows
   bool pack_x, pack_w;           // rows / head copied to aligned rows first
   bool slab_x, slab_w;           // products summed in float32 slabs
+  bool big_x, big_w;             // products in 256 x 256 tiles
   int kbytes, split_x, split_w;
   int64_t Dp, nc, vc;            // padded D of the copies; rows of a chunk, classes of a piece
   int64_t np_r, np_v, ldg, ldgt, lds;

@@ -698,15 +698,37 @@ hipError_t launch_gemm(GemmArgs& P, bool big, hipStream_t s) {
 }
 
 int64_t tiles(int64_t M, int64_t N, int bt) { return ((M + bt - 1) / bt) * ((N + bt - 1) / bt); }
-// 256 x 256 tiles where they fill the card's compute units at least once
-bool big_tiles(int64_t M, int64_t N) { return tiles(M, N, 256) >= kNumCU; }
-// parts of the k axis that bring a product of few tiles to two workgroups per
-// compute unit, each part 8 k-tiles or longer
-int split_k(int64_t M, int64_t N, int64_t ktiles) {
-  const int64_t t = tiles(M, N, big_tiles(M, N) ? 256 : 128);
-  int64_t sp = t >= kNumCU ? 1 : (2 * kNumCU) / t;
-  sp = std::min<int64_t>(sp, ktiles / 8);
-  return (int)std::max<int64_t>(sp, 1);
+// Tile size and parts of the k axis for a product, by what they would cost in
+// multiply-adds of one compute unit: a unit runs one 256 x 256 workgroup at
+// full rate, two 128 x 128 at 0.95 of it, one alone at half; a workgroup's start
+// and end cost about 256 (512) of k; a part's float32 slab about 4 a value
+// (written and read at the memory's rate).  Parts are 8 k-tiles or longer.
+// Measured: 4096 x 1024 over 98304 (float32, six pairs of planes), 256
+// workgroups of 128 x 128 1475 us, 64 of 256 x 256 in 4 parts 647; 1000 x 50001
+// over 1024, 3128 tiles of 128 x 128 158 us, 784 of 256 x 256 138.
+struct Tiling {
+  bool big;
+  int splits;
+};
+Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts) {
+  Tiling best{true, 1};
+  double least = 1e300;
+  for (int big = 1; big >= 0; --big) {
+    const int64_t t = tiles(M, N, big ? 256 : 128);
+    for (int64_t s = 1; s == 1 || (parts && s <= ktiles / 8 && s <= 32); ++s) {
+      const int64_t wg = t * s;
+      const double k = 64.0 * (double)((ktiles + s - 1) / s) + (big ? 256.0 : 512.0);
+      const double rounds = big ? (double)((wg + kNumCU - 1) / kNumCU) * 65536.0
+                            : wg <= kNumCU ? 16384.0 / 0.5
+                                           : (double)((wg + 2 * kNumCU - 1) / (2 * kNumCU)) * 2 * 16384.0 / 0.95;
+      const double cost = rounds * k + (s > 1 ? 4.0 * (double)s * (double)M * (double)N : 0.0);
+      if (cost < least) {
+        least = cost;
+        best = Tiling{big != 0, (int)s};
+      }
+    }
+  }
+  return best;
 }
 unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64_t>(1, std::min((n + 255) / 256, cap)); }
 
@@ -798,14 +820,18 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
     if (want_dx) {
       p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * 2 * pl));
-      p.split_x = split_k(mc, a.D, p.ldg / kt * (pl == 1 ? 1 : 6));
+      const Tiling t = tiling(mc, a.D, p.ldg / kt * (pl == 1 ? 1 : 6), true);
+      p.split_x = t.splits;
+      p.big_x = t.big;
       p.slab_x = p.split_x > 1 || p.np_v > 1;
       if (p.slab_x) { p.off_sx = o; o = upz(o + sizeof(float) * (size_t)(p.split_x * R * p.lds)); }
     }
     if (want_dw) {
       p.off_GT = o; o = upz(o + (size_t)(vcc * p.ldgt * 2 * pl));
       p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * 2 * pl));
-      p.split_w = split_k(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6));
+      const Tiling t = tiling(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6), true);
+      p.split_w = t.splits;
+      p.big_w = t.big;
       p.slab_w = p.split_w > 1 || p.np_r > 1;
       if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
     }
@@ -1047,7 +1073,7 @@ hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse
         GMM_TRY(hipGetLastError());
         nt += grid.x;
       } else {
-        GMM_TRY((launch_gemm<T, LSE>(P, big_tiles(nr, nv), s)));
+        GMM_TRY((launch_gemm<T, LSE>(P, tiling(nr, nv, P.ktiles, false).big, s)));
         nt += P.tn;
       }
     }
@@ -1091,7 +1117,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       P.GT = dw ? ws + p.off_GT : nullptr;
       P.ldgt = up(nr, kt);
       P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
-      GMM_TRY((launch_gemm<T, GRAD>(P, big_tiles(nr, nv), s)));
+      GMM_TRY((launch_gemm<T, GRAD>(P, tiling(nr, nv, P.ktiles, false).big, s)));
       if (db) {
         hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((nv + 15) / 16)), dim3(256), 0, s, P.dbp, P.tm, nv, scal, db + v0,
                            accumulate || r0 > 0);
@@ -1121,7 +1147,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
           Q.slab_stride = R * p.lds;
           Q.add = v0 > 0;
         }
-        GMM_TRY((launch_gemm<T, OUT>(Q, big_tiles(nr, a.D), s)));
+        GMM_TRY((launch_gemm<T, OUT>(Q, p.big_x, s)));
         if (p.slab_x && v0 + nv >= a.V) {
           GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nr, a.D, scal, coef + r0, Q.out, accumulate, s));
         }
@@ -1150,7 +1176,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
           Q.slab_stride = std::min(p.vc, a.V) * p.lds;
           Q.add = r0 > 0;
         }
-        GMM_TRY((launch_gemm<T, OUT>(Q, big_tiles(nv, a.D), s)));
+        GMM_TRY((launch_gemm<T, OUT>(Q, p.big_w, s)));
         if (p.slab_w && r0 + nr >= R) {
           GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nv, a.D, scal, nullptr, Q.out, accumulate, s));
         }
