@@ -38,7 +38,8 @@
  *     per-row candidate lists with LDS atomic counters (top-m: the waves of a
  *     workgroup; kernel density: the 16 lanes of one row); the lists are
  *     sorted by (score, index), or walked in increasing index order, before
- *     any result depends on them, so the slot order never shows.
+ *     any result depends on them, so the slot order never shows.  The codebook
+ *     gradient's sort counts with LDS atomics (a count has no order).
  *   - Calls on distinct streams with distinct workspaces may run concurrently.
  */
 #ifndef GMM_H

@@ -13,15 +13,19 @@
 //   lookup   a thread per 16 bytes of a row; the row's codes are read by every
 //            thread of the row (one address, the L1 serves it).
 //   dw       a group of up to 64 lanes per row, the dot products over it.
-//   dT       deterministic, no atomics: the entries are sorted by code (a
-//            stable radix sort of at most 10 bits a pass: block histograms,
-//            their prefixes, ranks by ballot), then summed in that order in
+//   dT       deterministic, no global atomics: the entries are sorted by code
+//            (up to 8192 entries by ranks in one launch; above by a stable
+//            radix sort of at most 10 bits a pass: block histograms, their
+//            prefixes, ranks by ballot), then summed in that order in
 //            chunks of entries.  A run of one code inside a chunk is written
 //            at once; a run that crosses a chunk's ends leaves partial sums,
 //            which a last kernel joins, so that a code with most of the
 //            entries is summed by as many workgroups as many codes are.
 // Bound by memory: every dout row is read once per entry, every dT row
-// written once.
+// written once.  1M x 128, 4 codes a row of 4096, float32: lookup 114 us (4.8
+// TB/s).  262144 x 128, 4 codes of 4096, float32: dw 54 us, sort 57, sums 65
+// (8.3 TB/s out of the caches), joins 13.  32768 x 2048 into 65536 codes, bf16:
+// sort and zeros 64 us, sums 61 (rows in random order), joins 11.
 #include "gmm_internal.h"
 
 #include <hip/hip_runtime.h>

@@ -28,7 +28,15 @@
 // carry their own bounds: a row or k-chunk outside the operand has an offset
 // past the resource's end and arrives as zeros.  A row's 16-byte chunk c sits
 // in slot c ^ f(row) of its LDS row, so the fragment reads of 16 rows touch
-// all 64 banks.
+// all 64 banks.  Each quarter of a k-tile is multiplied from registers that the
+// quarter before it read.  Bound by the matrix cores: 4096 x 4096 rows, 65536
+// classes, bf16: LSE 1.76 ms (1.25 PFLOP/s), GRAD 2.14 (1.03; its epilogue adds
+// 0.2), G W and G^T X 1.85 each (1.19).
+//
+// float32 rows enter as three bf16 planes (kPairs), packed on the way in: six
+// products of planes follow each other along k, the smallest first.  4096 x 4096
+// rows, 16384 classes: loss 2.53 ms, loss and gradients 10.6 (the float32
+// instruction: 3.79 and 15.3).
 //
 // Rounding.  Accumulators, maxima, sums, G and the bias gradient are float32;
 // G is rounded once to the rows' type to enter the matrix cores (2^-9 of each
@@ -424,6 +432,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
 // bound by reading W once.  A wave owns 16 classes and walks their rows of W
 // from global memory into MFMA fragments (no LDS: nothing is shared); the
 // rows' fragments come from the L1.  One (max, sum) per row and 64 classes.
+// 1 x 2048 under 32768 classes, bf16: 24.8 us, 5.4 TB/s of W.
 template <typename T, int MT>
 __global__ void __launch_bounds__(256) skinny_kernel(GemmArgs P, RowsArgs R) {
   constexpr int U = 8;  // k-steps of 64 bytes in flight
@@ -488,7 +497,8 @@ __global__ void __launch_bounds__(256) skinny_kernel(GemmArgs P, RowsArgs R) {
   }
 }
 
-// Joins the tiles' (max, sum): RB rows per workgroup, 256 / RB threads a row.
+// Joins the tiles' (max, sum): RB rows per workgroup, 256 / RB threads a row,
+// so that few rows with many tiles wait for few loads (latency: 3.9 to 5.5 us).
 template <int RB>
 __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t ntiles, int64_t M, const int32_t* labels,
                                                    int64_t V, const float* lab, float* loss, float* lse) {
@@ -572,7 +582,8 @@ __global__ void __launch_bounds__(64) scal_kernel(const float* bmax, int n, floa
   }
 }
 
-// rows of any layout -> [nr][Dp], zeros past D; a thread per 16 bytes
+// rows of any layout -> [nr][Dp], zeros past D; a thread per 16 bytes.  Only
+// for rows that the GEMM's 16-byte loads cannot take (10007 x 515 half: 5.8 us).
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(RowsArgs R, T* dst, int Dp) {
   constexpr int E = 16 / (int)sizeof(T);
@@ -587,7 +598,8 @@ __global__ void __launch_bounds__(256) pack_kernel(RowsArgs R, T* dst, int Dp) {
 }
 
 // rows of any layout -> [D][ldo] 16-bit (float32: [3] planes of it), zeros past
-// nr; rows with live = 0 become zeros.  64 x 64 tiles, 16 bytes a thread in and out.
+// nr; rows with live = 0 become zeros.  64 x 64 tiles, 16 bytes a thread in and
+// out; bound by memory (32768 x 4096 bf16 twice read and written in 219 us, 4.9 TB/s).
 template <typename S>
 __global__ void __launch_bounds__(256) transpose_kernel(RowsArgs R, const float* live, char* dst, int64_t ldo) {
   constexpr int E = 16 / (int)sizeof(S), CR = 64 / E;  // elements of a chunk, chunks of a tile row
