@@ -294,11 +294,13 @@ struct XentPlan {
   bool small, skinny;            // at most 128 features (gmm_xent_small.hip); few rows
   bool pack_x, pack_w;           // rows / head copied to aligned rows first
   bool slab_x, slab_w;           // products summed in float32 slabs
-  bool big_x, big_w;             // products in 256 x 256 tiles
+  bool big_x, big_w, big_l;      // products in 256 x 256 tiles
   int kbytes, split_x, split_w;
+  int split_l;                   // parts of the logits' k axis (slabs), 0 or 1: none
+  int64_t ldl;                   // row of such a slab
   int64_t Dp, nc, vc;            // padded D of the copies; rows of a chunk, classes of a piece
   int64_t np_r, np_v, ldg, ldgt, lds;
-  size_t off_part, off_lab, off_coef, off_bmax, off_scal, off_G, off_GT, off_XT, off_WT, off_dbp, off_sx, off_sw, off_px,
+  size_t off_part, off_lab, off_coef, off_bmax, off_scal, off_G, off_GT, off_XT, off_WT, off_dbp, off_sx, off_sw, off_sl, off_px,
       off_pw, bytes;
 };
 XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db);

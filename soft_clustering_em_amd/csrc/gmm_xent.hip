@@ -16,7 +16,9 @@
 //         row, and the label's logit; a small kernel joins the tiles;
 //   GRAD  rows x classes of one piece: the logits again, turned into G in the
 //         accumulators; G and its transpose are written in the rows' type;
-//   OUT   the products G W and G^T X over such a piece.
+//   OUT   the products G W and G^T X over such a piece;
+// few tiles over a long k run as OUT too, in parts of k side by side, and two
+// small kernels do the other epilogues from the parts' sum (logit_parts).
 // A piece is at most 2^27 (float32: 2^26) elements of G, whatever N and V.
 // Recomputing the logits costs a third more arithmetic than keeping them and
 // takes their N V floats out of memory.  W and X enter the OUT products
@@ -698,6 +700,128 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* dbp, int tm, in
   }
 }
 
+// Few tiles over a long k (its parts side by side in float32 slabs, as the OUT
+// products write them): what the LSE and GRAD epilogues do, from the slabs.
+// Bound by the slabs' bytes and the launch.
+
+// the slabs' sum of 4 logits and their biases, -inf past the last class
+__device__ inline f32x4 logits_at(const GemmArgs& P, int64_t m, int64_t n) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  const float* p = P.slab + m * P.lds + n;
+#pragma unroll 4
+  for (int z = 0; z < P.splits; ++z) v += *reinterpret_cast<const f32x4*>(p + z * P.slab_stride);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = n + e < P.N ? v[e] + (P.bias ? P.bias[P.v0 + n + e] : 0.f) : -INFINITY;
+  return v;
+}
+
+// one wave per row and kRowSpan classes: their (max, sum), and the label's logit
+constexpr int kRowSpan = 512;
+__global__ void __launch_bounds__(256) slab_lse_kernel(GemmArgs P) {
+  const int lane = threadIdx.x & 63;
+  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (m >= P.M) return;
+  const int64_t n0 = (int64_t)blockIdx.y * kRowSpan;
+  const int y = label_at(P, m, n0);
+  f32x4 v[kRowSpan / 256];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kRowSpan / 256; ++u) {
+    const int c = 256 * u + 4 * lane;
+    v[u] = n0 + c < P.N ? logits_at(P, m, n0 + c) : f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      mx = fmaxf(mx, v[u][e]);
+      if (y == c + e && n0 + c + e < P.N) P.lab[m] = v[u][e];
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d));
+  const float base = mx == -INFINITY ? 0.f : mx;
+  float t = 0.f;
+#pragma unroll
+  for (int u = 0; u < kRowSpan / 256; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t += __builtin_amdgcn_exp2f((v[u][e] - base) * kLog2e);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) t += __shfl_xor(t, d);
+  if (lane == 0) P.part[(int64_t)blockIdx.y * P.M + m] = make_float2(mx, t);
+}
+
+// G and its transpose, 128 rows x 64 classes a workgroup (the column sums' row
+// tiles), 64 x 64 at a time; a thread holds 4 classes of every 16th row
+template <typename S>
+__global__ void __launch_bounds__(256) slab_grad_kernel(GemmArgs P) {
+  using T = std::conditional_t<sizeof(S) == 4, __bf16, S>;
+  constexpr int PL = planes(sizeof(S)), kRow = 72;  // elements of a transposed row in LDS: 64 and 16 bytes
+  __shared__ __attribute__((aligned(16))) T tile[PL][64][kRow];
+  __shared__ float red[16][64];
+  const int tid = threadIdx.x, c = (tid & 15) * 4, r = tid >> 4;
+  const int64_t n0 = (int64_t)blockIdx.y * 64;
+  const int64_t gp = P.M * P.ldg, tp = P.N * P.ldgt;
+  const float mult = P.scal ? P.scal[0] : 1.f;
+  f32x4 cs = {0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < 2; ++h) {
+    const int64_t m0 = (int64_t)blockIdx.x * 128 + 64 * h;
+    if (m0 >= P.M) break;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int ml = 16 * u + r;
+      const int64_t m = m0 + ml, n = n0 + c;
+      f32x4 g = {0.f, 0.f, 0.f, 0.f};
+      const float co = m < P.M ? P.coef[m] : 0.f;
+      if (co != 0.f && n < P.N) {  // NaN is live
+        const float ls = P.lse[m], cm = co * mult;
+        const int y = label_at(P, m, n);
+        const f32x4 v = logits_at(P, m, n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          g[e] = n + e < P.N ? cm * (__builtin_amdgcn_exp2f((v[e] - ls) * kLog2e) - (y == e ? 1.f : 0.f)) : 0.f;
+      }
+      cs += g;
+      u32x2 w[3];
+      if constexpr (PL == 1) {
+        const T t[4] = {(T)g[0], (T)g[1], (T)g[2], (T)g[3]};
+        w[0] = __builtin_bit_cast(u32x2, t);
+      } else {
+        split4(g, w);
+      }
+#pragma unroll
+      for (int l = 0; l < PL; ++l) {
+        if (m < P.M) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + l * gp + m * P.ldg + n) = w[l];
+        T t[4];
+        __builtin_memcpy(t, &w[l], 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tile[l][c + e][ml] = t[e];
+      }
+    }
+    __syncthreads();
+    if (P.GT) {
+#pragma unroll
+      for (int l = 0; l < PL; ++l)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int i = tid + 256 * u, nl = i / 8, ch = i % 8;
+          if (n0 + nl < P.N)
+            *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + l * tp + (n0 + nl) * P.ldgt + m0 + ch * 8) =
+                *reinterpret_cast<const u32x4*>(&tile[l][nl][ch * 8]);
+        }
+    }
+    __syncthreads();
+  }
+  if (P.dbp) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[r][c + e] = cs[e];
+    __syncthreads();
+    if (tid < 64 && n0 + tid < P.N) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += red[k][tid];
+      P.dbp[(int64_t)blockIdx.x * P.N + n0 + tid] = v;
+    }
+  }
+}
+
 template <typename T, int MODE>
 hipError_t launch_gemm(GemmArgs& P, bool big, hipStream_t s) {
   const int bt = big ? 256 : 128;
@@ -714,7 +838,8 @@ int64_t tiles(int64_t M, int64_t N, int bt) { return ((M + bt - 1) / bt) * ((N +
 // multiply-adds of one compute unit: a unit runs one 256 x 256 workgroup at
 // full rate, two 128 x 128 at 0.95 of it, one alone at half; a workgroup's start
 // and end cost about 256 (512) of k; a part's float32 slab about 4 a value
-// (written and read at the memory's rate).  Parts are 8 k-tiles or longer.
+// (written and read at the memory's rate), a launch for the parts' sum `apart`.
+// Parts are 8 k-tiles or longer.
 // Measured: 4096 x 1024 over 98304 (float32, six pairs of planes), 256
 // workgroups of 128 x 128 1475 us, 64 of 256 x 256 in 4 parts 647; 1000 x 50001
 // over 1024, 3128 tiles of 128 x 128 158 us, 784 of 256 x 256 138.
@@ -722,7 +847,7 @@ struct Tiling {
   bool big;
   int splits;
 };
-Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts) {
+Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts, double apart = 0.0) {
   Tiling best{true, 1};
   double least = 1e300;
   for (int big = 1; big >= 0; --big) {
@@ -733,7 +858,7 @@ Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts) {
       const double rounds = big ? (double)((wg + kNumCU - 1) / kNumCU) * 65536.0
                             : wg <= kNumCU ? 16384.0 / 0.5
                                            : (double)((wg + 2 * kNumCU - 1) / (2 * kNumCU)) * 2 * 16384.0 / 0.95;
-      const double cost = rounds * k + (s > 1 ? 4.0 * (double)s * (double)M * (double)N : 0.0);
+      const double cost = rounds * k + (s > 1 ? apart + 4.0 * (double)s * (double)M * (double)N : 0.0);
       if (cost < least) {
         least = cost;
         best = Tiling{big != 0, (int)s};
@@ -745,6 +870,17 @@ Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts) {
 unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64_t>(1, std::min((n + 255) / 256, cap)); }
 
 }  // namespace
+
+// the logits' parts: G or the (max, sum) pairs from slabs take a launch of about
+// 4 us more, at 4.9e6 multiply-adds of a compute unit a us.
+// Measured, loss and gradients: 871 x 2563 rows, 517 classes, float32, 35 tiles
+// of 128 x 128 whole 571 us, in parts 204; 500 x 4096, 1000 classes, bf16, 138
+// and 107; loss of 300 x 4000, 10 classes, float32, 226 and 39.
+static int logit_parts(int64_t M, int64_t N, int64_t ktiles, bool& big) {
+  const Tiling t = tiling(M, N, ktiles, true, 2e7);
+  big = t.big;
+  return t.splits;
+}
 
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -807,6 +943,12 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     const int64_t nt = (V + per - 1) / per + V / p.vc + 1;
     p.nc = std::min<int64_t>(R, std::max<int64_t>(256, ((int64_t)1 << 24) / nt / 256 * 256));
     p.off_part = o; o = upz(o + sizeof(float2) * (size_t)(nt * p.nc));
+    if (!p.skinny) {
+      const int64_t mc = std::min(p.nc, R), vcc = std::min(p.vc, V);
+      p.ldl = up(vcc, 4);
+      p.split_l = logit_parts(mc, vcc, (p.kbytes + 127) / 128 * (pl == 1 ? 1 : 6), p.big_l);
+      if (p.split_l > 1) { p.off_sl = o; o = upz(o + sizeof(float) * (size_t)(p.split_l * mc * p.ldl)); }
+    }
     p.off_lab = o;  o = upz(o + sizeof(float) * (size_t)p.nc);
   } else {
     const int64_t cap = (int64_t)1 << (es == 2 ? 27 : 26);
@@ -829,6 +971,9 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     p.off_bmax = o; o = upz(o + sizeof(float) * 1024);
     p.off_scal = o; o = upz(o + sizeof(float) * 2);
     p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * 2 * pl));
+    p.ldl = up(vcc, 4);
+    p.split_l = logit_parts(mc, vcc, (p.kbytes + 127) / 128 * (pl == 1 ? 1 : 6), p.big_l);
+    if (p.split_l > 1) { p.off_sl = o; o = upz(o + sizeof(float) * (size_t)(p.split_l * mc * p.ldl)); }
     if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
     if (want_dx) {
       p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * 2 * pl));
@@ -928,6 +1073,16 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
   P.labels = a.labels + r0;
   P.v0 = v0;
   return hipSuccess;
+}
+
+// the logits' product in parts, side by side in slabs
+template <typename T>
+hipError_t logit_slabs(const XentPlan& p, char* ws, GemmArgs& P, hipStream_t s) {
+  P.splits = p.split_l;
+  P.slab = reinterpret_cast<float*>(ws + p.off_sl);
+  P.lds = p.ldl;
+  P.slab_stride = P.M * p.ldl;
+  return launch_gemm<T, OUT>(P, p.big_l, s);
 }
 
 // ---- rows of at most 128 features (gmm_xent_small.hip)
@@ -1084,6 +1239,12 @@ hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse
         else hipLaunchKernelGGL((skinny_kernel<T, 4>), grid, dim3(256), 0, s, P, x);
         GMM_TRY(hipGetLastError());
         nt += grid.x;
+      } else if (p.split_l > 1) {
+        GMM_TRY(logit_slabs<T>(p, ws, P, s));
+        const dim3 grid((unsigned)((nr + 3) / 4), (unsigned)((nv + kRowSpan - 1) / kRowSpan));
+        hipLaunchKernelGGL(slab_lse_kernel, grid, dim3(256), 0, s, P);
+        GMM_TRY(hipGetLastError());
+        nt += grid.y;
       } else {
         GMM_TRY((launch_gemm<T, LSE>(P, tiling(nr, nv, P.ktiles, false).big, s)));
         nt += P.tn;
@@ -1129,7 +1290,15 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       P.GT = dw ? ws + p.off_GT : nullptr;
       P.ldgt = up(nr, kt);
       P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
-      GMM_TRY((launch_gemm<T, GRAD>(P, tiling(nr, nv, P.ktiles, false).big, s)));
+      if (p.split_l > 1) {
+        GMM_TRY(logit_slabs<T>(p, ws, P, s));
+        const dim3 grid((unsigned)((nr + 127) / 128), (unsigned)(P.ldg / 64));
+        hipLaunchKernelGGL(slab_grad_kernel<T>, grid, dim3(256), 0, s, P);
+        GMM_TRY(hipGetLastError());
+        P.tm = (int)grid.x;
+      } else {
+        GMM_TRY((launch_gemm<T, GRAD>(P, tiling(nr, nv, P.ktiles, false).big, s)));
+      }
       if (db) {
         hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((nv + 15) / 16)), dim3(256), 0, s, P.dbp, P.tm, nv, scal, db + v0,
                            accumulate || r0 > 0);

@@ -52,6 +52,35 @@ def test_sizes(g, dtype, N, D, V):
     check(g, *make(N, D, V, dtype))
 
 
+@pytest.mark.parametrize("dtype,N,D,V", [("f32", 300, 1000, 10), ("f32", 129, 700, 517), ("f32", 871, 1300, 77),
+                                         ("f32", 70, 400, 1), ("bf16", 130, 2048, 300), ("f16", 200, 4100, 131),
+                                         ("f32", 66, 520, 1025), ("bf16", 65, 8192, 513)])
+def test_few_tiles_over_long_rows(g, dtype, N, D, V):
+    X, W, b, y, gl = make(N, D, V, dtype)
+    whole = check(g, X, W, b, y, gl)
+    again = check(g, X, W, b, y, gl)
+    assert all(torch.equal(p, q) for p, q in zip(whole, again))
+    # one of the gradients alone
+    _, lse, dX, dW, db = whole
+    for i, want in ((0, dict(dW=False, dbias=False)), (1, dict(dX=False, dbias=False))):
+        only = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, **want)
+        assert torch.equal(only[i], (dX, dW)[i])
+
+
+@pytest.mark.parametrize("N", [70, 400])
+def test_few_tiles_with_masked_classes_and_rows(g, N):
+    X, W, b, y, gl = make(N, 1500, 600, "f32", ignored=0.4)
+    b[3:590] = -float("inf")  # a span without a class
+    y.copy_(torch.where(y < 0, y, y % 3))
+    X[y < 0] = float("nan")
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    assert not loss[y < 0].any() and not dX[y < 0].any()
+    assert all(torch.isfinite(t).all() for t in (loss, dX, dW, db)) and not dW[3:590].any() and not db[3:590].any()
+    y[5] = 600
+    assert torch.isnan(g.gmm_softmax_xent(X, W, y, bias=b)[0][5])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [3, 200])
 @pytest.mark.parametrize("pad,offset", [(8, 0), (13, 0), (0, 1), (5, 3), (0, 8)])
