@@ -292,11 +292,13 @@ struct XentArgs {
 };
 struct XentPlan {
   bool small, skinny;            // at most 128 features (gmm_xent_small.hip); few rows
+  bool few;                      // few classes, wide float32 rows (gmm_xent_few.hip)
+  bool slab_l;                   // logits in float32 slabs
   bool pack_x, pack_w;           // rows / head copied to aligned rows first
   bool slab_x, slab_w;           // products summed in float32 slabs
   bool big_x, big_w, big_l;      // products in 256 x 256 tiles
   int kbytes, split_x, split_w;
-  int split_l;                   // parts of the logits' k axis (slabs), 0 or 1: none
+  int split_l;                   // parts of the logits' k axis
   int64_t ldl;                   // row of such a slab
   int64_t Dp, nc, vc;            // padded D of the copies; rows of a chunk, classes of a piece
   int64_t np_r, np_v, ldg, ldgt, lds;

@@ -144,4 +144,25 @@ int xent_small_rows(int dtype, int64_t D, int pass);  // owner rows of a workgro
 // each part 4 tiles of 64 rows or longer
 int xent_small_splits(int64_t owners, int64_t streamed, int dtype, int64_t D, int pass);
 
+// Arguments of the kernels for wide float32 rows and at most 64 classes
+// (gmm_xent_few.hip).
+// Loss and gradients here and through tiles of 128 x 128: 65536 x 512, 64
+// classes, 338 and 633 us; 20000 x 2000, 64 classes, 414 and 617; 2000 x 1000, 64
+// classes, 110 and 116.
+constexpr int kFewClasses = 64;
+struct FewArgs {
+  RowsArgs rows;
+  int flat;                // rows of all problems evenly apart: row r at r ld
+  const char* b;           // bf16 planes [3][V][..]: logits the head's, dW the transpose of G
+  int64_t ldb, pb;         // bytes of a row, of a plane
+  int V, splits;           // classes; parts of k (logits: features, dW: rows)
+  float* slab;             // logits [split][rows][lds], dW [split][V][lds]
+  int64_t lds, slab_stride;
+  int add;                 // dW: add to what is there
+  const float* live;       // dW: rows with 0 take no part
+};
+hipError_t launch_xent_few_logits(const FewArgs& P, hipStream_t s);
+hipError_t launch_xent_few_dw(const FewArgs& P, hipStream_t s);
+int xent_few_splits(int64_t workgroups, int64_t k);
+
 }  // namespace gmm

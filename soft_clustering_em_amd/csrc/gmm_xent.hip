@@ -715,19 +715,19 @@ __device__ inline f32x4 logits_at(const GemmArgs& P, int64_t m, int64_t n) {
   return v;
 }
 
-// one wave per row and kRowSpan classes: their (max, sum), and the label's logit
-constexpr int kRowSpan = 512;
+// L lanes per row and 4 L U classes: their (max, sum), and the label's logit
+template <int L, int U>
 __global__ void __launch_bounds__(256) slab_lse_kernel(GemmArgs P) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x % L;
+  const int64_t m = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   if (m >= P.M) return;
-  const int64_t n0 = (int64_t)blockIdx.y * kRowSpan;
+  const int64_t n0 = (int64_t)blockIdx.y * (4 * L * U);
   const int y = label_at(P, m, n0);
-  f32x4 v[kRowSpan / 256];
+  f32x4 v[U];
   float mx = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < kRowSpan / 256; ++u) {
-    const int c = 256 * u + 4 * lane;
+  for (int u = 0; u < U; ++u) {
+    const int c = 4 * (L * u + lane);
     v[u] = n0 + c < P.N ? logits_at(P, m, n0 + c) : f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -736,15 +736,15 @@ __global__ void __launch_bounds__(256) slab_lse_kernel(GemmArgs P) {
     }
   }
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d));
+  for (int d = 1; d < L; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d));
   const float base = mx == -INFINITY ? 0.f : mx;
   float t = 0.f;
 #pragma unroll
-  for (int u = 0; u < kRowSpan / 256; ++u)
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int e = 0; e < 4; ++e) t += __builtin_amdgcn_exp2f((v[u][e] - base) * kLog2e);
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) t += __shfl_xor(t, d);
+  for (int d = 1; d < L; d *= 2) t += __shfl_xor(t, d);
   if (lane == 0) P.part[(int64_t)blockIdx.y * P.M + m] = make_float2(mx, t);
 }
 
@@ -871,19 +871,27 @@ unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64
 
 }  // namespace
 
+static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
 // the logits' parts: G or the (max, sum) pairs from slabs take a launch of about
 // 4 us more, at 4.9e6 multiply-adds of a compute unit a us.
 // Measured, loss and gradients: 871 x 2563 rows, 517 classes, float32, 35 tiles
 // of 128 x 128 whole 571 us, in parts 204; 500 x 4096, 1000 classes, bf16, 138
 // and 107; loss of 300 x 4000, 10 classes, float32, 226 and 39.
-static int logit_parts(int64_t M, int64_t N, int64_t ktiles, bool& big) {
-  const Tiling t = tiling(M, N, ktiles, true, 2e7);
-  big = t.big;
-  return t.splits;
+static void plan_logits(const XentArgs& a, XentPlan& p, int64_t mc, int64_t vcc, size_t& o) {
+  p.ldl = up(vcc, 4);
+  if (p.few) {
+    p.split_l = xent_few_splits((mc + 127) / 128, a.D);
+    p.slab_l = true;
+  } else {
+    const Tiling t = tiling(mc, vcc, (p.kbytes + 127) / 128 * (a.es == 4 ? 6 : 1), true, 2e7);
+    p.split_l = t.splits;
+    p.big_l = t.big;
+    p.slab_l = t.splits > 1;
+  }
+  if (p.slab_l) { p.off_sl = o; o = upz(o + sizeof(float) * (size_t)(p.split_l * mc * p.ldl)); }
 }
-
-static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 // what a call does and where its parts of the workspace lie
 XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db) {
@@ -901,6 +909,9 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
   const int64_t R = std::max<int64_t>(a.B * a.N, 1), V = a.V;
   size_t o = 0;
   p.small = a.D <= 128 && R > 64;
+  p.skinny = !grad && !p.small && R <= 64;
+  p.few = es == 4 && V <= kFewClasses && !p.small && !p.skinny;
+  if (p.few) p.pack_x = false;
   if (p.small) {
     // rows stream past in chunks only where they are copied to aligned rows
     // first (float32: as planes), classes likewise
@@ -934,7 +945,6 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
       }
     }
   } else if (!grad) {
-    p.skinny = R <= 64;
     if (p.skinny) p.pack_x = p.pack_w = false;  // it takes any alignment
     // rows of a chunk: at most 2^24 (max, sum) pairs; classes of a piece: all,
     // or 2^15 where they are copied to aligned rows first
@@ -942,13 +952,9 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     p.vc = p.pack_w ? std::min<int64_t>(V, 1 << 15) : V;
     const int64_t nt = (V + per - 1) / per + V / p.vc + 1;
     p.nc = std::min<int64_t>(R, std::max<int64_t>(256, ((int64_t)1 << 24) / nt / 256 * 256));
+    if (p.few) p.nc = std::min<int64_t>(p.nc, 1 << 20);
     p.off_part = o; o = upz(o + sizeof(float2) * (size_t)(nt * p.nc));
-    if (!p.skinny) {
-      const int64_t mc = std::min(p.nc, R), vcc = std::min(p.vc, V);
-      p.ldl = up(vcc, 4);
-      p.split_l = logit_parts(mc, vcc, (p.kbytes + 127) / 128 * (pl == 1 ? 1 : 6), p.big_l);
-      if (p.split_l > 1) { p.off_sl = o; o = upz(o + sizeof(float) * (size_t)(p.split_l * mc * p.ldl)); }
-    }
+    if (!p.skinny) plan_logits(a, p, std::min(p.nc, R), std::min(p.vc, V), o);
     p.off_lab = o;  o = upz(o + sizeof(float) * (size_t)p.nc);
   } else {
     const int64_t cap = (int64_t)1 << (es == 2 ? 27 : 26);
@@ -971,9 +977,7 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     p.off_bmax = o; o = upz(o + sizeof(float) * 1024);
     p.off_scal = o; o = upz(o + sizeof(float) * 2);
     p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * 2 * pl));
-    p.ldl = up(vcc, 4);
-    p.split_l = logit_parts(mc, vcc, (p.kbytes + 127) / 128 * (pl == 1 ? 1 : 6), p.big_l);
-    if (p.split_l > 1) { p.off_sl = o; o = upz(o + sizeof(float) * (size_t)(p.split_l * mc * p.ldl)); }
+    plan_logits(a, p, mc, vcc, o);
     if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
     if (want_dx) {
       p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * 2 * pl));
@@ -985,11 +989,12 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     }
     if (want_dw) {
       p.off_GT = o; o = upz(o + (size_t)(vcc * p.ldgt * 2 * pl));
-      p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * 2 * pl));
+      if (!p.few) { p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * 2 * pl)); }
       const Tiling t = tiling(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6), true);
       p.split_w = t.splits;
       p.big_w = t.big;
-      p.slab_w = p.split_w > 1 || p.np_r > 1;
+      if (p.few) p.split_w = xent_few_splits((a.D + 255) / 256, mc);
+      p.slab_w = p.few || p.split_w > 1 || p.np_r > 1;
       if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
     }
   }
@@ -1075,14 +1080,31 @@ hipError_t logit_operands(const XentArgs& a, const XentPlan& p, int64_t r0, int6
   return hipSuccess;
 }
 
+FewArgs few_args(const XentArgs& a, int64_t r0, int64_t nr) {
+  FewArgs F{};
+  F.rows = RowsArgs{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
+  F.flat = a.B == 1 || a.stride_b == a.N * a.ld;
+  F.V = (int)a.V;
+  return F;
+}
+
 // the logits' product in parts, side by side in slabs
 template <typename T>
-hipError_t logit_slabs(const XentPlan& p, char* ws, GemmArgs& P, hipStream_t s) {
+hipError_t logit_slabs(const XentArgs& a, const XentPlan& p, int64_t r0, char* ws, GemmArgs& P, hipStream_t s) {
   P.splits = p.split_l;
   P.slab = reinterpret_cast<float*>(ws + p.off_sl);
   P.lds = p.ldl;
   P.slab_stride = P.M * p.ldl;
-  return launch_gemm<T, OUT>(P, p.big_l, s);
+  if (!p.few) return launch_gemm<T, OUT>(P, p.big_l, s);
+  FewArgs F = few_args(a, r0, P.M);
+  F.b = P.B;
+  F.ldb = P.ldb;
+  F.pb = P.pb;
+  F.splits = P.splits;
+  F.slab = P.slab;
+  F.lds = P.lds;
+  F.slab_stride = P.slab_stride;
+  return launch_xent_few_logits(F, s);
 }
 
 // ---- rows of at most 128 features (gmm_xent_small.hip)
@@ -1239,10 +1261,12 @@ hipError_t forward(const XentArgs& a, const XentPlan& p, float* loss, float* lse
         else hipLaunchKernelGGL((skinny_kernel<T, 4>), grid, dim3(256), 0, s, P, x);
         GMM_TRY(hipGetLastError());
         nt += grid.x;
-      } else if (p.split_l > 1) {
-        GMM_TRY(logit_slabs<T>(p, ws, P, s));
-        const dim3 grid((unsigned)((nr + 3) / 4), (unsigned)((nv + kRowSpan - 1) / kRowSpan));
-        hipLaunchKernelGGL(slab_lse_kernel, grid, dim3(256), 0, s, P);
+      } else if (p.slab_l) {
+        GMM_TRY(logit_slabs<T>(a, p, r0, ws, P, s));
+        const int L = nv <= 64 ? 16 : 64, span = nv <= 64 ? 64 : 512;
+        const dim3 grid((unsigned)((nr + 256 / L - 1) / (256 / L)), (unsigned)((nv + span - 1) / span));
+        if (L == 16) hipLaunchKernelGGL((slab_lse_kernel<16, 1>), grid, dim3(256), 0, s, P);
+        else hipLaunchKernelGGL((slab_lse_kernel<64, 2>), grid, dim3(256), 0, s, P);
         GMM_TRY(hipGetLastError());
         nt += grid.y;
       } else {
@@ -1290,8 +1314,8 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       P.GT = dw ? ws + p.off_GT : nullptr;
       P.ldgt = up(nr, kt);
       P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
-      if (p.split_l > 1) {
-        GMM_TRY(logit_slabs<T>(p, ws, P, s));
+      if (p.slab_l) {
+        GMM_TRY(logit_slabs<T>(a, p, r0, ws, P, s));
         const dim3 grid((unsigned)((nr + 127) / 128), (unsigned)(P.ldg / 64));
         hipLaunchKernelGGL(slab_grad_kernel<T>, grid, dim3(256), 0, s, P);
         GMM_TRY(hipGetLastError());
@@ -1335,7 +1359,7 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       }
       if (dw) {  // dW of the piece += G^T X of the chunk
         RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
-        if (p.np_r > 1 || v0 == 0) GMM_TRY(transpose<T>(r, coef + r0, ws + p.off_XT, P.ldgt, s));
+        if (!p.few && (p.np_r > 1 || v0 == 0)) GMM_TRY(transpose<T>(r, coef + r0, ws + p.off_XT, P.ldgt, s));
         GemmArgs Q{};
         Q.A = P.GT;
         Q.lda = P.ldgt * 2;
@@ -1357,7 +1381,21 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
           Q.slab_stride = std::min(p.vc, a.V) * p.lds;
           Q.add = r0 > 0;
         }
-        GMM_TRY((launch_gemm<T, OUT>(Q, p.big_w, s)));
+        if (p.few) {
+          FewArgs F = few_args(a, r0, nr);
+          F.b = Q.A;
+          F.ldb = Q.lda;
+          F.pb = Q.pa;
+          F.splits = Q.splits;
+          F.slab = Q.slab;
+          F.lds = Q.lds;
+          F.slab_stride = Q.slab_stride;
+          F.add = Q.add;
+          F.live = coef + r0;
+          GMM_TRY(launch_xent_few_dw(F, s));
+        } else {
+          GMM_TRY((launch_gemm<T, OUT>(Q, p.big_w, s)));
+        }
         if (p.slab_w && r0 + nr >= R) {
           GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nv, a.D, scal, nullptr, Q.out, accumulate, s));
         }

@@ -67,17 +67,36 @@ def test_few_tiles_over_long_rows(g, dtype, N, D, V):
         assert torch.equal(only[i], (dX, dW)[i])
 
 
-@pytest.mark.parametrize("N", [70, 400])
-def test_few_tiles_with_masked_classes_and_rows(g, N):
-    X, W, b, y, gl = make(N, 1500, 600, "f32", ignored=0.4)
-    b[3:590] = -float("inf")  # a span without a class
+@pytest.mark.parametrize("N,D,V,pad,offset,bias", [(65, 129, 2, 0, 0, True), (200, 200, 16, 3, 1, True), (1000, 515, 17, 0, 0, False),
+                                                   (777, 1030, 33, 13, 5, True), (3000, 260, 64, 8, 0, True),
+                                                   (130, 4099, 64, 0, 2, False), (40, 300, 22, 0, 0, True)])
+def test_few_classes_over_wide_float32_rows(g, N, D, V, pad, offset, bias):
+    whole = check(g, *make(N, D, V, "f32", pad=pad, offset=offset, bias=bias))
+    again = check(g, *make(N, D, V, "f32", pad=pad, offset=offset, bias=bias))
+    assert all(p is None and q is None or torch.equal(p, q) for p, q in zip(whole, again))
+
+
+def test_few_classes_over_problems_apart(g):
+    X, W, b, y, gl = make(90, 200, 20, "f32", B=4, pad=5)
+    check(g, X, W, b, y, gl)
+    check(g, X[:, :41], W, b, y[:, :41].contiguous(), gl[:, :41].contiguous())
+
+
+def test_few_classes_over_chunks_of_rows(g):
+    check(g, *make((1 << 20) + 77, 130, 5, "f32", ignored=0.02))
+
+
+@pytest.mark.parametrize("N,D,V", [(70, 1500, 600), (400, 1500, 600), (150, 300, 40)])
+def test_few_tiles_with_masked_classes_and_rows(g, N, D, V):
+    X, W, b, y, gl = make(N, D, V, "f32", ignored=0.4)
+    b[3 : V - 10] = -float("inf")  # a span without a class
     y.copy_(torch.where(y < 0, y, y % 3))
     X[y < 0] = float("nan")
     loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
     dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
     assert not loss[y < 0].any() and not dX[y < 0].any()
-    assert all(torch.isfinite(t).all() for t in (loss, dX, dW, db)) and not dW[3:590].any() and not db[3:590].any()
-    y[5] = 600
+    assert all(torch.isfinite(t).all() for t in (loss, dX, dW, db)) and not dW[3 : V - 10].any() and not db[3 : V - 10].any()
+    y[5] = V
     assert torch.isnan(g.gmm_softmax_xent(X, W, y, bias=b)[0][5])
 
 
