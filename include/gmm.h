@@ -373,9 +373,10 @@ typedef struct {
  * still formed); a label >= V gives loss NaN.  Rows and head are float32, bf16
  * or half, of one type, at any stride and alignment of their elements
  * (operands off 16 bytes are copied piecewise); logits are summed in float32
- * (float32 rows of D <= 128: products of three bf16 planes, right to 2^-23 of
- * |x| |w|; a row with an infinity then has NaN results).  Scores of one row to 64 rows take a path that reads the
- * head once.  Window: D <= 65536, V < 2^27, B*N < 2^28.  A row whose logits
+ * (float32, more than 64 rows or gradients: products of three bf16 planes, right
+ * to 2^-23 of |x| |w|; elements up to bf16's largest finite value, 3.38e38; a row
+ * or class with an infinity then has NaN results).  The loss of 64 rows or fewer
+ * takes a path that reads the head once.  Window: D <= 65536, V < 2^27, B*N < 2^28.  A row whose logits
  * are all -inf has lse -inf and loss NaN.  N = 0 launches nothing.
  * Workspace: gmm_softmax_xent_workspace_bytes (bounded: rows are taken in
  * chunks).  Deterministic. */
@@ -410,8 +411,8 @@ gmm_status gmm_softmax_xent_grad(const gmm_data* rows, const gmm_head* head, con
  *   table   (B,K,D) rows as gmm_data describes them, with N = K
  *   idx     (B,N,m) int32; weights (B,N,m) float32, nullable (1)
  *   out     (B,N,D) in the table's type, contiguous; summed in float32
- * Any stride and alignment of the elements.  D <= 65536, B*N*m < 2^31,
- * B*K < 2^31.  N = 0 launches nothing.  No workspace. */
+ * Any stride and alignment of the elements.  D <= 65536, m <= 4096,
+ * B*N*m < 2^31, B*K < 2^31.  N = 0 launches nothing.  No workspace. */
 gmm_status gmm_codebook_lookup(const gmm_data* table, int64_t N, int32_t m, const int32_t* idx, const float* weights,
                                float scale, void* out, void* stream);
 

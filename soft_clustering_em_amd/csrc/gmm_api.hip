@@ -1441,6 +1441,7 @@ static gmm_status lookup_check(int64_t B, int64_t N, int32_t m, int64_t K, int64
   if (m < 1) return fail(GMM_ERR_INVALID_ARG, "m must be >= 1 (got %d)", m);
   if (K < 1) return fail(GMM_ERR_INVALID_ARG, "K must be >= 1 (got %lld)", (long long)K);
   if (N < 0) return fail(GMM_ERR_INVALID_ARG, "N must be >= 0");
+  if (m > 4096) return fail(GMM_ERR_UNSUPPORTED, "m (%d) > 4096", m);  // a row's codes are walked in order
   const int64_t lim = ((int64_t)1 << 31) - 1;
   if (N > 0 && (B > lim / N || B * N > lim / m)) return fail(GMM_ERR_UNSUPPORTED, "B*N*m must stay below 2^31");
   if (K > lim / B) return fail(GMM_ERR_UNSUPPORTED, "B*K must stay below 2^31");

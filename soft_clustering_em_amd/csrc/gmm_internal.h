@@ -318,6 +318,7 @@ struct LookupArgs {
   int64_t ld_g, stride_g;
   const int32_t* idx;      // (B, N, m)
   const float* weights;    // (B, N, m) or null
+  const int32_t* len;      // (B, N): codes of a row before the first outside, or null
   float scale;
   int dtype, m, accumulate;
   int64_t B, N, K, D;
@@ -347,7 +348,8 @@ struct LookupPlan {
   int64_t S, nblk, C, chunks, Dp;
   uint32_t none;
   int passes, bits, per;   // entries per thread of the sort
-  size_t off_key[2], off_src[2], off_hist, off_base, off_part, bytes;
+  bool lengths;            // rows' lengths counted first
+  size_t off_key[2], off_src[2], off_hist, off_base, off_part, off_len, bytes;
 };
 LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, int dtype, bool want_table);
 hipError_t launch_lookup(const LookupArgs& a, hipStream_t s);

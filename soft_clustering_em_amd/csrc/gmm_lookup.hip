@@ -179,11 +179,37 @@ __device__ inline uint32_t key_of(const LookupArgs& A, int64_t e, uint32_t none)
   const int j = (int)(e - row * A.m);
   const int32_t* ix = A.idx + row * A.m;
   int k = 0;
+  if (A.len) {
+    if (j >= A.len[row]) return none;
+    return (uint32_t)((A.B == 1 ? 0 : row / A.N) * A.K + ix[j]);
+  }
   for (int q = 0; q <= j; ++q) {
     k = ix[q];
     if (k < 0 || k >= A.K) return none;
   }
   return (uint32_t)((A.B == 1 ? 0 : row / A.N) * A.K + k);
+}
+
+// Rows of more than kScanCodes codes: their lengths, 16 lanes a row, so that an
+// entry does not look at every code before it.
+constexpr int kScanCodes = 16;
+__global__ void __launch_bounds__(256) length_kernel(LookupArgs A, int32_t* len) {
+  const int l = threadIdx.x & 15;
+  for (int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); row < A.B * A.N; row += (int64_t)gridDim.x * 16) {
+    const int32_t* ix = A.idx + row * A.m;
+    int n = A.m;
+    for (int j0 = 0; j0 < n; j0 += 16) {
+      int at = A.m;  // the first code outside among these 16
+      if (j0 + l < A.m) {
+        const int k = ix[j0 + l];
+        if (k < 0 || k >= A.K) at = j0 + l;
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) at = min(at, __shfl_xor(at, o));
+      n = min(n, at);
+    }
+    if (l == 0) len[row] = n;
+  }
 }
 
 // any bytes <- 0 (a kernel: memory operations in a captured graph are avoided)
@@ -522,7 +548,7 @@ hipError_t lookup(LookupArgs a, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipStream_t s) {
+hipError_t lookup_grad(LookupArgs a, const LookupPlan& p, char* ws, hipStream_t s) {
   const int64_t rows = a.B * a.N;
   if (a.dweights && rows > 0) {
     int lg = row_split(a.D, Vec<T>::E).lg;
@@ -535,6 +561,12 @@ hipError_t lookup_grad(const LookupArgs& a, const LookupPlan& p, char* ws, hipSt
   if (!a.dtable) return hipSuccess;
   const int64_t bytes = a.accumulate ? 0 : a.B * a.K * a.D * (int64_t)sizeof(T);
   if (rows == 0) return launch_zero(a.dtable, bytes, s);
+  if (p.lengths) {
+    int32_t* len = reinterpret_cast<int32_t*>(ws + p.off_len);
+    hipLaunchKernelGGL(length_kernel, dim3((unsigned)std::min<int64_t>((rows + 15) / 16, kLookupGrid)), dim3(256), 0, s, a, len);
+    GMM_TRY(hipGetLastError());
+    a.len = len;
+  }
   uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + p.off_key[0]), reinterpret_cast<uint32_t*>(ws + p.off_key[1])};
   uint32_t* srcs[2] = {reinterpret_cast<uint32_t*>(ws + p.off_src[0]), reinterpret_cast<uint32_t*>(ws + p.off_src[1])};
   SortPass P{};
@@ -640,6 +672,8 @@ LookupPlan lookup_plan(int64_t B, int64_t N, int64_t m, int64_t K, int64_t D, in
   p.off_hist = o; o = upz(o + sizeof(uint32_t) * ((size_t)p.nblk << p.bits));
   p.off_base = o; o = upz(o + sizeof(uint32_t) * ((size_t)1 << p.bits));
   p.off_part = o; o = upz(o + sizeof(float) * (size_t)(2 * p.chunks * p.Dp));
+  p.lengths = m > kScanCodes;
+  if (p.lengths) { p.off_len = o; o = upz(o + sizeof(int32_t) * (size_t)(B * N)); }
   p.bytes = o;
   return p;
 }

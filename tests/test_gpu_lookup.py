@@ -203,3 +203,20 @@ def test_table_past_32_bits(g):
     assert torch.equal(dt[at], dout)
     dt[at] = 0
     assert not dt.any()
+
+
+@pytest.mark.parametrize("N,m,D,K", [(1, 4096, 8, 50), (40, 700, 20, 90), (7, 17, 33, 5), (600, 33, 12, 3000)])
+def test_long_rows(g, N, m, D, K):
+    table, dout, idx, w = make(N, m, D, K, "f32")
+    gen = torch.Generator(device="cuda").manual_seed(N + m)
+    idx = torch.randint(0, K, (N, m), generator=gen, device="cuda", dtype=torch.int32)
+    ends = torch.randint(0, m + 1, (N,), generator=gen, device="cuda").tolist()
+    for i, e in enumerate(ends):  # one value outside: what is behind it takes no part
+        if e < m and N > 1:
+            idx[i, e] = (-1, K)[i % 2]
+    got = g.gmm_codebook_lookup(table, idx, weights=w)
+    ref.within("rows", got, *ref.lookup(table, idx, w, 1.0))
+    dt, dw = g.gmm_codebook_lookup_grad(dout, idx, K, table=table, weights=w)
+    (want, tol), wdw = ref.lookup_grad(dout, idx, K, table, w, 1.0)
+    ref.within("dtable", dt, want, tol)
+    ref.within("dweights", dw, *wdw)

@@ -174,3 +174,12 @@ def test_python_checks_on_the_host():
                 lambda: g.gmm_clip_grad_norm([X], 1.0)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_lookup_refuses_rows_of_more_than_4096_codes():
+    L = _abi.lib()
+    t = _abi.GmmData(ctypes.c_void_p(256), _abi.DT_F32, 1, 10, 8, 8, 80)
+    p = ctypes.c_void_p(4096)
+    assert L.gmm_codebook_lookup(ctypes.byref(t), 2, 4097, p, None, 1.0, p, None) == UNS
+    assert L.gmm_codebook_lookup_grad(ctypes.byref(t), 5, 4097, p, None, 1.0, None, p, None, 0, p, 1 << 20, None) == UNS
+    assert L.gmm_codebook_lookup_grad_workspace_bytes(ctypes.byref(t), 5, 4097) == 0
