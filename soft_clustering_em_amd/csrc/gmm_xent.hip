@@ -846,10 +846,10 @@ int64_t tiles(int64_t M, int64_t N, int bt) { return ((M + bt - 1) / bt) * ((N +
 struct Tiling {
   bool big;
   int splits;
+  double cost;
 };
 Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts, double apart = 0.0) {
-  Tiling best{true, 1};
-  double least = 1e300;
+  Tiling best{true, 1, 1e300};
   for (int big = 1; big >= 0; --big) {
     const int64_t t = tiles(M, N, big ? 256 : 128);
     for (int64_t s = 1; s == 1 || (parts && s <= ktiles / 8 && s <= 32); ++s) {
@@ -859,10 +859,7 @@ Tiling tiling(int64_t M, int64_t N, int64_t ktiles, bool parts, double apart = 0
                             : wg <= kNumCU ? 16384.0 / 0.5
                                            : (double)((wg + 2 * kNumCU - 1) / (2 * kNumCU)) * 2 * 16384.0 / 0.95;
       const double cost = rounds * k + (s > 1 ? apart + 4.0 * (double)s * (double)M * (double)N : 0.0);
-      if (cost < least) {
-        least = cost;
-        best = Tiling{big != 0, (int)s};
-      }
+      if (cost < best.cost) best = Tiling{big != 0, (int)s, cost};
     }
   }
   return best;
@@ -873,6 +870,18 @@ unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64
 
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+// Classes of the loss's first launch: where the 256 x 256 tiles' last round of
+// the compute units is nearly empty, the whole rounds', the rest in a launch of
+// its own (of smaller tiles mostly).  1000 rows, 50001 classes, 784 tiles over
+// D = 1000, half: 146 us at once, 132 so; over D = 4096, bf16, 438 and 362.
+static int64_t whole_rounds(int64_t M, int64_t V, int64_t ktiles) {
+  const int64_t tm = (M + 255) / 256, rounds = tiles(M, V, 256) / kNumCU;
+  const int64_t first = rounds * kNumCU / tm * 256;
+  if (rounds < 1 || first >= V) return V;
+  const double apart = tiling(M, first, ktiles, false).cost + tiling(M, V - first, ktiles, false).cost + 1e7;
+  return apart < tiling(M, V, ktiles, false).cost ? first : V;
+}
 
 // the logits' parts: G or the (max, sum) pairs from slabs take a launch of about
 // 4 us more, at 4.9e6 multiply-adds of a compute unit a us.
@@ -953,6 +962,7 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     const int64_t nt = (V + per - 1) / per + V / p.vc + 1;
     p.nc = std::min<int64_t>(R, std::max<int64_t>(256, ((int64_t)1 << 24) / nt / 256 * 256));
     if (p.few) p.nc = std::min<int64_t>(p.nc, 1 << 20);
+    else if (!p.skinny && p.vc == V) p.vc = whole_rounds(p.nc, V, (p.kbytes + 127) / 128 * (pl == 1 ? 1 : 6));
     p.off_part = o; o = upz(o + sizeof(float2) * (size_t)(nt * p.nc));
     if (!p.skinny) plan_logits(a, p, std::min(p.nc, R), std::min(p.vc, V), o);
     p.off_lab = o;  o = upz(o + sizeof(float) * (size_t)p.nc);

@@ -125,6 +125,13 @@ def test_chunks_of_rows_and_pieces_of_the_head(g, dtype, N, D, V):
     check(g, *make(N, D, V, dtype, ignored=0.02))
 
 
+@pytest.mark.parametrize("dtype,N,V", [("f16", 1000, 20000), ("bf16", 1025, 16385), ("f32", 300, 33001)])
+def test_classes_past_the_last_whole_round_of_tiles(g, dtype, N, V):
+    X, W, b, y, gl = make(N, 136, V, dtype, ignored=0.0)
+    y[::3] = V - 1 - torch.arange(len(y[::3]), device="cuda", dtype=torch.int32) % 200  # labels on both sides
+    check(g, X, W, b, y, gl)
+
+
 @pytest.mark.parametrize("N", [7, 200])
 def test_rows_left_out_take_no_part(g, N):
     X, W, b, y, gl = make(N, 64, 300, "bf16", ignored=0.5)
