@@ -79,6 +79,8 @@ struct GemmArgs {
   char* G;             // GRAD: [M][ldg] 16-bit, [3] of them for float32
   char* GT;            // GRAD: [N][ldgt] likewise, null: not wanted
   int64_t ldg, ldgt;   // elements, whole k-tiles
+  int64_t gcols;       // columns of G from this launch's first on, whole k-tiles
+  int64_t gp, tp;      // float32: elements from one plane of G, of its transpose, to the next
   float* dbp;          // GRAD: [tile m][N] column sums, null: not wanted
   // OUT
   float* slab;         // [splits][M][lds] float32, null: straight to out
@@ -332,7 +334,6 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
       constexpr int CR = SUB * 16 / EPC, CL = 16 / EPC;    // chunks of a transposed row; of 16 elements
       constexpr int kGPlane = NN * 16 * SUB * 16;          // elements of a plane in the region
       static_assert(MT % SUB == 0, "transposing in whole sub-tiles");
-      const int64_t gp = P.M * P.ldg, tp = P.N * P.ldgt;   // elements of a plane of G and of its transpose
       static_assert(WM * WN * kRegion <= 2 * kStage, "the waves' regions fill the two stages");
       T* reg = reinterpret_cast<T*>((wv < WM * WN / 2 ? st0 : st1) + (wv % (WM * WN / 2)) * kRegion);
       const float mult = P.scal ? P.scal[0] : 1.f;
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
             }
 #pragma unroll
             for (int l = 0; l < PL; ++l) {
-              if (m < P.M && n < P.ldg) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + l * gp + m * P.ldg + n) = w[l];
+              if (m < P.M && n < P.gcols) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + l * P.gp + m * P.ldg + n) = w[l];
               if (P.GT) {
                 // a dword holds two columns of one row; neighbouring rows' lanes
                 // trade, so that each writes two rows of one column
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gemm_kernel(GemmArgs P) {
               const u32x4 v = *reinterpret_cast<const u32x4*>(reg + l * kGPlane + nl * (SUB * 16) +
                                                               (ch ^ ((CL * ((nl >> 2) & 3)) & (CR - 1))) * EPC);
               const int64_t n = n0 + wn * NN * 16 + nl, m = m0 + wm * MT * 16 + i0 * 16 + ch * EPC;
-              if (n < P.N && m < P.ldgt) *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + l * tp + n * P.ldgt + m) = v;
+              if (n < P.N && m < P.ldgt) *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + l * P.tp + n * P.ldgt + m) = v;
             }
           __syncthreads();
         }
@@ -758,7 +759,6 @@ __global__ void __launch_bounds__(256) slab_grad_kernel(GemmArgs P) {
   __shared__ float red[16][64];
   const int tid = threadIdx.x, c = (tid & 15) * 4, r = tid >> 4;
   const int64_t n0 = (int64_t)blockIdx.y * 64;
-  const int64_t gp = P.M * P.ldg, tp = P.N * P.ldgt;
   const float mult = P.scal ? P.scal[0] : 1.f;
   f32x4 cs = {0.f, 0.f, 0.f, 0.f};
   for (int h = 0; h < 2; ++h) {
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(256) slab_grad_kernel(GemmArgs P) {
       }
 #pragma unroll
       for (int l = 0; l < PL; ++l) {
-        if (m < P.M) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + l * gp + m * P.ldg + n) = w[l];
+        if (m < P.M) *reinterpret_cast<u32x2*>(reinterpret_cast<T*>(P.G) + l * P.gp + m * P.ldg + n) = w[l];
         T t[4];
         __builtin_memcpy(t, &w[l], 8);
 #pragma unroll
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(256) slab_grad_kernel(GemmArgs P) {
         for (int u = 0; u < 2; ++u) {
           const int i = tid + 256 * u, nl = i / 8, ch = i % 8;
           if (n0 + nl < P.N)
-            *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + l * tp + (n0 + nl) * P.ldgt + m0 + ch * 8) =
+            *reinterpret_cast<u32x4*>(reinterpret_cast<T*>(P.GT) + l * P.tp + (n0 + nl) * P.ldgt + m0 + ch * 8) =
                 *reinterpret_cast<const u32x4*>(&tile[l][nl][ch * 8]);
         }
     }
@@ -871,10 +871,12 @@ unsigned blocks(int64_t n, int64_t cap = 4096) { return (unsigned)std::max<int64
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 static size_t upz(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
-// Classes of the loss's first launch: where the 256 x 256 tiles' last round of
+// Classes of the logits' first launch: where the 256 x 256 tiles' last round of
 // the compute units is nearly empty, the whole rounds', the rest in a launch of
 // its own (of smaller tiles mostly).  1000 rows, 50001 classes, 784 tiles over
 // D = 1000, half: 146 us at once, 132 so; over D = 4096, bf16, 438 and 362.
+// Loss and gradients, both passes so: 5634 x 1456, 5845 classes, float32, 2685
+// and 2543 us; 2000 x 1000, 20000 classes, float32, 2244 and 2110.
 static int64_t whole_rounds(int64_t M, int64_t V, int64_t ktiles) {
   const int64_t tm = (M + 255) / 256, rounds = tiles(M, V, 256) / kNumCU;
   const int64_t first = rounds * kNumCU / tm * 256;
@@ -1320,24 +1322,41 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
       P.coef = coef + r0;
       P.scal = scal;
       P.G = ws + p.off_G;
-      P.ldg = up(nv, kt);
+      P.ldg = P.gcols = up(nv, kt);
       P.GT = dw ? ws + p.off_GT : nullptr;
       P.ldgt = up(nr, kt);
+      P.gp = nr * P.ldg;
+      P.tp = nv * P.ldgt;
       P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
-      if (p.slab_l) {
-        GMM_TRY(logit_slabs<T>(a, p, r0, ws, P, s));
-        const dim3 grid((unsigned)((nr + 127) / 128), (unsigned)(P.ldg / 64));
-        hipLaunchKernelGGL(slab_grad_kernel<T>, grid, dim3(256), 0, s, P);
-        GMM_TRY(hipGetLastError());
-        P.tm = (int)grid.x;
-      } else {
-        GMM_TRY((launch_gemm<T, GRAD>(P, tiling(nr, nv, P.ktiles, false).big, s)));
-      }
-      if (db) {
-        hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((nv + 15) / 16)), dim3(256), 0, s, P.dbp, P.tm, nv, scal, db + v0,
-                           accumulate || r0 > 0);
-        GMM_TRY(hipGetLastError());
-      }
+      // classes c0 .. c0 + cn of the piece
+      auto columns = [&](int64_t c0, int64_t cn) -> hipError_t {
+        GemmArgs S = P;
+        S.B += c0 * S.ldb;
+        S.v0 += c0;
+        S.N = cn;
+        S.G += c0 * 2;
+        S.gcols -= c0;
+        if (S.GT) S.GT += c0 * S.ldgt * 2;
+        if (S.dbp) S.dbp += (nr + 127) / 128 * c0;
+        if (p.slab_l) {
+          GMM_TRY(logit_slabs<T>(a, p, r0, ws, S, s));
+          const dim3 grid((unsigned)((nr + 127) / 128), (unsigned)(S.gcols / 64));
+          hipLaunchKernelGGL(slab_grad_kernel<T>, grid, dim3(256), 0, s, S);
+          GMM_TRY(hipGetLastError());
+          S.tm = (int)grid.x;
+        } else {
+          GMM_TRY((launch_gemm<T, GRAD>(S, tiling(nr, cn, S.ktiles, false).big, s)));
+        }
+        if (db) {
+          hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((cn + 15) / 16)), dim3(256), 0, s, S.dbp, S.tm, cn, scal,
+                             db + v0 + c0, accumulate || r0 > 0);
+          GMM_TRY(hipGetLastError());
+        }
+        return hipSuccess;
+      };
+      const int64_t first = p.slab_l ? nv : whole_rounds(nr, nv, P.ktiles);
+      GMM_TRY(columns(0, first));
+      if (first < nv) GMM_TRY(columns(first, nv - first));
       if (dx) {  // dX of the chunk += G W of the piece
         GemmArgs Q{};
         Q.A = P.G;
