@@ -295,6 +295,46 @@ def test_same_inputs_same_bits_also_captured_and_on_another_stream(g, N):
     assert torch.equal(loss, outs[0])
 
 
+@pytest.mark.parametrize("dtype,N,D,V", [("f32", 500, 300, 20), ("f32", 200, 900, 300), ("bf16", 150, 4096, 200)])
+def test_logits_in_parts_captured_and_in_two_streams_at_once(g, dtype, N, D, V):
+    X, W, b, y, gl = make(N, D, V, dtype)
+
+    def step():
+        loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+        return (loss, lse) + g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+
+    want = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for k in range(3):
+        X.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        assert all(torch.equal(p, q) for p, q in zip(outs, want)), k
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st in sides:
+            with torch.cuda.stream(st):
+                got.append(step())
+    torch.cuda.synchronize()
+    for t in got:
+        assert all(torch.equal(p, q) for p, q in zip(t, want))
+
+
+def test_wide_rows_of_few_classes_far_apart(g):
+    """Row offsets past 2^31 bytes."""
+    ld = (1 << 22) + 4
+    big = torch.empty(300, ld, device="cuda")
+    X = big[:, 3:203]
+    X.copy_(torch.randn(300, 200, device="cuda"))
+    _, W, b, y, gl = make(300, 200, 12, "f32")
+    check(g, X, W, b, y, gl)
+
+
 def test_rows_far_apart(g):
     """Row offsets past 2^31 bytes: rows of a wide array."""
     ld = (1 << 22) + 8
