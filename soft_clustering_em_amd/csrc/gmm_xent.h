@@ -144,12 +144,13 @@ int xent_small_rows(int dtype, int64_t D, int pass);  // owner rows of a workgro
 // each part 4 tiles of 64 rows or longer
 int xent_small_splits(int64_t owners, int64_t streamed, int dtype, int64_t D, int pass);
 
-// Arguments of the kernels for wide float32 rows and at most 64 classes
-// (gmm_xent_few.hip).
+// Arguments of the kernels for wide float32 rows and at most 128 classes
+// (gmm_xent_few.hip), 64 a workgroup.
 // Loss and gradients here and through tiles of 128 x 128: 65536 x 512, 64
-// classes, 338 and 633 us; 20000 x 2000, 64 classes, 414 and 617; 2000 x 1000, 64
-// classes, 110 and 116.
-constexpr int kFewClasses = 64;
+// classes, 332 and 633 us; 20000 x 2000, 64 classes, 414 and 617; 65536 x 512, 128
+// classes, 547 and 675; 57491 x 2410, 128 classes, 2453 and 2493; 2000 x 700, 100
+// classes, 112 and 109.
+constexpr int kFewClasses = 128;
 struct FewArgs {
   RowsArgs rows;
   int flat;                // rows of all problems evenly apart: row r at r ld

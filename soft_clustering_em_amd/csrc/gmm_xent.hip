@@ -893,7 +893,7 @@ static int64_t whole_rounds(int64_t M, int64_t V, int64_t ktiles) {
 static void plan_logits(const XentArgs& a, XentPlan& p, int64_t mc, int64_t vcc, size_t& o) {
   p.ldl = up(vcc, 4);
   if (p.few) {
-    p.split_l = xent_few_splits((mc + 127) / 128, a.D);
+    p.split_l = xent_few_splits((mc + 127) / 128 * ((vcc + 63) / 64), a.D);
     p.slab_l = true;
   } else {
     const Tiling t = tiling(mc, vcc, (p.kbytes + 127) / 128 * (a.es == 4 ? 6 : 1), true, 2e7);
@@ -1005,7 +1005,7 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
       const Tiling t = tiling(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6), true);
       p.split_w = t.splits;
       p.big_w = t.big;
-      if (p.few) p.split_w = xent_few_splits((a.D + 255) / 256, mc);
+      if (p.few) p.split_w = xent_few_splits((a.D + 255) / 256 * ((vcc + 63) / 64), mc);
       p.slab_w = p.few || p.split_w > 1 || p.np_r > 1;
       if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
     }

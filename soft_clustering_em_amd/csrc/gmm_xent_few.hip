@@ -1,5 +1,5 @@
 // gmm_xent_few.hip -- softmax cross entropy of wide float32 rows under a head
-// of at most 64 classes: the two products that read the rows.
+// of at most 128 classes: the two products that read the rows.
 //
 // With few classes the rows' bytes are everything: a product does 2 V flops for
 // the 4 bytes of an element, so the rows are read where they lie, once a
@@ -44,14 +44,14 @@ __global__ void __launch_bounds__(256) few_logits_kernel(FewArgs P) {
   constexpr int U = NB == 4 ? 1 : 2;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lr = lane & 15, lq = lane >> 4;
   const int64_t m0 = ((int64_t)blockIdx.x * 4 + wv) * 32;
-  const int z = blockIdx.y, D = P.rows.D;
+  const int z = blockIdx.y, D = P.rows.D, cb = blockIdx.z * 64;  // first class
   const char* x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     x[i] = P.rows.x + 4 * few_row(P, min(m0 + 16 * i + lr, P.rows.nr - 1)) + 32 * lq;  // rows past the last are not stored
   const char* w[NB];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) w[j] = P.b + (int64_t)min(16 * j + lr, P.V - 1) * P.ldb + 16 * lq;
+  for (int j = 0; j < NB; ++j) w[j] = P.b + (int64_t)min(cb + 16 * j + lr, P.V - 1) * P.ldb + 16 * lq;
   f32x4 acc[2][NB];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(256) few_logits_kernel(FewArgs P) {
     if (m >= P.rows.nr) continue;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const int n = 16 * j + 4 * lq;
+      const int n = cb + 16 * j + 4 * lq;
       if (n < P.V) *reinterpret_cast<f32x4*>(P.slab + z * P.slab_stride + m * P.lds + n) = acc[i][j];
     }
   }
@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(256) few_dw_kernel(FewArgs P) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lr = lane & 15, lq = lane >> 4;
   const int d0 = (blockIdx.x * 4 + wv) * 64 + 4 * lr;
   if (d0 - 4 * lr >= P.rows.D) return;
-  const int z = blockIdx.y;
+  const int z = blockIdx.y, cb = blockIdx.z * 64;
   const int64_t nr = P.rows.nr;
   const char* g[NB];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) g[j] = P.b + (int64_t)min(16 * j + lr, P.V - 1) * P.ldb + 16 * lq;
+  for (int j = 0; j < NB; ++j) g[j] = P.b + (int64_t)min(cb + 16 * j + lr, P.V - 1) * P.ldb + 16 * lq;
   f32x4 acc[NB][4];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) few_dw_kernel(FewArgs P) {
     for (int c = 0; c < 4; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t steps = (nr + 31) / 32;
   const int64_t s0 = steps * z / P.splits, s1 = steps * (z + 1) / P.splits;
-  auto load = [&](int64_t s, f32x4* v, float* live, u32x4 (*b)[3], auto whole) {
+  auto load = [&](int64_t s, f32x4* v, float* live, auto whole) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t r = 32 * s + 8 * lq + k, rc = min(r, nr - 1);
@@ -166,6 +166,9 @@ __global__ void __launch_bounds__(256) few_dw_kernel(FewArgs P) {
       const float t = P.live[rc];
       live[k] = r < nr ? t : 0.f;
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto planes_of = [&](int64_t s, u32x4 (*b)[3]) {
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -190,16 +193,21 @@ __global__ void __launch_bounds__(256) few_dw_kernel(FewArgs P) {
     if (s0 >= s1) return;
     f32x4 v0[8], v1[8];
     float l0[8], l1[8];
-    u32x4 b0[NB][3], b1[NB][3];
-    load(s0, v0, l0, b0, whole);
+    u32x4 b[NB][3];
+    load(s0, v0, l0, whole);
     int64_t s = s0;
     for (; s + 2 <= s1; s += 2) {
-      load(s + 1, v1, l1, b1, whole);
-      multiply(v0, l0, b0);
-      load(min(s + 2, s1 - 1), v0, l0, b0, whole);
-      multiply(v1, l1, b1);
+      planes_of(s, b);
+      load(s + 1, v1, l1, whole);
+      multiply(v0, l0, b);
+      planes_of(s + 1, b);
+      load(min(s + 2, s1 - 1), v0, l0, whole);
+      multiply(v1, l1, b);
     }
-    if (s < s1) multiply(v0, l0, b0);
+    if (s < s1) {
+      planes_of(s, b);
+      multiply(v0, l0, b);
+    }
   };
   if (d0 - 4 * lr + 64 <= P.rows.D) run(std::true_type{});
   else run(std::false_type{});
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(256) few_dw_kernel(FewArgs P) {
   for (int j = 0; j < NB; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int n = 16 * j + 4 * lq + e;
+      const int n = cb + 16 * j + 4 * lq + e;
       if (n >= P.V) continue;
       float* p = P.slab + z * P.slab_stride + n * P.lds + d0;  // rows of D rounded up to 4
       f32x4 t = {acc[j][0][e], acc[j][1][e], acc[j][2][e], acc[j][3][e]};
@@ -226,7 +234,7 @@ int xent_few_splits(int64_t workgroups, int64_t k) {
 }
 
 hipError_t launch_xent_few_logits(const FewArgs& P, hipStream_t s) {
-  const dim3 grid((unsigned)((P.rows.nr + 127) / 128), (unsigned)P.splits);
+  const dim3 grid((unsigned)((P.rows.nr + 127) / 128), (unsigned)P.splits, (unsigned)((P.V + 63) / 64));
   if (P.V <= 16) hipLaunchKernelGGL(few_logits_kernel<1>, grid, dim3(256), 0, s, P);
   else if (P.V <= 32) hipLaunchKernelGGL(few_logits_kernel<2>, grid, dim3(256), 0, s, P);
   else hipLaunchKernelGGL(few_logits_kernel<4>, grid, dim3(256), 0, s, P);
@@ -234,7 +242,7 @@ hipError_t launch_xent_few_logits(const FewArgs& P, hipStream_t s) {
 }
 
 hipError_t launch_xent_few_dw(const FewArgs& P, hipStream_t s) {
-  const dim3 grid((unsigned)((P.rows.D + 255) / 256), (unsigned)P.splits);
+  const dim3 grid((unsigned)((P.rows.D + 255) / 256), (unsigned)P.splits, (unsigned)((P.V + 63) / 64));
   if (P.V <= 16) hipLaunchKernelGGL(few_dw_kernel<1>, grid, dim3(256), 0, s, P);
   else if (P.V <= 32) hipLaunchKernelGGL(few_dw_kernel<2>, grid, dim3(256), 0, s, P);
   else hipLaunchKernelGGL(few_dw_kernel<4>, grid, dim3(256), 0, s, P);

@@ -69,7 +69,8 @@ def test_few_tiles_over_long_rows(g, dtype, N, D, V):
 
 @pytest.mark.parametrize("N,D,V,pad,offset,bias", [(65, 129, 2, 0, 0, True), (200, 200, 16, 3, 1, True), (1000, 515, 17, 0, 0, False),
                                                    (777, 1030, 33, 13, 5, True), (3000, 260, 64, 8, 0, True),
-                                                   (130, 4099, 64, 0, 2, False), (40, 300, 22, 0, 0, True)])
+                                                   (130, 4099, 64, 0, 2, False), (40, 300, 22, 0, 0, True),
+                                                   (500, 300, 65, 0, 0, True), (70, 1000, 128, 1, 0, True), (300, 520, 97, 0, 3, False)])
 def test_few_classes_over_wide_float32_rows(g, N, D, V, pad, offset, bias):
     whole = check(g, *make(N, D, V, "f32", pad=pad, offset=offset, bias=bias))
     again = check(g, *make(N, D, V, "f32", pad=pad, offset=offset, bias=bias))
