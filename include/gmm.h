@@ -375,9 +375,14 @@ typedef struct {
  * (operands off 16 bytes are copied piecewise); logits are summed in float32
  * (float32, more than 64 rows or gradients: products of three bf16 planes, right
  * to 2^-23 of |x| |w|; elements up to bf16's largest finite value, 3.38e38; a row
- * or class with an infinity then has NaN results).  The loss of 64 rows or fewer
+ * or class with an infinity then has NaN results; bf16 and half rows or classes
+ * with an infinity, where the definition leaves it finite, may).  The loss of 64 rows or fewer
  * takes a path that reads the head once.  Window: D <= 65536, V < 2^27, B*N < 2^28.  A row whose logits
- * are all -inf has lse -inf and loss NaN.  N = 0 launches nothing.
+ * are all -inf has lse -inf and loss NaN; finite logits have a finite lse down to
+ * float32's lowest value.  A logit of +inf or NaN makes its row's lse NaN.  loss, and
+ * the p of the gradients, carry lse's own rounding (2^-24 |lse|): where |lse| has no
+ * room for log V, as under a mask of finite values over every class, p is no longer
+ * normalised.  N = 0 launches nothing.
  * Workspace: gmm_softmax_xent_workspace_bytes (bounded: rows are taken in
  * chunks).  Deterministic. */
 size_t gmm_softmax_xent_workspace_bytes(const gmm_data* rows, const gmm_head* head);

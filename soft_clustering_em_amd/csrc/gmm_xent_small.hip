@@ -40,6 +40,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 namespace gmm {
@@ -51,6 +52,16 @@ enum Pass { LSE = 0, DX = 1, DW = 2 };
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+// exp(l - z) is exp2 of one fma, k l - k z, with k = log2(e).  Where |z| is so
+// large that k z could leave float32, two float32 values apart are 2^99 apart or
+// more, and exp(l - z) is 0 or 1 whatever k: there k = 1.  Over k = log2(e) for
+// every row, which overflows there, that takes 0.8% more of the loss and gradients
+// of 262144 x 128 bf16 rows, 4096 classes; the subtraction first everywhere 3.7%;
+// a branch between the two inside the loop 5%, between two bodies of a tile
+// spills (DW 562 -> 1684 us).
+constexpr float kFar = 1e38f;
+__device__ inline float factor_of(float z) { return fabsf(z) > kFar ? 1.f : kLog2e; }
 
 // streamed rows per tile
 constexpr int tile_rows(int es, int dp) { return es == 4 && dp == 128 ? 32 : 64; }
@@ -80,9 +91,13 @@ __device__ inline float dot16(u32x4 a, u32x4 b) {
   return s;
 }
 
+// waves per SIMD: DX at 32 features takes a few registers more than three waves
+// leave it (262144 x 24 half rows, 4096 classes: 217 us with two, 205 so)
+constexpr int min_waves(int es, int dp, int pass) { return es == 2 && dp == 32 && pass == DX ? 3 : 2; }
+
 // S: the rows' type; its matrix-core form is itself, or bf16 planes
 template <typename S, int DP, int RB, int PASS>
-__global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
+__global__ void __launch_bounds__(256, min_waves(sizeof(S), DP, PASS)) small_kernel(SmallArgs P) {
   using T = std::conditional_t<sizeof(S) == 4, __bf16, S>;
   constexpr int PL = planes(sizeof(S)), NP = PL == 1 ? 1 : 6, kTile = tile_rows(sizeof(S), DP);
   constexpr int RBytes = DP * 2, KC = RBytes / 16, KS = KC / 4;
@@ -100,8 +115,8 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   constexpr float kTop = __is_same(S, _Float16) ? 32768.f : 1.f;  // DX: scale of p
   __shared__ __attribute__((aligned(1024))) char st0[kBytes];
   __shared__ __attribute__((aligned(1024))) char st1[kBytes];
-  __shared__ __attribute__((aligned(16))) float sp0[PASS == DW ? 3 * kTile : kTile];
-  __shared__ __attribute__((aligned(16))) float sp1[PASS == DW ? 3 * kTile : kTile];
+  __shared__ __attribute__((aligned(16))) float sp0[PASS == DW ? 4 * kTile : kTile];
+  __shared__ __attribute__((aligned(16))) float sp1[PASS == DW ? 4 * kTile : kTile];
 
   // workgroups of one split of the stream on one XCD (they go round the 8)
   const unsigned total = gridDim.x, id = blockIdx.x, q8 = total / 8, r8 = total % 8, xc = id % 8;
@@ -119,7 +134,8 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
 
   // ---- the owner's rows and what goes with each
   u32x4 own[RB][PL][KS];
-  float oa[RB];  // LSE, DX: -lse log2(e) (+ log2 kTop);  DW: the class's bias
+  float oa[RB];  // DX: -k lse (+ log2 kTop);  DW: the class's bias
+  float ok[RB];  // DX: k
   float oc[RB];  // DX: the row's coefficient
   int oy[RB];    // LSE: label;  DX: label within the piece;  DW: the class
 #pragma unroll
@@ -134,7 +150,10 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
       live = oc[i] != 0.f;  // a row that takes no part is read as zeros
     }
     if (PASS == DX) {
-      oa[i] = live ? fmaf(-P.lse[o], kLog2e, __builtin_log2f(kTop)) : -INFINITY;
+      const float z = live ? P.lse[o] : 0.f;
+      ok[i] = factor_of(z);
+      // k = 1: kTop has no room beside z, the row goes without it
+      oa[i] = live ? fmaf(-z, ok[i], ok[i] == 1.f ? 0.f : __builtin_log2f(kTop)) : -INFINITY;
       if (live) oy[i] = P.labels[o] - (int)P.v0;  // a class of this piece, or none
     }
     if (PASS == DW) {
@@ -189,7 +208,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
       }
     }
   };
-  // what goes with each streamed row: LSE, DX: bias;  DW: -lse log2(e), c, label
+  // what goes with each streamed row: LSE, DX: bias;  DW: -k lse, c, label, k
   float pa = 0.f, pb = 0.f;
   int py = -1;
   const float mult = PASS == DW && P.scal ? P.scal[0] : 1.f;
@@ -208,7 +227,9 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
     const bool in = lane < rows_of(t);
     if constexpr (PASS == DW) {
       const bool live = in && pb != 0.f;
-      sp[lane] = live ? pa * -kLog2e : -INFINITY;
+      const float k = factor_of(pa);
+      sp[lane] = live ? pa * -k : -INFINITY;
+      sp[3 * kTile + lane] = k;
       sp[kTile + lane] = live ? pb * mult : 0.f;
       sp[2 * kTile + lane] = __builtin_bit_cast(float, live ? py : -1);
     } else {
@@ -225,7 +246,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
   float mx[RB], sm[RB];  // LSE: maximum and sum;  DW: mx is the bias gradient
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
-    mx[i] = PASS == LSE ? -1e38f : 0.f;  // finite: -inf logits stay below it
+    mx[i] = PASS == LSE ? -FLT_MAX : 0.f;  // finite: -inf logits stay below it
     sm[i] = 0.f;
   }
 
@@ -252,6 +273,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
         for (int i = 0; i < RB; ++i) s[i] = mma<T>(a[kPairs[p][0]], own[i][kPairs[p][1]][k], s[i]);
     }
   };
+  auto top_of = [](float k) { return kTop == 1.f || k == 1.f ? 1.f : kTop; };
   // G of a block, in place
   // (a block holds few labels: the lanes vote before they look for theirs)
   auto gradient = [&](const float* sp, int jb, int t, f32x4* s) {
@@ -259,20 +281,21 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, oa[i]));
+        for (int e = 0; e < 4; ++e) s[i][e] = __builtin_amdgcn_exp2f(fmaf(s[i][e], ok[i], oa[i]));
         const int y = oy[i] - t * kTile - 16 * jb;  // outside 0 .. 15 where the block has not got the label
         if (__builtin_amdgcn_ballot_w64((unsigned)y < 16u))
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] -= y == 4 * lq + e ? kTop : 0.f;
+          for (int e = 0; e < 4; ++e) s[i][e] -= y == 4 * lq + e ? top_of(ok[i]) : 0.f;
       }
     } else {
       const f32x4 nl = *reinterpret_cast<const f32x4*>(sp + 16 * jb + 4 * lq);
       const f32x4 c = *reinterpret_cast<const f32x4*>(sp + kTile + 16 * jb + 4 * lq);
+      const f32x4 k = *reinterpret_cast<const f32x4*>(sp + 3 * kTile + 16 * jb + 4 * lq);
       const i32x4 y = *reinterpret_cast<const i32x4*>(sp + 2 * kTile + 16 * jb + 4 * lq);
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = c[e] * __builtin_amdgcn_exp2f(fmaf(s[i][e], kLog2e, nl[e]));
+        for (int e = 0; e < 4; ++e) s[i][e] = c[e] * __builtin_amdgcn_exp2f(fmaf(s[i][e], k[e], nl[e]));
         if (__builtin_amdgcn_ballot_w64(y[0] == oy[i] || y[1] == oy[i] || y[2] == oy[i] || y[3] == oy[i]))
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[i][e] -= y[e] == oy[i] ? c[e] : 0.f;
@@ -295,12 +318,12 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
         for (int jb = 0; jb < NB; ++jb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = fmaxf(m, s[jb][i][e]);
-        const float nm = -m * kLog2e;
+        const float k = factor_of(m), nm = -m * k;
         float a = sm[i] * __builtin_amdgcn_exp2f((mx[i] - m) * kLog2e);  // exactly 1 where nothing changed
 #pragma unroll
         for (int jb = 0; jb < NB; ++jb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a += __builtin_amdgcn_exp2f(fmaf(s[jb][i][e], kLog2e, nm));
+          for (int e = 0; e < 4; ++e) a += __builtin_amdgcn_exp2f(fmaf(s[jb][i][e], k, nm));
         sm[i] = a;
         mx[i] = m;
       }
@@ -417,7 +440,7 @@ __global__ void __launch_bounds__(256, 2) small_kernel(SmallArgs P) {
         if (in && lq == 0) P.dbp[split * P.own.nr + o] = v;
       }
       if (!in) continue;
-      const float c = PASS == DX ? oc[i] / kTop : back;
+      const float c = PASS == DX ? oc[i] / top_of(ok[i]) : back;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         const int64_t f = 16 * d + 4 * lq;

@@ -345,3 +345,56 @@ def test_rows_far_apart(g):
     _, W, b, y, gl = make(520, 40, 120, "bf16")
     check(g, X, W, b, y, gl)
     check(g, X[::40], W, b, y[::40].contiguous(), gl[::40].contiguous())
+
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("N,D,V", [(6, 64, 300), (140, 64, 300), (140, 20, 3000), (140, 128, 77), (140, 200, 300), (20000, 40, 500)])
+def test_every_class_masked_with_the_lowest_value(g, dtype, N, D, V):
+    """float32 has no room for log V beside 3.4e38: lse is the mask's value, on
+    every path, and what follows from it is finite."""
+    X, W, b, y, gl = make(N, D, V, dtype, ignored=0.0)
+    b[:] = LOWEST
+    loss, lse, dX, dW, db = check(g, X, W, b, y, gl)
+    assert torch.equal(lse, torch.full_like(lse, LOWEST)) and torch.isfinite(loss).all()
+    assert all(torch.isfinite(t).all() for t in (dX, dW, db))
+
+
+@pytest.mark.parametrize("N", [6, 140])
+def test_classes_masked_with_the_lowest_value(g, N):
+    X, W, b, y, gl = make(N, 64, 400, "bf16", ignored=0.0)
+    b[3:390] = LOWEST
+    y.copy_(torch.arange(N, device="cuda", dtype=torch.int32) % 3)
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    assert not dW[3:390].any() and not db[3:390].any()
+    assert torch.isfinite(loss).all() and torch.isfinite(dX).all()
+    b[3:390] = -float("inf")
+    again = g.gmm_softmax_xent(X, W, y, bias=b)
+    assert torch.equal(loss, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("N,D,V", [(6, 64, 300), (140, 64, 300), (300, 20, 3000), (140, 128, 77), (140, 200, 300), (300, 1000, 100)])
+def test_one_class_far_above_the_rest(g, dtype, N, D, V):
+    """A logit of 3e38, whose product with log2(e) leaves float32: p is 1 there
+    and 0 elsewhere, so G is g ([v = 7] - [v = y]) without any error of its own;
+    what is left is G's rounding to the rows' type (half a step), the sums and
+    the last rounding."""
+    X, W, b, y, gl = make(N, D, V, dtype, ignored=0.0)
+    b[7] = 3e38
+    y[::2] = 7
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    assert (lse == b[7]).all() and not loss[::2].any()
+    dX, dW, db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    G = torch.zeros(N, V, dtype=torch.float64, device="cuda")
+    G[:, 7] = gl.double()
+    G[torch.arange(N, device="cuda"), y.long()] -= gl.double()
+    h = ref.half(X.dtype)
+    for name, got, a, c in (("dX", dX, G, W.double()), ("dW", dW, G.t().contiguous(), X.double())):
+        want, mag = a @ c, a.abs() @ c.abs()
+        tol = (h + (V + N + 8) * ref.U) * mag
+        ref.within(name, got, want, tol + (h + 2 * ref.U) * (want.abs() + tol) + ref.tiny(X.dtype))
+    ref.within("db", db, G.sum(0), (N + 8) * ref.U * G.abs().sum(0))
