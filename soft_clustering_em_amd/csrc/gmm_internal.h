@@ -302,7 +302,7 @@ struct XentPlan {
   int64_t ldl;                   // row of such a slab
   int64_t Dp, nc, vc;            // padded D of the copies; rows of a chunk, classes of a piece
   int64_t np_r, np_v, ldg, ldgt, lds;
-  size_t off_part, off_lab, off_coef, off_bmax, off_scal, off_G, off_GT, off_XT, off_WT, off_dbp, off_sx, off_sw, off_sl, off_px,
+  size_t off_part, off_lab, off_coef, off_bmax, off_scal, off_G, off_GT, off_XT, off_WT, off_dbp, off_dbr, off_sx, off_sw, off_sl, off_px,
       off_pw, bytes;
 };
 XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, bool want_db);

@@ -681,9 +681,10 @@ __global__ void __launch_bounds__(256) finish_kernel(const float* slab, int spli
   }
 }
 
-// db[n] = scale sum over tile rows of the column sums (+ db); 16 threads a sum
-__global__ void __launch_bounds__(256) dbias_kernel(const float* dbp, int tm, int64_t N, const float* scal, float* db,
-                                                    int add) {
+// out[n] = scale sum over tile rows of the column sums (+ before[n], the chunks'
+// before this one) (+ out[n]); 16 threads a sum
+__global__ void __launch_bounds__(256) dbias_kernel(const float* dbp, int tm, int64_t N, const float* scal,
+                                                    const float* before, float* out, int add) {
   __shared__ float red[16][16];
   const int c = threadIdx.x & 15, sl = threadIdx.x >> 4;
   const int64_t n = (int64_t)blockIdx.x * 16 + c;
@@ -697,7 +698,8 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* dbp, int tm, in
 #pragma unroll
     for (int k = 1; k < 16; ++k) v += red[k][c];
     v *= scal ? scal[1] : 1.f;
-    db[n] = add ? db[n] + v : v;
+    if (before) v += before[n];
+    out[n] = add ? out[n] + v : v;
   }
 }
 
@@ -953,6 +955,7 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
         p.slab_w = p.split_w > 1 || p.np_r > 1 || !want_dw;
         if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * V * p.lds)); }
         if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * V)); }
+        if (want_db && p.np_r > 1) { p.off_dbr = o; o = upz(o + sizeof(float) * (size_t)V); }
       }
     }
   } else if (!grad) {
@@ -991,6 +994,7 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * 2 * pl));
     plan_logits(a, p, mc, vcc, o);
     if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
+    if (want_db && p.np_r > 1) { p.off_dbr = o; o = upz(o + sizeof(float) * (size_t)vcc); }
     if (want_dx) {
       p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * 2 * pl));
       const Tiling t = tiling(mc, a.D, p.ldg / kt * (pl == 1 ? 1 : 6), true);
@@ -1119,6 +1123,16 @@ hipError_t logit_slabs(const XentArgs& a, const XentPlan& p, int64_t r0, char* w
   return launch_xent_few_logits(F, s);
 }
 
+// The bias gradients of a chunk of rows.  The chunks' sum stays in `run` until
+// the last of them: what a caller accumulates into is added to once, as dX and
+// dW are, and not rounded with every chunk.
+hipError_t dbias(const float* dbp, int tm, int64_t N, const float* scal, float* run, float* db, bool first, bool last,
+                 int accumulate, hipStream_t s) {
+  hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((N + 15) / 16)), dim3(256), 0, s, dbp, tm, N, scal,
+                     first ? (const float*)nullptr : run, last ? db : run, last && accumulate);
+  return hipGetLastError();
+}
+
 // ---- rows of at most 128 features (gmm_xent_small.hip)
 template <typename T>
 hipError_t copy_stream(const RowsArgs& r, char* dst, int64_t Dp, SmallArgs& P, hipStream_t s) {
@@ -1235,11 +1249,9 @@ hipError_t small_backward(const XentArgs& a, const XentPlan& p, const float* lse
     P.accumulate = accumulate;
     P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
     GMM_TRY(launch_xent_small(P, a.dtype, 2, s));
-    if (db) {  // the column sums were multiplied back already
-      hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((a.V + 15) / 16)), dim3(256), 0, s, P.dbp, p.split_w, a.V,
-                         (const float*)nullptr, db, accumulate || r0 > 0);
-      GMM_TRY(hipGetLastError());
-    }
+    if (db)  // the column sums were multiplied back already
+      GMM_TRY(dbias(P.dbp, p.split_w, a.V, nullptr, accumulate ? reinterpret_cast<float*>(ws + p.off_dbr) : db, db, r0 == 0,
+                    r0 + nr >= R, accumulate, s));
   }
   if (slab && dw) {
     GMM_TRY(finish<T>(slab, p.split_w, a.V * p.lds, p.lds, a.V, a.D, nullptr, nullptr, dw, accumulate, s));
@@ -1347,11 +1359,9 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
         } else {
           GMM_TRY((launch_gemm<T, GRAD>(S, tiling(nr, cn, S.ktiles, false).big, s)));
         }
-        if (db) {
-          hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((cn + 15) / 16)), dim3(256), 0, s, S.dbp, S.tm, cn, scal,
-                             db + v0 + c0, accumulate || r0 > 0);
-          GMM_TRY(hipGetLastError());
-        }
+        if (db)
+          GMM_TRY(dbias(S.dbp, S.tm, cn, scal, accumulate ? reinterpret_cast<float*>(ws + p.off_dbr) + c0 : db + v0 + c0,
+                        db + v0 + c0, r0 == 0, r0 + nr >= R, accumulate, s));
         return hipSuccess;
       };
       const int64_t first = p.slab_l ? nv : whole_rounds(nr, nv, P.ktiles);

@@ -398,3 +398,21 @@ def test_one_class_far_above_the_rest(g, dtype, N, D, V):
         tol = (h + (V + N + 8) * ref.U) * mag
         ref.within(name, got, want, tol + (h + 2 * ref.U) * (want.abs() + tol) + ref.tiny(X.dtype))
     ref.within("db", db, G.sum(0), (N + 8) * ref.U * G.abs().sum(0))
+
+
+@pytest.mark.parametrize("dtype,N,D,V", [("f16", 34000, 130, 33000), ("bf16", 60000, 136, 5000), ("f32", (3 << 20) + 5, 24, 40)])
+def test_bias_gradient_over_chunks_of_rows_is_added_once(g, dtype, N, D, V):
+    """Whatever the chunks: the sum, inside its own bound, and one rounding of
+    what it is added to."""
+    X, W, b, y, gl = make(N, D, V, dtype, ignored=0.02)
+    _, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    want, tol = ref.xent(X, W, y, b, gl)
+    only = dict(dX=False, dW=False)
+    db = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, **only)[2]
+    ref.within("db", db, want["db"], tol["db"])
+    old = torch.randn(V, device="cuda") * 100
+    acc = old.clone()
+    g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, dbias=acc, accumulate=True, **only)
+    s = old.double() + want["db"]
+    ref.within("db", acc, s, tol["db"] + 1.01 * ref.U * (s.abs() + tol["db"]))
+    assert torch.equal(acc, old + db)
