@@ -399,6 +399,11 @@ gmm_status gmm_softmax_xent(const gmm_data* rows, const gmm_head* head, const in
  * gradients that its row reaches NaN.  G is formed in pieces of at most 2^27
  * elements in the workspace and rounded once to the rows' type for the two
  * products (float32 accumulation; half rows scaled by a power of two first).
+ * Beside a piece and its transpose the workspace holds the chunk's rows and the
+ * piece's classes transposed (for at most 64 rows a piece is 2^21 classes, so up
+ * to a copy of the head) and, where rows and classes both are in several pieces,
+ * float32 sums of the gradients of the fewer of the two; it does not grow with
+ * rows or classes otherwise.
  * The gradients may not overlap each other or the inputs.  Workspace:
  * gmm_softmax_xent_grad_workspace_bytes, want = 1 (dx) + 2 (dw) + 4 (dbias).
  * Deterministic. */

@@ -296,6 +296,8 @@ struct XentPlan {
   bool slab_l;                   // logits in float32 slabs
   bool pack_x, pack_w;           // rows / head copied to aligned rows first
   bool slab_x, slab_w;           // products summed in float32 slabs
+  bool rows_out;                 // gradients: rows in the outer loop, classes in the inner
+  bool keep_x, keep_w;           // one slab of all rows / classes, filled over the outer loop
   bool big_x, big_w, big_l;      // products in 256 x 256 tiles
   int kbytes, split_x, split_w;
   int split_l;                   // parts of the logits' k axis

@@ -994,24 +994,32 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     p.off_G = o;    o = upz(o + (size_t)(mc * p.ldg * 2 * pl));
     plan_logits(a, p, mc, vcc, o);
     if (want_db) { p.off_dbp = o; o = upz(o + sizeof(float) * (size_t)(((mc + 127) / 128) * vcc)); }
-    if (want_db && p.np_r > 1) { p.off_dbr = o; o = upz(o + sizeof(float) * (size_t)vcc); }
+    // chunks of rows and pieces of classes both: the larger side in the outer
+    // loop finishes its gradients one by one, the smaller side's stay in one
+    // float32 slab until the end.  No parts of k beside that slab: a chunk or
+    // piece of that side has 2^15 rows, tiles enough.
+    const bool both = p.np_r > 1 && p.np_v > 1;
+    p.rows_out = both && R > V;
+    p.keep_x = both && !p.rows_out;
+    p.keep_w = p.rows_out;
+    if (want_db && p.np_r > 1) { p.off_dbr = o; o = upz(o + sizeof(float) * (size_t)(p.rows_out ? V : vcc)); }
     if (want_dx) {
       p.off_WT = o; o = upz(o + (size_t)(a.D * p.ldg * 2 * pl));
-      const Tiling t = tiling(mc, a.D, p.ldg / kt * (pl == 1 ? 1 : 6), true);
+      const Tiling t = tiling(mc, a.D, p.ldg / kt * (pl == 1 ? 1 : 6), !p.keep_x);
       p.split_x = t.splits;
       p.big_x = t.big;
       p.slab_x = p.split_x > 1 || p.np_v > 1;
-      if (p.slab_x) { p.off_sx = o; o = upz(o + sizeof(float) * (size_t)(p.split_x * R * p.lds)); }
+      if (p.slab_x) { p.off_sx = o; o = upz(o + sizeof(float) * (size_t)(p.split_x * (p.keep_x ? R : mc) * p.lds)); }
     }
     if (want_dw) {
       p.off_GT = o; o = upz(o + (size_t)(vcc * p.ldgt * 2 * pl));
       if (!p.few) { p.off_XT = o; o = upz(o + (size_t)(a.D * p.ldgt * 2 * pl)); }
-      const Tiling t = tiling(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6), true);
+      const Tiling t = tiling(vcc, a.D, p.ldgt / kt * (pl == 1 ? 1 : 6), !p.keep_w);
       p.split_w = t.splits;
       p.big_w = t.big;
       if (p.few) p.split_w = xent_few_splits((a.D + 255) / 256 * ((vcc + 63) / 64), mc);
       p.slab_w = p.few || p.split_w > 1 || p.np_r > 1;
-      if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * vcc * p.lds)); }
+      if (p.slab_w) { p.off_sw = o; o = upz(o + sizeof(float) * (size_t)(p.split_w * (p.keep_w ? V : vcc) * p.lds)); }
     }
   }
   if (p.pack_x) { p.off_px = o; o = upz(o + (size_t)(std::min(p.nc, R) * p.Dp * 2 * pl)); }
@@ -1320,126 +1328,134 @@ hipError_t backward(const XentArgs& a, const XentPlan& p, const float* lse, cons
     GMM_TRY(hipGetLastError());
   }
   if (p.small) return small_backward<T>(a, p, lse, coef, scal, dx, dw, db, accumulate, ws, s);
-  for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) {
-    const int64_t nv = std::min(p.vc, a.V - v0);
-    if (dx) {
+  // a chunk of rows against a piece of the classes
+  auto part = [&](int64_t r0, int64_t v0) -> hipError_t {
+    const int64_t nr = std::min(p.nc, R - r0), nv = std::min(p.vc, a.V - v0);
+    const bool new_rows = p.rows_out ? v0 == 0 : p.np_r > 1 || v0 == 0, new_classes = p.rows_out || r0 == 0;
+    if (dx && new_classes) {
       RowsArgs r{(const char*)a.w, a.V, a.ld_w, 0, v0, nv, (int)a.D};
       GMM_TRY(transpose<T>(r, nullptr, ws + p.off_WT, up(nv, kt), s));
     }
-    for (int64_t r0 = 0; r0 < R; r0 += p.nc) {
-      const int64_t nr = std::min(p.nc, R - r0);
-      GemmArgs P{};
-      GMM_TRY(logit_operands<T>(a, p, r0, nr, v0, nv, ws, p.np_r > 1 || v0 == 0, r0 == 0, P, s));
-      P.lse = lse + r0;
-      P.coef = coef + r0;
-      P.scal = scal;
-      P.G = ws + p.off_G;
-      P.ldg = P.gcols = up(nv, kt);
-      P.GT = dw ? ws + p.off_GT : nullptr;
-      P.ldgt = up(nr, kt);
-      P.gp = nr * P.ldg;
-      P.tp = nv * P.ldgt;
-      P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
-      // classes c0 .. c0 + cn of the piece
-      auto columns = [&](int64_t c0, int64_t cn) -> hipError_t {
-        GemmArgs S = P;
-        S.B += c0 * S.ldb;
-        S.v0 += c0;
-        S.N = cn;
-        S.G += c0 * 2;
-        S.gcols -= c0;
-        if (S.GT) S.GT += c0 * S.ldgt * 2;
-        if (S.dbp) S.dbp += (nr + 127) / 128 * c0;
-        if (p.slab_l) {
-          GMM_TRY(logit_slabs<T>(a, p, r0, ws, S, s));
-          const dim3 grid((unsigned)((nr + 127) / 128), (unsigned)(S.gcols / 64));
-          hipLaunchKernelGGL(slab_grad_kernel<T>, grid, dim3(256), 0, s, S);
-          GMM_TRY(hipGetLastError());
-          S.tm = (int)grid.x;
-        } else {
-          GMM_TRY((launch_gemm<T, GRAD>(S, tiling(nr, cn, S.ktiles, false).big, s)));
-        }
-        if (db)
-          GMM_TRY(dbias(S.dbp, S.tm, cn, scal, accumulate ? reinterpret_cast<float*>(ws + p.off_dbr) + c0 : db + v0 + c0,
-                        db + v0 + c0, r0 == 0, r0 + nr >= R, accumulate, s));
-        return hipSuccess;
-      };
-      const int64_t first = p.slab_l ? nv : whole_rounds(nr, nv, P.ktiles);
-      GMM_TRY(columns(0, first));
-      if (first < nv) GMM_TRY(columns(first, nv - first));
-      if (dx) {  // dX of the chunk += G W of the piece
-        GemmArgs Q{};
-        Q.A = P.G;
-        Q.lda = P.ldg * 2;
-        Q.pa = nr * P.ldg * 2;
-        Q.B = ws + p.off_WT;
-        Q.ldb = P.ldg * 2;
-        Q.pb = a.D * P.ldg * 2;
-        Q.M = nr;
-        Q.N = a.D;
-        Q.kbytes = (int)(P.ldg * 2);
-        Q.ktiles = (int)(P.ldg / kt) * pairs;
-        Q.splits = std::min<int>(p.split_x, Q.ktiles);
-        Q.scal = scal;
-        Q.rowlive = coef + r0;
-        Q.out = dx + r0 * a.D * es;
-        Q.accumulate = accumulate;
-        if (p.slab_x) {
-          Q.splits = p.split_x;  // every slab is written by the first piece; empty k ranges add zeros
-          Q.slab = reinterpret_cast<float*>(ws + p.off_sx) + r0 * p.lds;
-          Q.lds = p.lds;
-          Q.slab_stride = R * p.lds;
-          Q.add = v0 > 0;
-        }
-        GMM_TRY((launch_gemm<T, OUT>(Q, p.big_x, s)));
-        if (p.slab_x && v0 + nv >= a.V) {
-          GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nr, a.D, scal, coef + r0, Q.out, accumulate, s));
-        }
+    GemmArgs P{};
+    GMM_TRY(logit_operands<T>(a, p, r0, nr, v0, nv, ws, new_rows, new_classes, P, s));
+    P.lse = lse + r0;
+    P.coef = coef + r0;
+    P.scal = scal;
+    P.G = ws + p.off_G;
+    P.ldg = P.gcols = up(nv, kt);
+    P.GT = dw ? ws + p.off_GT : nullptr;
+    P.ldgt = up(nr, kt);
+    P.gp = nr * P.ldg;
+    P.tp = nv * P.ldgt;
+    P.dbp = db ? reinterpret_cast<float*>(ws + p.off_dbp) : nullptr;
+    // classes c0 .. c0 + cn of the piece
+    auto columns = [&](int64_t c0, int64_t cn) -> hipError_t {
+      GemmArgs S = P;
+      S.B += c0 * S.ldb;
+      S.v0 += c0;
+      S.N = cn;
+      S.G += c0 * 2;
+      S.gcols -= c0;
+      if (S.GT) S.GT += c0 * S.ldgt * 2;
+      if (S.dbp) S.dbp += (nr + 127) / 128 * c0;
+      if (p.slab_l) {
+        GMM_TRY(logit_slabs<T>(a, p, r0, ws, S, s));
+        const dim3 grid((unsigned)((nr + 127) / 128), (unsigned)(S.gcols / 64));
+        hipLaunchKernelGGL(slab_grad_kernel<T>, grid, dim3(256), 0, s, S);
+        GMM_TRY(hipGetLastError());
+        S.tm = (int)grid.x;
+      } else {
+        GMM_TRY((launch_gemm<T, GRAD>(S, tiling(nr, cn, S.ktiles, false).big, s)));
       }
-      if (dw) {  // dW of the piece += G^T X of the chunk
-        RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
-        if (!p.few && (p.np_r > 1 || v0 == 0)) GMM_TRY(transpose<T>(r, coef + r0, ws + p.off_XT, P.ldgt, s));
-        GemmArgs Q{};
-        Q.A = P.GT;
-        Q.lda = P.ldgt * 2;
-        Q.pa = nv * P.ldgt * 2;
-        Q.B = ws + p.off_XT;
-        Q.ldb = P.ldgt * 2;
-        Q.pb = a.D * P.ldgt * 2;
-        Q.M = nv;
-        Q.N = a.D;
-        Q.kbytes = (int)(P.ldgt * 2);
-        Q.ktiles = (int)(P.ldgt / kt) * pairs;
-        Q.splits = p.split_w;
-        Q.scal = scal;
-        Q.out = dw + v0 * a.D * es;
-        Q.accumulate = accumulate;
-        if (p.slab_w) {
-          Q.slab = reinterpret_cast<float*>(ws + p.off_sw);
-          Q.lds = p.lds;
-          Q.slab_stride = std::min(p.vc, a.V) * p.lds;
-          Q.add = r0 > 0;
-        }
-        if (p.few) {
-          FewArgs F = few_args(a, r0, nr);
-          F.b = Q.A;
-          F.ldb = Q.lda;
-          F.pb = Q.pa;
-          F.splits = Q.splits;
-          F.slab = Q.slab;
-          F.lds = Q.lds;
-          F.slab_stride = Q.slab_stride;
-          F.add = Q.add;
-          F.live = coef + r0;
-          GMM_TRY(launch_xent_few_dw(F, s));
-        } else {
-          GMM_TRY((launch_gemm<T, OUT>(Q, p.big_w, s)));
-        }
-        if (p.slab_w && r0 + nr >= R) {
-          GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nv, a.D, scal, nullptr, Q.out, accumulate, s));
-        }
+      if (db) {
+        float *out = db + v0 + c0, *run = reinterpret_cast<float*>(ws + p.off_dbr) + (p.rows_out ? v0 : 0) + c0;
+        GMM_TRY(dbias(S.dbp, S.tm, cn, scal, accumulate ? run : out, out, r0 == 0, r0 + nr >= R, accumulate, s));
+      }
+      return hipSuccess;
+    };
+    const int64_t first = p.slab_l ? nv : whole_rounds(nr, nv, P.ktiles);
+    GMM_TRY(columns(0, first));
+    if (first < nv) GMM_TRY(columns(first, nv - first));
+    if (dx) {  // dX of the chunk += G W of the piece
+      GemmArgs Q{};
+      Q.A = P.G;
+      Q.lda = P.ldg * 2;
+      Q.pa = nr * P.ldg * 2;
+      Q.B = ws + p.off_WT;
+      Q.ldb = P.ldg * 2;
+      Q.pb = a.D * P.ldg * 2;
+      Q.M = nr;
+      Q.N = a.D;
+      Q.kbytes = (int)(P.ldg * 2);
+      Q.ktiles = (int)(P.ldg / kt) * pairs;
+      Q.splits = std::min<int>(p.split_x, Q.ktiles);
+      Q.scal = scal;
+      Q.rowlive = coef + r0;
+      Q.out = dx + r0 * a.D * es;
+      Q.accumulate = accumulate;
+      if (p.slab_x) {
+        Q.splits = p.split_x;  // every slab is written by the first piece; empty k ranges add zeros
+        Q.slab = reinterpret_cast<float*>(ws + p.off_sx) + (p.keep_x ? r0 * p.lds : 0);
+        Q.lds = p.lds;
+        Q.slab_stride = nr * p.lds;
+        Q.add = v0 > 0;
+      }
+      GMM_TRY((launch_gemm<T, OUT>(Q, p.big_x, s)));
+      if (p.slab_x && v0 + nv >= a.V) {
+        GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nr, a.D, scal, coef + r0, Q.out, accumulate, s));
       }
     }
+    if (dw) {  // dW of the piece += G^T X of the chunk
+      RowsArgs r{(const char*)a.x, a.N, a.ld, a.stride_b, r0, nr, (int)a.D};
+      if (!p.few && new_rows) GMM_TRY(transpose<T>(r, coef + r0, ws + p.off_XT, P.ldgt, s));
+      GemmArgs Q{};
+      Q.A = P.GT;
+      Q.lda = P.ldgt * 2;
+      Q.pa = nv * P.ldgt * 2;
+      Q.B = ws + p.off_XT;
+      Q.ldb = P.ldgt * 2;
+      Q.pb = a.D * P.ldgt * 2;
+      Q.M = nv;
+      Q.N = a.D;
+      Q.kbytes = (int)(P.ldgt * 2);
+      Q.ktiles = (int)(P.ldgt / kt) * pairs;
+      Q.splits = p.split_w;
+      Q.scal = scal;
+      Q.out = dw + v0 * a.D * es;
+      Q.accumulate = accumulate;
+      if (p.slab_w) {
+        Q.slab = reinterpret_cast<float*>(ws + p.off_sw) + (p.keep_w ? v0 * p.lds : 0);
+        Q.lds = p.lds;
+        Q.slab_stride = std::min(p.vc, a.V) * p.lds;
+        Q.add = r0 > 0;
+      }
+      if (p.few) {
+        FewArgs F = few_args(a, r0, nr);
+        F.b = Q.A;
+        F.ldb = Q.lda;
+        F.pb = Q.pa;
+        F.splits = Q.splits;
+        F.slab = Q.slab;
+        F.lds = Q.lds;
+        F.slab_stride = Q.slab_stride;
+        F.add = Q.add;
+        F.live = coef + r0;
+        GMM_TRY(launch_xent_few_dw(F, s));
+      } else {
+        GMM_TRY((launch_gemm<T, OUT>(Q, p.big_w, s)));
+      }
+      if (p.slab_w && r0 + nr >= R) {
+        GMM_TRY(finish<T>(Q.slab, Q.splits, Q.slab_stride, p.lds, nv, a.D, scal, nullptr, Q.out, accumulate, s));
+      }
+    }
+    return hipSuccess;
+  };
+  if (p.rows_out) {
+    for (int64_t r0 = 0; r0 < R; r0 += p.nc)
+      for (int64_t v0 = 0; v0 < a.V; v0 += p.vc) GMM_TRY(part(r0, v0));
+  } else {
+    for (int64_t v0 = 0; v0 < a.V; v0 += p.vc)
+      for (int64_t r0 = 0; r0 < R; r0 += p.nc) GMM_TRY(part(r0, v0));
   }
   return hipSuccess;
 }

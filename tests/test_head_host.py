@@ -183,3 +183,28 @@ def test_lookup_refuses_rows_of_more_than_4096_codes():
     assert L.gmm_codebook_lookup(ctypes.byref(t), 2, 4097, p, None, 1.0, p, None) == UNS
     assert L.gmm_codebook_lookup_grad(ctypes.byref(t), 5, 4097, p, None, 1.0, None, p, None, 0, p, 1 << 20, None) == UNS
     assert L.gmm_codebook_lookup_grad_workspace_bytes(ctypes.byref(t), 5, 4097) == 0
+
+
+def _grad_bytes(N, D, V, dtype=_abi.DT_BF16, want=7):
+    return _abi.lib().gmm_softmax_xent_grad_workspace_bytes(ctypes.byref(rows(N=N, D=D, dtype=dtype)),
+                                                            ctypes.byref(head(V=V, D=D, dtype=dtype)), want)
+
+
+@pytest.mark.parametrize("want", [1, 2, 4, 7])
+@pytest.mark.parametrize("N,D,V,dtype", [(10 ** 6, 768, 16384, _abi.DT_BF16), (1 << 20, 256, 32768, _abi.DT_F32),
+                                         (1 << 24, 256, 32768, _abi.DT_BF16), (10 ** 6, 256, 50000, _abi.DT_BF16),
+                                         (10 ** 6, 1000, 200, _abi.DT_F16)])
+def test_gradient_workspaces_do_not_grow_with_the_rows(N, D, V, dtype, want):
+    """Rows in chunks: beside the chunks' parts there is a coefficient per row
+    (4 bytes), and one float32 slab of the smaller side where the classes are
+    in pieces too."""
+    a, b = _grad_bytes(N, D, V, dtype, want), _grad_bytes(2 * N, D, V, dtype, want)
+    assert 0 < a < 3 << 30 and 0 < b - a <= 4 * N + 256
+
+
+@pytest.mark.parametrize("want", [1, 2, 4, 7])
+def test_gradient_workspaces_do_not_grow_with_the_classes(want):
+    N, D = 40000, 256
+    a, b = _grad_bytes(N, D, 10 ** 6, want=want), _grad_bytes(N, D, 8 * 10 ** 6, want=want)
+    assert 0 < a == b < 3 << 30
+    assert 0 <= _grad_bytes(2 * N, D, 10 ** 6, want=want) - a <= (4 * D + 4) * N + 512
