@@ -416,3 +416,63 @@ def test_bias_gradient_over_chunks_of_rows_is_added_once(g, dtype, N, D, V):
     s = old.double() + want["db"]
     ref.within("db", acc, s, tol["db"] + 1.01 * ref.U * (s.abs() + tol["db"]))
     assert torch.equal(acc, old + db)
+
+
+def in_pieces(g, N, D, V, dtype):
+    """Whether a gradient call forms G in pieces: its workspace for the bias
+    gradient alone, which is one piece and little else, is below all of G."""
+    import ctypes
+
+    from soft_clustering_em_amd import _abi
+    code = {"f32": _abi.DT_F32, "bf16": _abi.DT_BF16, "f16": _abi.DT_F16}[dtype]
+    d = _abi.GmmData(ctypes.c_void_p(256), code, 1, N, D, D, N * D)
+    h = _abi.GmmHead(ctypes.c_void_p(1 << 40), code, V, D, None)
+    n = _abi.lib().gmm_softmax_xent_grad_workspace_bytes(ctypes.byref(d), ctypes.byref(h), 4)
+    return 0 < n < N * V * (6 if dtype == "f32" else 2)
+
+
+@pytest.mark.parametrize("dtype,N,D,V", [
+    ("bf16", 40000, 136, 5000), ("f32", 20000, 136, 4500),    # chunks of rows
+    ("bf16", 5000, 136, 40000), ("f32", 4500, 130, 20000),    # pieces of the classes
+    ("bf16", 33000, 136, 33000), ("f32", 33000, 136, 33300),  # both, classes in the outer loop
+    ("f16", 34000, 130, 33000), ("f32", 33500, 136, 33000),   # both, rows in the outer loop
+    ("f16", 33000, 131, 34000)])
+def test_wide_rows_in_chunks_and_classes_in_pieces(g, dtype, N, D, V):
+    """Rows and head past what one piece of G holds, the last chunk and piece
+    shorter than the others, written and added."""
+    assert in_pieces(g, N, D, V, dtype)
+    X, W, b, y, gl = make(N, D, V, dtype, ignored=0.02)
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    want, tol = ref.xent(X, W, y, b, gl)
+    ref.within("lse", lse, want["lse"], tol["lse"])
+    ref.within("loss", loss, want["loss"], tol["loss"])
+    got = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b)
+    for name, t in zip(("dX", "dW", "db"), got):
+        ref.within(name, t, want[name], tol[name])
+    old = [torch.randn_like(t) for t in got]
+    acc = [t.clone() for t in old]
+    g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, dX=acc[0], dW=acc[1], dbias=acc[2], accumulate=True)
+    for name, o, a in zip(("dX", "dW", "db"), old, acc):
+        s = want[name] + o.double()
+        ref.within(name, a, s, tol[name] + (ref.half(a.dtype) + 2 * ref.U) * (s.abs() + o.double().abs() + tol[name]))
+    # one of the gradients alone
+    for i, only in ((0, dict(dW=False, dbias=False)), (1, dict(dX=False, dbias=False)), (2, dict(dX=False, dW=False))):
+        assert torch.equal(g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, **only)[i], got[i])
+
+
+@pytest.mark.parametrize("dtype,N,D,V", [("bf16", 22000, 136, 100000), ("f32", 22000, 130, 100000)])
+def test_loss_of_wide_rows_in_chunks(g, dtype, N, D, V):
+    """More than 2^24 (maximum, sum) pairs: the loss takes the rows in chunks."""
+    assert (V + 127) // 128 * N > 1 << 24
+    X, W, b, y, gl = make(N, D, V, dtype, ignored=0.02)
+    loss, lse = g.gmm_softmax_xent(X, W, y, bias=b)
+    want, tol = ref.xent(X, W, y, b, gl, rows=1 << 11)
+    ref.within("lse", lse, want["lse"], tol["lse"])
+    ref.within("loss", loss, want["loss"], tol["loss"])
+
+
+@pytest.mark.parametrize("dtype,N,D,V,offset", [("f32", (1 << 20) + 77, 24, 30, 0), ("bf16", (1 << 20) + 77, 33, 12, 1),
+                                                ("f32", 200, 24, (1 << 18) + 100, 0), ("f16", 130, 33, (1 << 18) + 100, 1)])
+def test_narrow_rows_and_classes_copied_in_chunks(g, dtype, N, D, V, offset):
+    """Rows past 2^20 and classes past 2^18 that are copied to aligned ones first."""
+    check(g, *make(N, D, V, dtype, ignored=0.02, offset=offset))
