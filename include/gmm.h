@@ -452,11 +452,11 @@ typedef struct {
 } gmm_tensor;
 
 /* The 2-norm over every element of `count` gradients, and the gradients scaled
- * so that it is at most max_norm (>= 0; infinity: the norm and a copy):
+ * so that it is at most max_norm (>= 0; infinity: the norm and a copy, whatever the norm):
  *   norm = sqrt(sum g^2);  dst = min(1, max_norm / (norm + 1e-6)) src
- * norm float32 device, nullable.  Squares and sums are float64.  An infinite
- * norm scales by 0 (infinite elements become NaN), a NaN norm makes every
- * element NaN.  `grads` is host memory, read during the call.  No dst may
+ * norm float32 device, nullable.  Squares and sums are float64.  Under a finite
+ * max_norm an infinite norm scales by 0 (infinite elements become NaN), and a
+ * NaN norm makes every element NaN.  `grads` is host memory, read during the call.  No dst may
  * overlap another tensor, nor its own src in part.  Workspace:
  * gmm_clip_grad_norm_workspace_bytes.  Deterministic. */
 size_t gmm_clip_grad_norm_workspace_bytes(int32_t count);

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) coefficient_kernel(const double* part, in
   __syncthreads();
   if (threadIdx.x != 0) return;
   const double v = sqrt((red[0] + red[1]) + (red[2] + red[3]));
-  const double c = max_norm / (v + 1e-6);
+  const double c = max_norm == INFINITY ? 1.0 : max_norm / (v + 1e-6);  // no limit: a copy, also under an infinite norm
   if (norm) *norm = (float)v;
   *coef = c < 1.0 || c != c ? (float)c : 1.f;  // a NaN norm gives NaN gradients
 }

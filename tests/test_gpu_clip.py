@@ -97,3 +97,15 @@ def test_captured(g):
         torch.cuda.synchronize()
         assert torch.equal(norm, g.gmm_clip_grad_norm(grads, 1.0, out=eager)), k
         assert all(torch.equal(a, b) for a, b in zip(outs, eager)), k
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan"), 1.0])
+def test_no_limit_copies_whatever_the_norm(g, bad):
+    grads = make([100, 70000, 7], [F32, BF16, F16])
+    grads[0][3] = bad
+    kept = [t.clone() for t in grads]
+    outs = [torch.empty_like(t) for t in grads]
+    for norm in (g.gmm_clip_grad_norm(grads, float("inf"), out=outs), g.gmm_clip_grad_norm(grads, float("inf"))):
+        assert math.isfinite(float(norm)) == math.isfinite(bad)
+    for k, o, t in zip(kept, outs, grads):
+        assert torch.equal(k.view(torch.uint8), o.view(torch.uint8)) and torch.equal(k.view(torch.uint8), t.view(torch.uint8))
