@@ -1596,7 +1596,7 @@ gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max
   gmm_status st = check_ws(ws, ws_bytes, need);
   if (st != GMM_OK) return st;
   double* part = static_cast<double*>(ws);
-  float* coef = reinterpret_cast<float*>(static_cast<char*>(ws) + need - kAlign);
+  double* coef = reinterpret_cast<double*>(static_cast<char*>(ws) + need - kAlign);
   const hipError_t e = launch_clip(t.data(), count, max_norm, norm, part, coef, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "gradient clipping launch");
   return GMM_OK;

@@ -42,8 +42,8 @@ __device__ inline double squares(const T* p, int64_t n) {
   return s;
 }
 
-template <typename T>
-__device__ inline void scaled(const T* p, T* q, int64_t n, float c) {
+template <typename T, typename C>
+__device__ inline void scaled(const T* p, T* q, int64_t n, C c) {
   constexpr int E = 16 / (int)sizeof(T);
   const int64_t nv = n / E;
   const bool aligned = (uintptr_t)q % 16 == 0;  // stored past the caches: nobody reads it back soon
@@ -52,13 +52,13 @@ __device__ inline void scaled(const T* p, T* q, int64_t n, float c) {
     T v[E];
     __builtin_memcpy(v, p + t * E, 16);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (T)(c * (float)v[e]);
+    for (int e = 0; e < E; ++e) v[e] = (T)(float)(c * (C)(float)v[e]);
     if (aligned) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(q + t * E));
     else __builtin_memcpy(q + t * E, v, 16);
   }
   if ((int)threadIdx.x < n - nv * E) {
     const int64_t i = nv * E + threadIdx.x;
-    q[i] = (T)(c * (float)p[i]);
+    q[i] = (T)(float)(c * (C)(float)p[i]);
   }
 }
 
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(256) norm_kernel(ClipArgs A) {
 }
 
 __global__ void __launch_bounds__(256) coefficient_kernel(const double* part, int n, double max_norm, float* norm,
-                                                          float* coef) {
+                                                          double* coef) {
   __shared__ double red[4];
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += 256) s += part[i];
@@ -100,15 +100,15 @@ __global__ void __launch_bounds__(256) coefficient_kernel(const double* part, in
   const double v = sqrt((red[0] + red[1]) + (red[2] + red[3]));
   const double c = max_norm == INFINITY ? 1.0 : max_norm / (v + 1e-6);  // no limit: a copy, also under an infinite norm
   if (norm) *norm = (float)v;
-  *coef = c < 1.0 || c != c ? (float)c : 1.f;  // a NaN norm gives NaN gradients
+  *coef = c < 1.0 || c != c ? c : 1.0;  // a NaN norm gives NaN gradients
 }
 
-// from the last piece to the first: the norm's pass left the last ones in the caches
-__global__ void __launch_bounds__(256) scale_kernel(ClipArgs A, const float* coef) {
-  const float c = *coef;
+template <typename C>
+__device__ inline void scale_pieces(const ClipArgs& A, C c) {
+  // from the last piece to the first: the norm's pass left the last ones in the caches
   for (int64_t p = A.pieces - 1 - blockIdx.x; p >= 0; p -= gridDim.x) {
     const ClipTensor& t = A.t[tensor_of(A, p)];
-    if (c == 1.f && t.src == t.dst) continue;
+    if (c == C(1) && t.src == t.dst) continue;
     const int64_t i0 = (p - t.piece0) * kClipPiece, n = min(kClipPiece, t.n - i0);
     if (t.dtype == 0) scaled(static_cast<const float*>(t.src) + i0, static_cast<float*>(t.dst) + i0, n, c);
     else if (t.dtype == 1) scaled(static_cast<const __bf16*>(t.src) + i0, static_cast<__bf16*>(t.dst) + i0, n, c);
@@ -116,9 +116,17 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipArgs A, const float* coe
   }
 }
 
+// The products are float32, float64 where the coefficient has fewer bits in
+// float32 than its 24 (gradients of 1e25 and more under a small limit).
+__global__ void __launch_bounds__(256) scale_kernel(ClipArgs A, const double* coef) {
+  const double c = *coef;
+  if (c > 0.0 && c < 0x1p-100) scale_pieces(A, c);
+  else scale_pieces(A, (float)c);
+}
+
 }  // namespace
 
-hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, float* coef,
+hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, double* coef,
                        hipStream_t s) {
   int nparts = 0;
   for (int phase = 0; phase < 2; ++phase) {

@@ -374,7 +374,7 @@ struct ClipArgs {
   int64_t pieces;
   double* part;
 };
-hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, float* coef,
+hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, double* coef,
                        hipStream_t s);
 
 // fused E-step + statistics (gmm_estep.hip)

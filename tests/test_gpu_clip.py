@@ -109,3 +109,13 @@ def test_no_limit_copies_whatever_the_norm(g, bad):
         assert math.isfinite(float(norm)) == math.isfinite(bad)
     for k, o, t in zip(kept, outs, grads):
         assert torch.equal(k.view(torch.uint8), o.view(torch.uint8)) and torch.equal(k.view(torch.uint8), t.view(torch.uint8))
+
+
+@pytest.mark.parametrize("scale,max_norm", [(1e25, 1e-15), (1e25, 1e-30), (1e30, 1e-7), (1.0, 1e-41), (1e-20, 1e-37)])
+def test_coefficients_below_float32s_normal_values(g, scale, max_norm):
+    grads = make([1000, 20001, 7], [F32, BF16], scale=scale)
+    outs = [torch.empty_like(t) for t in grads]
+    norm = g.gmm_clip_grad_norm(grads, max_norm, out=outs)
+    check(grads, outs, norm, max_norm)
+    same = g.gmm_clip_grad_norm(grads, max_norm)  # in place
+    assert torch.equal(norm, same) and all(torch.equal(a, b) for a, b in zip(grads, outs))
