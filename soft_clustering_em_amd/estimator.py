@@ -422,7 +422,9 @@ class SoftmaxHead:
     row out), each step one gmm_softmax_xent, one gmm_softmax_xent_grad and,
     with max_grad_norm, one gmm_clip_grad_norm over both gradients, until the
     loss changes by less than tol.  X is (N, D) float32, bfloat16 or float16 on
-    the GPU.  Fitted state: coef_ (K, D) and intercept_ (K,) float32, loss_ (the
+    the GPU; float16 rows are taken as float32 (a copy of them), because a head
+    and its gradients leave half's range: coefficients past 65504, mean gradients
+    over many classes or confident rows below 6e-8.  Fitted state: coef_ (K, D) and intercept_ (K,) float32, loss_ (the
     mean loss entering the last step), loss_history_, grad_norm_ (the last
     step's norm before clipping, None without it), n_iter_."""
 
@@ -458,12 +460,13 @@ class SoftmaxHead:
             raise ValueError("X is (N, D)")
         if y.dtype != torch.int32 or y.shape != X.shape[:1]:
             raise ValueError("y is (N,) int32")
+        return X.float() if X.dtype == torch.float16 else X
 
     def loss_and_gradients(self, X, y):
         """(mean loss, its gradients for coef_ and intercept_): a 0-dimensional
         and two float32 tensors on the GPU."""
         torch = _torch()
-        self._check(X, y)
+        X = self._check(X, y)
         if not hasattr(self, "coef_"):
             raise RuntimeError("call fit first")
         y = y.contiguous()
@@ -476,7 +479,7 @@ class SoftmaxHead:
 
     def fit(self, X, y):
         torch = _torch()
-        self._check(X, y)
+        X = self._check(X, y)
         if not hasattr(self, "coef_"):
             self._set(torch.zeros(self.n_classes, X.shape[1], device=X.device),
                       torch.zeros(self.n_classes, device=X.device))
@@ -497,7 +500,7 @@ class SoftmaxHead:
 
     def log_proba(self, X, y):
         """log p(y_i | x_i) of every row (0 where the label is negative), (N,) float32."""
-        self._check(X, y)
+        X = self._check(X, y)
         if not hasattr(self, "coef_"):
             raise RuntimeError("call fit first")
         return -gmm_softmax_xent(X, self.coef_.to(X.dtype), y.contiguous(), bias=self.intercept_)[0]

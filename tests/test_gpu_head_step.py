@@ -177,3 +177,42 @@ def test_refusals_on_the_gpu(g):
     for bad in (lambda: SoftmaxHead(3).score(X, y), lambda: KMeans(2).reconstruct(y)):
         with pytest.raises(RuntimeError):
             bad()
+
+
+def test_head_of_half_rows_keeps_small_gradients(g):
+    """Confident rows: the gradients of the other classes are about exp(-25) of
+    a row, far below half's spacing, and come inside float32's bound."""
+    from soft_clustering_em_amd.estimator import SoftmaxHead
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn(1500, 24, generator=gen, device="cuda").half()
+    y = torch.zeros(1500, dtype=torch.int32, device="cuda")
+    coef = torch.randn(2000, 24, generator=gen, device="cuda") * 0.1
+    b = torch.zeros(2000, device="cuda")
+    b[0] = 25.0
+    loss, dW, db = SoftmaxHead(2000)._set(coef, b).loss_and_gradients(X, y)
+    want, tol = ref.xent(X.float(), coef, y, b, torch.full((1500,), 1.0 / 1500, device="cuda"))
+    assert 0 < float(want["dW"][1:].abs().max()) < 6e-8
+    ref.within("dW", dW, want["dW"], tol["dW"] + 4 * ref.U * want["dW"].abs())
+    ref.within("db", db, want["db"], tol["db"] + 4 * ref.U * want["db"].abs())
+
+
+def test_head_of_half_rows_with_coefficients_past_half(g):
+    from soft_clustering_em_amd.estimator import SoftmaxHead
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.randn(700, 40, generator=gen, device="cuda").half()
+    y = torch.randint(-1, 20, (700,), generator=gen, device="cuda", dtype=torch.int32)
+    coef, b = torch.randn(20, 40, generator=gen, device="cuda") * 1e6, torch.zeros(20, device="cuda")
+    head = SoftmaxHead(20)._set(coef, b)
+    want, tol = ref.xent(X.float(), coef, y, b)
+    ref.within("log_proba", -head.log_proba(X, y), want["loss"], tol["loss"])
+    assert math.isfinite(head.score(X, y)) and all(torch.isfinite(t).all() for t in head.loss_and_gradients(X, y))
+
+
+def test_head_fit_of_half_rows_is_the_fit_of_the_same_float32_rows(g):
+    from soft_clustering_em_amd.estimator import SoftmaxHead
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    X = torch.randn(900, 24, generator=gen, device="cuda").half()
+    y = torch.randint(-1, 300, (900,), generator=gen, device="cuda", dtype=torch.int32)
+    a, b = (SoftmaxHead(300, max_iter=3, max_grad_norm=0.01).fit(rows, y) for rows in (X, X.float()))
+    assert torch.equal(a.coef_, b.coef_) and torch.equal(a.intercept_, b.intercept_)
+    assert torch.equal(a.grad_norm_, b.grad_norm_) and a.loss_history_ == b.loss_history_
