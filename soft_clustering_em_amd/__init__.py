@@ -383,6 +383,8 @@ class _on:
         for t in tensors:
             if t is not None and (index < 0 or t.get_device() != index):
                 raise ValueError(f"every tensor must be on one GPU (got {t.device} and {tensors[0].device})")
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {tensors[0].device}")
         # a guard costs microseconds: none where the call changes nothing
         self.guards = [torch.cuda.device(index)] if torch.cuda.current_device() != index else []
         if stream is not None:

@@ -208,3 +208,22 @@ def test_gradient_workspaces_do_not_grow_with_the_classes(want):
     a, b = _grad_bytes(N, D, 10 ** 6, want=want), _grad_bytes(N, D, 8 * 10 ** 6, want=want)
     assert 0 < a == b < 3 << 30
     assert 0 <= _grad_bytes(2 * N, D, 10 ** 6, want=want) - a <= (4 * D + 4) * N + 512
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Two devices are stood in for: the check comes before any call to a GPU."""
+    import torch
+
+    from soft_clustering_em_amd import _on
+
+    class On:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+        def get_device(self):
+            return self.device.index
+
+    with pytest.raises(ValueError, match="stream"):
+        _on(On(1), On(0), None, On(0))
+    with pytest.raises(ValueError, match="one GPU"):
+        _on(On(0), On(0), On(1))
