@@ -411,6 +411,13 @@ def _expect(name, t, dtype, shape):
                          f"(got {t.dtype}, {tuple(t.shape)})")
 
 
+def _check_ws(ws):
+    """A caller's workspace is one block of ws.numel() elements: an expanded or
+    strided view covers less, or more, than it counts."""
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor")
+
+
 def _rows(name, t):
     """The gmm_data of rows at any strides that keep D contiguous and rows apart."""
     torch = _torch()
@@ -453,6 +460,7 @@ def gmm_softmax_xent(X, W, labels, bias=None, loss=None, lse=None, ws=None, stre
     d, h = _rows("X", X), _head(X, W, bias)
     lead = X.shape[:-1]
     _expect("labels", labels, torch.int32, lead)
+    _check_ws(ws)
     with _on(stream, X, W, labels, bias, loss, lse, ws) as s:
         loss = torch.empty(lead, dtype=torch.float32, device=X.device) if loss is None else loss
         lse = torch.empty(lead, dtype=torch.float32, device=X.device) if lse is None else lse
@@ -486,6 +494,7 @@ def gmm_softmax_xent_grad(X, W, labels, lse, gloss=None, bias=None, dX=None, dW=
     lead = X.shape[:-1]
     _expect("labels", labels, torch.int32, lead)
     _expect("lse", lse, torch.float32, lead)
+    _check_ws(ws)
     if gloss is not None:
         _expect("gloss", gloss, torch.float32, lead)
     if bias is None and dbias is None:
@@ -559,6 +568,7 @@ def gmm_codebook_lookup_grad(dout, idx, K, table=None, weights=None, scale=1.0, 
     B, N, m, lead = _code_shape(dout.dim(), idx, weights)
     if (B, N) != (d.B, d.N):
         raise ValueError("idx and dout differ in their rows")
+    _check_ws(ws)
     t = None
     if table is not None:
         if table.dtype != dout.dtype or table.dim() != dout.dim() or table.shape[-1] != dout.shape[-1] \
@@ -605,6 +615,7 @@ def gmm_clip_grad_norm(grads, max_norm, out=None, norm=None, ws=None, stream=Non
         raise ValueError("need one gradient or more")
     if len(outs) != len(grads):
         raise ValueError("out must hold one tensor per gradient")
+    _check_ws(ws)
     codes = {torch.float32: _abi.DT_F32, torch.bfloat16: _abi.DT_BF16, torch.float16: _abi.DT_F16}
     desc = array("q")  # a gmm_tensor is four 8-byte words: src, dst, n, dtype
     for i, (g, o) in enumerate(zip(grads, outs)):

@@ -227,3 +227,16 @@ def test_a_stream_of_another_device_is_refused():
         _on(On(1), On(0), None, On(0))
     with pytest.raises(ValueError, match="one GPU"):
         _on(On(0), On(0), On(1))
+
+
+def test_workspaces_that_count_more_than_they_hold_are_refused():
+    import torch
+
+    import soft_clustering_em_amd as g
+    X, W, z = torch.randn(4, 8), torch.randn(5, 8), torch.zeros(4)
+    y = torch.zeros(4, dtype=torch.int32)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 12, dtype=torch.uint8)[::2]):
+        for call in (lambda: g.gmm_softmax_xent(X, W, y, ws=ws), lambda: g.gmm_softmax_xent_grad(X, W, y, z, ws=ws),
+                     lambda: g.gmm_codebook_lookup_grad(X, y, 5, ws=ws), lambda: g.gmm_clip_grad_norm([X], 1.0, ws=ws)):
+            with pytest.raises(ValueError, match="ws must"):
+                call()
