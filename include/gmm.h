@@ -457,7 +457,7 @@ typedef struct {
  * norm float32 device, nullable.  Squares and sums are float64.  Under a finite
  * max_norm an infinite norm scales by 0 (infinite elements become NaN), and a
  * NaN norm makes every element NaN.  `grads` is host memory, read during the call.  No dst may
- * overlap another tensor, nor its own src in part.  Workspace:
+ * overlap another tensor, nor its own src in part; norm may overlap none.  Workspace:
  * gmm_clip_grad_norm_workspace_bytes.  Deterministic. */
 size_t gmm_clip_grad_norm_workspace_bytes(int32_t count);
 gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max_norm, float* norm, void* ws,

@@ -1591,6 +1591,7 @@ gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max
     if (s.out ? s.p < end_any : s.p < end_out) return fail(GMM_ERR_INVALID_ARG, "gradient %d overlaps another tensor", s.tensor);
     end_any = std::max(end_any, s.q);
     if (s.out) end_out = std::max(end_out, s.q);
+    if (overlap(norm, sizeof(float), s.p, s.q - s.p)) return fail(GMM_ERR_INVALID_ARG, "norm overlaps gradient %d", s.tensor);
   }
   const size_t need = gmm_clip_grad_norm_workspace_bytes(count);
   gmm_status st = check_ws(ws, ws_bytes, need);

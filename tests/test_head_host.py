@@ -240,3 +240,16 @@ def test_workspaces_that_count_more_than_they_hold_are_refused():
                      lambda: g.gmm_codebook_lookup_grad(X, y, 5, ws=ws), lambda: g.gmm_clip_grad_norm([X], 1.0, ws=ws)):
             with pytest.raises(ValueError, match="ws must"):
                 call()
+
+
+def test_clip_refuses_a_norm_on_a_gradient():
+    """It would be written before the gradients are read for the scaling."""
+    L = _abi.lib()
+    a, b = 1 << 40, 2 << 40
+    arr = (_abi.GmmTensor * 2)(_abi.GmmTensor(a, b, 10, 0), _abi.GmmTensor(a + 64, a + 64, 10, 1))
+    # accepted operands stop at the missing workspace: nothing reaches a GPU
+    clip = lambda norm: L.gmm_clip_grad_norm(arr, 2, 1.0, P(norm), None, 0, None)  # noqa: E731
+    for at in (a, a + 36, b, b + 36, a + 64, a + 80):
+        assert clip(at) == INV and "norm overlaps" in last()
+    for at in (a + 40, b + 40, a - 4, a + 84, 3 << 40):
+        assert clip(at) == WSE
