@@ -431,6 +431,8 @@ class SoftmaxHead:
     def __init__(self, n_classes, learning_rate=1.0, momentum=0.9, max_iter=100, tol=1e-6, max_grad_norm=None):
         if int(n_classes) < 1:
             raise ValueError("n_classes must be >= 1")
+        if int(max_iter) < 1:
+            raise ValueError("max_iter must be >= 1")
         if max_grad_norm is not None and not float(max_grad_norm) > 0.0:
             raise ValueError("max_grad_norm must be > 0")
         self.n_classes = int(n_classes)

@@ -253,3 +253,10 @@ def test_clip_refuses_a_norm_on_a_gradient():
         assert clip(at) == INV and "norm overlaps" in last()
     for at in (a + 40, b + 40, a - 4, a + 84, 3 << 40):
         assert clip(at) == WSE
+
+
+def test_head_refuses_no_iterations():
+    from soft_clustering_em_amd.estimator import SoftmaxHead
+    for n in (0, -3):
+        with pytest.raises(ValueError, match="max_iter"):
+            SoftmaxHead(3, max_iter=n)
