@@ -8,7 +8,7 @@
 // calls can be captured into a graph.  Bound by memory: the gradients are
 // read twice and written once (in place with c = 1: nothing is written).
 // 340M elements, 0.85 GB: norm 137 us (6.2 TB/s, part of it from the caches),
-// scale 271 (6.3 TB/s read and written).
+// scale 267 (6.4 TB/s read and written).
 #include "gmm_internal.h"
 
 #include <hip/hip_runtime.h>

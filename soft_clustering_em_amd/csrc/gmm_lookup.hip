@@ -15,9 +15,10 @@
 //   dw       a group of up to 64 lanes per row, the dot products over it.
 //   dT       deterministic, no global atomics: the entries are sorted by code
 //            (up to 8192 entries by ranks in one launch; above by a stable
-//            radix sort of at most 10 bits a pass: block histograms, their
-//            prefixes, ranks by ballot), then summed in that order in
-//            chunks of entries.  A run of one code inside a chunk is written
+//            radix sort of at most 10 bits a pass, three launches each: block
+//            histograms, their prefixes, ranks by ballot; entries that take no
+//            part go along under a key past every code's), then summed
+//            in that order in chunks of entries.  A run of one code inside a chunk is written
 //            at once; a run that crosses a chunk's ends leaves partial sums,
 //            which a last kernel joins, so that a code with most of the
 //            entries is summed by as many workgroups as many codes are.

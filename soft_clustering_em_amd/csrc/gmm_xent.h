@@ -145,7 +145,8 @@ int xent_small_rows(int dtype, int64_t D, int pass);  // owner rows of a workgro
 int xent_small_splits(int64_t owners, int64_t streamed, int dtype, int64_t D, int pass);
 
 // Arguments of the kernels for wide float32 rows and at most 128 classes
-// (gmm_xent_few.hip), 64 a workgroup.
+// (gmm_xent_few.hip), 64 a workgroup: above 64 the rows are read twice.  The
+// border goes by the classes alone; near it the two ways are within a few percent.
 // Loss and gradients here and through tiles of 128 x 128: 65536 x 512, 64
 // classes, 332 and 633 us; 20000 x 2000, 64 classes, 414 and 617; 65536 x 512, 128
 // classes, 547 and 675; 57491 x 2410, 128 classes, 2453 and 2493; 2000 x 700, 100

@@ -20,10 +20,13 @@
 // few tiles over a long k run as OUT too, in parts of k side by side, and two
 // small kernels do the other epilogues from the parts' sum (logit_parts).
 // A piece is at most 2^27 (float32: 2^26) elements of G, whatever N and V.
-// Recomputing the logits costs a third more arithmetic than keeping them and
-// takes their N V floats out of memory.  W and X enter the OUT products
-// transposed (a piece of W, the rows of a chunk: copies of a few percent of
-// the product's traffic), so that one main loop serves all three.
+// The gradients form the logits again, a third more arithmetic (4096 x 4096
+// rows, 65536 classes, bf16: 1.8 ms), and no N V floats are allocated; kept in
+// float32, chunk by chunk, they would cost 8 N V bytes written and read (0.4 ms
+// there) and a call that takes the loss and its gradients together.  W and X
+// enter the OUT products transposed, so that one main loop serves all three: a
+// copy of a piece of W and one of a chunk's rows, a few percent of the time over
+// many rows (0.24 of 7.4 ms), but most of W's traffic where the rows are few.
 //
 // The tile's operands go from global memory straight into LDS with 16-byte
 // buffer loads, two buffers, one barrier per k-tile of 128 bytes.  The loads

@@ -3,15 +3,18 @@
 //
 // With few classes the rows' bytes are everything: a product does 2 V flops for
 // the 4 bytes of an element, so the rows are read where they lie, once a
-// product, and become their three bf16 planes in registers (kPairs); copies
-// with their planes side by side and their transposes, which a product over
-// many classes repays, would be most of the traffic here.
+// product for every 64 classes (twice above 64), and become their three bf16
+// planes in registers (kPairs); copies with their planes side by side and their
+// transposes, which a product over many classes repays, would be most of the
+// traffic here.
 //   logits  X W^T, parts of k side by side in float32 slabs
 //   dW      G^T X, parts of the rows side by side in float32 slabs
 // 83230 x 2800 rows, 22 classes: the logits 293 us (3.2 TB/s: rows in pieces of
 // 256 bytes), dW 402 (2.3 TB/s, two waves a SIMD), loss and gradients 1.32 ms;
 // through packed planes and 128 x 128 tiles 600 and 1013 us, 3.4 ms.
-// 65536 x 512, 10 classes: logits 32 us (4.2 TB/s), dW 33 (4.0).
+// 65536 x 512, 10 classes: logits 32 us (4.2 TB/s), dW 33 (4.0); 64 classes 69
+// and 73 (1.9 TB/s; from 33 classes on dW's registers leave one wave a SIMD);
+// 128 classes 131 and 137.
 #include "gmm_internal.h"
 #include "gmm_xent.h"
 

@@ -15,14 +15,16 @@
 // streamed rows of one owner row: the k order that the second product's
 // fragment wants (two blocks for the 32 of an instruction), and its other
 // operand, the streamed tile with its rows along k, comes out of LDS through
-// the transposing read.  The bias enters as the accumulator's start.  Three exponentials an element (LSE, DX, DW) and 10 N V D
-// flops take the place of G's traffic, 8 bytes an element.
+// the transposing read.  The bias enters as the accumulator's start.
+// Three exponentials an element (LSE, DX, DW) and 10 N V D flops take the place
+// of G's traffic, 8 bytes an element.
 //
 // Bound by the matrix cores and the exponentials together, at the 1.9 GHz that
 // the card holds under them: 262144 x 128 rows, 4096 classes, bf16: LSE 0.32 ms,
-// DX 0.58, DW 0.67 (0.85, 0.95 and 0.82 PFLOP/s with the logits' share); 1M x 64,
-// 256 classes, float32: 0.26, 0.46, 0.42.  Two waves a SIMD: with three the
-// fragments spill (DX 0.80, DW 1.55 ms).
+// DX 0.58, DW 0.68 (0.84, 0.95 and 0.81 PFLOP/s with the logits' share); 1M x 64,
+// 256 classes, float32: 0.26, 0.47, 0.43.  Two waves a SIMD: with three the
+// fragments spill (DX 0.80, DW 1.55 ms); LSE of 128 features in 16 bits spills
+// 8 of its 256 registers with two.
 //
 // LDS: a tile's rows are RBytes = D_padded * size apart, a row's 16-byte chunk c
 // in slot c ^ f(row); f makes the reads of 16 rows touch all 64 banks.
