@@ -374,7 +374,8 @@ typedef struct {
  * or half, of one type, at any stride and alignment of their elements
  * (operands off 16 bytes are copied piecewise); logits are summed in float32
  * (float32, more than 64 rows or gradients: products of three bf16 planes, right
- * to 2^-23 of |x| |w|; elements up to bf16's largest finite value, 3.38e38; a row
+ * to 2^-23 of |x| |w|; elements up to bf16's largest finite value, 3.38e38, and
+ * with fewer bits below 2^-100, as products with a gloss below that; a row
  * or class with an infinity then has NaN results; bf16 and half rows or classes
  * with an infinity, where the definition leaves it finite, may).  The loss of 64 rows or fewer
  * takes a path that reads the head once.  Window: D <= 65536, V < 2^27, B*N < 2^28.  A row whose logits

@@ -119,3 +119,9 @@ def test_coefficients_below_float32s_normal_values(g, scale, max_norm):
     check(grads, outs, norm, max_norm)
     same = g.gmm_clip_grad_norm(grads, max_norm)  # in place
     assert torch.equal(norm, same) and all(torch.equal(a, b) for a, b in zip(grads, outs))
+
+
+def test_thousands_of_tensors(g):
+    grads = make([1 + 7 * i % 900 for i in range(3000)], [F32, BF16, F16])
+    outs = [torch.empty_like(t) for t in grads]
+    check(grads, outs, g.gmm_clip_grad_norm(grads, 1.0, out=outs), 1.0)

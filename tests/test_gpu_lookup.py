@@ -220,3 +220,13 @@ def test_long_rows(g, N, m, D, K):
     (want, tol), wdw = ref.lookup_grad(dout, idx, K, table, w, 1.0)
     ref.within("dtable", dt, want, tol)
     ref.within("dweights", dw, *wdw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_widest_rows(g, dtype):
+    table, dout, idx, w = make(40, 3, 65536, 20, dtype)
+    ref.within("rows", g.gmm_codebook_lookup(table, idx, weights=w), *ref.lookup(table, idx, w))
+    dt, dw = g.gmm_codebook_lookup_grad(dout, idx, 20, table=table, weights=w)
+    (want, tol), wdw = ref.lookup_grad(dout, idx, 20, table, w)
+    ref.within("dtable", dt, want, tol)
+    ref.within("dweights", dw, *wdw)

@@ -476,3 +476,72 @@ def test_loss_of_wide_rows_in_chunks(g, dtype, N, D, V):
 def test_narrow_rows_and_classes_copied_in_chunks(g, dtype, N, D, V, offset):
     """Rows past 2^20 and classes past 2^18 that are copied to aligned ones first."""
     check(g, *make(N, D, V, dtype, ignored=0.02, offset=offset))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("N,V", [(5, 130), (70, 130), (300, 700)])
+def test_widest_rows(g, dtype, N, V):
+    check(g, *make(N, 65536, V, dtype))
+
+
+@pytest.mark.parametrize("D", [136, 64])
+def test_rows_and_classes_as_far_apart_as_loads_reach(g, D):
+    """256 rows just inside 2^31 bytes: taken where they lie."""
+    ld = 4194296
+    big = torch.empty(300, ld, device="cuda", dtype=torch.bfloat16)
+    X, W, b, y, gl = make(300, D, 300, "bf16")
+    for far, other in ((X, W), (W, X)):
+        at = big[:, :D]
+        at.copy_(far)
+        check(g, *((at, other) if far is X else (other, at)), b, y, gl)
+
+
+def test_problems_of_one_row(g):
+    check(g, *make(1, 40, 30, "f32", B=70000))
+    check(g, *make(1, 200, 30, "bf16", B=7000, pad=8))
+
+
+@pytest.mark.parametrize("N,D", [(20, 64), (200, 64), (200, 300)])
+def test_labels_at_the_ends_of_their_type(g, N, D):
+    X, W, b, y, gl = make(N, D, 100, "bf16", ignored=0.0)
+    y[3], y[7] = -(2 ** 31), 5 - 2 ** 31
+    check(g, X, W, b, y, gl)
+    y[5] = 2 ** 31 - 1
+    loss, _ = g.gmm_softmax_xent(X, W, y, bias=b)
+    assert torch.isnan(loss[5]) and torch.isnan(loss).sum() == 1
+
+
+def test_captured_with_its_stream_named(g):
+    X, W, b, y, gl = make(300, 64, 100, "bf16")
+    want = g.gmm_softmax_xent(X, W, y, bias=b)
+    grads = g.gmm_softmax_xent_grad(X, W, y, want[1], gloss=gl, bias=b)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        loss, lse = g.gmm_softmax_xent(X, W, y, bias=b, stream=side)
+        outs = g.gmm_softmax_xent_grad(X, W, y, lse, gloss=gl, bias=b, stream=side)
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want[0]) and all(torch.equal(p, q) for p, q in zip(outs, grads))
+
+
+def test_more_than_2_27_rows(g):
+    """Row numbers past 27 bits, against a sample of the rows."""
+    N, D, V = (1 << 27) + 3, 8, 5
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn(N, D, generator=gen, device="cuda").bfloat16()
+    W = torch.randn(V, D, generator=gen, device="cuda").bfloat16()
+    y = torch.randint(-1, V, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    loss, lse = g.gmm_softmax_xent(X, W, y)
+    dX, dW, _ = g.gmm_softmax_xent_grad(X, W, y, lse)
+    at = torch.cat([torch.arange(0, N, 9973, device="cuda"), torch.arange(N - 1000, N, device="cuda")])
+    want, tol = ref.xent(X[at].contiguous(), W, y[at].contiguous())
+    for name, t in (("lse", lse), ("loss", loss), ("dX", dX)):
+        ref.within(name, t[at], want[name], tol[name])
+    # one more than the rows before the last, whose gradient is one row's
+    again = g.gmm_softmax_xent_grad(X[:-1], W, y[:-1], lse[:-1], dX=False)[1]
+    assert torch.isfinite(dW).all() and float((dW.double() - again.double()).abs().max()) <= 2 * ref.half(X.dtype) * float(dW.double().abs().max())
