@@ -18,10 +18,10 @@
 //            radix sort of at most 10 bits a pass, three launches each: block
 //            histograms, their prefixes, ranks by ballot; entries that take no
 //            part go along under a key past every code's), then summed
-//            in that order in chunks of entries.  A run of one code inside a chunk is written
-//            at once; a run that crosses a chunk's ends leaves partial sums,
-//            which a last kernel joins, so that a code with most of the
-//            entries is summed by as many workgroups as many codes are.
+//            in that order in chunks of entries.  A run of one code inside a
+//            chunk is written at once; a run that crosses a chunk's ends leaves
+//            partial sums, which a last kernel joins, so that a code with most
+//            of the entries is summed by as many workgroups as many codes are.
 // Bound by memory: every dout row is read once per entry, every dT row
 // written once.  1M x 128, 4 codes a row of 4096, float32: lookup 114 us (4.8
 // TB/s).  262144 x 128, 4 codes of 4096, float32: dw 54 us, sort 57, sums 65

@@ -1000,7 +1000,10 @@ XentPlan xent_plan(const XentArgs& a, bool grad, bool want_dx, bool want_dw, boo
     // chunks of rows and pieces of classes both: the larger side in the outer
     // loop finishes its gradients one by one, the smaller side's stay in one
     // float32 slab until the end.  No parts of k beside that slab: a chunk or
-    // piece of that side has 2^15 rows, tiles enough.
+    // piece of that side has 2^15 rows, tiles enough.  Against slabs of every row
+    // times every part: 200000 x 256 bf16, 50000 classes, 37.5 and 37.2 ms; 60000 x
+    // 256, 70000 classes, 14.2 and 14.5; 50000 x 256 float32, 40000 classes, 33.9
+    // and 32.7.
     const bool both = p.np_r > 1 && p.np_v > 1;
     p.rows_out = both && R > V;
     p.keep_x = both && !p.rows_out;

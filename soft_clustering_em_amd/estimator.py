@@ -424,9 +424,10 @@ class SoftmaxHead:
     loss changes by less than tol.  X is (N, D) float32, bfloat16 or float16 on
     the GPU; float16 rows are taken as float32 (a copy of them), because a head
     and its gradients leave half's range: coefficients past 65504, mean gradients
-    over many classes or confident rows below 6e-8.  Fitted state: coef_ (K, D) and intercept_ (K,) float32, loss_ (the
-    mean loss entering the last step), loss_history_, grad_norm_ (the last
-    step's norm before clipping, None without it), n_iter_."""
+    over many classes or confident rows below 6e-8.  Fitted state: coef_ (K, D)
+    and intercept_ (K,) float32, loss_ (the mean loss entering the last step),
+    loss_history_, grad_norm_ (the last step's norm before clipping, None without
+    it), n_iter_."""
 
     def __init__(self, n_classes, learning_rate=1.0, momentum=0.9, max_iter=100, tol=1e-6, max_grad_norm=None):
         if int(n_classes) < 1:
