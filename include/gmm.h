@@ -464,6 +464,147 @@ size_t gmm_clip_grad_norm_workspace_bytes(int32_t count);
 gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max_norm, float* norm, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* Layer norm of rows: with mean = sum_d x_d / D and r = 1 / sqrt(sum_d (x_d -
+ * mean)^2 / D + eps), per row
+ *   out_d = (x_d - mean) r gamma_d + beta_d
+ *   gamma, beta (D) of affine_dtype: float32 or the rows' type; nullable (1, 0)
+ *   out (B,N,D) in the rows' type, contiguous; mean and rstd (= r) (B,N)
+ *   float32, nullable, as gmm_layer_norm_grad takes them.
+ * The variance is that of the differences from the mean, in float32.  Any
+ * stride and alignment of the elements.  D <= 32768, B*N < 2^31.  out may not
+ * overlap an input.  N = 0 launches nothing.  No workspace. */
+gmm_status gmm_layer_norm(const gmm_data* rows, const void* gamma, const void* beta, int32_t affine_dtype, double eps,
+                          void* out, float* mean, float* rstd, void* stream);
+
+/* Its gradients, dout (B,N,D) rows of the rows' type being the gradient of
+ * out, with mean and rstd as gmm_layer_norm wrote them.  With xh = (x - mean) r
+ * and q = dout gamma:
+ *   dx (B,N,D) = r (q - sum_d q / D - xh sum_d q xh / D)
+ *   dgamma (D) = sum over the rows of dout xh;  dbeta (D) = sum of dout
+ * dx in the rows' type, contiguous, dgamma and dbeta float32; each nullable,
+ * one given.  accumulate != 0 adds to what they hold.  The gradients may not
+ * overlap each other or the inputs.  Workspace:
+ * gmm_layer_norm_grad_workspace_bytes, want = 1 (dx) + 2 (dgamma) + 4 (dbeta);
+ * it does not grow with the rows past 16384 of them.  Deterministic. */
+size_t gmm_layer_norm_grad_workspace_bytes(const gmm_data* rows, int32_t want);
+gmm_status gmm_layer_norm_grad(const gmm_data* dout, const gmm_data* rows, const float* mean, const float* rstd,
+                               const void* gamma, int32_t affine_dtype, void* dx, float* dgamma, float* dbeta,
+                               int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Routing of rows to experts (rows of D = E logits): a top-m assignment by
+ * scores, in the form that gmm_codebook_lookup and gmm_ivf_lists read.
+ *   s = softmax(l) (GMM_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (GMM_SCORE_SIGMOID)
+ *   t = s + bias_e; bias (E) float32, nullable: it takes part in the choice only
+ *   groups > 1: the experts are `groups` equal runs; a group's score is the sum of
+ *     its group_top (1 or 2) largest t, and the keep_groups groups of the largest
+ *     scores stay (ties: lower group)
+ *   idx (B,N,m) int32: the experts of the m largest t, in descending order, ties
+ *     to the lower index; -1 where fewer are left
+ *   weights (B,N,m) float32: scale s, divided by the sum of the row's selected s
+ *     if renormalize; 0 behind the last one
+ * Orders are decided on float64 scores; without a bias (and, for the groups, with
+ * group_top = 1) on the logits themselves.  An expert whose logit is -inf or NaN
+ * is never selected and has no part in the softmax; +inf counts as float32's
+ * largest value.  E <= 1024, m <= 16, groups <= 64, B*N < 2^31.  N = 0 launches
+ * nothing.  No workspace. */
+enum { GMM_SCORE_SOFTMAX = 0, GMM_SCORE_SIGMOID = 1 };
+typedef struct {
+  int32_t score;        /* GMM_SCORE_SOFTMAX or GMM_SCORE_SIGMOID */
+  int32_t groups;       /* divides E */
+  int32_t keep_groups;  /* 1 .. groups */
+  int32_t group_top;    /* 1 or 2 */
+  int32_t renormalize;
+  float scale;
+} gmm_routing;
+gmm_status gmm_route_topm(const gmm_data* logits, const float* bias, const gmm_routing* how, int32_t m, int32_t* idx,
+                          float* weights, void* stream);
+
+/* Its gradient: dlogits (B,N,E), contiguous, in the logits' type, for idx as
+ * gmm_route_topm wrote it (a row's leading values in [0, E); the first value
+ * outside ends the row), from
+ *   dweights (B,N,m) float32: the weights' gradient, nullable
+ *   dscores (E) float32: the gradient of every row's scores s, the same for all
+ *     rows (that of a balance loss), nullable; one of the two given.
+ * Experts that are switched off get 0.  The same windows; groups and bias have no
+ * part in it.  dlogits may not overlap an input. */
+gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, int32_t m, const int32_t* idx,
+                               const float* dweights, const float* dscores, void* dlogits, void* stream);
+
+/* One AdamW step over `count` tensors, in place.  With g' = c g, where c is 1 or,
+ * given a norm (float32, device, as gmm_clip_grad_norm writes it; max_norm = its
+ * limit; infinity: 1, whatever the norm), min(1, max_norm / (norm + 1e-6)):
+ *   m' = beta1 m + (1 - beta1) g';  v' = beta2 v + (1 - beta2) g'^2
+ *   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ * in float32, p' rounded once to its type and once to the copy's (param float32
+ * and a 16-bit copy: master weights).  t = step >= 1, or what step_dev (device)
+ * holds when the kernel runs (values below 1 count as 1); lr_dev likewise, so
+ * that a captured step can be replayed.
+ * States: m and v float32 (m_scale = v_scale = NULL), or 8 bits: m and v (n) OCP
+ * e4m3 bytes, m_scale and v_scale ((n + 255) / 256) float32, one for every 256
+ * elements, m = byte value x scale and sqrt(v) = byte value x scale, with scale =
+ * max / 448 of the block (0 for a block below 2^-100).  x = value / scale is rounded
+ * to the neighbour above with the probability of its remainder: up when the bits
+ * below the last kept one (as 16 bits) plus d reach 2^16, with d the upper (m) or
+ * lower (sqrt v) half of
+ *   h = mix(mix(mix(mix(seed + 0x9E3779B1 t) ^ tensor) + block) + 0x9E3779B1 i)
+ *   mix(x): x = (x ^ x >> 16) 0x9E3779B1; x = (x ^ x >> 15) 0x6A09E667; x ^ x >> 16
+ * in 32 bits, tensor its place in the call, i the element in its block; a root
+ * that is not 0 becomes 2^-9 at least.  A NaN or infinite gradient makes its
+ * element NaN, or the states of its block.
+ * Nothing written may overlap another tensor.  `tensors` is host memory, read
+ * during the call.  n < 2^40.  No workspace.  Deterministic. */
+typedef struct {
+  void* param;        /* n elements of dtype, updated */
+  const void* grad;   /* n elements of grad_dtype */
+  void* m;            /* first moments, updated */
+  void* v;            /* second moments, updated */
+  float* m_scale;
+  float* v_scale;     /* both or neither */
+  void* copy;         /* n elements of copy_dtype, written; nullable */
+  int64_t n;
+  double weight_decay;
+  int32_t dtype, grad_dtype, copy_dtype, reserved; /* gmm_dtype; reserved 0 */
+} gmm_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps;
+  double max_norm;         /* read with norm only */
+  const float* norm;       /* nullable */
+  int64_t step;
+  const int64_t* step_dev; /* nullable: step */
+  const float* lr_dev;     /* nullable: lr */
+  uint32_t seed;           /* of the 8-bit states' rounding */
+} gmm_adamw_options;
+gmm_status gmm_adamw_step(const gmm_adamw_tensor* tensors, int32_t count, const gmm_adamw_options* opts, void* stream);
+
+/* One token a row (of D = V logits), given one number u in [0, 1) a row.  With
+ * w_i = exp((l_i - max l) / temperature), the elements in descending order of l
+ * (ties: lower index) are cut to
+ *   the first top_k (top_k <= 0: all), of these
+ *   the shortest prefix whose sum of w reaches top_p of theirs (top_p >= 1: all), of these
+ *   the ones with w >= min_p (<= 0: all; above 1 counts as 1)
+ * and at least the first one.  tokens (B,N) int32: the first kept index at which
+ * the sum of the kept w, by index, exceeds u times their total; logp (B,N)
+ * float32, nullable: the log of its share of that total.  A temperature that is
+ * not above 0 takes the first element itself (logp 0).  The settings are one for
+ * all rows, or (B,N) device arrays, which go before them where given.
+ * The w are float64 values rounded to multiples of 2^-S, S = min(52, 62 -
+ * ceil(log2 V)), and summed as integers: the result does not depend on how the
+ * work is split.  Logits of -inf or NaN are left out, +inf counts as float32's
+ * largest value; a row without any other gets token -1 and logp -inf.  u outside
+ * [0, 1) (NaN too) counts as the nearer end.  V <= 2^24, B*N < 2^31.  N = 0 launches nothing.
+ * Workspace: gmm_sample_workspace_bytes. */
+typedef struct {
+  double temperature, top_p, min_p;
+  int64_t top_k;
+  const float* row_temperature;
+  const float* row_top_p;
+  const float* row_min_p;
+  const int32_t* row_top_k;
+} gmm_sampling;
+size_t gmm_sample_workspace_bytes(const gmm_data* logits);
+gmm_status gmm_sample(const gmm_data* logits, const gmm_sampling* how, const float* u, int32_t* tokens, float* logp,
+                      void* ws, size_t ws_bytes, void* stream);
+
 /* Host-side summary of a comp_status array that the caller copied to host
  * memory (count int32 values, as written by gmm_mstep / gmm_fit_step /
  * gmm_topk_fit_step): GMM_ERR_NOT_PD if any component carries flag 2 (its

@@ -28,6 +28,18 @@ torch stream; every step of the computation runs in the HIP kernels.
   gmm_clip_grad_norm(grads, max_norm, out=None, norm=None, ws=None)                   -> norm
   gmm_check_components(comp_status)          -> (status, first index or -1); synchronises
 
+  gmm_layer_norm(X, gamma=None, beta=None, eps=1e-5, out=None, mean=None, rstd=None)  -> (out, mean, rstd)
+  gmm_layer_norm_grad(dout, X, mean, rstd, gamma=None, dX=None, dgamma=None, dbeta=None, accumulate=False,
+                      ws=None)                                                        -> (dX, dgamma, dbeta)
+  gmm_route_topm(logits, m, bias=None, score="softmax", groups=1, keep_groups=None, group_top=1,
+                 renormalize=True, scale=1.0, idx=None, weights=None)                 -> (idx, weights)
+  gmm_route_topm_grad(dweights, logits, idx, score="softmax", renormalize=True, scale=1.0, dscores=None,
+                      dlogits=None)                                                   -> dlogits
+  gmm_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 m_scale=None, v_scale=None, copies=None, norm=None, max_norm=None, seed=0)   (in place)
+  gmm_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logp=None,
+             ws=None)                                                                 -> (tokens, logp)
+
 The estimator calls (score_samples, predict, score, aic, bic, fit with
 restarts) are in soft_clustering_em_amd.estimator.
 
@@ -47,8 +59,9 @@ __all__ = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step"
            "gmm_predict_proba_topm", "gmm_ivf_workspace_bytes", "gmm_ivf_lists", "gmm_kmeans_workspace_bytes",
            "gmm_kmeans_step", "gmm_fisher_vector_workspace_bytes", "gmm_fisher_vector",
            "gmm_topk_fit_workspace_bytes", "gmm_topk_fit_step", "gmm_softmax_xent", "gmm_softmax_xent_grad",
-           "gmm_codebook_lookup", "gmm_codebook_lookup_grad", "gmm_clip_grad_norm", "new_stats", "GmmError",
-           "cov_shape"]
+           "gmm_codebook_lookup", "gmm_codebook_lookup_grad", "gmm_clip_grad_norm", "gmm_layer_norm",
+           "gmm_layer_norm_grad", "gmm_route_topm", "gmm_route_topm_grad", "gmm_adamw_step", "gmm_sample",
+           "new_adamw_state", "new_stats", "GmmError", "cov_shape"]
 
 
 def _torch():
@@ -635,6 +648,280 @@ def gmm_clip_grad_norm(grads, max_norm, out=None, norm=None, ws=None, stream=Non
         _abi.check(_abi.lib().gmm_clip_grad_norm(desc.buffer_info()[0], len(grads), float(max_norm), _ptr(norm), _ptr(ws),
                                                  ws.numel() * ws.element_size(), s))
     return norm
+
+
+def gmm_layer_norm(X, gamma=None, beta=None, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows X ((N, D) or (B, N, D) float32, bfloat16 or
+    float16): out = (X - mean) rstd gamma + beta with rstd = 1 / sqrt(var + eps).
+    gamma and beta (D,): both float32 or both of X's type (None: 1 and 0).
+    Returns (out, mean, rstd): out contiguous in X's type and shape, mean and
+    rstd float32 of X's leading shape, as gmm_layer_norm_grad takes them (False
+    leaves one out)."""
+    torch = _torch()
+    d = _rows("X", X)
+    code = _affine(X, gamma, beta)
+    lead = X.shape[:-1]
+    given = [t for t in (out, mean, rstd) if t is not None and t is not False]
+    with _on(stream, X, gamma, beta, *given) as s:
+        out = torch.empty(X.shape, dtype=X.dtype, device=X.device) if out is None else out
+        mean, rstd = _wanted(mean, X, lead, torch.float32), _wanted(rstd, X, lead, torch.float32)
+        _expect("out", out, X.dtype, X.shape)
+        for name, t in (("mean", mean), ("rstd", rstd)):
+            if t is not None:
+                _expect(name, t, torch.float32, lead)
+        _abi.check(_abi.lib().gmm_layer_norm(ctypes.byref(d), _ptr(gamma), _ptr(beta), code, float(eps), _ptr(out),
+                                             _ptr(mean), _ptr(rstd), s))
+    return out, mean, rstd
+
+
+def _affine(X, gamma, beta=None):
+    """The type code of gamma and beta, float32 or X's."""
+    torch = _torch()
+    kinds = {t.dtype for t in (gamma, beta) if t is not None}
+    if len(kinds) > 1 or not kinds <= {torch.float32, X.dtype}:
+        raise ValueError("gamma and beta must both be float32 or both of X's type")
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _expect(name, t, t.dtype, X.shape[-1:])
+    return _dtype_code(gamma if gamma is not None else beta) if kinds else _abi.DT_F32
+
+
+def gmm_layer_norm_grad(dout, X, mean, rstd, gamma=None, dX=None, dgamma=None, dbeta=None, accumulate=False, ws=None,
+                        stream=None):
+    """Gradients of gmm_layer_norm for the rows' gradient dout (X's shape and
+    type, any row stride), with its mean and rstd: (dX, dgamma, dbeta), dX
+    contiguous in X's type, dgamma and dbeta (D,) float32 (left out without
+    gamma unless given).  Buffers not given are allocated; False leaves one out.
+    accumulate=True adds to the buffers, all of which are then given."""
+    torch = _torch()
+    d, y = _rows("X", X), _rows("dout", dout)
+    if dout.shape != X.shape or dout.dtype != X.dtype:
+        raise ValueError("dout must be of X's shape and type")
+    code = _affine(X, gamma)
+    lead, D = X.shape[:-1], X.shape[-1]
+    _expect("mean", mean, torch.float32, lead)
+    _expect("rstd", rstd, torch.float32, lead)
+    _check_ws(ws)
+    if gamma is None:
+        dgamma, dbeta = (False if t is None else t for t in (dgamma, dbeta))
+    if accumulate and any(t is None for t in (dX, dgamma, dbeta)):
+        raise ValueError("accumulate=True adds to given buffers (False leaves a gradient out)")
+    given = [t for t in (dX, dgamma, dbeta) if t is not None and t is not False]
+    with _on(stream, X, dout, mean, rstd, gamma, ws, *given) as s:
+        dX = _wanted(dX, X, X.shape, X.dtype)
+        dgamma, dbeta = _wanted(dgamma, X, (D,), torch.float32), _wanted(dbeta, X, (D,), torch.float32)
+        for name, t, dtype, shape in (("dX", dX, X.dtype, X.shape), ("dgamma", dgamma, torch.float32, (D,)),
+                                      ("dbeta", dbeta, torch.float32, (D,))):
+            if t is not None:
+                _expect(name, t, dtype, shape)
+        if ws is None:
+            want = (dX is not None) + 2 * (dgamma is not None) + 4 * (dbeta is not None)
+            n = int(_abi.lib().gmm_layer_norm_grad_workspace_bytes(ctypes.byref(d), want))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=X.device)
+        _abi.check(_abi.lib().gmm_layer_norm_grad(ctypes.byref(y), ctypes.byref(d), _ptr(mean), _ptr(rstd), _ptr(gamma),
+                                                  code, _ptr(dX), _ptr(dgamma), _ptr(dbeta), int(bool(accumulate)),
+                                                  _ptr(ws), ws.numel() * ws.element_size(), s))
+    return dX, dgamma, dbeta
+
+
+def _routing(score, groups, keep_groups, group_top, renormalize, scale):
+    if score not in _abi.SCORES:
+        raise ValueError(f"score must be one of {sorted(_abi.SCORES)} (got {score!r})")
+    return _abi.GmmRouting(_abi.SCORES[score], int(groups), int(groups if keep_groups is None else keep_groups),
+                           int(group_top), int(bool(renormalize)), float(scale))
+
+
+def gmm_route_topm(logits, m, bias=None, score="softmax", groups=1, keep_groups=None, group_top=1, renormalize=True,
+                   scale=1.0, idx=None, weights=None, stream=None):
+    """Top-m routing of rows of expert logits ((N, E) or (B, N, E) float32,
+    bfloat16 or float16): the m experts of the largest score ("softmax" or
+    "sigmoid" of the logits, plus bias (E,) float32 for the choice alone) in the
+    keep_groups groups (of `groups` equal runs of experts; None: all) of the
+    largest sum of their group_top best, and their weights, scale times the
+    score, over the sum of the selected scores if renormalize.  Returns (idx,
+    weights), int32 and float32 of logits' leading shape + (m,), best first, -1
+    and 0 behind a row's last expert: what gmm_codebook_lookup and gmm_ivf_lists
+    take."""
+    torch = _torch()
+    d = _rows("logits", logits)
+    how = _routing(score, groups, keep_groups, group_top, renormalize, scale)
+    shape = logits.shape[:-1] + (int(m),)
+    if bias is not None:
+        _expect("bias", bias, torch.float32, logits.shape[-1:])
+    if int(m) < 1:
+        raise ValueError("m must be >= 1")
+    with _on(stream, logits, bias, idx, weights) as s:
+        idx = torch.empty(shape, dtype=torch.int32, device=logits.device) if idx is None else idx
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device) if weights is None else weights
+        _expect("idx", idx, torch.int32, shape)
+        _expect("weights", weights, torch.float32, shape)
+        _abi.check(_abi.lib().gmm_route_topm(ctypes.byref(d), _ptr(bias), ctypes.byref(how), int(m), _ptr(idx),
+                                             _ptr(weights), s))
+    return idx, weights
+
+
+def gmm_route_topm_grad(dweights, logits, idx, score="softmax", renormalize=True, scale=1.0, dscores=None, dlogits=None,
+                        stream=None):
+    """The logits' gradient of gmm_route_topm, for its idx and the weights'
+    gradient dweights (idx's shape, float32, None: none) and, the same for all
+    rows, the gradient dscores (E,) float32 of the scores (that of a balance
+    loss; None: none).  Returns dlogits, contiguous, in the logits' type and
+    shape."""
+    torch = _torch()
+    d = _rows("logits", logits)
+    how = _routing(score, 1, None, 1, renormalize, scale)
+    if idx.dim() != logits.dim() or idx.shape[:-1] != logits.shape[:-1]:
+        raise ValueError("idx must be of the logits' leading shape and (m,)")
+    _expect("idx", idx, torch.int32, idx.shape)
+    if dweights is None and dscores is None:
+        raise ValueError("need dweights or dscores")
+    if dweights is not None:
+        _expect("dweights", dweights, torch.float32, idx.shape)
+    if dscores is not None:
+        _expect("dscores", dscores, torch.float32, logits.shape[-1:])
+    with _on(stream, logits, idx, dweights, dscores, dlogits) as s:
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        _expect("dlogits", dlogits, logits.dtype, logits.shape)
+        _abi.check(_abi.lib().gmm_route_topm_grad(ctypes.byref(d), ctypes.byref(how), int(idx.shape[-1]), _ptr(idx),
+                                                  _ptr(dweights), _ptr(dscores), _ptr(dlogits), s))
+    return dlogits
+
+
+ADAMW_BLOCK = 256  # elements under one scale of an 8-bit state
+
+
+def new_adamw_state(params, bits=32):
+    """Zeroed states of gmm_adamw_step for a list of tensors, as its keyword
+    arguments: dict(m, v, m_scale, v_scale), float32 tensors with bits = 32
+    (scales None), float8_e4m3fn values and float32 scales with bits = 8."""
+    torch = _torch()
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    kind = torch.float32 if bits == 32 else torch.uint8
+    zeros = lambda: [torch.zeros(p.shape, dtype=kind, device=p.device) for p in params]  # noqa: E731
+    m, v = zeros(), zeros()
+    if bits == 32:
+        return dict(m=m, v=v, m_scale=None, v_scale=None)
+    scales = lambda: [torch.zeros(-(-p.numel() // ADAMW_BLOCK), dtype=torch.float32, device=p.device)  # noqa: E731
+                      for p in params]
+    fp8 = torch.float8_e4m3fn
+    return dict(m=[t.view(fp8) for t in m], v=[t.view(fp8) for t in v], m_scale=scales(), v_scale=scales())
+
+
+def gmm_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, m_scale=None,
+                   v_scale=None, copies=None, norm=None, max_norm=None, seed=0, stream=None):
+    """One AdamW step over the contiguous tensors `params` (float32, bfloat16
+    or float16) with gradients `grads` (of any of these types) and the states m
+    and v (new_adamw_state), all updated in place; step counts from 1.
+    weight_decay: a number, or one per tensor.  m_scale, v_scale: lists for 8-bit
+    states (None, or None entries: float32 states).  copies: tensors (or None
+    entries) of the parameters' shapes that receive the new values in their own
+    type, such as bfloat16 copies of float32 parameters.  norm with max_norm
+    clips the gradients on the way: norm (1,) float32 as gmm_clip_grad_norm(grads,
+    inf) returns it.  step (int64) and lr (float32) may be one-element tensors on
+    the GPU, read when the call runs.  seed: of the rounding of 8-bit states, which
+    also hashes the step, the tensor's place and the element."""
+    torch = _torch()
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    count = len(params)
+    if not params:
+        raise ValueError("need one tensor or more")
+    opt = lambda t: [None] * count if t is None else list(t)  # noqa: E731
+    m_scale, v_scale, copies = opt(m_scale), opt(v_scale), opt(copies)
+    decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
+    for name, t in (("grads", grads), ("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale),
+                    ("copies", copies), ("weight_decay", decay)):
+        if len(t) != count:
+            raise ValueError(f"{name} must hold one entry per tensor")
+    if (norm is None) != (max_norm is None):
+        raise ValueError("norm and max_norm go together")
+    codes = {torch.float32: _abi.DT_F32, torch.bfloat16: _abi.DT_BF16, torch.float16: _abi.DT_F16}
+    desc = array("q")  # a gmm_adamw_tensor is eleven 8-byte words
+    decays = array("q", array("d", map(float, decay)).tobytes())
+    used = []
+    for i, (p, g, a, b, sa, sb, c) in enumerate(zip(params, grads, m, v, m_scale, v_scale, copies)):
+        code, gcode, n = codes.get(p.dtype), codes.get(g.dtype), p.numel()
+        if code is None or gcode is None or g.shape != p.shape or not (p.is_contiguous() and g.is_contiguous()):
+            raise ValueError(f"parameter {i} and its gradient must be contiguous float32, bfloat16 or float16 tensors "
+                             "of one shape")
+        if (sa is None) != (sb is None):
+            raise ValueError(f"state {i} has one scale of two")
+        kinds = (torch.float32,) if sa is None else (torch.float8_e4m3fn, torch.uint8)
+        for t in (a, b):
+            if t.dtype not in kinds or t.shape != p.shape or not t.is_contiguous():
+                raise ValueError(f"states {i} must be contiguous {kinds[0]} tensors of the parameter's shape")
+        used += (p, g, a, b)
+        if sa is not None:
+            blocks = (-(-n // ADAMW_BLOCK),)
+            _expect(f"m_scale[{i}]", sa, torch.float32, blocks)
+            _expect(f"v_scale[{i}]", sb, torch.float32, blocks)
+            used += (sa, sb)
+        ccode = 0
+        if c is not None:
+            ccode = codes.get(c.dtype)
+            if ccode is None or c.shape != p.shape or not c.is_contiguous():
+                raise ValueError(f"copy {i} must be a contiguous float32, bfloat16 or float16 tensor of the parameter's "
+                                 "shape")
+            used.append(c)
+        desc.extend((p.data_ptr(), g.data_ptr(), a.data_ptr(), b.data_ptr(), 0 if sa is None else sa.data_ptr(),
+                     0 if sb is None else sb.data_ptr(), 0 if c is None else c.data_ptr(), n, decays[i],
+                     code | gcode << 32, ccode))
+    o = _abi.GmmAdamwOptions(eps=float(eps), beta1=float(betas[0]), beta2=float(betas[1]), seed=int(seed) & 0xFFFFFFFF)
+    for name, t, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32), ("norm", norm, torch.float32)):
+        if isinstance(t, torch.Tensor):
+            if t.dtype != dtype or t.numel() != 1:
+                raise ValueError(f"{name} must be a one-element {dtype} tensor")
+            setattr(o, name if name == "norm" else name + "_dev", t.data_ptr())
+            used.append(t)
+    if not isinstance(step, torch.Tensor):
+        o.step = int(step)
+    if not isinstance(lr, torch.Tensor):
+        o.lr = float(lr)
+    if norm is not None:
+        if not isinstance(norm, torch.Tensor):
+            raise ValueError("norm must be a one-element float32 tensor")
+        o.max_norm = float(max_norm)
+    with _on(stream, *used) as s:
+        _abi.check(_abi.lib().gmm_adamw_step(desc.buffer_info()[0], count, ctypes.byref(o), s))
+
+
+def gmm_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logp=None, ws=None, stream=None):
+    """One token for every row of logits ((N, V) or (B, N, V) float32, bfloat16
+    or float16) from the uniform numbers u (logits' leading shape, float32, in
+    [0, 1)): softmax(logits / temperature) cut to its top_k largest (0: all), of
+    these to the shortest prefix that holds top_p of them (1: all), of these to
+    the ones with at least min_p of the largest; the first kept index at which the
+    cumulated probability exceeds u.  temperature 0 takes the largest logit.  Each
+    setting is a number or a tensor of u's shape (float32, top_k int32).  Returns
+    (tokens, logp), int32 and float32 of u's shape; logp, the log of the token's
+    share of what was kept, is left out with False."""
+    torch = _torch()
+    d = _rows("logits", logits)
+    lead = logits.shape[:-1]
+    _expect("u", u, torch.float32, lead)
+    _check_ws(ws)
+    how, rows = _abi.GmmSampling(temperature=1.0, top_p=1.0), []
+    for name, v in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
+        if isinstance(v, torch.Tensor):
+            _expect(name, v, torch.int32 if name == "top_k" else torch.float32, lead)
+            setattr(how, "row_" + name, v.data_ptr())
+            rows.append(v)
+        else:
+            setattr(how, name, int(v) if name == "top_k" else float(v))
+    given = [t for t in (tokens, logp) if t is not None and t is not False]
+    with _on(stream, logits, u, ws, *rows, *given) as s:
+        tokens = torch.empty(lead, dtype=torch.int32, device=logits.device) if tokens is None else tokens
+        logp = _wanted(logp, logits, lead, torch.float32)
+        _expect("tokens", tokens, torch.int32, lead)
+        if logp is not None:
+            _expect("logp", logp, torch.float32, lead)
+        if ws is None:
+            n = int(_abi.lib().gmm_sample_workspace_bytes(ctypes.byref(d)))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=logits.device)
+        _abi.check(_abi.lib().gmm_sample(ctypes.byref(d), ctypes.byref(how), _ptr(u), _ptr(tokens), _ptr(logp), _ptr(ws),
+                                         ws.numel() * ws.element_size(), s))
+    return tokens, logp
 
 
 def gmm_check_components(comp_status):

@@ -17,6 +17,7 @@ COV_SPHERICAL, COV_DIAG, COV_TIED, COV_FULL = 0, 1, 2, 3
 COV_CODES = {"spherical": COV_SPHERICAL, "diag": COV_DIAG, "tied": COV_TIED, "full": COV_FULL}
 DT_F32, DT_BF16, DT_F16 = 0, 1, 2
 OP_FIT, OP_ESTEP, OP_TOPM = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
 GMM_OK, GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED, GMM_ERR_WORKSPACE, GMM_ERR_HIP, GMM_ERR_NOT_PD = 0, 1, 2, 3, 4, 5
 
 EXPORTED = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step", "gmm_fit", "gmm_fit_step_noalloc",
@@ -27,6 +28,8 @@ EXPORTED = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step
             "gmm_softmax_xent_workspace_bytes", "gmm_softmax_xent", "gmm_softmax_xent_grad_workspace_bytes",
             "gmm_softmax_xent_grad", "gmm_codebook_lookup", "gmm_codebook_lookup_grad_workspace_bytes",
             "gmm_codebook_lookup_grad", "gmm_clip_grad_norm_workspace_bytes", "gmm_clip_grad_norm",
+            "gmm_layer_norm", "gmm_layer_norm_grad_workspace_bytes", "gmm_layer_norm_grad", "gmm_route_topm",
+            "gmm_route_topm_grad", "gmm_adamw_step", "gmm_sample_workspace_bytes", "gmm_sample",
             "gmm_check_components", "gmm_status_str",
             "gmm_last_error", "gmm_version"]
 
@@ -60,6 +63,31 @@ class GmmHead(ctypes.Structure):
 class GmmTensor(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("dtype", ctypes.c_int32)]
+
+
+class GmmRouting(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("keep_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class GmmAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GmmAdamwOptions(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("max_norm", ctypes.c_double), ("norm", ctypes.c_void_p),
+                ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p), ("lr_dev", ctypes.c_void_p),
+                ("seed", ctypes.c_uint32)]
+
+
+class GmmSampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_double), ("top_p", ctypes.c_double), ("min_p", ctypes.c_double),
+                ("top_k", ctypes.c_int64), ("row_temperature", ctypes.c_void_p), ("row_top_p", ctypes.c_void_p),
+                ("row_min_p", ctypes.c_void_p), ("row_top_k", ctypes.c_void_p)]
 
 
 class GmmError(RuntimeError):
@@ -134,6 +162,20 @@ def lib() -> ctypes.CDLL:
         L.gmm_clip_grad_norm_workspace_bytes.argtypes = [ctypes.c_int32]
         L.gmm_clip_grad_norm.argtypes = [P, ctypes.c_int32, ctypes.c_double, P, P,
                                          ctypes.c_size_t, P]
+        I, Z = ctypes.c_int32, ctypes.c_size_t
+        L.gmm_layer_norm.argtypes = [D, P, P, I, ctypes.c_double, P, P, P, P]
+        L.gmm_layer_norm_grad_workspace_bytes.argtypes = [D, I]
+        L.gmm_layer_norm_grad.argtypes = [D, D, P, P, P, I, P, P, P, I, P, Z, P]
+        L.gmm_route_topm.argtypes = [D, P, ctypes.POINTER(GmmRouting), I, P, P, P]
+        L.gmm_route_topm_grad.argtypes = [D, ctypes.POINTER(GmmRouting), I, P, P, P, P, P]
+        L.gmm_adamw_step.argtypes = [P, I, ctypes.POINTER(GmmAdamwOptions), P]
+        L.gmm_sample_workspace_bytes.argtypes = [D]
+        L.gmm_sample.argtypes = [D, ctypes.POINTER(GmmSampling), P, P, P, P, Z, P]
+        for f in (L.gmm_layer_norm_grad_workspace_bytes, L.gmm_sample_workspace_bytes):
+            f.restype = Z
+        for f in (L.gmm_layer_norm, L.gmm_layer_norm_grad, L.gmm_route_topm, L.gmm_route_topm_grad, L.gmm_adamw_step,
+                  L.gmm_sample):
+            f.restype = I
         for f in (L.gmm_softmax_xent_workspace_bytes, L.gmm_softmax_xent_grad_workspace_bytes,
                   L.gmm_codebook_lookup_grad_workspace_bytes, L.gmm_clip_grad_norm_workspace_bytes):
             f.restype = ctypes.c_size_t

@@ -1,0 +1,259 @@
+// gmm_adamw.hip -- one AdamW step over many tensors.
+//   g' = c g,  m' = b1 m + (1 - b1) g',  v' = b2 v + (1 - b2) g'^2
+//   p' = p (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+// with c the clipping coefficient of a given norm.  Every operation is float32,
+// rounded by itself (no contraction), so that the states do not depend on how
+// the compiler pairs them; the factors that all elements share are formed in
+// float64.  8-bit states: e4m3 values under one float32 scale for 256 elements,
+// the second moment as its root (whose ratio of largest to smallest is half as
+// wide in bits).  They are rounded up with the probability of their remainder,
+// from a hash of (seed, step, tensor, element): a state that moves by less than
+// half a step of its 3 bits a call, as the second moment under b2 = 0.999 does,
+// would never move under rounding to nearest.  A root that is not zero is not
+// rounded to zero: m' over the next root would be too large a step.
+// Bound by memory: every tensor read once and written once.
+#include "gmm_device.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+namespace gmm {
+
+namespace {
+
+constexpr int kEach = 8;  // elements a thread: a state block of 256 is half a wave
+
+__device__ inline uint32_t mix32(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x9E3779B1u;
+  x = (x ^ (x >> 15)) * 0x6A09E667u;
+  return x ^ (x >> 16);
+}
+
+template <typename T>
+__device__ inline void load_each(float (&f)[kEach], const T* p, int n) {
+  T v[kEach];
+  if (n >= kEach) {
+    __builtin_memcpy(v, p, sizeof(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) v[e] = e < n ? p[e] : (T)0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) f[e] = (float)v[e];
+}
+
+template <typename T>
+__device__ inline void store_each(T* p, const float (&f)[kEach], int n) {
+  T v[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) v[e] = (T)f[e];
+  if (n >= kEach) {
+    __builtin_memcpy(p, v, sizeof(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+
+__device__ inline void load_codes(float (&f)[kEach], const uint8_t* p, int n, float scale) {
+#pragma clang fp contract(off)
+  uint32_t w[2] = {0, 0};
+  if (n >= kEach) {
+    __builtin_memcpy(w, p, 8);
+  } else {
+    uint8_t b[8];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) b[e] = e < n ? p[e] : 0;
+    __builtin_memcpy(w, b, 8);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    f[4 * h] = __builtin_amdgcn_cvt_f32_fp8(w[h], 0) * scale;
+    f[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(w[h], 1) * scale;
+    f[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(w[h], 2) * scale;
+    f[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(w[h], 3) * scale;
+  }
+}
+
+// the largest of 32 lanes' values, NaN among them kept
+__device__ inline float half_wave_max(float v) {
+  const bool bad = v != v;
+  v = row16_max(v);
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const uint64_t any = __ballot(bad);
+  const uint32_t mine = (threadIdx.x & 32) ? (uint32_t)(any >> 32) : (uint32_t)any;
+  return mine ? __builtin_nanf("") : v;
+}
+
+// f (8 elements a lane, 256 a half wave) as e4m3 values and their scale: the
+// value below or above, by the 16 bits d of each element.
+template <bool ROOT>
+__device__ inline void store_codes(uint8_t* p, float* scale, const float (&f)[kEach], const uint32_t (&h)[kEach], int n) {
+#pragma clang fp contract(off)
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const float a = e < n ? fabsf(f[e]) : 0.f;
+    top = a > top || a != a ? a : top;
+  }
+  top = half_wave_max(top);
+  const bool none = top < 0x1p-100f;  // 448 / top would leave float32
+  const float s = none ? 0.f : top / 448.f, inv = none ? 0.f : 448.f / top;
+  uint8_t b[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const float x = f[e] * inv, a = fminf(fabsf(x), 448.f);
+    const uint32_t d = ROOT ? h[e] & 0xffff : h[e] >> 16;
+    // from 2^-6 on 3 of the 23 mantissa bits stay; below, steps of 2^-9
+    uint32_t c = a < 0x1p-6f ? (uint32_t)(a * 512.f + (float)d * 0x1p-16f)
+                             : ((__float_as_uint(a) + (d << 4)) >> 20) - (120u << 3);
+    if (ROOT && x > 0.f && c == 0) c = 1;
+    if (!ROOT && x < 0.f && c != 0) c |= 0x80;
+    if (x != x) c = 0x7f;
+    b[e] = (uint8_t)c;
+  }
+  if (n >= kEach) {
+    __builtin_memcpy(p, b, 8);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (e < n) p[e] = b[e];
+  }
+  if ((threadIdx.x & 31) == 0 && n > 0) *scale = s;
+}
+
+struct Factors {
+  float c, decay, alpha, root, b1, c1, b2, c2, eps;
+  uint32_t key;
+};
+
+template <typename P, typename G, bool BITS8>
+__device__ inline void adam_piece(const AdamTensor& t, int64_t i0, int64_t n, const Factors& F) {
+#pragma clang fp contract(off)
+  // every lane of a wave takes part in the blocks' maxima
+  for (int64_t k = 0; k < n; k += 256 * kEach) {
+    const int64_t at = k + (int64_t)threadIdx.x * kEach, i = i0 + at;
+    const int have = n - at >= kEach ? kEach : n - at > 0 ? (int)(n - at) : 0;
+    if (!BITS8 && have == 0) return;
+    float p[kEach], g[kEach], m[kEach], v[kEach];
+    load_each<P>(p, static_cast<const P*>(t.p) + i, have);
+    load_each<G>(g, static_cast<const G*>(t.g) + i, have);
+    const int64_t block = i / kAdamBlock;
+    if constexpr (BITS8) {
+      load_codes(m, static_cast<const uint8_t*>(t.m) + i, have, have ? t.ms[block] : 0.f);
+      load_codes(v, static_cast<const uint8_t*>(t.v) + i, have, have ? t.vs[block] : 0.f);
+    } else {
+      load_each<float>(m, static_cast<const float*>(t.m) + i, have);
+      load_each<float>(v, static_cast<const float*>(t.v) + i, have);
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const float d = F.c * g[e];
+      if constexpr (BITS8) v[e] = v[e] * v[e];
+      m[e] = F.b1 * m[e] + F.c1 * d;
+      v[e] = F.b2 * v[e] + F.c2 * (d * d);
+      const float r = sqrtf(v[e]);
+      p[e] = p[e] * F.decay - F.alpha * (m[e] / (r * F.root + F.eps));
+      if constexpr (BITS8) v[e] = r;
+    }
+    store_each<P>(static_cast<P*>(t.p) + i, p, have);
+    if (t.copy && have) {
+      if (t.copy_dtype == 1) store_each<__bf16>(static_cast<__bf16*>(t.copy) + i, p, have);
+      else if (t.copy_dtype == 2) store_each<_Float16>(static_cast<_Float16*>(t.copy) + i, p, have);
+      else store_each<float>(static_cast<float*>(t.copy) + i, p, have);
+    }
+    if constexpr (BITS8) {
+      const uint32_t kb = mix32(F.key + (uint32_t)block);
+      uint32_t h[kEach];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) h[e] = mix32(kb + ((uint32_t)(i % kAdamBlock) + e) * 0x9E3779B1u);
+      store_codes<false>(static_cast<uint8_t*>(t.m) + i, t.ms + block, m, h, have);
+      store_codes<true>(static_cast<uint8_t*>(t.v) + i, t.vs + block, v, h, have);
+    } else {
+      store_each<float>(static_cast<float*>(t.m) + i, m, have);
+      store_each<float>(static_cast<float*>(t.v) + i, v, have);
+    }
+  }
+}
+
+template <typename P, typename G>
+__device__ inline void adam_bits(const AdamTensor& t, int64_t i0, int64_t n, const Factors& F) {
+  if (t.ms) adam_piece<P, G, true>(t, i0, n, F);
+  else adam_piece<P, G, false>(t, i0, n, F);
+}
+
+template <typename P>
+__device__ inline void adam_grad(const AdamTensor& t, int64_t i0, int64_t n, const Factors& F) {
+  if (t.grad_dtype == 0) adam_bits<P, float>(t, i0, n, F);
+  else if (t.grad_dtype == 1) adam_bits<P, __bf16>(t, i0, n, F);
+  else adam_bits<P, _Float16>(t, i0, n, F);
+}
+
+__global__ void __launch_bounds__(256) adamw_kernel(AdamArgs A) {
+  __shared__ Factors shared;
+  __shared__ double lr;
+  if (threadIdx.x == 0) {
+    const int64_t step = A.step_dev ? (*A.step_dev > 1 ? *A.step_dev : 1) : A.step;
+    lr = A.lr_dev ? (double)*A.lr_dev : A.lr;
+    double c = 1.0;
+    if (A.norm && A.max_norm != INFINITY) {
+      const double q = A.max_norm / ((double)*A.norm + 1e-6);
+      c = q < 1.0 || q != q ? q : 1.0;
+    }
+    Factors f;
+    f.c = (float)c;
+    f.alpha = (float)(lr / -expm1((double)step * A.log_b1));
+    f.root = (float)(1.0 / sqrt(-expm1((double)step * A.log_b2)));
+    f.b1 = (float)A.b1;
+    f.c1 = (float)(1.0 - A.b1);
+    f.b2 = (float)A.b2;
+    f.c2 = (float)(1.0 - A.b2);
+    f.eps = (float)A.eps;
+    f.decay = 0.f;
+    f.key = mix32(A.seed + 0x9E3779B1u * (uint32_t)step);
+    shared = f;
+  }
+  __syncthreads();
+  for (int64_t q = blockIdx.x; q < A.pieces; q += gridDim.x) {
+    int lo = 0, hi = A.count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (A.t[mid].piece0 <= q) lo = mid;
+      else hi = mid - 1;
+    }
+    const AdamTensor& t = A.t[lo];
+    const int64_t i0 = (q - t.piece0) * kAdamPiece, n = min(kAdamPiece, t.n - i0);
+    Factors F = shared;
+    F.decay = (float)(1.0 - lr * t.weight_decay);
+    F.key = mix32(F.key ^ (uint32_t)(A.first + lo));
+    if (t.dtype == 0) adam_grad<float>(t, i0, n, F);
+    else if (t.dtype == 1) adam_grad<__bf16>(t, i0, n, F);
+    else adam_grad<_Float16>(t, i0, n, F);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs A, hipStream_t s) {
+  for (int i0 = 0; i0 < count; i0 += kAdamTensors) {
+    A.first = i0;
+    A.count = std::min(kAdamTensors, count - i0);
+    A.pieces = 0;
+    for (int i = 0; i < A.count; ++i) {
+      A.t[i] = t[i0 + i];
+      A.t[i].piece0 = A.pieces;
+      A.pieces += (A.t[i].n + kAdamPiece - 1) / kAdamPiece;
+    }
+    if (A.pieces == 0) continue;
+    hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)std::min<int64_t>(A.pieces, 1 << 13)), dim3(256), 0, s, A);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace gmm

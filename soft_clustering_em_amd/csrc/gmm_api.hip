@@ -1603,6 +1603,358 @@ gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max
   return GMM_OK;
 }
 
+// ---- layer norm, routing, sampling: rows whose outputs are contiguous
+struct Span {
+  const void* p;
+  int64_t n;
+  const char* name;
+};
+// outputs may overlap neither inputs nor each other
+static gmm_status check_spans(const std::initializer_list<Span>& out, const std::initializer_list<Span>& in) {
+  for (auto o = out.begin(); o != out.end(); ++o) {
+    for (const Span& i : in)
+      if (overlap(o->p, o->n, i.p, i.n)) return fail(GMM_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
+    for (auto q = out.begin(); q != o; ++q)
+      if (overlap(o->p, o->n, q->p, q->n)) return fail(GMM_ERR_INVALID_ARG, "%s overlaps %s", o->name, q->name);
+  }
+  return GMM_OK;
+}
+
+static gmm_status rows_check(const gmm_data* d, int64_t max_d, const char* what) {
+  gmm_status st = check_data(d);
+  if (st != GMM_OK) return st;
+  if (d->D > max_d) return fail(GMM_ERR_UNSUPPORTED, "%s (%lld) > %lld", what, (long long)d->D, (long long)max_d);
+  if (d->N > 0 && d->B > (((int64_t)1 << 31) - 1) / d->N) return fail(GMM_ERR_UNSUPPORTED, "B*N must stay below 2^31");
+  if ((uintptr_t)d->x % (d->dtype == GMM_DT_F32 ? 4 : 2))
+    return fail(GMM_ERR_INVALID_ARG, "the rows must be aligned to their elements");
+  return GMM_OK;
+}
+// 0: row r lies r ld behind the first, whatever its problem
+static int64_t rows_stride(const gmm_data* d) { return d->B > 1 && d->stride_b != d->N * d->ld_x ? d->stride_b : 0; }
+static bool is_dtype(int32_t t) { return t == GMM_DT_F32 || t == GMM_DT_BF16 || t == GMM_DT_F16; }
+
+static gmm_status norm_check(const gmm_data* rows, const void* gamma, const void* beta, int32_t affine_dtype) {
+  gmm_status st = rows_check(rows, 32768, "D");
+  if (st != GMM_OK) return st;
+  if (!is_dtype(affine_dtype)) return fail(GMM_ERR_INVALID_ARG, "unknown dtype %d", affine_dtype);
+  if (affine_dtype != GMM_DT_F32 && affine_dtype != rows->dtype)
+    return fail(GMM_ERR_UNSUPPORTED, "gamma and beta are float32 or of the rows' dtype (%d)", rows->dtype);
+  const uintptr_t es = affine_dtype == GMM_DT_F32 ? 4 : 2;
+  if ((uintptr_t)gamma % es || (uintptr_t)beta % es) return fail(GMM_ERR_INVALID_ARG, "gamma or beta is misaligned");
+  return GMM_OK;
+}
+
+gmm_status gmm_layer_norm(const gmm_data* rows, const void* gamma, const void* beta, int32_t affine_dtype, double eps,
+                          void* out, float* mean, float* rstd, void* stream) {
+  g_err.clear();
+  gmm_status st = norm_check(rows, gamma, beta, affine_dtype);
+  if (st != GMM_OK) return st;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(GMM_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+  const int64_t R = rows->B * rows->N, es = rows->dtype == GMM_DT_F32 ? 4 : 2, na = rows->D * (affine_dtype == GMM_DT_F32 ? 4 : 2);
+  if (R > 0 && !out) return fail(GMM_ERR_INVALID_ARG, "out must be non-NULL");
+  if ((uintptr_t)out % es || ((uintptr_t)mean | (uintptr_t)rstd) % 4)
+    return fail(GMM_ERR_INVALID_ARG, "out, mean and rstd must be aligned to their elements");
+  st = check_spans({{out, R * rows->D * es, "out"}, {mean, 4 * R, "mean"}, {rstd, 4 * R, "rstd"}},
+                   {{rows->x, data_span(rows, es), "the rows"}, {gamma, na, "gamma"}, {beta, na, "beta"}});
+  if (st != GMM_OK) return st;
+  if (R == 0) return GMM_OK;
+  NormArgs a{};
+  a.x = rows->x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.affine_t = affine_dtype == rows->dtype;
+  a.out = out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.R = R;
+  a.N = rows->N;
+  a.D = rows->D;
+  a.ld = rows->ld_x;
+  a.stride_b = rows_stride(rows);
+  a.eps = (float)eps;
+  a.dtype = rows->dtype;
+  const hipError_t e = launch_norm(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "layer norm launch");
+  return GMM_OK;
+}
+
+size_t gmm_layer_norm_grad_workspace_bytes(const gmm_data* rows, int32_t want) {
+  if (rows_check(rows, 32768, "D") != GMM_OK) return 0;
+  return std::max(kAlign, align_up(norm_plan(rows->B * rows->N, rows->D, rows->dtype, want & 6).bytes));
+}
+
+gmm_status gmm_layer_norm_grad(const gmm_data* dout, const gmm_data* rows, const float* mean, const float* rstd,
+                               const void* gamma, int32_t affine_dtype, void* dx, float* dgamma, float* dbeta,
+                               int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  gmm_status st = norm_check(rows, gamma, nullptr, affine_dtype);
+  if (st != GMM_OK) return st;
+  if ((st = rows_check(dout, 32768, "D")) != GMM_OK) return st;
+  if (dout->B != rows->B || dout->N != rows->N || dout->D != rows->D)
+    return fail(GMM_ERR_INVALID_ARG, "dout must be (B, N, D) of the rows");
+  if (dout->dtype != rows->dtype) return fail(GMM_ERR_UNSUPPORTED, "dout's dtype must be the rows'");
+  const int64_t R = rows->B * rows->N, es = rows->dtype == GMM_DT_F32 ? 4 : 2, D = rows->D;
+  const int64_t na = D * (affine_dtype == GMM_DT_F32 ? 4 : 2);
+  if (R > 0 && !dx && !dgamma && !dbeta)
+    return fail(GMM_ERR_INVALID_ARG, "one of dx, dgamma and dbeta must be non-NULL");
+  if (R > 0 && (!mean || !rstd)) return fail(GMM_ERR_INVALID_ARG, "mean and rstd must be non-NULL");
+  if ((uintptr_t)dx % es || ((uintptr_t)dgamma | (uintptr_t)dbeta | (uintptr_t)mean | (uintptr_t)rstd) % 4)
+    return fail(GMM_ERR_INVALID_ARG, "gradients, mean and rstd must be aligned to their elements");
+  st = check_spans({{dx, R * D * es, "dx"}, {dgamma, 4 * D, "dgamma"}, {dbeta, 4 * D, "dbeta"}},
+                   {{rows->x, data_span(rows, es), "the rows"}, {dout->x, data_span(dout, es), "dout"},
+                    {gamma, na, "gamma"}, {mean, 4 * R, "mean"}, {rstd, 4 * R, "rstd"}});
+  if (st != GMM_OK) return st;
+  const NormPlan p = norm_plan(R, D, rows->dtype, dgamma || dbeta);
+  if ((st = check_ws(ws, ws_bytes, std::max(kAlign, align_up(p.bytes)))) != GMM_OK) return st;
+  hipError_t e = hipSuccess;
+  if (R == 0) {  // sums over no rows
+    if (!accumulate && dgamma) e = launch_zero(dgamma, 4 * D, (hipStream_t)stream);
+    if (!accumulate && dbeta && e == hipSuccess) e = launch_zero(dbeta, 4 * D, (hipStream_t)stream);
+    return e == hipSuccess ? GMM_OK : hip_fail(e, "gradient zero launch");
+  }
+  NormArgs a{};
+  a.x = rows->x;
+  a.dy = dout->x;
+  a.gamma = gamma;
+  a.affine_t = affine_dtype == rows->dtype;
+  a.dx = dx;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.part = static_cast<float*>(ws);
+  a.R = R;
+  a.N = rows->N;
+  a.D = D;
+  a.ld = rows->ld_x;
+  a.stride_b = rows_stride(rows);
+  a.ld_dy = dout->ld_x;
+  a.stride_dy = rows_stride(dout);
+  a.dtype = rows->dtype;
+  a.accumulate = accumulate != 0;
+  e = launch_norm_grad(a, p, dgamma, dbeta, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "layer norm gradient launch");
+  return GMM_OK;
+}
+
+// ---- routing
+static gmm_status route_args(const gmm_data* logits, const gmm_routing* how, int32_t m, RouteArgs* a) {
+  gmm_status st = rows_check(logits, kRouteMaxE, "E");
+  if (st != GMM_OK) return st;
+  if (!how) return fail(GMM_ERR_INVALID_ARG, "routing descriptor is NULL");
+  if (how->score != GMM_SCORE_SOFTMAX && how->score != GMM_SCORE_SIGMOID)
+    return fail(GMM_ERR_INVALID_ARG, "unknown score %d", how->score);
+  if (m < 1 || m > kRouteMaxM) return fail(GMM_ERR_INVALID_ARG, "m must be in [1, %d] (got %d)", kRouteMaxM, m);
+  if (how->groups < 1 || logits->D % how->groups)
+    return fail(GMM_ERR_INVALID_ARG, "groups (%d) must divide E (%lld)", how->groups, (long long)logits->D);
+  if (how->groups > kRouteMaxGroups) return fail(GMM_ERR_UNSUPPORTED, "groups (%d) > %d", how->groups, kRouteMaxGroups);
+  if (how->keep_groups < 1 || how->keep_groups > how->groups)
+    return fail(GMM_ERR_INVALID_ARG, "keep_groups must be in [1, groups] (got %d)", how->keep_groups);
+  if (how->group_top != 1 && how->group_top != 2)
+    return fail(GMM_ERR_INVALID_ARG, "group_top must be 1 or 2 (got %d)", how->group_top);
+  if (!std::isfinite(how->scale)) return fail(GMM_ERR_INVALID_ARG, "scale must be finite");
+  a->l = logits->x;
+  a->R = logits->B * logits->N;
+  a->N = logits->N;
+  a->ld = logits->ld_x;
+  a->stride_b = rows_stride(logits);
+  a->dtype = logits->dtype;
+  a->E = (int)logits->D;
+  a->m = m;
+  a->groups = how->groups;
+  a->keep = how->keep_groups;
+  a->top = how->group_top;
+  a->sigmoid = how->score == GMM_SCORE_SIGMOID;
+  a->renorm = how->renormalize != 0;
+  a->scale = how->scale;
+  return GMM_OK;
+}
+
+gmm_status gmm_route_topm(const gmm_data* logits, const float* bias, const gmm_routing* how, int32_t m, int32_t* idx,
+                          float* weights, void* stream) {
+  g_err.clear();
+  RouteArgs a{};
+  gmm_status st = route_args(logits, how, m, &a);
+  if (st != GMM_OK) return st;
+  if (a.R > 0 && (!idx || !weights)) return fail(GMM_ERR_INVALID_ARG, "idx and weights must be non-NULL");
+  if (((uintptr_t)bias | (uintptr_t)idx | (uintptr_t)weights) % 4)
+    return fail(GMM_ERR_INVALID_ARG, "bias, idx and weights must be aligned to their elements");
+  const int64_t es = logits->dtype == GMM_DT_F32 ? 4 : 2, nw = 4 * a.R * m;
+  st = check_spans({{idx, nw, "idx"}, {weights, nw, "weights"}},
+                   {{logits->x, data_span(logits, es), "the logits"}, {bias, 4 * (int64_t)a.E, "bias"}});
+  if (st != GMM_OK) return st;
+  if (a.R == 0) return GMM_OK;
+  a.bias = bias;
+  a.idx = idx;
+  a.weights = weights;
+  const hipError_t e = launch_route(a, false, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "routing launch");
+  return GMM_OK;
+}
+
+gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, int32_t m, const int32_t* idx,
+                               const float* dweights, const float* dscores, void* dlogits, void* stream) {
+  g_err.clear();
+  RouteArgs a{};
+  gmm_status st = route_args(logits, how, m, &a);
+  if (st != GMM_OK) return st;
+  if (a.R > 0 && !dweights && !dscores) return fail(GMM_ERR_INVALID_ARG, "one of dweights and dscores must be non-NULL");
+  if (a.R > 0 && ((dweights && !idx) || !dlogits)) return fail(GMM_ERR_INVALID_ARG, "idx and dlogits must be non-NULL");
+  const int64_t es = logits->dtype == GMM_DT_F32 ? 4 : 2, nw = 4 * a.R * m;
+  if ((uintptr_t)dlogits % es || ((uintptr_t)idx | (uintptr_t)dweights | (uintptr_t)dscores) % 4)
+    return fail(GMM_ERR_INVALID_ARG, "idx, gradients and dlogits must be aligned to their elements");
+  st = check_spans({{dlogits, a.R * a.E * es, "dlogits"}},
+                   {{logits->x, data_span(logits, es), "the logits"}, {idx, nw, "idx"}, {dweights, nw, "dweights"},
+                    {dscores, 4 * (int64_t)a.E, "dscores"}});
+  if (st != GMM_OK) return st;
+  if (a.R == 0) return GMM_OK;
+  a.idx = const_cast<int32_t*>(idx);
+  a.dweights = dweights;
+  a.dscores = dscores;
+  a.dlogits = dlogits;
+  const hipError_t e = launch_route(a, true, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "routing gradient launch");
+  return GMM_OK;
+}
+
+// ---- AdamW
+gmm_status gmm_adamw_step(const gmm_adamw_tensor* tensors, int32_t count, const gmm_adamw_options* o, void* stream) {
+  g_err.clear();
+  if (!tensors || count < 1) return fail(GMM_ERR_INVALID_ARG, "need one tensor or more");
+  if (!o) return fail(GMM_ERR_INVALID_ARG, "options are NULL");
+  if (!(o->lr >= 0.0) || !std::isfinite(o->lr)) return fail(GMM_ERR_INVALID_ARG, "lr must be >= 0 and finite");
+  if (!(o->beta1 >= 0.0 && o->beta1 < 1.0) || !(o->beta2 >= 0.0 && o->beta2 < 1.0))
+    return fail(GMM_ERR_INVALID_ARG, "betas must be in [0, 1)");
+  if (!(o->eps >= 0.0) || !std::isfinite(o->eps)) return fail(GMM_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+  if (!o->step_dev && o->step < 1) return fail(GMM_ERR_INVALID_ARG, "step must be >= 1 (got %lld)", (long long)o->step);
+  if (o->norm && !(o->max_norm >= 0.0)) return fail(GMM_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if (((uintptr_t)o->norm | (uintptr_t)o->lr_dev) % 4 || (uintptr_t)o->step_dev % 8)
+    return fail(GMM_ERR_INVALID_ARG, "norm, lr_dev or step_dev is misaligned");
+  struct Piece {
+    const char *p, *q;
+    int tensor;
+    bool out;
+  };
+  std::vector<AdamTensor> t;
+  std::vector<Piece> spans;
+  try {
+    t.resize(count);
+    spans.reserve(7 * (size_t)count + 3);
+  } catch (...) {
+    return fail(GMM_ERR_INVALID_ARG, "no host memory for %d tensors", count);
+  }
+  const auto add = [&](const void* p, int64_t n, int i, bool out) {
+    if (p && n > 0) spans.push_back({(const char*)p, (const char*)p + n, i, out});
+  };
+  add(o->norm, 4, -1, false);
+  add(o->step_dev, 8, -1, false);
+  add(o->lr_dev, 4, -1, false);
+  for (int i = 0; i < count; ++i) {
+    const gmm_adamw_tensor& a = tensors[i];
+    if (!is_dtype(a.dtype) || !is_dtype(a.grad_dtype) || (a.copy && !is_dtype(a.copy_dtype)))
+      return fail(GMM_ERR_INVALID_ARG, "tensor %d: unknown dtype", i);
+    if (a.n < 0) return fail(GMM_ERR_INVALID_ARG, "tensor %d: n must be >= 0", i);
+    if (a.n >= ((int64_t)1 << 40)) return fail(GMM_ERR_UNSUPPORTED, "tensor %d: too large", i);
+    if (!(a.weight_decay >= 0.0) || !std::isfinite(a.weight_decay))
+      return fail(GMM_ERR_INVALID_ARG, "tensor %d: weight_decay must be >= 0 and finite", i);
+    if (a.n > 0 && (!a.param || !a.grad || !a.m || !a.v))
+      return fail(GMM_ERR_INVALID_ARG, "tensor %d: param, grad, m and v must be non-NULL", i);
+    if (!a.m_scale != !a.v_scale) return fail(GMM_ERR_INVALID_ARG, "tensor %d: one of m_scale and v_scale is NULL", i);
+    if (a.reserved != 0) return fail(GMM_ERR_INVALID_ARG, "tensor %d: reserved must be 0", i);
+    const int64_t ep = a.dtype == GMM_DT_F32 ? 4 : 2, eg = a.grad_dtype == GMM_DT_F32 ? 4 : 2;
+    const int64_t ec = a.copy_dtype == GMM_DT_F32 ? 4 : 2, em = a.m_scale ? 1 : 4;
+    if ((uintptr_t)a.param % ep || (uintptr_t)a.grad % eg || ((uintptr_t)a.m | (uintptr_t)a.v) % em ||
+        ((uintptr_t)a.m_scale | (uintptr_t)a.v_scale) % 4 || (a.copy && (uintptr_t)a.copy % ec))
+      return fail(GMM_ERR_INVALID_ARG, "tensor %d is misaligned", i);
+    const int64_t blocks = a.m_scale ? 4 * ((a.n + kAdamBlock - 1) / kAdamBlock) : 0;
+    add(a.param, a.n * ep, i, true);
+    add(a.grad, a.n * eg, i, false);
+    add(a.m, a.n * em, i, true);
+    add(a.v, a.n * em, i, true);
+    add(a.m_scale, blocks, i, true);
+    add(a.v_scale, blocks, i, true);
+    add(a.copy, a.n * ec, i, true);
+    t[i] = AdamTensor{a.param, a.grad, a.m, a.v, a.m_scale, a.v_scale, a.copy, a.n, 0, a.weight_decay,
+                      a.dtype, a.grad_dtype, a.copy_dtype};
+  }
+  std::sort(spans.begin(), spans.end(), [](const Piece& a, const Piece& b) { return a.p < b.p; });
+  const char *end_any = nullptr, *end_out = nullptr;
+  for (const Piece& s : spans) {
+    if (s.out ? s.p < end_any : s.p < end_out)
+      return fail(GMM_ERR_INVALID_ARG, "tensor %d overlaps another tensor", std::max(0, s.tensor));
+    end_any = std::max(end_any, s.q);
+    if (s.out) end_out = std::max(end_out, s.q);
+  }
+  AdamArgs a{};
+  a.step = o->step;
+  a.lr = o->lr;
+  a.b1 = o->beta1;
+  a.b2 = o->beta2;
+  a.log_b1 = std::log(o->beta1);
+  a.log_b2 = std::log(o->beta2);
+  a.eps = o->eps;
+  a.max_norm = o->max_norm;
+  a.norm = o->norm;
+  a.lr_dev = o->lr_dev;
+  a.step_dev = o->step_dev;
+  a.seed = o->seed;
+  const hipError_t e = launch_adamw(t.data(), count, a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "AdamW launch");
+  return GMM_OK;
+}
+
+// ---- sampling
+static gmm_status sample_check(const gmm_data* logits) { return rows_check(logits, (int64_t)1 << 24, "V"); }
+
+size_t gmm_sample_workspace_bytes(const gmm_data* logits) {
+  if (sample_check(logits) != GMM_OK) return 0;
+  return kAlign;
+}
+
+gmm_status gmm_sample(const gmm_data* logits, const gmm_sampling* how, const float* u, int32_t* tokens, float* logp,
+                      void* ws, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  gmm_status st = sample_check(logits);
+  if (st != GMM_OK) return st;
+  if (!how) return fail(GMM_ERR_INVALID_ARG, "sampling descriptor is NULL");
+  const int64_t R = logits->B * logits->N, es = logits->dtype == GMM_DT_F32 ? 4 : 2;
+  if (!(how->temperature >= 0.0)) return fail(GMM_ERR_INVALID_ARG, "temperature must be >= 0");
+  if (std::isnan(how->top_p) || std::isnan(how->min_p)) return fail(GMM_ERR_INVALID_ARG, "top_p and min_p must be numbers");
+  if (R > 0 && (!u || !tokens)) return fail(GMM_ERR_INVALID_ARG, "u and tokens must be non-NULL");
+  if (((uintptr_t)u | (uintptr_t)tokens | (uintptr_t)logp | (uintptr_t)how->row_temperature | (uintptr_t)how->row_top_p |
+       (uintptr_t)how->row_min_p | (uintptr_t)how->row_top_k) % 4)
+    return fail(GMM_ERR_INVALID_ARG, "u, the rows' settings, tokens and logp must be aligned to their elements");
+  const Span in[6] = {{logits->x, data_span(logits, es), "the logits"}, {u, 4 * R, "u"}, {how->row_temperature, 4 * R, "row_temperature"},
+                      {how->row_top_p, 4 * R, "row_top_p"}, {how->row_min_p, 4 * R, "row_min_p"}, {how->row_top_k, 4 * R, "row_top_k"}};
+  st = check_spans({{tokens, 4 * R, "tokens"}, {logp, 4 * R, "logp"}}, {in[0], in[1], in[2], in[3], in[4], in[5]});
+  if (st != GMM_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, gmm_sample_workspace_bytes(logits))) != GMM_OK) return st;
+  if (R == 0) return GMM_OK;
+  SampleArgs a{};
+  a.l = logits->x;
+  a.u = u;
+  a.row_temperature = how->row_temperature;
+  a.row_top_p = how->row_top_p;
+  a.row_min_p = how->row_min_p;
+  a.row_top_k = how->row_top_k;
+  a.tokens = tokens;
+  a.logp = logp;
+  a.R = R;
+  a.N = logits->N;
+  a.V = logits->D;
+  a.ld = logits->ld_x;
+  a.stride_b = rows_stride(logits);
+  a.top_k = how->top_k;
+  a.temperature = how->temperature;
+  a.top_p = how->top_p;
+  a.min_p = how->min_p;
+  int bits = 0;
+  while (((int64_t)1 << bits) < a.V) ++bits;
+  a.scale = std::ldexp(1.0, std::min(52, 62 - bits));
+  a.dtype = logits->dtype;
+  const hipError_t e = launch_sample(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "sampling launch");
+  return GMM_OK;
+}
+
 const char* gmm_status_str(int32_t status) {
   switch (status) {
     case GMM_OK: return "ok";

@@ -377,6 +377,80 @@ struct ClipArgs {
 hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, double* coef,
                        hipStream_t s);
 
+// layer norm (gmm_norm.hip)
+struct NormArgs {
+  const void *x, *dy, *gamma, *beta;
+  void *out, *dx;
+  float *mean, *rstd;      // written forward, read backward
+  float* part;             // (parts, 2, D): shares of dgamma and dbeta
+  int64_t R, N, D, ld, stride_b, ld_dy, stride_dy;  // stride 0: rows ld apart throughout
+  float eps;
+  int dtype, accumulate;
+  bool affine_t;           // gamma and beta in the rows' type (else float32)
+};
+struct NormPlan {
+  int tpr, c;              // threads a row, 16-byte pieces a thread
+  bool wide;
+  int64_t grid, parts;
+  size_t bytes;
+};
+NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums);
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_grad(NormArgs a, const NormPlan& p, float* dgamma, float* dbeta, hipStream_t s);
+
+// routing (gmm_route.hip)
+constexpr int kRouteMaxE = 1024, kRouteMaxGroups = 64, kRouteMaxM = 16;
+struct RouteArgs {
+  const void* l;
+  const float *bias, *dweights, *dscores;
+  int32_t* idx;
+  float* weights;
+  void* dlogits;
+  int64_t R, N, ld, stride_b;  // stride 0: rows ld apart throughout
+  int dtype, E, m, groups, keep, top;
+  bool sigmoid, renorm;
+  float scale;
+};
+hipError_t launch_route(const RouteArgs& a, bool grad, hipStream_t s);
+
+// AdamW (gmm_adamw.hip)
+constexpr int kAdamTensors = 32;      // tensors per launch (their descriptions are kernel arguments)
+constexpr int64_t kAdamPiece = 8192;  // elements per piece, a multiple of 2048
+constexpr int kAdamBlock = 256;       // elements under one scale of an 8-bit state
+struct AdamTensor {
+  void* p;
+  const void* g;
+  void *m, *v;
+  float *ms, *vs;          // null: float32 states
+  void* copy;
+  int64_t n, piece0;
+  double weight_decay;
+  int32_t dtype, grad_dtype, copy_dtype;
+};
+struct AdamArgs {
+  AdamTensor t[kAdamTensors];
+  int count, first;
+  int64_t pieces, step;
+  double lr, b1, b2, log_b1, log_b2, eps, max_norm;
+  const float *norm, *lr_dev;
+  const int64_t* step_dev;
+  uint32_t seed;
+};
+hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs a, hipStream_t s);
+
+// sampling (gmm_sample.hip)
+struct SampleArgs {
+  const void* l;
+  const float *u, *row_temperature, *row_top_p, *row_min_p;
+  const int32_t* row_top_k;
+  int32_t* tokens;
+  float* logp;
+  int64_t R, N, V, ld, stride_b, top_k;
+  double temperature, top_p, min_p, scale;
+  int dtype;
+};
+hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
+
 // fused E-step + statistics (gmm_estep.hip)
 hipError_t launch_estep(const Plan& p, const EStepArgs& a, hipStream_t s);
 // blocked components: mode 1 the per-(row, block) (max, sum) pass, 2 the

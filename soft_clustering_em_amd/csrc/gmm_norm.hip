@@ -1,0 +1,421 @@
+// gmm_norm.hip -- layer norm of rows and its gradients.
+//   mean = sum_d x_d / D,  r = 1 / sqrt(sum_d (x_d - mean)^2 / D + eps)
+//   y_d  = (x_d - mean) r gamma_d + beta_d
+//   dx_d = r (q_d - sum q / D - xh_d sum (q xh) / D),  q = dy gamma, xh = (x - mean) r
+//   dgamma_d = sum_rows dy xh,  dbeta_d = sum_rows dy
+// A row's values stay in registers from the one read to the one write: TPR
+// threads a row, C pieces of 16 bytes a thread.  The mean is corrected by the
+// mean of the differences from its first value, and the variance is that of the
+// corrected differences, so rows far from zero keep their digits.  Sums are
+// float32: per thread, then in a fixed order over the row's threads.  The
+// gradients of gamma and beta: a thread owns its columns over all the rows that
+// its workgroup walks, then the workgroups' sums are added in a fixed order.
+#include "gmm_device.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace gmm {
+
+namespace {
+
+template <typename T>
+constexpr int kPer = 16 / (int)sizeof(T);  // elements of a 16-byte piece
+
+template <typename T>
+__device__ inline void load_piece(T (&v)[kPer<T>], const T* row, int64_t c0, int64_t D) {
+  if (c0 + kPer<T> <= D) {
+    __builtin_memcpy(v, row + c0, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPer<T>; ++e) v[e] = c0 + e < D ? row[c0 + e] : (T)0.f;
+  }
+}
+
+template <typename T>
+__device__ inline void store_piece(T* row, const T (&v)[kPer<T>], int64_t c0, int64_t D) {
+  if (c0 + kPer<T> <= D) {
+    __builtin_memcpy(row + c0, v, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPer<T>; ++e)
+      if (c0 + e < D) row[c0 + e] = v[e];
+  }
+}
+
+// E values of gamma or beta as float32 (is_t: stored in the rows' type), `none` past D or without a tensor
+template <typename T>
+__device__ inline void load_affine(float (&v)[kPer<T>], const void* p, bool is_t, int64_t c0, int64_t D, float none) {
+  constexpr int E = kPer<T>;
+  if (!p || c0 >= D) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = none;
+  } else if (is_t) {
+    T t[E];
+    load_piece<T>(t, static_cast<const T*>(p), c0, D);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (float)t[e];
+  } else {
+    const float* f = static_cast<const float*>(p) + c0;
+    if (c0 + E <= D) {
+      __builtin_memcpy(v, f, sizeof(v));
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = c0 + e < D ? f[e] : none;
+    }
+  }
+}
+
+// The sums of a and b over the TPR threads of a row, in every one of them.
+// Rows of more than a wave meet in LDS; `red` alternates between two halves,
+// so that one barrier a call is enough.
+template <int TPR>
+__device__ inline void row_sum2(float& a, float& b, float2 (*red)[16], int& turn) {
+  a = row16_sum(a);
+  b = row16_sum(b);
+  if constexpr (TPR >= 64) {
+    a = rows4_sum(a);
+    b = rows4_sum(b);
+  }
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 v = red[turn][w];
+      a += v.x;
+      b += v.y;
+    }
+    turn ^= 1;
+  }
+}
+
+__device__ inline int64_t row_at(int64_t r, int64_t N, int64_t ld, int64_t stride_b) {
+  if (stride_b == 0) return r * ld;
+  const uint32_t b = (uint32_t)r / (uint32_t)N;
+  return (int64_t)b * stride_b + (r - (int64_t)b * N) * ld;
+}
+
+template <typename T, int TPR, int C>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs A) {
+  constexpr int E = kPer<T>, RPB = TPR > 256 ? 1 : 256 / TPR;
+  __shared__ float2 red[2][16];
+  const int t = threadIdx.x % TPR;
+  const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool live = r < A.R;  // rows of more than a wave: the whole workgroup agrees
+  if (TPR > 64 && !live) return;
+  const T* x = static_cast<const T*>(A.x) + (live ? row_at(r, A.N, A.ld, A.stride_b) : 0);
+  const float inv = 1.f / (float)A.D;
+  T v[C][E];
+  float s = 0.f, s1 = 0.f, s2 = 0.f, none = 0.f;
+  int turn = 0;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    load_piece<T>(v[j], x, live ? ((int64_t)j * TPR + t) * E : A.D, A.D);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += (float)v[j][e];
+  }
+  row_sum2<TPR>(s, none, red, turn);
+  const float m1 = s * inv;
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float d = ((int64_t)j * TPR + t) * E + e < A.D ? (float)v[j][e] - m1 : 0.f;
+      s1 += d;
+      s2 += d * d;
+    }
+  row_sum2<TPR>(s1, s2, red, turn);
+  const float m2 = s1 * inv, mean = m1 + m2;
+  const float var = fmaxf(0.f, (s2 - s1 * m2) * inv), rstd = 1.f / sqrtf(var + A.eps);
+  // NaN in a row stays NaN: fmaxf would drop it
+  const float rs = s2 != s2 ? s2 : rstd;
+  if (!live) return;
+  if (t == 0) {
+    if (A.mean) A.mean[r] = mean;
+    if (A.rstd) A.rstd[r] = rs;
+  }
+  T* out = static_cast<T*>(A.out) + r * A.D;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int64_t c0 = ((int64_t)j * TPR + t) * E;
+    if (c0 >= A.D) break;
+    float g[E], b[E];
+    load_affine<T>(g, A.gamma, A.affine_t, c0, A.D, 1.f);
+    load_affine<T>(b, A.beta, A.affine_t, c0, A.D, 0.f);
+    T o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = (T)((((float)v[j][e] - m1) - m2) * rs * g[e] + b[e]);
+    store_piece<T>(out, o, c0, A.D);
+  }
+}
+
+// The gradients of rows, and (ACC) this workgroup's share of gamma's and
+// beta's: sums over the rows blockIdx.x * RPB + k gridDim.x * RPB.
+template <typename T, int TPR, int C, bool ACC>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_grad_kernel(NormArgs A) {
+  constexpr int E = kPer<T>, RPB = TPR > 256 ? 1 : 256 / TPR, W = (TPR > 256 ? TPR : 256) / 64;
+  __shared__ float2 red[2][16];
+  const int t = threadIdx.x % TPR;
+  const float inv = 1.f / (float)A.D;
+  float g[C][E], dg[ACC ? C : 1][E], db[ACC ? C : 1][E];
+  int turn = 0;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    load_affine<T>(g[j], A.gamma, A.affine_t, ((int64_t)j * TPR + t) * E, A.D, 1.f);
+    if constexpr (ACC) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) dg[j][e] = db[j][e] = 0.f;
+    }
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < A.R; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    const bool live = r < A.R;
+    const T* x = static_cast<const T*>(A.x) + (live ? row_at(r, A.N, A.ld, A.stride_b) : 0);
+    const T* dy = static_cast<const T*>(A.dy) + (live ? row_at(r, A.N, A.ld_dy, A.stride_dy) : 0);
+    const float mean = live ? A.mean[r] : 0.f, rstd = live ? A.rstd[r] : 0.f;
+    T vx[C][E], vy[C][E];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int64_t c0 = live ? ((int64_t)j * TPR + t) * E : A.D;
+      load_piece<T>(vx[j], x, c0, A.D);
+      load_piece<T>(vy[j], dy, c0, A.D);
+    }
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        // past D the row's gradient is 0, but xh is not: a column of no row
+        const float xh = ((float)vx[j][e] - mean) * rstd, y = (float)vy[j][e], q = y * g[j][e];
+        const bool in = ((int64_t)j * TPR + t) * E + e < A.D;
+        a += q;
+        b += in ? q * xh : 0.f;
+        if constexpr (ACC) {
+          dg[j][e] += in ? y * xh : 0.f;
+          db[j][e] += y;
+        }
+      }
+    if (A.dx) {
+      row_sum2<TPR>(a, b, red, turn);
+      if (live) {
+        T* dx = static_cast<T*>(A.dx) + r * A.D;
+        const float ma = a * inv, mb = b * inv;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const int64_t c0 = ((int64_t)j * TPR + t) * E;
+          if (c0 >= A.D) break;
+          T o[E];
+          if (A.accumulate) load_piece<T>(o, dx, c0, A.D);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float xh = ((float)vx[j][e] - mean) * rstd;
+            const float d = rstd * ((float)vy[j][e] * g[j][e] - ma - xh * mb);
+            o[e] = (T)(A.accumulate ? (float)o[e] + d : d);
+          }
+          store_piece<T>(dx, o, c0, A.D);
+        }
+      }
+    }
+  }
+  if constexpr (ACC) {
+    if constexpr (TPR == 16) {  // the four rows of a wave
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          dg[j][e] = rows4_sum(dg[j][e]);
+          db[j][e] = rows4_sum(db[j][e]);
+        }
+    }
+    constexpr int L = TPR < 64 ? TPR : 64, S = TPR < 64 ? W : RPB;  // lanes with columns of their own, waves to join
+    float* part = A.part + (int64_t)blockIdx.x * 2 * A.D;
+    if constexpr (S > 1) {
+      __shared__ float join[S][2 * E][L];
+      const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        __syncthreads();
+        if (lane < L) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            join[w][e][lane] = dg[j][e];
+            join[w][E + e][lane] = db[j][e];
+          }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * E * L; i += W * 64) {
+          const int l = i / (2 * E), e = i % (2 * E);
+          float v = 0.f;
+#pragma unroll
+          for (int k = 0; k < S; ++k) v += join[k][e][l];
+          const int64_t c = ((int64_t)j * TPR + l) * E + e % E;
+          if (c < A.D) part[(e / E) * A.D + c] = v;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int64_t c = ((int64_t)j * TPR + t) * E + e;
+          if (c < A.D) {
+            part[c] = dg[j][e];
+            part[A.D + c] = db[j][e];
+          }
+        }
+    }
+  }
+}
+
+// gamma's and beta's share of rows too wide for a thread to own its columns
+// beside the row: a workgroup takes 256 columns of a slab of rows.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_columns_kernel(NormArgs A, int64_t rows) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= A.D) return;
+  const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = r0 + rows < A.R ? r0 + rows : A.R;
+  float dg = 0.f, db = 0.f;
+  for (int64_t r = r0; r < r1; ++r) {
+    const float x = (float)static_cast<const T*>(A.x)[row_at(r, A.N, A.ld, A.stride_b) + c];
+    const float y = (float)static_cast<const T*>(A.dy)[row_at(r, A.N, A.ld_dy, A.stride_dy) + c];
+    dg += y * ((x - A.mean[r]) * A.rstd[r]);
+    db += y;
+  }
+  float* part = A.part + (int64_t)blockIdx.y * 2 * A.D;
+  part[c] = dg;
+  part[A.D + c] = db;
+}
+
+// dgamma and dbeta from `parts` rows of 2 D sums: 64 columns a workgroup, the
+// parts shared among 16 waves.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int parts, int64_t D, float* dgamma, float* dbeta,
+                                                         int accumulate) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float v = 0.f;
+  if (c < 2 * D) {
+#pragma unroll 8
+    for (int p = w; p < parts; p += 16) v += part[(int64_t)p * 2 * D + c];
+  }
+  red[w][lane] = v;
+  __syncthreads();
+  if (w != 0 || c >= 2 * D) return;
+  v = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v += red[k][lane];
+  float* o = c < D ? dgamma : dbeta;
+  if (!o) return;
+  const int64_t i = c < D ? c : c - D;
+  o[i] = accumulate ? o[i] + v : v;
+}
+
+template <typename F>
+hipError_t by_type(int dtype, F f) {
+  if (dtype == 0) return f((float)0);
+  if (dtype == 1) return f((__bf16)0.f);
+  return f((_Float16)0.f);
+}
+
+template <typename T, int TPR, int C>
+hipError_t run_norm(const NormArgs& A, hipStream_t s) {
+  constexpr int RPB = TPR > 256 ? 1 : 256 / TPR;
+  hipLaunchKernelGGL((norm_kernel<T, TPR, C>), dim3((unsigned)((A.R + RPB - 1) / RPB)), dim3(TPR > 256 ? TPR : 256), 0, s, A);
+  return hipGetLastError();
+}
+
+template <typename T, int TPR, int C, bool ACC>
+hipError_t run_grad(const NormArgs& A, unsigned grid, hipStream_t s) {
+  hipLaunchKernelGGL((norm_grad_kernel<T, TPR, C, ACC>), dim3(grid), dim3(TPR > 256 ? TPR : 256), 0, s, A);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Threads a row and pieces a thread for rows of `pieces` 16-byte pieces.
+static void norm_shape(int64_t pieces, int* tpr, int* c) {
+  *tpr = pieces <= 16 ? 16 : pieces <= 256 ? 64 : pieces <= 1024 ? 256 : 1024;
+  const int64_t per = (pieces + *tpr - 1) / *tpr;
+  *c = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
+}
+
+hipError_t launch_norm(const NormArgs& A, hipStream_t s) {
+  return by_type(A.dtype, [&](auto zero) {
+    using T = decltype(zero);
+    int tpr, c;
+    norm_shape((A.D + kPer<T> - 1) / kPer<T>, &tpr, &c);
+    switch (tpr * 16 + c) {
+      case 16 * 16 + 1: return run_norm<T, 16, 1>(A, s);
+      case 64 * 16 + 1: return run_norm<T, 64, 1>(A, s);
+      case 64 * 16 + 2: return run_norm<T, 64, 2>(A, s);
+      case 64 * 16 + 4: return run_norm<T, 64, 4>(A, s);
+      case 256 * 16 + 2: return run_norm<T, 256, 2>(A, s);
+      case 256 * 16 + 4: return run_norm<T, 256, 4>(A, s);
+      case 1024 * 16 + 2: return run_norm<T, 1024, 2>(A, s);
+      case 1024 * 16 + 4: return run_norm<T, 1024, 4>(A, s);
+      default: break;
+    }
+    if constexpr (sizeof(T) == 4) return run_norm<T, 1024, 8>(A, s);
+    return hipErrorInvalidValue;  // D <= 32768
+  });
+}
+
+NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums) {
+  NormPlan p{};
+  const int e = dtype == 0 ? 4 : 8;
+  norm_shape((D + e - 1) / e, &p.tpr, &p.c);
+  p.wide = D > 16384;  // more accumulators than registers
+  const int64_t rpb = p.tpr >= 256 ? 1 : 256 / p.tpr, groups = (R + rpb - 1) / rpb;
+  p.grid = want_sums && !p.wide ? std::min<int64_t>(groups, 1024) : std::min<int64_t>(groups, 1 << 16);
+  p.parts = p.wide ? std::min<int64_t>(64, std::max<int64_t>(1, R)) : p.grid;
+  p.bytes = want_sums ? sizeof(float) * 2 * (size_t)D * (size_t)p.parts : 0;
+  return p;
+}
+
+hipError_t launch_norm_grad(NormArgs A, const NormPlan& p, float* dgamma, float* dbeta, hipStream_t s) {
+  const bool sums = dgamma || dbeta, acc = sums && !p.wide;
+  if (A.dx || acc) {
+    const hipError_t e = by_type(A.dtype, [&](auto zero) {
+      using T = decltype(zero);
+      const unsigned g = (unsigned)p.grid;
+      switch ((p.tpr * 16 + p.c) * 2 + acc) {
+#define GMM_NORM_GRAD(TPR, C)                                                    \
+  case (TPR * 16 + C) * 2: return run_grad<T, TPR, C, false>(A, g, s);           \
+  case (TPR * 16 + C) * 2 + 1: return run_grad<T, TPR, C, true>(A, g, s);
+        GMM_NORM_GRAD(16, 1)
+        GMM_NORM_GRAD(64, 1)
+        GMM_NORM_GRAD(64, 2)
+        GMM_NORM_GRAD(64, 4)
+        GMM_NORM_GRAD(256, 2)
+        GMM_NORM_GRAD(256, 4)
+        GMM_NORM_GRAD(1024, 2)
+#undef GMM_NORM_GRAD
+        case (1024 * 16 + 4) * 2: return run_grad<T, 1024, 4, false>(A, g, s);
+        default: break;
+      }
+      if constexpr (sizeof(T) == 4)  // D <= 16384, and past it without sums
+        return acc ? run_grad<T, 1024, 4, true>(A, g, s) : run_grad<T, 1024, 8, false>(A, g, s);
+      return hipErrorInvalidValue;
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!sums) return hipSuccess;
+  if (p.wide) {
+    const hipError_t e = by_type(A.dtype, [&](auto zero) {
+      using T = decltype(zero);
+      hipLaunchKernelGGL(norm_columns_kernel<T>, dim3((unsigned)((A.D + 255) / 256), (unsigned)p.parts), dim3(256), 0, s, A,
+                         (A.R + p.parts - 1) / p.parts);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((2 * A.D + 63) / 64)), dim3(1024), 0, s, A.part, (int)p.parts, A.D,
+                     dgamma, dbeta, A.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace gmm

@@ -1,0 +1,235 @@
+"""gmm_adamw_step on the GPU: against the same float32 operations in numpy, bit
+by bit, and against the formula in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import head_ref
+import step_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def g():
+    assert torch.cuda.is_available(), "GPU tests need a visible GPU"
+    import soft_clustering_em_amd as g
+    return g
+
+
+def npf(t):
+    return t.detach().float().cpu().numpy().reshape(-1)
+
+
+def make(sizes, types=((F32, F32),), seed=0, scale=1e-2):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda n: torch.randn(n, generator=gen, device="cuda")  # noqa: E731
+    p = [rand(n).to(types[i % len(types)][0]) for i, n in enumerate(sizes)]
+    return p, [(scale * rand(n)).to(types[i % len(types)][1]) for i, n in enumerate(sizes)]
+
+
+def same(name, got, want):
+    got, want = (a.view(np.uint32) if a.dtype == np.float32 else a for a in (np.asarray(got), np.asarray(want)))
+    bad = np.flatnonzero(got != want)
+    if bad.size:
+        raise AssertionError(f"{name}: {bad.size} of {got.size} differ, first at {bad[:5]}: {got[bad[:3]]} {want[bad[:3]]}")
+
+
+def run_both(g, p, grads, bits, steps=3, copies=None, seed=7, **kw):
+    """Some steps of the library beside the numpy form; states and values equal bit for bit."""
+    st = g.new_adamw_state(p, bits)
+    bits_of = bits if isinstance(bits, list) else [bits] * len(p)
+    mirror = []
+    for t, b in zip(p, bits_of):
+        n = t.numel()
+        z = np.zeros(n, np.float32)
+        mirror.append([npf(t), z, z.copy()] if b == 32 else
+                      [npf(t), np.zeros(n, np.uint8), np.zeros(n, np.uint8)] + [np.zeros(-(-n // 256), np.float32) for _ in range(2)])
+    for step in range(1, steps + 1):
+        g.gmm_adamw_step(p, grads, step=step, seed=seed, copies=copies, **st, **kw)
+        for j, (t, gr, s) in enumerate(zip(p, grads, mirror)):
+            args = {k: v for k, v in kw.items() if k in ("lr", "betas", "eps")}
+            wd = kw.get("weight_decay", 0.01)
+            args["weight_decay"] = wd[j] if isinstance(wd, (list, tuple)) else wd
+            if kw.get("norm") is not None:
+                q = kw["max_norm"] / (float(kw["norm"].double()) + 1e-6)
+                args["clip"] = 1.0 if kw["max_norm"] == math.inf else q if q < 1 or q != q else 1.0  # no limit: no clipping
+            if bits_of[j] == 32:
+                new, s[1], s[2], _ = ref.adamw(s[0], npf(gr), s[1], s[2], step, **args)
+                same("m", npf(st["m"][j]), s[1])
+                same("v", npf(st["v"][j]), s[2])
+            else:
+                r = ref.decode(s[2], s[4])
+                new, m, _, r = ref.adamw(s[0], npf(gr), ref.decode(s[1], s[3]), r * r, step, **args)
+                dm, dv = ref.dither(len(m), j, step, seed)
+                s[1], s[3] = ref.encode(m, dm, False)
+                s[2], s[4] = ref.encode(r, dv, True)
+                for k, name in ((1, "m"), (2, "v")):
+                    same(name, st[name][j].view(torch.uint8).cpu().numpy().reshape(-1), s[k])
+                    same(name + "_scale", npf(st[name + "_scale"][j]), s[k + 2])
+            stored = torch.from_numpy(new).to(t.dtype)
+            assert torch.equal(t.cpu().reshape(-1), stored), j
+            s[0] = npf(stored)
+            if copies is not None and copies[j] is not None:
+                assert torch.equal(copies[j].cpu().reshape(-1), torch.from_numpy(new).to(copies[j].dtype))
+
+
+SIZES = [[1], [7], [256], [257], [8191], [8192, 1, 8193], [5, 1000, 33, 20000, 1, 255], list(range(1, 80)), [300001, 17, 0, 3]]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", SIZES)
+def test_sizes(g, sizes, bits):
+    p, gr = make(sizes)
+    run_both(g, p, gr, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("tp", [F32, BF16, F16])
+@pytest.mark.parametrize("tg", [F32, BF16, F16])
+def test_types_and_copies(g, tp, tg, bits):
+    p, gr = make([5000, 77], ((tp, tg),))
+    copies = [torch.empty(5000, dtype=BF16, device="cuda"), None if tp == F16 else torch.empty(77, dtype=F16, device="cuda")]
+    run_both(g, p, gr, bits, copies=copies)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kw", [dict(lr=0.0), dict(lr=0.3, betas=(0.0, 0.0), eps=1e-3), dict(betas=(0.95, 0.9), weight_decay=0.0),
+                                dict(weight_decay=[0.1, 0.0, 0.3]), dict(eps=0.0)])
+def test_settings(g, kw, bits):
+    p, gr = make([1000, 300, 4097], ((F32, BF16), (F32, F32)))
+    run_both(g, p, gr, bits, **kw)
+
+
+@pytest.mark.parametrize("norm,max_norm", [(5.0, 1.0), (0.5, 1.0), (0.0, 1.0), (3.0, 0.0), (1e30, 1e-3), (2.0, math.inf),
+                                           (math.inf, math.inf)])
+def test_clipping_on_the_way(g, norm, max_norm):
+    p, gr = make([1000, 300])
+    run_both(g, p, gr, 32, norm=torch.tensor([norm], device="cuda"), max_norm=max_norm)
+
+
+def test_clipping_is_that_of_the_clipping_call(g):
+    p, gr = make([1000, 300], scale=1.0)
+    q, st, st2 = [t.clone() for t in p], g.new_adamw_state(p), g.new_adamw_state(p)
+    norm = g.gmm_clip_grad_norm([t.clone() for t in gr], math.inf)
+    g.gmm_adamw_step(p, gr, step=1, norm=norm, max_norm=0.5, **st)
+    g.gmm_clip_grad_norm(gr, 0.5)
+    g.gmm_adamw_step(q, gr, step=1, **st2)
+    assert all(torch.equal(a, b) for a, b in zip(p + st["m"] + st["v"], q + st2["m"] + st2["v"]))
+
+
+def test_against_the_formula_in_64_bits(g):
+    """One step from given states: m' three roundings, v' four, the update under
+    ten and the last difference one, each relative to the terms' absolute sum."""
+    p, gr = make([20000])
+    m, v = make([20000], seed=5)[1], [t.square() for t in make([20000], seed=6)[1]]
+    old = [npf(t[0]) for t in (p, gr, m, v)]
+    g.gmm_adamw_step(p, gr, m, v, 37, lr=0.01, weight_decay=0.1)
+    P, M, V, _ = ref.adamw(*old, 37, lr=0.01, weight_decay=0.1, real=np.float64)
+    u = ref.U
+    assert (np.abs(npf(m[0]) - M) <= 3 * u * (0.9 * np.abs(old[2]) + 0.1 * np.abs(old[1]))).all()
+    assert (np.abs(npf(v[0]) - V) <= 5 * u * V).all()
+    m_rel = 3 * u * (0.9 * np.abs(old[2]) + 0.1 * np.abs(old[1]))
+    step = 0.01 / (1 - 0.9 ** 37) / (np.sqrt(V / (1 - 0.999 ** 37)) + 1e-8)
+    tol = step * (m_rel + 12 * u * np.abs(M)) + 3 * u * (np.abs(old[0]) + np.abs(P))
+    assert (np.abs(npf(p[0]) - P) <= tol).all()
+
+
+def test_unaligned_views(g):
+    flat, grad = make([50000], ((BF16, BF16),))
+    flat, grad = flat[0], grad[0]
+    cuts = [(1, 5000), (5003, 40001), (40001, 40002)]
+    keep = flat[5000:5003].clone()
+    run_both(g, [flat[a:b] for a, b in cuts], [grad[a:b] for a, b in cuts], 32)
+    assert torch.equal(flat[5000:5003], keep)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_small_and_zero_gradients(g, bits):
+    p, gr = make([2000, 2000, 600, 700], scale=1e-30)
+    gr[1].zero_()
+    gr[2].mul_(1e-8)
+    gr[3][::2] = 1e-3  # beside values far below one block's smallest step
+    run_both(g, p, gr, bits, steps=4)
+    assert all(torch.isfinite(t).all() for t in p)
+
+
+def test_nan_gradients_stay_in_their_block(g):
+    for bits in (32, 8):
+        p, gr = make([1000])
+        gr[0][300], gr[0][700] = float("nan"), float("inf")
+        st = g.new_adamw_state(p, bits)
+        for step in (1, 2):
+            g.gmm_adamw_step(p, gr, step=step, **st)
+        bad = ~torch.isfinite(p[0])
+        assert bad[300] and bad[700]
+        if bits == 32:
+            assert bad.sum() == 2
+        else:
+            assert not bad[:256].any() and not bad[768:].any()
+
+
+def test_rounding_of_8_bit_states_is_unbiased(g):
+    """A constant between two steps: 65536 elements, of which the share rounded up
+    is the remainder's, 0.5 / sqrt(65536) = 0.002 a standard deviation; and a state
+    whose second moment falls by half a thousandth a step falls with it."""
+    n = 65536
+    p, gr = [torch.zeros(n, device="cuda")], [torch.full((n,), 10.3, device="cuda")]
+    gr[0][::256] = 448.0
+    st = g.new_adamw_state(p, 8)
+    g.gmm_adamw_step(p, gr, step=1, betas=(0.0, 0.0), **st)
+    for name in ("m", "v"):
+        t = st[name][0].float().view(-1, 256)[:, 1:].double()
+        assert set(t.unique().tolist()) == {10.0, 11.0}
+        assert abs(float((t == 11.0).double().mean()) - 0.3) < 6 * 0.002
+    assert (st["m"][0].float() != st["v"][0].float()).any()  # numbers of their own
+    gr[0].fill_(0.0)
+    gr[0][::256] = 448.0  # the scale stays, the others decay by 0.9995 a step
+    for step in range(2, 202):
+        g.gmm_adamw_step(p, gr, step=step, betas=(0.9, 0.999), **st)
+    left = float((st["v"][0].float() * st["v_scale"][0].repeat_interleave(256)).view(-1, 256)[:, 1:].mean())
+    assert abs(left / (10.3 * 0.999 ** 100) - 1) < 0.02
+
+
+def test_step_and_rate_on_the_device_captured(g):
+    p, gr = make([3000, 500], ((F32, BF16),))
+    for bits in (32, 8):
+        q = [t.clone() for t in p]
+        st, st2 = g.new_adamw_state(p, bits), g.new_adamw_state(p, bits)
+        count, lr = torch.ones((), dtype=torch.int64, device="cuda"), torch.tensor([1e-2], device="cuda")
+        w = [t.clone() for t in p]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            g.gmm_adamw_step(w, gr, step=count, lr=lr, seed=3, **st)
+            count.add_(1)
+        for step in range(1, 5):
+            for t in gr:
+                t.normal_()
+            lr.fill_(1e-2 / step)
+            graph.replay()
+            torch.cuda.synchronize()
+            g.gmm_adamw_step(q, gr, step=step, lr=float(lr), seed=3, **st2)
+            for a, b in zip(w + st["m"] + st["v"], q + st2["m"] + st2["v"]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (bits, step)
+
+
+def test_many_tensors(g):
+    p, gr = make([1 + 13 * i % 700 for i in range(200)], ((F32, F32), (BF16, BF16)))
+    run_both(g, p, gr, 32, steps=1)
+    p, gr = make([1 + 13 * i % 700 for i in range(200)])
+    run_both(g, p, gr, 8, steps=2)
+
+
+def test_mixed_states_in_one_call(g):
+    p, gr = make([700, 900])
+    a, b = g.new_adamw_state(p[:1], 8), g.new_adamw_state(p[1:], 32)
+    q = [t.clone() for t in p]
+    g.gmm_adamw_step(p, gr, a["m"] + b["m"], a["v"] + b["v"], 1, m_scale=a["m_scale"] + [None], v_scale=a["v_scale"] + [None])
+    c, d = g.new_adamw_state(p[:1], 8), g.new_adamw_state(p[1:], 32)
+    g.gmm_adamw_step(q[:1], gr[:1], step=1, **c)
+    g.gmm_adamw_step(q[1:], gr[1:], step=1, **d)
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(p + a["m"] + b["v"], q + c["m"] + d["v"]))
