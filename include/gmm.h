@@ -542,8 +542,8 @@ gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, i
  * States: m and v float32 (m_scale = v_scale = NULL), or 8 bits: m and v (n) OCP
  * e4m3 bytes, m_scale and v_scale ((n + 255) / 256) float32, one for every 256
  * elements, m = byte value x scale and sqrt(v) = byte value x scale, with scale =
- * max / 448 of the block (0 for a block below 2^-100).  x = value / scale is rounded
- * to the neighbour above with the probability of its remainder: up when the bits
+ * max (1 / 448) of the block (0 for a block below 2^-100).  x = value (1 / max 448),
+ * at most 448, is rounded to the neighbour above with the probability of its remainder: up when the bits
  * below the last kept one (as 16 bits) plus d reach 2^16, with d the upper (m) or
  * lower (sqrt v) half of
  *   h = mix(mix(mix(mix(seed + 0x9E3779B1 t) ^ tensor) + block) + 0x9E3779B1 i)

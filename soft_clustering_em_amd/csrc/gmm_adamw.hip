@@ -101,8 +101,8 @@ __device__ inline void store_codes(uint8_t* p, float* scale, const float (&f)[kE
     top = a > top || a != a ? a : top;
   }
   top = half_wave_max(top);
-  const bool none = top < 0x1p-100f;  // 448 / top would leave float32
-  const float s = none ? 0.f : top / 448.f, inv = none ? 0.f : 448.f / top;
+  const bool none = top < 0x1p-100f;  // 1 / top times 448 would leave float32
+  const float s = none ? 0.f : top * (1.f / 448.f), inv = none ? 0.f : 1.f / top * 448.f;
   uint8_t b[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {

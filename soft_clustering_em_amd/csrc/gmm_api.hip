@@ -1906,7 +1906,7 @@ static gmm_status sample_check(const gmm_data* logits) { return rows_check(logit
 
 size_t gmm_sample_workspace_bytes(const gmm_data* logits) {
   if (sample_check(logits) != GMM_OK) return 0;
-  return kAlign;
+  return std::max(kAlign, align_up(sample_bytes(logits->B * logits->N, logits->D)));
 }
 
 gmm_status gmm_sample(const gmm_data* logits, const gmm_sampling* how, const float* u, int32_t* tokens, float* logp,
@@ -1950,7 +1950,7 @@ gmm_status gmm_sample(const gmm_data* logits, const gmm_sampling* how, const flo
   while (((int64_t)1 << bits) < a.V) ++bits;
   a.scale = std::ldexp(1.0, std::min(52, 62 - bits));
   a.dtype = logits->dtype;
-  const hipError_t e = launch_sample(a, (hipStream_t)stream);
+  const hipError_t e = launch_sample(a, ws, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "sampling launch");
   return GMM_OK;
 }

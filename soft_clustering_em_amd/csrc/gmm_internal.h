@@ -439,6 +439,14 @@ struct AdamArgs {
 hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs a, hipStream_t s);
 
 // sampling (gmm_sample.hip)
+constexpr int kSampleParts = 64, kSampleList = 2048;
+struct SampleRow {         // of a long row, in the workspace
+  unsigned long long best[kSampleParts], mass[kSampleParts];  // of every part
+  unsigned long long bin[2048];
+  unsigned long long list[2 * kSampleList];
+  unsigned long long whole, above;
+  int at, na, nb, pad;
+};
 struct SampleArgs {
   const void* l;
   const float *u, *row_temperature, *row_top_p, *row_min_p;
@@ -448,8 +456,11 @@ struct SampleArgs {
   int64_t R, N, V, ld, stride_b, top_k;
   double temperature, top_p, min_p, scale;
   int dtype;
+  int64_t r0, part;        // first row of a launch, elements of a part
+  SampleRow* rows;
 };
-hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
+size_t sample_bytes(int64_t R, int64_t V);
+hipError_t launch_sample(SampleArgs a, void* ws, hipStream_t s);
 
 // fused E-step + statistics (gmm_estep.hip)
 hipError_t launch_estep(const Plan& p, const EStepArgs& a, hipStream_t s);

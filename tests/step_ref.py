@@ -182,8 +182,8 @@ def encode(x, d, root):
     top = np.abs(pad).max(1)
     none = top < f(2.0 ** -100)
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
-        s = np.where(none, f(0), top / f(448)).astype(f)
-        inv = np.where(none, f(0), f(448) / top).astype(f)
+        s = np.where(none, f(0), top * (f(1) / f(448))).astype(f)
+        inv = np.where(none, f(0), f(1) / top * f(448)).astype(f)
         y = (pad * inv[:, None]).reshape(-1)[:n].astype(f)
     a = np.minimum(np.abs(y), f(448)).astype(f)
     up = ((a.view(np.uint32) + (d << np.uint32(4))) >> np.uint32(20)).astype(np.int64) - (120 << 3)
