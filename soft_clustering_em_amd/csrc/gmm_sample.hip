@@ -31,35 +31,34 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kBins = 2048, kSegs = 128, kList = 2048;
+constexpr int kFewKept = 256;  // top-p: so few elements down to the cut are sorted, more are passed over once more
 constexpr float kBinsPerUnit = 64.f;
 
-// Live logits in the order of their values, from 1 up; 0 for NaN and -inf.
+// Logits in the order of their values, from 1 up.
 __device__ inline uint32_t key_of(float l) {
-  if (!(l > -INFINITY)) return 0;
-  l = fminf(l, FLT_MAX) + 0.f;  // -0 is 0
+  l += 0.f;  // -0 is 0
   const uint32_t u = __float_as_uint(l);
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 __device__ inline float logit_of(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key); }
 
-// exp(z) for z <= 0: 2^n exp(r), |r| <= ln 2 / 2, by its series to r^13 / 13!
-// (what is left out is below 2^-57), 0 below -745.
+// exp(z) for z <= 0: 2^n exp(r), |r| <= ln 2 / 2, by a polynomial whose
+// coefficients from r^2 on are fitted to that interval (off by 2^-58; with its
+// roundings under 1.4 units of 2^-53); 1 at 0, 0 below -745.
 __device__ inline double exp_neg(double z) {
   z = fmax(z, -800.0);
   const double n = rint(z * 1.4426950408889634);
   const double r = fma(n, -2.3190468138462996e-17, fma(n, -0.6931471805599453, z));  // ln 2 in two parts
-  double p = 1.0 / 6227020800.0;
-  p = fma(p, r, 1.0 / 479001600.0);
-  p = fma(p, r, 1.0 / 39916800.0);
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
+  double p = 2.511786550847911e-08;
+  p = fma(p, r, 2.7631288950513367e-07);
+  p = fma(p, r, 2.7557216288999207e-06);
+  p = fma(p, r, 2.480148991617872e-05);
+  p = fma(p, r, 0.00019841269917404014);
+  p = fma(p, r, 0.0013888888947043258);
+  p = fma(p, r, 0.00833333333330718);
+  p = fma(p, r, 0.041666666666515306);
+  p = fma(p, r, 0.166666666666667);
+  p = fma(p, r, 0.5000000000000012);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
   return ldexp(p, (int)n);
@@ -74,22 +73,22 @@ struct Row {
   double inv, S;   // 1 / temperature, 2^S
   double least;    // min-p
   float bins;      // bins a unit of logits
-  __device__ double z(uint32_t key) const { return ((double)logit_of(key) - (double)mx) * inv; }
-  __device__ double share(uint32_t key) const { return exp_neg(z(key)); }
+  __device__ double z(float l) const { return ((double)l - (double)mx) * inv; }
+  __device__ double share(float l) const { return exp_neg(z(l)); }
   // e 2^S rounded to an integer: at most 2^52, the low bits of its sum with 2^52
   __device__ u64 fixed(double e) const {
     return (u64)__double_as_longlong(e * S + 0x1p52) - (u64)__double_as_longlong(0x1p52);
   }
-  __device__ u64 weight(uint32_t key) const { return fixed(share(key)); }
-  __device__ u64 weight_min_p(uint32_t key) const {
-    const double e = share(key);
+  __device__ u64 weight(float l) const { return fixed(share(l)); }
+  __device__ u64 weight_min_p(float l) const {
+    const double e = share(l);
     return e >= least ? fixed(e) : 0;
   }
   // descending logits have ascending bins
-  __device__ int bin(uint32_t key) const { return (int)fminf((mx - logit_of(key)) * bins, (float)(kBins - 1)); }
+  __device__ int bin(float l) const { return (int)fminf((mx - l) * bins, (float)(kBins - 1)); }
 };
 
-// f(index, key) for the live elements of [i0, i1), i0 a multiple of the piece, by `threads` threads
+// f(index, logit) for the live elements of [i0, i1), i0 a multiple of the piece, by `threads` threads
 template <typename T, typename F>
 __device__ inline void pieces(const Row& R, int64_t i0, int64_t i1, int thread, int threads, F f) {
   constexpr int E = 16 / (int)sizeof(T);
@@ -104,8 +103,8 @@ __device__ inline void pieces(const Row& R, int64_t i0, int64_t i1, int thread, 
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint32_t key = key_of((float)v[e]);
-      if (key) f(i + e, key);
+      const float l = fminf((float)v[e], FLT_MAX);
+      if ((float)v[e] > -INFINITY) f(i + e, l);
     }
   }
 }
@@ -161,14 +160,15 @@ __device__ inline u64 block_scan(u64 v, u64* red) {
   __syncthreads();
   if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  for (int k = 0; k < (int)(threadIdx.x >> 6); ++k) v += red[k];
+#pragma unroll
+  for (int k = 0; k < TH / 64 - 1; ++k) v += k < (int)(threadIdx.x >> 6) ? red[k] : 0;
   return v;
 }
 
-// What is kept: keys above `key`, and of the keys equal to it the first `ties`
-// by index.  {0, 0}: every live element.
+// What is kept: logits above l, and of those equal to it the first `ties` by
+// index.  {-INFINITY, 0}: every live element.
 struct Cut {
-  uint32_t key;
+  float l;
   u64 ties;
 };
 
@@ -206,29 +206,54 @@ __device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row&
   q.k = A.row_top_k ? A.row_top_k[r] : A.top_k;
   q.top_p = A.row_top_p ? (double)A.row_top_p[r] : A.top_p;
   q.mode = !best ? kNone : !(T > 0.0) || q.k == 1 ? kGreedy : q.k > 0 && q.k < A.V ? kCount : q.top_p < 1.0 ? kMass : kOpen;
-  R.inv = T > 0.0 ? 1.0 / T : 1.0;
+  R.inv = T > 0.0 ? fmin(1.0 / T, 1e300) : 1.0;
   R.least = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
   R.bins = (float)fmin((double)kBinsPerUnit * R.inv, (double)FLT_MAX);
   return q;
 }
 
-// a share of the row: its largest key with ~ its lowest index
-__device__ inline u64 best_of(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
-  uint32_t top = 0, at = 0;
-  each(R, i0, i1, thread, threads, [&](int64_t i, uint32_t key) {
-    if (key > top) {
-      top = key;
-      at = (uint32_t)i;
+// a share of the row: its largest key with ~ its lowest index.  A thread notes
+// the piece that its maximum came with, and looks into it at the end.
+template <typename T>
+__device__ inline u64 best_pieces(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const T* p = static_cast<const T*>(R.l) + R.at;
+  float top = -INFINITY;
+  int64_t at = -1;
+#pragma unroll 4
+  for (int64_t i = i0 + (int64_t)thread * E; i < i1; i += (int64_t)threads * E) {
+    T v[E];
+    if (i + E <= i1) {
+      __builtin_memcpy(v, p + i, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = i + e < i1 ? p[i + e] : (T)-INFINITY;
     }
-  });
-  return top ? (u64)top << 32 | (uint32_t)~at : 0;
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, (float)v[e]);  // NaN is passed over
+    m = fminf(m, FLT_MAX);
+    at = m > top ? i : at;
+    top = fmaxf(m, top);
+  }
+  if (at < 0) return 0;
+  uint32_t index = 0;
+#pragma unroll
+  for (int e = E - 1; e >= 0; --e)
+    if (at + e < i1 && fminf((float)p[at + e], FLT_MAX) == top) index = (uint32_t)(at + e);
+  return (u64)key_of(top) << 32 | (uint32_t)~index;
+}
+__device__ inline u64 best_of(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
+  if (R.dtype == 0) return best_pieces<float>(R, i0, i1, thread, threads);
+  if (R.dtype == 1) return best_pieces<__bf16>(R, i0, i1, thread, threads);
+  return best_pieces<_Float16>(R, i0, i1, thread, threads);
 }
 
 __device__ inline void fill_bins(const Row& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin) {
   if (mode == kCount)
-    each(R, i0, i1, thread, threads, [&](int64_t, uint32_t key) { atomicAdd(&bin[R.bin(key)], (u64)1); });
+    each(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
   else
-    each(R, i0, i1, thread, threads, [&](int64_t, uint32_t key) { atomicAdd(&bin[R.bin(key)], R.weight(key)); });
+    each(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], R.weight(l)); });
 }
 
 // sh.at: the bin at which the count or the mass reaches its target (the last one
@@ -269,10 +294,10 @@ __device__ inline u64 cut_bin(const Settings& q, Cutting& sh, const u64* bin) {
 // ~index from the two ends of sh.list; counters that pass its half say so.
 __device__ inline void collect(const Row& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
   const int at = sh.at;
-  each(R, i0, i1, thread, threads, [&](int64_t i, uint32_t key) {
-    const int b = R.bin(key);
+  each(R, i0, i1, thread, threads, [&](int64_t i, float l) {
+    const int b = R.bin(l);
     if (b > at) return;
-    const u64 v = (u64)key << 32 | (uint32_t)~(uint32_t)i;
+    const u64 v = (u64)key_of(l) << 32 | (uint32_t)~(uint32_t)i;
     const int slot = atomicAdd(b < at ? &sh.na : &sh.nb, 1);
     if (slot < kList / 2) sh.list[b < at ? slot : kList - 1 - slot] = v;
   });
@@ -313,9 +338,10 @@ __device__ inline void scan_list(Shared& sh, int n, F f) {
   }
 }
 
-__device__ inline void answer(const SampleArgs& A, const Row& R, int64_t r, uint32_t key, int64_t i, u64 total) {
+__device__ inline float list_logit(u64 v) { return logit_of((uint32_t)(v >> 32)); }
+__device__ inline void answer(const SampleArgs& A, const Row& R, int64_t r, float l, int64_t i, u64 total) {
   A.tokens[r] = (int32_t)i;
-  if (A.logp) A.logp[r] = (float)(R.z(key) - log((double)total / R.S));
+  if (A.logp) A.logp[r] = (float)(R.z(l) - log((double)total / R.S));
 }
 __device__ inline double aim(const SampleArgs& A, int64_t r, u64 total) {
   return (double)fminf(fmaxf(A.u[r], 0.f), 0x1.fffffep-1f) * (double)total;
@@ -327,13 +353,13 @@ template <int TH>
 __device__ void finish_list(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
   sort_list<TH>(sh, n);
   if (q.mode == kCount) n = (int)min((int64_t)n, q.k);
-  scan_list<TH>(sh, n, [&](int i) { return R.weight((uint32_t)(sh.list[i] >> 32)); });
+  scan_list<TH>(sh, n, [&](int i) { return R.weight(list_logit(sh.list[i])); });
   // the kept ones are a prefix: count them
   const double target = q.top_p * (double)(q.mode == kCount ? sh.sum[n - 1] : mass);
   u64 mine = 0;
   for (int i = threadIdx.x; i < n; i += TH) {
     const bool in = i == 0 || ((!(q.top_p < 1.0) || (double)sh.sum[i - 1] < target) &&
-                               (R.least == 0.0 || R.share((uint32_t)(sh.list[i] >> 32)) >= R.least));
+                               (R.least == 0.0 || R.share(list_logit(sh.list[i])) >= R.least));
     mine += in;
   }
   const int kept = (int)block_sum<TH>(mine, sh.red);
@@ -363,7 +389,7 @@ __device__ void finish_list(const SampleArgs& A, const Row& R, const Settings& q
     const u64 mine_w = i < kept ? w[e] : 0, to = base + block_scan<TH>(mine_w, sh.red);
     if (i < kept && (double)to > goal && !((double)(to - mine_w) > goal)) {
       const uint32_t index = ~(uint32_t)(sh.list[i] >> 32);
-      answer(A, R, r, key_of(x_value(R.l, R.dtype, R.at + index)), index, total);
+      answer(A, R, r, fminf(x_value(R.l, R.dtype, R.at + index), FLT_MAX), index, total);
     }
     __syncthreads();
     if (threadIdx.x == TH - 1) sh.above = to;
@@ -372,89 +398,97 @@ __device__ void finish_list(const SampleArgs& A, const Row& R, const Settings& q
   }
 }
 
-// Segments of [i0, i1): their kept weights, and their elements equal to the cut.
+// One wave: the place at which sums over lanes pass the goal.  n and ties are
+// this lane's, wt the weight of a tie, of which `left` are kept; before is what
+// lies before lane 0.  Afterwards `before` and `left` are those of the lane
+// returned (the last one with anything if none passes).
+__device__ inline int pass_at(u64 n, u64 ties, u64 wt, double goal, u64& before, u64& left) {
+  const u64 ties_to = wave_scan_u64(ties), ties_from = ties_to - ties;
+  n += (min(ties_to, left) - min(ties_from, left)) * wt;
+  const u64 to = before + wave_scan_u64(n);
+  const u64 hit = __ballot((double)to > goal), any = __ballot(n != 0);
+  const int lane = hit ? __builtin_ctzll(hit) : any ? 63 - __builtin_clzll(any) : 0;
+  before = __shfl(to - n, lane);
+  left -= min(__shfl(ties_from, lane), left);
+  return lane;
+}
+
+// The row's (or a part's) segments of whole tiles: their kept weights and their
+// elements equal to the cut; then, in one wave, the segment, the tile and the
+// element at which the sum passes the goal.  goal < 0: that of the whole.
 template <int TH>
-__device__ inline int64_t segments(const Row& R, const Cut& cut, int64_t i0, int64_t i1, Shared& sh) {
+__device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_t r, int64_t i0, int64_t i1, u64 before, u64 total,
+                       double goal, Shared& sh) {
   const int E = R.dtype == 0 ? 4 : 8, lane = threadIdx.x & 63;
   const int64_t tile = 64 * E, tiles = (i1 - i0 + tile - 1) / tile, len = (tiles + kSegs - 1) / kSegs * tile;
+  __syncthreads();
   for (int s = threadIdx.x >> 6; s < kSegs; s += TH / 64) {
     const int64_t a = i0 + s * len, b = min(a + len, i1);
     u64 mass = 0, ties = 0;
-    if (a < i1)
-      each(R, a, b, lane, 64, [&](int64_t, uint32_t key) {
-        if (key > cut.key) mass += R.weight_min_p(key);
-        else if (key == cut.key) ++ties;
+    if (a < i1) {
+      each(R, a, b, lane, 64, [&](int64_t, float l) {
+        if (l > cut.l) mass += R.weight_min_p(l);
+        ties += l == cut.l;
       });
-    mass = wave_sum_u64(mass);
-    ties = wave_sum_u64(ties);
+      mass = wave_sum_u64(mass);
+      ties = wave_sum_u64(ties);
+    }
     if (lane == 0) {
       sh.seg[s] = mass;
       sh.tie[s] = (uint32_t)ties;
     }
   }
   __syncthreads();
-  return len;
-}
-
-// The token: the segment in which the sum passes the goal, then its tiles.  One wave.
-__device__ inline void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_t r, int64_t i0, int64_t i1, int64_t len,
-                              u64 before, u64 total, double goal, Shared& sh) {
-  const int E = R.dtype == 0 ? 4 : 8, lane = threadIdx.x & 63;
-  const int64_t tile = 64 * E;
-  const u64 wt = cut.key ? R.weight_min_p(cut.key) : 0;
-  u64 ties = 0;
-  int s = 0;
-  for (; s < kSegs - 1; ++s) {
-    const u64 t = min((u64)sh.tie[s], cut.ties - ties), n = sh.seg[s] + t * wt;
-    if ((double)(before + n) > goal) break;
-    before += n;
-    ties += t;
+  if (threadIdx.x >= 64) return;
+  static_assert(kSegs == 128, "two segments a lane");
+  const u64 wt = cut.ties ? R.weight_min_p(cut.l) : 0;
+  const u64 n0 = sh.seg[2 * lane], n1 = sh.seg[2 * lane + 1], t0 = sh.tie[2 * lane], t1 = sh.tie[2 * lane + 1];
+  if (goal < 0.0) {
+    const u64 ties = min(wave_sum_u64(t0 + t1), cut.ties);
+    total = wave_sum_u64(n0 + n1) + ties * wt;
+    goal = aim(A, r, total);
+  }
+  u64 left = cut.ties;
+  int s = pass_at(n0 + n1, t0 + t1, wt, goal, before, left);
+  // of the lane's two segments
+  const u64 first = __shfl(n0, s) + min(__shfl(t0, s), left) * wt;
+  if (!((double)(before + first) > goal)) {
+    before += first;
+    left -= min(__shfl(t0, s), left);
+    s = 2 * s + 1;
+  } else {
+    s = 2 * s;
   }
   for (int64_t a = i0 + s * len, end = min(a + len, i1); a < end; a += tile) {
     const int64_t b = min(a + tile, end);
     u64 mass = 0, tied = 0;
-    each(R, a, b, lane, 64, [&](int64_t, uint32_t key) {
-      if (key > cut.key) mass += R.weight_min_p(key);
-      else if (key == cut.key) ++tied;
+    each(R, a, b, lane, 64, [&](int64_t, float l) {
+      if (l > cut.l) mass += R.weight_min_p(l);
+      tied += l == cut.l;
     });
-    const u64 tied_to = ties + wave_scan_u64(tied), tied_from = tied_to - tied;
-    mass += (min(tied_to, cut.ties) - min(tied_from, cut.ties)) * wt;
+    const u64 tied_to = wave_scan_u64(tied), tied_from = tied_to - tied;
+    mass += (min(tied_to, left) - min(tied_from, left)) * wt;
     const u64 to = before + wave_scan_u64(mass);
     const u64 hit = __ballot((double)to > goal);
     if (hit) {
       if (lane == __builtin_ctzll(hit)) {
         u64 sum = to - mass, rank = tied_from;
         bool found = false;
-        each(R, a + (int64_t)lane * E, min(a + (int64_t)(lane + 1) * E, b), 0, 64, [&](int64_t i, uint32_t key) {
+        each(R, a + (int64_t)lane * E, min(a + (int64_t)(lane + 1) * E, b), 0, 64, [&](int64_t i, float l) {
           if (found) return;
-          if (key > cut.key) sum += R.weight_min_p(key);
-          else if (key == cut.key && rank++ < cut.ties) sum += wt;
+          if (l > cut.l) sum += R.weight_min_p(l);
+          else if (l == cut.l && rank++ < left) sum += wt;
           if ((double)sum > goal) {
             found = true;
-            answer(A, R, r, key, i, total);
+            answer(A, R, r, l, i, total);
           }
         });
       }
       return;
     }
     before = __shfl(to, 63);
-    ties = __shfl(tied_to, 63);
+    left -= min(__shfl(tied_to, 63), left);
   }
-}
-
-template <int TH>
-__device__ void finish_cut(const SampleArgs& A, const Row& R, const Cut& cut, int64_t r, Shared& sh) {
-  __syncthreads();
-  const int64_t len = segments<TH>(R, cut, 0, R.V, sh);
-  if (threadIdx.x >= 64) return;
-  const u64 wt = cut.key ? R.weight_min_p(cut.key) : 0;
-  u64 total = 0, ties = 0;
-  for (int s = 0; s < kSegs; ++s) {
-    const u64 t = min((u64)sh.tie[s], cut.ties - ties);
-    total += sh.seg[s] + t * wt;
-    ties += t;
-  }
-  choose(A, R, cut, r, 0, R.V, len, 0, total, aim(A, r, total), sh);
 }
 
 // The prefix of the kept elements, by descending key, at which the count (by
@@ -462,22 +496,24 @@ __device__ void finish_cut(const SampleArgs& A, const Row& R, const Cut& cut, in
 // range, then of the bin that it is reached in, until one key is left.  For
 // rows whose cut lies among more equal or nearly equal logits than a list holds.
 template <int TH, bool MASS>
-__device__ Cut reach(const Row& R, Shared& sh, Cut kept, uint32_t hi, double target) {
-  uint32_t lo = kept.key ? kept.key : 1;
+__device__ Cut reach(const Row& R, Shared& sh, Cut kept, double target) {
+  const uint32_t cut = kept.ties ? key_of(kept.l) : 0;
+  uint32_t lo = cut ? cut : 1, hi = key_of(R.mx);
   u64 above = 0;
-  const u64 tied = kept.key ? kept.ties * (MASS ? R.weight(kept.key) : 1) : 0;
+  const u64 tied = kept.ties * (MASS && cut ? R.weight(kept.l) : 1);
   for (;;) {
     int shift = 0;
     while (((hi - lo) >> shift) >= kBins) ++shift;
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
     __syncthreads();
-    each(R, 0, R.V, threadIdx.x, TH, [&](int64_t, uint32_t key) {
-      if (key >= lo && key <= hi && key != kept.key) atomicAdd(&sh.bin[(hi - key) >> shift], MASS ? R.weight(key) : (u64)1);
+    each(R, 0, R.V, threadIdx.x, TH, [&](int64_t, float l) {
+      const uint32_t key = key_of(l);
+      if (key >= lo && key <= hi && key != cut) atomicAdd(&sh.bin[(hi - key) >> shift], MASS ? R.weight(l) : (u64)1);
     });
     __syncthreads();
     if (threadIdx.x == 0) {
-      if (kept.key >= lo && kept.key <= hi && kept.key) sh.bin[(hi - kept.key) >> shift] += tied;
+      if (cut >= lo && cut <= hi) sh.bin[(hi - cut) >> shift] += tied;
       sh.at = -1;
     }
     __syncthreads();
@@ -507,59 +543,46 @@ __device__ Cut reach(const Row& R, Shared& sh, Cut kept, uint32_t hi, double tar
     const uint32_t last = hi - (((uint32_t)1 << shift) - 1);
     lo = last > lo && last <= hi ? last : lo;
     if (shift != 0) continue;
-    const u64 w = MASS ? R.weight(hi) : 1, have = in / w;
+    const u64 w = MASS ? R.weight(logit_of(hi)) : 1, have = in / w;
     u64 ties = target > (double)above ? (u64)((target - (double)above) / (double)w) : 1;
     ties = ties < 1 ? 1 : ties > have ? have : ties;
     while (ties > 1 && (double)(above + (ties - 1) * w) >= target) --ties;
     while (ties < have && (double)(above + ties * w) < target) ++ties;
-    return Cut{hi, ties};
+    return Cut{logit_of(hi), ties};
   }
 }
 
 template <int TH>
 __device__ void finish_reach(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh) {
-  const uint32_t top = key_of(R.mx);
-  Cut cut{0, 0};
-  if (q.mode == kCount) cut = reach<TH, false>(R, sh, cut, top, (double)q.k);
+  Cut cut{-INFINITY, 0};
+  if (q.mode == kCount) cut = reach<TH, false>(R, sh, cut, (double)q.k);
   if (q.top_p < 1.0) {
     u64 mass = 0;
-    each(R, 0, R.V, threadIdx.x, TH, [&](int64_t, uint32_t key) {
-      if (key > cut.key) mass += R.weight(key);
+    each(R, 0, R.V, threadIdx.x, TH, [&](int64_t, float l) {
+      if (l > cut.l) mass += R.weight(l);
     });
-    mass = block_sum<TH>(mass, sh.red) + (cut.key ? cut.ties * R.weight(cut.key) : 0);
-    cut = reach<TH, true>(R, sh, cut, top, q.top_p * (double)mass);
+    mass = block_sum<TH>(mass, sh.red) + (cut.ties ? cut.ties * R.weight(cut.l) : 0);
+    cut = reach<TH, true>(R, sh, cut, q.top_p * (double)mass);
   }
-  finish_cut<TH>(A, R, cut, r, sh);
+  choose<TH>(A, R, cut, r, 0, R.V, 0, 0, -1.0, sh);
 }
 
-// The row from its bins' cut (sh.at, sh.above), the `nb` elements of that bin and
-// the `na` above it, which `copy` brings into sh.list.
-template <int TH, typename F>
-__device__ void finish(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh, u64 whole, int na, int nb,
-                       int cap, F copy) {
-  if (na <= cap && nb <= cap && na + nb <= kList) {
-    copy(0, na, nb);
-    __syncthreads();
-    finish_list<TH>(A, R, q, r, sh, na + nb, whole);
-  } else if (q.mode == kMass && nb <= min(cap, kList)) {
-    // the cut inside its bin, then the row by index
-    const u64 above = sh.above;
-    copy(0, 0, nb);
-    __syncthreads();
-    sort_list<TH>(sh, nb);
-    scan_list<TH>(sh, nb, [&](int i) { return R.weight((uint32_t)(sh.list[i] >> 32)); });
-    const double target = q.top_p * (double)whole;
-    for (int i = threadIdx.x; i < nb; i += TH)
-      if ((double)(above + sh.sum[i]) >= target && (i == 0 || (double)(above + sh.sum[i - 1]) < target)) sh.at = i;
-    __syncthreads();
-    const int at = sh.at;
-    const uint32_t key = (uint32_t)(sh.list[at] >> 32);
-    u64 same = 0;
-    for (int i = threadIdx.x; i <= at; i += TH) same += (uint32_t)(sh.list[i] >> 32) == key;
-    finish_cut<TH>(A, R, Cut{key, block_sum<TH>(same, sh.red)}, r, sh);
-  } else {
-    finish_reach<TH>(A, R, q, r, sh);
-  }
+// The cut of a row whose mass is `whole`, among the nb elements of its bin in
+// sh.list (sh.above: the mass before them); sh.at: its place in the sorted list.
+template <int TH>
+__device__ Cut cut_of_bin(const Row& R, const Settings& q, Shared& sh, u64 whole, int nb) {
+  const u64 above = sh.above;
+  sort_list<TH>(sh, nb);
+  scan_list<TH>(sh, nb, [&](int i) { return R.weight(list_logit(sh.list[i])); });
+  const double target = q.top_p * (double)whole;
+  for (int i = threadIdx.x; i < nb; i += TH)
+    if ((double)(above + sh.sum[i]) >= target && (i == 0 || (double)(above + sh.sum[i - 1]) < target)) sh.at = i;
+  __syncthreads();
+  const int at = sh.at;
+  const float l = list_logit(sh.list[at]);
+  u64 same = 0;
+  for (int i = threadIdx.x; i <= at; i += TH) same += list_logit(sh.list[i]) == l;
+  return Cut{l, block_sum<TH>(same, sh.red)};
 }
 
 __device__ inline bool plain_answer(const SampleArgs& A, const Row& R, const Settings& q, int64_t r) {
@@ -581,7 +604,7 @@ __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
   const Settings q = row_of(A, r, block_max<TH>(best_of(R, 0, R.V, threadIdx.x, TH), sh.red), R);
   if (plain_answer(A, R, q, r)) return;
   if (q.mode == kOpen) {
-    finish_cut<TH>(A, R, Cut{0, 0}, r, sh);
+    choose<TH>(A, R, Cut{-INFINITY, 0}, r, 0, R.V, 0, 0, -1.0, sh);
     return;
   }
   for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
@@ -592,21 +615,28 @@ __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
   const u64 whole = cut_bin<TH>(q, sh, sh.bin);
   collect(R, sh, 0, R.V, threadIdx.x, TH);
   const int na = sh.na, nb = sh.nb;
-  // from the list's two ends to its front
-  finish<TH>(A, R, q, r, sh, whole, na, nb, kList / 2, [&](int to, int a, int b) {
-    u64 v[kList / 2 / TH];
+  const bool list = na <= kList / 2 && nb <= kList / 2 && (q.mode == kCount || na + nb <= kFewKept);
+  if (!list && (q.mode == kCount || nb > kList / 2)) {
+    finish_reach<TH>(A, R, q, r, sh);
+    return;
+  }
+  // the bin's elements from the list's end to its front, behind those above it
+  const int to = list ? na : 0;
+  u64 v[kList / 2 / TH];
 #pragma unroll
-    for (int e = 0; e < kList / 2 / TH; ++e) {
-      const int i = e * TH + threadIdx.x;
-      if (i < b) v[e] = sh.list[kList - 1 - i];
-    }
-    __syncthreads();
+  for (int e = 0; e < kList / 2 / TH; ++e) {
+    const int i = e * TH + threadIdx.x;
+    if (i < nb) v[e] = sh.list[kList - 1 - i];
+  }
+  __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kList / 2 / TH; ++e) {
-      const int i = e * TH + threadIdx.x;
-      if (i < b) sh.list[to + a + i] = v[e];
-    }
-  });
+  for (int e = 0; e < kList / 2 / TH; ++e) {
+    const int i = e * TH + threadIdx.x;
+    if (i < nb) sh.list[to + i] = v[e];
+  }
+  __syncthreads();
+  if (list) finish_list<TH>(A, R, q, r, sh, na + nb, whole);
+  else choose<TH>(A, R, cut_of_bin<TH>(R, q, sh, whole, nb), r, 0, R.V, 0, 0, -1.0, sh);
 }
 
 // Long rows: parts of a row in workgroups of their own.
@@ -614,10 +644,10 @@ __device__ inline void part_of(const SampleArgs& A, int64_t& i0, int64_t& i1) {
   i0 = (int64_t)blockIdx.x * A.part;
   i1 = min(i0 + A.part, A.V);
 }
+// every wave looks at all parts
 __device__ inline u64 best_part(const SampleRow& w, int parts) {
-  u64 v = 0;
-  for (int k = 0; k < parts; ++k) v = max(v, (u64)w.best[k]);
-  return v;
+  const int lane = threadIdx.x & 63;
+  return wave_max_u64(lane < parts ? (u64)w.best[lane] : 0);
 }
 
 __global__ void __launch_bounds__(256) sample_best_kernel(SampleArgs A) {
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   part_of(A, i0, i1);
   if (q.mode == kOpen) {
     u64 mass = 0;
-    each(R, i0, i1, threadIdx.x, TH, [&](int64_t, uint32_t key) { mass += R.weight_min_p(key); });
+    each(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) { mass += R.weight_min_p(l); });
     mass = block_sum<TH>(mass, red);
     if (threadIdx.x == 0) w.mass[blockIdx.x] = mass;
     return;
@@ -686,6 +716,17 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
   collect(R, sh, i0, i1, threadIdx.x, TH);
   // a place in the row's list for all of them; too many here are too many there
   const int na = sh.na, nb = sh.nb;
+  if (q.mode == kMass) {  // what the part keeps for sure
+    u64 mass = 0;
+    if (na <= kList / 2)
+      for (int i = threadIdx.x; i < na; i += TH) mass += R.weight_min_p(list_logit(sh.list[i]));
+    else
+      each(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) {
+        if (R.bin(l) < sh.at) mass += R.weight_min_p(l);
+      });
+    mass = block_sum<TH>(mass, sh.red);
+    if (threadIdx.x == 0) w.mass[blockIdx.x] = mass;
+  }
   __shared__ int base[2];
   if (threadIdx.x == 0) {
     base[0] = na ? atomicAdd(&w.na, na > kList / 2 ? kSampleList + 1 : na) : 0;
@@ -708,25 +749,49 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
   Row R;
   const Settings q = row_of(A, r, best_part(w, parts), R);
   if (plain_answer(A, R, q, r)) return;
+  const int lane = threadIdx.x & 63;
+  Cut cut{-INFINITY, 0};
+  u64 mine = 0, ties = 0, wt = 0;  // every wave: a lane a part
   if (q.mode == kOpen) {
-    u64 total = 0, before = 0;
-    for (int k = 0; k < parts; ++k) total += w.mass[k];
-    const double goal = aim(A, r, total);
-    int k = 0;
-    for (; k < parts - 1 && !((double)(before + w.mass[k]) > goal); ++k) before += w.mass[k];
-    const int64_t i0 = k * A.part, i1 = min(i0 + A.part, A.V), len = segments<TH>(R, Cut{0, 0}, i0, i1, sh);
-    if (threadIdx.x < 64) choose(A, R, Cut{0, 0}, r, i0, i1, len, before, total, goal, sh);
-    return;
+    mine = lane < parts ? w.mass[lane] : 0;
+  } else {
+    const int na = w.na, nb = w.nb;
+    const bool list = na <= kSampleList && nb <= kSampleList && (q.mode == kCount ? na + nb <= kList : na + nb <= kFewKept);
+    if (!list && (q.mode == kCount || nb > kList)) {
+      finish_reach<TH>(A, R, q, r, sh);
+      return;
+    }
+    const int to = list ? na : 0;
+    for (int i = threadIdx.x; i < to; i += TH) sh.list[i] = w.list[i];
+    for (int i = threadIdx.x; i < nb; i += TH) sh.list[to + i] = w.list[2 * kSampleList - 1 - i];
+    if (threadIdx.x == 0) sh.above = w.above;
+    if (threadIdx.x < kSegs) {
+      sh.seg[threadIdx.x] = 0;
+      sh.tie[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    if (list) {
+      finish_list<TH>(A, R, q, r, sh, na + nb, w.whole);
+      return;
+    }
+    cut = cut_of_bin<TH>(R, q, sh, w.whole, nb);
+    // what the parts keep of the bin: all above the cut, and the ties by index
+    for (int i = threadIdx.x; i <= sh.at; i += TH) {
+      const float l = list_logit(sh.list[i]);
+      const int part = (int)(~(uint32_t)sh.list[i] / (uint32_t)A.part);
+      if (l > cut.l) atomicAdd(&sh.seg[part], R.weight_min_p(l));
+      else atomicAdd(&sh.tie[part], 1u);
+    }
+    __syncthreads();
+    wt = R.weight_min_p(cut.l);
+    mine = lane < parts ? w.mass[lane] + sh.seg[lane] : 0;
+    ties = sh.tie[lane];
   }
-  if (threadIdx.x == 0) {
-    sh.at = w.at;
-    sh.above = w.above;
-  }
-  __syncthreads();
-  finish<TH>(A, R, q, r, sh, w.whole, w.na, w.nb, kSampleList, [&](int to, int a, int b) {
-    for (int i = threadIdx.x; i < a; i += TH) sh.list[to + i] = w.list[i];
-    for (int i = threadIdx.x; i < b; i += TH) sh.list[to + a + i] = w.list[2 * kSampleList - 1 - i];
-  });
+  const u64 total = wave_sum_u64(mine) + cut.ties * wt;
+  const double goal = aim(A, r, total);
+  u64 before = 0, left = cut.ties;
+  const int part = pass_at(mine, ties, wt, goal, before, left);
+  choose<TH>(A, R, Cut{cut.l, left}, r, part * A.part, min((part + 1) * A.part, A.V), before, total, goal, sh);
 }
 
 constexpr int64_t kFused = 8192;     // longest row that one workgroup takes
