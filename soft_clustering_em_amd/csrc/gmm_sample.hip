@@ -88,31 +88,43 @@ struct Row {
   __device__ int bin(float l) const { return (int)fminf((mx - l) * bins, (float)(kBins - 1)); }
 };
 
-// f(index, logit) for the live elements of [i0, i1), i0 a multiple of the piece, by `threads` threads
-template <typename T, typename F>
+// U pieces of 16 bytes, `step` elements apart from i on, without a branch: those
+// that do not lie whole in [0, i1) are read from its last whole piece (i1 >= E).
+template <typename T, int U>
+__device__ inline void load_pieces(T (&v)[U][16 / sizeof(T)], const T* p, int64_t i, int64_t step, int64_t i1) {
+  constexpr int E = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int u = 0; u < U; ++u) __builtin_memcpy(v[u], p + min(i + u * step, i1 - E), 16);
+}
+
+// f(index, logit) for the live elements of [i0, i1), i0 a multiple of the
+// piece, by `threads` threads, U pieces in flight each
+template <typename T, int U, typename F>
 __device__ inline void pieces(const Row& R, int64_t i0, int64_t i1, int thread, int threads, F f) {
   constexpr int E = 16 / (int)sizeof(T);
   const T* p = static_cast<const T*>(R.l) + R.at;
-  for (int64_t i = i0 + (int64_t)thread * E; i < i1; i += (int64_t)threads * E) {
-    T v[E];
-    if (i + E <= i1) {
-      __builtin_memcpy(v, p + i, 16);
-    } else {
+  const auto one = [&](int64_t i, T v) {
+    const float l = fminf((float)v, FLT_MAX);
+    if ((float)v > -INFINITY) f(i, l);
+  };
+  const int64_t step = (int64_t)threads * E, whole = i0 + (i1 - i0) / E * E;
+  for (int64_t i = i0 + (int64_t)thread * E; i < whole; i += U * step) {
+    T v[U][E];
+    load_pieces<T, U>(v, p, i, step, whole);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = i + e < i1 ? p[i + e] : (T)-INFINITY;
-    }
+    for (int u = 0; u < U; ++u) {
+      if (u && i + u * step >= whole) break;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float l = fminf((float)v[e], FLT_MAX);
-      if ((float)v[e] > -INFINITY) f(i + e, l);
+      for (int e = 0; e < E; ++e) one(i + u * step + e, v[u][e]);
     }
   }
+  if (i1 - whole > thread && thread < E) one(whole + thread, p[whole + thread]);
 }
-template <typename F>
+template <int U, typename F>
 __device__ inline void each(const Row& R, int64_t i0, int64_t i1, int thread, int threads, F f) {
-  if (R.dtype == 0) pieces<float>(R, i0, i1, thread, threads, f);
-  else if (R.dtype == 1) pieces<__bf16>(R, i0, i1, thread, threads, f);
-  else pieces<_Float16>(R, i0, i1, thread, threads, f);
+  if (R.dtype == 0) pieces<float, U>(R, i0, i1, thread, threads, f);
+  else if (R.dtype == 1) pieces<__bf16, U>(R, i0, i1, thread, threads, f);
+  else pieces<_Float16, U>(R, i0, i1, thread, threads, f);
 }
 
 __device__ inline u64 wave_sum_u64(u64 v) {
@@ -180,7 +192,7 @@ struct Settings {
 };
 
 struct Cutting {
-  u64 red[16], above;
+  u64 red[16], above, edge;
   u64 list[kList];
   int at, na, nb;
 };
@@ -216,32 +228,39 @@ __device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row&
 // the piece that its maximum came with, and looks into it at the end.
 template <typename T>
 __device__ inline u64 best_pieces(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
-  constexpr int E = 16 / (int)sizeof(T);
+  constexpr int E = 16 / (int)sizeof(T), U = 8;
   const T* p = static_cast<const T*>(R.l) + R.at;
+  const int64_t step = (int64_t)threads * E, whole = i0 + (i1 - i0) / E * E;
   float top = -INFINITY;
   int64_t at = -1;
-#pragma unroll 4
-  for (int64_t i = i0 + (int64_t)thread * E; i < i1; i += (int64_t)threads * E) {
-    T v[E];
-    if (i + E <= i1) {
-      __builtin_memcpy(v, p + i, 16);
-    } else {
+  for (int64_t i = i0 + (int64_t)thread * E; i < whole; i += U * step) {
+    T v[U][E];
+    load_pieces<T, U>(v, p, i, step, whole);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = i + e < i1 ? p[i + e] : (T)-INFINITY;
+    for (int u = 0; u < U; ++u) {
+      if (u && i + u * step >= whole) break;
+      float m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) m = fmaxf(m, (float)v[u][e]);  // NaN is passed over
+      m = fminf(m, FLT_MAX);
+      at = m > top ? i + u * step : at;
+      top = fmaxf(m, top);
     }
-    float m = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) m = fmaxf(m, (float)v[e]);  // NaN is passed over
-    m = fminf(m, FLT_MAX);
-    at = m > top ? i : at;
-    top = fmaxf(m, top);
   }
-  if (at < 0) return 0;
   uint32_t index = 0;
+  if (at >= 0) {
 #pragma unroll
-  for (int e = E - 1; e >= 0; --e)
-    if (at + e < i1 && fminf((float)p[at + e], FLT_MAX) == top) index = (uint32_t)(at + e);
-  return (u64)key_of(top) << 32 | (uint32_t)~index;
+    for (int e = E - 1; e >= 0; --e)
+      if (fminf((float)p[at + e], FLT_MAX) == top) index = (uint32_t)(at + e);
+  }
+  if (i1 - whole > thread && thread < E) {
+    const float l = (float)p[whole + thread];
+    if (l > -INFINITY && fminf(l, FLT_MAX) > top) {
+      top = fminf(l, FLT_MAX);
+      index = (uint32_t)(whole + thread);
+    }
+  }
+  return top > -INFINITY ? (u64)key_of(top) << 32 | (uint32_t)~index : 0;
 }
 __device__ inline u64 best_of(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
   if (R.dtype == 0) return best_pieces<float>(R, i0, i1, thread, threads);
@@ -251,9 +270,9 @@ __device__ inline u64 best_of(const Row& R, int64_t i0, int64_t i1, int thread, 
 
 __device__ inline void fill_bins(const Row& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin) {
   if (mode == kCount)
-    each(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
+    each<4>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
   else
-    each(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], R.weight(l)); });
+    each<2>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], R.weight(l)); });
 }
 
 // sh.at: the bin at which the count or the mass reaches its target (the last one
@@ -294,7 +313,7 @@ __device__ inline u64 cut_bin(const Settings& q, Cutting& sh, const u64* bin) {
 // ~index from the two ends of sh.list; counters that pass its half say so.
 __device__ inline void collect(const Row& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
   const int at = sh.at;
-  each(R, i0, i1, thread, threads, [&](int64_t i, float l) {
+  each<4>(R, i0, i1, thread, threads, [&](int64_t i, float l) {
     const int b = R.bin(l);
     if (b > at) return;
     const u64 v = (u64)key_of(l) << 32 | (uint32_t)~(uint32_t)i;
@@ -347,10 +366,65 @@ __device__ inline double aim(const SampleArgs& A, int64_t r, u64 total) {
   return (double)fminf(fmaxf(A.u[r], 0.f), 0x1.fffffep-1f) * (double)total;
 }
 
+template <int TH>
+__device__ inline u64 group_sum(u64 v, u64* red) {
+  if constexpr (TH == 64) return wave_sum_u64(v);
+  else return block_sum<TH>(v, red);
+}
+template <int TH>
+__device__ inline void group_sync() {
+  if constexpr (TH == 64) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
+
+// finish_list for n <= kFewKept: places and sums by comparing each element with
+// every other one, a thread an element (one wave, without barriers, where n <= 64).
+template <int TH>
+__device__ void finish_few(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
+  const int i = threadIdx.x;
+  const u64 mine = i < n ? sh.list[i] : 0;
+  const double e = i < n ? R.share(list_logit(mine)) : 0.0;
+  const u64 w = i < n ? R.fixed(e) : 0;
+  if (i < n) sh.sum[i] = w;
+  group_sync<TH>();
+  int place = 0;
+  u64 before = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const bool ahead = sh.list[j] > mine;
+    place += ahead;
+    before += ahead ? sh.sum[j] : 0;
+  }
+  const bool first = q.mode != kCount || place < q.k;
+  if (q.mode == kCount && q.top_p < 1.0) mass = group_sum<TH>(first ? w : 0, sh.red);
+  const bool in = i < n && (place == 0 || (first && (!(q.top_p < 1.0) || (double)before < q.top_p * (double)mass) && e >= R.least));
+  const u64 total = group_sum<TH>(in ? w : 0, sh.red);
+  const double goal = aim(A, r, total);
+  group_sync<TH>();
+  if (i < n) sh.sum[i] = in ? w : 0;
+  group_sync<TH>();
+  u64 to = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) to += (uint32_t)sh.list[j] >= (uint32_t)mine ? sh.sum[j] : 0;  // ~index: descending
+  if (in && (double)to > goal && !((double)(to - w) > goal)) answer(A, R, r, list_logit(mine), ~(uint32_t)mine, total);
+}
+
 // The row ends with a list of its n largest elements, among which the cut lies.
 // mass: of the row (top-p without top-k).
 template <int TH>
 __device__ void finish_list(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
+  if (n <= 64) {
+    if (threadIdx.x < 64) finish_few<64>(A, R, q, r, sh, n, mass);
+    return;
+  }
+  if (n <= kFewKept) {
+    finish_few<TH>(A, R, q, r, sh, n, mass);
+    return;
+  }
   sort_list<TH>(sh, n);
   if (q.mode == kCount) n = (int)min((int64_t)n, q.k);
   scan_list<TH>(sh, n, [&](int i) { return R.weight(list_logit(sh.list[i])); });
@@ -413,6 +487,58 @@ __device__ inline int pass_at(u64 n, u64 ties, u64 wt, double goal, u64& before,
   return lane;
 }
 
+// Kept weights and elements equal to the cut of the segments of `len` elements;
+// a wave reads four of them at once.
+template <typename T, int TH>
+__device__ inline void segments(const Row& R, const Cut& cut, int64_t i0, int64_t i1, int64_t len, Shared& sh) {
+  constexpr int E = 16 / (int)sizeof(T), U = 4;
+  const T* p = static_cast<const T*>(R.l) + R.at;
+  const int lane = threadIdx.x & 63;
+  const int64_t whole = i0 + (i1 - i0) / E * E;
+  for (int s = (threadIdx.x >> 6) * U; s < kSegs; s += TH / 64 * U) {
+    u64 mass[U] = {}, ties[U] = {};
+    const auto one = [&](int u, float v) {
+      const float l = fminf(v, FLT_MAX);
+      if (!(v > -INFINITY)) return;
+      if (l > cut.l) mass[u] += R.weight_min_p(l);
+      ties[u] += l == cut.l;
+    };
+    for (int64_t t = 0; t < len && i0 + s * len + t < whole; t += 64 * E) {
+      const int64_t i = i0 + s * len + t + lane * E;
+      T v[U][E];
+      load_pieces<T, U>(v, p, i, len, whole);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i + u * len >= whole) break;
+#pragma unroll
+        for (int e = 0; e < E; ++e) one(u, (float)v[u][e]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // the last elements, less than a piece, belong to the segment that they lie in
+      const int64_t a = i0 + (s + u) * len;
+      if (whole + lane < i1 && lane < E && whole >= a && whole < a + len) one(u, (float)p[whole + lane]);
+      mass[u] = wave_sum_u64(mass[u]);
+      ties[u] = wave_sum_u64(ties[u]);
+      if (lane == 0) {
+        sh.seg[s + u] = mass[u];
+        sh.tie[s + u] = (uint32_t)ties[u];
+      }
+    }
+  }
+}
+
+// f(index, logit) for the live ones of E elements from i on, below b, in order
+template <typename F>
+__device__ inline void own_piece(const Row& R, int64_t i, int64_t b, int E, F f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = e < E && i + e < b ? x_value(R.l, R.dtype, R.at + i + e) : -INFINITY;
+    if (v > -INFINITY) f(i + e, fminf(v, FLT_MAX));
+  }
+}
+
 // The row's (or a part's) segments of whole tiles: their kept weights and their
 // elements equal to the cut; then, in one wave, the segment, the tile and the
 // element at which the sum passes the goal.  goal < 0: that of the whole.
@@ -422,22 +548,9 @@ __device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_
   const int E = R.dtype == 0 ? 4 : 8, lane = threadIdx.x & 63;
   const int64_t tile = 64 * E, tiles = (i1 - i0 + tile - 1) / tile, len = (tiles + kSegs - 1) / kSegs * tile;
   __syncthreads();
-  for (int s = threadIdx.x >> 6; s < kSegs; s += TH / 64) {
-    const int64_t a = i0 + s * len, b = min(a + len, i1);
-    u64 mass = 0, ties = 0;
-    if (a < i1) {
-      each(R, a, b, lane, 64, [&](int64_t, float l) {
-        if (l > cut.l) mass += R.weight_min_p(l);
-        ties += l == cut.l;
-      });
-      mass = wave_sum_u64(mass);
-      ties = wave_sum_u64(ties);
-    }
-    if (lane == 0) {
-      sh.seg[s] = mass;
-      sh.tie[s] = (uint32_t)ties;
-    }
-  }
+  if (R.dtype == 0) segments<float, TH>(R, cut, i0, i1, len, sh);
+  else if (R.dtype == 1) segments<__bf16, TH>(R, cut, i0, i1, len, sh);
+  else segments<_Float16, TH>(R, cut, i0, i1, len, sh);
   __syncthreads();
   if (threadIdx.x >= 64) return;
   static_assert(kSegs == 128, "two segments a lane");
@@ -462,7 +575,7 @@ __device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_
   for (int64_t a = i0 + s * len, end = min(a + len, i1); a < end; a += tile) {
     const int64_t b = min(a + tile, end);
     u64 mass = 0, tied = 0;
-    each(R, a, b, lane, 64, [&](int64_t, float l) {
+    own_piece(R, a + (int64_t)lane * E, b, E, [&](int64_t, float l) {
       if (l > cut.l) mass += R.weight_min_p(l);
       tied += l == cut.l;
     });
@@ -474,7 +587,7 @@ __device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_
       if (lane == __builtin_ctzll(hit)) {
         u64 sum = to - mass, rank = tied_from;
         bool found = false;
-        each(R, a + (int64_t)lane * E, min(a + (int64_t)(lane + 1) * E, b), 0, 64, [&](int64_t i, float l) {
+        own_piece(R, a + (int64_t)lane * E, b, E, [&](int64_t i, float l) {
           if (found) return;
           if (l > cut.l) sum += R.weight_min_p(l);
           else if (l == cut.l && rank++ < left) sum += wt;
@@ -507,7 +620,7 @@ __device__ Cut reach(const Row& R, Shared& sh, Cut kept, double target) {
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
     __syncthreads();
-    each(R, 0, R.V, threadIdx.x, TH, [&](int64_t, float l) {
+    each<1>(R, 0, R.V, threadIdx.x, TH, [&](int64_t, float l) {
       const uint32_t key = key_of(l);
       if (key >= lo && key <= hi && key != cut) atomicAdd(&sh.bin[(hi - key) >> shift], MASS ? R.weight(l) : (u64)1);
     });
@@ -558,7 +671,7 @@ __device__ void finish_reach(const SampleArgs& A, const Row& R, const Settings& 
   if (q.mode == kCount) cut = reach<TH, false>(R, sh, cut, (double)q.k);
   if (q.top_p < 1.0) {
     u64 mass = 0;
-    each(R, 0, R.V, threadIdx.x, TH, [&](int64_t, float l) {
+    each<1>(R, 0, R.V, threadIdx.x, TH, [&](int64_t, float l) {
       if (l > cut.l) mass += R.weight(l);
     });
     mass = block_sum<TH>(mass, sh.red) + (cut.ties ? cut.ties * R.weight(cut.l) : 0);
@@ -568,21 +681,42 @@ __device__ void finish_reach(const SampleArgs& A, const Row& R, const Settings& 
 }
 
 // The cut of a row whose mass is `whole`, among the nb elements of its bin in
-// sh.list (sh.above: the mass before them); sh.at: its place in the sorted list.
+// sh.list (sh.above: the mass before them); sh.edge: its last element.
 template <int TH>
 __device__ Cut cut_of_bin(const Row& R, const Settings& q, Shared& sh, u64 whole, int nb) {
   const u64 above = sh.above;
+  const double target = q.top_p * (double)whole;
+  if (nb <= kFewKept) {
+    const int i = threadIdx.x;
+    const u64 mine = i < nb ? sh.list[i] : 0, w = i < nb ? R.weight(list_logit(mine)) : 0;
+    if (i < nb) sh.sum[i] = w;
+    __syncthreads();
+    u64 before = above, same = 0, place = 0;
+#pragma unroll 4
+    for (int j = 0; j < nb; ++j) {
+      const u64 other = sh.list[j];
+      if (other > mine) {
+        before += sh.sum[j];
+        ++place;
+        same += other >> 32 == mine >> 32;
+      }
+    }
+    if (i < nb && (double)(before + w) >= target && (place == 0 || (double)before < target)) {
+      sh.edge = mine;
+      sh.above = same + 1;
+    }
+    __syncthreads();
+    return Cut{list_logit(sh.edge), sh.above};
+  }
   sort_list<TH>(sh, nb);
   scan_list<TH>(sh, nb, [&](int i) { return R.weight(list_logit(sh.list[i])); });
-  const double target = q.top_p * (double)whole;
   for (int i = threadIdx.x; i < nb; i += TH)
-    if ((double)(above + sh.sum[i]) >= target && (i == 0 || (double)(above + sh.sum[i - 1]) < target)) sh.at = i;
+    if ((double)(above + sh.sum[i]) >= target && (i == 0 || (double)(above + sh.sum[i - 1]) < target)) sh.edge = sh.list[i];
   __syncthreads();
-  const int at = sh.at;
-  const float l = list_logit(sh.list[at]);
+  const u64 edge = sh.edge;
   u64 same = 0;
-  for (int i = threadIdx.x; i <= at; i += TH) same += list_logit(sh.list[i]) == l;
-  return Cut{l, block_sum<TH>(same, sh.red)};
+  for (int i = threadIdx.x; i < nb; i += TH) same += sh.list[i] >= edge && sh.list[i] >> 32 == edge >> 32;
+  return Cut{list_logit(edge), block_sum<TH>(same, sh.red)};
 }
 
 __device__ inline bool plain_answer(const SampleArgs& A, const Row& R, const Settings& q, int64_t r) {
@@ -680,7 +814,7 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   part_of(A, i0, i1);
   if (q.mode == kOpen) {
     u64 mass = 0;
-    each(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) { mass += R.weight_min_p(l); });
+    each<2>(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) { mass += R.weight_min_p(l); });
     mass = block_sum<TH>(mass, red);
     if (threadIdx.x == 0) w.mass[blockIdx.x] = mass;
     return;
@@ -721,7 +855,7 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
     if (na <= kList / 2)
       for (int i = threadIdx.x; i < na; i += TH) mass += R.weight_min_p(list_logit(sh.list[i]));
     else
-      each(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) {
+      each<1>(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) {
         if (R.bin(l) < sh.at) mass += R.weight_min_p(l);
       });
     mass = block_sum<TH>(mass, sh.red);
@@ -776,7 +910,8 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
     }
     cut = cut_of_bin<TH>(R, q, sh, w.whole, nb);
     // what the parts keep of the bin: all above the cut, and the ties by index
-    for (int i = threadIdx.x; i <= sh.at; i += TH) {
+    for (int i = threadIdx.x; i < nb; i += TH) {
+      if (sh.list[i] < sh.edge) continue;
       const float l = list_logit(sh.list[i]);
       const int part = (int)(~(uint32_t)sh.list[i] / (uint32_t)A.part);
       if (l > cut.l) atomicAdd(&sh.seg[part], R.weight_min_p(l));
