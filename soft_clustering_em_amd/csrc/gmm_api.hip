@@ -1949,8 +1949,7 @@ gmm_status gmm_sample(const gmm_data* logits, const gmm_sampling* how, const flo
   int bits = 0;
   while (((int64_t)1 << bits) < a.V) ++bits;
   a.scale = std::ldexp(1.0, std::min(52, 62 - bits));
-  a.dtype = logits->dtype;
-  const hipError_t e = launch_sample(a, ws, (hipStream_t)stream);
+  const hipError_t e = launch_sample(a, logits->dtype, ws, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "sampling launch");
   return GMM_OK;
 }

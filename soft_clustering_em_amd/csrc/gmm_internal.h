@@ -455,12 +455,11 @@ struct SampleArgs {
   float* logp;
   int64_t R, N, V, ld, stride_b, top_k;
   double temperature, top_p, min_p, scale;
-  int dtype;
   int64_t r0, part;        // first row of a launch, elements of a part
   SampleRow* rows;
 };
 size_t sample_bytes(int64_t R, int64_t V);
-hipError_t launch_sample(SampleArgs a, void* ws, hipStream_t s);
+hipError_t launch_sample(const SampleArgs& a, int dtype, void* ws, hipStream_t s);
 
 // fused E-step + statistics (gmm_estep.hip)
 hipError_t launch_estep(const Plan& p, const EStepArgs& a, hipStream_t s);

@@ -64,10 +64,10 @@ __device__ inline double exp_neg(double z) {
   return ldexp(p, (int)n);
 }
 
+template <typename T>
 struct Row {
-  const void* l;
-  int64_t V, at;   // elements, first element
-  int dtype;
+  const T* p;
+  int64_t V;
   float mx;
   uint32_t first;  // the lowest index of the maximum
   double inv, S;   // 1 / temperature, 2^S
@@ -99,10 +99,9 @@ __device__ inline void load_pieces(T (&v)[U][16 / sizeof(T)], const T* p, int64_
 
 // f(index, logit) for the live elements of [i0, i1), i0 a multiple of the
 // piece, by `threads` threads, U pieces in flight each
-template <typename T, int U, typename F>
-__device__ inline void pieces(const Row& R, int64_t i0, int64_t i1, int thread, int threads, F f) {
+template <int U, typename T, typename F>
+__device__ inline void each(const Row<T>& R, int64_t i0, int64_t i1, int thread, int threads, F f) {
   constexpr int E = 16 / (int)sizeof(T);
-  const T* p = static_cast<const T*>(R.l) + R.at;
   const auto one = [&](int64_t i, T v) {
     const float l = fminf((float)v, FLT_MAX);
     if ((float)v > -INFINITY) f(i, l);
@@ -110,7 +109,7 @@ __device__ inline void pieces(const Row& R, int64_t i0, int64_t i1, int thread, 
   const int64_t step = (int64_t)threads * E, whole = i0 + (i1 - i0) / E * E;
   for (int64_t i = i0 + (int64_t)thread * E; i < whole; i += U * step) {
     T v[U][E];
-    load_pieces<T, U>(v, p, i, step, whole);
+    load_pieces<T, U>(v, R.p, i, step, whole);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u && i + u * step >= whole) break;
@@ -118,15 +117,8 @@ __device__ inline void pieces(const Row& R, int64_t i0, int64_t i1, int thread, 
       for (int e = 0; e < E; ++e) one(i + u * step + e, v[u][e]);
     }
   }
-  if (i1 - whole > thread && thread < E) one(whole + thread, p[whole + thread]);
+  if (i1 - whole > thread && thread < E) one(whole + thread, R.p[whole + thread]);
 }
-template <int U, typename F>
-__device__ inline void each(const Row& R, int64_t i0, int64_t i1, int thread, int threads, F f) {
-  if (R.dtype == 0) pieces<float, U>(R, i0, i1, thread, threads, f);
-  else if (R.dtype == 1) pieces<__bf16, U>(R, i0, i1, thread, threads, f);
-  else pieces<_Float16, U>(R, i0, i1, thread, threads, f);
-}
-
 __device__ inline u64 wave_sum_u64(u64 v) {
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
   return v;
@@ -203,22 +195,21 @@ struct Shared : Cutting {
 
 // The row's elements, and what `best` (its largest key, and ~ its lowest index)
 // and the settings make of it.
-__device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row& R) {
-  R.l = A.l;
+template <typename T>
+__device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row<T>& R) {
   R.V = A.V;
-  R.dtype = A.dtype;
   const int64_t b = A.stride_b ? r / A.N : 0;
-  R.at = b * A.stride_b + (r - b * A.N) * A.ld;
+  R.p = static_cast<const T*>(A.l) + b * A.stride_b + (r - b * A.N) * A.ld;
   R.S = A.scale;
   R.mx = best ? logit_of((uint32_t)(best >> 32)) : 0.f;
   R.first = ~(uint32_t)best;
-  const double T = A.row_temperature ? (double)A.row_temperature[r] : A.temperature;
+  const double t = A.row_temperature ? (double)A.row_temperature[r] : A.temperature;
   const double min_p = A.row_min_p ? (double)A.row_min_p[r] : A.min_p;
   Settings q;
   q.k = A.row_top_k ? A.row_top_k[r] : A.top_k;
   q.top_p = A.row_top_p ? (double)A.row_top_p[r] : A.top_p;
-  q.mode = !best ? kNone : !(T > 0.0) || q.k == 1 ? kGreedy : q.k > 0 && q.k < A.V ? kCount : q.top_p < 1.0 ? kMass : kOpen;
-  R.inv = T > 0.0 ? fmin(1.0 / T, 1e300) : 1.0;
+  q.mode = !best ? kNone : !(t > 0.0) || q.k == 1 ? kGreedy : q.k > 0 && q.k < A.V ? kCount : q.top_p < 1.0 ? kMass : kOpen;
+  R.inv = t > 0.0 ? fmin(1.0 / t, 1e300) : 1.0;
   R.least = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
   R.bins = (float)fmin((double)kBinsPerUnit * R.inv, (double)FLT_MAX);
   return q;
@@ -227,9 +218,9 @@ __device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row&
 // a share of the row: its largest key with ~ its lowest index.  A thread notes
 // the piece that its maximum came with, and looks into it at the end.
 template <typename T>
-__device__ inline u64 best_pieces(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
+__device__ inline u64 best_of(const Row<T>& R, int64_t i0, int64_t i1, int thread, int threads) {
   constexpr int E = 16 / (int)sizeof(T), U = 8;
-  const T* p = static_cast<const T*>(R.l) + R.at;
+  const T* p = R.p;
   const int64_t step = (int64_t)threads * E, whole = i0 + (i1 - i0) / E * E;
   float top = -INFINITY;
   int64_t at = -1;
@@ -262,13 +253,8 @@ __device__ inline u64 best_pieces(const Row& R, int64_t i0, int64_t i1, int thre
   }
   return top > -INFINITY ? (u64)key_of(top) << 32 | (uint32_t)~index : 0;
 }
-__device__ inline u64 best_of(const Row& R, int64_t i0, int64_t i1, int thread, int threads) {
-  if (R.dtype == 0) return best_pieces<float>(R, i0, i1, thread, threads);
-  if (R.dtype == 1) return best_pieces<__bf16>(R, i0, i1, thread, threads);
-  return best_pieces<_Float16>(R, i0, i1, thread, threads);
-}
-
-__device__ inline void fill_bins(const Row& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin) {
+template <typename T>
+__device__ inline void fill_bins(const Row<T>& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin) {
   if (mode == kCount)
     each<4>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
   else
@@ -311,7 +297,8 @@ __device__ inline u64 cut_bin(const Settings& q, Cutting& sh, const u64* bin) {
 
 // Elements of the bins before sh.at, and of the bin itself, as key << 32 |
 // ~index from the two ends of sh.list; counters that pass its half say so.
-__device__ inline void collect(const Row& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
+template <typename T>
+__device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
   const int at = sh.at;
   each<4>(R, i0, i1, thread, threads, [&](int64_t i, float l) {
     const int b = R.bin(l);
@@ -358,7 +345,8 @@ __device__ inline void scan_list(Shared& sh, int n, F f) {
 }
 
 __device__ inline float list_logit(u64 v) { return logit_of((uint32_t)(v >> 32)); }
-__device__ inline void answer(const SampleArgs& A, const Row& R, int64_t r, float l, int64_t i, u64 total) {
+template <typename T>
+__device__ inline void answer(const SampleArgs& A, const Row<T>& R, int64_t r, float l, int64_t i, u64 total) {
   A.tokens[r] = (int32_t)i;
   if (A.logp) A.logp[r] = (float)(R.z(l) - log((double)total / R.S));
 }
@@ -383,8 +371,8 @@ __device__ inline void group_sync() {
 
 // finish_list for n <= kFewKept: places and sums by comparing each element with
 // every other one, a thread an element (one wave, without barriers, where n <= 64).
-template <int TH>
-__device__ void finish_few(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
+template <int TH, typename T>
+__device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
   const int i = threadIdx.x;
   const u64 mine = i < n ? sh.list[i] : 0;
   const double e = i < n ? R.share(list_logit(mine)) : 0.0;
@@ -415,8 +403,8 @@ __device__ void finish_few(const SampleArgs& A, const Row& R, const Settings& q,
 
 // The row ends with a list of its n largest elements, among which the cut lies.
 // mass: of the row (top-p without top-k).
-template <int TH>
-__device__ void finish_list(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
+template <int TH, typename T>
+__device__ __forceinline__ void finish_list(const SampleArgs& A, const Row<T>& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
   if (n <= 64) {
     if (threadIdx.x < 64) finish_few<64>(A, R, q, r, sh, n, mass);
     return;
@@ -463,7 +451,7 @@ __device__ void finish_list(const SampleArgs& A, const Row& R, const Settings& q
     const u64 mine_w = i < kept ? w[e] : 0, to = base + block_scan<TH>(mine_w, sh.red);
     if (i < kept && (double)to > goal && !((double)(to - mine_w) > goal)) {
       const uint32_t index = ~(uint32_t)(sh.list[i] >> 32);
-      answer(A, R, r, fminf(x_value(R.l, R.dtype, R.at + index), FLT_MAX), index, total);
+      answer(A, R, r, fminf((float)R.p[index], FLT_MAX), index, total);
     }
     __syncthreads();
     if (threadIdx.x == TH - 1) sh.above = to;
@@ -488,11 +476,11 @@ __device__ inline int pass_at(u64 n, u64 ties, u64 wt, double goal, u64& before,
 }
 
 // Kept weights and elements equal to the cut of the segments of `len` elements;
-// a wave reads four of them at once.
-template <typename T, int TH>
-__device__ inline void segments(const Row& R, const Cut& cut, int64_t i0, int64_t i1, int64_t len, Shared& sh) {
-  constexpr int E = 16 / (int)sizeof(T), U = 4;
-  const T* p = static_cast<const T*>(R.l) + R.at;
+// a wave reads two of them at once.
+template <int TH, typename T>
+__device__ inline void segments(const Row<T>& R, const Cut& cut, int64_t i0, int64_t i1, int64_t len, Shared& sh) {
+  constexpr int E = 16 / (int)sizeof(T), U = 2;
+  const T* p = R.p;
   const int lane = threadIdx.x & 63;
   const int64_t whole = i0 + (i1 - i0) / E * E;
   for (int s = (threadIdx.x >> 6) * U; s < kSegs; s += TH / 64 * U) {
@@ -529,12 +517,12 @@ __device__ inline void segments(const Row& R, const Cut& cut, int64_t i0, int64_
   }
 }
 
-// f(index, logit) for the live ones of E elements from i on, below b, in order
-template <typename F>
-__device__ inline void own_piece(const Row& R, int64_t i, int64_t b, int E, F f) {
+// f(index, logit) for the live ones of the piece from i on, below b, in order
+template <typename T, typename F>
+__device__ inline void own_piece(const Row<T>& R, int64_t i, int64_t b, F f) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float v = e < E && i + e < b ? x_value(R.l, R.dtype, R.at + i + e) : -INFINITY;
+  for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
+    const float v = i + e < b ? (float)R.p[i + e] : -INFINITY;
     if (v > -INFINITY) f(i + e, fminf(v, FLT_MAX));
   }
 }
@@ -542,15 +530,14 @@ __device__ inline void own_piece(const Row& R, int64_t i, int64_t b, int E, F f)
 // The row's (or a part's) segments of whole tiles: their kept weights and their
 // elements equal to the cut; then, in one wave, the segment, the tile and the
 // element at which the sum passes the goal.  goal < 0: that of the whole.
-template <int TH>
-__device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_t r, int64_t i0, int64_t i1, u64 before, u64 total,
+template <int TH, typename T>
+__device__ __forceinline__ void choose(const SampleArgs& A, const Row<T>& R, const Cut& cut, int64_t r, int64_t i0, int64_t i1, u64 before, u64 total,
                        double goal, Shared& sh) {
-  const int E = R.dtype == 0 ? 4 : 8, lane = threadIdx.x & 63;
+  constexpr int E = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 63;
   const int64_t tile = 64 * E, tiles = (i1 - i0 + tile - 1) / tile, len = (tiles + kSegs - 1) / kSegs * tile;
   __syncthreads();
-  if (R.dtype == 0) segments<float, TH>(R, cut, i0, i1, len, sh);
-  else if (R.dtype == 1) segments<__bf16, TH>(R, cut, i0, i1, len, sh);
-  else segments<_Float16, TH>(R, cut, i0, i1, len, sh);
+  segments<TH>(R, cut, i0, i1, len, sh);
   __syncthreads();
   if (threadIdx.x >= 64) return;
   static_assert(kSegs == 128, "two segments a lane");
@@ -575,7 +562,7 @@ __device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_
   for (int64_t a = i0 + s * len, end = min(a + len, i1); a < end; a += tile) {
     const int64_t b = min(a + tile, end);
     u64 mass = 0, tied = 0;
-    own_piece(R, a + (int64_t)lane * E, b, E, [&](int64_t, float l) {
+    own_piece(R, a + (int64_t)lane * E, b, [&](int64_t, float l) {
       if (l > cut.l) mass += R.weight_min_p(l);
       tied += l == cut.l;
     });
@@ -587,7 +574,7 @@ __device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_
       if (lane == __builtin_ctzll(hit)) {
         u64 sum = to - mass, rank = tied_from;
         bool found = false;
-        own_piece(R, a + (int64_t)lane * E, b, E, [&](int64_t i, float l) {
+        own_piece(R, a + (int64_t)lane * E, b, [&](int64_t i, float l) {
           if (found) return;
           if (l > cut.l) sum += R.weight_min_p(l);
           else if (l == cut.l && rank++ < left) sum += wt;
@@ -608,8 +595,8 @@ __device__ void choose(const SampleArgs& A, const Row& R, const Cut& cut, int64_
 // mass: the sum of the weights) first reaches `target`: bins of the keys'
 // range, then of the bin that it is reached in, until one key is left.  For
 // rows whose cut lies among more equal or nearly equal logits than a list holds.
-template <int TH, bool MASS>
-__device__ Cut reach(const Row& R, Shared& sh, Cut kept, double target) {
+template <int TH, bool MASS, typename T>
+__device__ __forceinline__ Cut reach(const Row<T>& R, Shared& sh, Cut kept, double target) {
   const uint32_t cut = kept.ties ? key_of(kept.l) : 0;
   uint32_t lo = cut ? cut : 1, hi = key_of(R.mx);
   u64 above = 0;
@@ -665,8 +652,8 @@ __device__ Cut reach(const Row& R, Shared& sh, Cut kept, double target) {
   }
 }
 
-template <int TH>
-__device__ void finish_reach(const SampleArgs& A, const Row& R, const Settings& q, int64_t r, Shared& sh) {
+template <int TH, typename T>
+__device__ __forceinline__ Cut cut_by_reach(const Row<T>& R, const Settings& q, Shared& sh) {
   Cut cut{-INFINITY, 0};
   if (q.mode == kCount) cut = reach<TH, false>(R, sh, cut, (double)q.k);
   if (q.top_p < 1.0) {
@@ -677,13 +664,13 @@ __device__ void finish_reach(const SampleArgs& A, const Row& R, const Settings& 
     mass = block_sum<TH>(mass, sh.red) + (cut.ties ? cut.ties * R.weight(cut.l) : 0);
     cut = reach<TH, true>(R, sh, cut, q.top_p * (double)mass);
   }
-  choose<TH>(A, R, cut, r, 0, R.V, 0, 0, -1.0, sh);
+  return cut;
 }
 
 // The cut of a row whose mass is `whole`, among the nb elements of its bin in
 // sh.list (sh.above: the mass before them); sh.edge: its last element.
-template <int TH>
-__device__ Cut cut_of_bin(const Row& R, const Settings& q, Shared& sh, u64 whole, int nb) {
+template <int TH, typename T>
+__device__ __forceinline__ Cut cut_of_bin(const Row<T>& R, const Settings& q, Shared& sh, u64 whole, int nb) {
   const u64 above = sh.above;
   const double target = q.top_p * (double)whole;
   if (nb <= kFewKept) {
@@ -719,7 +706,8 @@ __device__ Cut cut_of_bin(const Row& R, const Settings& q, Shared& sh, u64 whole
   return Cut{list_logit(edge), block_sum<TH>(same, sh.red)};
 }
 
-__device__ inline bool plain_answer(const SampleArgs& A, const Row& R, const Settings& q, int64_t r) {
+template <typename T>
+__device__ inline bool plain_answer(const SampleArgs& A, const Row<T>& R, const Settings& q, int64_t r) {
   if (q.mode != kNone && q.mode != kGreedy) return false;
   if (threadIdx.x == 0) {
     A.tokens[r] = q.mode == kNone ? -1 : (int32_t)R.first;
@@ -729,48 +717,52 @@ __device__ inline bool plain_answer(const SampleArgs& A, const Row& R, const Set
 }
 
 // A short row by one workgroup.
+template <typename T>
 __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
   constexpr int TH = 256;
   __shared__ Shared sh;
   const int64_t r = (int64_t)blockIdx.x + A.r0;
-  Row R;
+  Row<T> R;
   row_of(A, r, 0, R);
   const Settings q = row_of(A, r, block_max<TH>(best_of(R, 0, R.V, threadIdx.x, TH), sh.red), R);
   if (plain_answer(A, R, q, r)) return;
-  if (q.mode == kOpen) {
-    choose<TH>(A, R, Cut{-INFINITY, 0}, r, 0, R.V, 0, 0, -1.0, sh);
-    return;
-  }
-  for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
-  if (threadIdx.x == 0) sh.na = sh.nb = 0;
-  __syncthreads();
-  fill_bins(R, q.mode, 0, R.V, threadIdx.x, TH, sh.bin);
-  __syncthreads();
-  const u64 whole = cut_bin<TH>(q, sh, sh.bin);
-  collect(R, sh, 0, R.V, threadIdx.x, TH);
-  const int na = sh.na, nb = sh.nb;
-  const bool list = na <= kList / 2 && nb <= kList / 2 && (q.mode == kCount || na + nb <= kFewKept);
-  if (!list && (q.mode == kCount || nb > kList / 2)) {
-    finish_reach<TH>(A, R, q, r, sh);
-    return;
-  }
-  // the bin's elements from the list's end to its front, behind those above it
-  const int to = list ? na : 0;
-  u64 v[kList / 2 / TH];
+  Cut cut{-INFINITY, 0};
+  if (q.mode != kOpen) {
+    for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
+    if (threadIdx.x == 0) sh.na = sh.nb = 0;
+    __syncthreads();
+    fill_bins(R, q.mode, 0, R.V, threadIdx.x, TH, sh.bin);
+    __syncthreads();
+    const u64 whole = cut_bin<TH>(q, sh, sh.bin);
+    collect(R, sh, 0, R.V, threadIdx.x, TH);
+    const int na = sh.na, nb = sh.nb;
+    const bool list = na <= kList / 2 && nb <= kList / 2 && (q.mode == kCount || na + nb <= kFewKept);
+    if (!list && (q.mode == kCount || nb > kList / 2)) {
+      cut = cut_by_reach<TH>(R, q, sh);
+    } else {
+      // the bin's elements from the list's end to its front, behind those above it
+      const int to = list ? na : 0;
+      u64 v[kList / 2 / TH];
 #pragma unroll
-  for (int e = 0; e < kList / 2 / TH; ++e) {
-    const int i = e * TH + threadIdx.x;
-    if (i < nb) v[e] = sh.list[kList - 1 - i];
-  }
-  __syncthreads();
+      for (int e = 0; e < kList / 2 / TH; ++e) {
+        const int i = e * TH + threadIdx.x;
+        if (i < nb) v[e] = sh.list[kList - 1 - i];
+      }
+      __syncthreads();
 #pragma unroll
-  for (int e = 0; e < kList / 2 / TH; ++e) {
-    const int i = e * TH + threadIdx.x;
-    if (i < nb) sh.list[to + i] = v[e];
+      for (int e = 0; e < kList / 2 / TH; ++e) {
+        const int i = e * TH + threadIdx.x;
+        if (i < nb) sh.list[to + i] = v[e];
+      }
+      __syncthreads();
+      if (list) {
+        finish_list<TH>(A, R, q, r, sh, na + nb, whole);
+        return;
+      }
+      cut = cut_of_bin<TH>(R, q, sh, whole, nb);
+    }
   }
-  __syncthreads();
-  if (list) finish_list<TH>(A, R, q, r, sh, na + nb, whole);
-  else choose<TH>(A, R, cut_of_bin<TH>(R, q, sh, whole, nb), r, 0, R.V, 0, 0, -1.0, sh);
+  choose<TH>(A, R, cut, r, 0, R.V, 0, 0, -1.0, sh);
 }
 
 // Long rows: parts of a row in workgroups of their own.
@@ -784,12 +776,13 @@ __device__ inline u64 best_part(const SampleRow& w, int parts) {
   return wave_max_u64(lane < parts ? (u64)w.best[lane] : 0);
 }
 
+template <typename T>
 __global__ void __launch_bounds__(256) sample_best_kernel(SampleArgs A) {
   constexpr int TH = 256;
   __shared__ u64 red[TH / 64];
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
-  Row R;
+  Row<T> R;
   row_of(A, r, 0, R);
   int64_t i0, i1;
   part_of(A, i0, i1);
@@ -801,13 +794,14 @@ __global__ void __launch_bounds__(256) sample_best_kernel(SampleArgs A) {
   for (int i = blockIdx.x * TH + threadIdx.x; i < kBins; i += gridDim.x * TH) w.bin[i] = 0;
 }
 
+template <typename T>
 __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   constexpr int TH = 256;
   __shared__ u64 bin[kBins];
   __shared__ u64 red[TH / 64];
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
-  Row R;
+  Row<T> R;
   const Settings q = row_of(A, r, best_part(w, gridDim.x), R);
   if (q.mode == kNone || q.mode == kGreedy) return;
   int64_t i0, i1;
@@ -827,12 +821,13 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
     if (bin[i]) atomicAdd((u64*)&w.bin[i], bin[i]);
 }
 
+template <typename T>
 __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
   constexpr int TH = 256;
   __shared__ Cutting sh;
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
-  Row R;
+  Row<T> R;
   const Settings q = row_of(A, r, best_part(w, gridDim.x), R);
   if (q.mode != kCount && q.mode != kMass) return;
   const u64 whole = cut_bin<TH>(q, sh, (const u64*)w.bin);
@@ -875,58 +870,64 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
       if (base[1] + i < kSampleList) w.list[2 * kSampleList - 1 - base[1] - i] = sh.list[kList - 1 - i];
 }
 
+template <typename T>
 __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int parts) {
   constexpr int TH = 1024;
   __shared__ Shared sh;
   const int64_t r = (int64_t)blockIdx.x + A.r0;
   SampleRow& w = A.rows[blockIdx.x];
-  Row R;
+  Row<T> R;
   const Settings q = row_of(A, r, best_part(w, parts), R);
   if (plain_answer(A, R, q, r)) return;
   const int lane = threadIdx.x & 63;
   Cut cut{-INFINITY, 0};
   u64 mine = 0, ties = 0, wt = 0;  // every wave: a lane a part
-  if (q.mode == kOpen) {
-    mine = lane < parts ? w.mass[lane] : 0;
+  int64_t i0 = 0, i1 = A.V;
+  u64 before = 0, total = 0;
+  double goal = -1.0;
+  const int na = w.na, nb = w.nb;
+  const bool list = na <= kSampleList && nb <= kSampleList && na + nb <= (q.mode == kCount ? kList : kFewKept);
+  if (q.mode != kOpen && !list && (q.mode == kCount || nb > kList)) {
+    cut = cut_by_reach<TH>(R, q, sh);
   } else {
-    const int na = w.na, nb = w.nb;
-    const bool list = na <= kSampleList && nb <= kSampleList && (q.mode == kCount ? na + nb <= kList : na + nb <= kFewKept);
-    if (!list && (q.mode == kCount || nb > kList)) {
-      finish_reach<TH>(A, R, q, r, sh);
-      return;
+    mine = lane < parts ? w.mass[lane] : 0;
+    if (q.mode != kOpen) {
+      const int to = list ? na : 0;
+      for (int i = threadIdx.x; i < to; i += TH) sh.list[i] = w.list[i];
+      for (int i = threadIdx.x; i < nb; i += TH) sh.list[to + i] = w.list[2 * kSampleList - 1 - i];
+      if (threadIdx.x == 0) sh.above = w.above;
+      if (threadIdx.x < kSegs) {
+        sh.seg[threadIdx.x] = 0;
+        sh.tie[threadIdx.x] = 0;
+      }
+      __syncthreads();
+      if (list) {
+        finish_list<TH>(A, R, q, r, sh, na + nb, w.whole);
+        return;
+      }
+      cut = cut_of_bin<TH>(R, q, sh, w.whole, nb);
+      // what the parts keep of the bin: all above the cut, and the ties by index
+      for (int i = threadIdx.x; i < nb; i += TH) {
+        if (sh.list[i] < sh.edge) continue;
+        const float l = list_logit(sh.list[i]);
+        const int part = (int)(~(uint32_t)sh.list[i] / (uint32_t)A.part);
+        if (l > cut.l) atomicAdd(&sh.seg[part], R.weight_min_p(l));
+        else atomicAdd(&sh.tie[part], 1u);
+      }
+      __syncthreads();
+      wt = R.weight_min_p(cut.l);
+      if (lane < parts) mine += sh.seg[lane];
+      ties = sh.tie[lane];
     }
-    const int to = list ? na : 0;
-    for (int i = threadIdx.x; i < to; i += TH) sh.list[i] = w.list[i];
-    for (int i = threadIdx.x; i < nb; i += TH) sh.list[to + i] = w.list[2 * kSampleList - 1 - i];
-    if (threadIdx.x == 0) sh.above = w.above;
-    if (threadIdx.x < kSegs) {
-      sh.seg[threadIdx.x] = 0;
-      sh.tie[threadIdx.x] = 0;
-    }
-    __syncthreads();
-    if (list) {
-      finish_list<TH>(A, R, q, r, sh, na + nb, w.whole);
-      return;
-    }
-    cut = cut_of_bin<TH>(R, q, sh, w.whole, nb);
-    // what the parts keep of the bin: all above the cut, and the ties by index
-    for (int i = threadIdx.x; i < nb; i += TH) {
-      if (sh.list[i] < sh.edge) continue;
-      const float l = list_logit(sh.list[i]);
-      const int part = (int)(~(uint32_t)sh.list[i] / (uint32_t)A.part);
-      if (l > cut.l) atomicAdd(&sh.seg[part], R.weight_min_p(l));
-      else atomicAdd(&sh.tie[part], 1u);
-    }
-    __syncthreads();
-    wt = R.weight_min_p(cut.l);
-    mine = lane < parts ? w.mass[lane] + sh.seg[lane] : 0;
-    ties = sh.tie[lane];
+    total = wave_sum_u64(mine) + cut.ties * wt;
+    goal = aim(A, r, total);
+    u64 left = cut.ties;
+    const int part = pass_at(mine, ties, wt, goal, before, left);
+    cut.ties = left;
+    i0 = part * A.part;
+    i1 = min(i0 + A.part, A.V);
   }
-  const u64 total = wave_sum_u64(mine) + cut.ties * wt;
-  const double goal = aim(A, r, total);
-  u64 before = 0, left = cut.ties;
-  const int part = pass_at(mine, ties, wt, goal, before, left);
-  choose<TH>(A, R, Cut{cut.l, left}, r, part * A.part, min((part + 1) * A.part, A.V), before, total, goal, sh);
+  choose<TH>(A, R, cut, r, i0, i1, before, total, goal, sh);
 }
 
 constexpr int64_t kFused = 8192;     // longest row that one workgroup takes
@@ -938,11 +939,12 @@ constexpr int64_t kPartLeast = 4096; // a workgroup's least share of a long row
 static int64_t sample_rows(int64_t R, int64_t V) { return V <= kFused ? 0 : std::min<int64_t>(R, 1024); }
 size_t sample_bytes(int64_t R, int64_t V) { return sizeof(SampleRow) * (size_t)sample_rows(R, V); }
 
-hipError_t launch_sample(SampleArgs A, void* ws, hipStream_t s) {
+template <typename T>
+static hipError_t run_sample(SampleArgs A, void* ws, hipStream_t s) {
   const int64_t step = sample_rows(A.R, A.V);
   if (step == 0) {
     for (A.r0 = 0; A.r0 < A.R; A.r0 += 1 << 22) {
-      hipLaunchKernelGGL(sample_row_kernel, dim3((unsigned)std::min<int64_t>(A.R - A.r0, 1 << 22)), dim3(256), 0, s, A);
+      hipLaunchKernelGGL(sample_row_kernel<T>, dim3((unsigned)std::min<int64_t>(A.R - A.r0, 1 << 22)), dim3(256), 0, s, A);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
@@ -956,14 +958,20 @@ hipError_t launch_sample(SampleArgs A, void* ws, hipStream_t s) {
     const int64_t most = std::min<int64_t>(want, kSampleParts);
     A.part = ((A.V + most - 1) / most + 7) / 8 * 8;
     const unsigned parts = (unsigned)((A.V + A.part - 1) / A.part);
-    hipLaunchKernelGGL(sample_best_kernel, dim3(parts, n), dim3(256), 0, s, A);
-    hipLaunchKernelGGL(sample_bins_kernel, dim3(parts, n), dim3(256), 0, s, A);
-    hipLaunchKernelGGL(sample_collect_kernel, dim3(parts, n), dim3(256), 0, s, A);
-    hipLaunchKernelGGL(sample_finish_kernel, dim3(n), dim3(1024), 0, s, A, (int)parts);
+    hipLaunchKernelGGL(sample_best_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
+    hipLaunchKernelGGL(sample_bins_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
+    hipLaunchKernelGGL(sample_collect_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
+    hipLaunchKernelGGL(sample_finish_kernel<T>, dim3(n), dim3(1024), 0, s, A, (int)parts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+hipError_t launch_sample(const SampleArgs& A, int dtype, void* ws, hipStream_t s) {
+  if (dtype == 0) return run_sample<float>(A, ws, s);
+  if (dtype == 1) return run_sample<__bf16>(A, ws, s);
+  return run_sample<_Float16>(A, ws, s);
 }
 
 }  // namespace gmm
