@@ -1756,7 +1756,6 @@ static gmm_status route_args(const gmm_data* logits, const gmm_routing* how, int
   a->N = logits->N;
   a->ld = logits->ld_x;
   a->stride_b = rows_stride(logits);
-  a->dtype = logits->dtype;
   a->E = (int)logits->D;
   a->m = m;
   a->groups = how->groups;
@@ -1785,7 +1784,7 @@ gmm_status gmm_route_topm(const gmm_data* logits, const float* bias, const gmm_r
   a.bias = bias;
   a.idx = idx;
   a.weights = weights;
-  const hipError_t e = launch_route(a, false, (hipStream_t)stream);
+  const hipError_t e = launch_route(a, logits->dtype, false, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "routing launch");
   return GMM_OK;
 }
@@ -1810,7 +1809,7 @@ gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, i
   a.dweights = dweights;
   a.dscores = dscores;
   a.dlogits = dlogits;
-  const hipError_t e = launch_route(a, true, (hipStream_t)stream);
+  const hipError_t e = launch_route(a, logits->dtype, true, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "routing gradient launch");
   return GMM_OK;
 }

@@ -407,11 +407,11 @@ struct RouteArgs {
   float* weights;
   void* dlogits;
   int64_t R, N, ld, stride_b;  // stride 0: rows ld apart throughout
-  int dtype, E, m, groups, keep, top;
+  int E, m, groups, keep, top;
   bool sigmoid, renorm;
   float scale;
 };
-hipError_t launch_route(const RouteArgs& a, bool grad, hipStream_t s);
+hipError_t launch_route(const RouteArgs& a, int dtype, bool grad, hipStream_t s);
 
 // AdamW (gmm_adamw.hip)
 constexpr int kAdamTensors = 32;      // tensors per launch (their descriptions are kernel arguments)

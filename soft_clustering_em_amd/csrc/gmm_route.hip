@@ -6,6 +6,12 @@
 //   w_j = scale s_j / sum_selected s
 // Orders are decided in float64; without a bias the order of the scores is that
 // of the logits, which are exact.
+// L lanes take a row (16 up to 256 experts: four rows a wave).  float32 scores,
+// off by at most kOff(t), leave the few candidates that may be among the m
+// largest: those not below the m-th largest of the lanes' maxima.  These alone
+// are scored in float64, a lane each, and placed by comparing each with every
+// other one.  Rows whose groups are too close to tell in float32, or with more
+// candidates than places, go through the float64 scores of every expert.
 #include "gmm_device.h"
 
 #include <hip/hip_runtime.h>
@@ -16,6 +22,36 @@ namespace gmm {
 
 namespace {
 
+// float32 scores and sums with a bias: exp's argument (at most |x| e^x 2^-23 <
+// 2^-24), 2^-21 for exp, sum and quotient, the sum's rounding 2^-24 |t|
+__device__ inline float kOff(float t) { return 0x1p-20f + 0x1p-23f * fabsf(t); }
+
+template <typename T>
+__device__ inline float logit(const RouteArgs& A, int64_t i) {
+  return (float)static_cast<const T*>(A.l)[i];
+}
+
+__device__ inline int64_t row_base(const RouteArgs& A, int64_t r) {
+  const int64_t b = A.stride_b ? (uint32_t)r / (uint32_t)A.N : 0;
+  return b * A.stride_b + (r - b * A.N) * A.ld;
+}
+
+template <int L>
+__device__ inline float lanes_max(float v) {
+  v = row16_max(v);
+  return L == 64 ? rows4_max(v) : v;
+}
+template <int L>
+__device__ inline float lanes_sum(float v) {
+  v = row16_sum(v);
+  return L == 64 ? rows4_sum(v) : v;
+}
+template <int L>
+__device__ inline double lanes_sum_f64(double v) {
+  v = row16_sum_f64(v);
+  return L == 64 ? rows4_sum_f64(v) : v;
+}
+
 // LDS written by some lanes of a wave, read by others of the same wave
 __device__ inline void wave_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -25,32 +61,30 @@ __device__ inline void wave_lds() {
 // s_e of the code `e` that this lane holds (e < 0: none), over the sum of the
 // row's codes (renorm), or over `total`: the largest logit among the codes
 // stands for the row's, so that their sum cannot vanish.
+template <typename T, int L>
 __device__ inline double selected(const RouteArgs& A, int64_t base, int e, float mx, double total) {
-  const float l = e >= 0 ? fminf(x_value(A.l, A.dtype, base + e), FLT_MAX) : -INFINITY;
+  const float l = e >= 0 ? fminf(logit<T>(A, base + e), FLT_MAX) : -INFINITY;
   double q = 0.0;
   if (A.sigmoid) {
     if (e >= 0) q = 1.0 / (1.0 + exp(-(double)l));
   } else {
-    const float top = A.renorm ? rows4_max(row16_max(l)) : mx;
+    const float top = A.renorm ? lanes_max<L>(l) : mx;
     if (e >= 0) q = exp((double)l - (double)top);
     if (!A.renorm && e >= 0) q /= total;
   }
   if (A.renorm) {
-    const double sum = wave_sum(q);
+    const double sum = lanes_sum_f64<L>(q);
     q = sum > 0.0 ? q / sum : 0.0;
   }
   return q;
 }
 
-// One wave a row: EPL experts a lane, e = lane + 64 k.
-template <int EPL>
-__global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
-  extern __shared__ double lds[];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t r = (int64_t)blockIdx.x * 4 + w;
-  if (r >= A.R) return;
-  const int64_t b = A.stride_b ? (uint32_t)r / (uint32_t)A.N : 0;
-  const int64_t base = b * A.stride_b + (r - b * A.N) * A.ld;
+// Row r by a whole wave, every score in float64: EPL experts a lane, e = lane +
+// 64 k.  row: E doubles of LDS.
+template <typename T, int EPL>
+__device__ void route_exact(const RouteArgs& A, int64_t r, double* row) {
+  const int lane = threadIdx.x & 63;
+  const int64_t base = row_base(A, r);
   float l[EPL];
   double t[EPL], s[EPL];
   float mx = -INFINITY;
@@ -59,7 +93,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
     const int e = lane + 64 * k;
     l[k] = -INFINITY;
     if (e < A.E) {
-      const float v = x_value(A.l, A.dtype, base + e);
+      const float v = logit<T>(A, base + e);
       if (v > -INFINITY) l[k] = fminf(v, FLT_MAX);
     }
     mx = fmaxf(mx, l[k]);
@@ -87,7 +121,6 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
     t[k] = l[k] > -INFINITY ? (by_score ? s[k] + (double)A.bias[e] : (double)l[k]) : -INFINITY;
   }
   if (A.groups > 1 && A.keep < A.groups) {
-    double* row = lds + (size_t)w * A.E;
     const int gs = A.E / A.groups;
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {
@@ -141,118 +174,319 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
     for (int k = 0; k < EPL; ++k)
       if (at == lane + 64 * k) t[k] = -INFINITY;
   }
-  const double q = selected(A, base, mine, mx, total);
+  const double q = selected<T, 64>(A, base, mine, mx, total);
   if (lane < A.m) {
     A.idx[r * A.m + lane] = mine;
     A.weights[r * A.m + lane] = (float)((double)A.scale * q);
   }
 }
 
-// One wave a row.  With u_j = scale dw_j and q_j = s_j / sum_selected s:
-//   softmax: dl_e = s_e (ds_e - sum_f ds_f s_f);  sigmoid: dl_e = s_e (1 - s_e) ds_e
-// where ds_e = dscores_e, and without renormalising + u_j of the code e; renormalised
-// the codes' part is q_j (u_j - sum u q), times 1 - s_j for the sigmoid.
-template <int EPL>
-__global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs A) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t r = (int64_t)blockIdx.x * 4 + w;
-  if (r >= A.R) return;
-  const int64_t b = A.stride_b ? (uint32_t)r / (uint32_t)A.N : 0;
-  const int64_t base = b * A.stride_b + (r - b * A.N) * A.ld;
-  float l[EPL], s[EPL], rest[EPL], ds[EPL], dl[EPL];
+constexpr int kPlaces = 64;  // candidates of a row at most
+
+// doubles of LDS a row: its scores and the groups' (float32; float64 in
+// route_exact, which has a wave's share), or its candidates and codes
+__host__ __device__ inline int route_room(int E, int groups, int lanes) {
+  const int scores = groups == 1 ? 0 : lanes == 64 ? E : (E + groups + 1) / 2, list = kPlaces * 2 + kRouteMaxM / 2;
+  return ((scores > list ? scores : list) + 1) / 2 * 2;
+}
+
+struct Candidate {
+  double t;
+  int e;
+  float l;
+};
+
+template <typename T, int L, int EPL>
+__global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
+  constexpr int RPW = 64 / L, EXACT = L * EPL > 64 ? L * EPL / 64 : 1;
+  extern __shared__ double lds[];  // a wave: RPW rows of `room` doubles
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sub = lane % L, row = lane / L;
+  const int room = route_room(A.E, A.groups, L);
+  double* mine_lds = lds + (size_t)(w * RPW + row) * room;
+  const int64_t r = ((int64_t)blockIdx.x * 4 + w) * RPW + row;
+  const bool in = r < A.R;
+  const int64_t base = in ? row_base(A, r) : 0;
+  const bool grouped = A.groups > 1 && A.keep < A.groups, by_score = A.bias != nullptr;
+  float l[EPL], t[EPL];
   float mx = -INFINITY;
 #pragma unroll
   for (int k = 0; k < EPL; ++k) {
-    const int e = lane + 64 * k;
+    const int e = sub + L * k;
+    l[k] = -INFINITY;
+    if (in && e < A.E) {
+      const float v = logit<T>(A, base + e);
+      if (v > -INFINITY) l[k] = fminf(v, FLT_MAX);
+    }
+  }
+  // scores in float32, where the order is not that of the logits; the softmax's
+  // sum in float64, where a score itself is asked for
+  double total = 1.0;
+  const bool need_s = by_score || (grouped && A.top == 2);
+  if (!A.sigmoid && (need_s || !A.renorm)) {
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) mx = fmaxf(mx, l[k]);
+    mx = lanes_max<L>(mx);
+    total = 0.0;
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) total += l[k] > -INFINITY ? exp((double)l[k] - (double)mx) : 0.0;
+    total = lanes_sum_f64<L>(total);
+  }
+  const float inv = total > 0.0 ? (float)(1.0 / total) : 0.f;
+  const auto score = [&](int k) {
+    if (A.sigmoid) return __builtin_amdgcn_rcpf(1.f + __expf(-l[k]));
+    return __expf(l[k] - mx) * inv;
+  };
+#pragma unroll
+  for (int k = 0; k < EPL; ++k) {
+    const int e = sub + L * k;
+    t[k] = l[k];
+    if (by_score && l[k] > -INFINITY) t[k] = score(k) + A.bias[e];
+  }
+  bool unsure = false;
+  if (grouped) {
+    // the groups' scores, a lane a group (L groups at a time), from LDS
+    float* row_t = reinterpret_cast<float*>(mine_lds);
+    float* group_t = row_t + A.E;
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) {
+      const int e = sub + L * k;
+      if (e < A.E) row_t[e] = !by_score && A.top == 2 && l[k] > -INFINITY ? score(k) : t[k];
+    }
+    wave_lds();
+    const int gs = A.E / A.groups;
+    for (int g = sub; g < A.groups; g += L) {
+      float best = -INFINITY, next = -INFINITY;
+      int i = sub % gs;  // lanes start at places of their own: other banks
+      for (int j = 0; j < gs; ++j) {
+        const float v = row_t[g * gs + i];
+        next = fmaxf(next, fminf(best, v));
+        best = fmaxf(best, v);
+        i = i + 1 < gs ? i + 1 : 0;
+      }
+      group_t[g] = A.top == 2 && next > -INFINITY ? best + next : best;
+    }
+    wave_lds();
+    uint64_t kept = 0;
+    float least = INFINITY, most = -INFINITY;  // of the groups kept and of the others
+    for (int g0 = 0; g0 < A.groups; g0 += L) {
+      const int g = g0 + sub;
+      int place = A.groups;
+      if (g < A.groups) {
+        const float v = group_t[g];
+        place = 0;
+        for (int j = 0; j < A.groups; ++j) place += group_t[j] > v || (group_t[j] == v && j < g);
+        if (place < A.keep) least = fminf(least, v);
+        else most = fmaxf(most, v);
+      }
+      const uint64_t b = __ballot(place < A.keep);
+      kept |= (L == 64 ? b : (b >> (row * L)) & 0xffff) << g0;
+    }
+    least = -lanes_max<L>(-least);
+    most = lanes_max<L>(most);
+    if (need_s) unsure = most > -INFINITY && !(least - most > 4.f * fmaxf(kOff(least), kOff(most)));
+    const uint32_t magic = ((1u << 21) + gs - 1) / gs;  // e / gs = e magic >> 21, for e < 1024 and gs <= 512
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) {
+      const uint32_t e = sub + L * k;
+      if (!((kept >> ((e * magic >> 21) & 63)) & 1)) t[k] = -INFINITY;
+    }
+  }
+  // at least m experts are not below the m-th largest of the lanes' maxima
+  float top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < EPL; ++k) top = fmaxf(top, t[k]);
+  float bound;
+  if constexpr (EPL == 1) {
+    bound = -INFINITY;  // every expert may be placed
+  } else {
+    int reach = 0;  // lanes whose maximum is not below this one
+#pragma unroll
+    for (int j = 0; j < L; ++j) reach += __shfl(top, j, L) >= top;
+    bound = lanes_max<L>(reach >= A.m ? top : -INFINITY);
+    if (by_score) bound -= 3.f * kOff(bound);
+  }
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < EPL; ++k) count += t[k] >= bound && t[k] > -INFINITY;
+  int before = count;
+#pragma unroll
+  for (int o = 1; o < L; o *= 2) {
+    const int x = __shfl_up(before, o, L);
+    if (sub >= o) before += x;
+  }
+  const int n = __shfl(before, L - 1, L);
+  before -= count;
+  unsure |= n > kPlaces;
+  Candidate* list = reinterpret_cast<Candidate*>(mine_lds);
+  wave_lds();
+  if (n <= kPlaces) {
+#pragma unroll
+    for (int k = 0; k < EPL; ++k)
+      if (t[k] >= bound && t[k] > -INFINITY) {
+        const int e = sub + L * k;
+        list[before++] = Candidate{(double)l[k], e, l[k]};
+      }
+  }
+  wave_lds();
+  const int rounds = (n <= kPlaces ? n + L - 1 : 0) / L;  // of L candidates
+  // float64 scores where a bias takes part
+  if (by_score) {
+    for (int s = 0; s < rounds; ++s) {
+      const int i = s * L + sub;
+      if (i < n) {
+        const double x = list[i].t;
+        list[i].t = (A.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx) / total) + (double)A.bias[list[i].e];
+      }
+    }
+    wave_lds();
+  }
+  int e_mine = -1;
+  for (int s = 0; s < rounds; ++s) {
+    const int i = s * L + sub;
+    int place = A.m;
+    if (i < n) {
+      const Candidate c = list[i];
+      place = 0;
+      for (int j = 0; j < n; ++j) {
+        const Candidate o = list[j];
+        place += o.t > c.t || (o.t == c.t && o.e < c.e);
+      }
+      // the winners' codes to the row's lanes, through what the list has spare
+      if (place < A.m) reinterpret_cast<int*>(list + kPlaces)[place] = c.e;
+    }
+  }
+  wave_lds();
+  if (!unsure && sub < A.m && sub < n) e_mine = reinterpret_cast<int*>(list + kPlaces)[sub];
+  const double q = selected<T, L>(A, base, e_mine, mx, total);
+  if (in && !unsure && sub < A.m) {
+    A.idx[r * A.m + sub] = e_mine;
+    A.weights[r * A.m + sub] = (float)((double)A.scale * q);
+  }
+  uint64_t again = __ballot(in && unsure && sub == 0);
+  while (again) {
+    const int at = __builtin_ctzll(again);
+    again &= again - 1;
+    wave_lds();
+    route_exact<T, EXACT>(A, r - row + at / L, lds + (size_t)w * RPW * room);
+  }
+}
+
+// L lanes a row.  With u_j = scale dw_j and q_j = s_j / sum_selected s:
+//   softmax: dl_e = s_e (ds_e - sum_f ds_f s_f);  sigmoid: dl_e = s_e (1 - s_e) ds_e
+// where ds_e = dscores_e, and without renormalising + u_j of the code e; renormalised
+// the codes' part is q_j (u_j - sum u q), times 1 - s_j for the sigmoid.
+template <typename T, int L, int EPL>
+__global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs A) {
+  constexpr int RPW = 64 / L;
+  const int lane = threadIdx.x & 63, sub = lane % L, row = lane / L;
+  const int64_t r = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * RPW + row;
+  const bool in = r < A.R;
+  const int64_t base = in ? row_base(A, r) : 0;
+  float l[EPL], s[EPL], rest[EPL], ds[EPL], dl[EPL];
+  float mx = -INFINITY;
+  int mine = in && A.dweights && sub < A.m ? A.idx[r * A.m + sub] : -1;
+  float u = mine >= 0 ? A.scale * A.dweights[r * A.m + sub] : 0.f;
+#pragma unroll
+  for (int k = 0; k < EPL; ++k) {
+    const int e = sub + L * k;
     l[k] = -INFINITY;
     ds[k] = dl[k] = 0.f;
-    if (e < A.E) {
-      const float v = x_value(A.l, A.dtype, base + e);
+    if (in && e < A.E) {
+      const float v = logit<T>(A, base + e);
       if (v > -INFINITY) l[k] = fminf(v, FLT_MAX);
       if (A.dscores) ds[k] = A.dscores[e];
     }
     mx = fmaxf(mx, l[k]);
   }
-  mx = rows4_max(row16_max(mx));
+  mx = lanes_max<L>(mx);
+  // a renormalised row without dscores needs no softmax of its own
+  const bool need_s = A.dscores || !A.renorm;
   float total = 0.f;
 #pragma unroll
   for (int k = 0; k < EPL; ++k) {
     const bool on = l[k] > -INFINITY;
+    s[k] = 0.f;
+    rest[k] = 1.f;
     if (A.sigmoid) {
-      const float z = expf(-fabsf(l[k])), hi = 1.f / (1.f + z), lo = z / (1.f + z);
+      const float z = expf(-fabsf(l[k])), hi = 1.f / (1.f + z), lo = z * hi;
       s[k] = on ? (l[k] >= 0.f ? hi : lo) : 0.f;
       rest[k] = l[k] >= 0.f ? lo : hi;
-    } else {
+    } else if (need_s) {
       s[k] = on ? expf(l[k] - mx) : 0.f;
-      rest[k] = 1.f;
       total += s[k];
     }
   }
-  if (!A.sigmoid) {
-    total = rows4_sum(row16_sum(total));
+  if (!A.sigmoid && need_s) {
+    total = lanes_sum<L>(total);
     const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
     for (int k = 0; k < EPL; ++k) s[k] *= inv;
   }
   if (A.dweights) {
-    int mine = lane < A.m ? A.idx[r * A.m + lane] : -1;
     // the row's leading codes in [0, E)
-    const uint64_t bad = __ballot(mine < 0 || mine >= A.E);
-    const int n = __builtin_ctzll(bad | ((uint64_t)1 << 63));
-    if (lane >= n) mine = -1;
-    float u = mine >= 0 ? A.scale * A.dweights[r * A.m + lane] : 0.f;
+    const uint64_t bad = __ballot(mine < 0 || mine >= A.E) >> (row * L);
+    const int n = __builtin_ctzll(bad | (uint64_t)1 << kRouteMaxM);
+    if (sub >= n) mine = -1;
+    if (mine < 0) u = 0.f;
     if (A.renorm) {
-      const float q = (float)selected(A, base, mine, mx, 1.0);
-      u = q * (u - rows4_sum(row16_sum(q * u)));
+      const float q = (float)selected<T, L>(A, base, mine, mx, 1.0);
+      u = q * (u - lanes_sum<L>(q * u));
     }
-    for (int j = 0; j < n; ++j) {
-      const int e = __shfl(mine, j);
-      const float v = __shfl(u, j);
+#pragma unroll 1
+    for (int j = 0; j < A.m; ++j) {
+      const int e = __shfl(mine, j, L) - sub;
+      const float v = __shfl(u, j, L);
 #pragma unroll
-      for (int k = 0; k < EPL; ++k)
-        if (e == lane + 64 * k) {
-          if (A.renorm) dl[k] += v * rest[k];
-          else ds[k] += v;
-        }
+      for (int k = 0; k < EPL; ++k) dl[k] += e == L * k ? v : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) {
+      if (!A.renorm) ds[k] += dl[k];
+      dl[k] = A.renorm ? dl[k] * rest[k] : 0.f;
     }
   }
   float c = 0.f;
-  if (!A.sigmoid) {
+  if (!A.sigmoid && need_s) {
 #pragma unroll
     for (int k = 0; k < EPL; ++k) c += s[k] > 0.f ? ds[k] * s[k] : 0.f;
-    c = rows4_sum(row16_sum(c));
+    c = lanes_sum<L>(c);
   }
+  if (!in) return;
 #pragma unroll
   for (int k = 0; k < EPL; ++k) {
-    const int e = lane + 64 * k;
+    const int e = sub + L * k;
     if (e >= A.E) break;
     const float d = l[k] > -INFINITY ? dl[k] + s[k] * rest[k] * (ds[k] - c) : 0.f;
-    const int64_t o = r * A.E + e;
-    if (A.dtype == 0) static_cast<float*>(A.dlogits)[o] = d;
-    else if (A.dtype == 1) static_cast<__bf16*>(A.dlogits)[o] = (__bf16)d;
-    else static_cast<_Float16*>(A.dlogits)[o] = (_Float16)d;
+    static_cast<T*>(A.dlogits)[r * A.E + e] = (T)d;
   }
 }
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& A, bool grad, hipStream_t s) {
-  const dim3 grid((unsigned)((A.R + 3) / 4)), block(256);
-  const size_t lds = A.groups > 1 ? sizeof(double) * 4 * (size_t)A.E : 0;
-  const int per = (A.E + 63) / 64;
-#define GMM_ROUTE(EPL)                                                                      \
-  if (per <= EPL) {                                                                         \
-    if (grad) hipLaunchKernelGGL(route_grad_kernel<EPL>, grid, block, 0, s, A);             \
-    else hipLaunchKernelGGL(route_kernel<EPL>, grid, block, lds, s, A);                     \
-    return hipGetLastError();                                                               \
-  }
-  GMM_ROUTE(1)
-  GMM_ROUTE(2)
-  GMM_ROUTE(4)
-  GMM_ROUTE(8)
-  GMM_ROUTE(16)
-#undef GMM_ROUTE
-  return hipErrorInvalidValue;
+template <typename T, int L, int EPL>
+static hipError_t run_route(const RouteArgs& A, bool grad, hipStream_t s) {
+  constexpr int rows = 4 * (64 / L);
+  const dim3 grid((unsigned)((A.R + rows - 1) / rows)), block(256);
+  if (grad) hipLaunchKernelGGL((route_grad_kernel<T, L, EPL>), grid, block, 0, s, A);
+  else hipLaunchKernelGGL((route_kernel<T, L, EPL>), grid, block, sizeof(double) * rows * route_room(A.E, A.groups, L), s, A);
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t run_routes(const RouteArgs& A, bool grad, hipStream_t s) {
+  if (A.E <= 16) return run_route<T, 16, 1>(A, grad, s);
+  if (A.E <= 32) return run_route<T, 16, 2>(A, grad, s);
+  if (A.E <= 64) return run_route<T, 16, 4>(A, grad, s);
+  if (A.E <= 128) return run_route<T, 16, 8>(A, grad, s);
+  if (A.E <= 256) return run_route<T, 16, 16>(A, grad, s);
+  if (A.E <= 512) return run_route<T, 64, 8>(A, grad, s);
+  return run_route<T, 64, 16>(A, grad, s);
+}
+
+hipError_t launch_route(const RouteArgs& A, int dtype, bool grad, hipStream_t s) {
+  if (dtype == 0) return run_routes<float>(A, grad, s);
+  if (dtype == 1) return run_routes<__bf16>(A, grad, s);
+  return run_routes<_Float16>(A, grad, s);
 }
 
 }  // namespace gmm
