@@ -20,16 +20,54 @@ namespace gmm {
 
 namespace {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 template <typename T>
 constexpr int kPer = 16 / (int)sizeof(T);  // elements of a 16-byte piece
 
+// Element e of a piece.  Pieces stay packed in registers, 4 for 8 values of 16
+// bits, and are opened where they are used.
 template <typename T>
-__device__ inline void load_piece(T (&v)[kPer<T>], const T* row, int64_t c0, int64_t D) {
+__device__ inline float element(u32x4 v, int e) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(v[e]);
+  } else {
+    const unsigned short h = (unsigned short)(v[e / 2] >> (16 * (e & 1)));
+    return (float)__builtin_bit_cast(T, h);
+  }
+}
+// The compiler keeps no opened copies of v beyond this point.
+__device__ inline void packed(u32x4& v) { asm volatile("" : "+v"(v)); }
+
+template <typename T>
+__device__ inline u32x4 load_piece(const T* row, int64_t c0, int64_t D) {
+  T v[kPer<T>];
   if (c0 + kPer<T> <= D) {
     __builtin_memcpy(v, row + c0, 16);
   } else {
 #pragma unroll
     for (int e = 0; e < kPer<T>; ++e) v[e] = c0 + e < D ? row[c0 + e] : (T)0.f;
+  }
+  return __builtin_bit_cast(u32x4, v);
+}
+
+// A thread's C pieces of a row (zeros past D, and everywhere if not `live`).
+// The loads come first and without a branch, so that they are in flight
+// together; pieces that do not lie whole in the row read its start instead.
+template <typename T, int TPR, int C>
+__device__ inline void load_row(u32x4 (&v)[C], const T* row, int t, int64_t D, bool live) {
+  constexpr int E = kPer<T>;
+  if (D >= E) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int64_t c0 = ((int64_t)j * TPR + t) * E;
+      __builtin_memcpy(&v[j], row + (c0 + E <= D ? c0 : 0), 16);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int64_t c0 = ((int64_t)j * TPR + t) * E;
+    if (!live || c0 + E > D) v[j] = load_piece<T>(row, c0, live ? D : 0);
   }
 }
 
@@ -52,10 +90,9 @@ __device__ inline void load_affine(float (&v)[kPer<T>], const void* p, bool is_t
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = none;
   } else if (is_t) {
-    T t[E];
-    load_piece<T>(t, static_cast<const T*>(p), c0, D);
+    const u32x4 t = load_piece<T>(static_cast<const T*>(p), c0, D);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (float)t[e];
+    for (int e = 0; e < E; ++e) v[e] = element<T>(t, e);
   } else {
     const float* f = static_cast<const float*>(p) + c0;
     if (c0 + E <= D) {
@@ -109,25 +146,28 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs A)
   if (TPR > 64 && !live) return;
   const T* x = static_cast<const T*>(A.x) + (live ? row_at(r, A.N, A.ld, A.stride_b) : 0);
   const float inv = 1.f / (float)A.D;
-  T v[C][E];
+  u32x4 v[C];
   float s = 0.f, s1 = 0.f, s2 = 0.f, none = 0.f;
   int turn = 0;
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    load_piece<T>(v[j], x, live ? ((int64_t)j * TPR + t) * E : A.D, A.D);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += (float)v[j][e];
-  }
-  row_sum2<TPR>(s, none, red, turn);
-  const float m1 = s * inv;
+  load_row<T, TPR, C>(v, x, t, A.D, live);
 #pragma unroll
   for (int j = 0; j < C; ++j)
 #pragma unroll
+    for (int e = 0; e < E; ++e) s += element<T>(v[j], e);
+  row_sum2<TPR>(s, none, red, turn);
+  const float m1 = s * inv;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    packed(v[j]);
+    const int64_t c0 = ((int64_t)j * TPR + t) * E;
+    if (c0 >= A.D) break;
+#pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float d = ((int64_t)j * TPR + t) * E + e < A.D ? (float)v[j][e] - m1 : 0.f;
+      const float d = c0 + e < A.D ? element<T>(v[j], e) - m1 : 0.f;
       s1 += d;
       s2 += d * d;
     }
+  }
   row_sum2<TPR>(s1, s2, red, turn);
   const float m2 = s1 * inv, mean = m1 + m2;
   const float var = fmaxf(0.f, (s2 - s1 * m2) * inv), rstd = 1.f / sqrtf(var + A.eps);
@@ -143,55 +183,84 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs A)
   for (int j = 0; j < C; ++j) {
     const int64_t c0 = ((int64_t)j * TPR + t) * E;
     if (c0 >= A.D) break;
+    packed(v[j]);
     float g[E], b[E];
     load_affine<T>(g, A.gamma, A.affine_t, c0, A.D, 1.f);
     load_affine<T>(b, A.beta, A.affine_t, c0, A.D, 0.f);
     T o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = (T)((((float)v[j][e] - m1) - m2) * rs * g[e] + b[e]);
+    for (int e = 0; e < E; ++e) o[e] = (T)(((element<T>(v[j], e) - m1) - m2) * rs * g[e] + b[e]);
     store_piece<T>(out, o, c0, A.D);
   }
 }
 
 // The gradients of rows, and (ACC) this workgroup's share of gamma's and
-// beta's: sums over the rows blockIdx.x * RPB + k gridDim.x * RPB.
+// beta's: sums over the rows blockIdx.x * RPB + k gridDim.x * RPB.  The next
+// row's loads are under way while a row is summed, where there are registers.
 template <typename T, int TPR, int C, bool ACC>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_grad_kernel(NormArgs A) {
   constexpr int E = kPer<T>, RPB = TPR > 256 ? 1 : 256 / TPR, W = (TPR > 256 ? TPR : 256) / 64;
+  constexpr bool AHEAD = TPR <= 256;
   __shared__ float2 red[2][16];
   const int t = threadIdx.x % TPR;
   const float inv = 1.f / (float)A.D;
-  float g[C][E], dg[ACC ? C : 1][E], db[ACC ? C : 1][E];
+  u32x4 g[C], nx[C], ny[C];
+  float dg[ACC ? C : 1][E], db[ACC ? C : 1][E], next_mean, next_rstd;
   int turn = 0;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    load_affine<T>(g[j], A.gamma, A.affine_t, ((int64_t)j * TPR + t) * E, A.D, 1.f);
+    // gamma in the rows' type where it is stored so; opened like them
+    if (A.affine_t && A.gamma) g[j] = load_piece<T>(static_cast<const T*>(A.gamma), ((int64_t)j * TPR + t) * E, A.D);
     if constexpr (ACC) {
 #pragma unroll
       for (int e = 0; e < E; ++e) dg[j][e] = db[j][e] = 0.f;
     }
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < A.R; r0 += (int64_t)gridDim.x * RPB) {
-    const int64_t r = r0 + threadIdx.x / TPR;
+  const bool stored = A.affine_t && A.gamma;
+  const auto gamma = [&](int j, float (&f)[E]) {
+    if (stored) {
+      packed(g[j]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = element<T>(g[j], e);
+    } else {
+      load_affine<T>(f, A.gamma, false, ((int64_t)j * TPR + t) * E, A.D, 1.f);
+    }
+  };
+  const auto fetch = [&](int64_t r) {
     const bool live = r < A.R;
-    const T* x = static_cast<const T*>(A.x) + (live ? row_at(r, A.N, A.ld, A.stride_b) : 0);
-    const T* dy = static_cast<const T*>(A.dy) + (live ? row_at(r, A.N, A.ld_dy, A.stride_dy) : 0);
-    const float mean = live ? A.mean[r] : 0.f, rstd = live ? A.rstd[r] : 0.f;
-    T vx[C][E], vy[C][E];
+    const int64_t at = live ? r : 0;
+    load_row<T, TPR, C>(nx, static_cast<const T*>(A.x) + row_at(at, A.N, A.ld, A.stride_b), t, A.D, live);
+    load_row<T, TPR, C>(ny, static_cast<const T*>(A.dy) + row_at(at, A.N, A.ld_dy, A.stride_dy), t, A.D, live);
+    next_mean = live ? A.mean[r] : 0.f;
+    next_rstd = live ? A.rstd[r] : 0.f;
+  };
+  int64_t r0 = (int64_t)blockIdx.x * RPB;
+  if (AHEAD && r0 < A.R) fetch(r0 + threadIdx.x / TPR);
+  while (r0 < A.R) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    if (!AHEAD) fetch(r);
+    const bool live = r < A.R;
+    const float mean = next_mean, rstd = next_rstd;
+    u32x4 vx[C], vy[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const int64_t c0 = live ? ((int64_t)j * TPR + t) * E : A.D;
-      load_piece<T>(vx[j], x, c0, A.D);
-      load_piece<T>(vy[j], dy, c0, A.D);
+      vx[j] = nx[j];
+      vy[j] = ny[j];
     }
+    r0 += (int64_t)gridDim.x * RPB;
+    if (AHEAD && r0 < A.R) fetch(r0 + threadIdx.x / TPR);
     float a = 0.f, b = 0.f;
 #pragma unroll
-    for (int j = 0; j < C; ++j)
+    for (int j = 0; j < C; ++j) {
+      const int64_t c0 = ((int64_t)j * TPR + t) * E;
+      if (c0 >= A.D) break;
+      float f[E];
+      gamma(j, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         // past D the row's gradient is 0, but xh is not: a column of no row
-        const float xh = ((float)vx[j][e] - mean) * rstd, y = (float)vy[j][e], q = y * g[j][e];
-        const bool in = ((int64_t)j * TPR + t) * E + e < A.D;
+        const float xh = (element<T>(vx[j], e) - mean) * rstd, y = element<T>(vy[j], e), q = y * f[e];
+        const bool in = c0 + e < A.D;
         a += q;
         b += in ? q * xh : 0.f;
         if constexpr (ACC) {
@@ -199,26 +268,32 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_grad_kernel(NormAr
           db[j][e] += y;
         }
       }
-    if (A.dx) {
-      row_sum2<TPR>(a, b, red, turn);
-      if (live) {
-        T* dx = static_cast<T*>(A.dx) + r * A.D;
-        const float ma = a * inv, mb = b * inv;
+      packed(vx[j]);
+      packed(vy[j]);
+    }
+    if (!A.dx) continue;
+    row_sum2<TPR>(a, b, red, turn);
+    if (!live) continue;
+    T* dx = static_cast<T*>(A.dx) + r * A.D;
+    const float ma = a * inv, mb = b * inv;
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          const int64_t c0 = ((int64_t)j * TPR + t) * E;
-          if (c0 >= A.D) break;
-          T o[E];
-          if (A.accumulate) load_piece<T>(o, dx, c0, A.D);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float xh = ((float)vx[j][e] - mean) * rstd;
-            const float d = rstd * ((float)vy[j][e] * g[j][e] - ma - xh * mb);
-            o[e] = (T)(A.accumulate ? (float)o[e] + d : d);
-          }
-          store_piece<T>(dx, o, c0, A.D);
-        }
+    for (int j = 0; j < C; ++j) {
+      const int64_t c0 = ((int64_t)j * TPR + t) * E;
+      if (c0 >= A.D) break;
+      float f[E];
+      gamma(j, f);
+      T o[E];
+      if (A.accumulate) {
+        const u32x4 old = load_piece<T>(dx, c0, A.D);
+        __builtin_memcpy(o, &old, 16);
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float xh = (element<T>(vx[j], e) - mean) * rstd;
+        const float d = rstd * (element<T>(vy[j], e) * f[e] - ma - xh * mb);
+        o[e] = (T)(A.accumulate ? (float)o[e] + d : d);
+      }
+      store_piece<T>(dx, o, c0, A.D);
     }
   }
   if constexpr (ACC) {
@@ -336,9 +411,10 @@ hipError_t run_grad(const NormArgs& A, unsigned grid, hipStream_t s) {
 
 }  // namespace
 
-// Threads a row and pieces a thread for rows of `pieces` 16-byte pieces.
-static void norm_shape(int64_t pieces, int* tpr, int* c) {
-  *tpr = pieces <= 16 ? 16 : pieces <= 256 ? 64 : pieces <= 1024 ? 256 : 1024;
+// Threads a row and pieces a thread for rows of `pieces` 16-byte pieces: whole
+// waves side by side as long as a thread holds at most `most` pieces.
+static void norm_shape(int64_t pieces, int most, int* tpr, int* c) {
+  *tpr = pieces <= 16 ? 16 : pieces <= 64 * most ? 64 : pieces <= 256 * most ? 256 : 1024;
   const int64_t per = (pieces + *tpr - 1) / *tpr;
   *c = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
 }
@@ -347,7 +423,7 @@ hipError_t launch_norm(const NormArgs& A, hipStream_t s) {
   return by_type(A.dtype, [&](auto zero) {
     using T = decltype(zero);
     int tpr, c;
-    norm_shape((A.D + kPer<T> - 1) / kPer<T>, &tpr, &c);
+    norm_shape((A.D + kPer<T> - 1) / kPer<T>, 4, &tpr, &c);
     switch (tpr * 16 + c) {
       case 16 * 16 + 1: return run_norm<T, 16, 1>(A, s);
       case 64 * 16 + 1: return run_norm<T, 64, 1>(A, s);
@@ -367,8 +443,8 @@ hipError_t launch_norm(const NormArgs& A, hipStream_t s) {
 NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums) {
   NormPlan p{};
   const int e = dtype == 0 ? 4 : 8;
-  norm_shape((D + e - 1) / e, &p.tpr, &p.c);
-  p.wide = D > 16384;  // more accumulators than registers
+  norm_shape((D + e - 1) / e, 2, &p.tpr, &p.c);  // more pieces, fewer waves: their sums beside the row take registers
+  p.wide = p.c > 2;  // more sums than registers
   const int64_t rpb = p.tpr >= 256 ? 1 : 256 / p.tpr, groups = (R + rpb - 1) / rpb;
   p.grid = want_sums && !p.wide ? std::min<int64_t>(groups, 1024) : std::min<int64_t>(groups, 1 << 16);
   p.parts = p.wide ? std::min<int64_t>(64, std::max<int64_t>(1, R)) : p.grid;
@@ -389,17 +465,16 @@ hipError_t launch_norm_grad(NormArgs A, const NormPlan& p, float* dgamma, float*
         GMM_NORM_GRAD(16, 1)
         GMM_NORM_GRAD(64, 1)
         GMM_NORM_GRAD(64, 2)
-        GMM_NORM_GRAD(64, 4)
+        GMM_NORM_GRAD(256, 1)
         GMM_NORM_GRAD(256, 2)
-        GMM_NORM_GRAD(256, 4)
+        GMM_NORM_GRAD(1024, 1)
         GMM_NORM_GRAD(1024, 2)
 #undef GMM_NORM_GRAD
         case (1024 * 16 + 4) * 2: return run_grad<T, 1024, 4, false>(A, g, s);
         default: break;
       }
-      if constexpr (sizeof(T) == 4)  // D <= 16384, and past it without sums
-        return acc ? run_grad<T, 1024, 4, true>(A, g, s) : run_grad<T, 1024, 8, false>(A, g, s);
-      return hipErrorInvalidValue;
+      if constexpr (sizeof(T) == 4) return run_grad<T, 1024, 8, false>(A, g, s);
+      return hipErrorInvalidValue;  // D <= 32768
     });
     if (e != hipSuccess) return e;
   }
