@@ -441,7 +441,7 @@ hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs a, hipStream_t 
 // sampling (gmm_sample.hip)
 constexpr int kSampleParts = 64, kSampleList = 2048;
 struct SampleRow {         // of a long row, in the workspace
-  unsigned long long best[kSampleParts], mass[kSampleParts];  // of every part
+  unsigned long long best[kSampleParts], mass[4 * kSampleParts];  // of every part, and of its quarters
   unsigned long long bin[2048];
   unsigned long long list[2 * kSampleList];
   unsigned long long whole, above;

@@ -186,15 +186,27 @@ constexpr int kPlaces = 64;  // candidates of a row at most
 // doubles of LDS a row: its scores and the groups' (float32; float64 in
 // route_exact, which has a wave's share), or its candidates and codes
 __host__ __device__ inline int route_room(int E, int groups, int lanes) {
-  const int scores = groups == 1 ? 0 : lanes == 64 ? E : (E + groups + 1) / 2, list = kPlaces * 2 + kRouteMaxM / 2;
+  const int f32 = (E + E / 32 + 1 + groups + 1) / 2, list = kPlaces * 2 + kRouteMaxM / 2;
+  const int scores = groups == 1 ? 0 : lanes == 64 && E > f32 ? E : f32;
   return ((scores > list ? scores : list) + 1) / 2 * 2;
 }
 
-struct Candidate {
-  double t;
-  int e;
-  float l;
-};
+// how many of the row's lanes hold a value not below v, this one included
+template <int L>
+__device__ inline int not_below(float v) {
+  int n = 0;
+  if constexpr (L == 16) {
+    n = 1;
+#define GMM_ROTATED(R) n += dpp_mov<0x120 + R>(v) >= v;
+    GMM_ROTATED(1) GMM_ROTATED(2) GMM_ROTATED(3) GMM_ROTATED(4) GMM_ROTATED(5) GMM_ROTATED(6) GMM_ROTATED(7) GMM_ROTATED(8)
+    GMM_ROTATED(9) GMM_ROTATED(10) GMM_ROTATED(11) GMM_ROTATED(12) GMM_ROTATED(13) GMM_ROTATED(14) GMM_ROTATED(15)
+#undef GMM_ROTATED
+  } else {
+#pragma unroll 8
+    for (int j = 0; j < L; ++j) n += __shfl(v, j, L) >= v;
+  }
+  return n;
+}
 
 template <typename T, int L, int EPL>
 __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
@@ -244,70 +256,82 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
   }
   bool unsure = false;
   if (grouped) {
-    // the groups' scores, a lane a group (L groups at a time), from LDS
+    // the groups' scores from LDS: P lanes a group, each over a run of it.  One
+    // place in 33 stays empty, so that runs 32 apart start in other banks.
     float* row_t = reinterpret_cast<float*>(mine_lds);
-    float* group_t = row_t + A.E;
+    const auto at = [](int e) { return e + (e >> 5); };
+    float* group_t = row_t + at(A.E);
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {
       const int e = sub + L * k;
-      if (e < A.E) row_t[e] = !by_score && A.top == 2 && l[k] > -INFINITY ? score(k) : t[k];
+      if (e < A.E) row_t[at(e)] = !by_score && A.top == 2 && l[k] > -INFINITY ? score(k) : t[k];
     }
     wave_lds();
     const int gs = A.E / A.groups;
-    for (int g = sub; g < A.groups; g += L) {
+    int P = 1;
+    while (2 * P * A.groups <= L) P *= 2;
+    const int run = (gs + P - 1) / P;
+    for (int g0 = 0; g0 < A.groups; g0 += L / P) {
+      const int g = g0 + sub / P, first = g * gs + sub % P * run;
+      const int n = g < A.groups ? min(run, (g + 1) * gs - first) : 0;
       float best = -INFINITY, next = -INFINITY;
-      int i = sub % gs;  // lanes start at places of their own: other banks
-      for (int j = 0; j < gs; ++j) {
-        const float v = row_t[g * gs + i];
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float v = row_t[at(first + i)];
         next = fmaxf(next, fminf(best, v));
         best = fmaxf(best, v);
-        i = i + 1 < gs ? i + 1 : 0;
       }
-      group_t[g] = A.top == 2 && next > -INFINITY ? best + next : best;
+      for (int o = 1; o < P; o *= 2) {
+        const float b = __shfl_xor(best, o), x = __shfl_xor(next, o);
+        next = fmaxf(fmaxf(next, x), fminf(best, b));
+        best = fmaxf(best, b);
+      }
+      if (g < A.groups) group_t[g] = A.top == 2 && next > -INFINITY ? best + next : best;
     }
     wave_lds();
-    uint64_t kept = 0;
     float least = INFINITY, most = -INFINITY;  // of the groups kept and of the others
-    for (int g0 = 0; g0 < A.groups; g0 += L) {
-      const int g = g0 + sub;
-      int place = A.groups;
-      if (g < A.groups) {
-        const float v = group_t[g];
-        place = 0;
-        for (int j = 0; j < A.groups; ++j) place += group_t[j] > v || (group_t[j] == v && j < g);
-        if (place < A.keep) least = fminf(least, v);
-        else most = fmaxf(most, v);
+    for (int g0 = 0; g0 < A.groups; g0 += L / P) {
+      const int g = g0 + sub / P, first = g * gs + sub % P * run;
+      if (g >= A.groups) continue;
+      const float v = group_t[g];
+      int place = 0;
+      for (int j = 0; j < A.groups; ++j) {
+        const float o = group_t[j];
+        place += o > v || (o == v && j < g);
       }
-      const uint64_t b = __ballot(place < A.keep);
-      kept |= (L == 64 ? b : (b >> (row * L)) & 0xffff) << g0;
+      if (place < A.keep) {
+        least = fminf(least, v);
+      } else {
+        most = fmaxf(most, v);
+        const int n = min(run, (g + 1) * gs - first);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) row_t[at(first + i)] = -INFINITY;
+      }
     }
     least = -lanes_max<L>(-least);
     most = lanes_max<L>(most);
     if (need_s) unsure = most > -INFINITY && !(least - most > 4.f * fmaxf(kOff(least), kOff(most)));
-    const uint32_t magic = ((1u << 21) + gs - 1) / gs;  // e / gs = e magic >> 21, for e < 1024 and gs <= 512
+    wave_lds();
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {
-      const uint32_t e = sub + L * k;
-      if (!((kept >> ((e * magic >> 21) & 63)) & 1)) t[k] = -INFINITY;
+      const int e = sub + L * k;
+      if (e < A.E && row_t[at(e)] == -INFINITY) t[k] = -INFINITY;
     }
   }
   // at least m experts are not below the m-th largest of the lanes' maxima
-  float top = -INFINITY;
+  float bound = -FLT_MAX;  // EPL = 1: every expert may be placed
+  if constexpr (EPL > 1) {
+    float top = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < EPL; ++k) top = fmaxf(top, t[k]);
-  float bound;
-  if constexpr (EPL == 1) {
-    bound = -INFINITY;  // every expert may be placed
-  } else {
-    int reach = 0;  // lanes whose maximum is not below this one
-#pragma unroll
-    for (int j = 0; j < L; ++j) reach += __shfl(top, j, L) >= top;
+    for (int k = 0; k < EPL; ++k) top = fmaxf(top, t[k]);
+    const int reach = not_below<L>(top);  // lanes whose maximum is not below this one
     bound = lanes_max<L>(reach >= A.m ? top : -INFINITY);
     if (by_score) bound -= 3.f * kOff(bound);
+    bound = fmaxf(bound, -FLT_MAX);
   }
   int count = 0;
 #pragma unroll
-  for (int k = 0; k < EPL; ++k) count += t[k] >= bound && t[k] > -INFINITY;
+  for (int k = 0; k < EPL; ++k) count += t[k] >= bound;
   int before = count;
 #pragma unroll
   for (int o = 1; o < L; o *= 2) {
@@ -317,46 +341,49 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
   const int n = __shfl(before, L - 1, L);
   before -= count;
   unsure |= n > kPlaces;
-  Candidate* list = reinterpret_cast<Candidate*>(mine_lds);
+  double* list_t = mine_lds;                                        // kPlaces float64 scores,
+  int* list_e = reinterpret_cast<int*>(mine_lds + kPlaces);         // their experts,
+  float* list_l = reinterpret_cast<float*>(list_e + kPlaces);       // and their logits;
+  int* placed = reinterpret_cast<int*>(list_l + kPlaces);           // the m codes
   wave_lds();
   if (n <= kPlaces) {
 #pragma unroll
     for (int k = 0; k < EPL; ++k)
-      if (t[k] >= bound && t[k] > -INFINITY) {
-        const int e = sub + L * k;
-        list[before++] = Candidate{(double)l[k], e, l[k]};
+      if (t[k] >= bound) {
+        list_e[before] = sub + L * k;
+        list_l[before++] = l[k];
       }
   }
   wave_lds();
   const int rounds = (n <= kPlaces ? n + L - 1 : 0) / L;  // of L candidates
   // float64 scores where a bias takes part
-  if (by_score) {
-    for (int s = 0; s < rounds; ++s) {
-      const int i = s * L + sub;
-      if (i < n) {
-        const double x = list[i].t;
-        list[i].t = (A.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx) / total) + (double)A.bias[list[i].e];
-      }
-    }
-    wave_lds();
-  }
-  int e_mine = -1;
   for (int s = 0; s < rounds; ++s) {
     const int i = s * L + sub;
-    int place = A.m;
     if (i < n) {
-      const Candidate c = list[i];
-      place = 0;
-      for (int j = 0; j < n; ++j) {
-        const Candidate o = list[j];
-        place += o.t > c.t || (o.t == c.t && o.e < c.e);
-      }
-      // the winners' codes to the row's lanes, through what the list has spare
-      if (place < A.m) reinterpret_cast<int*>(list + kPlaces)[place] = c.e;
+      double x = (double)list_l[i];
+      if (by_score)
+        x = (A.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx) / total) + (double)A.bias[list_e[i]];
+      list_t[i] = x;
     }
   }
   wave_lds();
-  if (!unsure && sub < A.m && sub < n) e_mine = reinterpret_cast<int*>(list + kPlaces)[sub];
+  int e_mine = -1;
+  for (int s = 0; s < rounds; ++s) {
+    const int i = s * L + sub;
+    if (i < n) {
+      const double t_i = list_t[i];
+      const int e_i = list_e[i];
+      int place = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const double o = list_t[j];
+        place += o > t_i || (o == t_i && list_e[j] < e_i);
+      }
+      if (place < A.m) placed[place] = e_i;
+    }
+  }
+  wave_lds();
+  if (!unsure && sub < A.m && sub < n) e_mine = placed[sub];
   const double q = selected<T, L>(A, base, e_mine, mx, total);
   if (in && !unsure && sub < A.m) {
     A.idx[r * A.m + sub] = e_mine;

@@ -30,7 +30,7 @@ namespace gmm {
 namespace {
 
 typedef unsigned long long u64;
-constexpr int kBins = 2048, kSegs = 128, kList = 2048;
+constexpr int kBins = 2048, kSegs = 256, kList = 2048;
 constexpr int kFewKept = 256;  // top-p: so few elements down to the cut are sorted, more are passed over once more
 constexpr float kBinsPerUnit = 64.f;
 
@@ -297,16 +297,43 @@ __device__ inline u64 cut_bin(const Settings& q, Cutting& sh, const u64* bin) {
 
 // Elements of the bins before sh.at, and of the bin itself, as key << 32 |
 // ~index from the two ends of sh.list; counters that pass its half say so.
+// Most elements lie below: a thread marks the others of the pieces that it has
+// in flight by one comparison each (NaN too for now, and all where the bin is
+// the last one, which has no lower end), and looks at the marked ones after.
 template <typename T>
 __device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
+  constexpr int E = 16 / (int)sizeof(T), U = 4;
   const int at = sh.at;
-  each<4>(R, i0, i1, thread, threads, [&](int64_t i, float l) {
+  const float end = at == kBins - 1 ? __builtin_nanf("") : (float)(at + 1);
+  const auto add = [&](int64_t i, float v) {
+    if (!(v > -INFINITY)) return;
+    const float l = fminf(v, FLT_MAX);
     const int b = R.bin(l);
     if (b > at) return;
-    const u64 v = (u64)key_of(l) << 32 | (uint32_t)~(uint32_t)i;
+    const u64 entry = (u64)key_of(l) << 32 | (uint32_t)~(uint32_t)i;
     const int slot = atomicAdd(b < at ? &sh.na : &sh.nb, 1);
-    if (slot < kList / 2) sh.list[b < at ? slot : kList - 1 - slot] = v;
-  });
+    if (slot < kList / 2) sh.list[b < at ? slot : kList - 1 - slot] = entry;
+  };
+  const int64_t step = (int64_t)threads * E, whole = i0 + (i1 - i0) / E * E;
+  for (int64_t i = i0 + (int64_t)thread * E; i < whole; i += U * step) {
+    T v[U][E];
+    load_pieces<T, U>(v, R.p, i, step, whole);
+    uint32_t marked = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) m |= (R.mx - (float)v[u][e]) * R.bins >= end ? 0u : 1u << e;
+      if (i + u * step < whole) marked |= m << (u * E);
+    }
+    while (marked) {
+      const int k = __builtin_ctz(marked);
+      marked &= marked - 1;
+      const int64_t j = i + k / E * step + k % E;
+      add(j, (float)R.p[j]);
+    }
+  }
+  if (i1 - whole > thread && thread < E) add(whole + thread, (float)R.p[whole + thread]);
   __syncthreads();
 }
 
@@ -381,8 +408,9 @@ __device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R,
   group_sync<TH>();
   int place = 0;
   u64 before = 0;
+  const int others = (i & ~63) < n ? n : 0;  // waves without an element have nothing to compare
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) {
+  for (int j = 0; j < others; ++j) {
     const bool ahead = sh.list[j] > mine;
     place += ahead;
     before += ahead ? sh.sum[j] : 0;
@@ -397,7 +425,7 @@ __device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R,
   group_sync<TH>();
   u64 to = 0;
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) to += (uint32_t)sh.list[j] >= (uint32_t)mine ? sh.sum[j] : 0;  // ~index: descending
+  for (int j = 0; j < others; ++j) to += (uint32_t)sh.list[j] >= (uint32_t)mine ? sh.sum[j] : 0;  // ~index: descending
   if (in && (double)to > goal && !((double)(to - w) > goal)) answer(A, R, r, list_logit(mine), ~(uint32_t)mine, total);
 }
 
@@ -475,6 +503,39 @@ __device__ inline int pass_at(u64 n, u64 ties, u64 wt, double goal, u64& before,
   return lane;
 }
 
+// One wave: the entry of sh.seg (and sh.tie), PER a lane, at which the sum
+// passes the goal, as pass_at has it.
+template <int PER>
+__device__ inline int pass_list(const Shared& sh, u64 wt, double goal, u64& before, u64& left) {
+  const int lane = threadIdx.x & 63;
+  u64 n = 0, ties = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    n += sh.seg[lane * PER + e];
+    ties += sh.tie[lane * PER + e];
+  }
+  int s = pass_at(n, ties, wt, goal, before, left) * PER;
+  for (int e = 0; e < PER - 1; ++e, ++s) {
+    const u64 t = min((u64)sh.tie[s], left), m = sh.seg[s] + t * wt;
+    if ((double)(before + m) > goal) break;
+    before += m;
+    left -= t;
+  }
+  return s;
+}
+// the whole of sh.seg and sh.tie, by one wave
+template <int PER>
+__device__ inline u64 whole_list(const Shared& sh, u64 wt, u64 left) {
+  const int lane = threadIdx.x & 63;
+  u64 n = 0, ties = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    n += sh.seg[lane * PER + e];
+    ties += sh.tie[lane * PER + e];
+  }
+  return wave_sum_u64(n) + min(wave_sum_u64(ties), left) * wt;
+}
+
 // Kept weights and elements equal to the cut of the segments of `len` elements;
 // a wave reads two of them at once.
 template <int TH, typename T>
@@ -483,7 +544,12 @@ __device__ inline void segments(const Row<T>& R, const Cut& cut, int64_t i0, int
   const T* p = R.p;
   const int lane = threadIdx.x & 63;
   const int64_t whole = i0 + (i1 - i0) / E * E;
-  for (int s = (threadIdx.x >> 6) * U; s < kSegs; s += TH / 64 * U) {
+  const int used = (int)((i1 - i0 + len - 1) / len);
+  for (int s = used + threadIdx.x; s < kSegs; s += TH) {
+    sh.seg[s] = 0;
+    sh.tie[s] = 0;
+  }
+  for (int s = (threadIdx.x >> 6) * U; s < used; s += TH / 64 * U) {
     u64 mass[U] = {}, ties[U] = {};
     const auto one = [&](int u, float v) {
       const float l = fminf(v, FLT_MAX);
@@ -507,6 +573,7 @@ __device__ inline void segments(const Row<T>& R, const Cut& cut, int64_t i0, int
       // the last elements, less than a piece, belong to the segment that they lie in
       const int64_t a = i0 + (s + u) * len;
       if (whole + lane < i1 && lane < E && whole >= a && whole < a + len) one(u, (float)p[whole + lane]);
+      if (s + u >= used) break;
       mass[u] = wave_sum_u64(mass[u]);
       ties[u] = wave_sum_u64(ties[u]);
       if (lane == 0) {
@@ -540,25 +607,13 @@ __device__ __forceinline__ void choose(const SampleArgs& A, const Row<T>& R, con
   segments<TH>(R, cut, i0, i1, len, sh);
   __syncthreads();
   if (threadIdx.x >= 64) return;
-  static_assert(kSegs == 128, "two segments a lane");
   const u64 wt = cut.ties ? R.weight_min_p(cut.l) : 0;
-  const u64 n0 = sh.seg[2 * lane], n1 = sh.seg[2 * lane + 1], t0 = sh.tie[2 * lane], t1 = sh.tie[2 * lane + 1];
   if (goal < 0.0) {
-    const u64 ties = min(wave_sum_u64(t0 + t1), cut.ties);
-    total = wave_sum_u64(n0 + n1) + ties * wt;
+    total = whole_list<kSegs / 64>(sh, wt, cut.ties);
     goal = aim(A, r, total);
   }
   u64 left = cut.ties;
-  int s = pass_at(n0 + n1, t0 + t1, wt, goal, before, left);
-  // of the lane's two segments
-  const u64 first = __shfl(n0, s) + min(__shfl(t0, s), left) * wt;
-  if (!((double)(before + first) > goal)) {
-    before += first;
-    left -= min(__shfl(t0, s), left);
-    s = 2 * s + 1;
-  } else {
-    s = 2 * s;
-  }
+  const int s = pass_list<kSegs / 64>(sh, wt, goal, before, left);
   for (int64_t a = i0 + s * len, end = min(a + len, i1); a < end; a += tile) {
     const int64_t b = min(a + tile, end);
     u64 mass = 0, tied = 0;
@@ -679,8 +734,9 @@ __device__ __forceinline__ Cut cut_of_bin(const Row<T>& R, const Settings& q, Sh
     if (i < nb) sh.sum[i] = w;
     __syncthreads();
     u64 before = above, same = 0, place = 0;
+    const int others = (i & ~63) < nb ? nb : 0;
 #pragma unroll 4
-    for (int j = 0; j < nb; ++j) {
+    for (int j = 0; j < others; ++j) {
       const u64 other = sh.list[j];
       if (other > mine) {
         before += sh.sum[j];
@@ -765,10 +821,17 @@ __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
   choose<TH>(A, R, cut, r, 0, R.V, 0, 0, -1.0, sh);
 }
 
-// Long rows: parts of a row in workgroups of their own.
+// Long rows: parts of a row in workgroups of their own, whose waves have a
+// quarter each where what is kept is summed.
+constexpr int kQuarters = 4;
 __device__ inline void part_of(const SampleArgs& A, int64_t& i0, int64_t& i1) {
   i0 = (int64_t)blockIdx.x * A.part;
   i1 = min(i0 + A.part, A.V);
+}
+__device__ inline void quarter_of(const SampleArgs& A, int64_t& q0, int64_t& q1) {
+  const int64_t quarter = A.part / kQuarters;
+  q0 = min((int64_t)blockIdx.x * A.part + (threadIdx.x >> 6) * quarter, A.V);
+  q1 = min(q0 + quarter, A.V);
 }
 // every wave looks at all parts
 __device__ inline u64 best_part(const SampleRow& w, int parts) {
@@ -798,7 +861,6 @@ template <typename T>
 __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   constexpr int TH = 256;
   __shared__ u64 bin[kBins];
-  __shared__ u64 red[TH / 64];
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
   Row<T> R;
@@ -808,9 +870,10 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   part_of(A, i0, i1);
   if (q.mode == kOpen) {
     u64 mass = 0;
-    each<2>(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) { mass += R.weight_min_p(l); });
-    mass = block_sum<TH>(mass, red);
-    if (threadIdx.x == 0) w.mass[blockIdx.x] = mass;
+    quarter_of(A, i0, i1);
+    each<2>(R, i0, i1, threadIdx.x & 63, 64, [&](int64_t, float l) { mass += R.weight_min_p(l); });
+    mass = wave_sum_u64(mass);
+    if ((threadIdx.x & 63) == 0) w.mass[blockIdx.x * kQuarters + (threadIdx.x >> 6)] = mass;
     return;
   }
   for (int i = threadIdx.x; i < kBins; i += TH) bin[i] = 0;
@@ -840,21 +903,29 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
     sh.na = sh.nb = 0;
   }
   __syncthreads();
-  int64_t i0, i1;
+  int64_t i0, i1, q0, q1;
   part_of(A, i0, i1);
+  quarter_of(A, q0, q1);
+  const int64_t quarter = A.part / kQuarters;
   collect(R, sh, i0, i1, threadIdx.x, TH);
   // a place in the row's list for all of them; too many here are too many there
   const int na = sh.na, nb = sh.nb;
   if (q.mode == kMass) {  // what the part keeps for sure
     u64 mass = 0;
-    if (na <= kList / 2)
-      for (int i = threadIdx.x; i < na; i += TH) mass += R.weight_min_p(list_logit(sh.list[i]));
-    else
-      each<1>(R, i0, i1, threadIdx.x, TH, [&](int64_t, float l) {
+    if (na <= kList / 2) {
+      if (threadIdx.x < kQuarters) sh.red[threadIdx.x] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < na; i += TH)
+        atomicAdd(&sh.red[(~(uint32_t)sh.list[i] - (uint32_t)i0) / (uint32_t)quarter], R.weight_min_p(list_logit(sh.list[i])));
+      __syncthreads();
+      if (threadIdx.x < kQuarters) w.mass[blockIdx.x * kQuarters + threadIdx.x] = sh.red[threadIdx.x];
+    } else {
+      each<1>(R, q0, q1, threadIdx.x & 63, 64, [&](int64_t, float l) {
         if (R.bin(l) < sh.at) mass += R.weight_min_p(l);
       });
-    mass = block_sum<TH>(mass, sh.red);
-    if (threadIdx.x == 0) w.mass[blockIdx.x] = mass;
+      mass = wave_sum_u64(mass);
+      if ((threadIdx.x & 63) == 0) w.mass[blockIdx.x * kQuarters + (threadIdx.x >> 6)] = mass;
+    }
   }
   __shared__ int base[2];
   if (threadIdx.x == 0) {
@@ -879,9 +950,7 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
   Row<T> R;
   const Settings q = row_of(A, r, best_part(w, parts), R);
   if (plain_answer(A, R, q, r)) return;
-  const int lane = threadIdx.x & 63;
   Cut cut{-INFINITY, 0};
-  u64 mine = 0, ties = 0, wt = 0;  // every wave: a lane a part
   int64_t i0 = 0, i1 = A.V;
   u64 before = 0, total = 0;
   double goal = -1.0;
@@ -890,42 +959,45 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
   if (q.mode != kOpen && !list && (q.mode == kCount || nb > kList)) {
     cut = cut_by_reach<TH>(R, q, sh);
   } else {
-    mine = lane < parts ? w.mass[lane] : 0;
+    static_assert(kSegs >= kSampleParts * kQuarters && TH >= kSegs, "a segment a quarter, a thread a segment");
+    const int s = threadIdx.x;
+    const int64_t quarter = A.part / kQuarters;
+    if (s < kSegs) {
+      sh.seg[s] = s < parts * kQuarters ? w.mass[s] : 0;
+      sh.tie[s] = 0;
+    }
+    u64 wt = 0;
     if (q.mode != kOpen) {
       const int to = list ? na : 0;
       for (int i = threadIdx.x; i < to; i += TH) sh.list[i] = w.list[i];
       for (int i = threadIdx.x; i < nb; i += TH) sh.list[to + i] = w.list[2 * kSampleList - 1 - i];
       if (threadIdx.x == 0) sh.above = w.above;
-      if (threadIdx.x < kSegs) {
-        sh.seg[threadIdx.x] = 0;
-        sh.tie[threadIdx.x] = 0;
-      }
       __syncthreads();
       if (list) {
         finish_list<TH>(A, R, q, r, sh, na + nb, w.whole);
         return;
       }
       cut = cut_of_bin<TH>(R, q, sh, w.whole, nb);
-      // what the parts keep of the bin: all above the cut, and the ties by index
+      // what the quarters keep of the bin: all above the cut, and the ties by index
       for (int i = threadIdx.x; i < nb; i += TH) {
         if (sh.list[i] < sh.edge) continue;
         const float l = list_logit(sh.list[i]);
-        const int part = (int)(~(uint32_t)sh.list[i] / (uint32_t)A.part);
-        if (l > cut.l) atomicAdd(&sh.seg[part], R.weight_min_p(l));
-        else atomicAdd(&sh.tie[part], 1u);
+        const uint32_t at = ~(uint32_t)sh.list[i], part = at / (uint32_t)A.part;
+        const int k = (int)(part * kQuarters + (at - part * (uint32_t)A.part) / (uint32_t)quarter);
+        if (l > cut.l) atomicAdd(&sh.seg[k], R.weight_min_p(l));
+        else atomicAdd(&sh.tie[k], 1u);
       }
-      __syncthreads();
       wt = R.weight_min_p(cut.l);
-      if (lane < parts) mine += sh.seg[lane];
-      ties = sh.tie[lane];
     }
-    total = wave_sum_u64(mine) + cut.ties * wt;
+    __syncthreads();
+    // every wave
+    total = whole_list<kSegs / 64>(sh, wt, cut.ties);
     goal = aim(A, r, total);
     u64 left = cut.ties;
-    const int part = pass_at(mine, ties, wt, goal, before, left);
+    const int k = pass_list<kSegs / 64>(sh, wt, goal, before, left);
     cut.ties = left;
-    i0 = part * A.part;
-    i1 = min(i0 + A.part, A.V);
+    i0 = (k / kQuarters) * A.part + (k % kQuarters) * quarter;
+    i1 = min(i0 + quarter, A.V);
   }
   choose<TH>(A, R, cut, r, i0, i1, before, total, goal, sh);
 }
@@ -956,7 +1028,7 @@ static hipError_t run_sample(SampleArgs A, void* ws, hipStream_t s) {
     // about four workgroups a compute unit, of whole pieces
     const int64_t want = std::min<int64_t>(std::max<int64_t>(1, 1024 / n), (A.V + kPartLeast - 1) / kPartLeast);
     const int64_t most = std::min<int64_t>(want, kSampleParts);
-    A.part = ((A.V + most - 1) / most + 7) / 8 * 8;
+    A.part = ((A.V + most - 1) / most + 8 * kQuarters - 1) / (8 * kQuarters) * (8 * kQuarters);
     const unsigned parts = (unsigned)((A.V + A.part - 1) / A.part);
     hipLaunchKernelGGL(sample_best_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
     hipLaunchKernelGGL(sample_bins_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
