@@ -36,6 +36,17 @@ __device__ inline int64_t row_base(const RouteArgs& A, int64_t r) {
   return b * A.stride_b + (r - b * A.N) * A.ld;
 }
 
+// 1 / x for x in [1, 2^60]: two Newton steps leave about 1 unit in the last place
+__device__ inline double reciprocal(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+  y = fma(fma(-x, y, 1.0), y, y);
+  return fma(fma(-x, y, 1.0), y, y);
+}
+__device__ inline double sigmoid_f64(double l) {
+  const double z = exp_neg(-fabs(l)), y = reciprocal(1.0 + z);
+  return l >= 0.0 ? y : z * y;
+}
+
 template <int L>
 __device__ inline float lanes_max(float v) {
   v = row16_max(v);
@@ -66,10 +77,10 @@ __device__ inline double selected(const RouteArgs& A, int64_t base, int e, float
   const float l = e >= 0 ? fminf(logit<T>(A, base + e), FLT_MAX) : -INFINITY;
   double q = 0.0;
   if (A.sigmoid) {
-    if (e >= 0) q = 1.0 / (1.0 + exp(-(double)l));
+    if (e >= 0) q = sigmoid_f64((double)l);
   } else {
     const float top = A.renorm ? lanes_max<L>(l) : mx;
-    if (e >= 0) q = exp((double)l - (double)top);
+    if (e >= 0) q = exp_neg((double)l - (double)top);
     if (!A.renorm && e >= 0) q /= total;
   }
   if (A.renorm) {
@@ -102,12 +113,12 @@ __device__ void route_exact(const RouteArgs& A, int64_t r, double* row) {
   double total = 1.0;
   if (A.sigmoid) {
 #pragma unroll
-    for (int k = 0; k < EPL; ++k) s[k] = l[k] > -INFINITY ? 1.0 / (1.0 + exp(-(double)l[k])) : 0.0;
+    for (int k = 0; k < EPL; ++k) s[k] = l[k] > -INFINITY ? sigmoid_f64((double)l[k]) : 0.0;
   } else {
     total = 0.0;
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {
-      s[k] = l[k] > -INFINITY ? exp((double)l[k] - (double)mx) : 0.0;
+      s[k] = l[k] > -INFINITY ? exp_neg((double)l[k] - (double)mx) : 0.0;
       total += s[k];
     }
     total = wave_sum(total);
@@ -191,6 +202,26 @@ __host__ __device__ inline int route_room(int E, int groups, int lanes) {
   return ((scores > list ? scores : list) + 1) / 2 * 2;
 }
 
+// The row's logits, expert sub + L k in l[k]: -inf past E, where there is no row
+// and for NaN, at most FLT_MAX.  The loads are made without a branch.
+template <typename T, int L, int EPL>
+__device__ inline void load_logits(float (&l)[EPL], const T* row, int sub, int E, bool in) {
+  T v[EPL];
+  if (E == L * EPL) {
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) v[k] = row[sub + L * k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) v[k] = row[min(sub + L * k, E - 1)];
+  }
+#pragma unroll
+  for (int k = 0; k < EPL; ++k) {
+    l[k] = fminf(fmaxf((float)v[k], -INFINITY), FLT_MAX);  // NaN gives way to -inf
+    if (E != L * EPL && sub + L * k >= E) l[k] = -INFINITY;
+    if (!in) l[k] = -INFINITY;
+  }
+}
+
 // how many of the row's lanes hold a value not below v, this one included
 template <int L>
 __device__ inline int not_below(float v) {
@@ -221,15 +252,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
   const bool grouped = A.groups > 1 && A.keep < A.groups, by_score = A.bias != nullptr;
   float l[EPL], t[EPL];
   float mx = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < EPL; ++k) {
-    const int e = sub + L * k;
-    l[k] = -INFINITY;
-    if (in && e < A.E) {
-      const float v = logit<T>(A, base + e);
-      if (v > -INFINITY) l[k] = fminf(v, FLT_MAX);
-    }
-  }
+  load_logits<T, L, EPL>(l, static_cast<const T*>(A.l) + base, sub, A.E, in);
   // scores in float32, where the order is not that of the logits; the softmax's
   // sum in float64, where a score itself is asked for
   double total = 1.0;
@@ -240,7 +263,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
     mx = lanes_max<L>(mx);
     total = 0.0;
 #pragma unroll
-    for (int k = 0; k < EPL; ++k) total += l[k] > -INFINITY ? exp((double)l[k] - (double)mx) : 0.0;
+    for (int k = 0; k < EPL; ++k) total += l[k] > -INFINITY ? exp_neg((double)l[k] - (double)mx) : 0.0;
     total = lanes_sum_f64<L>(total);
   }
   const float inv = total > 0.0 ? (float)(1.0 / total) : 0.f;
@@ -249,10 +272,13 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
     return __expf(l[k] - mx) * inv;
   };
 #pragma unroll
-  for (int k = 0; k < EPL; ++k) {
-    const int e = sub + L * k;
-    t[k] = l[k];
-    if (by_score && l[k] > -INFINITY) t[k] = score(k) + A.bias[e];
+  for (int k = 0; k < EPL; ++k) t[k] = l[k];
+  if (by_score) {
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) {
+      const float v = score(k) + A.bias[min(sub + L * k, A.E - 1)];
+      t[k] = l[k] > -INFINITY ? v : -INFINITY;
+    }
   }
   bool unsure = false;
   if (grouped) {
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
     if (i < n) {
       double x = (double)list_l[i];
       if (by_score)
-        x = (A.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx) / total) + (double)A.bias[list_e[i]];
+        x = (A.sigmoid ? sigmoid_f64(x) : exp_neg(x - (double)mx) / total) + (double)A.bias[list_e[i]];
       list_t[i] = x;
     }
   }
@@ -413,16 +439,11 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs A) {
   float mx = -INFINITY;
   int mine = in && A.dweights && sub < A.m ? A.idx[r * A.m + sub] : -1;
   float u = mine >= 0 ? A.scale * A.dweights[r * A.m + sub] : 0.f;
+  load_logits<T, L, EPL>(l, static_cast<const T*>(A.l) + base, sub, A.E, in);
 #pragma unroll
   for (int k = 0; k < EPL; ++k) {
-    const int e = sub + L * k;
-    l[k] = -INFINITY;
-    ds[k] = dl[k] = 0.f;
-    if (in && e < A.E) {
-      const float v = logit<T>(A, base + e);
-      if (v > -INFINITY) l[k] = fminf(v, FLT_MAX);
-      if (A.dscores) ds[k] = A.dscores[e];
-    }
+    ds[k] = A.dscores ? A.dscores[min(sub + L * k, A.E - 1)] : 0.f;
+    dl[k] = 0.f;
     mx = fmaxf(mx, l[k]);
   }
   mx = lanes_max<L>(mx);
