@@ -64,14 +64,30 @@ __all__ = ["gmm_workspace_bytes", "gmm_estep_stats", "gmm_mstep", "gmm_fit_step"
            "new_adamw_state", "new_stats", "GmmError", "cov_shape"]
 
 
+_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported at the first call (an import statement in every call costs a lookup each)."""
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
+
+
+_codes = {}
+
+
+def _dtype_codes():
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float32: _abi.DT_F32, torch.bfloat16: _abi.DT_BF16, torch.float16: _abi.DT_F16})
+    return _codes
 
 
 def _dtype_code(t):
-    torch = _torch()
-    return {torch.float32: _abi.DT_F32, torch.bfloat16: _abi.DT_BF16, torch.float16: _abi.DT_F16}[t.dtype]
+    return _dtype_codes()[t.dtype]
 
 
 def _data(X) -> GmmData:
@@ -85,7 +101,7 @@ def _data(X) -> GmmData:
         raise ValueError("X must be (N, D) or (B, N, D)")
     if D > 0 and N > 0 and X.stride(-1) != 1:
         raise ValueError("X needs unit stride along D")
-    return GmmData(ctypes.c_void_p(X.data_ptr()), _dtype_code(X), B, N, D, ld, sb)
+    return GmmData(X.data_ptr(), _dtype_code(X), B, N, D, ld, sb)
 
 
 def _cov_code(cov):
@@ -112,7 +128,7 @@ def _stream(stream):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def gmm_workspace_bytes(X, K, cov, op=OP_FIT, m=0) -> int:
@@ -419,7 +435,7 @@ class _on:
 
 def _expect(name, t, dtype, shape):
     """t as the library takes it: a contiguous tensor of one type and shape."""
-    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
                          f"(got {t.dtype}, {tuple(t.shape)})")
 
@@ -433,24 +449,24 @@ def _check_ws(ws):
 
 def _rows(name, t):
     """The gmm_data of rows at any strides that keep D contiguous and rows apart."""
-    torch = _torch()
-    if t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    code, shape = _dtype_codes().get(t.dtype), t.shape
+    if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
-    if t.dim() not in (2, 3):
+    if len(shape) not in (2, 3):
         raise ValueError(f"{name} must be (N, D) or (B, N, D)")
-    D = int(t.shape[-1])
-    if D < 1 or (t.dim() == 3 and t.shape[0] < 1):
+    D, N = shape[-1], shape[-2]
+    if D < 1 or (len(shape) == 3 and shape[0] < 1):
         raise ValueError(f"{name} needs B >= 1 and D >= 1")
-    if D > 1 and t.numel() > 0 and t.stride(-1) != 1:
+    stride = t.stride()
+    if D > 1 and stride[-1] != 1 and t.numel() > 0:
         raise ValueError(f"{name} needs unit stride along D")
     # strides along an axis of one element mean nothing
-    N = int(t.shape[-2])
-    ld = int(t.stride(-2)) if N > 1 else D
-    if t.dim() == 2:
-        return GmmData(ctypes.c_void_p(t.data_ptr()), _dtype_code(t), 1, N, D, max(ld, D) if N <= 1 else ld, N * ld)
-    B = int(t.shape[0])
-    sb = int(t.stride(0)) if B > 1 else N * ld
-    return GmmData(ctypes.c_void_p(t.data_ptr()), _dtype_code(t), B, N, D, ld, max(sb, N * ld) if N == 0 else sb)
+    ld = stride[-2] if N > 1 else D
+    if len(shape) == 2:
+        return GmmData(t.data_ptr(), code, 1, N, D, max(ld, D) if N <= 1 else ld, N * ld)
+    B = shape[0]
+    sb = stride[0] if B > 1 else N * ld
+    return GmmData(t.data_ptr(), code, B, N, D, ld, max(sb, N * ld) if N == 0 else sb)
 
 
 def _head(X, W, bias):
@@ -661,14 +677,14 @@ def gmm_layer_norm(X, gamma=None, beta=None, eps=1e-5, out=None, mean=None, rstd
     d = _rows("X", X)
     code = _affine(X, gamma, beta)
     lead = X.shape[:-1]
+    for name, t, dtype, shape in (("out", out, X.dtype, X.shape), ("mean", mean, torch.float32, lead),
+                                  ("rstd", rstd, torch.float32, lead)):
+        if t is not None and t is not False:
+            _expect(name, t, dtype, shape)
     given = [t for t in (out, mean, rstd) if t is not None and t is not False]
     with _on(stream, X, gamma, beta, *given) as s:
         out = torch.empty(X.shape, dtype=X.dtype, device=X.device) if out is None else out
         mean, rstd = _wanted(mean, X, lead, torch.float32), _wanted(rstd, X, lead, torch.float32)
-        _expect("out", out, X.dtype, X.shape)
-        for name, t in (("mean", mean), ("rstd", rstd)):
-            if t is not None:
-                _expect(name, t, torch.float32, lead)
         _abi.check(_abi.lib().gmm_layer_norm(ctypes.byref(d), _ptr(gamma), _ptr(beta), code, float(eps), _ptr(out),
                                              _ptr(mean), _ptr(rstd), s))
     return out, mean, rstd
@@ -677,13 +693,15 @@ def gmm_layer_norm(X, gamma=None, beta=None, eps=1e-5, out=None, mean=None, rstd
 def _affine(X, gamma, beta=None):
     """The type code of gamma and beta, float32 or X's."""
     torch = _torch()
-    kinds = {t.dtype for t in (gamma, beta) if t is not None}
-    if len(kinds) > 1 or not kinds <= {torch.float32, X.dtype}:
+    one = gamma if gamma is not None else beta
+    if one is None:
+        return _abi.DT_F32
+    if one.dtype not in (torch.float32, X.dtype) or (beta is not None and beta.dtype != one.dtype):
         raise ValueError("gamma and beta must both be float32 or both of X's type")
     for name, t in (("gamma", gamma), ("beta", beta)):
         if t is not None:
-            _expect(name, t, t.dtype, X.shape[-1:])
-    return _dtype_code(gamma if gamma is not None else beta) if kinds else _abi.DT_F32
+            _expect(name, t, one.dtype, X.shape[-1:])
+    return _dtype_code(one)
 
 
 def gmm_layer_norm_grad(dout, X, mean, rstd, gamma=None, dX=None, dgamma=None, dbeta=None, accumulate=False, ws=None,
@@ -706,14 +724,14 @@ def gmm_layer_norm_grad(dout, X, mean, rstd, gamma=None, dX=None, dgamma=None, d
         dgamma, dbeta = (False if t is None else t for t in (dgamma, dbeta))
     if accumulate and any(t is None for t in (dX, dgamma, dbeta)):
         raise ValueError("accumulate=True adds to given buffers (False leaves a gradient out)")
+    for name, t, dtype, shape in (("dX", dX, X.dtype, X.shape), ("dgamma", dgamma, torch.float32, (D,)),
+                                  ("dbeta", dbeta, torch.float32, (D,))):
+        if t is not None and t is not False:
+            _expect(name, t, dtype, shape)
     given = [t for t in (dX, dgamma, dbeta) if t is not None and t is not False]
     with _on(stream, X, dout, mean, rstd, gamma, ws, *given) as s:
         dX = _wanted(dX, X, X.shape, X.dtype)
         dgamma, dbeta = _wanted(dgamma, X, (D,), torch.float32), _wanted(dbeta, X, (D,), torch.float32)
-        for name, t, dtype, shape in (("dX", dX, X.dtype, X.shape), ("dgamma", dgamma, torch.float32, (D,)),
-                                      ("dbeta", dbeta, torch.float32, (D,))):
-            if t is not None:
-                _expect(name, t, dtype, shape)
         if ws is None:
             want = (dX is not None) + 2 * (dgamma is not None) + 4 * (dbeta is not None)
             n = int(_abi.lib().gmm_layer_norm_grad_workspace_bytes(ctypes.byref(d), want))
@@ -750,11 +768,13 @@ def gmm_route_topm(logits, m, bias=None, score="softmax", groups=1, keep_groups=
         _expect("bias", bias, torch.float32, logits.shape[-1:])
     if int(m) < 1:
         raise ValueError("m must be >= 1")
+    if idx is not None:
+        _expect("idx", idx, torch.int32, shape)
+    if weights is not None:
+        _expect("weights", weights, torch.float32, shape)
     with _on(stream, logits, bias, idx, weights) as s:
         idx = torch.empty(shape, dtype=torch.int32, device=logits.device) if idx is None else idx
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device) if weights is None else weights
-        _expect("idx", idx, torch.int32, shape)
-        _expect("weights", weights, torch.float32, shape)
         _abi.check(_abi.lib().gmm_route_topm(ctypes.byref(d), _ptr(bias), ctypes.byref(how), int(m), _ptr(idx),
                                              _ptr(weights), s))
     return idx, weights
@@ -779,10 +799,11 @@ def gmm_route_topm_grad(dweights, logits, idx, score="softmax", renormalize=True
         _expect("dweights", dweights, torch.float32, idx.shape)
     if dscores is not None:
         _expect("dscores", dscores, torch.float32, logits.shape[-1:])
+    if dlogits is not None:
+        _expect("dlogits", dlogits, logits.dtype, logits.shape)
     with _on(stream, logits, idx, dweights, dscores, dlogits) as s:
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        _expect("dlogits", dlogits, logits.dtype, logits.shape)
         _abi.check(_abi.lib().gmm_route_topm_grad(ctypes.byref(d), ctypes.byref(how), int(idx.shape[-1]), _ptr(idx),
                                                   _ptr(dweights), _ptr(dscores), _ptr(dlogits), s))
     return dlogits
@@ -836,20 +857,21 @@ def gmm_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1
             raise ValueError(f"{name} must hold one entry per tensor")
     if (norm is None) != (max_norm is None):
         raise ValueError("norm and max_norm go together")
-    codes = {torch.float32: _abi.DT_F32, torch.bfloat16: _abi.DT_BF16, torch.float16: _abi.DT_F16}
+    codes = _dtype_codes()
+    full, coded = (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
     desc = array("q")  # a gmm_adamw_tensor is eleven 8-byte words
     decays = array("q", array("d", map(float, decay)).tobytes())
     used = []
     for i, (p, g, a, b, sa, sb, c) in enumerate(zip(params, grads, m, v, m_scale, v_scale, copies)):
-        code, gcode, n = codes.get(p.dtype), codes.get(g.dtype), p.numel()
-        if code is None or gcode is None or g.shape != p.shape or not (p.is_contiguous() and g.is_contiguous()):
+        code, gcode, n, shape = codes.get(p.dtype), codes.get(g.dtype), p.numel(), p.shape
+        if code is None or gcode is None or g.shape != shape or not (p.is_contiguous() and g.is_contiguous()):
             raise ValueError(f"parameter {i} and its gradient must be contiguous float32, bfloat16 or float16 tensors "
                              "of one shape")
         if (sa is None) != (sb is None):
             raise ValueError(f"state {i} has one scale of two")
-        kinds = (torch.float32,) if sa is None else (torch.float8_e4m3fn, torch.uint8)
+        kinds = full if sa is None else coded
         for t in (a, b):
-            if t.dtype not in kinds or t.shape != p.shape or not t.is_contiguous():
+            if t.dtype not in kinds or t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"states {i} must be contiguous {kinds[0]} tensors of the parameter's shape")
         used += (p, g, a, b)
         if sa is not None:
@@ -860,7 +882,7 @@ def gmm_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1
         ccode = 0
         if c is not None:
             ccode = codes.get(c.dtype)
-            if ccode is None or c.shape != p.shape or not c.is_contiguous():
+            if ccode is None or c.shape != shape or not c.is_contiguous():
                 raise ValueError(f"copy {i} must be a contiguous float32, bfloat16 or float16 tensor of the parameter's "
                                  "shape")
             used.append(c)
@@ -909,13 +931,14 @@ def gmm_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens
             rows.append(v)
         else:
             setattr(how, name, int(v) if name == "top_k" else float(v))
+    if tokens is not None:
+        _expect("tokens", tokens, torch.int32, lead)
+    if logp is not None and logp is not False:
+        _expect("logp", logp, torch.float32, lead)
     given = [t for t in (tokens, logp) if t is not None and t is not False]
     with _on(stream, logits, u, ws, *rows, *given) as s:
         tokens = torch.empty(lead, dtype=torch.int32, device=logits.device) if tokens is None else tokens
         logp = _wanted(logp, logits, lead, torch.float32)
-        _expect("tokens", tokens, torch.int32, lead)
-        if logp is not None:
-            _expect("logp", logp, torch.float32, lead)
         if ws is None:
             n = int(_abi.lib().gmm_sample_workspace_bytes(ctypes.byref(d)))
             ws = torch.empty(max(n, 256), dtype=torch.uint8, device=logits.device)

@@ -9,9 +9,11 @@ component and log p(x_i)), score from gmm_estep_stats (sum_i log p(x_i)),
 fit from gmm_fit_step (or gmm_topk_fit_step, the approximate top-k mode of
 the GMMXX README), KernelDensity.score_samples from gmm_kde_score, the rows
 that reconstruct rebuilds from gmm_codebook_lookup, SoftmaxHead's losses and
-gradients from gmm_softmax_xent, gmm_softmax_xent_grad and gmm_clip_grad_norm.
-What runs here is argument handling, the stopping rule, the AIC/BIC arithmetic
-on B returned scalars and SoftmaxHead's parameter update.
+gradients from gmm_softmax_xent, gmm_softmax_xent_grad, gmm_clip_grad_norm and
+gmm_layer_norm with its gradient, its AdamW steps from gmm_adamw_step, its
+routing and its draws from gmm_route_topm and gmm_sample.  What runs here is
+argument handling, the stopping rule, the AIC/BIC arithmetic on B returned
+scalars, SoftmaxHead's momentum update and the library product of its logits.
 
   n_parameters(cov, K, D)                       -> int
   score_samples(X, w, mu, cv, cov)              -> (B, N) float32 log p(x_i)
@@ -32,9 +34,10 @@ from dataclasses import dataclass
 
 import numpy as np
 
-from . import (gmm_clip_grad_norm, gmm_codebook_lookup, gmm_estep_stats, gmm_fit, gmm_fit_step, gmm_kde_score,
-               gmm_kmeans_step, gmm_predict_proba_topm, gmm_softmax_xent, gmm_softmax_xent_grad, gmm_topk_fit_step,
-               gmm_topk_fit_workspace_bytes, new_stats)
+from . import (gmm_adamw_step, gmm_clip_grad_norm, gmm_codebook_lookup, gmm_estep_stats, gmm_fit, gmm_fit_step,
+               gmm_kde_score, gmm_kmeans_step, gmm_layer_norm, gmm_layer_norm_grad, gmm_predict_proba_topm,
+               gmm_route_topm, gmm_sample, gmm_softmax_xent, gmm_softmax_xent_grad, gmm_topk_fit_step,
+               gmm_topk_fit_workspace_bytes, new_adamw_state, new_stats)
 
 
 def _torch():
@@ -417,29 +420,43 @@ class SoftmaxHead:
     instead of on the rows' density -- a router over the lists of a coarse
     quantizer, for example, from the labels of KMeans or GaussianMixture.
 
-    fit(X, y) runs full-batch gradient descent with momentum on the mean
-    cross entropy of the labelled rows (y (N,) int32; a negative label leaves a
-    row out), each step one gmm_softmax_xent, one gmm_softmax_xent_grad and,
-    with max_grad_norm, one gmm_clip_grad_norm over both gradients, until the
-    loss changes by less than tol.  X is (N, D) float32, bfloat16 or float16 on
-    the GPU; float16 rows are taken as float32 (a copy of them), because a head
-    and its gradients leave half's range: coefficients past 65504, mean gradients
-    over many classes or confident rows below 6e-8.  Fitted state: coef_ (K, D)
-    and intercept_ (K,) float32, loss_ (the mean loss entering the last step),
-    loss_history_, grad_norm_ (the last step's norm before clipping, None without
-    it), n_iter_."""
+    fit(X, y) runs full-batch gradient descent on the mean cross entropy of the
+    labelled rows (y (N,) int32; a negative label leaves a row out), each step one
+    gmm_softmax_xent, one gmm_softmax_xent_grad and, with max_grad_norm, one
+    gmm_clip_grad_norm over the gradients, until the loss changes by less than tol.
+    optimizer "momentum", or "adamw": gmm_adamw_step with weight_decay on coef_
+    alone and its states in state_bits (32 or 8).  layer_norm=True normalises the
+    rows first (gmm_layer_norm, with a scale and a shift that are trained too).  X is
+    (N, D) float32, bfloat16 or float16 on the GPU; float16 rows are taken as
+    float32 (a copy of them), because a head and its gradients leave half's range:
+    coefficients past 65504, mean gradients over many classes or confident rows
+    below 6e-8.  Fitted state: coef_ (K, D) and intercept_ (K,) float32, with
+    layer_norm norm_weight_ and norm_bias_ (D,) float32, loss_ (the mean loss
+    entering the last step), loss_history_, grad_norm_ (the last step's norm before
+    clipping, None without it), n_iter_."""
 
-    def __init__(self, n_classes, learning_rate=1.0, momentum=0.9, max_iter=100, tol=1e-6, max_grad_norm=None):
+    def __init__(self, n_classes, learning_rate=1.0, momentum=0.9, max_iter=100, tol=1e-6, max_grad_norm=None,
+                 optimizer="momentum", betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, layer_norm=False,
+                 random_state=0):
         if int(n_classes) < 1:
             raise ValueError("n_classes must be >= 1")
         if int(max_iter) < 1:
             raise ValueError("max_iter must be >= 1")
         if max_grad_norm is not None and not float(max_grad_norm) > 0.0:
             raise ValueError("max_grad_norm must be > 0")
+        if optimizer not in ("momentum", "adamw"):
+            raise ValueError("optimizer must be 'momentum' or 'adamw'")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if float(weight_decay) != 0.0 and optimizer != "adamw":
+            raise ValueError("weight_decay goes with optimizer='adamw'")
         self.n_classes = int(n_classes)
         self.learning_rate, self.momentum = float(learning_rate), float(momentum)
         self.max_iter, self.tol = int(max_iter), float(tol)
         self.max_grad_norm = None if max_grad_norm is None else float(max_grad_norm)
+        self.optimizer, self.betas, self.eps = optimizer, tuple(map(float, betas)), float(eps)
+        self.weight_decay, self.state_bits, self.layer_norm = float(weight_decay), state_bits, bool(layer_norm)
+        self.random_state = random_state
 
     @classmethod
     def from_mixture(cls, mixture, variance=None, **kwargs):
@@ -465,20 +482,39 @@ class SoftmaxHead:
             raise ValueError("y is (N,) int32")
         return X.float() if X.dtype == torch.float16 else X
 
-    def loss_and_gradients(self, X, y):
-        """(mean loss, its gradients for coef_ and intercept_): a 0-dimensional
-        and two float32 tensors on the GPU."""
-        torch = _torch()
-        X = self._check(X, y)
+    def _ready(self):
         if not hasattr(self, "coef_"):
             raise RuntimeError("call fit first")
+        if self.layer_norm and not hasattr(self, "norm_weight_"):
+            self._set_norm(self.coef_.shape[1], self.coef_.device)
+
+    def _set_norm(self, D, device):
+        torch = _torch()
+        self.norm_weight_, self.norm_bias_ = torch.ones(D, device=device), torch.zeros(D, device=device)
+
+    def _parameters(self):
+        return [self.coef_, self.intercept_] + ([self.norm_weight_, self.norm_bias_] if self.layer_norm else [])
+
+    def loss_and_gradients(self, X, y):
+        """(mean loss, its gradients for coef_ and intercept_, with layer_norm for
+        norm_weight_ and norm_bias_ too): a 0-dimensional and float32 tensors on the
+        GPU."""
+        X = self._check(X, y)
+        self._ready()
         y = y.contiguous()
+        rows = X
+        if self.layer_norm:
+            rows, mean, rstd = gmm_layer_norm(X, self.norm_weight_, self.norm_bias_)
         W = self.coef_.to(X.dtype)
-        loss, lse = gmm_softmax_xent(X, W, y, bias=self.intercept_)
+        loss, lse = gmm_softmax_xent(rows, W, y, bias=self.intercept_)
         n = (y >= 0).sum().clamp_min(1).float()
         gloss = (1.0 / n).expand(y.shape).contiguous()
-        _, dW, db = gmm_softmax_xent_grad(X, W, y, lse, gloss=gloss, bias=self.intercept_, dX=False)
-        return loss.sum() / n, dW.float(), db
+        dX, dW, db = gmm_softmax_xent_grad(rows, W, y, lse, gloss=gloss, bias=self.intercept_,
+                                           dX=None if self.layer_norm else False)
+        if not self.layer_norm:
+            return loss.sum() / n, dW.float(), db
+        _, dg, ds = gmm_layer_norm_grad(dX, X, mean, rstd, gamma=self.norm_weight_, dX=False)
+        return loss.sum() / n, dW.float(), db, dg, ds
 
     def fit(self, X, y):
         torch = _torch()
@@ -486,27 +522,70 @@ class SoftmaxHead:
         if not hasattr(self, "coef_"):
             self._set(torch.zeros(self.n_classes, X.shape[1], device=X.device),
                       torch.zeros(self.n_classes, device=X.device))
-        step = [torch.zeros_like(self.coef_), torch.zeros_like(self.intercept_)]
+        self._ready()
+        params = self._parameters()
+        adamw = self.optimizer == "adamw"
+        if adamw:
+            state = new_adamw_state(params, self.state_bits)
+            decay = [self.weight_decay] + [0.0] * (len(params) - 1)
+        else:
+            step = [torch.zeros_like(p) for p in params]
         self.loss_history_, self.grad_norm_ = [], None
         for self.n_iter_ in range(1, self.max_iter + 1):
             loss, *grads = self.loss_and_gradients(X, y)
             if self.max_grad_norm is not None:
-                self.grad_norm_ = gmm_clip_grad_norm(grads, self.max_grad_norm)
-            for p, v, g in zip((self.coef_, self.intercept_), step, grads):
-                v.mul_(self.momentum).add_(g)
-                p.sub_(v, alpha=self.learning_rate)
+                # AdamW scales the gradients on its way: the norm alone
+                self.grad_norm_ = gmm_clip_grad_norm(grads, float("inf") if adamw else self.max_grad_norm)
+            if adamw:
+                gmm_adamw_step(params, grads, step=self.n_iter_, lr=self.learning_rate, betas=self.betas, eps=self.eps,
+                               weight_decay=decay, norm=self.grad_norm_, max_norm=self.max_grad_norm,
+                               seed=int(self.random_state or 0), **state)
+            else:
+                for p, v, g in zip(params, step, grads):
+                    v.mul_(self.momentum).add_(g)
+                    p.sub_(v, alpha=self.learning_rate)
             self.loss_history_.append(float(loss))
             if len(self.loss_history_) > 1 and abs(self.loss_history_[-2] - self.loss_history_[-1]) < self.tol:
                 break
         self.loss_ = self.loss_history_[-1]
         return self
 
+    def _rows(self, X):
+        return gmm_layer_norm(X, self.norm_weight_, self.norm_bias_)[0] if self.layer_norm else X
+
+    def logits(self, X):
+        """W x + b of every row (normalised first with layer_norm), (N, n_classes)
+        float32: a library product, for the calls that choose among classes."""
+        torch = _torch()
+        if X.dim() != 2:
+            raise ValueError("X is (N, D)")
+        self._ready()
+        X = X.float() if X.dtype == torch.float16 else X
+        return torch.addmm(self.intercept_, self._rows(X).float(), self.coef_.t())
+
+    def route(self, X, m=4, **how):
+        """The m best classes of every row and their weights, as an assignment that
+        gmm_codebook_lookup and gmm_ivf_lists read: (idx (N, m) int32, weights (N, m)
+        float32).  Keyword arguments are gmm_route_topm's (bias, score, groups,
+        keep_groups, group_top, renormalize, scale)."""
+        return gmm_route_topm(self.logits(X), m, **how)
+
+    def sample(self, X, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, u=None):
+        """A class drawn for every row from its posterior, cut by top_k, top_p and
+        min_p (gmm_sample): (classes (N,) int32, log of their share (N,) float32).  u:
+        uniform numbers (N,) float32 in [0, 1); None: drawn from random_state."""
+        torch = _torch()
+        logits = self.logits(X)
+        if u is None:
+            gen = torch.Generator(device=logits.device).manual_seed(int(self.random_state or 0))
+            u = torch.rand(logits.shape[0], generator=gen, device=logits.device)
+        return gmm_sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+
     def log_proba(self, X, y):
         """log p(y_i | x_i) of every row (0 where the label is negative), (N,) float32."""
         X = self._check(X, y)
-        if not hasattr(self, "coef_"):
-            raise RuntimeError("call fit first")
-        return -gmm_softmax_xent(X, self.coef_.to(X.dtype), y.contiguous(), bias=self.intercept_)[0]
+        self._ready()
+        return -gmm_softmax_xent(self._rows(X), self.coef_.to(X.dtype), y.contiguous(), bias=self.intercept_)[0]
 
     def score(self, X, y):
         """The mean log p(y_i | x_i) of the labelled rows, on the host."""
