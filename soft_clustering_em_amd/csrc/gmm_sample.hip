@@ -10,7 +10,7 @@
 // 2^-(S+1) a weight.
 //
 // A row is cut where k elements, or top_p of the mass, are reached by bins of
-// its distance to the maximum (1 / 64 of a temperature's unit each): one pass
+// its distance to the maximum (1 / 32 of a temperature's unit each): one pass
 // finds the maximum, one fills the bins (counts under top-k, sums of weights
 // under top-p, by integer atomics in LDS), one collects the elements of the bin
 // that the cut falls into and those above it; few enough, they are sorted and
@@ -32,7 +32,7 @@ namespace {
 typedef unsigned long long u64;
 constexpr int kBins = 2048, kSegs = 256, kList = 2048;
 constexpr int kFewKept = 256;  // top-p: so few elements down to the cut are sorted, more are passed over once more
-constexpr float kBinsPerUnit = 64.f;
+constexpr double kBinsPerUnit = 32.0;
 
 // Logits in the order of their values, from 1 up.
 __device__ inline uint32_t key_of(float l) {
@@ -48,11 +48,30 @@ struct Row {
   int64_t V;
   float mx;
   uint32_t first;  // the lowest index of the maximum
-  double inv, S;   // 1 / temperature, 2^S
+  double scale, S; // kBinsPerUnit / temperature, 2^S
   double least;    // min-p
-  float bins;      // bins a unit of logits
-  __device__ double z(float l) const { return ((double)l - (double)mx) * inv; }
-  __device__ double share(float l) const { return exp_neg(z(l)); }
+  float bins;      // scale, at most FLT_MAX
+  // The distance to the maximum in bins, y >= 0.  exp((l - max) / T) = exp(-b / 32)
+  // exp(-t / 32) with b = y rounded and |t| <= 1/2: the first factor is one of
+  // kBins values, 0 from there on (2^-92 is below half of any 2^-S), the second
+  // its series to t^6 (off by 2^-54).  Descending logits have ascending bins.
+  __device__ double distance(float l) const { return ((double)mx - (double)l) * scale; }
+  __device__ int bin(float l) const { return (int)fmin(rint(distance(l)), (double)(kBins - 1)); }
+  static __device__ double near(double t) {
+    t *= -1.0 / kBinsPerUnit;
+    double q = 1.0 / 720.0;
+    q = fma(q, t, 1.0 / 120.0);
+    q = fma(q, t, 1.0 / 24.0);
+    q = fma(q, t, 1.0 / 6.0);
+    q = fma(q, t, 0.5);
+    q = fma(q, t, 1.0);
+    return fma(q, t, 1.0);
+  }
+  static __device__ double far(double b) { return exp_neg(b * (-1.0 / kBinsPerUnit)); }
+  __device__ double share(float l) const {
+    const double y = distance(l), b = rint(y);
+    return b < (double)kBins ? far(b) * near(y - b) : 0.0;
+  }
   // e 2^S rounded to an integer: at most 2^52, the low bits of its sum with 2^52
   __device__ u64 fixed(double e) const {
     return (u64)__double_as_longlong(e * S + 0x1p52) - (u64)__double_as_longlong(0x1p52);
@@ -62,8 +81,6 @@ struct Row {
     const double e = share(l);
     return e >= least ? fixed(e) : 0;
   }
-  // descending logits have ascending bins
-  __device__ int bin(float l) const { return (int)fminf((mx - l) * bins, (float)(kBins - 1)); }
 };
 
 // U pieces of 16 bytes, `step` elements apart from i on, without a branch: those
@@ -187,9 +204,9 @@ __device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row<
   q.k = A.row_top_k ? A.row_top_k[r] : A.top_k;
   q.top_p = A.row_top_p ? (double)A.row_top_p[r] : A.top_p;
   q.mode = !best ? kNone : !(t > 0.0) || q.k == 1 ? kGreedy : q.k > 0 && q.k < A.V ? kCount : q.top_p < 1.0 ? kMass : kOpen;
-  R.inv = t > 0.0 ? fmin(1.0 / t, 1e300) : 1.0;
+  R.scale = t > 0.0 ? fmin(kBinsPerUnit / t, 1e300) : 1.0;
   R.least = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
-  R.bins = (float)fmin((double)kBinsPerUnit * R.inv, (double)FLT_MAX);
+  R.bins = (float)fmin(R.scale, (double)FLT_MAX);
   return q;
 }
 
@@ -231,12 +248,22 @@ __device__ inline u64 best_of(const Row<T>& R, int64_t i0, int64_t i1, int threa
   }
   return top > -INFINITY ? (u64)key_of(top) << 32 | (uint32_t)~index : 0;
 }
+// factor: exp(-b / 32) of every bin, for the weights
 template <typename T>
-__device__ inline void fill_bins(const Row<T>& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin) {
-  if (mode == kCount)
+__device__ inline void fill_bins(const Row<T>& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin,
+                                 double* factor) {
+  if (mode == kCount) {
     each<4>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
-  else
-    each<2>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], R.weight(l)); });
+    return;
+  }
+  for (int b = thread; b < kBins; b += threads) factor[b] = R.far((double)b);
+  __syncthreads();
+  each<2>(R, i0, i1, thread, threads, [&](int64_t, float l) {
+    const double y = R.distance(l), b = rint(y);
+    const int at = (int)fmin(b, (double)(kBins - 1));
+    const u64 w = R.fixed(factor[at] * R.near(y - b));
+    atomicAdd(&bin[at], b < (double)kBins ? w : 0);
+  });
 }
 
 // sh.at: the bin at which the count or the mass reaches its target (the last one
@@ -282,7 +309,8 @@ template <typename T>
 __device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
   constexpr int E = 16 / (int)sizeof(T), U = 4;
   const int at = sh.at;
-  const float end = at == kBins - 1 ? __builtin_nanf("") : (float)(at + 1);
+  // the float32 distance is off by less than 2^-22 of itself
+  const float end = at == kBins - 1 ? __builtin_nanf("") : ((float)at + 0.5f) * (1.f + 0x1p-20f);
   const auto add = [&](int64_t i, float v) {
     if (!(v > -INFINITY)) return;
     const float l = fminf(v, FLT_MAX);
@@ -353,7 +381,7 @@ __device__ inline float list_logit(u64 v) { return logit_of((uint32_t)(v >> 32))
 template <typename T>
 __device__ inline void answer(const SampleArgs& A, const Row<T>& R, int64_t r, float l, int64_t i, u64 total) {
   A.tokens[r] = (int32_t)i;
-  if (A.logp) A.logp[r] = (float)(R.z(l) - log((double)total / R.S));
+  if (A.logp) A.logp[r] = (float)(-R.distance(l) / kBinsPerUnit - log((double)total / R.S));
 }
 __device__ inline double aim(const SampleArgs& A, int64_t r, u64 total) {
   return (double)fminf(fmaxf(A.u[r], 0.f), 0x1.fffffep-1f) * (double)total;
@@ -765,7 +793,7 @@ __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
     for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
     if (threadIdx.x == 0) sh.na = sh.nb = 0;
     __syncthreads();
-    fill_bins(R, q.mode, 0, R.V, threadIdx.x, TH, sh.bin);
+    fill_bins(R, q.mode, 0, R.V, threadIdx.x, TH, sh.bin, reinterpret_cast<double*>(sh.sum));
     __syncthreads();
     const u64 whole = cut_bin<TH>(q, sh, sh.bin);
     collect(R, sh, 0, R.V, threadIdx.x, TH);
@@ -839,9 +867,11 @@ template <typename T>
 __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   constexpr int TH = 256;
   __shared__ u64 bin[kBins];
+  __shared__ double factor[kBins];
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
   Row<T> R;
+  for (int i = threadIdx.x; i < kBins; i += TH) bin[i] = 0;
   const Settings q = row_of(A, r, best_part(w, gridDim.x), R);
   if (q.mode == kNone || q.mode == kGreedy) return;
   int64_t i0, i1;
@@ -854,9 +884,8 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
     if ((threadIdx.x & 63) == 0) w.mass[blockIdx.x * kQuarters + (threadIdx.x >> 6)] = mass;
     return;
   }
-  for (int i = threadIdx.x; i < kBins; i += TH) bin[i] = 0;
   __syncthreads();
-  fill_bins(R, q.mode, i0, i1, threadIdx.x, TH, bin);
+  fill_bins(R, q.mode, i0, i1, threadIdx.x, TH, bin, factor);
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += TH)
     if (bin[i]) atomicAdd((u64*)&w.bin[i], bin[i]);
@@ -925,6 +954,10 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
   __shared__ Shared sh;
   const int64_t r = (int64_t)blockIdx.x + A.r0;
   SampleRow& w = A.rows[blockIdx.x];
+  // what the row may need, on its way while its maximum is found
+  const int na = w.na, nb = w.nb;
+  const u64 whole = w.whole, above = w.above, mass = threadIdx.x < parts * kQuarters ? w.mass[threadIdx.x] : 0;
+  const u64 front = w.list[threadIdx.x], back = w.list[2 * kSampleList - 1 - threadIdx.x];
   Row<T> R;
   const Settings q = row_of(A, r, best_part(w, parts), R);
   if (plain_answer(A, R, q, r)) return;
@@ -932,7 +965,6 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
   int64_t i0 = 0, i1 = A.V;
   u64 before = 0, total = 0;
   double goal = -1.0;
-  const int na = w.na, nb = w.nb;
   const bool list = na <= kSampleList && nb <= kSampleList && na + nb <= (q.mode == kCount ? kList : kFewKept);
   if (q.mode != kOpen && !list && (q.mode == kCount || nb > kList)) {
     cut = cut_by_reach<TH>(R, q, sh);
@@ -941,21 +973,21 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
     const int s = threadIdx.x;
     const int64_t quarter = A.part / kQuarters;
     if (s < kSegs) {
-      sh.seg[s] = s < parts * kQuarters ? w.mass[s] : 0;
+      sh.seg[s] = mass;
       sh.tie[s] = 0;
     }
     u64 wt = 0;
     if (q.mode != kOpen) {
       const int to = list ? na : 0;
-      for (int i = threadIdx.x; i < to; i += TH) sh.list[i] = w.list[i];
-      for (int i = threadIdx.x; i < nb; i += TH) sh.list[to + i] = w.list[2 * kSampleList - 1 - i];
-      if (threadIdx.x == 0) sh.above = w.above;
+      for (int i = threadIdx.x; i < to; i += TH) sh.list[i] = i < TH ? front : w.list[i];
+      for (int i = threadIdx.x; i < nb; i += TH) sh.list[to + i] = i < TH ? back : w.list[2 * kSampleList - 1 - i];
+      if (threadIdx.x == 0) sh.above = above;
       __syncthreads();
       if (list) {
-        finish_list<TH>(A, R, q, r, sh, na + nb, w.whole);
+        finish_list<TH>(A, R, q, r, sh, na + nb, whole);
         return;
       }
-      cut = cut_of_bin<TH>(R, q, sh, w.whole, nb);
+      cut = cut_of_bin<TH>(R, q, sh, whole, nb);
       // what the quarters keep of the bin: all above the cut, and the ties by index
       for (int i = threadIdx.x; i < nb; i += TH) {
         if (sh.list[i] < sh.edge) continue;
