@@ -240,7 +240,7 @@ __device__ inline int not_below(float v) {
 }
 
 template <typename T, int L, int EPL>
-__global__ void __launch_bounds__(256) route_kernel(RouteArgs A) {
+__global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_kernel(RouteArgs A) {
   constexpr int RPW = 64 / L, EXACT = L * EPL > 64 ? L * EPL / 64 : 1;
   extern __shared__ double lds[];  // a wave: RPW rows of `room` doubles
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sub = lane % L, row = lane / L;

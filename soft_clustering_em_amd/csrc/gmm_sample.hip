@@ -248,22 +248,39 @@ __device__ inline u64 best_of(const Row<T>& R, int64_t i0, int64_t i1, int threa
   }
   return top > -INFINITY ? (u64)key_of(top) << 32 | (uint32_t)~index : 0;
 }
-// factor: exp(-b / 32) of every bin, for the weights
+// The bins' counts or weights; of an open row the sum of what it keeps, in this
+// thread, instead.  factor: exp(-b / 32) of every bin.
 template <typename T>
-__device__ inline void fill_bins(const Row<T>& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin,
-                                 double* factor) {
+__device__ inline u64 fill_bins(const Row<T>& R, Mode mode, int64_t i0, int64_t i1, int thread, int threads, u64* bin,
+                                const double* factor) {
+  u64 sum = 0;
   if (mode == kCount) {
-    each<4>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
-    return;
+    each<2>(R, i0, i1, thread, threads, [&](int64_t, float l) { atomicAdd(&bin[R.bin(l)], (u64)1); });
+    return 0;
   }
-  for (int b = thread; b < kBins; b += threads) factor[b] = R.far((double)b);
-  __syncthreads();
-  each<2>(R, i0, i1, thread, threads, [&](int64_t, float l) {
+  const auto share = [&](float l, int& at) {
     const double y = R.distance(l), b = rint(y);
-    const int at = (int)fmin(b, (double)(kBins - 1));
-    const u64 w = R.fixed(factor[at] * R.near(y - b));
-    atomicAdd(&bin[at], b < (double)kBins ? w : 0);
-  });
+    at = (int)fmin(b, (double)(kBins - 1));
+    return b < (double)kBins ? factor[at] * R.near(y - b) : 0.0;
+  };
+  int at;
+  if (mode == kMass) {
+    each<2>(R, i0, i1, thread, threads, [&](int64_t, float l) {
+      const double e = share(l, at);
+      atomicAdd(&bin[at], R.fixed(e));
+    });
+  } else {
+    each<1>(R, i0, i1, thread, threads, [&](int64_t, float l) {
+      const double e = share(l, at);
+      sum += e >= R.least ? R.fixed(e) : 0;
+    });
+  }
+  return sum;
+}
+template <typename T>
+__device__ inline void fill_factors(const Row<T>& R, int thread, int threads, double* factor) {
+#pragma unroll 1
+  for (int b = thread; b < kBins; b += threads) factor[b] = R.far((double)b);
 }
 
 // sh.at: the bin at which the count or the mass reaches its target (the last one
@@ -403,35 +420,45 @@ __device__ inline void group_sync() {
 }
 
 // finish_list for n <= kFewKept: places and sums by comparing each element with
-// every other one, a thread an element (one wave, without barriers, where n <= 64).
+// every other one, G threads an element (one wave, without barriers, for n <= 64).
 template <int TH, typename T>
-__device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R, const Settings& q, int64_t r, Shared& sh, int n, u64 mass) {
-  const int i = threadIdx.x;
+__device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R, const Settings& q, int64_t r, Shared& sh, int n,
+                                           u64 mass) {
+  constexpr int G = TH / kFewKept > 0 ? TH / kFewKept : 1;
+  const int i = threadIdx.x / G, g = threadIdx.x % G;
+  const bool own = i < n && g == 0;
   const u64 mine = i < n ? sh.list[i] : 0;
   const double e = i < n ? R.share(list_logit(mine)) : 0.0;
   const u64 w = i < n ? R.fixed(e) : 0;
-  if (i < n) sh.sum[i] = w;
+  if (own) sh.sum[i] = w;
   group_sync<TH>();
   int place = 0;
   u64 before = 0;
-  const int others = (i & ~63) < n ? n : 0;  // waves without an element have nothing to compare
+  const int others = (threadIdx.x & ~63) / G < n ? n : 0;  // waves without an element have nothing to compare
 #pragma unroll 4
-  for (int j = 0; j < others; ++j) {
+  for (int j = g; j < others; j += G) {
     const bool ahead = sh.list[j] > mine;
     place += ahead;
     before += ahead ? sh.sum[j] : 0;
   }
+#pragma unroll
+  for (int o = 1; o < G; o *= 2) {
+    place += __shfl_xor(place, o);
+    before += __shfl_xor(before, o);
+  }
   const bool first = q.mode != kCount || place < q.k;
-  if (q.mode == kCount && q.top_p < 1.0) mass = group_sum<TH>(first ? w : 0, sh.red);
-  const bool in = i < n && (place == 0 || (first && (!(q.top_p < 1.0) || (double)before < q.top_p * (double)mass) && e >= R.least));
+  if (q.mode == kCount && q.top_p < 1.0) mass = group_sum<TH>(own && first ? w : 0, sh.red);
+  const bool in = own && (place == 0 || (first && (!(q.top_p < 1.0) || (double)before < q.top_p * (double)mass) && e >= R.least));
   const u64 total = group_sum<TH>(in ? w : 0, sh.red);
   const double goal = aim(A, r, total);
   group_sync<TH>();
-  if (i < n) sh.sum[i] = in ? w : 0;
+  if (own) sh.sum[i] = in ? w : 0;
   group_sync<TH>();
   u64 to = 0;
 #pragma unroll 4
-  for (int j = 0; j < others; ++j) to += (uint32_t)sh.list[j] >= (uint32_t)mine ? sh.sum[j] : 0;  // ~index: descending
+  for (int j = g; j < others; j += G) to += (uint32_t)sh.list[j] >= (uint32_t)mine ? sh.sum[j] : 0;  // ~index: descending
+#pragma unroll
+  for (int o = 1; o < G; o *= 2) to += __shfl_xor(to, o);
   if (in && (double)to > goal && !((double)(to - w) > goal)) answer(A, R, r, list_logit(mine), ~(uint32_t)mine, total);
 }
 
@@ -542,13 +569,26 @@ __device__ inline u64 whole_list(const Shared& sh, u64 wt, u64 left) {
   return wave_sum_u64(n) + min(wave_sum_u64(ties), left) * wt;
 }
 
+// The least logit that a cut may keep.
+__device__ inline float least_kept(const Cut& cut) { return cut.ties ? cut.l : nextafterf(cut.l, INFINITY); }
+
+// Bit e: element e of the piece at i may be kept; pieces that are not whole below
+// b are looked at one by one.
+template <typename T>
+__device__ inline uint32_t marks(const T (&v)[16 / sizeof(T)], float least) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 16 / (int)sizeof(T); ++e) m |= (float)v[e] >= least ? 1u << e : 0u;
+  return m;
+}
+
 // Kept weights and elements equal to the cut of the segments of `len` elements;
-// a wave reads two of them at once.
+// a wave reads two of them at once, and opens the marked elements after.
 template <int TH, typename T>
 __device__ inline void segments(const Row<T>& R, const Cut& cut, int64_t i0, int64_t i1, int64_t len, Shared& sh) {
   constexpr int E = 16 / (int)sizeof(T), U = 2;
-  const T* p = R.p;
   const int lane = threadIdx.x & 63;
+  const float least = least_kept(cut);
   const int64_t whole = i0 + (i1 - i0) / E * E;
   const int used = (int)((i1 - i0 + len - 1) / len);
   for (int s = used + threadIdx.x; s < kSegs; s += TH) {
@@ -556,47 +596,44 @@ __device__ inline void segments(const Row<T>& R, const Cut& cut, int64_t i0, int
     sh.tie[s] = 0;
   }
   for (int s = (threadIdx.x >> 6) * U; s < used; s += TH / 64 * U) {
-    u64 mass[U] = {}, ties[U] = {};
-    const auto one = [&](int u, float v) {
+    u64 mass0 = 0, mass1 = 0;
+    uint32_t ties0 = 0, ties1 = 0;
+    const auto one = [&](bool second, float v) {
+      if (!(v >= least)) return;
       const float l = fminf(v, FLT_MAX);
-      if (!(v > -INFINITY)) return;
-      if (l > cut.l) mass[u] += R.weight_min_p(l);
-      ties[u] += l == cut.l;
+      const u64 w = l > cut.l ? R.weight_min_p(l) : 0;
+      const uint32_t t = l == cut.l;
+      (second ? mass1 : mass0) += w;
+      (second ? ties1 : ties0) += t;
     };
     for (int64_t t = 0; t < len && i0 + s * len + t < whole; t += 64 * E) {
       const int64_t i = i0 + s * len + t + lane * E;
       T v[U][E];
-      load_pieces<T, U>(v, p, i, len, whole);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u * len >= whole) break;
-#pragma unroll
-        for (int e = 0; e < E; ++e) one(u, (float)v[u][e]);
+      load_pieces<T, U>(v, R.p, i, len, whole);
+      uint32_t marked = i < whole ? marks<T>(v[0], least) : 0;
+      if (i + len < whole) marked |= marks<T>(v[1], least) << E;
+#pragma unroll 1
+      while (marked) {
+        const int k = __builtin_ctz(marked);
+        marked &= marked - 1;
+        one(k >= E, (float)R.p[i + k / E * len + k % E]);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // the last elements, less than a piece, belong to the segment that they lie in
-      const int64_t a = i0 + (s + u) * len;
-      if (whole + lane < i1 && lane < E && whole >= a && whole < a + len) one(u, (float)p[whole + lane]);
-      if (s + u >= used) break;
-      mass[u] = wave_sum_u64(mass[u]);
-      ties[u] = wave_sum_u64(ties[u]);
-      if (lane == 0) {
-        sh.seg[s + u] = mass[u];
-        sh.tie[s + u] = (uint32_t)ties[u];
+    // the last elements, less than a piece, belong to the segment that they lie in
+    const int64_t a = i0 + s * len;
+    if (whole + lane < i1 && lane < E && whole >= a && whole < a + U * len)
+      one(whole >= a + len, (float)R.p[whole + lane]);
+    mass0 = wave_sum_u64(mass0);
+    mass1 = wave_sum_u64(mass1);
+    const u64 ties = wave_sum_u64((u64)ties1 << 32 | ties0);
+    if (lane == 0) {
+      sh.seg[s] = mass0;
+      sh.tie[s] = (uint32_t)ties;
+      if (s + 1 < used) {
+        sh.seg[s + 1] = mass1;
+        sh.tie[s + 1] = (uint32_t)(ties >> 32);
       }
     }
-  }
-}
-
-// f(index, logit) for the live ones of the piece from i on, below b, in order
-template <typename T, typename F>
-__device__ inline void own_piece(const Row<T>& R, int64_t i, int64_t b, F f) {
-#pragma unroll
-  for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
-    const float v = i + e < b ? (float)R.p[i + e] : -INFINITY;
-    if (v > -INFINITY) f(i + e, fminf(v, FLT_MAX));
   }
 }
 
@@ -620,35 +657,49 @@ __device__ __forceinline__ void choose(const SampleArgs& A, const Row<T>& R, con
   }
   u64 left = cut.ties;
   const int s = pass_list<kSegs / 64>(sh, wt, goal, before, left);
+  const float least = least_kept(cut);
   for (int64_t a = i0 + s * len, end = min(a + len, i1); a < end; a += tile) {
-    const int64_t b = min(a + tile, end);
-    u64 mass = 0, tied = 0;
-    own_piece(R, a + (int64_t)lane * E, b, [&](int64_t, float l) {
-      if (l > cut.l) mass += R.weight_min_p(l);
-      tied += l == cut.l;
-    });
-    const u64 tied_to = wave_scan_u64(tied), tied_from = tied_to - tied;
-    mass += (min(tied_to, left) - min(tied_from, left)) * wt;
-    const u64 to = before + wave_scan_u64(mass);
-    const u64 hit = __ballot((double)to > goal);
-    if (hit) {
-      if (lane == __builtin_ctzll(hit)) {
-        u64 sum = to - mass, rank = tied_from;
-        bool found = false;
-        own_piece(R, a + (int64_t)lane * E, b, [&](int64_t i, float l) {
-          if (found) return;
-          if (l > cut.l) sum += R.weight_min_p(l);
-          else if (l == cut.l && rank++ < left) sum += wt;
+    const int64_t i = a + (int64_t)lane * E;
+    uint32_t marked = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (i + e < end && (float)R.p[i + e] >= least) marked |= 1u << e;
+    // twice over the lane's kept elements: their sum, then the one that passes
+    u64 mass = 0, tied = 0, rank = 0, sum = 0;
+    bool last = false;
+    for (;;) {
+#pragma unroll 1
+      for (uint32_t m = marked; m; m &= m - 1) {
+        const int64_t at = i + __builtin_ctz(m);
+        const float l = fminf((float)R.p[at], FLT_MAX);
+        const bool tie = l == cut.l;
+        if (!last) {
+          tied += tie;
+          if (!tie) mass += R.weight_min_p(l);
+        } else {
+          if (!tie) sum += R.weight_min_p(l);
+          else if (rank++ < left) sum += wt;
           if ((double)sum > goal) {
-            found = true;
-            answer(A, R, r, l, i, total);
+            answer(A, R, r, l, at, total);
+            return;
           }
-        });
+        }
       }
-      return;
+      if (last) return;
+      const u64 tied_to = wave_scan_u64(tied), tied_from = tied_to - tied;
+      mass += (min(tied_to, left) - min(tied_from, left)) * wt;
+      const u64 to = before + wave_scan_u64(mass);
+      const u64 hit = __ballot((double)to > goal);
+      if (!hit) {
+        before = __shfl(to, 63);
+        left -= min(__shfl(tied_to, 63), left);
+        break;
+      }
+      if (lane != __builtin_ctzll(hit)) return;
+      last = true;
+      sum = to - mass;
+      rank = tied_from;
     }
-    before = __shfl(to, 63);
-    left -= min(__shfl(tied_to, 63), left);
   }
 }
 
@@ -735,22 +786,29 @@ __device__ __forceinline__ Cut cut_of_bin(const Row<T>& R, const Settings& q, Sh
   const u64 above = sh.above;
   const double target = q.top_p * (double)whole;
   if (nb <= kFewKept) {
-    const int i = threadIdx.x;
+    constexpr int G = TH / kFewKept;
+    const int i = threadIdx.x / G, g = threadIdx.x % G;
     const u64 mine = i < nb ? sh.list[i] : 0, w = i < nb ? R.weight(list_logit(mine)) : 0;
-    if (i < nb) sh.sum[i] = w;
+    if (i < nb && g == 0) sh.sum[i] = w;
     __syncthreads();
-    u64 before = above, same = 0, place = 0;
-    const int others = (i & ~63) < nb ? nb : 0;
+    u64 before = 0, same = 0, place = 0;
+    const int others = (threadIdx.x & ~63) / G < nb ? nb : 0;
 #pragma unroll 4
-    for (int j = 0; j < others; ++j) {
+    for (int j = g; j < others; j += G) {
       const u64 other = sh.list[j];
-      if (other > mine) {
-        before += sh.sum[j];
-        ++place;
-        same += other >> 32 == mine >> 32;
-      }
+      const bool ahead = other > mine;
+      before += ahead ? sh.sum[j] : 0;
+      place += ahead;
+      same += ahead && other >> 32 == mine >> 32;
     }
-    if (i < nb && (double)(before + w) >= target && (place == 0 || (double)before < target)) {
+#pragma unroll
+    for (int o = 1; o < G; o *= 2) {
+      before += __shfl_xor(before, o);
+      place += __shfl_xor(place, o);
+      same += __shfl_xor(same, o);
+    }
+    before += above;
+    if (i < nb && g == 0 && (double)(before + w) >= target && (place == 0 || (double)before < target)) {
       sh.edge = mine;
       sh.above = same + 1;
     }
@@ -792,8 +850,10 @@ __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
   if (q.mode != kOpen) {
     for (int i = threadIdx.x; i < kBins; i += TH) sh.bin[i] = 0;
     if (threadIdx.x == 0) sh.na = sh.nb = 0;
+    double* factor = reinterpret_cast<double*>(sh.sum);
+    if (q.mode == kMass) fill_factors(R, threadIdx.x, TH, factor);
     __syncthreads();
-    fill_bins(R, q.mode, 0, R.V, threadIdx.x, TH, sh.bin, reinterpret_cast<double*>(sh.sum));
+    fill_bins(R, q.mode, 0, R.V, threadIdx.x, TH, sh.bin, factor);
     __syncthreads();
     const u64 whole = cut_bin<TH>(q, sh, sh.bin);
     collect(R, sh, 0, R.V, threadIdx.x, TH);
@@ -876,16 +936,16 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   if (q.mode == kNone || q.mode == kGreedy) return;
   int64_t i0, i1;
   part_of(A, i0, i1);
-  if (q.mode == kOpen) {
-    u64 mass = 0;
-    quarter_of(A, i0, i1);
-    each<2>(R, i0, i1, threadIdx.x & 63, 64, [&](int64_t, float l) { mass += R.weight_min_p(l); });
-    mass = wave_sum_u64(mass);
+  if (q.mode != kCount) fill_factors(R, threadIdx.x, TH, factor);
+  __syncthreads();
+  const bool open = q.mode == kOpen;  // its waves take a quarter each
+  if (open) quarter_of(A, i0, i1);
+  const u64 mass = wave_sum_u64(
+      fill_bins(R, q.mode, i0, i1, open ? threadIdx.x & 63 : threadIdx.x, open ? 64 : TH, bin, factor));
+  if (open) {
     if ((threadIdx.x & 63) == 0) w.mass[blockIdx.x * kQuarters + (threadIdx.x >> 6)] = mass;
     return;
   }
-  __syncthreads();
-  fill_bins(R, q.mode, i0, i1, threadIdx.x, TH, bin, factor);
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += TH)
     if (bin[i]) atomicAdd((u64*)&w.bin[i], bin[i]);
