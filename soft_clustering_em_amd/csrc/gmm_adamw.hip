@@ -23,6 +23,7 @@ namespace gmm {
 
 namespace {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kEach = 8;  // elements a thread: a state block of 256 is half a wave
 
 __device__ inline uint32_t mix32(uint32_t x) {
@@ -50,7 +51,15 @@ __device__ inline void store_each(T* p, const float (&f)[kEach], int n) {
 #pragma unroll
   for (int e = 0; e < kEach; ++e) v[e] = (T)f[e];
   if (n >= kEach) {
-    __builtin_memcpy(p, v, sizeof(v));
+    constexpr int Q = (int)sizeof(v) / 16;
+    u32x4 q[Q];
+    __builtin_memcpy(q, v, sizeof(v));
+    if ((uintptr_t)p % 16 == 0) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k) __builtin_nontemporal_store(q[k], reinterpret_cast<u32x4*>(p) + k);
+    } else {
+      __builtin_memcpy(p, v, sizeof(v));
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < kEach; ++e)

@@ -387,6 +387,7 @@ struct NormArgs {
   float eps;
   int dtype, accumulate;
   bool affine_t;           // gamma and beta in the rows' type (else float32)
+  bool stream;             // rows stored past the caches
 };
 struct NormPlan {
   int tpr, c;              // threads a row, 16-byte pieces a thread
@@ -395,7 +396,7 @@ struct NormPlan {
   size_t bytes;
 };
 NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums);
-hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm(NormArgs a, hipStream_t s);
 hipError_t launch_norm_grad(NormArgs a, const NormPlan& p, float* dgamma, float* dbeta, hipStream_t s);
 
 // routing (gmm_route.hip)

@@ -71,10 +71,13 @@ __device__ inline void load_row(u32x4 (&v)[C], const T* row, int t, int64_t D, b
   }
 }
 
+// stream: past the caches
 template <typename T>
-__device__ inline void store_piece(T* row, const T (&v)[kPer<T>], int64_t c0, int64_t D) {
+__device__ inline void store_piece(T* row, const T (&v)[kPer<T>], int64_t c0, int64_t D, bool stream) {
   if (c0 + kPer<T> <= D) {
-    __builtin_memcpy(row + c0, v, 16);
+    if (stream && (uintptr_t)(row + c0) % 16 == 0)
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(row + c0));
+    else __builtin_memcpy(row + c0, v, 16);
   } else {
 #pragma unroll
     for (int e = 0; e < kPer<T>; ++e)
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs A)
     T o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = (T)(((element<T>(v[j], e) - m1) - m2) * rs * g[e] + b[e]);
-    store_piece<T>(out, o, c0, A.D);
+    store_piece<T>(out, o, c0, A.D, A.stream);
   }
 }
 
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_grad_kernel(NormAr
         const float d = rstd * (element<T>(vy[j], e) * f[e] - ma - xh * mb);
         o[e] = (T)(A.accumulate ? (float)o[e] + d : d);
       }
-      store_piece<T>(dx, o, c0, A.D);
+      store_piece<T>(dx, o, c0, A.D, A.stream);
     }
   }
   if constexpr (ACC) {
@@ -419,7 +422,13 @@ static void norm_shape(int64_t pieces, int most, int* tpr, int* c) {
   *c = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
 }
 
-hipError_t launch_norm(const NormArgs& A, hipStream_t s) {
+// Rows beyond the 32 MB of the eight L2 caches are stored past them: 32768 x 2048
+// bf16 forward 80 -> 55 us, with the gradients 168 -> 147.  Fewer stay for the next
+// reader.
+static bool norm_streams(const NormArgs& A) { return A.R * A.D * (A.dtype == 0 ? 4 : 2) > (int64_t)32 << 20; }
+
+hipError_t launch_norm(NormArgs A, hipStream_t s) {
+  A.stream = norm_streams(A);
   return by_type(A.dtype, [&](auto zero) {
     using T = decltype(zero);
     int tpr, c;
@@ -454,6 +463,7 @@ NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums) {
 
 hipError_t launch_norm_grad(NormArgs A, const NormPlan& p, float* dgamma, float* dbeta, hipStream_t s) {
   const bool sums = dgamma || dbeta, acc = sums && !p.wide;
+  A.stream = norm_streams(A);
   if (A.dx || acc) {
     const hipError_t e = by_type(A.dtype, [&](auto zero) {
       using T = decltype(zero);
