@@ -863,16 +863,16 @@ def gmm_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1
     decays = array("q", array("d", map(float, decay)).tobytes())
     used = []
     for i, (p, g, a, b, sa, sb, c) in enumerate(zip(params, grads, m, v, m_scale, v_scale, copies)):
-        code, gcode, n, shape = codes.get(p.dtype), codes.get(g.dtype), p.numel(), p.shape
-        if code is None or gcode is None or g.shape != shape or not (p.is_contiguous() and g.is_contiguous()):
+        code, gcode, n = codes.get(p.dtype), codes.get(g.dtype), p.numel()
+        if code is None or gcode is None or g.shape != p.shape or not (p.is_contiguous() and g.is_contiguous()):
             raise ValueError(f"parameter {i} and its gradient must be contiguous float32, bfloat16 or float16 tensors "
                              "of one shape")
         if (sa is None) != (sb is None):
             raise ValueError(f"state {i} has one scale of two")
         kinds = full if sa is None else coded
         for t in (a, b):
-            if t.dtype not in kinds or t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"states {i} must be contiguous {kinds[0]} tensors of the parameter's shape")
+            if t.dtype not in kinds or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"states {i} must be contiguous {kinds[0]} tensors of the parameter's size")
         used += (p, g, a, b)
         if sa is not None:
             blocks = (-(-n // ADAMW_BLOCK),)
@@ -882,9 +882,9 @@ def gmm_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1
         ccode = 0
         if c is not None:
             ccode = codes.get(c.dtype)
-            if ccode is None or c.shape != shape or not c.is_contiguous():
+            if ccode is None or c.numel() != n or not c.is_contiguous():
                 raise ValueError(f"copy {i} must be a contiguous float32, bfloat16 or float16 tensor of the parameter's "
-                                 "shape")
+                                 "size")
             used.append(c)
         desc.extend((p.data_ptr(), g.data_ptr(), a.data_ptr(), b.data_ptr(), 0 if sa is None else sa.data_ptr(),
                      0 if sb is None else sb.data_ptr(), 0 if c is None else c.data_ptr(), n, decays[i],

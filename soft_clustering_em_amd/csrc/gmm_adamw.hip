@@ -87,9 +87,8 @@ __device__ inline void load_codes(float (&f)[kEach], const uint8_t* p, int n, fl
   }
 }
 
-// the largest of 32 lanes' values, NaN among them kept
-__device__ inline float half_wave_max(float v) {
-  const bool bad = v != v;
+// the largest of 32 lanes' values; NaN if a lane is `bad`
+__device__ inline float half_wave_max(float v, bool bad) {
   v = row16_max(v);
   auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
@@ -103,28 +102,34 @@ __device__ inline float half_wave_max(float v) {
 template <bool ROOT>
 __device__ inline void store_codes(uint8_t* p, float* scale, const float (&f)[kEach], const uint32_t (&h)[kEach], int n) {
 #pragma clang fp contract(off)
-  float top = 0.f;
+  float top = 0.f, zero = 0.f;  // elements behind the last one are 0
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const float a = e < n ? fabsf(f[e]) : 0.f;
-    top = a > top || a != a ? a : top;
+    top = fmaxf(top, fabsf(f[e]));
+    zero = fmaf(f[e], 0.f, zero);  // NaN from NaN and infinities
   }
-  top = half_wave_max(top);
+  top = half_wave_max(top, zero != zero);
   const bool none = top < 0x1p-100f;  // 1 / top times 448 would leave float32
   const float s = none ? 0.f : top * (1.f / 448.f), inv = none ? 0.f : 1.f / top * 448.f;
-  uint8_t b[kEach];
+  uint32_t c[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const float x = f[e] * inv, a = fminf(fabsf(x), 448.f);
     const uint32_t d = ROOT ? h[e] & 0xffff : h[e] >> 16;
-    // from 2^-6 on 3 of the 23 mantissa bits stay; below, steps of 2^-9
-    uint32_t c = a < 0x1p-6f ? (uint32_t)(a * 512.f + (float)d * 0x1p-16f)
-                             : ((__float_as_uint(a) + (d << 4)) >> 20) - (120u << 3);
-    if (ROOT && x > 0.f && c == 0) c = 1;
-    if (!ROOT && x < 0.f && c != 0) c |= 0x80;
-    if (x != x) c = 0x7f;
-    b[e] = (uint8_t)c;
+    // from 2^-6 on 3 of the 23 mantissa bits stay; below, steps of 2^-9, which few
+    // waves have any of
+    c[e] = ((__float_as_uint(a) + (d << 4)) >> 20) - (120u << 3);
+    if (__ballot(a < 0x1p-6f)) {
+      asm volatile("");  // a branch, not work for every wave
+      c[e] = a < 0x1p-6f ? (uint32_t)(a * 512.f + (float)d * 0x1p-16f) : c[e];
+    }
+    if (ROOT) c[e] = max(c[e], min(__float_as_uint(a), 1u));
+    else c[e] |= c[e] ? __float_as_uint(x) >> 24 & 0x80 : 0;
   }
+  uint8_t b[kEach];
+  const bool bad = top != top;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) b[e] = bad ? 0x7f : (uint8_t)c[e];
   if (n >= kEach) {
     __builtin_memcpy(p, b, 8);
   } else {
@@ -144,7 +149,8 @@ template <typename P, typename G, bool BITS8>
 __device__ inline void adam_piece(const AdamTensor& t, int64_t i0, int64_t n, const Factors& F) {
 #pragma clang fp contract(off)
   // every lane of a wave takes part in the blocks' maxima
-  for (int64_t k = 0; k < n; k += 256 * kEach) {
+  static_assert(kAdamRound == 256 * kEach, "a round of the workgroup");
+  for (int64_t k = 0; k < n; k += kAdamRound) {
     const int64_t at = k + (int64_t)threadIdx.x * kEach, i = i0 + at;
     const int have = n - at >= kEach ? kEach : n - at > 0 ? (int)(n - at) : 0;
     if (!BITS8 && have == 0) return;
@@ -176,10 +182,10 @@ __device__ inline void adam_piece(const AdamTensor& t, int64_t i0, int64_t n, co
       else store_each<float>(static_cast<float*>(t.copy) + i, p, have);
     }
     if constexpr (BITS8) {
-      const uint32_t kb = mix32(F.key + (uint32_t)block);
+      const uint32_t kb = mix32(F.key + (uint32_t)block) + (uint32_t)(i % kAdamBlock) * 0x9E3779B1u;
       uint32_t h[kEach];
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) h[e] = mix32(kb + ((uint32_t)(i % kAdamBlock) + e) * 0x9E3779B1u);
+      for (int e = 0; e < kEach; ++e) h[e] = mix32(kb + (uint32_t)e * 0x9E3779B1u);
       store_codes<false>(static_cast<uint8_t*>(t.m) + i, t.ms + block, m, h, have);
       store_codes<true>(static_cast<uint8_t*>(t.v) + i, t.vs + block, v, h, have);
     } else {
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(AdamArgs A) {
       else hi = mid - 1;
     }
     const AdamTensor& t = A.t[lo];
-    const int64_t i0 = (q - t.piece0) * kAdamPiece, n = min(kAdamPiece, t.n - i0);
+    const int64_t i0 = (q - t.piece0) * A.piece, n = min(A.piece, t.n - i0);
     Factors F = shared;
     F.decay = (float)(1.0 - lr * t.weight_decay);
     F.key = mix32(F.key ^ (uint32_t)(A.first + lo));
@@ -252,10 +258,15 @@ hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs A, hipStream_t 
     A.first = i0;
     A.count = std::min(kAdamTensors, count - i0);
     A.pieces = 0;
+    // a workgroup's round is 2048 elements: one a piece as long as that fills the
+    // card, then four, with a quarter of the look-ups
+    int64_t total = 0;
+    for (int i = 0; i < A.count; ++i) total += t[i0 + i].n;
+    A.piece = total <= 2048 * kAdamRound ? kAdamRound : 4 * kAdamRound;
     for (int i = 0; i < A.count; ++i) {
       A.t[i] = t[i0 + i];
       A.t[i].piece0 = A.pieces;
-      A.pieces += (A.t[i].n + kAdamPiece - 1) / kAdamPiece;
+      A.pieces += (A.t[i].n + A.piece - 1) / A.piece;
     }
     if (A.pieces == 0) continue;
     hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)std::min<int64_t>(A.pieces, 1 << 13)), dim3(256), 0, s, A);

@@ -416,7 +416,7 @@ hipError_t launch_route(const RouteArgs& a, int dtype, bool grad, hipStream_t s)
 
 // AdamW (gmm_adamw.hip)
 constexpr int kAdamTensors = 32;      // tensors per launch (their descriptions are kernel arguments)
-constexpr int64_t kAdamPiece = 8192;  // elements per piece, a multiple of 2048
+constexpr int64_t kAdamRound = 2048;  // elements that a workgroup takes at once
 constexpr int kAdamBlock = 256;       // elements under one scale of an 8-bit state
 struct AdamTensor {
   void* p;
@@ -431,7 +431,7 @@ struct AdamTensor {
 struct AdamArgs {
   AdamTensor t[kAdamTensors];
   int count, first;
-  int64_t pieces, step;
+  int64_t piece, pieces, step;  // elements of a piece, pieces of the launch
   double lr, b1, b2, log_b1, log_b2, eps, max_norm;
   const float *norm, *lr_dev;
   const int64_t* step_dev;
