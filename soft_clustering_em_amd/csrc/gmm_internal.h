@@ -377,6 +377,8 @@ struct ClipArgs {
 hipError_t launch_clip(const ClipTensor* t, int count, double max_norm, float* norm, double* part, double* coef,
                        hipStream_t s);
 
+constexpr int64_t kLaunchThreads = (int64_t)1 << 31;  // threads of a launch at most, a power of two
+
 // layer norm (gmm_norm.hip)
 struct NormArgs {
   const void *x, *dy, *gamma, *beta;
@@ -384,6 +386,7 @@ struct NormArgs {
   float *mean, *rstd;      // written forward, read backward
   float* part;             // (parts, 2, D): shares of dgamma and dbeta
   int64_t R, N, D, ld, stride_b, ld_dy, stride_dy;  // stride 0: rows ld apart throughout
+  int64_t r0;              // first row of a launch
   float eps;
   int dtype, accumulate;
   bool affine_t;           // gamma and beta in the rows' type (else float32)
@@ -408,6 +411,7 @@ struct RouteArgs {
   float* weights;
   void* dlogits;
   int64_t R, N, ld, stride_b;  // stride 0: rows ld apart throughout
+  int64_t r0;              // first row of a launch
   int E, m, groups, keep, top;
   bool sigmoid, renorm;
   float scale;
@@ -441,7 +445,13 @@ hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs a, hipStream_t 
 
 // sampling (gmm_sample.hip)
 constexpr int kSampleParts = 64, kSampleList = 2048;
+struct SampleSettings {    // of a row
+  double temperature, top_p, min_p;
+  int64_t top_k;
+  float u;
+};
 struct SampleRow {         // of a long row, in the workspace
+  SampleSettings settings;
   unsigned long long best[kSampleParts], mass[4 * kSampleParts];  // of every part, and of its quarters
   unsigned long long bin[2048];
   unsigned long long list[2 * kSampleList];

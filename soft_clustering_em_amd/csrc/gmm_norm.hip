@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs A)
   constexpr int E = kPer<T>, RPB = TPR > 256 ? 1 : 256 / TPR;
   __shared__ float2 red[2][16];
   const int t = threadIdx.x % TPR;
-  const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const int64_t r = A.r0 + (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool live = r < A.R;  // rows of more than a wave: the whole workgroup agrees
   if (TPR > 64 && !live) return;
   const T* x = static_cast<const T*>(A.x) + (live ? row_at(r, A.N, A.ld, A.stride_b) : 0);
@@ -400,10 +400,16 @@ hipError_t by_type(int dtype, F f) {
 }
 
 template <typename T, int TPR, int C>
-hipError_t run_norm(const NormArgs& A, hipStream_t s) {
+hipError_t run_norm(NormArgs A, hipStream_t s) {
   constexpr int RPB = TPR > 256 ? 1 : 256 / TPR;
-  hipLaunchKernelGGL((norm_kernel<T, TPR, C>), dim3((unsigned)((A.R + RPB - 1) / RPB)), dim3(TPR > 256 ? TPR : 256), 0, s, A);
-  return hipGetLastError();
+  // a launch has fewer than 2^32 threads
+  for (const int64_t step = kLaunchThreads / TPR; A.r0 < A.R; A.r0 += step) {
+    const int64_t rows = std::min(step, A.R - A.r0);
+    hipLaunchKernelGGL((norm_kernel<T, TPR, C>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(TPR > 256 ? TPR : 256), 0, s, A);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T, int TPR, int C, bool ACC>

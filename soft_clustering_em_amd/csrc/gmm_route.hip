@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sub = lane % L, row = lane / L;
   const int room = route_room(A.E, A.groups, L);
   double* mine_lds = lds + (size_t)(w * RPW + row) * room;
-  const int64_t r = ((int64_t)blockIdx.x * 4 + w) * RPW + row;
+  const int64_t r = A.r0 + ((int64_t)blockIdx.x * 4 + w) * RPW + row;
   const bool in = r < A.R;
   const int64_t base = in ? row_base(A, r) : 0;
   const bool grouped = A.groups > 1 && A.keep < A.groups, by_score = A.bias != nullptr;
@@ -432,7 +432,7 @@ template <typename T, int L, int EPL>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs A) {
   constexpr int RPW = 64 / L;
   const int lane = threadIdx.x & 63, sub = lane % L, row = lane / L;
-  const int64_t r = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * RPW + row;
+  const int64_t r = A.r0 + ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * RPW + row;
   const bool in = r < A.R;
   const int64_t base = in ? row_base(A, r) : 0;
   float l[EPL], s[EPL], rest[EPL], ds[EPL], dl[EPL];
@@ -512,12 +512,18 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs A) {
 }  // namespace
 
 template <typename T, int L, int EPL>
-static hipError_t run_route(const RouteArgs& A, bool grad, hipStream_t s) {
+static hipError_t run_route(RouteArgs A, bool grad, hipStream_t s) {
   constexpr int rows = 4 * (64 / L);
-  const dim3 grid((unsigned)((A.R + rows - 1) / rows)), block(256);
-  if (grad) hipLaunchKernelGGL((route_grad_kernel<T, L, EPL>), grid, block, 0, s, A);
-  else hipLaunchKernelGGL((route_kernel<T, L, EPL>), grid, block, sizeof(double) * rows * route_room(A.E, A.groups, L), s, A);
-  return hipGetLastError();
+  const size_t lds = sizeof(double) * rows * route_room(A.E, A.groups, L);
+  for (const int64_t step = kLaunchThreads / L; A.r0 < A.R; A.r0 += step) {
+    const int64_t n = A.R - A.r0 < step ? A.R - A.r0 : step;
+    const dim3 grid((unsigned)((n + rows - 1) / rows)), block(256);
+    if (grad) hipLaunchKernelGGL((route_grad_kernel<T, L, EPL>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((route_kernel<T, L, EPL>), grid, block, lds, s, A);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T>

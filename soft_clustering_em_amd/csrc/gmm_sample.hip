@@ -50,6 +50,7 @@ struct Row {
   uint32_t first;  // the lowest index of the maximum
   double scale, S; // kBinsPerUnit / temperature, 2^S
   double least;    // min-p
+  double u;        // the row's number, in [0, 1)
   float bins;      // scale, at most FLT_MAX
   // The distance to the maximum in bins, y >= 0.  exp((l - max) / T) = exp(-b / 32)
   // exp(-t / 32) with b = y rounded and |t| <= 1/2: the first factor is one of
@@ -188,24 +189,39 @@ struct Shared : Cutting {
   uint32_t tie[kSegs];
 };
 
+// A row's settings, its own before those of the call.
+__device__ inline SampleSettings settings_of(const SampleArgs& A, int64_t r) {
+  SampleSettings s;
+  s.temperature = A.row_temperature ? (double)A.row_temperature[r] : A.temperature;
+  s.top_p = A.row_top_p ? (double)A.row_top_p[r] : A.top_p;
+  s.min_p = A.row_min_p ? (double)A.row_min_p[r] : A.min_p;
+  s.top_k = A.row_top_k ? A.row_top_k[r] : A.top_k;
+  s.u = fminf(fmaxf(A.u[r], 0.f), 0x1.fffffep-1f);
+  return s;
+}
+
 // The row's elements, and what `best` (its largest key, and ~ its lowest index)
 // and the settings make of it.
 template <typename T>
-__device__ inline Settings row_of(const SampleArgs& A, int64_t r, u64 best, Row<T>& R) {
-  R.V = A.V;
+__device__ inline void place_of(const SampleArgs& A, int64_t r, Row<T>& R) {
   const int64_t b = A.stride_b ? r / A.N : 0;
   R.p = static_cast<const T*>(A.l) + b * A.stride_b + (r - b * A.N) * A.ld;
+  R.V = A.V;
   R.S = A.scale;
+}
+template <typename T>
+__device__ inline Settings row_of(const SampleArgs& A, int64_t r, const SampleSettings& s, u64 best, Row<T>& R) {
+  place_of(A, r, R);
   R.mx = best ? logit_of((uint32_t)(best >> 32)) : 0.f;
   R.first = ~(uint32_t)best;
-  const double t = A.row_temperature ? (double)A.row_temperature[r] : A.temperature;
-  const double min_p = A.row_min_p ? (double)A.row_min_p[r] : A.min_p;
+  const double t = s.temperature;
   Settings q;
-  q.k = A.row_top_k ? A.row_top_k[r] : A.top_k;
-  q.top_p = A.row_top_p ? (double)A.row_top_p[r] : A.top_p;
+  q.k = s.top_k;
+  q.top_p = s.top_p;
   q.mode = !best ? kNone : !(t > 0.0) || q.k == 1 ? kGreedy : q.k > 0 && q.k < A.V ? kCount : q.top_p < 1.0 ? kMass : kOpen;
+  R.u = (double)s.u;
   R.scale = t > 0.0 ? fmin(kBinsPerUnit / t, 1e300) : 1.0;
-  R.least = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
+  R.least = s.min_p > 0.0 ? fmin(s.min_p, 1.0) : 0.0;
   R.bins = (float)fmin(R.scale, (double)FLT_MAX);
   return q;
 }
@@ -400,8 +416,9 @@ __device__ inline void answer(const SampleArgs& A, const Row<T>& R, int64_t r, f
   A.tokens[r] = (int32_t)i;
   if (A.logp) A.logp[r] = (float)(-R.distance(l) / kBinsPerUnit - log((double)total / R.S));
 }
-__device__ inline double aim(const SampleArgs& A, int64_t r, u64 total) {
-  return (double)fminf(fmaxf(A.u[r], 0.f), 0x1.fffffep-1f) * (double)total;
+template <typename T>
+__device__ inline double aim(const Row<T>& R, u64 total) {
+  return R.u * (double)total;
 }
 
 template <int TH>
@@ -450,7 +467,7 @@ __device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R,
   if (q.mode == kCount && q.top_p < 1.0) mass = group_sum<TH>(own && first ? w : 0, sh.red);
   const bool in = own && (place == 0 || (first && (!(q.top_p < 1.0) || (double)before < q.top_p * (double)mass) && e >= R.least));
   const u64 total = group_sum<TH>(in ? w : 0, sh.red);
-  const double goal = aim(A, r, total);
+  const double goal = aim(R, total);
   group_sync<TH>();
   if (own) sh.sum[i] = in ? w : 0;
   group_sync<TH>();
@@ -504,7 +521,7 @@ __device__ __forceinline__ void finish_list(const SampleArgs& A, const Row<T>& R
   }
   __syncthreads();
   u64 base = 0;
-  const double goal = aim(A, r, total);
+  const double goal = aim(R, total);
 #pragma unroll
   for (int e = 0; e < kList / TH; ++e) {
     if (e * TH >= kept) break;
@@ -653,7 +670,7 @@ __device__ __forceinline__ void choose(const SampleArgs& A, const Row<T>& R, con
   const u64 wt = cut.ties ? R.weight_min_p(cut.l) : 0;
   if (goal < 0.0) {
     total = whole_list<kSegs / 64>(sh, wt, cut.ties);
-    goal = aim(A, r, total);
+    goal = aim(R, total);
   }
   u64 left = cut.ties;
   const int s = pass_list<kSegs / 64>(sh, wt, goal, before, left);
@@ -843,8 +860,9 @@ __global__ void __launch_bounds__(256) sample_row_kernel(SampleArgs A) {
   __shared__ Shared sh;
   const int64_t r = (int64_t)blockIdx.x + A.r0;
   Row<T> R;
-  row_of(A, r, 0, R);
-  const Settings q = row_of(A, r, block_max<TH>(best_of(R, 0, R.V, threadIdx.x, TH), sh.red), R);
+  const SampleSettings own = settings_of(A, r);
+  place_of(A, r, R);
+  const Settings q = row_of(A, r, own, block_max<TH>(best_of(R, 0, R.V, threadIdx.x, TH), sh.red), R);
   if (plain_answer(A, R, q, r)) return;
   Cut cut{-INFINITY, 0};
   if (q.mode != kOpen) {
@@ -912,13 +930,16 @@ __global__ void __launch_bounds__(256) sample_best_kernel(SampleArgs A) {
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
   Row<T> R;
-  row_of(A, r, 0, R);
+  place_of(A, r, R);
   int64_t i0, i1;
   part_of(A, i0, i1);
   const u64 best = block_max<TH>(best_of(R, i0, i1, threadIdx.x, TH), red);
   if (threadIdx.x == 0) {
     w.best[blockIdx.x] = best;
-    if (blockIdx.x == 0) w.na = w.nb = 0;
+    if (blockIdx.x == 0) {
+      w.na = w.nb = 0;
+      w.settings = settings_of(A, r);
+    }
   }
   for (int i = blockIdx.x * TH + threadIdx.x; i < kBins; i += gridDim.x * TH) w.bin[i] = 0;
 }
@@ -932,7 +953,7 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleArgs A) {
   SampleRow& w = A.rows[blockIdx.y];
   Row<T> R;
   for (int i = threadIdx.x; i < kBins; i += TH) bin[i] = 0;
-  const Settings q = row_of(A, r, best_part(w, gridDim.x), R);
+  const Settings q = row_of(A, r, w.settings, best_part(w, gridDim.x), R);
   if (q.mode == kNone || q.mode == kGreedy) return;
   int64_t i0, i1;
   part_of(A, i0, i1);
@@ -958,7 +979,7 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
   const int64_t r = (int64_t)blockIdx.y + A.r0;
   SampleRow& w = A.rows[blockIdx.y];
   Row<T> R;
-  const Settings q = row_of(A, r, best_part(w, gridDim.x), R);
+  const Settings q = row_of(A, r, w.settings, best_part(w, gridDim.x), R);
   if (q.mode != kCount && q.mode != kMass) return;
   const u64 whole = cut_bin<TH>(q, sh, (const u64*)w.bin);
   if (threadIdx.x == 0) {
@@ -1015,11 +1036,12 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
   const int64_t r = (int64_t)blockIdx.x + A.r0;
   SampleRow& w = A.rows[blockIdx.x];
   // what the row may need, on its way while its maximum is found
+  const SampleSettings own = w.settings;
   const int na = w.na, nb = w.nb;
   const u64 whole = w.whole, above = w.above, mass = threadIdx.x < parts * kQuarters ? w.mass[threadIdx.x] : 0;
   const u64 front = w.list[threadIdx.x], back = w.list[2 * kSampleList - 1 - threadIdx.x];
   Row<T> R;
-  const Settings q = row_of(A, r, best_part(w, parts), R);
+  const Settings q = row_of(A, r, own, best_part(w, parts), R);
   if (plain_answer(A, R, q, r)) return;
   Cut cut{-INFINITY, 0};
   int64_t i0 = 0, i1 = A.V;
@@ -1062,7 +1084,7 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
     __syncthreads();
     // every wave
     total = whole_list<kSegs / 64>(sh, wt, cut.ties);
-    goal = aim(A, r, total);
+    goal = aim(R, total);
     u64 left = cut.ties;
     const int k = pass_list<kSegs / 64>(sh, wt, goal, before, left);
     cut.ties = left;

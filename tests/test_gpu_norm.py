@@ -171,3 +171,14 @@ def test_captured_and_on_a_stream(g):
     other = step(stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, other))
+
+
+def test_more_rows_than_a_launch_takes(g):
+    """2^31 threads of a launch are 2^27 rows of 16 threads: the rows behind them come in a second one."""
+    n = (1 << 27) + 37
+    X = torch.arange(8, device="cuda").to(BF16).expand(n, 8).contiguous()
+    X[1 << 27:, 0] = 5.0
+    out, _, _ = g.gmm_layer_norm(X, mean=False, rstd=False)
+    at = torch.tensor([0, 1, (1 << 27) - 1, 1 << 27, n - 2, n - 1], device="cuda")
+    head_ref.within("out", out[at], *ref.norm(X[at])[0])
+    assert torch.equal(out[:1000], out[0].expand(1000, 8)) and torch.equal(out[1 << 27:], out[n - 1].expand(37, 8))

@@ -181,3 +181,25 @@ def test_captured(g):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, step())), k
+
+
+def test_more_experts_asked_for_than_there_are(g):
+    for E, m in ((1, 4), (3, 16), (20, 16)):
+        for b in (None, torch.randn(E, device="cuda")):
+            idx, w = check(g, make((9, E)), m, bias=b)
+            assert (idx[:, min(E, m):] == -1).all()
+
+
+def test_more_rows_than_a_launch_takes(g):
+    """2^31 threads of a launch are 2^27 rows of 16 lanes: the rows behind them come in a second one."""
+    n = (1 << 27) + 37
+    l = torch.zeros(n, 2, dtype=BF16, device="cuda")  # noqa: E741
+    l[::2, 1] = 1.0
+    idx, w = g.gmm_route_topm(l, 1, renormalize=False)
+    at = torch.tensor([0, 1, (1 << 27) - 1, 1 << 27, (1 << 27) + 1, n - 2, n - 1], device="cuda")
+    i_want, w_want = ref.route(l[at], 1, renorm=False)
+    assert torch.equal(idx[at].cpu(), i_want)
+    head_ref.within("weights", w[at].cpu(), w_want, 1.01 * ref.U * w_want)
+    assert int(idx.sum(dtype=torch.int64)) == (n + 1) // 2
+    dl = g.gmm_route_topm_grad(w, l, idx, renormalize=False)
+    head_ref.within("dlogits", dl[at].cpu(), *ref.route_grad(w[at], l[at], idx[at], renorm=False))
