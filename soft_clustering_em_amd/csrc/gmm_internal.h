@@ -467,6 +467,7 @@ struct SampleArgs {
   int64_t R, N, V, ld, stride_b, top_k;
   double temperature, top_p, min_p, scale;
   int64_t r0, part;        // first row of a launch, elements of a part
+  int part_bits;           // part = 2^part_bits
   SampleRow* rows;
 };
 size_t sample_bytes(int64_t R, int64_t V);

@@ -115,20 +115,53 @@ __device__ inline void each(const Row<T>& R, int64_t i0, int64_t i1, int thread,
   }
   if (i1 - whole > thread && thread < E) one(whole + thread, R.p[whole + thread]);
 }
+// 64-bit integers between lanes by DPP: lanes without a source get 0
+template <int CTRL, int ROWS = 0xF>
+__device__ inline u64 dpp_u64(u64 v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+  return (u64)hi << 32 | lo;
+}
+// the two halves of 16-lane rows' pairs, and of the wave, as v_permlane*_swap has them
+__device__ inline void pair16_u64(u64 v, u64& a, u64& b) {
+  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+  a = (u64)hi[0] << 32 | lo[0];
+  b = (u64)hi[1] << 32 | lo[1];
+}
+__device__ inline void pair32_u64(u64 v, u64& a, u64& b) {
+  const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+  a = (u64)hi[0] << 32 | lo[0];
+  b = (u64)hi[1] << 32 | lo[1];
+}
 __device__ inline u64 wave_sum_u64(u64 v) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  u64 a, b;
+  v += dpp_u64<0xB1>(v);
+  v += dpp_u64<0x4E>(v);
+  v += dpp_u64<0x141>(v);
+  v += dpp_u64<0x140>(v);
+  pair16_u64(v, a, b);
+  pair32_u64(a + b, a, b);
+  return a + b;
 }
 __device__ inline u64 wave_max_u64(u64 v) {
-  for (int o = 32; o; o >>= 1) v = max(v, (u64)__shfl_xor(v, o));
-  return v;
+  u64 a, b;
+  v = max(v, dpp_u64<0xB1>(v));
+  v = max(v, dpp_u64<0x4E>(v));
+  v = max(v, dpp_u64<0x141>(v));
+  v = max(v, dpp_u64<0x140>(v));
+  pair16_u64(v, a, b);
+  pair32_u64(max(a, b), a, b);
+  return max(a, b);
 }
 __device__ inline u64 wave_scan_u64(u64 v) {  // inclusive
-  const int lane = threadIdx.x & 63;
-  for (int o = 1; o < 64; o <<= 1) {
-    const u64 x = __shfl_up(v, o);
-    if (lane >= o) v += x;
-  }
+  v += dpp_u64<0x111>(v);  // from 1, 2, 4 and 8 lanes before in the row
+  v += dpp_u64<0x112>(v);
+  v += dpp_u64<0x114>(v);
+  v += dpp_u64<0x118>(v);
+  v += dpp_u64<0x142, 0xA>(v);  // the last lane of the row before, in rows 1 and 3
+  v += dpp_u64<0x143, 0xC>(v);  // of the wave's first half, in its second
   return v;
 }
 template <int TH>
@@ -452,7 +485,7 @@ __device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R,
   int place = 0;
   u64 before = 0;
   const int others = (threadIdx.x & ~63) / G < n ? n : 0;  // waves without an element have nothing to compare
-#pragma unroll 4
+#pragma unroll 8
   for (int j = g; j < others; j += G) {
     const bool ahead = sh.list[j] > mine;
     place += ahead;
@@ -472,7 +505,7 @@ __device__ __forceinline__ void finish_few(const SampleArgs& A, const Row<T>& R,
   if (own) sh.sum[i] = in ? w : 0;
   group_sync<TH>();
   u64 to = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int j = g; j < others; j += G) to += (uint32_t)sh.list[j] >= (uint32_t)mine ? sh.sum[j] : 0;  // ~index: descending
 #pragma unroll
   for (int o = 1; o < G; o *= 2) to += __shfl_xor(to, o);
@@ -808,29 +841,26 @@ __device__ __forceinline__ Cut cut_of_bin(const Row<T>& R, const Settings& q, Sh
     const u64 mine = i < nb ? sh.list[i] : 0, w = i < nb ? R.weight(list_logit(mine)) : 0;
     if (i < nb && g == 0) sh.sum[i] = w;
     __syncthreads();
-    u64 before = 0, same = 0, place = 0;
+    u64 before = 0;
+    int place = 0;
     const int others = (threadIdx.x & ~63) / G < nb ? nb : 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = g; j < others; j += G) {
-      const u64 other = sh.list[j];
-      const bool ahead = other > mine;
+      const bool ahead = sh.list[j] > mine;
       before += ahead ? sh.sum[j] : 0;
       place += ahead;
-      same += ahead && other >> 32 == mine >> 32;
     }
 #pragma unroll
     for (int o = 1; o < G; o *= 2) {
       before += __shfl_xor(before, o);
       place += __shfl_xor(place, o);
-      same += __shfl_xor(same, o);
     }
     before += above;
-    if (i < nb && g == 0 && (double)(before + w) >= target && (place == 0 || (double)before < target)) {
-      sh.edge = mine;
-      sh.above = same + 1;
-    }
+    if (i < nb && g == 0 && (double)(before + w) >= target && (place == 0 || (double)before < target)) sh.edge = mine;
     __syncthreads();
-    return Cut{list_logit(sh.edge), sh.above};
+    const u64 edge = sh.edge;
+    const bool tie = i < nb && g == 0 && mine >= edge && mine >> 32 == edge >> 32;
+    return Cut{list_logit(edge), block_sum<TH>(tie, sh.red)};
   }
   sort_list<TH>(sh, nb);
   scan_list<TH>(sh, nb, [&](int i) { return R.weight(list_logit(sh.list[i])); });
@@ -994,7 +1024,6 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
   int64_t i0, i1, q0, q1;
   part_of(A, i0, i1);
   quarter_of(A, q0, q1);
-  const int64_t quarter = A.part / kQuarters;
   collect(R, sh, i0, i1, threadIdx.x, TH);
   // a place in the row's list for all of them; too many here are too many there
   const int na = sh.na, nb = sh.nb;
@@ -1004,7 +1033,7 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
       if (threadIdx.x < kQuarters) sh.red[threadIdx.x] = 0;
       __syncthreads();
       for (int i = threadIdx.x; i < na; i += TH)
-        atomicAdd(&sh.red[(~(uint32_t)sh.list[i] - (uint32_t)i0) / (uint32_t)quarter], R.weight_min_p(list_logit(sh.list[i])));
+        atomicAdd(&sh.red[(~(uint32_t)sh.list[i] - (uint32_t)i0) >> (A.part_bits - 2)], R.weight_min_p(list_logit(sh.list[i])));
       __syncthreads();
       if (threadIdx.x < kQuarters) w.mass[blockIdx.x * kQuarters + threadIdx.x] = sh.red[threadIdx.x];
     } else {
@@ -1074,8 +1103,7 @@ __global__ void __launch_bounds__(1024) sample_finish_kernel(SampleArgs A, int p
       for (int i = threadIdx.x; i < nb; i += TH) {
         if (sh.list[i] < sh.edge) continue;
         const float l = list_logit(sh.list[i]);
-        const uint32_t at = ~(uint32_t)sh.list[i], part = at / (uint32_t)A.part;
-        const int k = (int)(part * kQuarters + (at - part * (uint32_t)A.part) / (uint32_t)quarter);
+        const int k = (int)(~(uint32_t)sh.list[i] >> (A.part_bits - 2));  // its quarter
         if (l > cut.l) atomicAdd(&sh.seg[k], R.weight_min_p(l));
         else atomicAdd(&sh.tie[k], 1u);
       }
@@ -1117,10 +1145,13 @@ static hipError_t run_sample(SampleArgs A, void* ws, hipStream_t s) {
   A.rows = static_cast<SampleRow*>(ws);
   for (A.r0 = 0; A.r0 < A.R; A.r0 += step) {
     const unsigned n = (unsigned)std::min(step, A.R - A.r0);
-    // about four workgroups a compute unit, of whole pieces
+    // four workgroups a compute unit or more, where the rows are long enough; the
+    // parts are powers of two
     const int64_t want = std::min<int64_t>(std::max<int64_t>(1, 1024 / n), (A.V + kPartLeast - 1) / kPartLeast);
-    const int64_t most = std::min<int64_t>(want, kSampleParts);
-    A.part = ((A.V + most - 1) / most + 8 * kQuarters - 1) / (8 * kQuarters) * (8 * kQuarters);
+    A.part_bits = 12;
+    static_assert(kPartLeast == 1 << 12, "the least part");
+    while (((int64_t)1 << A.part_bits) * want * 2 <= A.V || ((int64_t)kSampleParts << A.part_bits) < A.V) ++A.part_bits;
+    A.part = (int64_t)1 << A.part_bits;
     const unsigned parts = (unsigned)((A.V + A.part - 1) / A.part);
     hipLaunchKernelGGL(sample_best_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
     hipLaunchKernelGGL(sample_bins_kernel<T>, dim3(parts, n), dim3(256), 0, s, A);
