@@ -485,7 +485,7 @@ gmm_status gmm_layer_norm(const gmm_data* rows, const void* gamma, const void* b
  * one given.  accumulate != 0 adds to what they hold.  The gradients may not
  * overlap each other or the inputs.  Workspace:
  * gmm_layer_norm_grad_workspace_bytes, want = 1 (dx) + 2 (dgamma) + 4 (dbeta);
- * it does not grow with the rows past 16384 of them.  Deterministic. */
+ * it does not grow with the rows past 65536 of them.  Deterministic. */
 size_t gmm_layer_norm_grad_workspace_bytes(const gmm_data* rows, int32_t want);
 gmm_status gmm_layer_norm_grad(const gmm_data* dout, const gmm_data* rows, const float* mean, const float* rstd,
                                const void* gamma, int32_t affine_dtype, void* dx, float* dgamma, float* dbeta,

@@ -51,23 +51,42 @@ __device__ inline u32x4 load_piece(const T* row, int64_t c0, int64_t D) {
   return __builtin_bit_cast(u32x4, v);
 }
 
+// v shifted down by k elements, zeros behind them
+template <typename T>
+__device__ inline u32x4 shifted(u32x4 v, int k) {
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  const int s = k * 8 * (int)sizeof(T);  // 16 to 112
+  if (s >= 64) {
+    lo = hi >> (s - 64);
+    hi = 0;
+  } else {
+    lo = lo >> s | hi << (64 - s);
+    hi >>= s;
+  }
+  return u32x4{(unsigned)lo, (unsigned)(lo >> 32), (unsigned)hi, (unsigned)(hi >> 32)};
+}
+
 // A thread's C pieces of a row (zeros past D, and everywhere if not `live`).
 // The loads come first and without a branch, so that they are in flight
-// together; pieces that do not lie whole in the row read its start instead.
+// together: a piece that reaches past D is the row's last 16 bytes, shifted.
 template <typename T, int TPR, int C>
 __device__ inline void load_row(u32x4 (&v)[C], const T* row, int t, int64_t D, bool live) {
   constexpr int E = kPer<T>;
-  if (D >= E) {
+  if (D < E) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int64_t c0 = ((int64_t)j * TPR + t) * E;
-      __builtin_memcpy(&v[j], row + (c0 + E <= D ? c0 : 0), 16);
-    }
+    for (int j = 0; j < C; ++j) v[j] = load_piece<T>(row, ((int64_t)j * TPR + t) * E, live ? D : 0);
+    return;
   }
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int64_t c0 = ((int64_t)j * TPR + t) * E;
-    if (!live || c0 + E > D) v[j] = load_piece<T>(row, c0, live ? D : 0);
+    __builtin_memcpy(&v[j], row + (c0 + E <= D ? c0 : D - E), 16);
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int64_t c0 = ((int64_t)j * TPR + t) * E;
+    if (!live || c0 >= D) v[j] = u32x4{0, 0, 0, 0};
+    else if (c0 + E > D) v[j] = shifted<T>(v[j], (int)(c0 + E - D));
   }
 }
 
@@ -107,17 +126,28 @@ __device__ inline void load_affine(float (&v)[kPer<T>], const void* p, bool is_t
   }
 }
 
+// over groups of L neighbouring lanes, in every one of them
+template <int L>
+__device__ inline float lanes_sum(float v) {
+  v += dpp_mov<0xB1>(v);
+  v += dpp_mov<0x4E>(v);
+  if constexpr (L >= 8) v += dpp_mov<0x141>(v);
+  if constexpr (L >= 16) v += dpp_mov<0x140>(v);
+  if constexpr (L == 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if constexpr (L == 64) v = rows4_sum(v);
+  return v;
+}
+
 // The sums of a and b over the TPR threads of a row, in every one of them.
 // Rows of more than a wave meet in LDS; `red` alternates between two halves,
 // so that one barrier a call is enough.
 template <int TPR>
-__device__ inline void row_sum2(float& a, float& b, float2 (*red)[16], int& turn) {
-  a = row16_sum(a);
-  b = row16_sum(b);
-  if constexpr (TPR >= 64) {
-    a = rows4_sum(a);
-    b = rows4_sum(b);
-  }
+__device__ inline void row_sum2(float& a, float& b, float2 (*red)[TPR > 64 ? TPR / 64 : 1], int& turn) {
+  a = lanes_sum<TPR < 64 ? TPR : 64>(a);
+  b = lanes_sum<TPR < 64 ? TPR : 64>(b);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = make_float2(a, b);
@@ -142,7 +172,7 @@ __device__ inline int64_t row_at(int64_t r, int64_t N, int64_t ld, int64_t strid
 template <typename T, int TPR, int C>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs A) {
   constexpr int E = kPer<T>, RPB = TPR > 256 ? 1 : 256 / TPR;
-  __shared__ float2 red[2][16];
+  __shared__ float2 red[2][TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR;
   const int64_t r = A.r0 + (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool live = r < A.R;  // rows of more than a wave: the whole workgroup agrees
@@ -204,7 +234,7 @@ template <typename T, int TPR, int C, bool ACC>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_grad_kernel(NormArgs A) {
   constexpr int E = kPer<T>, RPB = TPR > 256 ? 1 : 256 / TPR, W = (TPR > 256 ? TPR : 256) / 64;
   constexpr bool AHEAD = TPR <= 256;
-  __shared__ float2 red[2][16];
+  __shared__ float2 red[2][TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR;
   const float inv = 1.f / (float)A.D;
   u32x4 g[C], nx[C], ny[C];
@@ -300,14 +330,16 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_grad_kernel(NormAr
     }
   }
   if constexpr (ACC) {
-    if constexpr (TPR == 16) {  // the four rows of a wave
+    if constexpr (TPR < 64) {  // the rows of a wave
 #pragma unroll
       for (int j = 0; j < C; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          dg[j][e] = rows4_sum(dg[j][e]);
-          db[j][e] = rows4_sum(db[j][e]);
-        }
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int o = TPR; o < 64; o *= 2) {
+            dg[j][e] += __shfl_xor(dg[j][e], o);
+            db[j][e] += __shfl_xor(db[j][e], o);
+          }
     }
     constexpr int L = TPR < 64 ? TPR : 64, S = TPR < 64 ? W : RPB;  // lanes with columns of their own, waves to join
     float* part = A.part + (int64_t)blockIdx.x * 2 * A.D;
@@ -420,10 +452,13 @@ hipError_t run_grad(const NormArgs& A, unsigned grid, hipStream_t s) {
 
 }  // namespace
 
-// Threads a row and pieces a thread for rows of `pieces` 16-byte pieces: whole
-// waves side by side as long as a thread holds at most `most` pieces.
+// Threads a row and pieces a thread for rows of `pieces` 16-byte pieces: the
+// fewest threads, a power of two, that hold one piece each up to a wave, then up to
+// `most` a thread.
 static void norm_shape(int64_t pieces, int most, int* tpr, int* c) {
-  *tpr = pieces <= 16 ? 16 : pieces <= 64 * most ? 64 : pieces <= 256 * most ? 256 : 1024;
+  *tpr = 4;
+  while (*tpr < 64 && *tpr < pieces) *tpr *= 2;
+  if (pieces > 64 * most) *tpr = pieces <= 256 * most ? 256 : pieces <= 512 * most ? 512 : 1024;
   const int64_t per = (pieces + *tpr - 1) / *tpr;
   *c = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
 }
@@ -440,13 +475,16 @@ hipError_t launch_norm(NormArgs A, hipStream_t s) {
     int tpr, c;
     norm_shape((A.D + kPer<T> - 1) / kPer<T>, 4, &tpr, &c);
     switch (tpr * 16 + c) {
+      case 4 * 16 + 1: return run_norm<T, 4, 1>(A, s);
+      case 8 * 16 + 1: return run_norm<T, 8, 1>(A, s);
       case 16 * 16 + 1: return run_norm<T, 16, 1>(A, s);
+      case 32 * 16 + 1: return run_norm<T, 32, 1>(A, s);
       case 64 * 16 + 1: return run_norm<T, 64, 1>(A, s);
       case 64 * 16 + 2: return run_norm<T, 64, 2>(A, s);
       case 64 * 16 + 4: return run_norm<T, 64, 4>(A, s);
       case 256 * 16 + 2: return run_norm<T, 256, 2>(A, s);
       case 256 * 16 + 4: return run_norm<T, 256, 4>(A, s);
-      case 1024 * 16 + 2: return run_norm<T, 1024, 2>(A, s);
+      case 512 * 16 + 4: return run_norm<T, 512, 4>(A, s);
       case 1024 * 16 + 4: return run_norm<T, 1024, 4>(A, s);
       default: break;
     }
@@ -478,12 +516,15 @@ hipError_t launch_norm_grad(NormArgs A, const NormPlan& p, float* dgamma, float*
 #define GMM_NORM_GRAD(TPR, C)                                                    \
   case (TPR * 16 + C) * 2: return run_grad<T, TPR, C, false>(A, g, s);           \
   case (TPR * 16 + C) * 2 + 1: return run_grad<T, TPR, C, true>(A, g, s);
+        GMM_NORM_GRAD(4, 1)
+        GMM_NORM_GRAD(8, 1)
         GMM_NORM_GRAD(16, 1)
+        GMM_NORM_GRAD(32, 1)
         GMM_NORM_GRAD(64, 1)
         GMM_NORM_GRAD(64, 2)
         GMM_NORM_GRAD(256, 1)
         GMM_NORM_GRAD(256, 2)
-        GMM_NORM_GRAD(1024, 1)
+        GMM_NORM_GRAD(512, 2)
         GMM_NORM_GRAD(1024, 2)
 #undef GMM_NORM_GRAD
         case (1024 * 16 + 4) * 2: return run_grad<T, 1024, 4, false>(A, g, s);
