@@ -82,6 +82,7 @@ __device__ inline void load_row(u32x4 (&v)[C], const T* row, int t, int64_t D, b
     const int64_t c0 = ((int64_t)j * TPR + t) * E;
     __builtin_memcpy(&v[j], row + (c0 + E <= D ? c0 : D - E), 16);
   }
+  if (D == (int64_t)TPR * C * E && live) return;  // every piece lies in the row
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int64_t c0 = ((int64_t)j * TPR + t) * E;
