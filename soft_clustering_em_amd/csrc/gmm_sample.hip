@@ -369,14 +369,17 @@ __device__ inline u64 cut_bin(const Settings& q, Cutting& sh, const u64* bin) {
 // Elements of the bins before sh.at, and of the bin itself, as key << 32 |
 // ~index from the two ends of sh.list; counters that pass its half say so.
 // Most elements lie below: a thread marks the others of the pieces that it has
-// in flight by one comparison each (NaN too for now, and all where the bin is
-// the last one, which has no lower end), and looks at the marked ones after.
+// in flight by a comparison with either end (all below where the bin is the last
+// one, which has no lower end), and looks at the marked ones after.  Once the
+// first list is full, the elements before the bin are passed over.
 template <typename T>
 __device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
   constexpr int E = 16 / (int)sizeof(T), U = 4;
   const int at = sh.at;
   // the float32 distance is off by less than 2^-22 of itself
   const float end = at == kBins - 1 ? __builtin_nanf("") : ((float)at + 0.5f) * (1.f + 0x1p-20f);
+  const float begin = ((float)at - 0.5f) * (1.f - 0x1p-20f);
+  volatile int* filled = &sh.na;
   const auto add = [&](int64_t i, float v) {
     if (!(v > -INFINITY)) return;
     const float l = fminf(v, FLT_MAX);
@@ -390,12 +393,16 @@ __device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t
   for (int64_t i = i0 + (int64_t)thread * E; i < whole; i += U * step) {
     T v[U][E];
     load_pieces<T, U>(v, R.p, i, step, whole);
+    const float from = *filled > kList / 2 ? begin : -INFINITY;
     uint32_t marked = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) m |= (R.mx - (float)v[u][e]) * R.bins >= end ? 0u : 1u << e;
+      for (int e = 0; e < E; ++e) {
+        const float y = (R.mx - (float)v[u][e]) * R.bins;
+        m |= !(y >= end) && y >= from ? 1u << e : 0u;
+      }
       if (i + u * step < whole) marked |= m << (u * E);
     }
     while (marked) {
@@ -1027,23 +1034,6 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
   collect(R, sh, i0, i1, threadIdx.x, TH);
   // a place in the row's list for all of them; too many here are too many there
   const int na = sh.na, nb = sh.nb;
-  if (q.mode == kMass) {  // what the part keeps for sure
-    u64 mass = 0;
-    if (na <= kList / 2) {
-      if (threadIdx.x < kQuarters) sh.red[threadIdx.x] = 0;
-      __syncthreads();
-      for (int i = threadIdx.x; i < na; i += TH)
-        atomicAdd(&sh.red[(~(uint32_t)sh.list[i] - (uint32_t)i0) >> (A.part_bits - 2)], R.weight_min_p(list_logit(sh.list[i])));
-      __syncthreads();
-      if (threadIdx.x < kQuarters) w.mass[blockIdx.x * kQuarters + threadIdx.x] = sh.red[threadIdx.x];
-    } else {
-      each<1>(R, q0, q1, threadIdx.x & 63, 64, [&](int64_t, float l) {
-        if (R.bin(l) < sh.at) mass += R.weight_min_p(l);
-      });
-      mass = wave_sum_u64(mass);
-      if ((threadIdx.x & 63) == 0) w.mass[blockIdx.x * kQuarters + (threadIdx.x >> 6)] = mass;
-    }
-  }
   __shared__ int base[2];
   if (threadIdx.x == 0) {
     base[0] = na ? atomicAdd(&w.na, na > kList / 2 ? kSampleList + 1 : na) : 0;
@@ -1056,6 +1046,34 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
   if (nb <= kList / 2)
     for (int i = threadIdx.x; i < nb; i += TH)
       if (base[1] + i < kSampleList) w.list[2 * kSampleList - 1 - base[1] - i] = sh.list[kList - 1 - i];
+  if (q.mode == kMass) {  // what the part keeps for sure
+    if (na <= kList / 2) {
+      if (threadIdx.x < kQuarters) sh.red[threadIdx.x] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < na; i += TH)
+        atomicAdd(&sh.red[(~(uint32_t)sh.list[i] - (uint32_t)i0) >> (A.part_bits - 2)], R.weight_min_p(list_logit(sh.list[i])));
+      __syncthreads();
+      if (threadIdx.x < kQuarters) w.mass[blockIdx.x * kQuarters + threadIdx.x] = sh.red[threadIdx.x];
+    } else {
+      // many: by the bins' factors, in the list's place
+      static_assert(kList >= kBins, "a factor an entry");
+      double* factor = reinterpret_cast<double*>(sh.list);
+      __syncthreads();
+      fill_factors(R, threadIdx.x, TH, factor);
+      __syncthreads();
+      const double at = (double)sh.at;
+      u64 mass = 0;
+      each<1>(R, q0, q1, threadIdx.x & 63, 64, [&](int64_t, float l) {
+        const double y = R.distance(l), b = rint(y);
+        if (b < at) {
+          const double e = factor[(int)b] * R.near(y - b);
+          mass += e >= R.least ? R.fixed(e) : 0;
+        }
+      });
+      mass = wave_sum_u64(mass);
+      if ((threadIdx.x & 63) == 0) w.mass[blockIdx.x * kQuarters + (threadIdx.x >> 6)] = mass;
+    }
+  }
 }
 
 template <typename T>
