@@ -40,6 +40,9 @@
  *     sorted by (score, index), or walked in increasing index order, before
  *     any result depends on them, so the slot order never shows.  The codebook
  *     gradient's sort counts with LDS atomics (a count has no order).
+ *     Sampling adds counts and fixed-point weights as integers, by atomics in LDS
+ *     and, for the bins of a row in parts, in its workspace: integer sums are the
+ *     same in any order, and its lists are sorted or counted before use.
  *   - Calls on distinct streams with distinct workspaces may run concurrently.
  */
 #ifndef GMM_H
@@ -542,10 +545,10 @@ gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, i
  * States: m and v float32 (m_scale = v_scale = NULL), or 8 bits: m and v (n) OCP
  * e4m3 bytes, m_scale and v_scale ((n + 255) / 256) float32, one for every 256
  * elements, m = byte value x scale and sqrt(v) = byte value x scale, with scale =
- * max (1 / 448) of the block (0 for a block below 2^-100).  x = value (1 / max 448),
- * at most 448, is rounded to the neighbour above with the probability of its remainder: up when the bits
- * below the last kept one (as 16 bits) plus d reach 2^16, with d the upper (m) or
- * lower (sqrt v) half of
+ * max (1 / 448) of the block (0 for a block below 2^-100).  A value is rounded as
+ * x = value (1 / max 448), at most 448, to the neighbour above with the probability
+ * of its remainder: up when the bits below the last kept one (as 16 bits) plus d
+ * reach 2^16, with d the upper (m) or lower (sqrt v) half of
  *   h = mix(mix(mix(mix(seed + 0x9E3779B1 t) ^ tensor) + block) + 0x9E3779B1 i)
  *   mix(x): x = (x ^ x >> 16) 0x9E3779B1; x = (x ^ x >> 15) 0x6A09E667; x ^ x >> 16
  * in 32 bits, tensor its place in the call, i the element in its block; a root
@@ -591,8 +594,9 @@ gmm_status gmm_adamw_step(const gmm_adamw_tensor* tensors, int32_t count, const 
  * ceil(log2 V)), and summed as integers: the result does not depend on how the
  * work is split.  Logits of -inf or NaN are left out, +inf counts as float32's
  * largest value; a row without any other gets token -1 and logp -inf.  u outside
- * [0, 1) (NaN too) counts as the nearer end.  V <= 2^24, B*N < 2^31.  N = 0 launches nothing.
- * Workspace: gmm_sample_workspace_bytes. */
+ * [0, 1) (NaN too) counts as the nearer end.  V <= 2^24, B*N < 2^31.  N = 0
+ * launches nothing.  Workspace: gmm_sample_workspace_bytes, none of which has to
+ * be cleared; it does not grow with the rows past 1024 of them.  Deterministic. */
 typedef struct {
   double temperature, top_p, min_p;
   int64_t top_k;
