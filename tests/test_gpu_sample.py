@@ -190,3 +190,59 @@ def test_reference_on_the_host():
         q = np.zeros(40)
         q[keep] = p[keep] / p[keep].sum()
         assert t == int(np.searchsorted(np.cumsum(q), 0.37, side="right")) and abs(lp - math.log(q[t])) < 1e-9
+
+
+@pytest.mark.parametrize("kw", FILTERS)
+def test_long_rows_of_equal_few_and_masked_logits(g, kw):
+    """Rows in parts: equal logits, two values, one live element, dead parts, infinities."""
+    V = 40003
+    l, u = make((7, V))  # noqa: E741
+    l[0] = 3.0
+    l[1] = torch.where(torch.arange(V, device="cuda") % 2 == 0, 1.0, 2.0)
+    l[2] = -math.inf
+    l[2, V - 1] = -7.0
+    l[3, :20000] = -math.inf
+    l[4] = l[4].round()
+    l[5, 35001] = math.inf
+    l[5, ::3] = float("nan")
+    l[6] = -math.inf
+    tokens, logp = check(g, l, u, unsure=0.15, **kw)
+    assert int(tokens[2]) == V - 1 and int(tokens[6]) == -1 and float(logp[6]) == -math.inf
+
+
+@pytest.mark.parametrize("kw", FILTERS)
+@pytest.mark.parametrize("V,dtype", [(5, F32), (2049, BF16), (20001, F16), (32768, F32)])
+def test_many_rows_and_few(g, V, dtype, kw):
+    """300 rows in one call and by 100: the same tokens and logarithms."""
+    l, u = make((300, V), dtype, seed=V)  # noqa: E741
+    l[7] = 1.0
+    l[8, ::2] = -math.inf
+    tokens, logp = g.gmm_sample(l, u, **kw)
+    for i in range(0, 300, 100):
+        t, p = g.gmm_sample(l[i:i + 100], u[i:i + 100], **kw)
+        assert torch.equal(t, tokens[i:i + 100]) and torch.equal(p, logp[i:i + 100])
+    check(g, l[5:9], u[5:9], unsure=0.25, **kw)
+
+
+def test_long_rows_captured_and_on_two_streams(g):
+    l, u = make((30, 40001), BF16)  # noqa: E741
+    step = lambda **kw: g.gmm_sample(l, u, temperature=0.8, top_k=40, top_p=0.9, **kw)  # noqa: E731
+    step()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(step())
+    for k in range(4):
+        l.normal_()
+        u.uniform_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want)), k
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [step(stream=s) for _ in range(3) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in got for a, b in zip(o, want))
