@@ -262,7 +262,9 @@ hipError_t launch_adamw(const AdamTensor* t, int count, AdamArgs A, hipStream_t 
     A.count = std::min(kAdamTensors, count - i0);
     A.pieces = 0;
     // a workgroup's round is 2048 elements: one a piece as long as that fills the
-    // card, then four, with a quarter of the look-ups
+    // card, then four, with a quarter of the look-ups (float32 states, 40000 values 4.9
+    // us with one and 7.4 with four, 2M 11.7 and 13.5, 4M 21.7 and 22.5; 8-bit states,
+    // 4M 20.4 and 22.1, 8M 35.9 and 33.3, 110M 376 and 362)
     int64_t total = 0;
     for (int i = 0; i < A.count; ++i) total += t[i0 + i].n;
     A.piece = total <= 2048 * kAdamRound ? kAdamRound : 4 * kAdamRound;

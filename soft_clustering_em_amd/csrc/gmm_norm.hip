@@ -458,7 +458,9 @@ hipError_t run_grad(const NormArgs& A, unsigned grid, hipStream_t s) {
 
 // Threads a row and pieces a thread for rows of `pieces` 16-byte pieces: the
 // fewest threads, a power of two, that hold one piece each up to a wave, then up to
-// `most` a thread.
+// `most` a thread.  bf16 forward: 1M x 24 by 4 lanes 34 us, by 16 90; 65536 x 1024 by
+// a wave with 2 pieces 51 us, by 256 threads 101; 32768 x 2048 with 4 pieces 46
+// against 61.
 static void norm_shape(int64_t pieces, int most, int* tpr, int* c) {
   *tpr = 4;
   while (*tpr < 64 && *tpr < pieces) *tpr *= 2;
@@ -503,6 +505,8 @@ NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums) {
   norm_shape((D + e - 1) / e, 2, &p.tpr, &p.c);  // more pieces, fewer waves: their sums beside the row take registers
   p.wide = p.c > 2;  // more sums than registers
   const int64_t rpb = p.tpr >= 256 ? 1 : 256 / p.tpr, groups = (R + rpb - 1) / rpb;
+  // sums: enough workgroups to fill the card, each with sums to write and to join
+  // (32768 x 2048 bf16, forward and gradients: 512 of them 177 us, 1024 146, 4096 179)
   p.grid = want_sums && !p.wide ? std::min<int64_t>(groups, 1024) : std::min<int64_t>(groups, 1 << 16);
   p.parts = p.wide ? std::min<int64_t>(64, std::max<int64_t>(1, R)) : p.grid;
   p.bytes = want_sums ? sizeof(float) * 2 * (size_t)D * (size_t)p.parts : 0;
