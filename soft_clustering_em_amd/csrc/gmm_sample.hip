@@ -1199,7 +1199,8 @@ static hipError_t run_sample(SampleArgs A, void* ws, hipStream_t s) {
   for (A.r0 = 0; A.r0 < A.R; A.r0 += step) {
     const unsigned n = (unsigned)std::min(step, A.R - A.r0);
     // four workgroups a compute unit or more, where the rows are long enough; the
-    // parts are powers of two
+    // parts are powers of two.  256 x 131072 bf16, top-p 0.9: 89 us, with two workgroups
+    // and parts of 8192 at least 139, with eight and 2048 93; 64 rows 47, 48 and 53
     const int64_t want = std::min<int64_t>(std::max<int64_t>(1, 1024 / n), (A.V + kPartLeast - 1) / kPartLeast);
     A.part_bits = 12;
     static_assert(kPartLeast == 1 << 12, "the least part");
