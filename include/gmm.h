@@ -498,6 +498,7 @@ gmm_status gmm_layer_norm_grad(const gmm_data* dout, const gmm_data* rows, const
  * scores, in the form that gmm_codebook_lookup and gmm_ivf_lists read.
  *   s = softmax(l) (GMM_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (GMM_SCORE_SIGMOID)
  *   t = s + bias_e; bias (E) float32, nullable: it takes part in the choice only
+ *     (a bias of -inf or NaN keeps its expert from being selected)
  *   groups > 1: the experts are `groups` equal runs; a group's score is the sum of
  *     its group_top (1 or 2) largest t, and the keep_groups groups of the largest
  *     scores stay (ties: lower group)

@@ -13,7 +13,8 @@
 // other one.  Rows whose groups are too close to tell in float32, or with more
 // candidates than places, go through the float64 scores of every expert.
 // 65536 x 256 sigmoid in groups, float32, m = 8: 50 us where the bytes take 14; bound
-// by instructions, at six waves a SIMD (eight spill: 87 us).  One row: 9 us, latency.
+// by instructions, with registers for five waves a SIMD (six 58 us, eight 87:
+// spills).  One row: 9 us, latency.
 // The gradient forms the scores again from the logits: 100000 x 60 softmax, bf16,
 // m = 4: 20 us forward and 20 us gradient.
 #include "gmm_device.h"
@@ -133,7 +134,7 @@ __device__ void route_exact(const RouteArgs& A, int64_t r, double* row) {
 #pragma unroll
   for (int k = 0; k < EPL; ++k) {
     const int e = lane + 64 * k;
-    t[k] = l[k] > -INFINITY ? (by_score ? s[k] + (double)A.bias[e] : (double)l[k]) : -INFINITY;
+    t[k] = l[k] > -INFINITY ? (by_score ? fmax(s[k] + (double)A.bias[e], -INFINITY) : (double)l[k]) : -INFINITY;
   }
   if (A.groups > 1 && A.keep < A.groups) {
     const int gs = A.E / A.groups;
@@ -252,7 +253,7 @@ __device__ inline int not_below(float a, float v) {
 
 // TWO: m is more than half of L
 template <typename T, int L, int EPL, bool TWO>
-__global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_kernel(RouteArgs A) {
+__global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 5 : 7) : 1) route_kernel(RouteArgs A) {
   constexpr int RPW = 64 / L, EXACT = L * EPL > 64 ? L * EPL / 64 : 1;
   extern __shared__ double lds[];  // a wave: RPW rows of `room` doubles
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sub = lane % L, row = lane / L;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {
       const float v = score(k) + A.bias[min(sub + L * k, A.E - 1)];
-      t[k] = l[k] > -INFINITY ? v : -INFINITY;
+      t[k] = l[k] > -INFINITY ? v : -INFINITY;  // NaN, from a NaN bias, is passed over below
     }
   }
   bool unsure = false;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
         const float v = row_t[at(first + i)];
-        next = fmaxf(next, fminf(best, v));
+        next = __builtin_amdgcn_fmed3f(best, next, v);  // of a NaN and two numbers the lower one
         best = fmaxf(best, v);
       }
       for (int o = 1; o < P; o *= 2) {
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_
   // at least m experts are not below the m-th largest of the lanes' maxima, or,
   // where m is more than half the lanes, of their two largest each (with one each
   // the bound would be among the smallest maxima, and hold few experts off: 65536 x
-  // 256, m = 16 130 -> 73 us)
+  // 256, m = 16 130 -> 56 us)
   float bound = -FLT_MAX;  // EPL = 1: every expert may be placed
   if constexpr (EPL > 1) {
     float top = -INFINITY, next = -INFINITY;
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 6 : 7) : 1) route_
       float first = -INFINITY;
 #pragma unroll
       for (int k = 0; k < EPL; ++k) {
-        next = fmaxf(next, fminf(first, t[k]));
+        next = __builtin_amdgcn_fmed3f(first, next, t[k]);
         first = fmaxf(first, t[k]);
       }
       reach += not_below<L>(next, top);

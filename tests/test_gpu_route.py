@@ -203,3 +203,21 @@ def test_more_rows_than_a_launch_takes(g):
     assert int(idx.sum(dtype=torch.int64)) == (n + 1) // 2
     dl = g.gmm_route_topm_grad(w, l, idx, renormalize=False)
     head_ref.within("dlogits", dl[at].cpu(), *ref.route_grad(w[at], l[at], idx[at], renorm=False))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,keep,top", [(12, 1, 1, 1), (64, 8, 3, 2), (256, 8, 4, 2), (256, 1, 1, 1), (600, 4, 2, 1)])
+def test_a_bias_that_switches_experts_off(g, score, E, groups, keep, top):
+    """-inf and NaN biases choose as a bias far below every score does, and +inf as one far above."""
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    l = torch.randn(500, E, generator=gen, device="cuda")  # noqa: E741
+    finite = 0.1 * torch.randn(E, generator=gen, device="cuda")
+    odd = finite.clone()
+    finite[1::4], odd[1::4] = -1e30, -float("inf")
+    finite[2::8], odd[2::8] = -1e30, float("nan")
+    how = dict(score=score, groups=groups, keep_groups=keep, group_top=top)
+    want, got = g.gmm_route_topm(l, 3, bias=finite, **how), g.gmm_route_topm(l, 3, bias=odd, **how)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool(torch.isfinite(got[1]).all())
+    finite[7], odd[7] = 1e30, float("inf")
+    want, got = g.gmm_route_topm(l, 3, bias=finite, **how), g.gmm_route_topm(l, 3, bias=odd, **how)
+    assert bool((got[0][:, 0] == 7).all()) and all(torch.equal(a, b) for a, b in zip(got, want))
