@@ -251,9 +251,11 @@ __device__ inline int not_below(float a, float v) {
   return n;
 }
 
-// TWO: m is more than half of L
+// TWO: m is more than half of L.  Registers for as many waves a SIMD as leave the
+// least spills: EPL = 16 five, 8 seven (131072 x 128 54 us; six 58), below eight
+// (262144 x 64 83 us; seven 86).
 template <typename T, int L, int EPL, bool TWO>
-__global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 5 : 7) : 1) route_kernel(RouteArgs A) {
+__global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 5 : EPL == 8 ? 7 : 8) : 1) route_kernel(RouteArgs A) {
   constexpr int RPW = 64 / L, EXACT = L * EPL > 64 ? L * EPL / 64 : 1;
   extern __shared__ double lds[];  // a wave: RPW rows of `room` doubles
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sub = lane % L, row = lane / L;
