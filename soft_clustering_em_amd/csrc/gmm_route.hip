@@ -199,10 +199,11 @@ __device__ void route_exact(const RouteArgs& A, int64_t r, double* row) {
 
 constexpr int kPlaces = 64;  // candidates of a row at most
 
-// doubles of LDS a row: its scores and the groups' (float32; float64 in
-// route_exact, which has a wave's share), or its candidates and codes
+// doubles of LDS a row: its scores, the groups' and what those are off by
+// (float32; float64 scores in route_exact, which has a wave's share), or its
+// candidates and codes
 __host__ __device__ inline int route_room(int E, int groups, int lanes) {
-  const int f32 = (E + E / 32 + 1 + groups + 1) / 2, list = kPlaces * 2 + kRouteMaxM / 2;
+  const int f32 = (E + E / 32 + 1 + 2 * groups + 1) / 2, list = kPlaces * 2 + kRouteMaxM / 2;
   const int scores = groups == 1 ? 0 : lanes == 64 && E > f32 ? E : f32;
   return ((scores > list ? scores : list) + 1) / 2 * 2;
 }
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 5 : EPL == 8 ? 7 :
     float* row_t = reinterpret_cast<float*>(mine_lds);
     const auto at = [](int e) { return e + (e >> 5); };
     float* group_t = row_t + at(A.E);
+    float* group_off = group_t + A.groups;
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {
       const int e = sub + L * k;
@@ -327,23 +329,31 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 5 : EPL == 8 ? 7 :
         next = fmaxf(fmaxf(next, x), fminf(best, b));
         best = fmaxf(best, b);
       }
-      if (g < A.groups) group_t[g] = A.top == 2 && next > -INFINITY ? best + next : best;
+      // a sum is off by what its terms are (biases of either sign may leave it far
+      // smaller than they are), and its rounding
+      const bool two = A.top == 2 && next > -INFINITY;
+      const float v = two ? best + next : best;
+      if (g < A.groups) {
+        group_t[g] = v;
+        group_off[g] = need_s && v > -INFINITY ? kOff(best) + (two ? kOff(next) : 0.f) + 0x1p-22f * fabsf(v) : 0.f;
+      }
     }
     wave_lds();
-    float least = INFINITY, most = -INFINITY;  // of the groups kept and of the others
+    // the least that a group kept may score and the most that another one may
+    float least = INFINITY, most = -INFINITY;
     for (int g0 = 0; g0 < A.groups; g0 += L / P) {
       const int g = g0 + sub / P, first = g * gs + sub % P * run;
       if (g >= A.groups) continue;
-      const float v = group_t[g];
+      const float v = group_t[g], off = group_off[g];
       int place = 0;
       for (int j = 0; j < A.groups; ++j) {
         const float o = group_t[j];
         place += o > v || (o == v && j < g);
       }
       if (place < A.keep) {
-        least = fminf(least, v);
+        least = v - off < least ? v - off : v < INFINITY ? least : -INFINITY;
       } else {
-        most = fmaxf(most, v);
+        most = fmaxf(most, v + off);
         const int n = min(run, (g + 1) * gs - first);
 #pragma unroll 4
         for (int i = 0; i < n; ++i) row_t[at(first + i)] = -INFINITY;
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(256, L == 16 ? (EPL == 16 ? 5 : EPL == 8 ? 7 :
     }
     least = -lanes_max<L>(-least);
     most = lanes_max<L>(most);
-    if (need_s) unsure = most > -INFINITY && !(least - most > 4.f * fmaxf(kOff(least), kOff(most)));
+    if (need_s) unsure = most > -INFINITY && !(least > most);
     wave_lds();
 #pragma unroll
     for (int k = 0; k < EPL; ++k) {

@@ -221,3 +221,33 @@ def test_a_bias_that_switches_experts_off(g, score, E, groups, keep, top):
     finite[7], odd[7] = 1e30, float("inf")
     want, got = g.gmm_route_topm(l, 3, bias=finite, **how), g.gmm_route_topm(l, 3, bias=odd, **how)
     assert bool((got[0][:, 0] == 7).all()) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,keep,m", [(4, 2, 1, 2), (64, 16, 5, 8), (320, 64, 20, 8)])
+def test_biases_that_cancel_within_a_group(g, score, E, groups, keep, m):
+    """A group's two best are forced apart by a bias of either sign, so that its
+    score is small and each of its terms is not; groups lie 1e-5 apart.  Rows whose
+    float64 scores of the last group kept and the first one dropped differ by less
+    than 1e-11 (64 units of float64 at the largest bias) may go either way."""
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    n, gs = 20000, E // groups
+    rand = lambda *s: torch.rand(*s, generator=gen, device="cuda", dtype=torch.float64)  # noqa: E731
+    s = 0.05 * rand(n, groups, gs)
+    s[:, :, 0] = 0.35 + 0.2 * rand(n, groups)
+    s[:, :, 1] = 0.9 + 1e-5 * (2 * rand(n, groups) - 1) - s[:, :, 0]
+    l = (torch.log(s) if score == "softmax" else torch.logit(s)).view(n, E).float()  # noqa: E741
+    for by in (1.0, 30.0, 100.0, 1000.0):
+        bias = torch.full((groups, gs), -4.0 * by, device="cuda")
+        bias[:, 0], bias[:, 1] = by, -by
+        bias = bias.view(E)
+        idx, _ = g.gmm_route_topm(l, m, bias=bias, score=score, groups=groups, keep_groups=keep, group_top=2)
+        t = (torch.softmax(l.double(), 1) if score == "softmax" else torch.sigmoid(l.double())) + bias.double()
+        value, order = (t.view(n, groups, gs).topk(2, dim=2).values.sum(2)).sort(dim=1, descending=True, stable=True)
+        clear = (value[:, keep - 1] - value[:, keep] > 1e-11) & (value[:, :keep].diff(dim=1).abs() > 0).all(1)
+        kept = torch.zeros(n, groups, dtype=torch.bool, device="cuda").scatter_(1, order[:, :keep], True)
+        t = t.masked_fill(~kept.repeat_interleave(gs, 1), -math.inf)
+        best, at = t.sort(dim=1, descending=True, stable=True)
+        clear &= (best[:, :m].diff(dim=1).abs() > 1e-11).all(1)
+        assert float(clear.double().mean()) > 0.99
+        assert torch.equal(idx[clear].long(), at[clear, :m]), (by, int((idx[clear].long() != at[clear, :m]).any(1).sum()))
