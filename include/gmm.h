@@ -529,7 +529,8 @@ gmm_status gmm_route_topm(const gmm_data* logits, const float* bias, const gmm_r
  *   dweights (B,N,m) float32: the weights' gradient, nullable
  *   dscores (E) float32: the gradient of every row's scores s, the same for all
  *     rows (that of a balance loss), nullable; one of the two given.
- * Experts that are switched off get 0.  The same windows; groups and bias have no
+ * Experts that are switched off get 0 and, as codes, have no part in the others'
+ * gradients.  The same windows; groups and bias have no
  * part in it.  dlogits may not overlap an input. */
 gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, int32_t m, const int32_t* idx,
                                const float* dweights, const float* dscores, void* dlogits, void* stream);

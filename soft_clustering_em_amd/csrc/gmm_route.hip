@@ -79,7 +79,8 @@ __device__ inline void wave_lds() {
 // stands for the row's, so that their sum cannot vanish.
 template <typename T, int L>
 __device__ inline double selected(const RouteArgs& A, int64_t base, int e, float mx, double total) {
-  const float l = e >= 0 ? fminf(logit<T>(A, base + e), FLT_MAX) : -INFINITY;
+  // a NaN, which only a caller's own code can lead to, is switched off like -inf
+  const float l = e >= 0 ? fminf(fmaxf(logit<T>(A, base + e), -INFINITY), FLT_MAX) : -INFINITY;
   double q = 0.0;
   if (A.sigmoid) {
     if (e >= 0) q = sigmoid_f64((double)l);

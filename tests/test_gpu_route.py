@@ -251,3 +251,16 @@ def test_biases_that_cancel_within_a_group(g, score, E, groups, keep, m):
         clear &= (best[:, :m].diff(dim=1).abs() > 1e-11).all(1)
         assert float(clear.double().mean()) > 0.99
         assert torch.equal(idx[clear].long(), at[clear, :m]), (by, int((idx[clear].long() != at[clear, :m]).any(1).sum()))
+
+
+@pytest.mark.parametrize("E", [20, 300])
+def test_gradient_of_codes_that_are_switched_off(g, E):
+    """Codes of experts whose logit is NaN or -inf have no weight and no gradient, and the others' is theirs alone."""
+    l = make((4, E))  # noqa: E741
+    l[0, 3], l[1, 3], l[2, :] = float("nan"), -math.inf, float("nan")
+    idx = torch.tensor([[3, 4], [4, 3], [1, 2], [3, 4]], dtype=torch.int32, device="cuda")
+    dw = torch.randn(4, 2, device="cuda")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            dl = g.gmm_route_topm_grad(dw, l, idx, score=score, renormalize=renorm)
+            head_ref.within("dlogits", dl.cpu(), *ref.route_grad(dw, l, idx, score, renorm))
