@@ -288,8 +288,11 @@ __device__ inline u64 best_of(const Row<T>& R, int64_t i0, int64_t i1, int threa
   uint32_t index = 0;
   if (at >= 0) {
 #pragma unroll
-    for (int e = E - 1; e >= 0; --e)
-      if (fminf((float)p[at + e], FLT_MAX) == top) index = (uint32_t)(at + e);
+    for (int e = E - 1; e >= 0; --e) {
+      // top is at most FLT_MAX, which +inf counts as; NaN is not above anything
+      const float l = (float)p[at + e];
+      if (l >= top) index = (uint32_t)(at + e);
+    }
   }
   if (i1 - whole > thread && thread < E) {
     const float l = (float)p[whole + thread];

@@ -246,3 +246,32 @@ def test_long_rows_captured_and_on_two_streams(g):
     got = [step(stream=s) for _ in range(3) for s in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o in got for a, b in zip(o, want))
+
+
+@pytest.mark.parametrize("kw", [dict(temperature=0.0), dict(top_k=1), dict(top_k=7), dict(top_p=0.9), dict(), dict(min_p=0.5)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("V", [301, 40003])
+def test_nan_beside_the_largest_value(g, V, dtype, kw):
+    """NaN below, above and on both sides of +inf or of float32's largest value, in one piece of 16 bytes and at a row's end."""
+    l, u = make((6, V), dtype)  # noqa: E741
+    nan, top = float("nan"), math.inf
+    l[0, 0], l[0, 1] = nan, top
+    l[1, V // 2 // 8 * 8], l[1, V // 2 // 8 * 8 + 3] = nan, torch.finfo(dtype).max
+    l[2, 16], l[2, 17], l[2, 18] = nan, top, nan
+    l[3, V - 2], l[3, V - 1] = nan, top
+    l[4, 8:16], l[4, 15] = nan, top
+    l[5, 24:27], l[5, 26:28] = nan, top
+    tokens, _ = check(g, l, u, unsure=0.2, **kw)
+    if kw.get("temperature") == 0.0 or kw.get("top_k") == 1:
+        assert tokens.tolist() == [1, V // 2 // 8 * 8 + 3, 17, V - 1, 15, 26]
+
+
+@pytest.mark.parametrize("kw", FILTERS)
+def test_infinite_logits_among_nan_in_long_rows(g, kw):
+    V = 40003
+    l, u = make((3, V))  # noqa: E741
+    l[:, ::3] = float("nan")
+    l[0, 35002] = math.inf
+    l[1, 35002:35005] = math.inf
+    l[2, 20] = torch.finfo(F32).max
+    check(g, l, u, unsure=0.34, **kw)
