@@ -54,7 +54,7 @@ struct Row {
   double scale, S; // kBinsPerUnit / temperature, 2^S
   double least;    // min-p
   double u;        // the row's number, in [0, 1)
-  float bins;      // scale, at most FLT_MAX
+  float bins;      // scale; NaN where float32 distances would leave its range
   // The distance to the maximum in bins, y >= 0.  exp((l - max) / T) = exp(-b / 32)
   // exp(-t / 32) with b = y rounded and |t| <= 1/2: the first factor is one of
   // kBins values, 0 from there on (2^-92 is below half of any 2^-S), the second
@@ -258,7 +258,9 @@ __device__ inline Settings row_of(const SampleArgs& A, int64_t r, const SampleSe
   R.u = (double)s.u;
   R.scale = t > 0.0 ? fmin(kBinsPerUnit / t, 1e300) : 1.0;
   R.least = s.min_p > 0.0 ? fmin(s.min_p, 1.0) : 0.0;
-  R.bins = (float)fmin(R.scale, (double)FLT_MAX);
+  // below 2^-100 a difference past float32's largest value may lie in any bin, above
+  // 2^100 one among float32's smallest values may
+  R.bins = R.scale >= 0x1p-100 && R.scale <= 0x1p100 ? (float)R.scale : __builtin_nanf("");
   return q;
 }
 
@@ -382,7 +384,8 @@ template <typename T>
 __device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t i1, int thread, int threads) {
   constexpr int E = 16 / (int)sizeof(T), U = 4;
   const int at = sh.at;
-  // the float32 distance is off by less than 2^-22 of itself
+  // the float32 distance is off by less than 2^-22 of itself; where it is NaN (no
+  // distance in float32, or a NaN logit) the element is looked at
   const float end = at == kBins - 1 ? __builtin_nanf("") : ((float)at + 0.5f) * (1.f + 0x1p-20f);
   const float begin = ((float)at - 0.5f) * (1.f - 0x1p-20f);
   volatile int* filled = &sh.na;
@@ -407,7 +410,7 @@ __device__ inline void collect(const Row<T>& R, Cutting& sh, int64_t i0, int64_t
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float y = (R.mx - (float)v[u][e]) * R.bins;
-        m |= !(y >= end) && y >= from ? 1u << e : 0u;
+        m |= !(y >= end) && !(y < from) ? 1u << e : 0u;
       }
       if (i + u * step < whole) marked |= m << (u * E);
     }

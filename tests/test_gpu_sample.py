@@ -275,3 +275,20 @@ def test_infinite_logits_among_nan_in_long_rows(g, kw):
     l[1, 35002:35005] = math.inf
     l[2, 20] = torch.finfo(F32).max
     check(g, l, u, unsure=0.34, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_p=0.9), dict(top_p=0.99), dict(top_p=0.5), dict(top_k=40, top_p=0.9), dict(min_p=0.1)])
+@pytest.mark.parametrize("V", [300, 20000, 40003])
+def test_temperatures_near_the_ends_of_float32(g, V, kw):
+    """Logits a few of float32's smallest steps apart under a temperature as small,
+    and logits further apart than float32's largest value under one as large."""
+    i = torch.arange(V, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    u = torch.rand(4, generator=gen, device="cuda")
+    small = (i * 2000 // V - (1 << 31)).int().view(F32)  # 0 to -1999 steps of 2^-149
+    rows = torch.stack([small[torch.randperm(V, generator=gen, device="cuda")] for _ in range(4)])
+    tokens, logp = check(g, rows, u, unsure=0.26, temperature=1e-43, **kw)
+    many = g.gmm_sample(rows.repeat(75, 1), u.repeat(75), temperature=1e-43, **kw)  # fewer threads a row, more steps each
+    assert torch.equal(many[0], tokens.repeat(75)) and torch.equal(many[1], logp.repeat(75))
+    large = 6.7e38 * (torch.rand(4, V, generator=gen, device="cuda", dtype=torch.float64) - 0.5)
+    check(g, large.float(), u, unsure=0.26, temperature=1e38, **kw)
