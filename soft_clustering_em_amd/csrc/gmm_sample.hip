@@ -58,11 +58,18 @@ struct Row {
   // The distance to the maximum in bins, y >= 0.  exp((l - max) / T) = exp(-b / 32)
   // exp(-t / 32) with b = y rounded and |t| <= 1/2: the first factor is one of
   // kBins values, 0 from there on (2^-92 is below half of any 2^-S), the second
-  // its series to t^6 (off by 2^-54).  Descending logits have ascending bins.
-  __device__ double distance(float l) const { return ((double)mx - (double)l) * scale; }
+  // its series to t^6 (off by 2^-54).  Descending logits have ascending bins.  A
+  // logit's weight is formed again by every pass and each of them has to find the
+  // same bits (a token is the element at which sums of two passes meet), so the
+  // distance is rounded before b is taken off it, wherever that is compiled.
+  __device__ double distance(float l) const {
+#pragma clang fp contract(off)
+    return ((double)mx - (double)l) * scale;
+  }
   __device__ int bin(float l) const { return (int)fmin(rint(distance(l)), (double)(kBins - 1)); }
-  static __device__ double near(double t) {
-    t *= -1.0 / kBinsPerUnit;
+  static __device__ double near(double y, double b) {
+#pragma clang fp contract(off)
+    const double t = (y - b) * (-1.0 / kBinsPerUnit);
     double q = 1.0 / 720.0;
     q = fma(q, t, 1.0 / 120.0);
     q = fma(q, t, 1.0 / 24.0);
@@ -74,7 +81,7 @@ struct Row {
   static __device__ double far(double b) { return exp_neg(b * (-1.0 / kBinsPerUnit)); }
   __device__ double share(float l) const {
     const double y = distance(l), b = rint(y);
-    return b < (double)kBins ? far(b) * near(y - b) : 0.0;
+    return b < (double)kBins ? far(b) * near(y, b) : 0.0;
   }
   // e 2^S rounded to an integer: at most 2^52, the low bits of its sum with 2^52
   __device__ u64 fixed(double e) const {
@@ -318,7 +325,7 @@ __device__ inline u64 fill_bins(const Row<T>& R, Mode mode, int64_t i0, int64_t 
   const auto share = [&](float l, int& at) {
     const double y = R.distance(l), b = rint(y);
     at = (int)fmin(b, (double)(kBins - 1));
-    return b < (double)kBins ? factor[at] * R.near(y - b) : 0.0;
+    return b < (double)kBins ? factor[at] * R.near(y, b) : 0.0;
   };
   int at;
   if (mode == kMass) {
@@ -462,6 +469,7 @@ __device__ inline void scan_list(Shared& sh, int n, F f) {
 __device__ inline float list_logit(u64 v) { return logit_of((uint32_t)(v >> 32)); }
 template <typename T>
 __device__ inline void answer(const SampleArgs& A, const Row<T>& R, int64_t r, float l, int64_t i, u64 total) {
+#pragma clang fp contract(off)
   A.tokens[r] = (int32_t)i;
   if (A.logp) A.logp[r] = (float)(-R.distance(l) / kBinsPerUnit - log((double)total / R.S));
 }
@@ -1096,7 +1104,7 @@ __global__ void __launch_bounds__(256) sample_collect_kernel(SampleArgs A) {
       each<1>(R, q0, q1, threadIdx.x & 63, 64, [&](int64_t, float l) {
         const double y = R.distance(l), b = rint(y);
         if (b < at) {
-          const double e = factor[(int)b] * R.near(y - b);
+          const double e = factor[(int)b] * R.near(y, b);
           mass += e >= R.least ? R.fixed(e) : 0;
         }
       });
