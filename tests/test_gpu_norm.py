@@ -182,3 +182,19 @@ def test_more_rows_than_a_launch_takes(g):
     at = torch.tensor([0, 1, (1 << 27) - 1, 1 << 27, n - 2, n - 1], device="cuda")
     head_ref.within("out", out[at], *ref.norm(X[at])[0])
     assert torch.equal(out[:1000], out[0].expand(1000, 8)) and torch.equal(out[1 << 27:], out[n - 1].expand(37, 8))
+
+
+def test_rows_behind_those_of_a_launch(g):
+    """2^31 threads of a launch are 2^29 rows of 4 lanes (two bf16 values are one piece): the last 37 come in a second one."""
+    n = (1 << 29) + 37
+    X = torch.zeros(n, 2, dtype=BF16, device="cuda")
+    X[:, 1] = 1.0
+    X[1 << 29:, 0] = 5.0
+    X[n - 1, 0] = -3.0
+    mean = torch.zeros(n, device="cuda")
+    out, _, _ = g.gmm_layer_norm(X, mean=mean, rstd=False)
+    at = torch.tensor([0, 1, (1 << 29) - 1, 1 << 29, (1 << 29) + 1, n - 2, n - 1], device="cuda")
+    head_ref.within("out", out[at], *ref.norm(X[at])[0])
+    head_ref.within("mean", mean[at], *ref.norm(X[at])[1])
+    assert torch.equal(out[:1000], out[0].expand(1000, 2)) and torch.equal(out[(1 << 29) - 1000:1 << 29], out[0].expand(1000, 2))
+    assert torch.equal(out[1 << 29:n - 1], out[n - 2].expand(36, 2))

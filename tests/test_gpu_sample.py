@@ -292,3 +292,20 @@ def test_temperatures_near_the_ends_of_float32(g, V, kw):
     assert torch.equal(many[0], tokens.repeat(75)) and torch.equal(many[1], logp.repeat(75))
     large = 6.7e38 * (torch.rand(4, V, generator=gen, device="cuda", dtype=torch.float64) - 0.5)
     check(g, large.float(), u, unsure=0.26, temperature=1e38, **kw)
+
+
+def test_more_long_rows_than_are_in_flight(g):
+    """1040 rows in parts, 1024 at a time over one workspace: each as in a call of its own."""
+    R, V = 1040, 32769
+    l, u = make((R, V), BF16, pad=5)  # noqa: E741
+    i = torch.arange(R, device="cuda")
+    kw = dict(temperature=torch.tensor([0.7, 0.0, 1.0, 1.3], device="cuda")[i % 4],
+              top_k=torch.tensor([0, 50, 5000], dtype=torch.int32, device="cuda")[i % 3],
+              top_p=torch.tensor([0.9, 1.0, 0.999, 0.5, 1.0], device="cuda")[i % 5],
+              min_p=torch.tensor([0.0, 0.05], device="cuda")[i % 7 % 2])
+    tokens, logp = g.gmm_sample(l, u, **kw)
+    for r in [0, 1, 511] + list(range(1020, R)):
+        t, p = g.gmm_sample(l[r:r + 1], u[r:r + 1], **{k: v[r:r + 1] for k, v in kw.items()})
+        assert t.item() == tokens[r].item() and p.item() == logp[r].item(), r
+    at = torch.tensor([0, 1023, 1024, 1039], device="cuda")
+    check(g, l[at], u[at], unsure=0.25, **{k: v[at] for k, v in kw.items()})
