@@ -145,6 +145,7 @@ __device__ inline void store_codes(uint8_t* p, float* scale, const float (&f)[kE
 
 struct Factors {
   float c, decay, alpha, root, b1, c1, b2, c2, eps;
+  int c_exp;  // the clipping coefficient is c 2^c_exp, c below 1 where c_exp is not 0
   uint32_t key;
 };
 
@@ -170,7 +171,7 @@ __device__ inline void adam_piece(const AdamTensor& t, int64_t i0, int64_t n, co
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const float d = F.c * g[e];
+      const float d = ldexpf(F.c * g[e], F.c_exp);
       if constexpr (BITS8) v[e] = v[e] * v[e];
       m[e] = F.b1 * m[e] + F.c1 * d;
       v[e] = F.b2 * v[e] + F.c2 * (d * d);
@@ -223,7 +224,10 @@ __global__ void __launch_bounds__(256) adamw_kernel(AdamArgs A) {
       c = q < 1.0 || q != q ? q : 1.0;
     }
     Factors f;
-    f.c = (float)c;
+    // float32 holds few bits, or none, of a coefficient below 2^-126 (gradients of 1e25
+    // and more under a small limit): its power of two goes on the product then
+    f.c_exp = c > 0.0 && c < 0x1p-100 ? ilogb(c) + 1 : 0;
+    f.c = (float)ldexp(c, -f.c_exp);
     f.alpha = (float)(lr / -expm1((double)step * A.log_b1));
     f.root = (float)(1.0 / sqrt(-expm1((double)step * A.log_b2)));
     f.b1 = (float)A.b1;

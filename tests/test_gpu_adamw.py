@@ -233,3 +233,18 @@ def test_mixed_states_in_one_call(g):
     g.gmm_adamw_step(q[:1], gr[:1], step=1, **c)
     g.gmm_adamw_step(q[1:], gr[1:], step=1, **d)
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(p + a["m"] + b["v"], q + c["m"] + d["v"]))
+
+
+@pytest.mark.parametrize("norm,max_norm", [(1e30, 1e-12), (3e38, 1e-30), (1e36, 1e-3)])
+@pytest.mark.parametrize("tg", [F32, BF16])
+def test_clipping_coefficients_below_float32(g, tg, norm, max_norm):
+    """Coefficients that float32 holds with few bits or not at all: c, the product
+    and its place among the float32 values are three roundings, m' three more."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    gr = (torch.randn(5000, generator=gen, device="cuda") * (norm / 100)).to(tg)
+    p, m, v = torch.zeros(5000, device="cuda"), torch.zeros(5000, device="cuda"), torch.zeros(5000, device="cuda")
+    n = torch.tensor([norm], device="cuda")
+    g.gmm_adamw_step([p], [gr], [m], [v], 1, betas=(0.9, 0.9), norm=n, max_norm=max_norm)
+    want = 0.1 * (max_norm / (float(n.double()) + 1e-6)) * gr.double()
+    assert float(want.abs().max()) > 2.0 ** -120
+    assert bool(((m.double() - want).abs() <= 6 * ref.U * want.abs() + 2.0 ** -148).all())
