@@ -555,7 +555,9 @@ gmm_status gmm_route_topm_grad(const gmm_data* logits, const gmm_routing* how, i
  *   mix(x): x = (x ^ x >> 16) 0x9E3779B1; x = (x ^ x >> 15) 0x6A09E667; x ^ x >> 16
  * in 32 bits, tensor its place in the call, i the element in its block; a root
  * that is not 0 becomes 2^-9 at least.  A NaN or infinite gradient makes its
- * element NaN, or the states of its block.
+ * element NaN, or the states of its block.  A finite one whose square leaves
+ * float32 (past 1.8e19) makes its float32 v infinite, and its p moves by the decay
+ * alone from then on; roots in 8 bits stay finite.
  * Nothing written may overlap another tensor.  `tensors` is host memory, read
  * during the call.  n < 2^40.  No workspace.  Deterministic. */
 typedef struct {

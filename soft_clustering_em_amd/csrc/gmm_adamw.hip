@@ -169,15 +169,33 @@ __device__ inline void adam_piece(const AdamTensor& t, int64_t i0, int64_t n, co
       load_each<float>(m, static_cast<const float*>(t.m) + i, have);
       load_each<float>(v, static_cast<const float*>(t.v) + i, have);
     }
+    float before[kEach], r[kEach], most = 0.f;  // 8 bits: the roots
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const float d = ldexpf(F.c * g[e], F.c_exp);
+      const float d = g[e] = ldexpf(F.c * g[e], F.c_exp);
+      before[e] = v[e];
       if constexpr (BITS8) v[e] = v[e] * v[e];
       m[e] = F.b1 * m[e] + F.c1 * d;
       v[e] = F.b2 * v[e] + F.c2 * (d * d);
-      const float r = sqrtf(v[e]);
-      p[e] = p[e] * F.decay - F.alpha * (m[e] / (r * F.root + F.eps));
-      if constexpr (BITS8) v[e] = r;
+      r[e] = sqrtf(v[e]);
+      most = fmaxf(most, v[e]);
+    }
+    if constexpr (BITS8) {
+      // squares past 1.8e19 leave float32, their root does not; a NaN would take the
+      // whole block with it
+      if (__ballot(most == INFINITY)) {
+        asm volatile("");  // a branch, not work for every wave
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const float x = before[e] * 0x1p-64f, y = g[e] * 0x1p-64f;
+          r[e] = r[e] == INFINITY ? sqrtf(F.b2 * (x * x) + F.c2 * (y * y)) * 0x1p64f : r[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      p[e] = p[e] * F.decay - F.alpha * (m[e] / (r[e] * F.root + F.eps));
+      if constexpr (BITS8) v[e] = r[e];
     }
     store_each<P>(static_cast<P*>(t.p) + i, p, have);
     if (t.copy && have) {

@@ -248,3 +248,32 @@ def test_clipping_coefficients_below_float32(g, tg, norm, max_norm):
     want = 0.1 * (max_norm / (float(n.double()) + 1e-6)) * gr.double()
     assert float(want.abs().max()) > 2.0 ** -120
     assert bool(((m.double() - want).abs() <= 6 * ref.U * want.abs() + 2.0 ** -148).all())
+
+
+def test_8_bit_states_of_gradients_whose_squares_leave_float32(g):
+    """|g| from 1e19 to 1e37 in some elements: root and value stay what the formula
+    gives, to the rounding of the states: the code is one of the two beside
+    root / max * 448 (a step is at most 1 / 8 of it, or 2^-9)."""
+    n = 1024
+    p, gr = make([n])
+    gr[0][5], gr[0][260:270], gr[0][600], gr[0][1023] = 3e19, 1e30, -1e37, 2e20
+    start, st = p[0].double(), g.new_adamw_state(p, 8)
+    root = torch.zeros(n, dtype=torch.float64, device="cuda")
+    first = root.clone()
+    for step in (1, 2, 3):
+        before_m = st["m"][0].float().double() * st["m_scale"][0].double().repeat_interleave(256)
+        before_r = st["v"][0].float().double() * st["v_scale"][0].double().repeat_interleave(256)
+        before_p = p[0].double()
+        g.gmm_adamw_step(p, gr, step=step, lr=0.01, betas=(0.9, 0.99), weight_decay=0.0, **st)
+        d = gr[0].double()
+        first, root = 0.9 * before_m + 0.1 * d, torch.sqrt(0.99 * before_r ** 2 + 0.01 * d * d)
+        for name, want in (("m", first), ("v", root)):
+            scale = st[name + "_scale"][0].double()
+            top = want.abs().view(-1, 256).amax(1)
+            assert bool(((scale * 448.0 - top).abs() <= 8 * ref.U * top).all()), (name, step)
+            x = want.abs() / top.repeat_interleave(256) * 448.0
+            got = st[name][0].float().double().abs()
+            assert bool(((got - x).abs() <= (1 + 1e-5) * (x / 8).clamp_min(2.0 ** -9)).all()), (name, step)
+        want = before_p - 0.01 / (1 - 0.9 ** step) * first / (root / math.sqrt(1 - 0.99 ** step) + 1e-8)
+        assert bool(((p[0].double() - want).abs() <= 30 * ref.U * (before_p.abs() + want.abs() + 0.1)).all()), step
+    assert bool(torch.isfinite(p[0]).all()) and float((p[0].double() - start).abs().max()) < 1.0
