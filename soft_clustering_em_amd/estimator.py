@@ -555,13 +555,14 @@ class SoftmaxHead:
 
     def logits(self, X):
         """W x + b of every row (normalised first with layer_norm), (N, n_classes)
-        float32: a library product, for the calls that choose among classes."""
+        float32, W rounded to the rows' type as fit and log_proba have it: a library
+        product in float32, for the calls that choose among classes."""
         torch = _torch()
         if X.dim() != 2:
             raise ValueError("X is (N, D)")
         self._ready()
         X = X.float() if X.dtype == torch.float16 else X
-        return torch.addmm(self.intercept_, self._rows(X).float(), self.coef_.t())
+        return torch.addmm(self.intercept_, self._rows(X).float(), self.coef_.to(X.dtype).float().t())
 
     def route(self, X, m=4, **how):
         """The m best classes of every row and their weights, as an assignment that

@@ -192,3 +192,21 @@ def test_refusals_on_the_gpu(g):
     for bad in (lambda: SoftmaxHead(3).sample(X), lambda: SoftmaxHead(3).route(X)):
         with pytest.raises(RuntimeError):
             bad()
+
+
+@pytest.mark.parametrize("layer_norm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_a_draw_has_the_probability_that_log_proba_gives(g, dtype, layer_norm):
+    """The head of bfloat16 rows is rounded to their type in both.  A logit is a sum
+    of 40 products in float32 in any order, the loss's bound beside it."""
+    from soft_clustering_em_amd.estimator import SoftmaxHead
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    X = torch.randn(500, 40, generator=gen, device="cuda").to(dtype)
+    head = SoftmaxHead(30, layer_norm=layer_norm)._set(torch.randn(30, 40, generator=gen, device="cuda"),
+                                                       torch.randn(30, generator=gen, device="cuda"))
+    u = torch.rand(500, generator=gen, device="cuda")
+    classes, logp = head.sample(X, u=u)
+    want = head.log_proba(X, classes)
+    size = float((head._rows(head._check(X, classes)).double().abs() @ head.coef_.double().abs().t()).max()) + 4.0
+    # both sides' logits (44 roundings), and log-sum-exps and differences (300)
+    assert float((logp.double() - want.double()).abs().max()) <= 2 * 44 * ref.U * size + 300 * ref.U * (size + 8)
