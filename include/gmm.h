@@ -484,6 +484,9 @@ gmm_status gmm_layer_norm(const gmm_data* rows, const void* gamma, const void* b
  * and q = dout gamma:
  *   dx (B,N,D) = r (q - sum_d q / D - xh sum_d q xh / D)
  *   dgamma (D) = sum over the rows of dout xh;  dbeta (D) = sum of dout
+ * xh is that of the mean given, a float32 value: rows far from zero lose in their
+ * gradients what it rounds off, half a unit in its last place times r a value of xh
+ * (mean 100: 4e-6 of a spread of 1; mean 30000: 1e-3).  The forward pass does not.
  * dx in the rows' type, contiguous, dgamma and dbeta float32; each nullable,
  * one given.  accumulate != 0 adds to what they hold.  The gradients may not
  * overlap each other or the inputs.  Workspace:

@@ -709,8 +709,10 @@ def gmm_layer_norm_grad(dout, X, mean, rstd, gamma=None, dX=None, dgamma=None, d
     """Gradients of gmm_layer_norm for the rows' gradient dout (X's shape and
     type, any row stride), with its mean and rstd: (dX, dgamma, dbeta), dX
     contiguous in X's type, dgamma and dbeta (D,) float32 (left out without
-    gamma unless given).  Buffers not given are allocated; False leaves one out.
-    accumulate=True adds to the buffers, all of which are then given."""
+    gamma unless given).  They are those of the float32 mean given, which rounds off
+    up to 2^-24 |mean| rstd of a normalised value (rows far from zero: 1e-3 at a mean
+    of 30000 and a spread of 1).  Buffers not given are allocated; False leaves one
+    out.  accumulate=True adds to the buffers, all of which are then given."""
     torch = _torch()
     d, y = _rows("X", X), _rows("dout", dout)
     if dout.shape != X.shape or dout.dtype != X.dtype:

@@ -6,7 +6,8 @@
 // A row's values stay in registers from the one read to the one write: TPR
 // threads a row, C pieces of 16 bytes a thread.  The mean is corrected by the
 // mean of the differences from its first value, and the variance is that of the
-// corrected differences, so rows far from zero keep their digits.  Sums are
+// corrected differences, so rows far from zero keep their digits; the gradients
+// take the mean as it was stored, rounded to float32.  Sums are
 // float32: per thread, then in a fixed order over the row's threads.  The
 // gradients of gamma and beta: a thread owns its columns over all the rows that
 // its workgroup walks, then the workgroups' sums are added in a fixed order.

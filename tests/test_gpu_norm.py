@@ -198,3 +198,25 @@ def test_rows_behind_those_of_a_launch(g):
     head_ref.within("mean", mean[at], *ref.norm(X[at])[1])
     assert torch.equal(out[:1000], out[0].expand(1000, 2)) and torch.equal(out[(1 << 29) - 1000:1 << 29], out[0].expand(1000, 2))
     assert torch.equal(out[1 << 29:n - 1], out[n - 2].expand(36, 2))
+
+
+@pytest.mark.parametrize("shape,dtype,offset", [((60, 300), F32, 0.0), ((60, 300), F32, 100.0), ((60, 300), F32, -3e4),
+                                                ((4, 9000), F32, 100.0), ((4, 9000), F32, -3e4), ((50, 64), BF16, 3.0)])
+def test_gradients_of_rows_far_from_zero(g, shape, dtype, offset):
+    """Against 64-bit gradients with their own mean and rstd: beside norm_grad's
+    bound, xh is off by what the float32 mean is (half a unit in its last place, and
+    the sum's own share) times rstd, and by rstd's own relative error."""
+    X, dout, gamma, beta = make(shape, dtype, dtype, offset=offset)
+    _, mean, rstd = g.gmm_layer_norm(X, gamma, beta)
+    grads = g.gmm_layer_norm_grad(dout, X, mean, rstd, gamma=gamma)
+    _, (m, m_tol), (r, r_tol) = ref.norm(X, gamma, beta)
+    x, y, q = X.double(), dout.double(), dout.double() * gamma.double()
+    m, r = m[:, None], r[:, None]
+    xh = (x - m) * r
+    off = ((m_tol[:, None] + ref.U * m.abs()) * r + r_tol[:, None] / r * xh.abs()) * 1.01
+    a, b = q.mean(1, keepdim=True), (q * xh).mean(1, keepdim=True)
+    dX = r * (q - a - xh * b)
+    more = r * (off * b.abs() + (xh.abs() + off) * (q.abs() * off).mean(1, keepdim=True)) + r_tol[:, None] * (dX / r).abs() * 1.01
+    for name, got, want, extra, (_, tol) in zip(("dX", "dgamma", "dbeta"), grads, (dX, (y * xh).sum(0), y.sum(0)),
+                                                (more, (y.abs() * off).sum(0), 0.0), ref.norm_grad(dout, X, mean, rstd, gamma)):
+        head_ref.within(name, got, want, tol + 1.01 * extra)
