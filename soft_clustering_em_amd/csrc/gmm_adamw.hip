@@ -12,9 +12,9 @@
 // would never move under rounding to nearest.  A root that is not zero is not
 // rounded to zero: m' over the next root would be too large a step.
 // Bound by memory: every tensor read once and written once.  110M float32 values,
-// bf16 gradients: with float32 states and bf16 copies 616 us (28 bytes a value, 5.0
-// TB/s), with 8-bit states 319 us (14 bytes, 4.8 TB/s, beside some 105 instructions a
-// value).
+// bf16 gradients: with float32 states and bf16 copies 615 us (28 bytes a value, 5.0
+// TB/s), with 8-bit states 321 us (14 bytes, 4.8 TB/s, beside 101 instructions a
+// value, which fill the vector units' issue).
 #include "gmm_device.h"
 
 #include <hip/hip_runtime.h>

@@ -11,7 +11,7 @@
 // float32: per thread, then in a fixed order over the row's threads.  The
 // gradients of gamma and beta: a thread owns its columns over all the rows that
 // its workgroup walks, then the workgroups' sums are added in a fixed order.
-// Bound by memory: 32768 x 2048 bf16 forward 56 us (4.8 TB/s), gradients 98 us (4.1
+// Bound by memory: 32768 x 2048 bf16 forward 50 to 56 us (4.8 TB/s and more), gradients 98 us (4.1
 // TB/s) and 7 for the join; 1M x 64 float32 102 and 162 us (5.0 and 4.7 TB/s); one
 // row of 4096 3.4 us, latency.
 #include "gmm_device.h"
@@ -459,9 +459,9 @@ hipError_t run_grad(const NormArgs& A, unsigned grid, hipStream_t s) {
 
 // Threads a row and pieces a thread for rows of `pieces` 16-byte pieces: the
 // fewest threads, a power of two, that hold one piece each up to a wave, then up to
-// `most` a thread.  bf16 forward: 1M x 24 by 4 lanes 34 us, by 16 90; 65536 x 1024 by
-// a wave with 2 pieces 51 us, by 256 threads 101; 32768 x 2048 with 4 pieces 46
-// against 61.
+// `most` a thread.  bf16 forward: 1M x 24 by 4 lanes 32 us, by 16 93; 65536 x 1024 by
+// a wave with 2 pieces 56 us, by 256 threads 123; 32768 x 2048 with 4 pieces 50
+// against 68.
 static void norm_shape(int64_t pieces, int most, int* tpr, int* c) {
   *tpr = 4;
   while (*tpr < 64 && *tpr < pieces) *tpr *= 2;
@@ -504,7 +504,9 @@ NormPlan norm_plan(int64_t R, int64_t D, int dtype, bool want_sums) {
   NormPlan p{};
   const int e = dtype == 0 ? 4 : 8;
   norm_shape((D + e - 1) / e, 2, &p.tpr, &p.c);  // more pieces, fewer waves: their sums beside the row take registers
-  p.wide = p.c > 2;  // more sums than registers
+  // more sums than registers: 2 pieces fit float32 rows (120 of 128) and spill 38 for
+  // 16-bit ones; without their sums 4 pieces spill 42 and 75, 8 spill 240
+  p.wide = p.c > 2;
   const int64_t rpb = p.tpr >= 256 ? 1 : 256 / p.tpr, groups = (R + rpb - 1) / rpb;
   // sums: enough workgroups to fill the card, each with sums to write and to join
   // (32768 x 2048 bf16, forward and gradients: 512 of them 177 us, 1024 146, 4096 179)

@@ -12,7 +12,8 @@
 // are scored in float64, a lane each, and placed by comparing each with every
 // other one.  Rows whose groups are too close to tell in float32, or with more
 // candidates than places, go through the float64 scores of every expert.
-// 65536 x 256 sigmoid in groups, float32, m = 8: 50 us where the bytes take 14; bound
+// 65536 x 256 sigmoid in groups, float32, m = 8: 50 us where the bytes take 14 (235 if
+// every row takes the float64 scores of all experts); bound
 // by instructions, with registers for five waves a SIMD (six 58 us, eight 87:
 // spills).  One row: 9 us, latency.
 // The gradient forms the scores again from the logits: 100000 x 60 softmax, bf16,
@@ -568,8 +569,8 @@ static hipError_t run_route(RouteArgs A, bool grad, hipStream_t s) {
 }
 
 // Sixteen lanes a row where they hold it, 16 experts each, a wave else (by a wave:
-// 65536 x 256 131 us against 55, 131072 x 128 189 against 61, 100000 x 60 143
-// against 21).
+// 65536 x 256 134 us against 52 to 56, 131072 x 128 143 against 41, 100000 x 60 153
+// against 19).
 template <typename T>
 static hipError_t run_routes(const RouteArgs& A, bool grad, hipStream_t s) {
   if (A.E <= 16) return run_route<T, 16, 1>(A, grad, s);

@@ -418,7 +418,8 @@ class SoftmaxHead:
     the posterior of a mixture with one shared spherical variance
     (W_k = mu_k / s^2, b_k = log pi_k - |mu_k|^2 / (2 s^2)), trained on labels
     instead of on the rows' density -- a router over the lists of a coarse
-    quantizer, for example, from the labels of KMeans or GaussianMixture.
+    quantizer (route: at most 1024 of them), for example, from the labels of KMeans
+    or GaussianMixture.
 
     fit(X, y) runs full-batch gradient descent on the mean cross entropy of the
     labelled rows (y (N,) int32; a negative label leaves a row out), each step one
@@ -567,14 +568,15 @@ class SoftmaxHead:
     def route(self, X, m=4, **how):
         """The m best classes of every row and their weights, as an assignment that
         gmm_codebook_lookup and gmm_ivf_lists read: (idx (N, m) int32, weights (N, m)
-        float32).  Keyword arguments are gmm_route_topm's (bias, score, groups,
-        keep_groups, group_top, renormalize, scale)."""
+        float32).  At most 1024 classes.  Keyword arguments are gmm_route_topm's (bias,
+        score, groups, keep_groups, group_top, renormalize, scale)."""
         return gmm_route_topm(self.logits(X), m, **how)
 
     def sample(self, X, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, u=None):
         """A class drawn for every row from its posterior, cut by top_k, top_p and
         min_p (gmm_sample): (classes (N,) int32, log of their share (N,) float32).  u:
-        uniform numbers (N,) float32 in [0, 1); None: drawn from random_state."""
+        uniform numbers (N,) float32 in [0, 1); None: drawn from random_state, the same
+        ones at every call."""
         torch = _torch()
         logits = self.logits(X)
         if u is None:
