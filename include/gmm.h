@@ -473,7 +473,9 @@ gmm_status gmm_clip_grad_norm(const gmm_tensor* grads, int32_t count, double max
  *   gamma, beta (D) of affine_dtype: float32 or the rows' type; nullable (1, 0)
  *   out (B,N,D) in the rows' type, contiguous; mean and rstd (= r) (B,N)
  *   float32, nullable, as gmm_layer_norm_grad takes them.
- * The variance is that of the differences from the mean, in float32.  Any
+ * The variance is that of the differences from the mean, in float32: rows whose
+ * sum, or whose squared differences (past 1.8e19 each), leave float32 are not
+ * normalised (NaN, or an rstd of 0).  Any
  * stride and alignment of the elements.  D <= 32768, B*N < 2^31.  out may not
  * overlap an input.  N = 0 launches nothing.  No workspace. */
 gmm_status gmm_layer_norm(const gmm_data* rows, const void* gamma, const void* beta, int32_t affine_dtype, double eps,
